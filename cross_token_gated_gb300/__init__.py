@@ -8,6 +8,7 @@ the library cannot be loaded, every call raises.
 Functions (same names as the C ABI):
   tango_aggregate, tango_aggregate_noalloc, wango_aggregate, tango_aggregate_save,
   wango_aggregate_save, tango_aggregate_backward, wango_aggregate_backward, wango_decode_step, tango_block_forward, tango_model_forward,
+  tango_qk_norm_rope, tango_qk_norm_rope_backward, tg_rope_freqs, tango_cache_append, tango_paged_aggregate,
   tg_workspace_size, tg_status_string, tg_check_device_error, tg_version
 """
 from __future__ import annotations
@@ -31,6 +32,9 @@ TG_FLAG_BWD_FAR_SCAN = 0x400
 TG_FLAG_BWD_FAR_PAIRS = 0x800
 TG_MODE_TANGO, TG_MODE_WANGO = 0, 1
 TG_WS_TANGO, TG_WS_WANGO, TG_WS_BLOCK, TG_WS_MODEL, TG_WS_DECODE, TG_WS_TANGO_BWD, TG_WS_WANGO_BWD = range(7)
+TG_WS_QK_BWD, TG_WS_PAGED = 16, 17
+TG_ROPE_HALF, TG_ROPE_INTERLEAVED = 0, 1
+TG_NORM_NONE, TG_NORM_UNIT, TG_NORM_RMS = range(3)
 
 HEADER = os.path.join(_build.INCLUDE, "tango.h")
 
@@ -66,6 +70,26 @@ class tg_model_params(ctypes.Structure):
     _fields_ = [("block", tg_block_params), ("vocab", ctypes.c_int), ("n_apps", ctypes.c_int),
                 ("n_sets", ctypes.c_int), ("set_of_app", ctypes.POINTER(ctypes.c_int)),
                 ("final_rms_eps", ctypes.c_float)]
+
+
+class tg_qk_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("H", ctypes.c_int), ("H_k", ctypes.c_int), ("d_h", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("norm", ctypes.c_int),
+                ("eps", ctypes.c_float), ("T", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("freqs", ctypes.c_void_p), ("q_gain", ctypes.c_void_p), ("k_gain", ctypes.c_void_p),
+                ("q_pitch", ctypes.c_longlong), ("k_pitch", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+class tg_paged_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "d_h", "m", "m_pitch", "N", "max_new", "max_len", "page_size",
+                                            "n_pages", "table_pitch")] +                [(n, ctypes.c_void_p) for n in ("cu_new", "lens", "page_table")] +                [("s", ctypes.c_float), ("tau", ctypes.c_void_p), ("null_bias", ctypes.c_void_p),
+                ("v_pitch", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+class tg_append_params(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("norm", ctypes.c_int),
+                ("eps", ctypes.c_float), ("freqs", ctypes.c_void_p), ("silu", ctypes.c_int),
+                ("q_pitch", ctypes.c_longlong), ("k_pitch", ctypes.c_longlong), ("g_pitch", ctypes.c_longlong)]
 
 
 _lib = None
@@ -113,6 +137,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.wango_decode_step.restype = ctypes.c_int
         lib.tango_model_forward.argtypes = [P(tg_model_params), P(tg_model_weights), vp, vp, vp, sz, vp]
         lib.tango_model_forward.restype = ctypes.c_int
+        lib.tango_qk_norm_rope.argtypes = [P(tg_qk_params), vp, vp, vp, vp, vp]
+        lib.tango_qk_norm_rope.restype = ctypes.c_int
+        lib.tango_qk_norm_rope_backward.argtypes = [P(tg_qk_params)] + [vp] * 9 + [sz, vp]
+        lib.tango_qk_norm_rope_backward.restype = ctypes.c_int
+        db = ctypes.c_double
+        lib.tg_rope_freqs.argtypes = [ctypes.c_int, db, db, ctypes.c_longlong, db, db, P(db)]
+        lib.tg_rope_freqs.restype = ctypes.c_int
+        lib.tango_cache_append.argtypes = [P(tg_paged_params), P(tg_append_params), vp, vp, vp, vp, vp, vp, vp]
+        lib.tango_cache_append.restype = ctypes.c_int
+        lib.tango_paged_aggregate.argtypes = [P(tg_paged_params), vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.tango_paged_aggregate.restype = ctypes.c_int
         lib.tg_workspace_size.argtypes = [ctypes.c_int, vp]
         lib.tg_workspace_size.restype = sz
         lib.tg_status_string.argtypes = [ctypes.c_int]
@@ -196,6 +231,15 @@ def _workspace(nbytes: int, device, ws):
     if ws is not None:
         return ws
     return torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+
+
+def _scratch(nbytes: int, device, ws, stream):
+    """_workspace for a call on `stream`: scratch made here stays allocated until that
+    stream has passed the call, also when it is not the current one."""
+    buf = _workspace(nbytes, device, ws)
+    if ws is None and buf is not None and stream is not None:
+        buf.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return buf
 
 
 def _ws_ptr(ws):
@@ -410,4 +454,216 @@ def wango_decode_step(q, k, g, v, out, state, pos, *, H, window, s=10.0, tau=Non
                                   wp, wn, _stream(stream))
     if st != TG_OK:
         raise TgError(st, "wango_decode_step")
+    return out
+
+
+# ----------------------------------------------- norm and rotary position of q and k
+
+def _check(t, name, dtype=None, like=None, dense=False, shape=None):
+    """Raises unless t is a tensor that the library can read as it lies."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _rows_pitch(t, name):
+    """(rows, width, pitch in elements) of a [..., width] tensor whose rows lie at one pitch
+    (a dense tensor, or a column slice of one)."""
+    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be [..., width] with unit stride along its last dimension")
+    width, rows, pitch = t.shape[-1], 1, None
+    for i in range(t.dim() - 2, -1, -1):
+        if t.shape[i] != 1:
+            if pitch is None:
+                pitch = t.stride(i)
+            elif rows and t.stride(i) != pitch * rows:
+                raise ValueError(f"{name}'s rows must lie at one pitch")
+        rows *= t.shape[i]
+    pitch = width if pitch is None else pitch
+    if rows > 1 and pitch < width:
+        raise ValueError(f"{name}'s rows overlap")
+    return rows, width, max(pitch, width)
+
+
+def _qk_params(q, k, outs, freqs, H, H_k, positions, layout, norm, q_gain, k_gain, eps):
+    rows, width, q_pitch = _rows_pitch(q, "q")
+    if width % H != 0:
+        raise ValueError("q's width must be H heads")
+    d_h, code = width // H, _dtype_code(q)
+    k_pitch = 0
+    if k is None:
+        H_k = 0
+    else:
+        H_k = H if H_k is None else H_k
+        _check(k, "k", q.dtype, q)
+        k_rows, k_width, k_pitch = _rows_pitch(k, "k")
+        if k_rows != rows or k_width != H_k * d_h:
+            raise ValueError("k must have q's rows and H_k heads of q's head width")
+    for name, t, src in outs:
+        if (t is None) != (src is None):
+            raise ValueError(f"{name} goes with its input")
+        if t is not None:
+            _check(t, name, q.dtype, q, True, src.shape)
+    rotary = 0
+    if freqs is not None:
+        _check(freqs, "freqs", torch.float64, q, True)
+        rotary = 2 * freqs.numel()
+    T = q.shape[-2]
+    if positions is not None:
+        _check(positions, "positions", torch.int32, q, True)
+        if positions.numel() != rows:
+            raise ValueError("positions must hold one entry per row")
+    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if t is not None:
+            _check(t, name, torch.float32, q, True, (d_h,))
+    return tg_qk_params(rows, H, H_k, d_h, rotary, layout, norm, eps, max(T, 1), _ptr(positions), _ptr(freqs),
+                        _ptr(q_gain), _ptr(k_gain), q_pitch, k_pitch, code)
+
+
+def tg_rope_freqs(rotary_dim, *, base=10000.0, factor=1.0, orig_len=0, turns_lo=1.0, turns_hi=32.0, device="cuda"):
+    """float64 [rotary_dim / 2]: radians per position, scaled for contexts `factor` times
+    longer than orig_len positions (0: all of them interpolated; see tango.h)."""
+    buf = (ctypes.c_double * max(1, rotary_dim // 2))()
+    st = load().tg_rope_freqs(int(rotary_dim), float(base), float(factor), int(orig_len), float(turns_lo),
+                              float(turns_hi), buf)
+    if st != TG_OK:
+        raise TgError(st, "tg_rope_freqs")
+    return torch.tensor(list(buf)[:rotary_dim // 2], dtype=torch.float64, device=device)
+
+
+def tango_qk_norm_rope(q, k, q_out, k_out, freqs, *, H, H_k=None, positions=None, layout=TG_ROPE_HALF,
+                       norm=TG_NORM_UNIT, q_gain=None, k_gain=None, eps=1e-6, stream=None):
+    """Norm and rotary position of every head of q [..., T, H * d_h] and k [..., T, H_k *
+    d_h] (k may be None) into q_out, k_out (dense).  q and k may be column slices.  freqs:
+    float64 [rotary / 2] from tg_rope_freqs, or None (no rotation).  positions: int32, one
+    per row, or None (the index along T).  q_gain, k_gain: float32 [d_h] or None."""
+    p = _qk_params(q, k, (("q_out", q_out, q), ("k_out", k_out, k)), freqs, H, H_k, positions, layout, norm, q_gain,
+                   k_gain, eps)
+    st = load().tango_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _stream(stream))
+    if st != TG_OK:
+        raise TgError(st, "tango_qk_norm_rope")
+    return q_out, k_out
+
+
+def tango_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, freqs, *, H, H_k=None, positions=None,
+                                layout=TG_ROPE_HALF, norm=TG_NORM_UNIT, q_gain=None, k_gain=None, dq_gain=None,
+                                dk_gain=None, eps=1e-6, ws=None, stream=None):
+    """Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) with respect to q and k (into
+    dq, dk, dense) and, where dq_gain / dk_gain (float32 [d_h]) are given, to the gains."""
+    p = _qk_params(q, k, (("dq_out", dq_out, q), ("dq", dq, q), ("dk_out", dk_out, k), ("dk", dk, k)), freqs, H, H_k,
+                   positions, layout, norm, q_gain, k_gain, eps)
+    for name, t in (("dq_gain", dq_gain), ("dk_gain", dk_gain)):
+        if t is not None:
+            _check(t, name, torch.float32, q, True, (p.d_h,))
+    wbuf = None
+    if dq_gain is not None or dk_gain is not None:
+        wbuf = _scratch(load().tg_workspace_size(TG_WS_QK_BWD, ctypes.byref(p)), q.device, ws, stream)
+    wp, wn = _ws_ptr(wbuf)
+    st = load().tango_qk_norm_rope_backward(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq),
+                                            _ptr(dk), _ptr(dq_gain), _ptr(dk_gain), wp, wn, _stream(stream))
+    if st != TG_OK:
+        raise TgError(st, "tango_qk_norm_rope_backward")
+    return dq, dk
+
+
+# --------------------------------------------------------------------- paged cache
+
+def cache_pools(n_pages, page_size, H, d_h, m_h, *, dtype=torch.bfloat16, m_pitch=None, device="cuda"):
+    """(k_pages, g_pages) of a paged cache: [n_pages, page_size, H * d_h] and [n_pages,
+    page_size, H * m_pitch].  In bf16 the default pitch is m_h rounded up to 8."""
+    if m_pitch is None:
+        m_pitch = -(-m_h // 8) * 8 if dtype == torch.bfloat16 else m_h
+    return (torch.zeros(n_pages, page_size, H * d_h, dtype=dtype, device=device),
+            torch.zeros(n_pages, page_size, H * m_pitch, dtype=dtype, device=device))
+
+
+def paged_params(N, k_pages, g_pages, page_table, cu_new, lens, *, H, max_new, max_len, m_h=None, s=10.0, tau=None,
+                 null_bias=None, v_pitch=0) -> tg_paged_params:
+    """tg_paged_params of a batch: page_table int32 [B, pages], cu_new int32 [B + 1], lens
+    int32 [B]."""
+    n_pages, page_size, dqk = k_pages.shape
+    if dqk % H != 0 or tuple(g_pages.shape[:2]) != (n_pages, page_size) or g_pages.shape[2] % H != 0:
+        raise ValueError("k_pages and g_pages must be [n_pages, page_size, H * width]")
+    _check(k_pages, "k_pages", dense=True)
+    _check(g_pages, "g_pages", k_pages.dtype, k_pages, True)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, pages]")
+    B = page_table.shape[0]
+    for name, t, shape in (("page_table", page_table, None), ("cu_new", cu_new, (B + 1,)), ("lens", lens, (B,))):
+        _check(t, name, torch.int32, k_pages, True, shape)
+    for name, t in (("tau", tau), ("null_bias", null_bias)):
+        if t is not None:
+            _check(t, name, torch.float32, k_pages, True, (H,))
+    pitch = g_pages.shape[2] // H
+    m_h = pitch if m_h is None else int(m_h)
+    return tg_paged_params(B, H, dqk // H, H * m_h, pitch, int(N), int(max_new), int(max_len), page_size, n_pages,
+                           page_table.shape[1], _ptr(cu_new), _ptr(lens), _ptr(page_table), float(s), _ptr(tau),
+                           _ptr(null_bias), int(v_pitch), _dtype_code(k_pages))
+
+
+def tango_cache_append(q, k, g, q_out, k_pages, g_pages, page_table, cu_new, lens, freqs, *, H, m_h=None,
+                       layout=TG_ROPE_HALF, norm=TG_NORM_UNIT, eps=1e-6, silu=True, stream=None):
+    """Appends the new tokens of a ragged batch to the paged cache: k [N, H * d_h] normed
+    and rotated at its position, g [N, H * pitch] (the gate projection; through SiLU unless
+    silu=False).  q (or None) is normed and rotated into q_out for the aggregation.  lens
+    [B] counts the new tokens in; cu_new [B + 1] are the sequences' row offsets."""
+    max_len = page_table.shape[-1] * k_pages.shape[1]
+    N, _, k_pitch = _rows_pitch(k, "k")
+    p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=max(1, N), max_len=max_len, m_h=m_h)
+    _check(k, "k", k_pages.dtype, k_pages)
+    _check(g, "g", k_pages.dtype, k_pages)
+    g_rows, g_width, g_pitch = _rows_pitch(g, "g")
+    if k.shape[-1] != k_pages.shape[2] or g_width != g_pages.shape[2] or g_rows != N:
+        raise ValueError("k and g must have one row per new token, as wide as the cache's")
+    q_pitch = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q_out goes with q")
+    if q is not None:
+        _check(q, "q", k.dtype, k)
+        q_rows, q_width, q_pitch = _rows_pitch(q, "q")
+        if q_rows != N or q_width != k.shape[-1]:
+            raise ValueError("q must have k's rows and width")
+        _check(q_out, "q_out", q.dtype, q, True, q.shape)
+    rotary = 0
+    if freqs is not None:
+        _check(freqs, "freqs", torch.float64, k, True)
+        rotary = 2 * freqs.numel()
+    a = tg_append_params(rotary, layout, norm, eps, _ptr(freqs), 1 if silu else 0, q_pitch, k_pitch, g_pitch)
+    st = load().tango_cache_append(ctypes.byref(p), ctypes.byref(a), _ptr(q), _ptr(k), _ptr(g), _ptr(q_out),
+                                   _ptr(k_pages), _ptr(g_pages), _stream(stream))
+    if st != TG_OK:
+        raise TgError(st, "tango_cache_append")
+    return q_out
+
+
+def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens, *, H, max_new, max_len, s=10.0,
+                          tau=None, null_bias=None, m_h=None, ws=None, stream=None):
+    """TANGO aggregation of the new tokens (already appended) over the paged cache.  q [N,
+    H * d_h] unit vectors per head; v [N, H * pitch] or None (out = gbar); out [N, H *
+    pitch].  max_new, max_len: host bounds of the sequences' new tokens and lengths."""
+    N, q_width, q_pitch = _rows_pitch(q, "q")
+    v_pitch = 0
+    _check(q, "q", k_pages.dtype, k_pages, True)
+    _check(out, "out", k_pages.dtype, k_pages, True)
+    if v is not None:
+        _check(v, "v", k_pages.dtype, k_pages)
+        v_rows, v_width, v_pitch = _rows_pitch(v, "v")
+        if v_rows != N or v_width != g_pages.shape[-1]:
+            raise ValueError("v must have one row per new token, as wide as the cache's gates")
+    p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=max_new, max_len=max_len, m_h=m_h,
+                     s=s, tau=tau, null_bias=null_bias, v_pitch=v_pitch)
+    if q_width != k_pages.shape[2] or out.numel() != N * g_pages.shape[2]:
+        raise ValueError("q and out must have one row per new token, as wide as the cache's")
+    wbuf = _scratch(load().tg_workspace_size(TG_WS_PAGED, ctypes.byref(p)), q.device, ws, stream)
+    wp, wn = _ws_ptr(wbuf)
+    st = load().tango_paged_aggregate(ctypes.byref(p), _ptr(q), _ptr(v), _ptr(out), _ptr(k_pages), _ptr(g_pages), wp, wn,
+                                      _stream(stream))
+    if st != TG_OK:
+        raise TgError(st, "tango_paged_aggregate")
     return out

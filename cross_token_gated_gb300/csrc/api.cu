@@ -1,6 +1,7 @@
 // C ABI of the gate-aggregation library: argument validation, workspace layout,
 // dispatch to the kernels, and the per-device error word.  See include/tango.h.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -9,6 +10,7 @@
 #include "tango.h"
 #include "tg_kernels.h"
 #include "tg_common.cuh"
+#include "tg_serve.h"
 #include "tg_tc.h"
 
 namespace tg {
@@ -485,6 +487,85 @@ tg_status aggregate_backward(bool wango, const tg_agg_params* p, const void* q, 
   return TG_OK;
 }
 
+// ---- norm and rotary position of q and k; the paged cache
+bool rope_ok(int rotary, int d_h, int layout, int norm, float eps, const double* freqs) {
+  if (rotary < 0 || rotary > d_h || rotary % 2 != 0 || (rotary > 0 && !freqs)) return false;
+  if (layout != TG_ROPE_HALF && layout != TG_ROPE_INTERLEAVED) return false;
+  if (norm != TG_NORM_NONE && norm != TG_NORM_UNIT && norm != TG_NORM_RMS) return false;
+  return norm != TG_NORM_RMS || eps > 0.f;
+}
+
+constexpr int kMaxQkHeads = 1024;
+
+tg_status validate_qk(const tg_qk_params* p) {
+  if (!p) return TG_ERR_INVALID_ARG;
+  if (p->rows < 0 || p->H < 1 || p->H > kMaxQkHeads || p->H_k < 0 || p->H_k > kMaxQkHeads || p->d_h < 1)
+    return TG_ERR_INVALID_ARG;
+  if (p->dtype != TG_F32 && p->dtype != TG_BF16) return TG_ERR_INVALID_ARG;
+  if (!rope_ok(p->rotary_dim, p->d_h, p->layout, p->norm, p->eps, p->freqs)) return TG_ERR_INVALID_ARG;
+  if (!p->positions && p->T < 1) return TG_ERR_INVALID_ARG;
+  if (p->q_pitch != 0 && p->q_pitch < (long long)p->H * p->d_h) return TG_ERR_INVALID_ARG;
+  if (p->k_pitch != 0 && p->k_pitch < (long long)p->H_k * p->d_h) return TG_ERR_INVALID_ARG;
+  if (p->d_h > 128) return TG_ERR_UNSUPPORTED;
+  if (p->rows > (1LL << 40)) return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+QkCall qk_call(const tg_qk_params* p, const void* q, const void* k) {
+  QkCall c = {};
+  c.rows = p->rows; c.H = p->H; c.Hk = p->H_k; c.d_h = p->d_h; c.rotary = p->rotary_dim;
+  c.layout = p->layout; c.norm = p->norm; c.T = p->positions ? 1 : p->T; c.eps = p->eps;
+  c.positions = p->positions; c.freqs = p->freqs; c.q_gain = p->q_gain; c.k_gain = p->k_gain;
+  c.q_pitch = p->q_pitch ? p->q_pitch : (long long)p->H * p->d_h;
+  c.k_pitch = p->k_pitch ? p->k_pitch : (long long)p->H_k * p->d_h;
+  c.q = q; c.k = k;
+  return c;
+}
+
+tg_status validate_paged(const tg_paged_params* p) {
+  if (!p) return TG_ERR_INVALID_ARG;
+  if (p->B < 1 || p->H < 1 || p->H > TG_MAX_HEADS || p->d_h < 1 || p->m < 1 || p->m % p->H != 0)
+    return TG_ERR_INVALID_ARG;
+  if (p->m_pitch != 0 && p->m_pitch < p->m / p->H) return TG_ERR_INVALID_ARG;
+  if (p->N < 0 || p->max_new < 1 || p->max_len < 1 || p->page_size < 1 || p->n_pages < 1 || p->table_pitch < 1)
+    return TG_ERR_INVALID_ARG;
+  if ((long long)p->table_pitch * p->page_size < p->max_len) return TG_ERR_INVALID_ARG;
+  if (p->dtype != TG_F32 && p->dtype != TG_BF16) return TG_ERR_INVALID_ARG;
+  if (!p->cu_new || !p->lens || !p->page_table) return TG_ERR_INVALID_ARG;
+  if (!p->tau && !(p->s >= 0.f && p->s <= 20.f)) return TG_ERR_INVALID_ARG;
+  const long long width = (long long)p->H * (p->m_pitch ? p->m_pitch : p->m / p->H);
+  if (p->v_pitch != 0 && p->v_pitch < width) return TG_ERR_INVALID_ARG;
+  if (p->d_h > 128 || p->page_size > 65536 || width > (1LL << 30)) return TG_ERR_UNSUPPORTED;
+  // slot numbers of the pool, and rows plus sequences, stay ints
+  if ((long long)p->n_pages * p->page_size > (1LL << 31) - 1) return TG_ERR_UNSUPPORTED;
+  if ((long long)p->N + 128LL * p->B > (1LL << 30) || p->max_len > (1 << 30)) return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
+PagedBatch paged_batch(const tg_paged_params* p, unsigned* err) {
+  PagedBatch b;
+  b.B = p->B; b.N = p->N; b.max_new = p->max_new; b.max_len = p->max_len;
+  b.page_size = p->page_size; b.n_pages = p->n_pages; b.table_pitch = p->table_pitch;
+  b.cu_new = p->cu_new; b.lens = p->lens; b.page_table = p->page_table; b.err = err;
+  return b;
+}
+
+PagedCall paged_call(const tg_paged_params* p, unsigned* err) {
+  PagedCall c = {};
+  c.p = paged_batch(p, err);
+  c.H = p->H; c.d_h = p->d_h; c.m_h = p->m / p->H; c.m_pitch = p->m_pitch ? p->m_pitch : c.m_h;
+  c.s = p->s; c.tau = p->tau; c.null_bias = p->null_bias;
+  c.v_pitch = p->v_pitch ? p->v_pitch : (long long)c.H * c.m_pitch;
+  return c;
+}
+
+size_t paged_ws_bytes(const tg_paged_params* p) {
+  if (p->N == 0) return 0;
+  return paged_simt_ws_bytes(p->dtype, paged_call(p, nullptr));
+}
+
 }  // namespace
 }  // namespace tg
 
@@ -691,8 +772,128 @@ tg_status wango_decode_step(const tg_agg_params* p, long long pos, const void* q
                                          k, g, v, out, ds, err, stream));
 }
 
+tg_status tango_qk_norm_rope(const tg_qk_params* p, const void* q, const void* k, void* q_out, void* k_out,
+                             tg_stream_t stream) {
+  tg_status st = validate_qk(p);
+  if (st != TG_OK) return st;
+  if (p->rows == 0) return TG_OK;  // an empty tensor may have no address
+  if (!q || !q_out || (p->H_k > 0 && (!k || !k_out)) || (p->H_k == 0 && (k || k_out))) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  const void* ptrs[] = {q, k, q_out, k_out};
+  for (const void* x : ptrs)
+    if (!aligned_to(x, es)) return TG_ERR_UNSUPPORTED;
+  QkCall c = qk_call(p, q, k);
+  c.q_out = q_out; c.k_out = k_out;
+  return cuda_status(launch_qk_forward(p->dtype, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tango_qk_norm_rope_backward(const tg_qk_params* p, const void* q, const void* k, const void* dq_out,
+                                      const void* dk_out, void* dq, void* dk, float* dq_gain, float* dk_gain, void* ws,
+                                      size_t ws_bytes, tg_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  tg_status st = validate_qk(p);
+  if (st != TG_OK) return st;
+  const bool has_k = p->H_k > 0;
+  if ((dq_gain && !p->q_gain) || (dk_gain && (!p->k_gain || !has_k))) return TG_ERR_INVALID_ARG;
+  if (p->rows == 0) {  // empty sums (and an empty tensor may have no address)
+    cudaError_t e = dq_gain ? cudaMemsetAsync(dq_gain, 0, p->d_h * sizeof(float), stream) : cudaSuccess;
+    if (e == cudaSuccess && dk_gain) e = cudaMemsetAsync(dk_gain, 0, p->d_h * sizeof(float), stream);
+    return cuda_status(e);
+  }
+  if (!q || !dq_out || !dq || (has_k && (!k || !dk_out || !dk)) || (!has_k && (k || dk_out || dk)))
+    return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  const void* ptrs[] = {q, k, dq_out, dk_out, dq, dk};
+  for (const void* x : ptrs)
+    if (!aligned_to(x, es)) return TG_ERR_UNSUPPORTED;
+  if (dq_gain || dk_gain) {
+    st = check_ws(ws, ws_bytes, align256(qk_backward_part_bytes(p->d_h)));
+    if (st != TG_OK) return st;
+  }
+  QkCall c = qk_call(p, q, k);
+  c.dq_out = dq_out; c.dk_out = dk_out; c.dq = dq; c.dk = dk;
+  c.dq_gain = dq_gain; c.dk_gain = dk_gain;
+  c.part = static_cast<float*>(ws);
+  return cuda_status(launch_qk_backward(p->dtype, c, stream));
+}
+
+tg_status tg_rope_freqs(int rotary_dim, double base, double factor, long long orig_len, double turns_lo,
+                        double turns_hi, double* freqs) {
+  if (rotary_dim < 0 || rotary_dim % 2 != 0 || (rotary_dim > 0 && !freqs)) return TG_ERR_INVALID_ARG;
+  if (!(base > 0) || !(factor >= 1) || orig_len < 0) return TG_ERR_INVALID_ARG;
+  if (orig_len > 0 && !(turns_lo >= 0 && turns_hi > turns_lo)) return TG_ERR_INVALID_ARG;
+  for (int c = 0; c < rotary_dim / 2; ++c) {
+    const double f = pow(base, -2.0 * c / rotary_dim);
+    double w = 0.0;
+    if (orig_len > 0) {
+      w = ((double)orig_len * f / 6.283185307179586 - turns_lo) / (turns_hi - turns_lo);
+      w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+    }
+    freqs[c] = f * (w + (1.0 - w) / factor);
+  }
+  return TG_OK;
+}
+
+tg_status tango_cache_append(const tg_paged_params* p, const tg_append_params* a, const void* q, const void* k,
+                             const void* g, void* q_out, void* k_pages, void* g_pages, tg_stream_t stream) {
+  tg_status st = validate_paged(p);
+  if (st != TG_OK) return st;
+  if (!a || !rope_ok(a->rotary_dim, p->d_h, a->layout, a->norm, a->eps, a->freqs)) return TG_ERR_INVALID_ARG;
+  AppendCall c = {};
+  c.H = p->H; c.d_h = p->d_h; c.m_h = p->m / p->H; c.m_pitch = p->m_pitch ? p->m_pitch : c.m_h;
+  const long long dqk = (long long)p->H * p->d_h, width = (long long)p->H * c.m_pitch;
+  if ((a->q_pitch != 0 && a->q_pitch < dqk) || (a->k_pitch != 0 && a->k_pitch < dqk) ||
+      (a->g_pitch != 0 && a->g_pitch < width))
+    return TG_ERR_INVALID_ARG;
+  if (p->N == 0) return TG_OK;
+  if (!k || !g || !k_pages || !g_pages || (q == nullptr) != (q_out == nullptr)) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  const void* ptrs[] = {q, k, g, q_out, k_pages, g_pages};
+  for (const void* x : ptrs)
+    if (!aligned_to(x, es)) return TG_ERR_UNSUPPORTED;
+  unsigned* err = nullptr;
+  if (error_word(&err) != cudaSuccess) return TG_ERR_CUDA;
+  c.p = paged_batch(p, err);
+  c.rotary = a->rotary_dim; c.layout = a->layout; c.norm = a->norm; c.eps = a->eps; c.freqs = a->freqs;
+  c.silu = a->silu != 0;
+  c.q_pitch = a->q_pitch ? a->q_pitch : dqk;
+  c.k_pitch = a->k_pitch ? a->k_pitch : dqk;
+  c.g_pitch = a->g_pitch ? a->g_pitch : width;
+  c.q = q; c.k = k; c.g = g; c.q_out = q_out; c.k_pages = k_pages; c.g_pages = g_pages;
+  return cuda_status(launch_cache_append(p->dtype, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tango_paged_aggregate(const tg_paged_params* p, const void* q, const void* v, void* out, const void* k_pages,
+                                const void* g_pages, void* ws, size_t ws_bytes, tg_stream_t stream) {
+  tg_status st = validate_paged(p);
+  if (st != TG_OK) return st;
+  if (p->N == 0) return TG_OK;
+  if (!q || !out || !k_pages || !g_pages) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  const void* ptrs[] = {q, v, out, k_pages, g_pages};
+  for (const void* x : ptrs)
+    if (!aligned_to(x, es)) return TG_ERR_UNSUPPORTED;
+  st = check_ws(ws, ws_bytes, paged_ws_bytes(p));
+  if (st != TG_OK) return st;
+  unsigned* err = nullptr;
+  if (error_word(&err) != cudaSuccess) return TG_ERR_CUDA;
+  PagedCall c = paged_call(p, err);
+  c.q = q; c.v = v; c.out = out; c.k_pages = k_pages; c.g_pages = g_pages; c.ws = ws;
+  return cuda_status(launch_paged_simt(p->dtype, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t tg_workspace_size(int which, const void* params) {
   if (!params) return 0;
+  if (which == TG_WS_QK_BWD) {
+    const tg_qk_params* p = static_cast<const tg_qk_params*>(params);
+    if (validate_qk(p) != TG_OK || (!p->q_gain && !p->k_gain)) return 0;
+    return align256(qk_backward_part_bytes(p->d_h));
+  }
+  if (which == TG_WS_PAGED) {
+    const tg_paged_params* p = static_cast<const tg_paged_params*>(params);
+    if (validate_paged(p) != TG_OK) return 0;
+    return paged_ws_bytes(p);
+  }
   if (which == TG_WS_TANGO || which == TG_WS_WANGO) {
     const tg_agg_params* p = static_cast<const tg_agg_params*>(params);
     if (validate_agg(p, which == TG_WS_WANGO) != TG_OK) return 0;

@@ -1,0 +1,378 @@
+// TANGO aggregation of new tokens over a paged cache, CUDA-core kernels ("TANGO:
+// Token-Aggregated Nonlinear Gating Operators ...", sec. 2.1 eq. 5 with sec. 2.2 eq. 6):
+//   out_i = v_i [ sum_{j<=i} w_ij g_j ] / [ sum_{j<=i} w_ij + (i+1) e^{b - tau} ],
+//   w_ij = e^{tau (q_i . k_j - 1)}.
+// The shift by tau cancels; with unit vectors and tau <= 20 every weight lies in
+// [e^-40, 1] and the sums of key ranges simply add, so no running maximum is kept.
+//
+// Rows are taken in tiles of R (1, 2, 4 or 8) new tokens of one sequence.
+//   paged_scores_kernel  one thread per cached key: its R dot products (q in shared memory),
+//       weights in f32 to scratch [tile][head][key][R], and the key span's weight sums.
+//   paged_gates_kernel   per (tile, head, 16-byte columns x 128 threads, span of keys): the
+//       weighted sum over the span's gate rows.  Bound by HBM for few rows: each gate is
+//       read once per tile with 16-byte loads, 8 keys of a thread in flight; a tile's
+//       blocks stand next to each other in the grid, so tiles of one chunk share the
+//       gates in L2.  The spans of one output are joined by the block that finishes last,
+//       in the spans' order (no order-dependent sums).
+// Weights past a row's own position are selected away, not multiplied by zero, so gates of
+// later tokens and of unused slots may be NaN.
+#include "tg_common.cuh"
+#include "tg_kernels.h"
+#include "tg_paged.cuh"
+#include "tg_ptx.cuh"
+#include "tg_serve.h"
+
+namespace tg {
+namespace {
+
+constexpr int kKeysBlk = 128;   // keys of a scores block
+constexpr int kVT = 128;        // column vectors of a gates block
+constexpr int kUnroll = 8;
+
+// Tiles of R rows are numbered so that no scan is needed: sequence b's first tile is
+// cu_new[b] / R + b (the numbers in between are skipped).
+struct TileRef {
+  int b, row0, n, pos0;  // first row, rows (0: no such tile), first row's position
+};
+template <int R>
+__device__ __forceinline__ TileRef find_tile(const PagedBatch& p, int tile, bool flag) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool le = lane * step < n && min(max(p.cu_new[i], 0), p.N) / R + i <= tile;
+    const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
+    const int adv = (cnt - 1) * step;
+    lo += adv;
+    n = min(step, n - adv);
+  }
+  const PagedSeq s = paged_seq(p, lo, flag);
+  const int k = tile - (s.r0 / R + lo);
+  TileRef t{lo, s.r0 + k * R, 0, 0};
+  if (k < 0 || k * R >= s.n) return t;
+  t.n = min(R, s.n - k * R);
+  t.pos0 = s.len - s.n + k * R;
+  return t;
+}
+
+template <typename T>
+struct SimtArgs {
+  PagedBatch p;
+  int H, d_h, m_h, m_pitch, h0;  // heads [h0, h0 + gridDim heads)
+  int key_pitch;                 // keys of a (tile, head) in the weights scratch
+  int spans;                     // score spans: ceil(max_len / kKeysBlk)
+  int span_keys, gspans;         // keys of a gates block's span; spans of the longest sequence
+  int chunks;                    // column chunks of a head
+  float s;
+  const float* tau;
+  const float* null_bias;
+  long long v_pitch;
+  const T *q, *v;
+  T* out;
+  const T *k_pages, *g_pages;
+  float* w;     // [tile][head of the pass][key][R]
+  float* den;   // [tile][head of the pass][span][R]
+  float* part;  // [tile][head of the pass][chunk][gspan][R][128 EV]
+  int* count;   // [tile][head of the pass][chunk]: spans that are done
+};
+
+// grid (tiles, heads, spans), 128 threads.
+template <typename T, int R, bool kVec>
+__global__ void __launch_bounds__(kKeysBlk) paged_scores_kernel(const SimtArgs<T> a) {
+  __shared__ __align__(16) float qs[R][128];
+  __shared__ float red[kKeysBlk / 32][R];
+  const int tile = blockIdx.x, hl = blockIdx.y, head = a.h0 + hl, t = threadIdx.x;
+  const size_t th = (size_t)tile * gridDim.y + hl;
+  if (blockIdx.z == 0 && a.count)
+    for (int c = t; c < a.chunks; c += kKeysBlk) a.count[th * a.chunks + c] = 0;
+  const TileRef tr = find_tile<R>(a.p, tile, hl == 0 && blockIdx.z == 0);
+  const int vis = tr.pos0 + tr.n;  // keys that the last row sees
+  if (tr.n == 0 || (int)blockIdx.z * kKeysBlk >= vis) return;
+  for (int i = t; i < tr.n * a.d_h; i += kKeysBlk) {
+    const int r = i / a.d_h, c = i - r * a.d_h;
+    qs[r][c] = io<T>::ld(a.q + ((size_t)(tr.row0 + r) * a.H + head) * a.d_h + c);
+  }
+  __syncthreads();
+  const int key = blockIdx.z * kKeysBlk + t;
+  const float tau = head_tau(a.tau, a.s, head, a.p.err, kKernPaged);
+  float x[R] = {};
+  if (key < vis) {
+    const int pi = key / a.p.page_size, pg = paged_page(a.p, tr.b, pi);
+    if (pg >= 0) {
+      const T* kp = a.k_pages + (((size_t)pg * a.p.page_size + (key - pi * a.p.page_size)) * a.H + head) * a.d_h;
+      if (kVec) {
+        constexpr int EV = 16 / sizeof(T);
+#pragma unroll 4
+        for (int c = 0; c < a.d_h; c += EV) {
+          const uint4 u = *reinterpret_cast<const uint4*>(kp + c);
+          const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if (sizeof(T) == 2) {
+                x[r] = fmaf(ptx::bf16lo(uu[e]), qs[r][c + 2 * e], x[r]);
+                x[r] = fmaf(ptx::bf16hi(uu[e]), qs[r][c + 2 * e + 1], x[r]);
+              } else {
+                x[r] = fmaf(__uint_as_float(uu[e]), qs[r][c + e], x[r]);
+              }
+            }
+          }
+        }
+      } else {
+        for (int c = 0; c < a.d_h; ++c) {
+          const float kv = io<T>::ld(kp + c);
+#pragma unroll
+          for (int r = 0; r < R; ++r) x[r] = fmaf(kv, qs[r][c], x[r]);
+        }
+      }
+    }
+  }
+  float* dst = a.w + (th * a.key_pitch + key) * R;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float w = r < tr.n && key <= tr.pos0 + r ? exp2f(tau * kLog2e * (x[r] - 1.f)) : 0.f;
+    if (key < vis) dst[r] = w;
+    float s = w;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((t & 31) == 0) red[t / 32][r] = s;
+  }
+  __syncthreads();
+  if (t < R) {
+    float s = 0.f;
+    for (int i = 0; i < kKeysBlk / 32; ++i) s += red[i][t];
+    a.den[(th * a.spans + blockIdx.z) * R + t] = s;
+  }
+}
+
+template <typename T> struct Cols;
+template <> struct Cols<float> {
+  static constexpr int EV = 4;
+  static __device__ __forceinline__ void get(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+};
+template <> struct Cols<__nv_bfloat16> {
+  static constexpr int EV = 8;
+  static __device__ __forceinline__ void get(const uint4& u, float* f) {
+    f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
+    f[4] = ptx::bf16lo(u.z); f[5] = ptx::bf16hi(u.z); f[6] = ptx::bf16lo(u.w); f[7] = ptx::bf16hi(u.w);
+  }
+};
+
+constexpr int kSpanMax = 512;
+
+// grid (tiles, chunks * heads, gspans), 128 threads; a thread owns EV columns of R rows.
+template <typename T, int R, bool kVec>
+__global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
+  constexpr int EV = Cols<T>::EV;
+  __shared__ int tok[kSpanMax];
+  __shared__ float dinv[R];
+  __shared__ int last;
+  const int tile = blockIdx.x, hl = blockIdx.y / a.chunks, chunk = blockIdx.y - hl * a.chunks, head = a.h0 + hl;
+  const int heads = gridDim.y / a.chunks, t = threadIdx.x;
+  const TileRef tr = find_tile<R>(a.p, tile, false);
+  if (tr.n == 0) return;
+  const int vis = max(0, tr.pos0 + tr.n), k0 = blockIdx.z * a.span_keys;
+  const int nsp = max(1, (vis + a.span_keys - 1) / a.span_keys);
+  if ((int)blockIdx.z >= nsp) return;
+  const int nk = min(a.span_keys, vis - k0);
+  const size_t th = (size_t)tile * heads + hl;
+  for (int i = t; i < nk; i += kVT) {
+    const int key = k0 + i, pi = key / a.p.page_size, pg = paged_page(a.p, tr.b, pi);
+    tok[i] = pg < 0 ? -1 : pg * a.p.page_size + (key - pi * a.p.page_size);
+  }
+  __syncthreads();
+  const int c0 = (chunk * kVT + t) * EV;  // first column of the head
+  const bool live = c0 < a.m_h;
+  float acc[R][EV] = {};
+  const size_t row_elems = (size_t)a.H * a.m_pitch;
+  const T* gcol = a.g_pages + (size_t)head * a.m_pitch + c0;
+  const float* w = a.w + (th * a.key_pitch + k0) * R;
+  // keys that every row of the tile sees, then the last ones, which some rows do not
+  const int all = min(nk, max(0, tr.pos0 + 1 - k0));
+  if (live) {
+    int i = 0;
+    if (kVec) {
+      for (; i + kUnroll <= all; i += kUnroll) {
+        uint4 u[kUnroll];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          const int tk = tok[i + j];
+          u[j] = tk >= 0 ? ptx::ld_global_v4(gcol + (size_t)tk * row_elems) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          float g[EV];
+          Cols<T>::get(u[j], g);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float wr = __ldg(w + (size_t)(i + j) * R + r);
+#pragma unroll
+            for (int e = 0; e < EV; ++e) acc[r][e] = fmaf(wr, g[e], acc[r][e]);
+          }
+        }
+      }
+    }
+    for (; i < nk; ++i) {
+      const int tk = tok[i];
+      if (tk < 0) continue;
+      float g[EV];
+      if (kVec) {
+        Cols<T>::get(ptx::ld_global_v4(gcol + (size_t)tk * row_elems), g);
+      } else {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) g[e] = c0 + e < a.m_h ? io<T>::ld(gcol + (size_t)tk * row_elems + e) : 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float wr = __ldg(w + (size_t)i * R + r);
+        if (i < all || k0 + i <= tr.pos0 + r) {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) acc[r][e] = fmaf(wr, g[e], acc[r][e]);
+        }
+      }
+    }
+  }
+  if (nsp > 1) {
+    float* base = a.part + ((th * a.chunks + chunk) * a.gspans) * (size_t)(R * kVT * EV);
+    float* mine = base + (size_t)blockIdx.z * (R * kVT * EV) + t * EV;
+    if (live) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < EV; e += 4)
+          *reinterpret_cast<float4*>(mine + (size_t)r * (kVT * EV) + e) =
+              make_float4(acc[r][e], acc[r][e + 1], acc[r][e + 2], acc[r][e + 3]);
+    }
+    __threadfence();
+    __syncthreads();
+    if (t == 0) last = atomicAdd(a.count + th * a.chunks + chunk, 1) == nsp - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if (live) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < EV; e += 4) {
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int z = 0; z < nsp; ++z) {
+            const float4 x =
+                __ldcg(reinterpret_cast<const float4*>(base + ((size_t)z * R + r) * (kVT * EV) + t * EV + e));
+            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+          }
+          acc[r][e] = s.x; acc[r][e + 1] = s.y; acc[r][e + 2] = s.z; acc[r][e + 3] = s.w;
+        }
+    }
+  }
+  // denominators of the tile's rows: the spans' sums, and the null gate
+  if (t < R) {
+    const int pos = tr.pos0 + t, ns = (vis + kKeysBlk - 1) / kKeysBlk;
+    float d = 0.f;
+    for (int z = 0; z < ns; ++z) d += a.den[(th * a.spans + z) * R + t];
+    if (a.null_bias && pos >= 0) {
+      const float tau = head_tau(a.tau, a.s, head, a.p.err, kKernPaged);
+      d += (float)(pos + 1) * expf(a.null_bias[head] - tau);
+    }
+    dinv[t] = t < tr.n && pos >= 0 ? 1.f / d : 0.f;
+  }
+  __syncthreads();
+  if (!live) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r >= tr.n) break;
+    const size_t row = tr.row0 + r, col = (size_t)head * a.m_pitch + c0;
+#pragma unroll
+    for (int e = 0; e < EV; ++e) {
+      if (c0 + e >= a.m_h) break;
+      float y = tr.pos0 + r >= 0 ? acc[r][e] * dinv[r] : 0.f;
+      if (a.v && tr.pos0 + r >= 0) y *= io<T>::ld(a.v + row * a.v_pitch + col + e);
+      io<T>::st(a.out + row * row_elems + col + e, y);
+    }
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct SimtPlan {
+  int R, tiles, heads, spans, span_keys, gspans, chunks, key_pitch;
+  size_t w, den, part, count, total;
+};
+
+SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
+  SimtPlan l;
+  const int EV = dt == TG_F32 ? 4 : 8;
+  l.R = c.p.max_new >= 5 ? 8 : c.p.max_new >= 3 ? 4 : c.p.max_new;
+  l.tiles = c.p.N / l.R + c.p.B;
+  l.spans = ceil_div(c.p.max_len, kKeysBlk);
+  l.key_pitch = l.spans * kKeysBlk;
+  l.chunks = ceil_div(c.m_h, kVT * EV);
+  l.span_keys = kSpanMax;
+  l.gspans = ceil_div(c.p.max_len, l.span_keys);
+  // heads of a pass: as many as keep the scratch near 1 GB
+  const size_t per_head = (size_t)l.tiles * ((size_t)l.key_pitch * l.R * 4 + (size_t)l.spans * l.R * 4 +
+                                             (size_t)l.chunks * l.gspans * l.R * kVT * EV * 4 + (size_t)l.chunks * 4);
+  const size_t fit = (size_t(1) << 30) / (per_head ? per_head : 1);
+  l.heads = (int)(fit < 1 ? 1 : fit > (size_t)c.H ? (size_t)c.H : fit);
+  const size_t th = (size_t)l.tiles * l.heads;
+  l.w = 0;
+  l.den = l.w + align256(th * l.key_pitch * l.R * 4);
+  l.part = l.den + align256(th * l.spans * l.R * 4);
+  l.count = l.part + align256(th * l.chunks * l.gspans * l.R * kVT * EV * 4);
+  l.total = l.count + align256(th * l.chunks * 4);
+  return l;
+}
+
+template <typename T, int R>
+cudaError_t run(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
+  SimtArgs<T> a;
+  a.p = c.p; a.H = c.H; a.d_h = c.d_h; a.m_h = c.m_h; a.m_pitch = c.m_pitch;
+  a.key_pitch = l.key_pitch; a.spans = l.spans; a.span_keys = l.span_keys; a.gspans = l.gspans; a.chunks = l.chunks;
+  a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
+  a.q = static_cast<const T*>(c.q); a.v = static_cast<const T*>(c.v); a.out = static_cast<T*>(c.out);
+  a.k_pages = static_cast<const T*>(c.k_pages); a.g_pages = static_cast<const T*>(c.g_pages);
+  char* base = static_cast<char*>(c.ws);
+  a.w = reinterpret_cast<float*>(base + l.w);
+  a.den = reinterpret_cast<float*>(base + l.den);
+  a.part = reinterpret_cast<float*>(base + l.part);
+  a.count = reinterpret_cast<int*>(base + l.count);
+  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const bool kvec = al(c.k_pages) && c.d_h * sizeof(T) % 16 == 0;
+  // whole 16-byte vectors of a head: its last one may run into the pitch's padding, never
+  // into the next head
+  const bool gvec = al(c.g_pages) && c.m_pitch * sizeof(T) % 16 == 0;
+  for (a.h0 = 0; a.h0 < c.H; a.h0 += l.heads) {
+    const int heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
+    const dim3 gs(l.tiles, heads, l.spans), gg(l.tiles, heads * l.chunks, l.gspans);
+    if (gs.z > 65535 || gg.y > 65535 || gg.z > 65535) return cudaErrorInvalidConfiguration;
+    if (kvec) paged_scores_kernel<T, R, true><<<gs, kKeysBlk, 0, s>>>(a);
+    else paged_scores_kernel<T, R, false><<<gs, kKeysBlk, 0, s>>>(a);
+    if (gvec) paged_gates_kernel<T, R, true><<<gg, kVT, 0, s>>>(a);
+    else paged_gates_kernel<T, R, false><<<gg, kVT, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t run_t(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
+  switch (l.R) {
+    case 1: return run<T, 1>(c, l, s);
+    case 2: return run<T, 2>(c, l, s);
+    case 4: return run<T, 4>(c, l, s);
+    default: return run<T, 8>(c, l, s);
+  }
+}
+
+}  // namespace
+
+size_t paged_simt_ws_bytes(tg_dtype dt, const PagedCall& c) { return simt_plan(dt, c).total; }
+
+cudaError_t launch_paged_simt(tg_dtype dt, const PagedCall& c, cudaStream_t s) {
+  const SimtPlan l = simt_plan(dt, c);
+  return dt == TG_F32 ? run_t<float>(c, l, s) : run_t<__nv_bfloat16>(c, l, s);
+}
+
+}  // namespace tg

@@ -1,0 +1,716 @@
+// Per-head norm of queries and keys with the rotary position in the same pass, its
+// gradient, and the append of new keys and gates to a paged cache ("TANGO: Token-Aggregated
+// Nonlinear Gating Operators ...", sec. 2.1: RoPE and the unit norm of q and k; eq. 2: the
+// SiLU gate).
+//
+//   n = x r,  z = gain n,  out = R(pos) z;   r = 1/max(|x|, 1e-12) or 1/sqrt(mean x^2 + eps) or 1
+//   backward: dz = R^T dout, dgain = sum dz n, dn = gain dz, dx = r (dn - n <n, dn>)
+//
+// Angles: a pair's frequency becomes turns per position as a 64-bit fraction F = frac(f / 2 pi)
+// 2^64, and pos * F wraps at whole turns by itself; its high 32 bits are the angle in units
+// of 2^-31 half turns, exact at any position, for sincospi.
+//
+// All of it is bound by HBM bandwidth (each value is read and written once) and, for few
+// rows, by launch latency.  A block takes a few rows at a time: one thread per (row, pair)
+// forms the angles' cos and sin in shared memory once for all heads of the row (a sincospi
+// per element pair and head would cost more issue slots than the copy leaves), then
+// threads walk the rows' heads in memory order, 32 bytes of a head per thread in two
+// 16-byte vectors, the norm's sums by shuffles between the d_h / E lanes of a head.
+#include <math.h>
+
+#include "tg_common.cuh"
+#include "tg_kernels.h"
+#include "tg_paged.cuh"
+#include "tg_ptx.cuh"
+#include "tg_serve.h"
+
+namespace tg {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 64;  // rotary_dim <= 128
+constexpr int kMaxRowsBlk = 8;
+
+struct QkShared {
+  uint64_t turns[kMaxPairs];
+  float2 cs[kMaxRowsBlk][kMaxPairs];
+};
+
+// Turns per position of frequency f (radians per position, >= 0), as a fraction of 2^64.
+__device__ __forceinline__ uint64_t turn_fraction(double f) {
+  double t = f * 0.15915494309189535;  // 1 / (2 pi)
+  t -= floor(t);
+  return t >= 0.0 && t < 1.0 ? (uint64_t)(t * 18446744073709551616.0) : 0;  // NaN, inf: no rotation
+}
+__device__ __forceinline__ float2 turn_cos_sin(uint64_t turns, int pos) {
+  const int half_turns = (int)((turns * (uint64_t)(int64_t)pos) >> 32);
+  float s, c;
+  sincospif((float)half_turns * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  return make_float2(c, s);
+}
+
+// A head's values as the threads of its group hold them: V pairs (x[i], y[i]).  Rotated
+// lanes hold pairs that turn together; the other lanes hold 2 V columns that pass.
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int E = 8;  // values of a thread: two 16-byte vectors
+  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int E = 16;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
+    f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
+    f[4] = ptx::bf16lo(u.z); f[5] = ptx::bf16hi(u.z); f[6] = ptx::bf16lo(u.w); f[7] = ptx::bf16hi(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]), ptx::pack_bf16x2(f[4], f[5]),
+                      ptx::pack_bf16x2(f[6], f[7]));
+  }
+};
+
+// Where lane l of a head's group finds its two vectors, and whether it rotates.
+struct LaneMap {
+  int off0, off1, pair0;
+  bool rot, half;
+};
+template <typename T>
+__device__ __forceinline__ LaneMap lane_map(int l, int rotary, int layout) {
+  constexpr int E = Vec<T>::E, V = E / 2;
+  LaneMap m;
+  m.rot = l < rotary / E;
+  m.half = m.rot && layout == TG_ROPE_HALF;
+  m.off0 = m.half ? l * V : l * E;
+  m.off1 = m.half ? rotary / 2 + l * V : l * E + V;
+  m.pair0 = l * V;
+  return m;
+}
+
+// The pairs of a lane: half layout pairs a[i] with b[i]; interleaved layout pairs
+// neighbours of the 2 V columns a then b.  sign = -1 turns back.
+template <int V>
+__device__ __forceinline__ void rotate(float* a, float* b, const float2* cs, const LaneMap& m, float sign) {
+  if (!m.rot) return;
+  if (m.half) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 e = cs[m.pair0 + i];
+      const float x = a[i], y = b[i], s = sign * e.y;
+      a[i] = x * e.x - y * s;
+      b[i] = x * s + y * e.x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float* v = i < V / 2 ? a + 2 * i : b + 2 * i - V;
+      const float2 e = cs[m.pair0 + i];
+      const float x = v[0], y = v[1], s = sign * e.y;
+      v[0] = x * e.x - y * s;
+      v[1] = x * s + y * e.x;
+    }
+  }
+}
+
+// Sum over the lh lanes of a head's group (lh a power of two, lanes aligned to it).
+__device__ __forceinline__ float group_sum(float v, int lh) {
+  for (int o = lh >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float inv_norm(float ss, int d_h, int norm, float eps) {
+  if (norm == TG_NORM_UNIT) return 1.f / fmaxf(sqrtf(ss), 1e-12f);
+  if (norm == TG_NORM_RMS) return 1.f / sqrtf(ss / (float)d_h + eps);
+  return 1.f;
+}
+
+// What a forward pass over rows needs, shared by the norm call and the cache append.
+struct FwdRows {
+  int d_h, rotary, layout, norm;
+  float eps;
+};
+
+// One head by its group of lanes: load, norm, gain, rotate, store (two vectors per lane).
+template <typename T>
+__device__ __forceinline__ void head_forward(const T* src, T* dst, bool live, const FwdRows& f, const LaneMap& m, int lh,
+                                             const float* gain, const float2* cs) {
+  constexpr int V = Vec<T>::E / 2;
+  float a[V], b[V];
+  uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+  if (live) {
+    u0 = *reinterpret_cast<const uint4*>(src + m.off0);
+    u1 = *reinterpret_cast<const uint4*>(src + m.off1);
+  }
+  Vec<T>::unpack(u0, a);
+  Vec<T>::unpack(u1, b);
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) ss += a[i] * a[i] + b[i] * b[i];
+  const float r = f.norm == TG_NORM_NONE ? 1.f : inv_norm(group_sum(ss, lh), f.d_h, f.norm, f.eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a[i] *= r;
+    b[i] *= r;
+    if (gain) {
+      a[i] *= gain[m.off0 + i];
+      b[i] *= gain[m.off1 + i];
+    }
+  }
+  rotate<V>(a, b, cs, m, 1.f);
+  if (live) {
+    *reinterpret_cast<uint4*>(dst + m.off0) = Vec<T>::pack(a);
+    *reinterpret_cast<uint4*>(dst + m.off1) = Vec<T>::pack(b);
+  }
+}
+
+// A head by a whole warp, any width, pairing and alignment: values go through `buf`
+// (2 x 128 floats per warp).
+template <typename T>
+__device__ __forceinline__ void head_forward_any(const T* src, T* dst, const FwdRows& f, const float* gain,
+                                                 const float2* cs, float* buf) {
+  const int lane = threadIdx.x & 31;
+  float ss = 0.f;
+  for (int c = lane; c < f.d_h; c += 32) {
+    const float x = io<T>::ld(src + c);
+    buf[c] = x;
+    ss += x * x;
+  }
+  const float r = f.norm == TG_NORM_NONE ? 1.f : inv_norm(group_sum(ss, 32), f.d_h, f.norm, f.eps);
+  __syncwarp();
+  const int hp = f.rotary / 2;
+  for (int c = lane; c < f.d_h; c += 32) {
+    float z = buf[c] * r * (gain ? gain[c] : 1.f);
+    if (c < f.rotary) {
+      const bool first = f.layout == TG_ROPE_HALF ? c < hp : !(c & 1);
+      const int pair = f.layout == TG_ROPE_HALF ? (first ? c : c - hp) : c >> 1;
+      const int mate = f.layout == TG_ROPE_HALF ? (first ? c + hp : c - hp) : c ^ 1;
+      const float w = buf[mate] * r * (gain ? gain[mate] : 1.f);
+      const float2 e = cs[pair];
+      z = first ? z * e.x - w * e.y : z * e.x + w * e.y;
+    }
+    io<T>::st(dst + c, z);
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void load_turns(QkShared& sh, const double* freqs, int pairs) {
+  for (int c = threadIdx.x; c < pairs; c += kThreads) sh.turns[c] = turn_fraction(freqs[c]);
+  __syncthreads();
+}
+
+template <typename T>
+struct QkArgs {
+  long long rows;
+  int H, Hk, T_len;
+  FwdRows f;
+  const int* positions;
+  const double* freqs;
+  const float *q_gain, *k_gain;
+  long long q_pitch, k_pitch;
+  const T *q, *k;
+  T *q_out, *k_out;
+  const T *dq_out, *dk_out;  // backward
+  T *dq, *dk;
+  float* part;               // backward: [blocks][2][d_h] gain gradients
+  int want_gain;
+  int rb;                    // rows of a block's step (<= kMaxRowsBlk)
+};
+
+__device__ __forceinline__ int row_pos(const int* positions, int T_len, long long row) {
+  return positions ? positions[row] : (int)(row % T_len);
+}
+
+// The rows' angles: one thread per (row, pair).
+template <typename T>
+__device__ __forceinline__ void row_angles(QkShared& sh, const QkArgs<T>& a, long long row0, int nr) {
+  const int pairs = a.f.rotary / 2;
+  for (int i = threadIdx.x; i < nr * pairs; i += kThreads) {
+    const int r = i / pairs, c = i - r * pairs;
+    sh.cs[r][c] = turn_cos_sin(sh.turns[c], row_pos(a.positions, a.T_len, row0 + r));
+  }
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads) qk_forward_kernel(const QkArgs<T> a) {
+  __shared__ QkShared sh;
+  __shared__ float buf[kVec ? 1 : kThreads / 32][kVec ? 1 : 128];
+  load_turns(sh, a.freqs, a.f.rotary / 2);
+  const int HT = a.H + a.Hk, lh = kVec ? a.f.d_h / Vec<T>::E : 32;
+  const int l = threadIdx.x % lh;
+  const LaneMap m = lane_map<T>(l, a.f.rotary, a.f.layout);
+  for (long long row0 = (long long)blockIdx.x * a.rb; row0 < a.rows; row0 += (long long)gridDim.x * a.rb) {
+    const int nr = (int)min((long long)a.rb, a.rows - row0);
+    row_angles(sh, a, row0, nr);
+    __syncthreads();
+    const int heads = nr * HT;
+    // a whole group takes a head; groups without one keep step with the shuffles
+    for (int h0 = 0; h0 < heads; h0 += kThreads / lh) {
+      const int h = h0 + threadIdx.x / lh;
+      const bool live = h < heads;
+      const int r = live ? h / HT : 0, hh = live ? h - r * HT : 0;
+      const bool is_q = hh < a.H;
+      const long long row = row0 + r;
+      const T* src = is_q ? a.q + row * a.q_pitch + (long long)hh * a.f.d_h
+                          : a.k + row * a.k_pitch + (long long)(hh - a.H) * a.f.d_h;
+      T* dst = is_q ? a.q_out + (row * a.H + hh) * a.f.d_h : a.k_out + (row * a.Hk + hh - a.H) * a.f.d_h;
+      const float* gain = is_q ? a.q_gain : a.k_gain;
+      if (kVec) {
+        head_forward<T>(src, dst, live, a.f, m, lh, gain, sh.cs[r]);
+      } else if (live) {
+        head_forward_any<T>(src, dst, a.f, gain, sh.cs[r], buf[threadIdx.x / 32]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------------ backward
+
+// One tensor's heads (q or k) of a block's rows; the lane's gain gradient goes to ga, gb.
+template <typename T>
+__device__ __forceinline__ void rows_backward(const QkArgs<T>& a, QkShared& sh, long long row0, int nr, int H,
+                                              const T* x, long long pitch, const T* dout, T* dx, const float* gain,
+                                              const LaneMap& m, int lh, float* ga, float* gb) {
+  constexpr int V = Vec<T>::E / 2;
+  const int heads = nr * H;
+  for (int h0 = 0; h0 < heads; h0 += kThreads / lh) {
+    const int h = h0 + threadIdx.x / lh;
+    const bool live = h < heads;
+    const int r = live ? h / H : 0, hh = live ? h - r * H : 0;
+    const long long row = row0 + r, at = (row * H + hh) * a.f.d_h;
+    float xa[V], xb[V], da[V], db[V];
+    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0, w0 = u0, w1 = u0;
+    if (live) {
+      const T* src = x + row * pitch + (long long)hh * a.f.d_h;
+      u0 = *reinterpret_cast<const uint4*>(src + m.off0);
+      u1 = *reinterpret_cast<const uint4*>(src + m.off1);
+      w0 = *reinterpret_cast<const uint4*>(dout + at + m.off0);
+      w1 = *reinterpret_cast<const uint4*>(dout + at + m.off1);
+    }
+    Vec<T>::unpack(u0, xa);
+    Vec<T>::unpack(u1, xb);
+    Vec<T>::unpack(w0, da);
+    Vec<T>::unpack(w1, db);
+    rotate<V>(da, db, sh.cs[r], m, -1.f);  // dz
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+    float rn = 1.f;
+    bool floor_hit = false;
+    if (a.f.norm != TG_NORM_NONE) {
+      ss = group_sum(ss, lh);
+      rn = inv_norm(ss, a.f.d_h, a.f.norm, a.f.eps);
+      floor_hit = a.f.norm == TG_NORM_UNIT && sqrtf(ss) < 1e-12f;
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      xa[i] *= rn;  // n
+      xb[i] *= rn;
+      if (gain) {
+        if (live && ga) {
+          ga[i] = fmaf(da[i], xa[i], ga[i]);
+          gb[i] = fmaf(db[i], xb[i], gb[i]);
+        }
+        da[i] *= gain[m.off0 + i];  // dn
+        db[i] *= gain[m.off1 + i];
+      }
+      dot += xa[i] * da[i] + xb[i] * db[i];
+    }
+    if (a.f.norm != TG_NORM_NONE) {
+      dot = group_sum(dot, lh);
+      if (a.f.norm == TG_NORM_RMS) dot /= (float)a.f.d_h;
+      if (floor_hit) dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        da[i] = rn * (da[i] - xa[i] * dot);
+        db[i] = rn * (db[i] - xb[i] * dot);
+      }
+    }
+    if (live) {
+      *reinterpret_cast<uint4*>(dx + at + m.off0) = Vec<T>::pack(da);
+      *reinterpret_cast<uint4*>(dx + at + m.off1) = Vec<T>::pack(db);
+    }
+  }
+}
+
+// The same by whole warps for any width and alignment; gain gradients go to acc[d_h],
+// one float per column of this warp.
+template <typename T>
+__device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& sh, long long row0, int nr, int H,
+                                                  const T* x, long long pitch, const T* dout, T* dx,
+                                                  const float* gain, float* buf, float* acc) {
+  const int lane = threadIdx.x & 31, hp = a.f.rotary / 2;
+  for (int h = threadIdx.x / 32; h < nr * H; h += kThreads / 32) {
+    const int r = h / H, hh = h - r * H;
+    const long long row = row0 + r, at = (row * H + hh) * a.f.d_h;
+    const T* src = x + row * pitch + (long long)hh * a.f.d_h;
+    float ss = 0.f;
+    for (int c = lane; c < a.f.d_h; c += 32) {
+      const float v = io<T>::ld(src + c);
+      ss += v * v;
+      buf[c] = io<T>::ld(dout + at + c);
+    }
+    float rn = 1.f;
+    bool floor_hit = false;
+    if (a.f.norm != TG_NORM_NONE) {
+      ss = group_sum(ss, 32);
+      rn = inv_norm(ss, a.f.d_h, a.f.norm, a.f.eps);
+      floor_hit = a.f.norm == TG_NORM_UNIT && sqrtf(ss) < 1e-12f;
+    }
+    __syncwarp();
+    float n[4], dn[4], dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = lane + 32 * i;
+      if (c >= a.f.d_h) break;
+      float dz = buf[c];
+      if (c < a.f.rotary) {
+        const bool first = a.f.layout == TG_ROPE_HALF ? c < hp : !(c & 1);
+        const int pair = a.f.layout == TG_ROPE_HALF ? (first ? c : c - hp) : c >> 1;
+        const int mate = a.f.layout == TG_ROPE_HALF ? (first ? c + hp : c - hp) : c ^ 1;
+        const float2 e = sh.cs[r][pair];
+        dz = first ? dz * e.x + buf[mate] * e.y : dz * e.x - buf[mate] * e.y;
+      }
+      n[i] = io<T>::ld(src + c) * rn;
+      if (gain && acc) acc[c] = fmaf(dz, n[i], acc[c]);
+      dn[i] = gain ? dz * gain[c] : dz;
+      dot += n[i] * dn[i];
+    }
+    if (a.f.norm != TG_NORM_NONE) {
+      dot = group_sum(dot, 32);
+      if (a.f.norm == TG_NORM_RMS) dot /= (float)a.f.d_h;
+    }
+    if (floor_hit || a.f.norm == TG_NORM_NONE) dot = 0.f;
+    __syncwarp();  // every lane has read buf, and dout where dx overwrites it
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = lane + 32 * i;
+      if (c >= a.f.d_h) break;
+      io<T>::st(dx + at + c, rn * (dn[i] - n[i] * dot));
+    }
+    __syncwarp();
+  }
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads) qk_backward_kernel(const QkArgs<T> a) {
+  constexpr int V = Vec<T>::E / 2;
+  __shared__ QkShared sh;
+  __shared__ float buf[kVec ? 1 : kThreads / 32][kVec ? 1 : 128];
+  __shared__ float acc[2][kThreads / 32][128];  // gain gradients, one copy per warp
+  load_turns(sh, a.freqs, a.f.rotary / 2);
+  const int lh = kVec ? a.f.d_h / Vec<T>::E : 32, l = threadIdx.x % lh, w = threadIdx.x / 32;
+  const LaneMap m = lane_map<T>(l, a.f.rotary, a.f.layout);
+  if (a.want_gain) {
+    for (int i = threadIdx.x; i < 2 * (kThreads / 32) * 128; i += kThreads) (&acc[0][0][0])[i] = 0.f;
+    __syncthreads();
+  }
+  float qa[V] = {}, qb[V] = {}, ka[V] = {}, kb[V] = {};
+  for (long long row0 = (long long)blockIdx.x * a.rb; row0 < a.rows; row0 += (long long)gridDim.x * a.rb) {
+    const int nr = (int)min((long long)a.rb, a.rows - row0);
+    row_angles(sh, a, row0, nr);
+    __syncthreads();
+    if (kVec) {
+      rows_backward<T>(a, sh, row0, nr, a.H, a.q, a.q_pitch, a.dq_out, a.dq, a.q_gain, m, lh, a.want_gain ? qa : nullptr, qb);
+      rows_backward<T>(a, sh, row0, nr, a.Hk, a.k, a.k_pitch, a.dk_out, a.dk, a.k_gain, m, lh, a.want_gain ? ka : nullptr, kb);
+    } else {
+      rows_backward_any<T>(a, sh, row0, nr, a.H, a.q, a.q_pitch, a.dq_out, a.dq, a.q_gain, buf[kVec ? 0 : w],
+                           a.want_gain ? acc[0][w] : nullptr);
+      rows_backward_any<T>(a, sh, row0, nr, a.Hk, a.k, a.k_pitch, a.dk_out, a.dk, a.k_gain, buf[kVec ? 0 : w],
+                           a.want_gain ? acc[1][w] : nullptr);
+    }
+    __syncthreads();
+  }
+  if (!a.want_gain) return;
+  if (kVec) {
+    // over the warp's heads (lanes l apart by lh), then each warp's copy
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      for (int o = 16; o >= lh; o >>= 1) {
+        qa[i] += __shfl_xor_sync(0xffffffffu, qa[i], o);
+        qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], o);
+        ka[i] += __shfl_xor_sync(0xffffffffu, ka[i], o);
+        kb[i] += __shfl_xor_sync(0xffffffffu, kb[i], o);
+      }
+      if ((threadIdx.x & 31) < lh) {
+        acc[0][w][m.off0 + i] = qa[i];
+        acc[0][w][m.off1 + i] = qb[i];
+        acc[1][w][m.off0 + i] = ka[i];
+        acc[1][w][m.off1 + i] = kb[i];
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.f.d_h; i += kThreads) {
+    const int side = i / a.f.d_h, c = i - side * a.f.d_h;
+    float s = 0.f;
+    for (int k = 0; k < kThreads / 32; ++k) s += acc[side][k][c];
+    a.part[((size_t)blockIdx.x * 2 + side) * a.f.d_h + c] = s;
+  }
+}
+
+// dgain[c] = sum of the blocks' partial sums, in a fixed order: grid (d_h / 8, 2), a warp per
+// column.
+__global__ void __launch_bounds__(256) qk_gain_sum_kernel(const float* part, int blocks, int d_h, float* dqg, float* dkg) {
+  const int c = blockIdx.x * 8 + threadIdx.x / 32, side = blockIdx.y, lane = threadIdx.x & 31;
+  float* dst = side ? dkg : dqg;
+  if (c >= d_h || !dst) return;
+  float s = 0.f;
+  for (int b = lane; b < blocks; b += 32) s += part[((size_t)b * 2 + side) * d_h + c];
+  s = group_sum(s, 32);
+  if (lane == 0) dst[c] = s;
+}
+
+// --------------------------------------------------------------------------- append
+
+template <typename T>
+struct AppendArgs {
+  PagedBatch p;
+  int H, m_h, m_pitch;
+  FwdRows f;
+  const double* freqs;
+  int silu;
+  long long q_pitch, k_pitch, g_pitch;
+  const T *q, *k, *g;
+  T *q_out, *k_pages, *g_pages;
+  int qk_blocks, rb;   // the first qk_blocks blocks take rb rows of q and k at a time
+  int chunks;          // gate chunks of a row
+};
+
+struct Slot {
+  int pos;        // position, negative: none
+  long long tok;  // page * page_size + offset, or -1
+};
+// Where new token `row` goes; a whole warp asks for one row.
+__device__ __forceinline__ Slot find_slot(const PagedBatch& p, int row) {
+  const int b = paged_find(p, row);
+  const PagedSeq s = paged_seq(p, b, true);
+  Slot r{-1, -1};
+  if (row < s.r0 || row >= s.r0 + s.n) {
+    return r;  // a row of no sequence
+  }
+  r.pos = s.len - s.n + (row - s.r0);
+  if (r.pos < 0) return r;
+  const int pi = r.pos / p.page_size, pg = paged_page(p, b, pi);
+  if (pg >= 0) r.tok = (long long)pg * p.page_size + (r.pos - pi * p.page_size);
+  return r;
+}
+
+// x sigmoid(x); the fast exponential's error (a few 2^-22) is far below a bf16 rounding
+template <typename T> __device__ __forceinline__ float silu_of(float x);
+template <> __device__ __forceinline__ float silu_of<float>(float x) { return x / (1.f + expf(-x)); }
+template <> __device__ __forceinline__ float silu_of<__nv_bfloat16>(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+constexpr int kGateVecs = 2;  // 16-byte vectors of a thread in a gate block
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs<T> a) {
+  __shared__ QkShared sh;
+  __shared__ Slot slot[kMaxRowsBlk];
+  __shared__ float buf[kVec ? 1 : kThreads / 32][kVec ? 1 : 128];
+  const int w = threadIdx.x / 32;
+  if ((int)blockIdx.x >= a.qk_blocks) {
+    // ---- gates: one chunk of one row
+    const int gb = blockIdx.x - a.qk_blocks, row = gb / a.chunks, chunk = gb - row * a.chunks;
+    const T* src = a.g + (long long)row * a.g_pitch;
+    if (kVec) {
+      // the loads are on their way before the slot is known
+      constexpr int EV = 16 / sizeof(T);
+      const int nv = a.H * a.m_pitch / EV;
+      uint4 u[kGateVecs];
+      const int v0 = chunk * (kThreads * kGateVecs) + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < kGateVecs; ++i)
+        if (v0 + i * kThreads < nv) u[i] = ptx::ld_global_v4(src + (long long)(v0 + i * kThreads) * EV);
+      const Slot s = find_slot(a.p, row);
+      if (s.tok < 0) return;
+      T* dst = a.g_pages + s.tok * ((long long)a.H * a.m_pitch);
+#pragma unroll
+      for (int i = 0; i < kGateVecs; ++i) {
+        if (v0 + i * kThreads >= nv) break;
+        if (a.silu) {
+          float x[EV];
+          Vec<T>::unpack(u[i], x);
+#pragma unroll
+          for (int e = 0; e < EV; ++e) x[e] = silu_of<T>(x[e]);
+          u[i] = Vec<T>::pack(x);
+        }
+        *reinterpret_cast<uint4*>(dst + (long long)(v0 + i * kThreads) * EV) = u[i];
+      }
+    } else {
+      const Slot s = find_slot(a.p, row);
+      if (s.tok < 0) return;
+      T* dst = a.g_pages + s.tok * ((long long)a.H * a.m_pitch);
+      const int m = a.H * a.m_h, c0 = chunk * (kThreads * 8);
+      for (int i = c0 + threadIdx.x; i < min(m, c0 + kThreads * 8); i += kThreads) {
+        const int h = i / a.m_h, at = h * a.m_pitch + (i - h * a.m_h);
+        const float x = io<T>::ld(src + at);
+        io<T>::st(dst + at, a.silu ? silu_of<T>(x) : x);
+      }
+    }
+    return;
+  }
+  // ---- keys, and queries where asked
+  load_turns(sh, a.freqs, a.f.rotary / 2);
+  const int HT = a.q ? 2 * a.H : a.H, lh = kVec ? a.f.d_h / Vec<T>::E : 32;
+  const LaneMap m = lane_map<T>(threadIdx.x % lh, a.f.rotary, a.f.layout);
+  const int pairs = a.f.rotary / 2;
+  for (int row0 = blockIdx.x * a.rb; row0 < a.p.N; row0 += a.qk_blocks * a.rb) {
+    const int nr = min(a.rb, a.p.N - row0);
+    for (int r = w; r < nr; r += kThreads / 32) {
+      const Slot s = find_slot(a.p, row0 + r);
+      if ((threadIdx.x & 31) == 0) slot[r] = s;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nr * pairs; i += kThreads) {
+      const int r = i / pairs, c = i - r * pairs;
+      sh.cs[r][c] = turn_cos_sin(sh.turns[c], slot[r].pos);
+    }
+    __syncthreads();
+    const int heads = nr * HT;
+    for (int h0 = 0; h0 < heads; h0 += kThreads / lh) {
+      const int h = h0 + threadIdx.x / lh;
+      const int r = h < heads ? h / HT : 0, hh = h < heads ? h - r * HT : 0;
+      const bool is_k = hh < a.H;  // keys first
+      const int hd = is_k ? hh : hh - a.H;
+      const long long row = row0 + r;
+      const bool live = h < heads && (is_k ? slot[r].tok >= 0 : true);
+      const T* src = is_k ? a.k + row * a.k_pitch + (long long)hd * a.f.d_h : a.q + row * a.q_pitch + (long long)hd * a.f.d_h;
+      T* dst = is_k ? a.k_pages + (max(slot[r].tok, 0ll) * a.H + hd) * a.f.d_h : a.q_out + (row * a.H + hd) * a.f.d_h;
+      if (kVec) {
+        head_forward<T>(src, dst, live, a.f, m, lh, nullptr, sh.cs[r]);
+      } else if (live) {
+        head_forward_any<T>(src, dst, a.f, nullptr, sh.cs[r], buf[kVec ? 0 : w]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// --------------------------------------------------------------------------- launch
+
+int sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+
+bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether heads split into two 16-byte vectors per lane: whole lanes rotate or pass, a
+// head's lanes are a power of two, and every row starts on 16 bytes.
+bool vec_heads(int d_h, int rotary, int es, std::initializer_list<const void*> ptrs,
+               std::initializer_list<long long> pitches) {
+  const int E = 32 / es;
+  if (d_h % E != 0 || rotary % E != 0 || !pow2(d_h / E)) return false;
+  for (const void* p : ptrs)
+    if (!al16(p)) return false;
+  for (long long x : pitches)
+    if (x * es % 16 != 0) return false;
+  return true;
+}
+
+// Rows of a block's step: 8, fewer while that leaves SMs idle.
+int rows_per_block(long long rows) {
+  const int want = 2 * sm_count();
+  int rb = kMaxRowsBlk;
+  while (rb > 1 && rows / rb < want) rb /= 2;
+  return rb;
+}
+
+template <typename T>
+QkArgs<T> qk_args(const QkCall& c) {
+  QkArgs<T> a;
+  a.rows = c.rows; a.H = c.H; a.Hk = c.Hk; a.T_len = c.T;
+  a.f = FwdRows{c.d_h, c.rotary, c.layout, c.norm, c.eps};
+  a.positions = c.positions; a.freqs = c.freqs; a.q_gain = c.q_gain; a.k_gain = c.k_gain;
+  a.q_pitch = c.q_pitch; a.k_pitch = c.k_pitch;
+  a.q = static_cast<const T*>(c.q); a.k = static_cast<const T*>(c.k);
+  a.q_out = static_cast<T*>(c.q_out); a.k_out = static_cast<T*>(c.k_out);
+  a.dq_out = static_cast<const T*>(c.dq_out); a.dk_out = static_cast<const T*>(c.dk_out);
+  a.dq = static_cast<T*>(c.dq); a.dk = static_cast<T*>(c.dk);
+  a.part = c.part;
+  a.want_gain = c.dq_gain || c.dk_gain;
+  a.rb = rows_per_block(c.rows);
+  return a;
+}
+
+int qk_grid(long long rows, int rb, int per_sm) {
+  const long long blocks = (rows + rb - 1) / rb, most = (long long)sm_count() * per_sm;
+  return (int)(blocks < most ? blocks : most);
+}
+
+template <typename T>
+cudaError_t forward_t(const QkCall& c, cudaStream_t s) {
+  const QkArgs<T> a = qk_args<T>(c);
+  const int grid = qk_grid(c.rows, a.rb, 8);
+  if (vec_heads(c.d_h, c.rotary, sizeof(T), {c.q, c.k, c.q_out, c.k_out}, {c.q_pitch, c.k_pitch}))
+    qk_forward_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
+  else
+    qk_forward_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+constexpr int kBwdPerSm = 4;
+
+template <typename T>
+cudaError_t backward_t(const QkCall& c, cudaStream_t s) {
+  const QkArgs<T> a = qk_args<T>(c);
+  const int grid = qk_grid(c.rows, a.rb, kBwdPerSm);
+  if (vec_heads(c.d_h, c.rotary, sizeof(T), {c.q, c.k, c.dq_out, c.dk_out, c.dq, c.dk}, {c.q_pitch, c.k_pitch}))
+    qk_backward_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
+  else
+    qk_backward_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !a.want_gain) return e;
+  qk_gain_sum_kernel<<<dim3(ceil_div(c.d_h, 8), 2), 256, 0, s>>>(c.part, grid, c.d_h, c.dq_gain, c.dk_gain);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t append_t(const AppendCall& c, cudaStream_t s) {
+  AppendArgs<T> a;
+  a.p = c.p; a.H = c.H; a.m_h = c.m_h; a.m_pitch = c.m_pitch;
+  a.f = FwdRows{c.d_h, c.rotary, c.layout, c.norm, c.eps};
+  a.freqs = c.freqs; a.silu = c.silu;
+  a.q_pitch = c.q_pitch; a.k_pitch = c.k_pitch; a.g_pitch = c.g_pitch;
+  a.q = static_cast<const T*>(c.q); a.k = static_cast<const T*>(c.k); a.g = static_cast<const T*>(c.g);
+  a.q_out = static_cast<T*>(c.q_out);
+  a.k_pages = static_cast<T*>(c.k_pages); a.g_pages = static_cast<T*>(c.g_pages);
+  a.rb = rows_per_block(c.p.N);
+  a.qk_blocks = qk_grid(c.p.N, a.rb, 2);
+  const bool vec = vec_heads(c.d_h, c.rotary, sizeof(T), {c.q, c.k, c.g, c.q_out, c.k_pages, c.g_pages},
+                             {c.q_pitch, c.k_pitch, c.g_pitch, (long long)c.H * c.m_pitch});
+  constexpr int EV = 16 / sizeof(T);
+  a.chunks = vec ? ceil_div((long long)c.H * c.m_pitch / EV, kThreads * kGateVecs)
+                 : ceil_div((long long)c.H * c.m_h, kThreads * 8);
+  const long long blocks = a.qk_blocks + (long long)c.p.N * a.chunks;
+  if (blocks > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
+  if (vec)
+    cache_append_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  else
+    cache_append_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t qk_backward_part_bytes(int d_h) { return (size_t)sm_count() * kBwdPerSm * 2 * d_h * sizeof(float); }
+
+cudaError_t launch_qk_forward(tg_dtype dt, const QkCall& c, cudaStream_t s) {
+  return dt == TG_F32 ? forward_t<float>(c, s) : forward_t<__nv_bfloat16>(c, s);
+}
+cudaError_t launch_qk_backward(tg_dtype dt, const QkCall& c, cudaStream_t s) {
+  return dt == TG_F32 ? backward_t<float>(c, s) : backward_t<__nv_bfloat16>(c, s);
+}
+cudaError_t launch_cache_append(tg_dtype dt, const AppendCall& c, cudaStream_t s) {
+  return dt == TG_F32 ? append_t<float>(c, s) : append_t<__nv_bfloat16>(c, s);
+}
+
+}  // namespace tg

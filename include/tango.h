@@ -99,7 +99,19 @@ typedef enum { TG_F32 = 0, TG_BF16 = 1 } tg_dtype;
 #define TG_WS_TANGO_BWD 5 /* params: const tg_agg_params*: tango_aggregate_backward */
 #define TG_WS_WANGO_BWD 6 /* params: const tg_agg_params*: wango_aggregate_backward */
 
+#define TG_WS_QK_BWD 16 /* params: const tg_qk_params*: tango_qk_norm_rope_backward */
+#define TG_WS_PAGED 17  /* params: const tg_paged_params*: tango_paged_aggregate */
+
 #define TG_MAX_HEADS 64
+
+/* tg_qk_params.layout, tg_append_params.layout: which columns of a head form a pair that
+ * turns together, for rotary width r: c and c + r/2, or 2c and 2c + 1 */
+#define TG_ROPE_HALF 0
+#define TG_ROPE_INTERLEAVED 1
+/* tg_qk_params.norm, tg_append_params.norm */
+#define TG_NORM_NONE 0 /* n = x                          */
+#define TG_NORM_UNIT 1 /* n = x / max(|x|, 1e-12)        */
+#define TG_NORM_RMS 2  /* n = x / sqrt(mean(x^2) + eps)  */
 
 /*
  * Parameters of one aggregation (eq. 5).
@@ -394,6 +406,150 @@ tg_status tango_model_forward(const tg_model_params *p, const tg_model_weights *
 tg_status tango_aggregate_noalloc(const tg_agg_params *p, const void *q, const void *k,
                                   const void *g, const void *v, void *out, tg_stream_t stream);
 
+/*
+ * Norm and rotary position of every query and key head in one pass (sec. 2.1 takes RoPE
+ * and the unit norm; the two commute), for callers that make q and k outside
+ * tango_block_forward.  Per row and head, with x the head's d_h values:
+ *   n = x r (r by `norm`),  z = gain * n,  out = R(position) z,
+ * R turning the pairs of the first rotary_dim columns by position * freqs[c]; the other
+ * columns pass.  The aggregations want unit vectors (TG_NORM_UNIT without a gain).
+ *   rows         rows (tokens) of q and k (0 launches nothing)
+ *   H, H_k       query and key heads (1..1024; H_k may be 0: no k)
+ *   d_h          head width (1..128)
+ *   rotary_dim   even, 0..d_h; 0 = no rotation
+ *   layout, norm TG_ROPE_*, TG_NORM_*
+ *   eps          TG_NORM_RMS only (> 0)
+ *   T            positions == NULL: row r stands at position r % T (T >= 1)
+ *   positions    device int[rows], any sign, or NULL
+ *   freqs        device double[rotary_dim / 2]: radians per position, >= 0 (a long
+ *                context's scaling is the caller's choice of these; tg_rope_freqs makes
+ *                the usual ones).  Angles are reduced exactly (64-bit turns), so a
+ *                position of a million is as accurate as position 1.
+ *   q_gain, k_gain  device float[d_h], shared by all heads, or NULL (gain 1)
+ *   q_pitch, k_pitch  elements between rows of q, k (0: H * d_h, H_k * d_h): q and k may
+ *                be slices of one fused projection
+ *   dtype        of q, k and the outputs; arithmetic is fp32, outputs are rounded once
+ */
+typedef struct {
+    long long rows;
+    int H, H_k, d_h, rotary_dim, layout, norm;
+    float eps;
+    int T;
+    const int *positions;
+    const double *freqs;
+    const float *q_gain, *k_gain;
+    long long q_pitch, k_pitch;
+    tg_dtype dtype;
+} tg_qk_params;
+
+/* q_out [rows, H * d_h], k_out [rows, H_k * d_h]: device, dense, written; q_out may be q
+ * and k_out may be k when those are dense.  k and k_out are NULL when H_k == 0. */
+tg_status tango_qk_norm_rope(const tg_qk_params *p, const void *q, const void *k, void *q_out, void *k_out,
+                             tg_stream_t stream);
+
+/*
+ * Gradients of tango_qk_norm_rope: given dq_out, dk_out = dL/d(q_out), dL/d(k_out) (dense),
+ *   dz = R^T dout,  dgain = sum over rows and heads of dz * n,  dn = gain * dz,
+ *   dx = r (dn - n <n, dn>) (unit; rms: the mean instead of the sum; none: dx = dn).
+ * A unit-norm head with |x| < 1e-12 takes dx = r dn.  q, k as for the forward call.
+ * dq [rows, H * d_h], dk: dense, written; may be dq_out, dk_out.  dq_gain, dk_gain: device
+ * float[d_h], written (summed in a fixed order), or NULL; they need the gain.  ws: device
+ * scratch of tg_workspace_size(TG_WS_QK_BWD, p) bytes (0 without gains).
+ */
+tg_status tango_qk_norm_rope_backward(const tg_qk_params *p, const void *q, const void *k, const void *dq_out,
+                                      const void *dk_out, void *dq, void *dk, float *dq_gain, float *dk_gain,
+                                      void *ws, size_t ws_bytes, tg_stream_t stream);
+
+/*
+ * Fills freqs (HOST double[rotary_dim / 2]) with f_c = base^(-2c / rotary_dim), scaled for
+ * contexts `factor` times longer than the orig_len positions a model was trained on:
+ *   orig_len == 0: every f_c / factor (interpolated positions);
+ *   orig_len > 0: with n_c = orig_len f_c / (2 pi) the turns that pair c makes over the
+ *     trained length and w = clamp((n_c - turns_lo) / (turns_hi - turns_lo), 0, 1),
+ *     f_c (w + (1 - w) / factor): fast pairs are kept, slow ones interpolated.
+ * Needs rotary_dim even and >= 0, base > 0, factor >= 1, orig_len >= 0, and turns_hi >
+ * turns_lo >= 0 when orig_len > 0.
+ */
+tg_status tg_rope_freqs(int rotary_dim, double base, double factor, long long orig_len, double turns_lo,
+                        double turns_hi, double *freqs);
+
+/*
+ * A ragged batch of B sequences over a paged cache of keys and gates.
+ *   B            sequences (>= 1)
+ *   H, d_h, m    heads, head width (1..128), total gate width (m % H == 0; m_h = m / H)
+ *   m_pitch      gate columns per head in memory (0: m_h; else >= m_h), as in
+ *                tg_agg_params, for the cache's gates and for g, v and out
+ *   N            rows of the new-token tensors, all sequences' new tokens in order (0
+ *                launches nothing)
+ *   max_new      upper bound of the new tokens of one sequence (>= 1)
+ *   max_len      upper bound of lens (>= 1); <= table_pitch * page_size
+ *   page_size    tokens of a page (1..65536); n_pages: pages of the pool (>= 1)
+ *   table_pitch  entries of page_table per sequence (>= 1)
+ *   cu_new       device int[B + 1]: sequence b owns rows [cu_new[b], cu_new[b+1])
+ *   lens         device int[B]: cached tokens of sequence b, its new ones included; the
+ *                new tokens stand at positions lens[b] - n_b .. lens[b] - 1.  A token
+ *                whose position is negative is not appended, and its outputs are 0
+ *   page_table   device int[B, table_pitch]: page of tokens [p * page_size, (p+1) *
+ *                page_size) of a sequence; entries past its last token are not used
+ *   s, tau, null_bias   as in tg_agg_params (aggregation only)
+ *   v_pitch      elements between rows of v (0: H * m_pitch)
+ *   dtype        of the cache and of every tensor
+ * Device values outside their range (cu_new not rising within [0, N], more new tokens
+ * than max_new, lens outside [0, max_len], a page outside [0, n_pages)) are clamped or
+ * skipped, never followed, and flagged TG_ERR_DEVICE; the sequence's results are then
+ * unspecified.
+ * The cache is two pools owned by the caller: k_pages [n_pages, page_size, H * d_h]
+ * (normed, rotated keys) and g_pages [n_pages, page_size, H * m_pitch].  Slots past a
+ * sequence's length may hold anything (NaN included): they are never used.
+ */
+typedef struct {
+    int B, H, d_h, m, m_pitch, N, max_new, max_len, page_size, n_pages, table_pitch;
+    const int *cu_new, *lens, *page_table;
+    float s;
+    const float *tau;
+    const float *null_bias;
+    long long v_pitch;
+    tg_dtype dtype;
+} tg_paged_params;
+
+/*
+ * What tango_cache_append does to the new tokens on their way into the cache.
+ *   rotary_dim, layout, norm, eps, freqs   as in tg_qk_params, positions from lens
+ *   silu         1: g holds the gate projection W_g x, and SiLU(g) is cached (eq. 2);
+ *                0: g is cached as it is
+ *   q_pitch, k_pitch, g_pitch   elements between rows of q, k, g (0: dense)
+ */
+typedef struct {
+    int rotary_dim, layout, norm;
+    float eps;
+    const double *freqs;
+    int silu;
+    long long q_pitch, k_pitch, g_pitch;
+} tg_append_params;
+
+/*
+ * Appends the new tokens' keys and gates to the cache: k [N, H * d_h] normed and rotated
+ * at its token's position, g [N, H * m_pitch] through SiLU if asked, both written to the
+ * token's slot.  q [N, H * d_h], if not NULL, is normed and rotated in the same launch into
+ * q_out [N, H * d_h] (dense; may be a dense q) for the aggregation that follows.  A token's slot must not be
+ * shared with another sequence's new token.
+ */
+tg_status tango_cache_append(const tg_paged_params *p, const tg_append_params *a, const void *q, const void *k,
+                             const void *g, void *q_out, void *k_pages, void *g_pages, tg_stream_t stream);
+
+/*
+ * TANGO aggregation of the new tokens over the cache: for the token at position i of its
+ * sequence (already appended),
+ *   out = v * sum_{j<=i} e^{l_j} g_j / (sum_{j<=i} e^{l_j} + (i+1) e^{b_a}),  l_j = tau_a q . k_j,
+ * as tango_aggregate gives for the row of the whole sequence.  q [N, H * d_h] and the cached
+ * keys are unit vectors per head.  v [N, H * m_pitch] or NULL (out = gbar); out [N, H *
+ * m_pitch], written (columns past m_h of a head: unspecified); may alias a dense v.
+ * ws: device scratch of tg_workspace_size(TG_WS_PAGED, p) bytes, 256-byte aligned.
+ */
+tg_status tango_paged_aggregate(const tg_paged_params *p, const void *q, const void *v, void *out,
+                                const void *k_pages, const void *g_pages, void *ws, size_t ws_bytes,
+                                tg_stream_t stream);
+
 /* Workspace bytes needed by the call `which` (TG_WS_*) with `params`; 0 for invalid
  * parameters (validate with the call itself to get the reason). */
 size_t tg_workspace_size(int which, const void *params);
@@ -407,7 +563,7 @@ const char *tg_status_string(tg_status s);
  * TG_ERR_CUDA if the synchronisation itself failed.  If `detail` is not NULL it
  * receives the raw word (bit 0: timeout, bit 1: value out of range; bits 8..15:
  * the kernel that recorded it, 1 = TANGO, 2 = WANGO, 3 = GEMM, 4 = embedding lookup,
- * 5 = the aggregation backward).
+ * 5 = the aggregation backward, 6 = the paged cache calls).
  */
 tg_status tg_check_device_error(tg_stream_t stream, unsigned *detail);
 

@@ -1,0 +1,197 @@
+"""Host-side checks of the norm-and-rotate calls and the paged cache calls: bad arguments
+are refused before anything is launched, on a machine without a GPU too."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import cross_token_gated_gb300 as tg
+
+A = 256  # a pointer that validation never follows
+
+
+def _qk(**kw):
+    base = dict(rows=4, H=2, H_k=2, d_h=64, rotary_dim=64, layout=0, norm=1, eps=1e-6, T=4, positions=None, freqs=A,
+                q_gain=None, k_gain=None, q_pitch=0, k_pitch=0, dtype=tg.TG_BF16)
+    base.update(kw)
+    return tg.tg_qk_params(*base.values())
+
+
+def _paged(**kw):
+    base = dict(B=2, H=2, d_h=64, m=512, m_pitch=0, N=3, max_new=2, max_len=40, page_size=16, n_pages=8, table_pitch=4,
+                cu_new=A, lens=A, page_table=A, s=10.0, tau=None, null_bias=None, v_pitch=0, dtype=tg.TG_BF16)
+    base.update(kw)
+    return tg.tg_paged_params(*base.values())
+
+
+def _append(**kw):
+    base = dict(rotary_dim=64, layout=0, norm=1, eps=1e-6, freqs=A, silu=1, q_pitch=0, k_pitch=0, g_pitch=0)
+    base.update(kw)
+    return tg.tg_append_params(*base.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), tg.TG_ERR_INVALID_ARG),
+    (dict(H=0), tg.TG_ERR_INVALID_ARG),
+    (dict(H_k=-1), tg.TG_ERR_INVALID_ARG),
+    (dict(d_h=0), tg.TG_ERR_INVALID_ARG),
+    (dict(rotary_dim=63), tg.TG_ERR_INVALID_ARG),
+    (dict(rotary_dim=66), tg.TG_ERR_INVALID_ARG),
+    (dict(freqs=None), tg.TG_ERR_INVALID_ARG),
+    (dict(layout=2), tg.TG_ERR_INVALID_ARG),
+    (dict(norm=3), tg.TG_ERR_INVALID_ARG),
+    (dict(norm=tg.TG_NORM_RMS, eps=0.0), tg.TG_ERR_INVALID_ARG),
+    (dict(T=0), tg.TG_ERR_INVALID_ARG),
+    (dict(q_pitch=127), tg.TG_ERR_INVALID_ARG),
+    (dict(k_pitch=127), tg.TG_ERR_INVALID_ARG),
+    (dict(dtype=2), tg.TG_ERR_INVALID_ARG),
+    (dict(d_h=130, rotary_dim=0), tg.TG_ERR_UNSUPPORTED),
+])
+def test_qk_refusals(lib, kw, status):
+    raw, p = tg.load(), _qk(**kw)
+    assert raw.tango_qk_norm_rope(ctypes.byref(p), A, A, A, A, None) == status
+    assert raw.tango_qk_norm_rope_backward(ctypes.byref(p), A, A, A, A, A, A, None, None, None, 0, None) == status
+    p.q_gain = A
+    assert tg.tg_workspace_size(tg.TG_WS_QK_BWD, p) == 0
+
+
+def test_qk_pointer_refusals(lib):
+    raw, p = tg.load(), _qk()
+    f, b = raw.tango_qk_norm_rope, raw.tango_qk_norm_rope_backward
+    bad = tg.TG_ERR_INVALID_ARG
+    assert f(None, A, A, A, A, None) == bad
+    assert f(ctypes.byref(p), None, A, A, A, None) == bad
+    assert f(ctypes.byref(p), A, None, A, A, None) == bad          # H_k = 2 needs k
+    assert f(ctypes.byref(_qk(H_k=0)), A, A, A, A, None) == bad    # and no k where it is 0
+    assert f(ctypes.byref(p), A + 1, A, A, A, None) == tg.TG_ERR_UNSUPPORTED
+    assert b(ctypes.byref(p), A, A, A, A, A, A, A, None, None, 0, None) == bad    # dq_gain without a gain
+    g = _qk(q_gain=A, k_gain=A)
+    assert b(ctypes.byref(g), A, A, A, A, A, A, A, A, None, 0, None) == tg.TG_ERR_WORKSPACE
+    assert tg.tg_workspace_size(tg.TG_WS_QK_BWD, p) == 0
+    assert f(ctypes.byref(_qk(rows=0)), A, A, A, A, None) == tg.TG_OK           # nothing to do
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), tg.TG_ERR_INVALID_ARG),
+    (dict(H=65), tg.TG_ERR_INVALID_ARG),
+    (dict(m=511), tg.TG_ERR_INVALID_ARG),
+    (dict(m_pitch=255), tg.TG_ERR_INVALID_ARG),
+    (dict(N=-1), tg.TG_ERR_INVALID_ARG),
+    (dict(max_new=0), tg.TG_ERR_INVALID_ARG),
+    (dict(max_len=0), tg.TG_ERR_INVALID_ARG),
+    (dict(max_len=65), tg.TG_ERR_INVALID_ARG),   # more than the table's pages hold
+    (dict(page_size=0), tg.TG_ERR_INVALID_ARG),
+    (dict(n_pages=0), tg.TG_ERR_INVALID_ARG),
+    (dict(table_pitch=0), tg.TG_ERR_INVALID_ARG),
+    (dict(cu_new=None), tg.TG_ERR_INVALID_ARG),
+    (dict(lens=None), tg.TG_ERR_INVALID_ARG),
+    (dict(page_table=None), tg.TG_ERR_INVALID_ARG),
+    (dict(s=21.0), tg.TG_ERR_INVALID_ARG),
+    (dict(s=math.nan), tg.TG_ERR_INVALID_ARG),
+    (dict(v_pitch=511), tg.TG_ERR_INVALID_ARG),
+    (dict(dtype=7), tg.TG_ERR_INVALID_ARG),
+    (dict(d_h=129), tg.TG_ERR_UNSUPPORTED),
+    (dict(page_size=1 << 17), tg.TG_ERR_UNSUPPORTED),
+    (dict(n_pages=1 << 28), tg.TG_ERR_UNSUPPORTED),   # slot numbers pass 31 bits
+])
+def test_paged_refusals(lib, kw, status):
+    raw, p, a = tg.load(), _paged(**kw), _append()
+    if kw.get("d_h") == 129:
+        a = _append(rotary_dim=0)
+    assert raw.tango_paged_aggregate(ctypes.byref(p), A, A, A, A, A, None, 0, None) == status
+    assert raw.tango_cache_append(ctypes.byref(p), ctypes.byref(a), A, A, A, A, A, A, None) == status
+    assert tg.tg_workspace_size(tg.TG_WS_PAGED, p) == 0
+
+
+def test_paged_pointer_refusals(lib):
+    raw, p, a = tg.load(), _paged(), _append()
+    P, bad = ctypes.byref, tg.TG_ERR_INVALID_ARG
+    agg, app = raw.tango_paged_aggregate, raw.tango_cache_append
+    assert agg(None, A, A, A, A, A, None, 0, None) == bad
+    for i in (0, 2, 3, 4):
+        args = [A] * 5
+        args[i] = None
+        assert agg(P(p), *args, None, 0, None) == bad
+    assert agg(P(p), A, A + 1, A, A, A, None, 0, None) == tg.TG_ERR_UNSUPPORTED
+    need = tg.tg_workspace_size(tg.TG_WS_PAGED, p)
+    assert need > 0
+    assert agg(P(p), A, A, A, A, A, None, 0, None) == tg.TG_ERR_WORKSPACE
+    assert agg(P(p), A, A, A, A, A, 4096, need - 1, None) == tg.TG_ERR_WORKSPACE
+    assert agg(P(p), A, A, A, A, A, 4096 + 16, need, None) == tg.TG_ERR_WORKSPACE
+    assert agg(P(_paged(N=0)), A, A, A, A, A, None, 0, None) == tg.TG_OK
+    assert app(P(p), None, A, A, A, A, A, A, None) == bad
+    assert app(P(p), P(a), A, A, A, None, A, A, None) == bad       # q without q_out
+    for i in (1, 2, 4, 5):
+        args = [A] * 6
+        args[i] = None
+        assert app(P(p), P(a), *args, None) == bad
+    for kw in (dict(rotary_dim=65), dict(rotary_dim=66), dict(freqs=None), dict(layout=5), dict(norm=9),
+               dict(k_pitch=127), dict(q_pitch=127), dict(g_pitch=511)):
+        assert app(P(p), P(_append(**kw)), A, A, A, A, A, A, None) == bad
+    assert app(P(_paged(N=0)), P(a), A, A, A, A, A, A, None) == tg.TG_OK
+
+
+def test_paged_workspace_grows_with_the_batch(lib):
+    small = tg.tg_workspace_size(tg.TG_WS_PAGED, _paged())
+    assert tg.tg_workspace_size(tg.TG_WS_PAGED, _paged(N=0)) == 0
+    assert tg.tg_workspace_size(tg.TG_WS_PAGED, _paged(B=64, N=64, max_new=1)) > small
+
+
+def test_rope_freqs(lib):
+    """Base frequencies; all interpolated; and, with a trained length, fast pairs kept, slow
+    ones interpolated, a linear ramp of turns between."""
+    f = tg.tg_rope_freqs(64, device="cpu")
+    want = torch.tensor([10000.0 ** (-2 * c / 64) for c in range(32)], dtype=torch.float64)
+    assert torch.allclose(f, want, rtol=1e-15, atol=0)
+    assert torch.allclose(tg.tg_rope_freqs(64, factor=8.0, device="cpu"), want / 8, rtol=1e-15, atol=0)
+    g = tg.tg_rope_freqs(64, factor=8.0, orig_len=8192, turns_lo=1.0, turns_hi=4.0, device="cpu")
+    turns = 8192 * want / (2 * math.pi)
+    w = ((turns - 1) / 3).clamp(0, 1)
+    assert torch.allclose(g, want * (w + (1 - w) / 8), rtol=1e-14, atol=0)
+    assert (w == 1).any() and (w == 0).any() and ((w > 0) & (w < 1)).any()
+    assert tg.tg_rope_freqs(0, device="cpu").numel() == 0
+    for bad in (dict(base=0.0), dict(factor=0.5), dict(orig_len=-1), dict(orig_len=64, turns_lo=2.0, turns_hi=2.0),
+                dict(factor=math.nan)):
+        with pytest.raises(tg.TgError):
+            tg.tg_rope_freqs(64, device="cpu", **bad)
+    with pytest.raises(tg.TgError):
+        tg.tg_rope_freqs(7, device="cpu")
+
+
+def test_binding_checks_tensors(lib):
+    """The binding refuses tensors the library would read as something else."""
+    bf = torch.bfloat16
+    q = torch.zeros(4, 128, dtype=bf)
+    o = torch.zeros(4, 128, dtype=bf)
+    fr = torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(TypeError):
+        tg.tango_qk_norm_rope(q, None, o.float(), None, fr, H=2)
+    with pytest.raises(TypeError):
+        tg.tango_qk_norm_rope(q, None, o, None, fr.float(), H=2)
+    with pytest.raises(ValueError):
+        tg.tango_qk_norm_rope(q.t(), None, o.t(), None, fr, H=2)          # columns not adjacent
+    with pytest.raises(ValueError):
+        tg.tango_qk_norm_rope(q, None, torch.zeros(4, 256, dtype=bf)[:, :128], None, fr, H=2)   # output not dense
+    with pytest.raises(ValueError):
+        tg.tango_qk_norm_rope(q, q[:2], o, o[:2], fr, H=2)
+    with pytest.raises(ValueError):
+        tg.tango_qk_norm_rope(q, None, o, None, fr, H=2, positions=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        tg.tango_qk_norm_rope(q[:1].expand(4, 128), None, o, None, fr, H=2)  # rows at pitch 0
+    kp, gp = tg.cache_pools(4, 16, 2, 64, 100, device="cpu")
+    assert gp.shape == (4, 16, 2 * 104)
+    ints = dict(dtype=torch.int32)
+    ok = dict(page_table=torch.zeros(1, 2, **ints), cu_new=torch.zeros(2, **ints), lens=torch.zeros(1, **ints))
+    out = torch.zeros(4, 208, dtype=bf)
+    kw = dict(H=2, max_new=4, max_len=32)
+    with pytest.raises(TypeError):
+        tg.tango_paged_aggregate(q, None, out, kp, gp, **dict(ok, lens=torch.zeros(1)), **kw)
+    with pytest.raises(ValueError):
+        tg.tango_paged_aggregate(q, None, out, kp, gp, **dict(ok, cu_new=torch.zeros(1, **ints)), **kw)
+    with pytest.raises(ValueError):
+        tg.tango_paged_aggregate(q, None, out[:3], kp, gp, **ok, **kw)
+    with pytest.raises(ValueError):
+        tg.tango_cache_append(None, q, out, q, kp, gp, **ok, freqs=fr, H=2)
+    with pytest.raises(ValueError):
+        tg.tango_cache_append(None, q, out[:, :200], None, kp, gp, **ok, freqs=fr, H=2)
