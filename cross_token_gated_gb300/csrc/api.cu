@@ -563,7 +563,12 @@ PagedCall paged_call(const tg_paged_params* p, unsigned* err) {
 
 size_t paged_ws_bytes(const tg_paged_params* p) {
   if (p->N == 0) return 0;
-  return paged_simt_ws_bytes(p->dtype, paged_call(p, nullptr));
+  const PagedCall c = paged_call(p, nullptr);
+  // pointers that are not 16-byte aligned take the CUDA-core kernels: room for either
+  const size_t simt = paged_simt_ws_bytes(p->dtype, c);
+  if (!paged_tc_takes(p->dtype, c)) return simt;
+  const size_t tc = paged_tc_ws_bytes(c);
+  return tc > simt ? tc : simt;
 }
 
 }  // namespace
@@ -879,7 +884,9 @@ tg_status tango_paged_aggregate(const tg_paged_params* p, const void* q, const v
   if (error_word(&err) != cudaSuccess) return TG_ERR_CUDA;
   PagedCall c = paged_call(p, err);
   c.q = q; c.v = v; c.out = out; c.k_pages = k_pages; c.g_pages = g_pages; c.ws = ws;
-  return cuda_status(launch_paged_simt(p->dtype, c, reinterpret_cast<cudaStream_t>(stream)));
+  const bool tc = paged_tc_takes(p->dtype, c) && aligned16(q) && aligned16(out) && aligned16(k_pages) && aligned16(g_pages);
+  return cuda_status(tc ? launch_paged_tc(c, reinterpret_cast<cudaStream_t>(stream))
+                        : launch_paged_simt(p->dtype, c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t tg_workspace_size(int which, const void* params) {

@@ -55,4 +55,30 @@ __device__ __forceinline__ int paged_find(const PagedBatch& p, int row) {
   return lo;
 }
 
+// Tiles of R rows are numbered so that no scan is needed: sequence b's first tile is
+// cu_new[b] / R + b (the numbers in between are skipped).
+struct TileRef {
+  int b, row0, n, pos0;  // first row, rows (0: no such tile), first row's position
+};
+template <int R>
+__device__ __forceinline__ TileRef find_tile(const PagedBatch& p, int tile, bool flag) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool le = lane * step < n && min(max(p.cu_new[i], 0), p.N) / R + i <= tile;
+    const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
+    const int adv = (cnt - 1) * step;
+    lo += adv;
+    n = min(step, n - adv);
+  }
+  const PagedSeq s = paged_seq(p, lo, flag);
+  const int k = tile - (s.r0 / R + lo);
+  TileRef t{lo, s.r0 + k * R, 0, 0};
+  if (k < 0 || k * R >= s.n) return t;
+  t.n = min(R, s.n - k * R);
+  t.pos0 = s.len - s.n + k * R;
+  return t;
+}
+
 }  // namespace tg
