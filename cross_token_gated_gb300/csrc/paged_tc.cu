@@ -10,21 +10,30 @@
 //     Weights are formed once per (row, head, key), not once per gate strip: at 14,240
 //     gates a head a strip-wise recomputation would spend as many exp2 as the product has
 //     tensor cycles.
+// paged_weights_few_kernel  the same P for up to 8 new tokens of a sequence on the CUDA
+//     cores, a thread per key: a 128-row product would be nearly all padding.
 // paged_gates_kernel    U = P G: tiles of 128 rows x 256 gate columns, 64 keys a step.
-//     warp 0     scheduler and TMA producer (4 stages of P 16 KB + G 32 KB): takes jobs from a
-//                counter, looks up pages 32 at a time, one lane per page issues its boxes
-//     warp 1     MMA issuer (128 x 256 x 16), two accumulators in TMEM
-//     warps 2-5  epilogue: times 1 / den and v, bf16 out; or f32 partial sums of a key range
+//     warp 0     TMA producer (4 stages of P 16 KB + G 32 KB), 32 pages looked up at a time,
+//                one lane per page issues its copies; the first job's G is asked for while
+//                the weights kernel still runs
+//     warp 1     MMA issuer (128 x 256 x 16), two accumulators in TMEM.  Tiles of a few rows
+//                run the same product on unused rows: it is shorter than the step's G takes
+//                from memory (D^T = G^T P^T with 16 columns, which does an eighth of the work,
+//                measured slower: 8 products a step of about 100 cycles each)
+//     warps 2-5  epilogue: times 1 / den and v, bf16 out; or f32 partial sums of a key range.
+//                Rows are turned into columns through shared memory, so that v and out move
+//                in whole 64-byte pieces of a row
 //     warps 6-9  scrub: only in steps with keys that some row of the tile does not see:
 //                slots past the sequence's length become zeros, and non-finite gates of the
 //                chunk's own tokens are taken out of the product (0 * NaN would reach rows
 //                that do not see them); the epilogue adds them back to the rows that do
+//     warp 10    scheduler: takes jobs from a counter, works out what they are
 //
-// A job is a (sequence, head, strip, key range, row tile) with the row tile fastest, so the
-// CTAs that work side by side share their G out of L2.  Key ranges are cut so that there are
-// about kJobsPerSm jobs per SM when the tiles alone would not fill the SMs; the job that
-// finishes a tile last adds the ranges' partial sums in their order.
-// Every wait is bounded; on expiry the kernel records a timeout in the error word.
+// A job is a (sequence, key range, head, strip, row tile) with the row tile fastest, so the
+// CTAs that work side by side share their G out of L2.  Key ranges are cut when the tiles
+// alone would not fill the SMs; the job that finishes a tile last adds the ranges' partial
+// sums in their order.  Every wait is bounded; on expiry the kernel records a timeout in
+// the error word.
 #include "tg_common.cuh"
 #include "tg_paged.cuh"
 #include "tg_ptx.cuh"
@@ -40,8 +49,8 @@ constexpr int kM = 128;           // rows of a tile
 constexpr int kN = 256;           // gate columns of a strip
 constexpr int kK = 64;            // keys of a step
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kJobsPerSm = 4;
-constexpr int kMinSteps = 8;      // a key range is at least this many steps
+constexpr int kJobsPerSm = 4;     // at most; see TcArgs::jobs_per_sm
+constexpr int kFewRows = 16;      // tiles of at most this many rows finish a thread per column
 
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -71,10 +80,12 @@ struct TcArgs {
   int h0, heads;             // heads of this pass
   int rows_tot;              // scratch rows of a head: up8(N) + 8 B
   int key_blocks;            // ceil(max_len / 64)
-  int span_keys, spans;      // of the weights kernel; spans: ceil(max_len / span_keys)
+  int span_keys, spans;      // of the weights kernel; spans: ceil(max_len / span_keys), up to 4s
   int strips;                // ceil(m_h / 256)
   int tiles;                 // tile numbers: N / 128 + B
   int r8cap;                 // rows of a partial: min(128, up8(max_new))
+  int min_steps;             // a key range is at least this many steps
+  int jobs_per_sm;           // key ranges are cut for about this many jobs per SM
   int nc_cap;                // key ranges of a tile, at most
   int n_slots;
   int box_rows;              // rows of a G box
@@ -88,7 +99,7 @@ struct TcArgs {
   const __nv_bfloat16 *k_pages, *g_pages;
   uint8_t* P;                // [head][row][key block][128 bytes], see p_block()
   float* den;                // [head][row][span]
-  float* part;               // [slot][64][r8cap][4]
+  float* part;               // [slot]: [64][r8cap][4], or [row][256] for tiles of few rows
   int* slot;                 // [head][strip][tile][nc_cap]
   int* done;                 // [head][strip][tile]: ranges that are done
   int* next;                 // [0] next job, [1] next partial slot
@@ -100,6 +111,14 @@ __device__ __forceinline__ int scratch_row(int r0, int b) { return up8(r0) + 8 *
 // P of key block kb of a tile with r8 scratch rows.
 __device__ __forceinline__ uint8_t* p_block(const TcArgs& a, int hl, int prow, int r8, int kb) {
   return a.P + (((size_t)hl * a.rows_tot + prow) * a.key_blocks + (size_t)kb * r8) * 128;
+}
+
+// The gates kernel's counters, cleared by all CTAs of a weights kernel together.
+__device__ __forceinline__ void clear_counters(const TcArgs& a, int tile, int hl, int span) {
+  const size_t n = (size_t)a.heads * a.strips * a.tiles;
+  const size_t cta = ((size_t)span * gridDim.y + hl) * gridDim.x + tile, ctas = (size_t)gridDim.x * gridDim.y * gridDim.z;
+  for (size_t i = cta * blockDim.x + threadIdx.x; i < n; i += ctas * blockDim.x) a.done[i] = 0;
+  if (cta == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
 }
 
 // ============================================================================ weights
@@ -120,12 +139,7 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
   const int tile = blockIdx.x, hl = blockIdx.y, span = blockIdx.z, head = a.h0 + hl;
 
   griddep_launch();
-  // the gates kernel's counters
-  const size_t nd = (size_t)a.heads * a.strips * a.tiles;
-  const size_t cta = ((size_t)span * gridDim.y + hl) * gridDim.x + tile, ctas = (size_t)gridDim.x * gridDim.y * gridDim.z;
-  for (size_t i = cta * kWThreads + t; i < nd; i += ctas * kWThreads) a.done[i] = 0;
-  if (cta == 0 && t < 2) a.next[t] = 0;
-
+  clear_counters(a, tile, hl, span);
   const TileRef tr = find_tile<kM>(a.p, tile, hl == 0 && span == 0);
   const int vis = tr.pos0 + tr.n;
   const int key0 = span * a.span_keys, key1 = min(key0 + a.span_keys, (vis + 63) & ~63);
@@ -255,15 +269,94 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
   }
 }
 
+// grid (tiles, heads, spans), 256 threads, one key each per round.
+template <int R, int DH>
+__global__ void __launch_bounds__(kWThreads) paged_weights_few_kernel(const TcArgs a) {
+  __shared__ __align__(16) float qs[R][DH];
+  __shared__ float red[kWThreads / 32][R];
+  const int t = threadIdx.x, lane = t & 31;
+  const int tile = blockIdx.x, hl = blockIdx.y, span = blockIdx.z, head = a.h0 + hl;
+  griddep_launch();
+  clear_counters(a, tile, hl, span);
+  const TileRef tr = find_tile<kM>(a.p, tile, hl == 0 && span == 0);
+  const int vis = tr.pos0 + tr.n;
+  const int key0 = span * a.span_keys, key1 = min(key0 + a.span_keys, (vis + 63) & ~63);
+  if (tr.n == 0 || vis <= 0 || key0 >= vis) return;
+  const int rows = min(tr.n, R);  // R >= max_new
+  const PagedSeq sq = paged_seq(a.p, tr.b, false);
+  const int prow = scratch_row(sq.r0, tr.b), r8 = up8(tr.n);
+  constexpr int C = DH / 8;
+  uint4 u[C];
+  auto load = [&](int key) {
+    const __nv_bfloat16* kp = nullptr;
+    if (key < vis) {
+      const int pi = key / a.p.page_size, pg = paged_page(a.p, tr.b, pi);
+      if (pg >= 0) kp = a.k_pages + (((size_t)pg * a.p.page_size + (key - pi * a.p.page_size)) * a.H + head) * DH;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) u[c] = kp ? ld_global_v4(kp + c * 8) : make_uint4(0, 0, 0, 0);
+  };
+  load(key0 + t);
+  for (int i = t; i < R * DH; i += kWThreads) {
+    const int r = i / DH, c = i - r * DH;
+    qs[r][c] = r < rows ? __bfloat162float(a.q[((size_t)(tr.row0 + r) * a.H + head) * DH + c]) : 0.f;
+  }
+  const float c2 = head_tau(a.tau, a.s, head, a.p.err, kKernPaged) * kLog2e;
+  float sum[R] = {};
+  __syncthreads();
+  for (int key = key0 + t; key < key1; key += kWThreads) {
+    float x[R] = {};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t uu[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 q0 = *reinterpret_cast<const float4*>(&qs[r][c * 8]);
+        const float4 q1 = *reinterpret_cast<const float4*>(&qs[r][c * 8 + 4]);
+        x[r] = fmaf(bf16lo(uu[0]), q0.x, x[r]);
+        x[r] = fmaf(bf16hi(uu[0]), q0.y, x[r]);
+        x[r] = fmaf(bf16lo(uu[1]), q0.z, x[r]);
+        x[r] = fmaf(bf16hi(uu[1]), q0.w, x[r]);
+        x[r] = fmaf(bf16lo(uu[2]), q1.x, x[r]);
+        x[r] = fmaf(bf16hi(uu[2]), q1.y, x[r]);
+        x[r] = fmaf(bf16lo(uu[3]), q1.z, x[r]);
+        x[r] = fmaf(bf16hi(uu[3]), q1.w, x[r]);
+      }
+    }
+    if (key + kWThreads < key1) load(key + kWThreads);
+    const int kc = key & 63;
+    uint8_t* pb = p_block(a, hl, prow, r8, key / kK) + (kc & 7) * 2;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float w = key <= tr.pos0 + r ? ex2_approx(fmaf(x[r], c2, -c2)) : 0.f;
+      const __nv_bfloat16 wb = __float2bfloat16_rn(w);
+      sum[r] += __bfloat162float(wb);
+      if (r < rows) *reinterpret_cast<__nv_bfloat16*>(pb + r * 128 + (((kc >> 3) ^ (r & 7)) << 4)) = wb;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float s = sum[r];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[t / 32][r] = s;
+  }
+  __syncthreads();
+  if (t < rows) {
+    float s = 0.f;
+    for (int i = 0; i < kWThreads / 32; ++i) s += red[i][t];
+    a.den[((size_t)hl * a.rows_tot + prow + t) * a.spans + span] = s;
+  }
+}
+
 // ============================================================================== gates
 
 constexpr int kStages = 4;
 constexpr uint32_t kABytes = kM * 128;       // 16 KB of P
-constexpr uint32_t kGBox = kK * 128;         // 8 KB: 64 keys x 64 columns
-constexpr uint32_t kBBytes = 4 * kGBox;      // 32 KB
-constexpr int kGThreads = 320;
+constexpr uint32_t kBBytes = kK * kN * 2;    // 32 KB of G
+constexpr uint32_t kTurnBytes = 4 * 4096;    // epilogue: 32 rows x 32 columns in f32 per warp
+constexpr int kGThreads = 352;
 constexpr int kJobSlots = 4;
-constexpr int kEpi0 = 2, kScrub0 = 6;
+constexpr int kEpi0 = 2, kScrub0 = 6, kSched = 10;
 
 struct Job {
   int b, row0, rows, pos0, hl, strip, it0, it1, nc, c, tile, prow;  // b < 0: no more jobs
@@ -271,7 +364,8 @@ struct Job {
 };
 
 struct __align__(8) GBars {
-  uint64_t full[kStages], empty[kStages], clean[kStages];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t dirty_full[kStages], clean[kStages];  // of the dirty steps' G, a ring of their own
   uint64_t acc_full[2], acc_empty[2];
   uint64_t job_full[kJobSlots], job_empty[kJobSlots];
   uint64_t drain;
@@ -279,26 +373,38 @@ struct __align__(8) GBars {
   int abort;
   int last;
   Job job[kJobSlots];
+  int page[kJobSlots][32];  // pages of a job's first 32 boxes
 };
 // With the weights kernel's shared memory this exceeds an SM's, so a CTA of this kernel that
 // is launched early never sits beside one of that kernel's (which may still have to
 // allocate its tensor memory).
-constexpr size_t kGSmem = 1024 + kStages * (size_t)(kABytes + kBBytes) + sizeof(GBars);
+constexpr size_t kGSmem = 1024 + kStages * (size_t)(kABytes + kBBytes) + kTurnBytes + sizeof(GBars);
 static_assert(kGSmem <= 232448, "shared memory budget");
 static_assert(kGSmem + kWSmem > 233472, "the two kernels never share an SM");
 
+// A bounded wait.  The wall clock is read only every 64 tries: a read takes longer than
+// the hand-over between two roles does.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, GBars& b, const TcArgs& a) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (*(volatile int*)&b.abort) return false;
-  if (mbar_wait(bar, parity, a.timeout_ns)) return true;
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*(volatile int*)&b.abort) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > a.timeout_ns) break;
+  }
   *(volatile int*)&b.abort = 1;
   record_error(a.p.err, kErrTimeout | kKernPaged);
   return false;
 }
 
-// The same for a whole warp: every lane returns the same answer.
+// The same for a whole warp: one lane polls, every lane returns its answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars& b, const TcArgs& a) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, b, a));
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, b, a);
+  return __shfl_sync(0xffffffffu, ok, 0);
 }
 
 // 64-key steps of a tile that sees keys [0, vis): at least one, so that rows without keys
@@ -320,27 +426,630 @@ struct Ring {
   }
 };
 
-// The keys of a step that are there, and whether some row of the tile misses one of them.
-__device__ __forceinline__ int step_keys(const Job& j, int it) { return min(kK, j.pos0 + j.rows - it * kK); }
-__device__ __forceinline__ bool step_dirty(const Job& j, int it) { return it * kK + kK - 1 > j.pos0; }
+// A tile's steps from this one on are dirty: they hold keys that some of its rows do not
+// see (and slots past the sequence's length).
+__device__ __forceinline__ int first_dirty(int pos0) { return pos0 < 0 ? 0 : (pos0 + 1) / kK; }
 
 __device__ __forceinline__ int job_cols(const TcArgs& a, const Job& j) { return min(kN, a.m_h - j.strip * kN); }
 
-__device__ __forceinline__ bool bad_bits(uint32_t x, uint32_t m) { return (x & m) == m; }
+// Of a pair of bf16: bits 15 and 31 set for a half whose exponent is all ones (an infinity or
+// NaN), and the pair with such halves zeroed.
+__device__ __forceinline__ uint32_t non_finite(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t drop(uint32_t x) { return x & ~((non_finite(x) >> 15) * 0xffffu); }
+
+// Page of box x (br keys) of a sequence; n_pages, which TMA reads as zeros, for a box past
+// box1 and for an entry that is not a page.
+__device__ __forceinline__ int box_page(const TcArgs& a, int b, int box, int box1) {
+  if (box >= box1) return a.p.n_pages;
+  const int pg = paged_page(a.p, b, box * a.box_rows / a.p.page_size);
+  return pg < 0 ? a.p.n_pages : pg;
+}
+// Boxes of a sequence up to the end of a job's keys.
+__device__ __forceinline__ int job_boxes(const TcArgs& a, const Job& j) {
+  const int vis = j.pos0 + j.rows;
+  return vis <= 0 ? 0 : (min(j.it1 * kK, vis) + a.box_rows - 1) / a.box_rows;
+}
+
+// Warp kSched: takes jobs from the counter, works out what they are and hands them to the
+// other roles, a few ahead of the one that runs.
+__device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
+  // steps of the whole launch, and from them the steps of a key range
+  const int HS = a.heads * a.strips;
+  long long total = 0;
+  for (int i = lane; i < a.p.B; i += 32) total += seq_steps(paged_seq(a.p, i, false));
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= HS;
+  const long long want = a.jobs_per_sm * (long long)gridDim.x;
+  const int range = (int)max((long long)a.min_steps, (total + want - 1) / want);
+
+  // a window of 32 sequences, one per lane: rows, length, jobs (inclusive prefix)
+  int w0 = -32;
+  long long jbase = 0, jend = 0, pre = 0;
+  PagedSeq ws{0, 0, 0};
+  int wmt = 0;
+  Ring jr;
+  int nxt = 0;
+  bool first = true;
+  long long j = blockIdx.x;  // then from the counter, gridDim.x on
+  while (true) {
+    while (j >= jend && w0 + 32 < a.p.B) {
+      w0 += 32;
+      jbase = jend;
+      long long jobs = 0;
+      if (w0 + lane < a.p.B) {
+        ws = paged_seq(a.p, w0 + lane, false);
+        wmt = (ws.n + kM - 1) / kM;
+        jobs = (long long)wmt * ((steps_of(ws.len) + range - 1) / range) * HS;
+      }
+      pre = jobs;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += x;
+      }
+      jend = jbase + __shfl_sync(0xffffffffu, pre, 31);
+    }
+    Job job;
+    job.b = -1;
+    bool skip = false;
+    if (j < jend) {
+      const long long rel = j - jbase;
+      const int owner = __popc(__ballot_sync(0xffffffffu, pre <= rel));
+      const long long before = __shfl_sync(0xffffffffu, pre, owner > 0 ? owner - 1 : 0);
+      const int idx = (int)(rel - (owner > 0 ? before : 0));
+      const int r0 = __shfl_sync(0xffffffffu, ws.r0, owner), n = __shfl_sync(0xffffffffu, ws.n, owner);
+      const int len = __shfl_sync(0xffffffffu, ws.len, owner), mt = __shfl_sync(0xffffffffu, wmt, owner);
+      // row tiles of a strip side by side (they share G in L2), then the strips of the same
+      // keys (they share DRAM pages), then the key ranges; later row tiles, the longer ones,
+      // come first
+      const int ti = mt - 1 - idx % mt, hs = idx / mt % HS;
+      job.c = idx / mt / HS;
+      job.b = w0 + owner;
+      job.row0 = r0 + ti * kM;
+      job.rows = min(kM, n - ti * kM);
+      job.pos0 = len - n + ti * kM;
+      job.hl = hs / a.strips;
+      job.strip = hs - job.hl * a.strips;
+      const int u = steps_of(job.pos0 + job.rows);
+      job.nc = (u + range - 1) / range;
+      job.it0 = job.c * range;
+      job.it1 = min(u, job.it0 + range);
+      job.tile = r0 / kM + job.b + ti;
+      job.prow = scratch_row(r0, job.b) + ti * kM;
+      job.poison = 0;
+      skip = job.c >= job.nc;  // a tile of the sequence that sees fewer keys
+    }
+    if (!skip) {
+      const int box = job.it0 * (kK / a.box_rows) + lane;
+      const int page = job.b < 0 ? 0 : box_page(a, job.b, box, job_boxes(a, job));
+      if (!warp_wait(&b.job_empty[jr.stage], jr.phase ^ 1, b, a)) break;
+      b.page[jr.stage][lane] = page;
+      if (lane == 0) b.job[jr.stage] = job;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.job_full[jr.stage]);
+      jr.next(kJobSlots);
+      if (job.b < 0) break;
+    }
+    if (first) {
+      griddep_wait();  // the counters are the weights kernel's
+      first = false;
+      if (lane == 0) nxt = atomicAdd(a.next, 1);
+    }
+    j = (long long)gridDim.x + __shfl_sync(0xffffffffu, nxt, 0);
+    if (lane == 0) nxt = atomicAdd(a.next, 1);  // the number after, while this job is handed out
+  }
+  if (first) griddep_wait();
+}
+
+// Warp 0: copies each step's P and G.
+__device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, uint8_t* sB, const CUtensorMap* tmG,
+                                        const CUtensorMap* tmG4, int lane) {
+  Ring st, jr, dr;
+  uint32_t issued_mask = 0, issued_phase = 0;  // bits 0..: full, 8..: dirty_full
+  bool ok = true, waited = false;
+  const int br = a.box_rows, spp = kK / br;  // boxes of a step
+  const int win = 32 / spp;                  // steps of a window of 32 boxes
+  const int lane_step = lane / spp, lane_dst = (lane - lane_step * spp) * (4 * br * 128);
+  while (ok) {
+    if (!(ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a))) break;
+    const Job job = b.job[jr.stage];
+    int page = b.page[jr.stage][lane], page2 = a.p.n_pages;  // this window's, and the next one's
+    if (job.b < 0) break;
+    const int nbc = (job_cols(a, job) + 63) / 64, head = a.h0 + job.hl, x0 = job.strip * kN;
+    const bool whole = x0 + kN <= a.m_h;  // the strip's four 64-column boxes in one copy
+    const int box1 = job_boxes(a, job), r8 = up8(job.rows);
+    const uint32_t pbytes = job.pos0 + job.rows > 0 ? (uint32_t)r8 * 128 : 0u;
+    const uint32_t box_bytes = (uint32_t)(whole ? 4 : nbc) * br * 128;
+    const uint8_t* psrc = p_block(a, job.hl, job.prow, r8, job.it0);
+    const int dirty = first_dirty(job.pos0), nsteps = job.it1 - job.it0;
+    for (int w = 0; w < nsteps && ok; w += win) {
+      const int box = (job.it0 + w) * spp + lane, prw = box * br % a.p.page_size;
+      if (w + win < nsteps) page2 = box_page(a, job.b, box + 32, box1);
+      const bool there = box < box1;
+      const int wn = min(win, nsteps - w);
+      for (int i = 0; i < wn; ++i) {
+        if (waited && !__all_sync(0xffffffffu, mbar_try_wait(&b.empty[st.stage], st.phase ^ 1))) {
+          ok = warp_wait(&b.empty[st.stage], st.phase ^ 1, b, a);
+          if (!ok) break;
+        }
+        const bool is_dirty = job.it0 + w + i >= dirty;
+        uint64_t* gbar = is_dirty ? &b.dirty_full[dr.stage] : &b.full[st.stage];
+        const bool issue = there && lane_step == i;
+        const uint32_t gbytes = __popc(__ballot_sync(0xffffffffu, issue)) * box_bytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&b.full[st.stage], pbytes + (is_dirty ? 0u : gbytes));
+          if (is_dirty) mbar_arrive_expect_tx(gbar, gbytes);
+          if (pbytes && waited) bulk_load(sA + st.stage * kABytes, psrc, pbytes, &b.full[st.stage]);
+        }
+        __syncwarp();
+        if (issue) {
+          uint8_t* dst = sB + st.stage * kBBytes + lane_dst;
+          if (whole) {
+            tma_load_5d(dst, tmG4, gbar, 0, prw, x0 / 64, head, page);
+          } else {
+            for (int c = 0; c < nbc; ++c) tma_load_4d(dst + c * br * 128, tmG, gbar, x0 + c * 64, head, prw, page);
+          }
+        }
+        issued_mask |= 1u << st.stage;
+        issued_phase = (issued_phase & ~(1u << st.stage)) | (st.phase << st.stage);
+        if (is_dirty) {
+          issued_mask |= 256u << dr.stage;
+          issued_phase = (issued_phase & ~(256u << dr.stage)) | (dr.phase << (dr.stage + 8));
+          dr.next(kStages);
+        }
+        st.next(kStages);
+        psrc += (size_t)r8 * 128;
+        if (!waited && w + i + 1 == min(nsteps, kStages)) {
+          // the first stages' G is on its way; their P once the weights are there
+          griddep_wait();
+          waited = true;
+          if (lane == 0 && pbytes)
+            for (int x = 0; x <= w + i; ++x)
+              bulk_load(sA + x * kABytes, p_block(a, job.hl, job.prow, r8, job.it0 + x), pbytes, &b.full[x]);
+        }
+      }
+      page = page2;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.job_empty[jr.stage]);
+    jr.next(kJobSlots);
+  }
+  if (!waited) griddep_wait();
+  // copies still in flight must land before the CTA exits
+  for (int s = 0; s < kStages; ++s) {
+    if (issued_mask >> s & 1) mbar_wait(&b.full[s], issued_phase >> s & 1, a.timeout_ns);
+    if (issued_mask >> (s + 8) & 1) mbar_wait(&b.dirty_full[s], issued_phase >> (s + 8) & 1, a.timeout_ns);
+  }
+}
+
+// Warp 1, one thread: issues the products.
+__device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_t* sA, const uint8_t* sB, uint32_t tmem) {
+  // Descriptors stay in registers: stages and k-steps differ in the start address alone,
+  // whose field (bytes / 16, shared memory < 256 KB) never carries.  G lies as [box of br
+  // keys][64-column chunk][key][128 bytes]: 64-column chunks are br * 128 bytes apart, 8-key
+  // groups 1024 (or, in boxes of 8 keys, a whole box).
+  const int br = a.box_rows;
+  const uint64_t pd0 = smem_desc(smem_u32(sA), 16, 1024, kSwizzle128B);
+  const uint64_t gd0 = smem_desc(smem_u32(sB), br * 128, br == 8 ? 4096u : 1024u, kSwizzle128B);
+  uint32_t koff[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    const int key = kk * 16, box = key / br;
+    koff[kk] = (uint32_t)(box * (4 * br * 128) + (key - box * br) * 128) >> 4;
+  }
+  Ring st, jr, acc, dr;
+  bool ok = true;
+  while (ok) {
+    if (!(ok = wait_bar(&b.job_full[jr.stage], jr.phase, b, a))) break;
+    const Job job = b.job[jr.stage];
+    if (job.b < 0) break;
+    const int vis = job.pos0 + job.rows;
+    const uint32_t idesc = idesc_bf16_f32(kM, (job_cols(a, job) + 15) & ~15, false, true);
+    const uint32_t d = tmem + acc.stage * kN;
+    if (!(ok = wait_bar(&b.acc_empty[acc.stage], acc.phase ^ 1, b, a))) break;
+    tc_fence_after_nc();
+    uint32_t accum = 0;  // of a step's first k-step
+    int it = job.it0;
+    for (const int e = min(first_dirty(job.pos0), job.it1); it < e; ++it) {
+      if (!(ok = wait_bar(&b.full[st.stage], st.phase, b, a))) break;
+      tc_fence_after_nc();
+      const uint64_t pd = pd0 + (uint64_t)(st.stage * (kABytes >> 4)), gd = gd0 + (uint64_t)(st.stage * (kBBytes >> 4));
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
+      accum = 1;
+      mma_commit_nc(&b.empty[st.stage]);
+      st.next(kStages);
+    }
+    for (; ok && it < job.it1; ++it) {
+      if (!(ok = wait_bar(&b.full[st.stage], st.phase, b, a))) break;
+      if (!(ok = wait_bar(&b.clean[dr.stage], dr.phase, b, a))) break;
+      dr.next(kStages);
+      tc_fence_after_nc();
+      const uint64_t pd = pd0 + (uint64_t)(st.stage * (kABytes >> 4)), gd = gd0 + (uint64_t)(st.stage * (kBBytes >> 4));
+      const int keys = vis - it * kK;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (kk * 16 < keys) mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
+      accum = 1;
+      mma_commit_nc(&b.empty[st.stage]);
+      st.next(kStages);
+    }
+    if (!ok) break;
+    mma_commit(&b.acc_full[acc.stage]);
+    mbar_arrive(&b.job_empty[jr.stage]);
+    acc.next(2);
+    jr.next(kJobSlots);
+  }
+  mma_commit(&b.drain);
+  mbar_wait(&b.drain, 0, a.timeout_ns);
+}
+
+// Warps 6-9: dirty steps.
+__device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, int t, int lane) {
+  const int br = a.box_rows;
+  Ring jr, dr;
+  int step = 0;  // steps before the job, modulo the stages
+  bool ok = true;
+  while (ok) {
+    if (!(ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a))) break;
+    const Job job = b.job[jr.stage];
+    if (job.b < 0) break;
+    for (int it = max(job.it0, first_dirty(job.pos0)); it < job.it1; ++it) {
+      if (!(ok = warp_wait(&b.dirty_full[dr.stage], dr.phase, b, a))) break;
+      const int keys = min(kK, max(0, job.pos0 + job.rows - it * kK)), rows = (keys + 15) & ~15;
+      const int lo = max(0, job.pos0 + 1 - it * kK);  // rows before are seen by all
+      const uint32_t s0 = smem_u32(sB + ((step + it - job.it0) % kStages) * kBBytes);
+      // rows t / 8 + 16 k: their 16-byte pieces are on their way before the first is looked
+      // at (this stands between a step's copy and its product)
+      bool found = false;
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        uint4 x[2][4];
+        uint32_t at[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = t / 8 + 16 * (2 * k2 + k), box = r / br;
+          at[k] = s0 + box * (4 * br * 128) + (r - box * br) * 128 + (t & 7) * 16;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            x[k][c] = r >= lo && r < keys ? ld_shared_v4(at[k] + c * br * 128) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = t / 8 + 16 * (2 * k2 + k);
+          uint32_t any = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            any |= non_finite(x[k][c].x) | non_finite(x[k][c].y) | non_finite(x[k][c].z) | non_finite(x[k][c].w);
+          if (r >= keys && r < rows) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) st_shared_v4(at[k] + c * br * 128, make_uint4(0, 0, 0, 0));
+          } else if (any) {  // (chunks past the strip's columns hold anything: unused)
+            found = true;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              st_shared_v4(at[k] + c * br * 128, make_uint4(drop(x[k][c].x), drop(x[k][c].y), drop(x[k][c].z), drop(x[k][c].w)));
+          }
+        }
+      }
+      if (found) *(volatile int*)&b.job[jr.stage].poison = 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.clean[dr.stage]);
+      dr.next(kStages);
+    }
+    if (!ok) break;
+    step = (step + job.it1 - job.it0) % kStages;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.job_empty[jr.stage]);
+    jr.next(kJobSlots);
+  }
+}
+
+// Warps 2-5: accumulators to outputs, or to partial sums.
+__device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t* sTurn, uint32_t tmem, int warp, int lane) {
+  const int quarter = warp & 3, r = quarter * 32 + lane;  // TMEM lane, the tile's row
+  const bool lead = warp == kEpi0 && lane == 0;
+  const size_t width = (size_t)a.H * a.m_pitch;
+  Ring jr, acc;
+  while (true) {
+    bool ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a);
+    const Job job = b.job[jr.stage];
+    const int cols = ok && job.b >= 0 ? job_cols(a, job) : 0;
+    // v's rows of the tile come into L2 while the products run
+    if (a.v && cols > 0 && r < job.rows) {
+      const char* vp = reinterpret_cast<const char*>(a.v + (size_t)(job.row0 + r) * a.v_pitch +
+                                                     (size_t)(a.h0 + job.hl) * a.m_pitch + job.strip * kN);
+      for (int x = 0; x < cols * 2; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + x));
+    }
+    if (cols > 0) ok = warp_wait(&b.acc_full[acc.stage], acc.phase, b, a);
+    if (!named_bar_and(1, 128, ok)) break;
+    if (job.b < 0) break;
+    tc_fence_after();
+    const bool poison = *(volatile int*)&b.job[jr.stage].poison != 0;
+    const int vis = job.pos0 + job.rows, head = a.h0 + job.hl, pos = job.pos0 + r, r8 = up8(job.rows);
+    const uint32_t trow = tmem + acc.stage * kN + ((uint32_t)(quarter * 32) << 16);
+    const bool warp_rows = quarter * 32 < job.rows;  // else this warp's rows are not there
+    const bool live = r < job.rows;
+    const size_t tkey = ((size_t)job.hl * a.strips + job.strip) * a.tiles + job.tile;
+    const size_t col0 = (size_t)head * a.m_pitch + job.strip * kN;
+    const float* den = a.den + ((size_t)job.hl * a.rows_tot + job.prow) * a.spans;
+    const int ns = vis <= 0 ? 0 : (vis + a.span_keys - 1) / a.span_keys;
+    const float null_w = a.null_bias ? expf(a.null_bias[head] - head_tau(a.tau, a.s, head, a.p.err, kKernPaged)) : 0.f;
+
+    // The keys whose non-finite gates the scrub warps took out of this job's product.
+    const int bad0 = max(job.pos0 + 1, job.it0 * kK), bad1 = min(vis, job.it1 * kK);
+    // The accumulator's 32 columns from c0 on of row r, with what was taken out put back
+    // where the row sees it.
+    auto fetch = [&](int c0, float (&y)[32]) {
+      uint32_t x[32];
+      __syncwarp();
+      tmem_ld32(trow + c0, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(x[c]);
+      if (poison && live) {
+        for (int key = bad0; key < min(bad1, pos + 1); ++key) {
+          const int pi = key / a.p.page_size, pg = paged_page(a.p, job.b, pi);
+          if (pg < 0) continue;
+          const __nv_bfloat16* g = a.g_pages + ((size_t)pg * a.p.page_size + (key - pi * a.p.page_size)) * width + col0 + c0;
+          const int kc = key % kK;
+          const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+              p_block(a, job.hl, job.prow, r8, key / kK) + r * 128 + ((((kc >> 3) ^ (r & 7)) << 4) | ((kc & 7) * 2))));
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float gv = c0 + c < cols ? __bfloat162float(g[c]) : 0.f;
+            if (!isfinite(gv)) y[c] += w * gv;
+          }
+        }
+      }
+    };
+    // A key range's slot for its partial sums, and, once they are written, whether this is
+    // the tile's last range to finish, which joins them all.
+    auto take_slot = [&]() -> int {
+      if (lead) {
+        const int sl = atomicAdd(a.next + 1, 1);
+        a.slot[tkey * a.nc_cap + job.c] = sl;
+        b.last = sl;
+      }
+      named_bar_sync(1, 128);
+      return b.last;
+    };
+    auto is_last = [&]() -> bool {
+      __threadfence();
+      named_bar_sync(1, 128);
+      if (lead) {
+        b.last = atomicAdd(a.done + tkey, 1) == job.nc - 1;
+        __threadfence();
+      }
+      named_bar_sync(1, 128);
+      return b.last != 0;
+    };
+    // slots of kSlotRegs ranges, looked up side by side
+    constexpr int kSlotRegs = 4;
+    int sl_reg[kSlotRegs];
+    auto slots = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < kSlotRegs; ++k) sl_reg[k] = k0 + k < job.nc ? __ldcg(a.slot + tkey * a.nc_cap + k0 + k) : -1;
+    };
+
+    if (job.rows <= kFewRows) {
+      // ---- few rows: the accumulator's rows go to shared memory, then this thread takes
+      // columns 2 t and 2 t + 1 of each
+      const int t = threadIdx.x - kEpi0 * 32, c = 2 * t;
+      float* turn = reinterpret_cast<float*>(sTurn);
+      auto at = [](int row, int col) { return row * kN + ((((col >> 2) ^ (row & 7)) << 2) | (col & 3)); };
+      // v and the denominators' parts arrive meanwhile
+      float2 vv[kFewRows];
+      float dn[kFewRows];
+      auto ask = [&]() {
+#pragma unroll
+        for (int i = 0; i < kFewRows; ++i) {
+          dn[i] = 0.f;
+          vv[i] = make_float2(1.f, 1.f);
+          if (i < job.rows && job.pos0 + i >= 0) {
+            for (int k = lane; k < ns; k += 32) dn[i] += __ldcg(den + (size_t)i * a.spans + k);
+            if (a.v && c < cols) {
+              const __nv_bfloat16* vp = a.v + (size_t)(job.row0 + i) * a.v_pitch + col0 + c;
+              if (a.v_vec) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(vp);
+                vv[i] = make_float2(bf16lo(x), bf16hi(x));
+              } else {
+                vv[i].x = __bfloat162float(vp[0]);
+                if (c + 1 < cols) vv[i].y = __bfloat162float(vp[1]);
+              }
+            }
+          }
+        }
+      };
+      if (job.nc == 1) ask();
+      if (quarter == 0) {
+        for (int c0 = 0; c0 < cols; c0 += 32) {
+          float y[32];
+          fetch(c0, y);
+          if (live) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<float4*>(turn + at(r, c0 + 4 * u)) =
+                  make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+          }
+        }
+      }
+      named_bar_sync(1, 128);
+      bool finish = true;
+      if (job.nc > 1) {
+        const int sl = take_slot();
+        float* dst = a.part + (size_t)sl * (kN * a.r8cap);
+        if ((unsigned)sl < (unsigned)a.n_slots) {
+          for (int i = 0; i < job.rows; ++i)
+            __stcg(reinterpret_cast<float2*>(dst + i * kN + c), *reinterpret_cast<const float2*>(turn + at(i, c)));
+        }
+        finish = is_last();
+        if (finish) ask();
+      }
+      if (finish) {
+        float2 y[kFewRows];
+#pragma unroll
+        for (int i = 0; i < kFewRows; ++i)
+          y[i] = job.nc == 1 && i < job.rows ? *reinterpret_cast<const float2*>(turn + at(i, c)) : make_float2(0.f, 0.f);
+        for (int k0 = 0; job.nc > 1 && k0 < job.nc; k0 += kSlotRegs) {
+          slots(k0);
+#pragma unroll
+          for (int k = 0; k < kSlotRegs; ++k) {
+            if ((unsigned)sl_reg[k] >= (unsigned)a.n_slots) continue;
+            const float* src = a.part + (size_t)sl_reg[k] * (kN * a.r8cap) + c;
+#pragma unroll
+            for (int i = 0; i < kFewRows; ++i) {
+              if (i >= job.rows) break;
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(src + i * kN));
+              y[i].x += x.x;
+              y[i].y += x.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kFewRows; ++i) {
+          if (i >= job.rows) break;
+          float d = dn[i];
+          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+          const int ps = job.pos0 + i;
+          const float inv = 1.f / (d + (float)(ps + 1) * null_w);
+          // pairs: the last one may run into the pitch's padding
+          if (c < cols)
+            *reinterpret_cast<uint32_t*>(a.out + (size_t)(job.row0 + i) * width + col0 + c) =
+                ps >= 0 ? pack_bf16x2(y[i].x * inv * vv[i].x, y[i].y * inv * vv[i].y) : 0u;
+        }
+      }
+    } else {
+      bool finish = true;
+      if (job.nc > 1) {
+        const int sl = take_slot();
+        float* dst = a.part + (size_t)sl * (kN * a.r8cap);
+        if (warp_rows && (unsigned)sl < (unsigned)a.n_slots) {
+          for (int c0 = 0; c0 < cols; c0 += 32) {
+            float y[32];
+            fetch(c0, y);
+            if (r < r8) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                __stcg(reinterpret_cast<float4*>(dst) + (size_t)(c0 / 4 + u) * a.r8cap + r,
+                       make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]));
+            }
+          }
+        }
+        finish = is_last();
+      }
+      if (finish && warp_rows) {
+        uint8_t* turn = sTurn + quarter * 4096;
+        const uint32_t t_s = smem_u32(turn);
+        // in row order this lane takes 4 columns of rows quarter * 32 + lane / 8 + 4 k
+        const int lr = quarter * 32 + lane / 8, lc = (lane & 7) * 4;
+        const bool all_rows = quarter * 32 + 32 <= job.rows && job.pos0 >= 0;
+        uint2 vn[8];  // v of the next 32 columns
+        auto load_v = [&](int c) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            vn[k] = make_uint2(0x3f803f80u, 0x3f803f80u);  // ones
+            const int rr = lr + 4 * k;
+            if (a.v && c < cols && (all_rows || (rr < job.rows && job.pos0 + rr >= 0))) {
+              const __nv_bfloat16* vp = a.v + (size_t)(job.row0 + rr) * a.v_pitch + col0 + c;
+              if (a.v_vec) {
+                vn[k] = *reinterpret_cast<const uint2*>(vp);
+              } else {
+                float e[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) e[q] = c + q < cols ? __bfloat162float(vp[q]) : 0.f;
+                vn[k] = make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
+              }
+            }
+          }
+        };
+        load_v(lc);
+        float inv = 0.f;
+        if (live && pos >= 0) {
+          float d = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < ns; i += 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(den + (size_t)r * a.spans + i));
+            d += x.x + (i + 1 < ns ? x.y : 0.f) + (i + 2 < ns ? x.z : 0.f) + (i + 3 < ns ? x.w : 0.f);
+          }
+          inv = 1.f / (d + (float)(pos + 1) * null_w);
+        }
+        for (int c0 = 0; c0 < cols; c0 += 32) {
+          const int c = c0 + lc;
+          uint2 vr[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) vr[k] = vn[k];
+          load_v(c + 32);
+          float y[32];
+          if (job.nc == 1) {
+            fetch(c0, y);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) y[q] = 0.f;
+            for (int k0 = 0; k0 < job.nc; k0 += kSlotRegs) {
+              if (c0 == 0 || job.nc > kSlotRegs) slots(k0);
+#pragma unroll
+              for (int k = 0; k < kSlotRegs; ++k) {
+                if (!live || (unsigned)sl_reg[k] >= (unsigned)a.n_slots) continue;
+                const float4* src = reinterpret_cast<const float4*>(a.part + (size_t)sl_reg[k] * (kN * a.r8cap));
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                  const float4 x = __ldcg(src + (size_t)(c0 / 4 + u) * a.r8cap + r);
+                  y[4 * u] += x.x; y[4 * u + 1] += x.y; y[4 * u + 2] += x.z; y[4 * u + 3] += x.w;
+                }
+              }
+            }
+          }
+          // a row without keys gives zeros, whatever its accumulator holds
+          const bool seen = live && pos >= 0;
+          __syncwarp();  // the previous columns have been read
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t e[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e[q] = seen ? __float_as_uint(y[4 * u + q] * inv) : 0u;
+            st_shared_v4(t_s + lane * 128 + ((u ^ (lane & 7)) << 4), make_uint4(e[0], e[1], e[2], e[3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rw = lane / 8 + 4 * k, rr = quarter * 32 + rw;
+            const uint4 x = ld_shared_v4(t_s + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
+            // four columns: the last ones may run into the pitch's padding
+            if (rr < job.rows && c < cols)
+              *reinterpret_cast<uint2*>(a.out + (size_t)(job.row0 + rr) * width + col0 + c) =
+                  make_uint2(pack_bf16x2(__uint_as_float(x.x) * bf16lo(vr[k].x), __uint_as_float(x.y) * bf16hi(vr[k].x)),
+                             pack_bf16x2(__uint_as_float(x.z) * bf16lo(vr[k].y), __uint_as_float(x.w) * bf16hi(vr[k].y)));
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&b.acc_empty[acc.stage]);
+      mbar_arrive(&b.job_empty[jr.stage]);
+    }
+    acc.next(2);
+    jr.next(kJobSlots);
+  }
+}
 
 __global__ void __launch_bounds__(kGThreads, 1)
-    paged_gates_kernel(const __grid_constant__ CUtensorMap tmG, const TcArgs a) {
+    paged_gates_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG4, const TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = base;
   uint8_t* sB = base + kStages * kABytes;
-  GBars& b = *reinterpret_cast<GBars*>(sB + kStages * kBBytes);
+  uint8_t* sTurn = sB + kStages * kBBytes;
+  GBars& b = *reinterpret_cast<GBars*>(sTurn + kTurnBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&b.full[s], 1);
-      mbar_init(&b.empty[s], 5);  // the products' commit and the 4 scrub warps
+      mbar_init(&b.empty[s], 1);
+      mbar_init(&b.dirty_full[s], 1);
       mbar_init(&b.clean[s], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -349,7 +1058,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
     for (int i = 0; i < kJobSlots; ++i) {
       mbar_init(&b.job_full[i], 1);
-      mbar_init(&b.job_empty[i], 9);  // MMA issuer, 4 epilogue warps, 4 scrub warps
+      mbar_init(&b.job_empty[i], 10);  // producer, MMA issuer, 4 epilogue warps, 4 scrub warps
     }
     mbar_init(&b.drain, 1);
     b.abort = 0;
@@ -365,368 +1074,15 @@ __global__ void __launch_bounds__(kGThreads, 1)
   const uint32_t tmem = b.tmem_base;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ scheduler, TMA producer
-    // steps of the whole launch, and from them the steps of a key range
-    const int HS = a.heads * a.strips;
-    long long total = 0;
-    for (int i = lane; i < a.p.B; i += 32) total += seq_steps(paged_seq(a.p, i, false));
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    total *= HS;
-    const int range = (int)max((long long)kMinSteps, (total + kJobsPerSm * gridDim.x - 1) / (kJobsPerSm * (long long)gridDim.x));
-    griddep_wait();  // P, den and the counters are the weights kernel's
-
-    // a window of 32 sequences, one per lane: rows, length, jobs (inclusive prefix)
-    int w0 = -32;
-    long long jbase = 0, jend = 0, pre = 0;
-    PagedSeq ws{0, 0, 0};
-    int wmt = 0, wnc = 0;
-    Ring st, jr;
-    uint32_t issued_mask = 0, issued_phase = 0;
-    bool ok = true;
-    int nxt = 0;
-    if (lane == 0) nxt = atomicAdd(a.next, 1);
-    while (ok) {
-      long long j = __shfl_sync(0xffffffffu, nxt, 0);
-      if (lane == 0) nxt = atomicAdd(a.next, 1);  // the next job's number, while this one runs
-      while (j >= jend && w0 + 32 < a.p.B) {
-        w0 += 32;
-        jbase = jend;
-        long long jobs = 0;
-        if (w0 + lane < a.p.B) {
-          ws = paged_seq(a.p, w0 + lane, false);
-          wmt = (ws.n + kM - 1) / kM;
-          wnc = (steps_of(ws.len) + range - 1) / range;
-          jobs = (long long)wmt * wnc * HS;
-        }
-        pre = jobs;
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long x = __shfl_up_sync(0xffffffffu, pre, o);
-          if (lane >= o) pre += x;
-        }
-        jend = jbase + __shfl_sync(0xffffffffu, pre, 31);
-      }
-      const bool none = j >= jend;
-      Job job;
-      job.b = -1;
-      int r8 = 0;
-      if (!none) {
-        const long long rel = j - jbase;
-        const int owner = __popc(__ballot_sync(0xffffffffu, pre <= rel));
-        const long long before = __shfl_sync(0xffffffffu, pre, owner > 0 ? owner - 1 : 0);
-        const int idx = (int)(rel - (owner > 0 ? before : 0));
-        const int r0 = __shfl_sync(0xffffffffu, ws.r0, owner), n = __shfl_sync(0xffffffffu, ws.n, owner);
-        const int len = __shfl_sync(0xffffffffu, ws.len, owner);
-        const int mt = __shfl_sync(0xffffffffu, wmt, owner), nc = __shfl_sync(0xffffffffu, wnc, owner);
-        const int i = idx % mt, hs = idx / mt / nc;
-        job.c = idx / mt % nc;
-        job.b = w0 + owner;
-        job.row0 = r0 + i * kM;
-        job.rows = min(kM, n - i * kM);
-        job.pos0 = len - n + i * kM;
-        job.hl = hs / a.strips;
-        job.strip = hs - job.hl * a.strips;
-        const int u = steps_of(job.pos0 + job.rows);
-        job.nc = (u + range - 1) / range;
-        job.it0 = job.c * range;
-        job.it1 = min(u, job.it0 + range);
-        job.tile = r0 / kM + job.b + i;
-        job.prow = scratch_row(r0, job.b) + i * kM;
-        job.poison = 0;
-        if (job.c >= job.nc) continue;  // an earlier tile of the sequence sees fewer keys
-        r8 = up8(job.rows);
-      }
-      ok = warp_wait(&b.job_empty[jr.stage], jr.phase ^ 1, b, a);
-      if (!ok) break;
-      if (lane == 0) {
-        b.job[jr.stage] = job;
-        mbar_arrive(&b.job_full[jr.stage]);
-      }
-      jr.next(kJobSlots);
-      if (none) break;
-
-      const int vis = job.pos0 + job.rows, cols = job_cols(a, job);
-      const int nbc = (cols + 63) / 64, head = a.h0 + job.hl;
-      const int br = a.box_rows, spp = kK / br;  // boxes of a step
-      const int box1 = vis <= 0 ? 0 : (min(job.it1 * kK, vis) + br - 1) / br;
-      int first = job.it0 * spp;  // box of lane 0
-      auto lookup = [&](int box) -> int {
-        if (box >= box1) return -1;
-        const int key = box * br, pi = key / a.p.page_size;
-        return paged_page(a.p, job.b, pi);
-      };
-      int page = lookup(first + lane);
-      for (int it = job.it0; ok && it < job.it1; ++it) {
-        if (it * spp >= first + 32) {
-          first += 32;
-          page = lookup(first + lane);
-        }
-        ok = warp_wait(&b.empty[st.stage], st.phase ^ 1, b, a);
-        if (!ok) break;
-        const int box0 = it * spp, nb = max(0, min(spp, box1 - box0));
-        uint8_t* dB = sB + st.stage * kBBytes;
-        // boxes whose page is not one of the pool are loaded as zeros (out of range)
-        const uint32_t bytes = (uint32_t)(vis > 0 ? r8 * 128 : 0) + (uint32_t)(nb * nbc * br * 128);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&b.full[st.stage], bytes);
-          if (vis > 0) bulk_load(sA + st.stage * kABytes, p_block(a, job.hl, job.prow, r8, it), r8 * 128, &b.full[st.stage]);
-        }
-        __syncwarp();
-        const int mybox = first + lane;
-        if (mybox >= box0 && mybox < box0 + nb) {
-          const int key = mybox * br, r = key % a.p.page_size;
-          const int pg = page < 0 ? a.p.n_pages : page;
-          for (int c = 0; c < nbc; ++c)
-            tma_load_4d(dB + c * kGBox + (mybox - box0) * br * 128, &tmG, &b.full[st.stage], job.strip * kN + c * 64,
-                        head, r, pg);
-        }
-        issued_mask |= 1u << st.stage;
-        issued_phase = (issued_phase & ~(1u << st.stage)) | (st.phase << st.stage);
-        st.next(kStages);
-      }
-    }
-    // copies still in flight must land before the CTA exits
-    for (int s = 0; s < kStages; ++s)
-      if (issued_mask >> s & 1) mbar_wait(&b.full[s], issued_phase >> s & 1, a.timeout_ns);
+    produce(a, b, sA, sB, &tmG, &tmG4, lane);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      Ring st, jr, acc;
-      uint32_t clean_phase = 0;
-      bool ok = true;
-      while (ok) {
-        if (!(ok = wait_bar(&b.job_full[jr.stage], jr.phase, b, a))) break;
-        const Job job = b.job[jr.stage];
-        if (job.b < 0) break;
-        const uint32_t idesc = idesc_bf16_f32(kM, (job_cols(a, job) + 15) & ~15, false, true);
-        const uint32_t d = tmem + acc.stage * kN;
-        if (!(ok = wait_bar(&b.acc_empty[acc.stage], acc.phase ^ 1, b, a))) break;
-        for (int it = job.it0; it < job.it1; ++it) {
-          if (!(ok = wait_bar(&b.full[st.stage], st.phase, b, a))) break;
-          if (step_dirty(job, it)) {
-            if (!(ok = wait_bar(&b.clean[st.stage], clean_phase >> st.stage & 1, b, a))) break;
-            clean_phase ^= 1u << st.stage;
-          }
-          tc_fence_after();
-          const uint32_t aa = smem_u32(sA + st.stage * kABytes), bb = smem_u32(sB + st.stage * kBBytes);
-          const int ks = (step_keys(job, it) + 15) / 16;
-          for (int kk = 0; kk < ks; ++kk)
-            mma_bf16_ss(d, smem_desc(aa + kk * 32, 16, 1024, kSwizzle128B),
-                        smem_desc(bb + kk * 2048, kGBox, 1024, kSwizzle128B), idesc, it != job.it0 || kk != 0);
-          mma_commit(&b.empty[st.stage]);
-          st.next(kStages);
-        }
-        if (!ok) break;
-        mma_commit(&b.acc_full[acc.stage]);
-        mbar_arrive(&b.job_empty[jr.stage]);
-        acc.next(2);
-        jr.next(kJobSlots);
-      }
-      mma_commit(&b.drain);
-      mbar_wait(&b.drain, 0, a.timeout_ns);
-    }
+    if (lane == 0) multiply(a, b, sA, sB, tmem);
   } else if (warp < kScrub0) {
-    // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, r = quarter * 32 + lane;
-    const bool lead = warp == kEpi0 && lane == 0;
-    Ring jr, acc;
-    while (true) {
-      bool ok = wait_bar(&b.job_full[jr.stage], jr.phase, b, a);
-      const Job job = b.job[jr.stage];
-      if (ok && job.b >= 0) ok = wait_bar(&b.acc_full[acc.stage], acc.phase, b, a);
-      if (!named_bar_and(1, 128, ok)) break;
-      if (job.b < 0) break;
-      tc_fence_after();
-      const bool poison = *(volatile int*)&b.job[jr.stage].poison != 0;
-      const int vis = job.pos0 + job.rows, cols = job_cols(a, job), head = a.h0 + job.hl, pos = job.pos0 + r;
-      const int r8 = up8(job.rows);
-      const uint32_t trow = tmem + acc.stage * kN + ((uint32_t)(quarter * 32) << 16);
-      const bool warp_rows = quarter * 32 < job.rows;  // else this warp's rows are not there
-      const bool live = r < job.rows;
-      const size_t tkey = ((size_t)job.hl * a.strips + job.strip) * a.tiles + job.tile;
-      const size_t width = (size_t)a.H * a.m_pitch;
-
-      // the accumulator's 32 columns from c0 on of this thread's row, with the non-finite
-      // gates that the scrub warps took out put back where the row sees them
-      auto fetch = [&](int c0, float (&y)[32]) {
-        uint32_t x[32];
-        __syncwarp();
-        tmem_ld32(trow + c0, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(x[c]);
-        if (poison && live) {
-          const int k1 = min(min(pos, vis - 1), job.it1 * kK - 1);
-          for (int key = max(job.pos0 + 1, job.it0 * kK); key <= k1; ++key) {
-            const int pi = key / a.p.page_size, pg = paged_page(a.p, job.b, pi);
-            if (pg < 0) continue;
-            const uint8_t* pb = p_block(a, job.hl, job.prow, r8, key / kK) + r * 128;
-            const int kc = key % kK;
-            const float w = __bfloat162float(
-                *reinterpret_cast<const __nv_bfloat16*>(pb + ((((kc >> 3) ^ (r & 7)) << 4) | ((kc & 7) * 2))));
-            const __nv_bfloat16* g = a.g_pages + ((size_t)pg * a.p.page_size + (key - pi * a.p.page_size)) * width +
-                                     (size_t)head * a.m_pitch + job.strip * kN + c0;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float gv = c0 + c < cols ? __bfloat162float(g[c]) : 0.f;
-              if (!isfinite(gv)) y[c] += w * gv;
-            }
-          }
-        }
-      };
-
-      bool finish = true;
-      if (job.nc > 1) {
-        // a key range's partial sums; the last range of the tile to finish joins them
-        if (lead) {
-          const int sl = atomicAdd(a.next + 1, 1);
-          a.slot[tkey * a.nc_cap + job.c] = sl;
-          b.last = sl;
-        }
-        named_bar_sync(1, 128);
-        const int sl = b.last;
-        float* dst = a.part + (size_t)sl * (kN * a.r8cap);
-        if (warp_rows && sl < a.n_slots) {
-          for (int c0 = 0; c0 < cols; c0 += 32) {
-            float y[32];
-            fetch(c0, y);
-            if (r < r8) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                __stcg(reinterpret_cast<float4*>(dst) + (size_t)(c0 / 4 + u) * a.r8cap + r,
-                       make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]));
-            }
-          }
-        }
-        __threadfence();
-        named_bar_sync(1, 128);
-        if (lead) {
-          b.last = atomicAdd(a.done + tkey, 1) == job.nc - 1;
-          __threadfence();
-        }
-        named_bar_sync(1, 128);
-        finish = b.last != 0;
-      }
-      if (finish && warp_rows) {
-        float inv = 0.f;
-        if (live && pos >= 0) {
-          const float* dp = a.den + ((size_t)job.hl * a.rows_tot + job.prow + r) * a.spans;
-          const int ns = (vis + a.span_keys - 1) / a.span_keys;
-          float d = 0.f;
-          for (int i = 0; i < ns; ++i) d += __ldcg(dp + i);
-          if (a.null_bias) {
-            const float tau = head_tau(a.tau, a.s, head, a.p.err, kKernPaged);
-            d += (float)(pos + 1) * expf(a.null_bias[head] - tau);
-          }
-          inv = 1.f / d;
-        }
-        const size_t row = job.row0 + r, col = (size_t)head * a.m_pitch + job.strip * kN;
-        for (int c0 = 0; c0 < cols; c0 += 32) {
-          float y[32];
-          if (job.nc == 1) {
-            fetch(c0, y);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) y[c] = 0.f;
-            if (live) {
-              for (int k = 0; k < job.nc; ++k) {
-                const int sl = __ldcg(a.slot + tkey * a.nc_cap + k);
-                if ((unsigned)sl >= (unsigned)a.n_slots) continue;
-                const float4* src = reinterpret_cast<const float4*>(a.part + (size_t)sl * (kN * a.r8cap));
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                  const float4 x = __ldcg(src + (size_t)(c0 / 4 + u) * a.r8cap + r);
-                  y[4 * u] += x.x; y[4 * u + 1] += x.y; y[4 * u + 2] += x.z; y[4 * u + 3] += x.w;
-                }
-              }
-            }
-          }
-          if (!live) continue;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int cc = c0 + 8 * u;
-            if (cc >= cols) break;
-            float z[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = pos >= 0 ? y[8 * u + e] * inv : 0.f;
-            if (a.v && pos >= 0) {
-              const __nv_bfloat16* vp = a.v + row * a.v_pitch + col + cc;
-              if (a.v_vec) {
-                const uint4 x = *reinterpret_cast<const uint4*>(vp);
-                z[0] *= bf16lo(x.x); z[1] *= bf16hi(x.x); z[2] *= bf16lo(x.y); z[3] *= bf16hi(x.y);
-                z[4] *= bf16lo(x.z); z[5] *= bf16hi(x.z); z[6] *= bf16lo(x.w); z[7] *= bf16hi(x.w);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] *= cc + e < cols ? __bfloat162float(vp[e]) : 0.f;
-              }
-            }
-            // whole vectors: the last one may run into the pitch's padding
-            st_global_v4(a.out + row * width + col + cc, pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
-                         pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&b.acc_empty[acc.stage]);
-        mbar_arrive(&b.job_empty[jr.stage]);
-      }
-      acc.next(2);
-      jr.next(kJobSlots);
-    }
+    finish_tiles(a, b, sTurn, tmem, warp, lane);
+  } else if (warp < kSched) {
+    scrub(a, b, sB, threadIdx.x - kScrub0 * 32, lane);
   } else {
-    // ------------------------------------------------------------ scrub
-    const int t = threadIdx.x - kScrub0 * 32;
-    Ring st, jr;
-    bool ok = true;
-    while (ok) {
-      if (!(ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a))) break;
-      const Job job = b.job[jr.stage];
-      if (job.b < 0) break;
-      const int nbc = (job_cols(a, job) + 63) / 64;
-      // every step is waited for, and its stage is free only once this warp has seen it too:
-      // a parity wait that ran more than one fill ahead or behind would see the wrong fill
-      for (int it = job.it0; it < job.it1; ++it) {
-        if (!(ok = warp_wait(&b.full[st.stage], st.phase, b, a))) break;
-        if (step_dirty(job, it)) {
-          const int keys = max(0, step_keys(job, it)), rows = (keys + 15) & ~15;
-          const int seen = job.pos0 - it * kK;  // rows <= seen are seen by all
-          const uint32_t s0 = smem_u32(sB + st.stage * kBBytes);
-          bool found = false;
-          for (int r = max(0, seen + 1) + t / 8; r < rows; r += 16) {
-            for (int c = 0; c < nbc; ++c) {
-              const uint32_t at = s0 + c * kGBox + r * 128 + (t & 7) * 16;
-              if (r >= keys) {
-                st_shared_v4(at, make_uint4(0, 0, 0, 0));
-                continue;
-              }
-              uint4 x = ld_shared_v4(at);
-              uint32_t y[4] = {x.x, x.y, x.z, x.w};
-              bool hit = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (bad_bits(y[e], 0x7f80u)) { y[e] &= 0xffff0000u; hit = true; }
-                if (bad_bits(y[e], 0x7f800000u)) { y[e] &= 0xffffu; hit = true; }
-              }
-              if (hit) {
-                st_shared_v4(at, make_uint4(y[0], y[1], y[2], y[3]));
-                found = true;
-              }
-            }
-          }
-          if (found) *(volatile int*)&b.job[jr.stage].poison = 1;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&b.clean[st.stage]);
-        }
-        if (lane == 0) mbar_arrive(&b.empty[st.stage]);
-        st.next(kStages);
-      }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b.job_empty[jr.stage]);
-      jr.next(kJobSlots);
-    }
+    schedule(a, b, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -754,7 +1110,7 @@ int box_rows(int page_size) {
 }
 
 struct TcPlan {
-  int rows_tot, key_blocks, span_keys, spans, strips, tiles, r8cap, nc_cap, n_slots, heads, grid;
+  int rows_tot, key_blocks, span_keys, spans, strips, tiles, r8cap, min_steps, jobs_per_sm, nc_cap, n_slots, heads, grid;
   size_t P, den, part, slot, done, next, total;
 };
 
@@ -766,11 +1122,15 @@ TcPlan tc_plan(const PagedCall& c) {
   // at most 32 spans of whole 128-key blocks (their sums are added once per strip)
   l.span_keys = ceil_div(ceil_div(c.p.max_len, 32), 128) * 128;
   if (l.span_keys < 256) l.span_keys = 256;
-  l.spans = ceil_div(c.p.max_len, l.span_keys);
+  l.spans = (ceil_div(c.p.max_len, l.span_keys) + 3) & ~3;
   l.strips = ceil_div(c.m_h, kN);
   l.tiles = c.p.N / kM + c.p.B;
   l.r8cap = c.p.max_new < kM ? up8(c.p.max_new) : kM;
-  l.nc_cap = ceil_div(l.key_blocks, kMinSteps);
+  // joining key ranges is cheap for few rows; for many it moves as much as their products
+  // take, so tiles are left whole when they are about two per SM
+  l.min_steps = l.r8cap <= kFewRows ? 3 : 8;
+  l.jobs_per_sm = l.r8cap <= kFewRows ? kJobsPerSm : 2;
+  l.nc_cap = ceil_div(l.key_blocks, l.min_steps);
   l.grid = sms;
   // a tile that is cut has at most twice as many ranges as whole ranges fit in it
   l.n_slots = 2 * kJobsPerSm * sms;
@@ -789,11 +1149,24 @@ TcPlan tc_plan(const PagedCall& c) {
   return l;
 }
 
+template <int DH>
+void launch_weights_few_dh(const TcArgs& a, int rows, dim3 g, cudaStream_t s) {
+  if (rows == 1) paged_weights_few_kernel<1, DH><<<g, kWThreads, 0, s>>>(a);
+  else if (rows == 2) paged_weights_few_kernel<2, DH><<<g, kWThreads, 0, s>>>(a);
+  else if (rows <= 4) paged_weights_few_kernel<4, DH><<<g, kWThreads, 0, s>>>(a);
+  else paged_weights_few_kernel<8, DH><<<g, kWThreads, 0, s>>>(a);
+}
+void launch_weights_few(const TcArgs& a, int rows, dim3 g, cudaStream_t s) {
+  if (a.d_h == 64) launch_weights_few_dh<64>(a, rows, g, s);
+  else if (a.d_h == 32) launch_weights_few_dh<32>(a, rows, g, s);
+  else launch_weights_few_dh<16>(a, rows, g, s);
+}
+
 }  // namespace
 
 bool paged_tc_takes(tg_dtype dt, const PagedCall& c) {
   // the shape alone decides, so that the workspace can be sized without the pointers
-  return dt == TG_BF16 && c.p.max_new > 8 && (c.d_h == 16 || c.d_h == 32 || c.d_h == 64) && c.m_pitch % 8 == 0 &&
+  return dt == TG_BF16 && (c.d_h == 16 || c.d_h == 32 || c.d_h == 64) && c.m_pitch % 8 == 0 &&
          box_rows(c.p.page_size) >= 8;
 }
 
@@ -804,7 +1177,7 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   TcArgs a = {};
   a.p = c.p; a.H = c.H; a.d_h = c.d_h; a.m_h = c.m_h; a.m_pitch = c.m_pitch;
   a.rows_tot = l.rows_tot; a.key_blocks = l.key_blocks; a.span_keys = l.span_keys; a.spans = l.spans;
-  a.strips = l.strips; a.tiles = l.tiles; a.r8cap = l.r8cap; a.nc_cap = l.nc_cap; a.n_slots = l.n_slots;
+  a.strips = l.strips; a.tiles = l.tiles; a.r8cap = l.r8cap; a.min_steps = l.min_steps; a.jobs_per_sm = l.jobs_per_sm; a.nc_cap = l.nc_cap; a.n_slots = l.n_slots;
   a.box_rows = box_rows(c.p.page_size);
   a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
   a.v_vec = c.v && (reinterpret_cast<uintptr_t>(c.v) & 15u) == 0 && c.v_pitch % 8 == 0;
@@ -820,8 +1193,11 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   a.next = reinterpret_cast<int*>(base + l.next);
   a.timeout_ns = kTimeoutNs;
 
-  CUtensorMap mG;
+  CUtensorMap mG, mG4;
   cudaError_t e = make_tmap_4d_heads(&mG, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 64);
+  mG4 = mG;  // used only where a head holds a whole strip
+  if (e == cudaSuccess && c.m_h >= kN)
+    e = make_tmap_5d_chunks(&mG4, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 4);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(paged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
   if (e == cudaSuccess)
@@ -829,7 +1205,9 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   for (a.h0 = 0; a.h0 < c.H; a.h0 += l.heads) {
     a.heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
-    paged_weights_kernel<<<dim3(l.tiles, a.heads, l.spans), kWThreads, kWSmem, s>>>(a);
+    const dim3 gw(l.tiles, a.heads, ceil_div(c.p.max_len, l.span_keys));
+    if (c.p.max_new > 8) paged_weights_kernel<<<gw, kWThreads, kWSmem, s>>>(a);
+    else launch_weights_few(a, c.p.max_new, gw, s);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -842,7 +1220,7 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_gates_kernel, mG, a);
+    e = cudaLaunchKernelEx(&cfg, paged_gates_kernel, mG, mG4, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

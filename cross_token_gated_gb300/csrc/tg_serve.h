@@ -57,9 +57,8 @@ struct PagedCall {
 size_t paged_simt_ws_bytes(tg_dtype dt, const PagedCall& c);
 cudaError_t launch_paged_simt(tg_dtype dt, const PagedCall& c, cudaStream_t s);
 
-// The same on the tensor cores (bf16 chunks).  Whether the shapes are ones it takes: more
-// than 8 new tokens of a sequence, head widths and pitches that TMA and tcgen05 read, pages
-// of a multiple of 8 tokens.  q, v, out and the pools must also be 16-byte aligned (v: else
+// The same on the tensor cores (bf16).  Whether the shapes are ones it takes: head widths and
+// pitches that TMA and tcgen05 read, pages of a multiple of 8 tokens.  q, v, out and the pools must also be 16-byte aligned (v: else
 // read element-wise).
 bool paged_tc_takes(tg_dtype dt, const PagedCall& c);
 size_t paged_tc_ws_bytes(const PagedCall& c);

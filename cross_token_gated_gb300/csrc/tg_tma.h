@@ -26,4 +26,11 @@ cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, uint64_t batch, uin
 cudaError_t make_tmap_4d_heads(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t heads,
                                uint64_t head_cols, uint64_t head_pitch, uint32_t box_rows, uint32_t box_cols);
 
+// Over the same tensor with the columns in whole chunks of 64, for boxes of several chunks
+// laid out one after the other: coordinates (column of a chunk, row, chunk, head, batch), box
+// [1, 1, box_chunks, box_rows, 64].  Only the head_cols / 64 whole chunks of a head exist;
+// reads past them are zeros.
+cudaError_t make_tmap_5d_chunks(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t heads,
+                                uint64_t head_cols, uint64_t head_pitch, uint32_t box_rows, uint32_t box_chunks);
+
 }  // namespace tg

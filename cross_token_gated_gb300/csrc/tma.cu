@@ -69,4 +69,12 @@ cudaError_t make_tmap_4d_heads(CUtensorMap* map, const void* base, uint64_t batc
   return encode(map, base, 4, dims, strides, box);
 }
 
+cudaError_t make_tmap_5d_chunks(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t heads,
+                                uint64_t head_cols, uint64_t head_pitch, uint32_t box_rows, uint32_t box_chunks) {
+  cuuint64_t dims[5] = {64, rows, head_cols / 64, heads, batch};
+  cuuint64_t strides[4] = {heads * head_pitch * 2, 128, head_pitch * 2, rows * heads * head_pitch * 2};
+  cuuint32_t box[5] = {64, box_rows, box_chunks, 1, 1};
+  return encode(map, base, 5, dims, strides, box);
+}
+
 }  // namespace tg
