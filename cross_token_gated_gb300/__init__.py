@@ -106,6 +106,9 @@ def declared_functions() -> list[str]:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Loads (building in-tree first if needed) the C-ABI library."""
     global _lib
+    lib = _lib
+    if lib is not None:
+        return lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -459,71 +462,101 @@ def wango_decode_step(q, k, g, v, out, state, pos, *, H, window, s=10.0, tau=Non
 
 # ----------------------------------------------- norm and rotary position of q and k
 
-def _check(t, name, dtype=None, like=None, dense=False, shape=None):
-    """Raises unless t is a tensor that the library can read as it lies."""
-    if dtype is not None and t.dtype != dtype:
+# These calls serve single tokens, whose kernels take a few microseconds: the checks are
+# written to cost little beside them.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev):
+    """The stream to launch on: the caller's, or device dev's current one."""
+    if stream is None and _raw_stream is not None and dev >= 0:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _bad(t, name, dtype, dev, shape):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not with the call's other tensors")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows_pitch(t, name):
+def _dense(t, name, dtype, dev, shape=None):
+    """Address of a contiguous tensor of this type, device and shape; raises otherwise."""
+    if t.dtype is not dtype or t.get_device() != dev or (shape is not None and t.shape != shape) \
+            or not t.is_contiguous():
+        _bad(t, name, dtype, dev, shape)
+    return t.data_ptr()
+
+
+def _rows_pitch(t, name, dtype, dev):
     """(rows, width, pitch in elements) of a [..., width] tensor whose rows lie at one pitch
     (a dense tensor, or a column slice of one)."""
-    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dtype is not dtype or t.get_device() != dev:
+        _bad(t, name, dtype, dev, None)
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 2 or (stride[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be [..., width] with unit stride along its last dimension")
-    width, rows, pitch = t.shape[-1], 1, None
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] != 1:
-            if pitch is None:
-                pitch = t.stride(i)
-            elif rows and t.stride(i) != pitch * rows:
+    if len(shape) == 2:
+        rows, width = shape
+        pitch = stride[0] if rows > 1 else width
+        if pitch < width and rows > 1:
+            raise ValueError(f"{name}'s rows overlap")
+        return rows, width, pitch
+    width, rows, pitch = shape[-1], 1, 0
+    for n, st in zip(shape[-2::-1], stride[-2::-1]):
+        if n != 1:
+            if rows == 1:
+                pitch = st
+            elif rows and st != pitch * rows:
                 raise ValueError(f"{name}'s rows must lie at one pitch")
-        rows *= t.shape[i]
-    pitch = width if pitch is None else pitch
+            rows *= n
     if rows > 1 and pitch < width:
         raise ValueError(f"{name}'s rows overlap")
-    return rows, width, max(pitch, width)
+    return rows, width, pitch if pitch > width else width
+
+
+def _optional(t, name, dtype, dev, shape=None):
+    return None if t is None else _dense(t, name, dtype, dev, shape)
 
 
 def _qk_params(q, k, outs, freqs, H, H_k, positions, layout, norm, q_gain, k_gain, eps):
-    rows, width, q_pitch = _rows_pitch(q, "q")
-    if width % H != 0:
+    """tg_qk_params, and the addresses of the dense tensors `outs`: (name, tensor, input)."""
+    dt, dev = q.dtype, q.get_device()
+    rows, width, q_pitch = _rows_pitch(q, "q", dt, dev)
+    d_h = width // H
+    if d_h * H != width:
         raise ValueError("q's width must be H heads")
-    d_h, code = width // H, _dtype_code(q)
     k_pitch = 0
     if k is None:
         H_k = 0
     else:
         H_k = H if H_k is None else H_k
-        _check(k, "k", q.dtype, q)
-        k_rows, k_width, k_pitch = _rows_pitch(k, "k")
+        k_rows, k_width, k_pitch = _rows_pitch(k, "k", dt, dev)
         if k_rows != rows or k_width != H_k * d_h:
             raise ValueError("k must have q's rows and H_k heads of q's head width")
+    ptrs = []
     for name, t, src in outs:
         if (t is None) != (src is None):
             raise ValueError(f"{name} goes with its input")
-        if t is not None:
-            _check(t, name, q.dtype, q, True, src.shape)
-    rotary = 0
+        ptrs.append(None if t is None else _dense(t, name, dt, dev, src.shape))
+    rotary, fp = 0, None
     if freqs is not None:
-        _check(freqs, "freqs", torch.float64, q, True)
+        fp = _dense(freqs, "freqs", torch.float64, dev)
         rotary = 2 * freqs.numel()
-    T = q.shape[-2]
+    pp = None
     if positions is not None:
-        _check(positions, "positions", torch.int32, q, True)
+        pp = _dense(positions, "positions", torch.int32, dev)
         if positions.numel() != rows:
             raise ValueError("positions must hold one entry per row")
-    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if t is not None:
-            _check(t, name, torch.float32, q, True, (d_h,))
-    return tg_qk_params(rows, H, H_k, d_h, rotary, layout, norm, eps, max(T, 1), _ptr(positions), _ptr(freqs),
-                        _ptr(q_gain), _ptr(k_gain), q_pitch, k_pitch, code)
+    p = tg_qk_params(rows, H, H_k, d_h, rotary, layout, norm, eps, q.shape[-2] or 1, pp, fp,
+                     _optional(q_gain, "q_gain", torch.float32, dev, (d_h,)),
+                     _optional(k_gain, "k_gain", torch.float32, dev, (d_h,)), q_pitch, k_pitch, _dtype_code(q))
+    return p, ptrs, dev
 
 
 def tg_rope_freqs(rotary_dim, *, base=10000.0, factor=1.0, orig_len=0, turns_lo=1.0, turns_hi=32.0, device="cuda"):
@@ -543,9 +576,9 @@ def tango_qk_norm_rope(q, k, q_out, k_out, freqs, *, H, H_k=None, positions=None
     d_h] (k may be None) into q_out, k_out (dense).  q and k may be column slices.  freqs:
     float64 [rotary / 2] from tg_rope_freqs, or None (no rotation).  positions: int32, one
     per row, or None (the index along T).  q_gain, k_gain: float32 [d_h] or None."""
-    p = _qk_params(q, k, (("q_out", q_out, q), ("k_out", k_out, k)), freqs, H, H_k, positions, layout, norm, q_gain,
-                   k_gain, eps)
-    st = load().tango_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _stream(stream))
+    p, (qo, ko), dev = _qk_params(q, k, (("q_out", q_out, q), ("k_out", k_out, k)), freqs, H, H_k, positions, layout,
+                                  norm, q_gain, k_gain, eps)
+    st = load().tango_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), qo, ko, _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_qk_norm_rope")
     return q_out, k_out
@@ -556,17 +589,17 @@ def tango_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, freqs, *, H, H_k=N
                                 dk_gain=None, eps=1e-6, ws=None, stream=None):
     """Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) with respect to q and k (into
     dq, dk, dense) and, where dq_gain / dk_gain (float32 [d_h]) are given, to the gains."""
-    p = _qk_params(q, k, (("dq_out", dq_out, q), ("dq", dq, q), ("dk_out", dk_out, k), ("dk", dk, k)), freqs, H, H_k,
-                   positions, layout, norm, q_gain, k_gain, eps)
-    for name, t in (("dq_gain", dq_gain), ("dk_gain", dk_gain)):
-        if t is not None:
-            _check(t, name, torch.float32, q, True, (p.d_h,))
-    wbuf = None
-    if dq_gain is not None or dk_gain is not None:
+    p, (dqo, dko, dqp, dkp), dev = _qk_params(
+        q, k, (("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q), ("dk", dk, k)), freqs, H, H_k, positions,
+        layout, norm, q_gain, k_gain, eps)
+    dqg = _optional(dq_gain, "dq_gain", torch.float32, dev, (p.d_h,))
+    dkg = _optional(dk_gain, "dk_gain", torch.float32, dev, (p.d_h,))
+    wp, wn, wbuf = None, 0, None
+    if dqg is not None or dkg is not None:
         wbuf = _scratch(load().tg_workspace_size(TG_WS_QK_BWD, ctypes.byref(p)), q.device, ws, stream)
-    wp, wn = _ws_ptr(wbuf)
-    st = load().tango_qk_norm_rope_backward(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq),
-                                            _ptr(dk), _ptr(dq_gain), _ptr(dk_gain), wp, wn, _stream(stream))
+        wp, wn = _ws_ptr(wbuf)
+    st = load().tango_qk_norm_rope_backward(ctypes.byref(p), _ptr(q), _ptr(k), dqo, dko, dqp, dkp, dqg, dkg, wp, wn,
+                                            _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_qk_norm_rope_backward")
     return dq, dk
@@ -588,23 +621,23 @@ def paged_params(N, k_pages, g_pages, page_table, cu_new, lens, *, H, max_new, m
     """tg_paged_params of a batch: page_table int32 [B, pages], cu_new int32 [B + 1], lens
     int32 [B]."""
     n_pages, page_size, dqk = k_pages.shape
-    if dqk % H != 0 or tuple(g_pages.shape[:2]) != (n_pages, page_size) or g_pages.shape[2] % H != 0:
+    gp, gs, width = g_pages.shape
+    pitch = width // H
+    if dqk % H != 0 or gp != n_pages or gs != page_size or pitch * H != width:
         raise ValueError("k_pages and g_pages must be [n_pages, page_size, H * width]")
-    _check(k_pages, "k_pages", dense=True)
-    _check(g_pages, "g_pages", k_pages.dtype, k_pages, True)
+    dt, dev = k_pages.dtype, k_pages.get_device()
+    _dense(k_pages, "k_pages", dt, dev)
+    _dense(g_pages, "g_pages", dt, dev)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, pages]")
-    B = page_table.shape[0]
-    for name, t, shape in (("page_table", page_table, None), ("cu_new", cu_new, (B + 1,)), ("lens", lens, (B,))):
-        _check(t, name, torch.int32, k_pages, True, shape)
-    for name, t in (("tau", tau), ("null_bias", null_bias)):
-        if t is not None:
-            _check(t, name, torch.float32, k_pages, True, (H,))
-    pitch = g_pages.shape[2] // H
-    m_h = pitch if m_h is None else int(m_h)
-    return tg_paged_params(B, H, dqk // H, H * m_h, pitch, int(N), int(max_new), int(max_len), page_size, n_pages,
-                           page_table.shape[1], _ptr(cu_new), _ptr(lens), _ptr(page_table), float(s), _ptr(tau),
-                           _ptr(null_bias), int(v_pitch), _dtype_code(k_pages))
+    B, cols = page_table.shape
+    i32 = torch.int32
+    tp = _dense(page_table, "page_table", i32, dev)
+    cp = _dense(cu_new, "cu_new", i32, dev, (B + 1,))
+    lp = _dense(lens, "lens", i32, dev, (B,))
+    return tg_paged_params(B, H, dqk // H, H * (pitch if m_h is None else int(m_h)), pitch, N, max_new, max_len,
+                           page_size, n_pages, cols, cp, lp, tp, s, _optional(tau, "tau", torch.float32, dev, (H,)),
+                           _optional(null_bias, "null_bias", torch.float32, dev, (H,)), v_pitch, _dtype_code(k_pages))
 
 
 def tango_cache_append(q, k, g, q_out, k_pages, g_pages, page_table, cu_new, lens, freqs, *, H, m_h=None,
@@ -613,30 +646,28 @@ def tango_cache_append(q, k, g, q_out, k_pages, g_pages, page_table, cu_new, len
     and rotated at its position, g [N, H * pitch] (the gate projection; through SiLU unless
     silu=False).  q (or None) is normed and rotated into q_out for the aggregation.  lens
     [B] counts the new tokens in; cu_new [B + 1] are the sequences' row offsets."""
-    max_len = page_table.shape[-1] * k_pages.shape[1]
-    N, _, k_pitch = _rows_pitch(k, "k")
-    p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=max(1, N), max_len=max_len, m_h=m_h)
-    _check(k, "k", k_pages.dtype, k_pages)
-    _check(g, "g", k_pages.dtype, k_pages)
-    g_rows, g_width, g_pitch = _rows_pitch(g, "g")
-    if k.shape[-1] != k_pages.shape[2] or g_width != g_pages.shape[2] or g_rows != N:
+    dt, dev = k_pages.dtype, k_pages.get_device()
+    N, k_width, k_pitch = _rows_pitch(k, "k", dt, dev)
+    g_rows, g_width, g_pitch = _rows_pitch(g, "g", dt, dev)
+    p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=N or 1,
+                     max_len=page_table.shape[-1] * k_pages.shape[1], m_h=m_h)
+    if k_width != k_pages.shape[2] or g_width != g_pages.shape[2] or g_rows != N:
         raise ValueError("k and g must have one row per new token, as wide as the cache's")
-    q_pitch = 0
     if (q is None) != (q_out is None):
         raise ValueError("q_out goes with q")
+    q_pitch, qo = 0, None
     if q is not None:
-        _check(q, "q", k.dtype, k)
-        q_rows, q_width, q_pitch = _rows_pitch(q, "q")
-        if q_rows != N or q_width != k.shape[-1]:
+        q_rows, q_width, q_pitch = _rows_pitch(q, "q", dt, dev)
+        if q_rows != N or q_width != k_width:
             raise ValueError("q must have k's rows and width")
-        _check(q_out, "q_out", q.dtype, q, True, q.shape)
-    rotary = 0
+        qo = _dense(q_out, "q_out", dt, dev, q.shape)
+    rotary, fp = 0, None
     if freqs is not None:
-        _check(freqs, "freqs", torch.float64, k, True)
+        fp = _dense(freqs, "freqs", torch.float64, dev)
         rotary = 2 * freqs.numel()
-    a = tg_append_params(rotary, layout, norm, eps, _ptr(freqs), 1 if silu else 0, q_pitch, k_pitch, g_pitch)
-    st = load().tango_cache_append(ctypes.byref(p), ctypes.byref(a), _ptr(q), _ptr(k), _ptr(g), _ptr(q_out),
-                                   _ptr(k_pages), _ptr(g_pages), _stream(stream))
+    a = tg_append_params(rotary, layout, norm, eps, fp, 1 if silu else 0, q_pitch, k_pitch, g_pitch)
+    st = load().tango_cache_append(ctypes.byref(p), ctypes.byref(a), _ptr(q), k.data_ptr(), g.data_ptr(), qo,
+                                   k_pages.data_ptr(), g_pages.data_ptr(), _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_cache_append")
     return q_out
@@ -647,23 +678,24 @@ def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens,
     """TANGO aggregation of the new tokens (already appended) over the paged cache.  q [N,
     H * d_h] unit vectors per head; v [N, H * pitch] or None (out = gbar); out [N, H *
     pitch].  max_new, max_len: host bounds of the sequences' new tokens and lengths."""
-    N, q_width, q_pitch = _rows_pitch(q, "q")
+    dt, dev = k_pages.dtype, k_pages.get_device()
+    N, width = q.shape[0], g_pages.shape[2]
+    qp = _dense(q, "q", dt, dev)
+    op = _dense(out, "out", dt, dev)
+    if q.numel() != N * k_pages.shape[2] or out.numel() != N * width:
+        raise ValueError("q and out must have one row per new token, as wide as the cache's")
     v_pitch = 0
-    _check(q, "q", k_pages.dtype, k_pages, True)
-    _check(out, "out", k_pages.dtype, k_pages, True)
     if v is not None:
-        _check(v, "v", k_pages.dtype, k_pages)
-        v_rows, v_width, v_pitch = _rows_pitch(v, "v")
-        if v_rows != N or v_width != g_pages.shape[-1]:
+        v_rows, v_width, v_pitch = _rows_pitch(v, "v", dt, dev)
+        if v_rows != N or v_width != width:
             raise ValueError("v must have one row per new token, as wide as the cache's gates")
     p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=max_new, max_len=max_len, m_h=m_h,
                      s=s, tau=tau, null_bias=null_bias, v_pitch=v_pitch)
-    if q_width != k_pages.shape[2] or out.numel() != N * g_pages.shape[2]:
-        raise ValueError("q and out must have one row per new token, as wide as the cache's")
-    wbuf = _scratch(load().tg_workspace_size(TG_WS_PAGED, ctypes.byref(p)), q.device, ws, stream)
+    lib = load()
+    wbuf = _scratch(lib.tg_workspace_size(TG_WS_PAGED, ctypes.byref(p)), q.device, ws, stream)
     wp, wn = _ws_ptr(wbuf)
-    st = load().tango_paged_aggregate(ctypes.byref(p), _ptr(q), _ptr(v), _ptr(out), _ptr(k_pages), _ptr(g_pages), wp, wn,
-                                      _stream(stream))
+    st = lib.tango_paged_aggregate(ctypes.byref(p), qp, _ptr(v), op, k_pages.data_ptr(), g_pages.data_ptr(), wp, wn,
+                                   _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_paged_aggregate")
     return out

@@ -8,11 +8,10 @@
 // Rows are taken in tiles of R (1, 2, 4 or 8) new tokens of one sequence.
 //   paged_scores_kernel  one thread per cached key: its R dot products (q in shared memory),
 //       weights in f32 to scratch [tile][head][key][R], and the key span's weight sums.
-//   paged_gates_kernel   per (tile, head, 16-byte columns x 128 threads, span of keys): the
-//       weighted sum over the span's gate rows.  Bound by HBM for few rows: each gate is
-//       read once per tile with 16-byte loads, 8 keys of a thread in flight; a tile's
-//       blocks stand next to each other in the grid, so tiles of one chunk share the
-//       gates in L2.  The spans of one output are joined by the block that finishes last,
+//   paged_gates_kernel   per (tile, head, 512 or 1024 columns, span of keys): the weighted sum
+//       over the span's gate rows.  Bound by HBM for few rows: each gate is read once per
+//       tile, 8 keys of a thread in flight; tiles of one chunk stand next to each other in
+//       the grid and share the gates in L2.  The spans of one output are joined by the block that finishes last,
 //       in the spans' order (no order-dependent sums).
 // Weights past a row's own position are selected away, not multiplied by zero, so gates of
 // later tokens and of unused slots may be NaN.
@@ -136,11 +135,14 @@ template <> struct Cols<__nv_bfloat16> {
 
 constexpr int kSpanMax = 512;
 
-// grid (tiles, chunks * heads, gspans), 128 threads; a thread owns EV columns of R rows.
+// grid (tiles, chunks * heads, gspans), 128 threads; a thread owns EV columns of R rows: EV
+// neighbours (one 16-byte load) where the gates' rows are 16-byte aligned, else every 128th
+// (so that a warp's loads are neighbours).
 template <typename T, int R, bool kVec>
 __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
   constexpr int EV = Cols<T>::EV;
   __shared__ int tok[kSpanMax];
+  __shared__ __align__(16) float ws[kSpanMax * R];
   __shared__ float dinv[R];
   __shared__ int last;
   const int tile = blockIdx.x, hl = blockIdx.y / a.chunks, chunk = blockIdx.y - hl * a.chunks, head = a.h0 + hl;
@@ -156,51 +158,50 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
     const int key = k0 + i, pi = key / a.p.page_size, pg = paged_page(a.p, tr.b, pi);
     tok[i] = pg < 0 ? -1 : pg * a.p.page_size + (key - pi * a.p.page_size);
   }
+  const float* w = a.w + (th * a.key_pitch + k0) * R;
+  for (int i = t; i < nk * R; i += kVT) ws[i] = w[i];
   __syncthreads();
-  const int c0 = (chunk * kVT + t) * EV;  // first column of the head
+  const int c0 = chunk * kVT * EV + (kVec ? t * EV : t);  // first column of the head
+  constexpr int cs = kVec ? 1 : kVT;                      // and the step to the next
   const bool live = c0 < a.m_h;
   float acc[R][EV] = {};
   const size_t row_elems = (size_t)a.H * a.m_pitch;
   const T* gcol = a.g_pages + (size_t)head * a.m_pitch + c0;
-  const float* w = a.w + (th * a.key_pitch + k0) * R;
+  auto load = [&](int i, float (&g)[EV]) {
+    const int tk = tok[i];
+    if (kVec) {
+      Cols<T>::get(tk >= 0 ? ptx::ld_global_v4(gcol + (size_t)tk * row_elems) : make_uint4(0, 0, 0, 0), g);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EV; ++e) g[e] = tk >= 0 && c0 + e * cs < a.m_h ? io<T>::ld(gcol + (size_t)tk * row_elems + e * cs) : 0.f;
+    }
+  };
   // keys that every row of the tile sees, then the last ones, which some rows do not
   const int all = min(nk, max(0, tr.pos0 + 1 - k0));
   if (live) {
+    constexpr int U = kVec ? kUnroll : kUnroll / 2;
     int i = 0;
-    if (kVec) {
-      for (; i + kUnroll <= all; i += kUnroll) {
-        uint4 u[kUnroll];
+    for (; i + U <= all; i += U) {
+      float g[U][EV];
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const int tk = tok[i + j];
-          u[j] = tk >= 0 ? ptx::ld_global_v4(gcol + (size_t)tk * row_elems) : make_uint4(0, 0, 0, 0);
-        }
+      for (int j = 0; j < U; ++j) load(i + j, g[j]);
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          float g[EV];
-          Cols<T>::get(u[j], g);
+      for (int j = 0; j < U; ++j) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float wr = __ldg(w + (size_t)(i + j) * R + r);
+        for (int r = 0; r < R; ++r) {
+          const float wr = ws[(i + j) * R + r];
 #pragma unroll
-            for (int e = 0; e < EV; ++e) acc[r][e] = fmaf(wr, g[e], acc[r][e]);
-          }
+          for (int e = 0; e < EV; ++e) acc[r][e] = fmaf(wr, g[j][e], acc[r][e]);
         }
       }
     }
     for (; i < nk; ++i) {
-      const int tk = tok[i];
-      if (tk < 0) continue;
+      if (tok[i] < 0) continue;
       float g[EV];
-      if (kVec) {
-        Cols<T>::get(ptx::ld_global_v4(gcol + (size_t)tk * row_elems), g);
-      } else {
-#pragma unroll
-        for (int e = 0; e < EV; ++e) g[e] = c0 + e < a.m_h ? io<T>::ld(gcol + (size_t)tk * row_elems + e) : 0.f;
-      }
+      load(i, g);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float wr = __ldg(w + (size_t)i * R + r);
+        const float wr = ws[i * R + r];
         if (i < all || k0 + i <= tr.pos0 + r) {
 #pragma unroll
           for (int e = 0; e < EV; ++e) acc[r][e] = fmaf(wr, g[e], acc[r][e]);
@@ -209,15 +210,14 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
     }
   }
   if (nsp > 1) {
+    // this span's sums, then, in the block that finishes last, all spans' in order
     float* base = a.part + ((th * a.chunks + chunk) * a.gspans) * (size_t)(R * kVT * EV);
-    float* mine = base + (size_t)blockIdx.z * (R * kVT * EV) + t * EV;
+    float* mine = base + (size_t)blockIdx.z * (R * kVT * EV) + t;
     if (live) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < EV; e += 4)
-          *reinterpret_cast<float4*>(mine + (size_t)r * (kVT * EV) + e) =
-              make_float4(acc[r][e], acc[r][e + 1], acc[r][e + 2], acc[r][e + 3]);
+        for (int e = 0; e < EV; ++e) __stcg(mine + (r * EV + e) * kVT, acc[r][e]);
     }
     __threadfence();
     __syncthreads();
@@ -229,15 +229,14 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < EV; e += 4) {
-          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int z = 0; z < nsp; ++z) {
-            const float4 x =
-                __ldcg(reinterpret_cast<const float4*>(base + ((size_t)z * R + r) * (kVT * EV) + t * EV + e));
-            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-          }
-          acc[r][e] = s.x; acc[r][e + 1] = s.y; acc[r][e + 2] = s.z; acc[r][e + 3] = s.w;
-        }
+        for (int e = 0; e < EV; ++e) acc[r][e] = 0.f;
+      for (int z = 0; z < nsp; ++z) {
+        const float* src = base + (size_t)z * (R * kVT * EV) + t;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(src + (r * EV + e) * kVT);
+      }
     }
   }
   // denominators of the tile's rows: the spans' sums, and the null gate
@@ -259,12 +258,19 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
     const size_t row = tr.row0 + r, col = (size_t)head * a.m_pitch + c0;
 #pragma unroll
     for (int e = 0; e < EV; ++e) {
-      if (c0 + e >= a.m_h) break;
+      if (c0 + e * cs >= a.m_h) break;
       float y = tr.pos0 + r >= 0 ? acc[r][e] * dinv[r] : 0.f;
-      if (a.v && tr.pos0 + r >= 0) y *= io<T>::ld(a.v + row * a.v_pitch + col + e);
-      io<T>::st(a.out + row * row_elems + col + e, y);
+      if (a.v && tr.pos0 + r >= 0) y *= io<T>::ld(a.v + row * a.v_pitch + col + e * cs);
+      io<T>::st(a.out + row * row_elems + col + e * cs, y);
     }
   }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -282,7 +288,11 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
   l.spans = ceil_div(c.p.max_len, kKeysBlk);
   l.key_pitch = l.spans * kKeysBlk;
   l.chunks = ceil_div(c.m_h, kVT * EV);
+  // spans of 512 keys, shorter where they would leave SMs without work
   l.span_keys = kSpanMax;
+  while (l.span_keys > 64 &&
+         (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 16LL * sm_count())
+    l.span_keys /= 2;
   l.gspans = ceil_div(c.p.max_len, l.span_keys);
   // heads of a pass: as many as keep the scratch near 1 GB
   const size_t per_head = (size_t)l.tiles * ((size_t)l.key_pitch * l.R * 4 + (size_t)l.spans * l.R * 4 +
