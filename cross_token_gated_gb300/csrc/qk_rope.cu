@@ -29,11 +29,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 64;  // rotary_dim <= 128
-constexpr int kMaxRowsBlk = 8;
+constexpr int kMaxRowsBlk = 32;
+constexpr int kAngles = 512;   // (row, pair) angles of a step
 
 struct QkShared {
   uint64_t turns[kMaxPairs];
-  float2 cs[kMaxRowsBlk][kMaxPairs];
+  float2 cs[2][kAngles];  // [row][pair]: the step's angles, and the one before's
 };
 
 // Turns per position of frequency f (radians per position, >= 0), as a fraction of 2^64.
@@ -133,17 +134,13 @@ struct FwdRows {
   float eps;
 };
 
-// One head by its group of lanes: load, norm, gain, rotate, store (two vectors per lane).
+// One head by its group of lanes, from the two vectors each has loaded: norm, gain, rotate,
+// store.
 template <typename T>
-__device__ __forceinline__ void head_forward(const T* src, T* dst, bool live, const FwdRows& f, const LaneMap& m, int lh,
-                                             const float* gain, const float2* cs) {
+__device__ __forceinline__ void head_forward(const uint4& u0, const uint4& u1, T* dst, bool live, const FwdRows& f,
+                                             const LaneMap& m, int lh, const float* gain, const float2* cs) {
   constexpr int V = Vec<T>::E / 2;
   float a[V], b[V];
-  uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-  if (live) {
-    u0 = *reinterpret_cast<const uint4*>(src + m.off0);
-    u1 = *reinterpret_cast<const uint4*>(src + m.off1);
-  }
   Vec<T>::unpack(u0, a);
   Vec<T>::unpack(u1, b);
   float ss = 0.f;
@@ -225,122 +222,159 @@ __device__ __forceinline__ int row_pos(const int* positions, int T_len, long lon
 
 // The rows' angles: one thread per (row, pair).
 template <typename T>
-__device__ __forceinline__ void row_angles(QkShared& sh, const QkArgs<T>& a, long long row0, int nr) {
+__device__ __forceinline__ void row_angles(QkShared& sh, int buf, const QkArgs<T>& a, long long row0, int nr) {
   const int pairs = a.f.rotary / 2;
   for (int i = threadIdx.x; i < nr * pairs; i += kThreads) {
     const int r = i / pairs, c = i - r * pairs;
-    sh.cs[r][c] = turn_cos_sin(sh.turns[c], row_pos(a.positions, a.T_len, row0 + r));
+    sh.cs[buf][i] = turn_cos_sin(sh.turns[c], row_pos(a.positions, a.T_len, row0 + r));
   }
 }
 
+constexpr int kAheadRows = 2;  // rows of a thread that are loaded before the angles are formed
+
+// Where head number h of a step's rows lies: q's heads of a row, then k's.
+struct HeadRef {
+  int r, hh;
+  bool live, is_q;
+};
+__device__ __forceinline__ HeadRef head_ref(int h, int heads, int H, int HT) {
+  HeadRef x;
+  x.live = h < heads;
+  x.r = x.live ? h / HT : 0;
+  x.hh = x.live ? h - x.r * HT : 0;
+  x.is_q = x.hh < H;
+  return x;
+}
+
+// A thread's fixed place in a row: one head (q's, then k's) and its lane there, `cols` places
+// in all; rows are spread over the block's other threads (no division is left in the loop).
+// Rows of more places than threads are walked in rounds of kThreads.
+struct Place {
+  int cols, row_step, row, first;  // row >= row_step: no work
+  __device__ __forceinline__ Place(int cols_) : cols(cols_) {
+    row_step = cols < kThreads ? kThreads / cols : 1;
+    row = cols < kThreads ? (int)threadIdx.x / cols : 0;
+    first = cols < kThreads ? (int)threadIdx.x - row * cols : (int)threadIdx.x;
+  }
+};
+
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) qk_forward_kernel(const QkArgs<T> a) {
+__global__ void __launch_bounds__(kThreads, 4) qk_forward_kernel(const QkArgs<T> a) {
   __shared__ QkShared sh;
   __shared__ float buf[kVec ? 1 : kThreads / 32][kVec ? 1 : 128];
   load_turns(sh, a.freqs, a.f.rotary / 2);
-  const int HT = a.H + a.Hk, lh = kVec ? a.f.d_h / Vec<T>::E : 32;
-  const int l = threadIdx.x % lh;
-  const LaneMap m = lane_map<T>(l, a.f.rotary, a.f.layout);
-  for (long long row0 = (long long)blockIdx.x * a.rb; row0 < a.rows; row0 += (long long)gridDim.x * a.rb) {
+  const int HT = a.H + a.Hk, lh = kVec ? a.f.d_h / Vec<T>::E : 32, pairs = a.f.rotary / 2;
+  const LaneMap m = lane_map<T>(threadIdx.x % lh, a.f.rotary, a.f.layout);
+  const Place pl(HT * lh);
+  int side = 0;
+  for (long long row0 = (long long)blockIdx.x * a.rb; row0 < a.rows; row0 += (long long)gridDim.x * a.rb, side ^= 1) {
     const int nr = (int)min((long long)a.rb, a.rows - row0);
-    row_angles(sh, a, row0, nr);
-    __syncthreads();
-    const int heads = nr * HT;
-    // a whole group takes a head; groups without one keep step with the shuffles
-    for (int h0 = 0; h0 < heads; h0 += kThreads / lh) {
-      const int h = h0 + threadIdx.x / lh;
-      const bool live = h < heads;
-      const int r = live ? h / HT : 0, hh = live ? h - r * HT : 0;
-      const bool is_q = hh < a.H;
-      const long long row = row0 + r;
-      const T* src = is_q ? a.q + row * a.q_pitch + (long long)hh * a.f.d_h
-                          : a.k + row * a.k_pitch + (long long)(hh - a.H) * a.f.d_h;
-      T* dst = is_q ? a.q_out + (row * a.H + hh) * a.f.d_h : a.k_out + (row * a.Hk + hh - a.H) * a.f.d_h;
-      const float* gain = is_q ? a.q_gain : a.k_gain;
-      if (kVec) {
-        head_forward<T>(src, dst, live, a.f, m, lh, gain, sh.cs[r]);
-      } else if (live) {
-        head_forward_any<T>(src, dst, a.f, gain, sh.cs[r], buf[threadIdx.x / 32]);
+    if (kVec) {
+      for (int c0 = 0; c0 < pl.cols; c0 += kThreads) {  // (one round but for very wide rows)
+        const int hh = (c0 + pl.first) / lh;
+        const bool is_q = hh < a.H, mine = pl.row < pl.row_step && hh < HT;
+        const T* src = is_q ? a.q + hh * a.f.d_h : a.k + (hh - a.H) * a.f.d_h;
+        T* dst = is_q ? a.q_out + hh * a.f.d_h : a.k_out + (hh - a.H) * a.f.d_h;
+        const long long sp = is_q ? a.q_pitch : a.k_pitch, dp = (long long)(is_q ? a.H : a.Hk) * a.f.d_h;
+        // the first rows are on their way while the angles are formed
+        uint4 u[kAheadRows][2];
+        auto load = [&](int k, int r) {
+          const bool live = mine && r < nr;
+          const T* x = src + (row0 + r) * sp;
+          u[k][0] = live ? *reinterpret_cast<const uint4*>(x + m.off0) : make_uint4(0, 0, 0, 0);
+          u[k][1] = live ? *reinterpret_cast<const uint4*>(x + m.off1) : make_uint4(0, 0, 0, 0);
+        };
+#pragma unroll
+        for (int k = 0; k < kAheadRows; ++k) load(k, pl.row + k * pl.row_step);
+        if (c0 == 0) {
+          row_angles(sh, side, a, row0, nr);
+          __syncthreads();
+        }
+        for (int r0 = 0; r0 < nr; r0 += kAheadRows * pl.row_step) {
+#pragma unroll
+          for (int k = 0; k < kAheadRows; ++k) {
+            const int r = r0 + k * pl.row_step + pl.row;
+            if (r0 > 0) load(k, r);
+            const bool live = mine && r < nr;
+            head_forward<T>(u[k][0], u[k][1], dst + (row0 + r) * dp, live, a.f, m, lh, is_q ? a.q_gain : a.k_gain,
+                            sh.cs[side] + (live ? r : 0) * pairs);
+          }
+        }
+      }
+    } else {
+      row_angles(sh, side, a, row0, nr);
+      __syncthreads();
+      for (int h = threadIdx.x / 32; h < nr * HT; h += kThreads / 32) {
+        const HeadRef x = head_ref(h, nr * HT, a.H, HT);
+        const long long row = row0 + x.r;
+        const T* src = x.is_q ? a.q + row * a.q_pitch + (long long)x.hh * a.f.d_h
+                              : a.k + row * a.k_pitch + (long long)(x.hh - a.H) * a.f.d_h;
+        T* dst = x.is_q ? a.q_out + (row * a.H + x.hh) * a.f.d_h : a.k_out + (row * a.Hk + x.hh - a.H) * a.f.d_h;
+        head_forward_any<T>(src, dst, a.f, x.is_q ? a.q_gain : a.k_gain, sh.cs[side] + x.r * pairs,
+                            buf[kVec ? 0 : threadIdx.x / 32]);
       }
     }
-    __syncthreads();
+    // (no barrier here: the next step's angles go to the other buffer)
   }
 }
 
 // ------------------------------------------------------------------------ backward
 
-// One tensor's heads (q or k) of a block's rows; the lane's gain gradient goes to ga, gb.
+// One head's gradient by its group of lanes, from the vectors of x and dout that each has
+// loaded.  n * dz of the lane's columns is left in ga, gb (for the gain's gradient).
 template <typename T>
-__device__ __forceinline__ void rows_backward(const QkArgs<T>& a, QkShared& sh, long long row0, int nr, int H,
-                                              const T* x, long long pitch, const T* dout, T* dx, const float* gain,
-                                              const LaneMap& m, int lh, float* ga, float* gb) {
+__device__ __forceinline__ void head_backward(const uint4 (&u)[4], T* dst, bool live, const FwdRows& f, const LaneMap& m,
+                                              int lh, const float* gain, const float2* cs, float* ga, float* gb) {
   constexpr int V = Vec<T>::E / 2;
-  const int heads = nr * H;
-  for (int h0 = 0; h0 < heads; h0 += kThreads / lh) {
-    const int h = h0 + threadIdx.x / lh;
-    const bool live = h < heads;
-    const int r = live ? h / H : 0, hh = live ? h - r * H : 0;
-    const long long row = row0 + r, at = (row * H + hh) * a.f.d_h;
-    float xa[V], xb[V], da[V], db[V];
-    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0, w0 = u0, w1 = u0;
-    if (live) {
-      const T* src = x + row * pitch + (long long)hh * a.f.d_h;
-      u0 = *reinterpret_cast<const uint4*>(src + m.off0);
-      u1 = *reinterpret_cast<const uint4*>(src + m.off1);
-      w0 = *reinterpret_cast<const uint4*>(dout + at + m.off0);
-      w1 = *reinterpret_cast<const uint4*>(dout + at + m.off1);
-    }
-    Vec<T>::unpack(u0, xa);
-    Vec<T>::unpack(u1, xb);
-    Vec<T>::unpack(w0, da);
-    Vec<T>::unpack(w1, db);
-    rotate<V>(da, db, sh.cs[r], m, -1.f);  // dz
-    float ss = 0.f;
+  float xa[V], xb[V], da[V], db[V];
+  Vec<T>::unpack(u[0], xa);
+  Vec<T>::unpack(u[1], xb);
+  Vec<T>::unpack(u[2], da);
+  Vec<T>::unpack(u[3], db);
+  rotate<V>(da, db, cs, m, -1.f);  // dz
+  float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
-    float rn = 1.f;
-    bool floor_hit = false;
-    if (a.f.norm != TG_NORM_NONE) {
-      ss = group_sum(ss, lh);
-      rn = inv_norm(ss, a.f.d_h, a.f.norm, a.f.eps);
-      floor_hit = a.f.norm == TG_NORM_UNIT && sqrtf(ss) < 1e-12f;
+  for (int i = 0; i < V; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+  float rn = 1.f;
+  bool floor_hit = false;
+  if (f.norm != TG_NORM_NONE) {
+    ss = group_sum(ss, lh);
+    rn = inv_norm(ss, f.d_h, f.norm, f.eps);
+    floor_hit = f.norm == TG_NORM_UNIT && sqrtf(ss) < 1e-12f;
+  }
+  float dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    xa[i] *= rn;  // n
+    xb[i] *= rn;
+    if (gain) {
+      ga[i] = live ? da[i] * xa[i] : 0.f;
+      gb[i] = live ? db[i] * xb[i] : 0.f;
+      da[i] *= gain[m.off0 + i];  // dn
+      db[i] *= gain[m.off1 + i];
     }
-    float dot = 0.f;
+    dot += xa[i] * da[i] + xb[i] * db[i];
+  }
+  if (f.norm != TG_NORM_NONE) {
+    dot = group_sum(dot, lh);
+    if (f.norm == TG_NORM_RMS) dot /= (float)f.d_h;
+    if (floor_hit) dot = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      xa[i] *= rn;  // n
-      xb[i] *= rn;
-      if (gain) {
-        if (live && ga) {
-          ga[i] = fmaf(da[i], xa[i], ga[i]);
-          gb[i] = fmaf(db[i], xb[i], gb[i]);
-        }
-        da[i] *= gain[m.off0 + i];  // dn
-        db[i] *= gain[m.off1 + i];
-      }
-      dot += xa[i] * da[i] + xb[i] * db[i];
+      da[i] = rn * (da[i] - xa[i] * dot);
+      db[i] = rn * (db[i] - xb[i] * dot);
     }
-    if (a.f.norm != TG_NORM_NONE) {
-      dot = group_sum(dot, lh);
-      if (a.f.norm == TG_NORM_RMS) dot /= (float)a.f.d_h;
-      if (floor_hit) dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        da[i] = rn * (da[i] - xa[i] * dot);
-        db[i] = rn * (db[i] - xb[i] * dot);
-      }
-    }
-    if (live) {
-      *reinterpret_cast<uint4*>(dx + at + m.off0) = Vec<T>::pack(da);
-      *reinterpret_cast<uint4*>(dx + at + m.off1) = Vec<T>::pack(db);
-    }
+  }
+  if (live) {
+    *reinterpret_cast<uint4*>(dst + m.off0) = Vec<T>::pack(da);
+    *reinterpret_cast<uint4*>(dst + m.off1) = Vec<T>::pack(db);
   }
 }
 
 // The same by whole warps for any width and alignment; gain gradients go to acc[d_h],
 // one float per column of this warp.
 template <typename T>
-__device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& sh, long long row0, int nr, int H,
+__device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& sh, int side, long long row0, int nr, int H,
                                                   const T* x, long long pitch, const T* dout, T* dx,
                                                   const float* gain, float* buf, float* acc) {
   const int lane = threadIdx.x & 31, hp = a.f.rotary / 2;
@@ -372,7 +406,7 @@ __device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& 
         const bool first = a.f.layout == TG_ROPE_HALF ? c < hp : !(c & 1);
         const int pair = a.f.layout == TG_ROPE_HALF ? (first ? c : c - hp) : c >> 1;
         const int mate = a.f.layout == TG_ROPE_HALF ? (first ? c + hp : c - hp) : c ^ 1;
-        const float2 e = sh.cs[r][pair];
+        const float2 e = sh.cs[side][r * hp + pair];
         dz = first ? dz * e.x + buf[mate] * e.y : dz * e.x - buf[mate] * e.y;
       }
       n[i] = io<T>::ld(src + c) * rn;
@@ -396,59 +430,102 @@ __device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& 
   }
 }
 
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) qk_backward_kernel(const QkArgs<T> a) {
+template <typename T, bool kVec, bool kGain>
+__global__ void __launch_bounds__(kThreads, kVec ? 2 : 1) qk_backward_kernel(const QkArgs<T> a) {
   constexpr int V = Vec<T>::E / 2;
   __shared__ QkShared sh;
   __shared__ float buf[kVec ? 1 : kThreads / 32][kVec ? 1 : 128];
-  __shared__ float acc[2][kThreads / 32][128];  // gain gradients, one copy per warp
+  __shared__ float acc[2][kGain ? kThreads / 32 : 1][128];  // gain gradients, one copy per warp
   load_turns(sh, a.freqs, a.f.rotary / 2);
-  const int lh = kVec ? a.f.d_h / Vec<T>::E : 32, l = threadIdx.x % lh, w = threadIdx.x / 32;
-  const LaneMap m = lane_map<T>(l, a.f.rotary, a.f.layout);
-  if (a.want_gain) {
+  const int HT = a.H + a.Hk, lh = kVec ? a.f.d_h / Vec<T>::E : 32, w = threadIdx.x / 32, pairs = a.f.rotary / 2;
+  const LaneMap m = lane_map<T>(threadIdx.x % lh, a.f.rotary, a.f.layout);
+  const Place pl(HT * lh);
+  if (kGain) {
     for (int i = threadIdx.x; i < 2 * (kThreads / 32) * 128; i += kThreads) (&acc[0][0][0])[i] = 0.f;
     __syncthreads();
   }
-  float qa[V] = {}, qb[V] = {}, ka[V] = {}, kb[V] = {};
-  for (long long row0 = (long long)blockIdx.x * a.rb; row0 < a.rows; row0 += (long long)gridDim.x * a.rb) {
-    const int nr = (int)min((long long)a.rb, a.rows - row0);
-    row_angles(sh, a, row0, nr);
-    __syncthreads();
-    if (kVec) {
-      rows_backward<T>(a, sh, row0, nr, a.H, a.q, a.q_pitch, a.dq_out, a.dq, a.q_gain, m, lh, a.want_gain ? qa : nullptr, qb);
-      rows_backward<T>(a, sh, row0, nr, a.Hk, a.k, a.k_pitch, a.dk_out, a.dk, a.k_gain, m, lh, a.want_gain ? ka : nullptr, kb);
-    } else {
-      rows_backward_any<T>(a, sh, row0, nr, a.H, a.q, a.q_pitch, a.dq_out, a.dq, a.q_gain, buf[kVec ? 0 : w],
-                           a.want_gain ? acc[0][w] : nullptr);
-      rows_backward_any<T>(a, sh, row0, nr, a.Hk, a.k, a.k_pitch, a.dk_out, a.dk, a.k_gain, buf[kVec ? 0 : w],
-                           a.want_gain ? acc[1][w] : nullptr);
-    }
-    __syncthreads();
-  }
-  if (!a.want_gain) return;
-  if (kVec) {
-    // over the warp's heads (lanes l apart by lh), then each warp's copy
+  int side = 0;
+  // the places of a round are walked over all the block's rows, so that a thread's head, and
+  // with it the gain it sums for, stays the same
+  for (int c0 = 0; c0 < (kVec ? pl.cols : 1); c0 += kThreads) {
+    const int hh = (c0 + pl.first) / lh;
+    const bool is_q = hh < a.H, mine = pl.row < pl.row_step && hh < HT;
+    const T* src = is_q ? a.q + hh * a.f.d_h : a.k + (hh - a.H) * a.f.d_h;
+    const T* dy = is_q ? a.dq_out + hh * a.f.d_h : a.dk_out + (hh - a.H) * a.f.d_h;
+    T* dst = is_q ? a.dq + hh * a.f.d_h : a.dk + (hh - a.H) * a.f.d_h;
+    const float* gain = is_q ? a.q_gain : a.k_gain;
+    const long long sp = is_q ? a.q_pitch : a.k_pitch, dp = (long long)(is_q ? a.H : a.Hk) * a.f.d_h;
+    float sa[V] = {}, sb[V] = {};  // the gain's gradient, this lane's columns
+    for (long long row0 = (long long)blockIdx.x * a.rb; row0 < a.rows; row0 += (long long)gridDim.x * a.rb, side ^= 1) {
+      const int nr = (int)min((long long)a.rb, a.rows - row0);
+      if (kVec) {
+        uint4 u[kAheadRows][4];
+        auto load = [&](int k, int r) {
+          const bool live = mine && r < nr;
+          const T *x = src + (row0 + r) * sp, *y = dy + (row0 + r) * dp;
+          const uint4 z = make_uint4(0, 0, 0, 0);
+          u[k][0] = live ? *reinterpret_cast<const uint4*>(x + m.off0) : z;
+          u[k][1] = live ? *reinterpret_cast<const uint4*>(x + m.off1) : z;
+          u[k][2] = live ? *reinterpret_cast<const uint4*>(y + m.off0) : z;
+          u[k][3] = live ? *reinterpret_cast<const uint4*>(y + m.off1) : z;
+        };
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      for (int o = 16; o >= lh; o >>= 1) {
-        qa[i] += __shfl_xor_sync(0xffffffffu, qa[i], o);
-        qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], o);
-        ka[i] += __shfl_xor_sync(0xffffffffu, ka[i], o);
-        kb[i] += __shfl_xor_sync(0xffffffffu, kb[i], o);
+        for (int k = 0; k < kAheadRows; ++k) load(k, pl.row + k * pl.row_step);
+        row_angles(sh, side, a, row0, nr);
+        __syncthreads();
+        for (int r0 = 0; r0 < nr; r0 += kAheadRows * pl.row_step) {
+#pragma unroll
+          for (int k = 0; k < kAheadRows; ++k) {
+            const int r = r0 + k * pl.row_step + pl.row;
+            if (r0 > 0) load(k, r);
+            const bool live = mine && r < nr;
+            float ga[V], gb[V];
+            head_backward<T>(u[k], dst + (row0 + r) * dp, live, a.f, m, lh, gain, sh.cs[side] + (live ? r : 0) * pairs, ga, gb);
+            if (kGain && gain) {
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                sa[i] += ga[i];
+                sb[i] += gb[i];
+              }
+            }
+          }
+        }
+      } else {
+        row_angles(sh, side, a, row0, nr);
+        __syncthreads();
+        rows_backward_any<T>(a, sh, side, row0, nr, a.H, a.q, a.q_pitch, a.dq_out, a.dq, a.q_gain, buf[kVec ? 0 : w],
+                             kGain ? acc[0][kGain ? w : 0] : nullptr);
+        rows_backward_any<T>(a, sh, side, row0, nr, a.Hk, a.k, a.k_pitch, a.dk_out, a.dk, a.k_gain, buf[kVec ? 0 : w],
+                             kGain ? acc[1][kGain ? w : 0] : nullptr);
       }
-      if ((threadIdx.x & 31) < lh) {
-        acc[0][w][m.off0 + i] = qa[i];
-        acc[0][w][m.off1 + i] = qb[i];
-        acc[1][w][m.off0 + i] = ka[i];
-        acc[1][w][m.off1 + i] = kb[i];
+    }
+    if (kVec && kGain) {
+      // over the warp's lanes of the same columns, q's and k's heads apart
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float qa = mine && is_q ? sa[i] : 0.f, qb = mine && is_q ? sb[i] : 0.f;
+        float ka = mine && !is_q ? sa[i] : 0.f, kb = mine && !is_q ? sb[i] : 0.f;
+        for (int o = 16; o >= lh; o >>= 1) {
+          qa += __shfl_xor_sync(0xffffffffu, qa, o);
+          qb += __shfl_xor_sync(0xffffffffu, qb, o);
+          ka += __shfl_xor_sync(0xffffffffu, ka, o);
+          kb += __shfl_xor_sync(0xffffffffu, kb, o);
+        }
+        if ((threadIdx.x & 31) < lh) {
+          acc[0][kGain ? w : 0][m.off0 + i] += qa;
+          acc[0][kGain ? w : 0][m.off1 + i] += qb;
+          acc[1][kGain ? w : 0][m.off0 + i] += ka;
+          acc[1][kGain ? w : 0][m.off1 + i] += kb;
+        }
       }
     }
   }
+  if (!kGain) return;
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * a.f.d_h; i += kThreads) {
-    const int side = i / a.f.d_h, c = i - side * a.f.d_h;
+    const int side = i / a.f.d_h, c = i - side * a.f.d_h;  // q's gain, k's gain
     float s = 0.f;
-    for (int k = 0; k < kThreads / 32; ++k) s += acc[side][k][c];
+    for (int k = 0; k < (kGain ? kThreads / 32 : 0); ++k) s += acc[side][k][c];
     a.part[((size_t)blockIdx.x * 2 + side) * a.f.d_h + c] = s;
   }
 }
@@ -505,7 +582,7 @@ template <typename T> __device__ __forceinline__ float silu_of(float x);
 template <> __device__ __forceinline__ float silu_of<float>(float x) { return x / (1.f + expf(-x)); }
 template <> __device__ __forceinline__ float silu_of<__nv_bfloat16>(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
-constexpr int kGateVecs = 2;  // 16-byte vectors of a thread in a gate block
+constexpr int kGateVecs = 4;  // 16-byte vectors of a thread that are on their way at a time
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs<T> a) {
@@ -518,35 +595,40 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
     const int gb = blockIdx.x - a.qk_blocks, row = gb / a.chunks, chunk = gb - row * a.chunks;
     const T* src = a.g + (long long)row * a.g_pitch;
     if (kVec) {
-      // the loads are on their way before the slot is known
       constexpr int EV = 16 / sizeof(T);
-      const int nv = a.H * a.m_pitch / EV;
+      const int nv = a.H * a.m_pitch / EV, per = (nv + a.chunks - 1) / a.chunks;
+      const int end = min(nv, (chunk + 1) * per);
       uint4 u[kGateVecs];
-      const int v0 = chunk * (kThreads * kGateVecs) + threadIdx.x;
+      int v0 = chunk * per + threadIdx.x;
+      auto load = [&]() {
 #pragma unroll
-      for (int i = 0; i < kGateVecs; ++i)
-        if (v0 + i * kThreads < nv) u[i] = ptx::ld_global_v4(src + (long long)(v0 + i * kThreads) * EV);
+        for (int i = 0; i < kGateVecs; ++i)
+          if (v0 + i * kThreads < end) u[i] = ptx::ld_global_v4(src + (long long)(v0 + i * kThreads) * EV);
+      };
+      load();  // on its way before the slot is known
       const Slot s = find_slot(a.p, row);
       if (s.tok < 0) return;
       T* dst = a.g_pages + s.tok * ((long long)a.H * a.m_pitch);
+      for (; v0 < end; v0 += kGateVecs * kThreads, load()) {
 #pragma unroll
-      for (int i = 0; i < kGateVecs; ++i) {
-        if (v0 + i * kThreads >= nv) break;
-        if (a.silu) {
-          float x[EV];
-          Vec<T>::unpack(u[i], x);
+        for (int i = 0; i < kGateVecs; ++i) {
+          if (v0 + i * kThreads >= end) break;
+          if (a.silu) {
+            float x[EV];
+            Vec<T>::unpack(u[i], x);
 #pragma unroll
-          for (int e = 0; e < EV; ++e) x[e] = silu_of<T>(x[e]);
-          u[i] = Vec<T>::pack(x);
+            for (int e = 0; e < EV; ++e) x[e] = silu_of<T>(x[e]);
+            u[i] = Vec<T>::pack(x);
+          }
+          *reinterpret_cast<uint4*>(dst + (long long)(v0 + i * kThreads) * EV) = u[i];
         }
-        *reinterpret_cast<uint4*>(dst + (long long)(v0 + i * kThreads) * EV) = u[i];
       }
     } else {
       const Slot s = find_slot(a.p, row);
       if (s.tok < 0) return;
       T* dst = a.g_pages + s.tok * ((long long)a.H * a.m_pitch);
-      const int m = a.H * a.m_h, c0 = chunk * (kThreads * 8);
-      for (int i = c0 + threadIdx.x; i < min(m, c0 + kThreads * 8); i += kThreads) {
+      const int m = a.H * a.m_h, per = (m + a.chunks - 1) / a.chunks;
+      for (int i = chunk * per + threadIdx.x; i < min(m, (chunk + 1) * per); i += kThreads) {
         const int h = i / a.m_h, at = h * a.m_pitch + (i - h * a.m_h);
         const float x = io<T>::ld(src + at);
         io<T>::st(dst + at, a.silu ? silu_of<T>(x) : x);
@@ -559,8 +641,10 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
   const int HT = a.q ? 2 * a.H : a.H, lh = kVec ? a.f.d_h / Vec<T>::E : 32;
   const LaneMap m = lane_map<T>(threadIdx.x % lh, a.f.rotary, a.f.layout);
   const int pairs = a.f.rotary / 2;
-  for (int row0 = blockIdx.x * a.rb; row0 < a.p.N; row0 += a.qk_blocks * a.rb) {
+  int side = 0;
+  for (int row0 = blockIdx.x * a.rb; row0 < a.p.N; row0 += a.qk_blocks * a.rb, side ^= 1) {
     const int nr = min(a.rb, a.p.N - row0);
+    __syncthreads();  // the step before has read its slots
     for (int r = w; r < nr; r += kThreads / 32) {
       const Slot s = find_slot(a.p, row0 + r);
       if ((threadIdx.x & 31) == 0) slot[r] = s;
@@ -568,26 +652,27 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
     __syncthreads();
     for (int i = threadIdx.x; i < nr * pairs; i += kThreads) {
       const int r = i / pairs, c = i - r * pairs;
-      sh.cs[r][c] = turn_cos_sin(sh.turns[c], slot[r].pos);
+      sh.cs[side][i] = turn_cos_sin(sh.turns[c], slot[r].pos);
     }
     __syncthreads();
     const int heads = nr * HT;
     for (int h0 = 0; h0 < heads; h0 += kThreads / lh) {
-      const int h = h0 + threadIdx.x / lh;
-      const int r = h < heads ? h / HT : 0, hh = h < heads ? h - r * HT : 0;
-      const bool is_k = hh < a.H;  // keys first
-      const int hd = is_k ? hh : hh - a.H;
-      const long long row = row0 + r;
-      const bool live = h < heads && (is_k ? slot[r].tok >= 0 : true);
+      const HeadRef x = head_ref(h0 + threadIdx.x / lh, heads, a.H, HT);
+      const bool is_k = x.is_q;  // keys come first here
+      const int hd = is_k ? x.hh : x.hh - a.H;
+      const long long row = row0 + x.r;
+      const bool live = x.live && (!is_k || slot[x.r].tok >= 0);
       const T* src = is_k ? a.k + row * a.k_pitch + (long long)hd * a.f.d_h : a.q + row * a.q_pitch + (long long)hd * a.f.d_h;
-      T* dst = is_k ? a.k_pages + (max(slot[r].tok, 0ll) * a.H + hd) * a.f.d_h : a.q_out + (row * a.H + hd) * a.f.d_h;
+      T* dst = is_k ? a.k_pages + (max(slot[x.r].tok, 0ll) * a.H + hd) * a.f.d_h : a.q_out + (row * a.H + hd) * a.f.d_h;
       if (kVec) {
-        head_forward<T>(src, dst, live, a.f, m, lh, nullptr, sh.cs[r]);
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const uint4 u0 = live ? *reinterpret_cast<const uint4*>(src + m.off0) : z;
+        const uint4 u1 = live ? *reinterpret_cast<const uint4*>(src + m.off1) : z;
+        head_forward<T>(u0, u1, dst, live, a.f, m, lh, nullptr, sh.cs[side] + x.r * pairs);
       } else if (live) {
-        head_forward_any<T>(src, dst, a.f, nullptr, sh.cs[r], buf[kVec ? 0 : w]);
+        head_forward_any<T>(src, dst, a.f, nullptr, sh.cs[side] + x.r * pairs, buf[kVec ? 0 : w]);
       }
     }
-    __syncthreads();
   }
 }
 
@@ -616,11 +701,14 @@ bool vec_heads(int d_h, int rotary, int es, std::initializer_list<const void*> p
   return true;
 }
 
-// Rows of a block's step: 8, fewer while that leaves SMs idle.
-int rows_per_block(long long rows) {
+// Rows of a block's step: as many as its threads load ahead (`places` threads a row), fewer
+// while that leaves SMs idle.
+int rows_per_block(long long rows, int places, int pairs) {
   const int want = 2 * sm_count();
-  int rb = kMaxRowsBlk;
-  while (rb > 1 && rows / rb < want) rb /= 2;
+  int rb = kAheadRows * (places < kThreads ? kThreads / places : 1);
+  if (rb > kMaxRowsBlk) rb = kMaxRowsBlk;
+  if (pairs > 0 && rb > kAngles / pairs) rb = kAngles / pairs;
+  while (rb > 1 && rows / rb < want) rb = (rb + 1) / 2;
   return rb;
 }
 
@@ -637,7 +725,7 @@ QkArgs<T> qk_args(const QkCall& c) {
   a.dq = static_cast<T*>(c.dq); a.dk = static_cast<T*>(c.dk);
   a.part = c.part;
   a.want_gain = c.dq_gain || c.dk_gain;
-  a.rb = rows_per_block(c.rows);
+  a.rb = rows_per_block(c.rows, (c.H + c.Hk) * ((c.d_h * (int)sizeof(T) + 31) / 32), c.rotary / 2);
   return a;
 }
 
@@ -659,14 +747,20 @@ cudaError_t forward_t(const QkCall& c, cudaStream_t s) {
 
 constexpr int kBwdPerSm = 4;
 
+template <typename T, bool kVec>
+void backward_vt(const QkArgs<T>& a, int grid, cudaStream_t s) {
+  if (a.want_gain) qk_backward_kernel<T, kVec, true><<<grid, kThreads, 0, s>>>(a);
+  else qk_backward_kernel<T, kVec, false><<<grid, kThreads, 0, s>>>(a);
+}
+
 template <typename T>
 cudaError_t backward_t(const QkCall& c, cudaStream_t s) {
   const QkArgs<T> a = qk_args<T>(c);
   const int grid = qk_grid(c.rows, a.rb, kBwdPerSm);
   if (vec_heads(c.d_h, c.rotary, sizeof(T), {c.q, c.k, c.dq_out, c.dk_out, c.dq, c.dk}, {c.q_pitch, c.k_pitch}))
-    qk_backward_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
+    backward_vt<T, true>(a, grid, s);
   else
-    qk_backward_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
+    backward_vt<T, false>(a, grid, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.want_gain) return e;
   qk_gain_sum_kernel<<<dim3(ceil_div(c.d_h, 8), 2), 256, 0, s>>>(c.part, grid, c.d_h, c.dq_gain, c.dk_gain);
@@ -683,13 +777,16 @@ cudaError_t append_t(const AppendCall& c, cudaStream_t s) {
   a.q = static_cast<const T*>(c.q); a.k = static_cast<const T*>(c.k); a.g = static_cast<const T*>(c.g);
   a.q_out = static_cast<T*>(c.q_out);
   a.k_pages = static_cast<T*>(c.k_pages); a.g_pages = static_cast<T*>(c.g_pages);
-  a.rb = rows_per_block(c.p.N);
+  a.rb = rows_per_block(c.p.N, (c.q ? 2 : 1) * c.H * ((c.d_h * (int)sizeof(T) + 31) / 32), c.rotary / 2);
   a.qk_blocks = qk_grid(c.p.N, a.rb, 2);
   const bool vec = vec_heads(c.d_h, c.rotary, sizeof(T), {c.q, c.k, c.g, c.q_out, c.k_pages, c.g_pages},
                              {c.q_pitch, c.k_pitch, c.g_pitch, (long long)c.H * c.m_pitch});
+  // a block takes a whole row (its slot is looked up once), or, for few rows, as large a part
+  // of one as keeps the SMs busy
   constexpr int EV = 16 / sizeof(T);
-  a.chunks = vec ? ceil_div((long long)c.H * c.m_pitch / EV, kThreads * kGateVecs)
-                 : ceil_div((long long)c.H * c.m_h, kThreads * 8);
+  const int most = ceil_div((long long)c.H * (vec ? c.m_pitch / EV : c.m_h), kThreads);
+  const int want = ceil_div(8LL * sm_count(), c.p.N);
+  a.chunks = want < most ? want : most;
   const long long blocks = a.qk_blocks + (long long)c.p.N * a.chunks;
   if (blocks > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
   if (vec)
