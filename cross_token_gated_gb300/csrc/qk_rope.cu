@@ -34,8 +34,17 @@ constexpr int kAngles = 512;   // (row, pair) angles of a step
 
 struct QkShared {
   uint64_t turns[kMaxPairs];
-  float2 cs[2][kAngles];  // [row][pair]: the step's angles, and the one before's
+  // [row][pair]: the step's angles, and the one before's
+  __align__(16) float cos[2][kAngles];
+  __align__(16) float sin[2][kAngles];
 };
+// One row's angles.
+struct RowAngles {
+  const float *c, *s;
+};
+__device__ __forceinline__ RowAngles angles_of(const QkShared& sh, int side, int at) {
+  return RowAngles{sh.cos[side] + at, sh.sin[side] + at};
+}
 
 // Turns per position of frequency f (radians per position, >= 0), as a fraction of 2^64.
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
@@ -50,11 +59,13 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t turns, int pos) {
   return make_float2(c, s);
 }
 
-// A head's values as the threads of its group hold them: V pairs (x[i], y[i]).  Rotated
-// lanes hold pairs that turn together; the other lanes hold 2 V columns that pass.
+// A head's values as the threads of its group hold them: E values in two 16-byte vectors,
+// V = E / 2 pairs that turn together, X the pairs' first values and Y their second ones, two
+// per register pair (packed f32 arithmetic takes half the instructions, and these kernels
+// are nearly bound by them).
 template <typename T> struct Vec;
 template <> struct Vec<float> {
-  static constexpr int E = 8;  // values of a thread: two 16-byte vectors
+  static constexpr int E = 8;  // values of a thread
   static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
     f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
   }
@@ -77,44 +88,97 @@ template <> struct Vec<__nv_bfloat16> {
 // Where lane l of a head's group finds its two vectors, and whether it rotates.
 struct LaneMap {
   int off0, off1, pair0;
-  bool rot, half;
+  bool rot;
 };
 template <typename T>
 __device__ __forceinline__ LaneMap lane_map(int l, int rotary, int layout) {
   constexpr int E = Vec<T>::E, V = E / 2;
   LaneMap m;
   m.rot = l < rotary / E;
-  m.half = m.rot && layout == TG_ROPE_HALF;
-  m.off0 = m.half ? l * V : l * E;
-  m.off1 = m.half ? rotary / 2 + l * V : l * E + V;
+  const bool split = m.rot && layout == TG_ROPE_HALF;
+  m.off0 = split ? l * V : l * E;
+  m.off1 = split ? rotary / 2 + l * V : l * E + V;
   m.pair0 = l * V;
   return m;
 }
 
-// The pairs of a lane: half layout pairs a[i] with b[i]; interleaved layout pairs
-// neighbours of the 2 V columns a then b.  sign = -1 turns back.
-template <int V>
-__device__ __forceinline__ void rotate(float* a, float* b, const float2* cs, const LaneMap& m, float sign) {
-  if (!m.rot) return;
-  if (m.half) {
+template <typename T, bool kHalf>
+struct Pairs {
+  static constexpr int V = Vec<T>::E / 2, W = V / 2;
+  uint64_t X[W], Y[W];
+  // half layout: X is the first vector and Y the second; interleaved: neighbours of both
+  __device__ __forceinline__ void load(const uint4& u0, const uint4& u1) {
+    float f[2 * V];
+    Vec<T>::unpack(u0, f);
+    Vec<T>::unpack(u1, f + V);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 e = cs[m.pair0 + i];
-      const float x = a[i], y = b[i], s = sign * e.y;
-      a[i] = x * e.x - y * s;
-      b[i] = x * s + y * e.x;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float* v = i < V / 2 ? a + 2 * i : b + 2 * i - V;
-      const float2 e = cs[m.pair0 + i];
-      const float x = v[0], y = v[1], s = sign * e.y;
-      v[0] = x * e.x - y * s;
-      v[1] = x * s + y * e.x;
+    for (int i = 0; i < W; ++i) {
+      X[i] = kHalf ? ptx::f32x2_pack(f[2 * i], f[2 * i + 1]) : ptx::f32x2_pack(f[4 * i], f[4 * i + 2]);
+      Y[i] = kHalf ? ptx::f32x2_pack(f[V + 2 * i], f[V + 2 * i + 1]) : ptx::f32x2_pack(f[4 * i + 1], f[4 * i + 3]);
     }
   }
-}
+  __device__ __forceinline__ void store(uint4& u0, uint4& u1) const {
+    float f[2 * V];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (kHalf) {
+        ptx::f32x2_unpack(X[i], f[2 * i], f[2 * i + 1]);
+        ptx::f32x2_unpack(Y[i], f[V + 2 * i], f[V + 2 * i + 1]);
+      } else {
+        ptx::f32x2_unpack(X[i], f[4 * i], f[4 * i + 2]);
+        ptx::f32x2_unpack(Y[i], f[4 * i + 1], f[4 * i + 3]);
+      }
+    }
+    u0 = Vec<T>::pack(f);
+    u1 = Vec<T>::pack(f + V);
+  }
+  // column of the pair's first (second) value
+  static __device__ __forceinline__ int col_x(const LaneMap& m, int i) { return kHalf ? m.off0 + i : m.off0 + 2 * i; }
+  static __device__ __forceinline__ int col_y(const LaneMap& m, int i) { return kHalf ? m.off1 + i : m.off0 + 2 * i + 1; }
+  __device__ __forceinline__ void scale(float r) {
+    const uint64_t rr = ptx::f32x2_pack(r, r);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      X[i] = ptx::mul_f32x2(X[i], rr);
+      Y[i] = ptx::mul_f32x2(Y[i], rr);
+    }
+  }
+  __device__ __forceinline__ void times(const float* gain, const LaneMap& m) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      X[i] = ptx::mul_f32x2(X[i], ptx::f32x2_pack(gain[col_x(m, 2 * i)], gain[col_x(m, 2 * i + 1)]));
+      Y[i] = ptx::mul_f32x2(Y[i], ptx::f32x2_pack(gain[col_y(m, 2 * i)], gain[col_y(m, 2 * i + 1)]));
+    }
+  }
+  // turned by the row's angles, or back
+  __device__ __forceinline__ void turn(const RowAngles& e, const LaneMap& m, bool back) {
+    if (!m.rot) return;
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float4 c = *reinterpret_cast<const float4*>(e.c + m.pair0 + 2 * i);
+      const float4 s = *reinterpret_cast<const float4*>(e.s + m.pair0 + 2 * i);
+      const uint64_t C[2] = {ptx::f32x2_pack(c.x, c.y), ptx::f32x2_pack(c.z, c.w)};
+      const uint64_t S[2] = {ptx::f32x2_pack(s.x, s.y), ptx::f32x2_pack(s.z, s.w)};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint64_t x = X[i + k], y = Y[i + k], n = ptx::neg_f32x2(S[k]);
+        X[i + k] = ptx::fma_f32x2(y, back ? S[k] : n, ptx::mul_f32x2(x, C[k]));
+        Y[i + k] = ptx::fma_f32x2(x, back ? n : S[k], ptx::mul_f32x2(y, C[k]));
+      }
+    }
+  }
+  __device__ __forceinline__ float dot(const Pairs& o) const {
+    uint64_t s = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      s = ptx::fma_f32x2(X[i], o.X[i], s);
+      s = ptx::fma_f32x2(Y[i], o.Y[i], s);
+    }
+    float lo, hi;
+    ptx::f32x2_unpack(s, lo, hi);
+    return lo + hi;
+  }
+};
 
 // Sum over the lh lanes of a head's group (lh a power of two, lanes aligned to it).
 __device__ __forceinline__ float group_sum(float v, int lh) {
@@ -122,9 +186,10 @@ __device__ __forceinline__ float group_sum(float v, int lh) {
   return v;
 }
 
+// r of the norm from the sum of squares (rsqrtf: within 2 units of the last place).
 __device__ __forceinline__ float inv_norm(float ss, int d_h, int norm, float eps) {
-  if (norm == TG_NORM_UNIT) return 1.f / fmaxf(sqrtf(ss), 1e-12f);
-  if (norm == TG_NORM_RMS) return 1.f / sqrtf(ss / (float)d_h + eps);
+  if (norm == TG_NORM_UNIT) return rsqrtf(fmaxf(ss, 1e-24f));  // 1 / max(|x|, 1e-12)
+  if (norm == TG_NORM_RMS) return rsqrtf(__fdividef(ss, (float)d_h) + eps);
   return 1.f;
 }
 
@@ -136,30 +201,19 @@ struct FwdRows {
 
 // One head by its group of lanes, from the two vectors each has loaded: norm, gain, rotate,
 // store.
-template <typename T>
+template <typename T, bool kHalf>
 __device__ __forceinline__ void head_forward(const uint4& u0, const uint4& u1, T* dst, bool live, const FwdRows& f,
-                                             const LaneMap& m, int lh, const float* gain, const float2* cs) {
-  constexpr int V = Vec<T>::E / 2;
-  float a[V], b[V];
-  Vec<T>::unpack(u0, a);
-  Vec<T>::unpack(u1, b);
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) ss += a[i] * a[i] + b[i] * b[i];
-  const float r = f.norm == TG_NORM_NONE ? 1.f : inv_norm(group_sum(ss, lh), f.d_h, f.norm, f.eps);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    a[i] *= r;
-    b[i] *= r;
-    if (gain) {
-      a[i] *= gain[m.off0 + i];
-      b[i] *= gain[m.off1 + i];
-    }
-  }
-  rotate<V>(a, b, cs, m, 1.f);
+                                             const LaneMap& m, int lh, const float* gain, const RowAngles& e) {
+  Pairs<T, kHalf> z;
+  z.load(u0, u1);
+  if (f.norm != TG_NORM_NONE) z.scale(inv_norm(group_sum(z.dot(z), lh), f.d_h, f.norm, f.eps));
+  if (gain) z.times(gain, m);
+  z.turn(e, m, false);
+  uint4 w0, w1;
+  z.store(w0, w1);
   if (live) {
-    *reinterpret_cast<uint4*>(dst + m.off0) = Vec<T>::pack(a);
-    *reinterpret_cast<uint4*>(dst + m.off1) = Vec<T>::pack(b);
+    *reinterpret_cast<uint4*>(dst + m.off0) = w0;
+    *reinterpret_cast<uint4*>(dst + m.off1) = w1;
   }
 }
 
@@ -167,7 +221,7 @@ __device__ __forceinline__ void head_forward(const uint4& u0, const uint4& u1, T
 // (2 x 128 floats per warp).
 template <typename T>
 __device__ __forceinline__ void head_forward_any(const T* src, T* dst, const FwdRows& f, const float* gain,
-                                                 const float2* cs, float* buf) {
+                                                 const RowAngles& e, float* buf) {
   const int lane = threadIdx.x & 31;
   float ss = 0.f;
   for (int c = lane; c < f.d_h; c += 32) {
@@ -185,8 +239,7 @@ __device__ __forceinline__ void head_forward_any(const T* src, T* dst, const Fwd
       const int pair = f.layout == TG_ROPE_HALF ? (first ? c : c - hp) : c >> 1;
       const int mate = f.layout == TG_ROPE_HALF ? (first ? c + hp : c - hp) : c ^ 1;
       const float w = buf[mate] * r * (gain ? gain[mate] : 1.f);
-      const float2 e = cs[pair];
-      z = first ? z * e.x - w * e.y : z * e.x + w * e.y;
+      z = first ? z * e.c[pair] - w * e.s[pair] : z * e.c[pair] + w * e.s[pair];
     }
     io<T>::st(dst + c, z);
   }
@@ -226,7 +279,9 @@ __device__ __forceinline__ void row_angles(QkShared& sh, int buf, const QkArgs<T
   const int pairs = a.f.rotary / 2;
   for (int i = threadIdx.x; i < nr * pairs; i += kThreads) {
     const int r = i / pairs, c = i - r * pairs;
-    sh.cs[buf][i] = turn_cos_sin(sh.turns[c], row_pos(a.positions, a.T_len, row0 + r));
+    const float2 e = turn_cos_sin(sh.turns[c], row_pos(a.positions, a.T_len, row0 + r));
+    sh.cos[buf][i] = e.x;
+    sh.sin[buf][i] = e.y;
   }
 }
 
@@ -258,7 +313,7 @@ struct Place {
   }
 };
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 4) qk_forward_kernel(const QkArgs<T> a) {
   __shared__ QkShared sh;
   __shared__ float buf[kVec ? 1 : kThreads / 32][kVec ? 1 : 128];
@@ -296,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 4) qk_forward_kernel(const QkArgs<T>
             const int r = r0 + k * pl.row_step + pl.row;
             if (r0 > 0) load(k, r);
             const bool live = mine && r < nr;
-            head_forward<T>(u[k][0], u[k][1], dst + (row0 + r) * dp, live, a.f, m, lh, is_q ? a.q_gain : a.k_gain,
-                            sh.cs[side] + (live ? r : 0) * pairs);
+            head_forward<T, kHalf>(u[k][0], u[k][1], dst + (row0 + r) * dp, live, a.f, m, lh, is_q ? a.q_gain : a.k_gain,
+                            angles_of(sh, side, (live ? r : 0) * pairs));
           }
         }
       }
@@ -310,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_forward_kernel(const QkArgs<T>
         const T* src = x.is_q ? a.q + row * a.q_pitch + (long long)x.hh * a.f.d_h
                               : a.k + row * a.k_pitch + (long long)(x.hh - a.H) * a.f.d_h;
         T* dst = x.is_q ? a.q_out + (row * a.H + x.hh) * a.f.d_h : a.k_out + (row * a.Hk + x.hh - a.H) * a.f.d_h;
-        head_forward_any<T>(src, dst, a.f, x.is_q ? a.q_gain : a.k_gain, sh.cs[side] + x.r * pairs,
+        head_forward_any<T>(src, dst, a.f, x.is_q ? a.q_gain : a.k_gain, angles_of(sh, side, x.r * pairs),
                             buf[kVec ? 0 : threadIdx.x / 32]);
       }
     }
@@ -321,53 +376,48 @@ __global__ void __launch_bounds__(kThreads, 4) qk_forward_kernel(const QkArgs<T>
 // ------------------------------------------------------------------------ backward
 
 // One head's gradient by its group of lanes, from the vectors of x and dout that each has
-// loaded.  n * dz of the lane's columns is left in ga, gb (for the gain's gradient).
-template <typename T>
+// loaded.  n * dz is added to the lane's sums for the gain's gradient.
+template <typename T, bool kHalf, bool kGain>
 __device__ __forceinline__ void head_backward(const uint4 (&u)[4], T* dst, bool live, const FwdRows& f, const LaneMap& m,
-                                              int lh, const float* gain, const float2* cs, float* ga, float* gb) {
-  constexpr int V = Vec<T>::E / 2;
-  float xa[V], xb[V], da[V], db[V];
-  Vec<T>::unpack(u[0], xa);
-  Vec<T>::unpack(u[1], xb);
-  Vec<T>::unpack(u[2], da);
-  Vec<T>::unpack(u[3], db);
-  rotate<V>(da, db, cs, m, -1.f);  // dz
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+                                              int lh, const float* gain, const RowAngles& e, Pairs<T, kHalf>& sum) {
+  Pairs<T, kHalf> n, d;
+  n.load(u[0], u[1]);
+  d.load(u[2], u[3]);
+  d.turn(e, m, true);  // dz
   float rn = 1.f;
   bool floor_hit = false;
   if (f.norm != TG_NORM_NONE) {
-    ss = group_sum(ss, lh);
+    const float ss = group_sum(n.dot(n), lh);
     rn = inv_norm(ss, f.d_h, f.norm, f.eps);
-    floor_hit = f.norm == TG_NORM_UNIT && sqrtf(ss) < 1e-12f;
+    floor_hit = f.norm == TG_NORM_UNIT && ss < 1e-24f;
+    n.scale(rn);
   }
-  float dot = 0.f;
+  if (gain) {
+    if (kGain) {  // (lanes without a row hold zeros)
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    xa[i] *= rn;  // n
-    xb[i] *= rn;
-    if (gain) {
-      ga[i] = live ? da[i] * xa[i] : 0.f;
-      gb[i] = live ? db[i] * xb[i] : 0.f;
-      da[i] *= gain[m.off0 + i];  // dn
-      db[i] *= gain[m.off1 + i];
+      for (int i = 0; i < Pairs<T, kHalf>::W; ++i) {
+        sum.X[i] = ptx::fma_f32x2(d.X[i], n.X[i], sum.X[i]);
+        sum.Y[i] = ptx::fma_f32x2(d.Y[i], n.Y[i], sum.Y[i]);
+      }
     }
-    dot += xa[i] * da[i] + xb[i] * db[i];
+    d.times(gain, m);  // dn
   }
   if (f.norm != TG_NORM_NONE) {
-    dot = group_sum(dot, lh);
-    if (f.norm == TG_NORM_RMS) dot /= (float)f.d_h;
-    if (floor_hit) dot = 0.f;
+    float along = group_sum(n.dot(d), lh);
+    if (f.norm == TG_NORM_RMS) along = __fdividef(along, (float)f.d_h);
+    if (floor_hit) along = 0.f;
+    const uint64_t rr = ptx::f32x2_pack(rn, rn), aa = ptx::f32x2_pack(-along * rn, -along * rn);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      da[i] = rn * (da[i] - xa[i] * dot);
-      db[i] = rn * (db[i] - xb[i] * dot);
+    for (int i = 0; i < Pairs<T, kHalf>::W; ++i) {
+      d.X[i] = ptx::fma_f32x2(n.X[i], aa, ptx::mul_f32x2(d.X[i], rr));
+      d.Y[i] = ptx::fma_f32x2(n.Y[i], aa, ptx::mul_f32x2(d.Y[i], rr));
     }
   }
+  uint4 w0, w1;
+  d.store(w0, w1);
   if (live) {
-    *reinterpret_cast<uint4*>(dst + m.off0) = Vec<T>::pack(da);
-    *reinterpret_cast<uint4*>(dst + m.off1) = Vec<T>::pack(db);
+    *reinterpret_cast<uint4*>(dst + m.off0) = w0;
+    *reinterpret_cast<uint4*>(dst + m.off1) = w1;
   }
 }
 
@@ -393,7 +443,7 @@ __device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& 
     if (a.f.norm != TG_NORM_NONE) {
       ss = group_sum(ss, 32);
       rn = inv_norm(ss, a.f.d_h, a.f.norm, a.f.eps);
-      floor_hit = a.f.norm == TG_NORM_UNIT && sqrtf(ss) < 1e-12f;
+      floor_hit = a.f.norm == TG_NORM_UNIT && ss < 1e-24f;
     }
     __syncwarp();
     float n[4], dn[4], dot = 0.f;
@@ -406,8 +456,8 @@ __device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& 
         const bool first = a.f.layout == TG_ROPE_HALF ? c < hp : !(c & 1);
         const int pair = a.f.layout == TG_ROPE_HALF ? (first ? c : c - hp) : c >> 1;
         const int mate = a.f.layout == TG_ROPE_HALF ? (first ? c + hp : c - hp) : c ^ 1;
-        const float2 e = sh.cs[side][r * hp + pair];
-        dz = first ? dz * e.x + buf[mate] * e.y : dz * e.x - buf[mate] * e.y;
+        const float c0 = sh.cos[side][r * hp + pair], s0 = sh.sin[side][r * hp + pair];
+        dz = first ? dz * c0 + buf[mate] * s0 : dz * c0 - buf[mate] * s0;
       }
       n[i] = io<T>::ld(src + c) * rn;
       if (gain && acc) acc[c] = fmaf(dz, n[i], acc[c]);
@@ -430,12 +480,13 @@ __device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& 
   }
 }
 
-template <typename T, bool kVec, bool kGain>
+template <typename T, bool kVec, bool kHalf, bool kGain>
 __global__ void __launch_bounds__(kThreads, kVec ? 2 : 1) qk_backward_kernel(const QkArgs<T> a) {
   constexpr int V = Vec<T>::E / 2;
   __shared__ QkShared sh;
   __shared__ float buf[kVec ? 1 : kThreads / 32][kVec ? 1 : 128];
-  __shared__ float acc[2][kGain ? kThreads / 32 : 1][128];  // gain gradients, one copy per warp
+  __shared__ float acc[2][kThreads / 32][kGain ? 128 : 1];  // gain gradients, one copy per warp
+  if (kGain) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   load_turns(sh, a.freqs, a.f.rotary / 2);
   const int HT = a.H + a.Hk, lh = kVec ? a.f.d_h / Vec<T>::E : 32, w = threadIdx.x / 32, pairs = a.f.rotary / 2;
   const LaneMap m = lane_map<T>(threadIdx.x % lh, a.f.rotary, a.f.layout);
@@ -455,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, kVec ? 2 : 1) qk_backward_kernel(con
     T* dst = is_q ? a.dq + hh * a.f.d_h : a.dk + (hh - a.H) * a.f.d_h;
     const float* gain = is_q ? a.q_gain : a.k_gain;
     const long long sp = is_q ? a.q_pitch : a.k_pitch, dp = (long long)(is_q ? a.H : a.Hk) * a.f.d_h;
-    float sa[V] = {}, sb[V] = {};  // the gain's gradient, this lane's columns
+    Pairs<T, kHalf> sum = {};  // the gain's gradient, this lane's columns
     for (long long row0 = (long long)blockIdx.x * a.rb; row0 < a.rows; row0 += (long long)gridDim.x * a.rb, side ^= 1) {
       const int nr = (int)min((long long)a.rb, a.rows - row0);
       if (kVec) {
@@ -479,43 +530,43 @@ __global__ void __launch_bounds__(kThreads, kVec ? 2 : 1) qk_backward_kernel(con
             const int r = r0 + k * pl.row_step + pl.row;
             if (r0 > 0) load(k, r);
             const bool live = mine && r < nr;
-            float ga[V], gb[V];
-            head_backward<T>(u[k], dst + (row0 + r) * dp, live, a.f, m, lh, gain, sh.cs[side] + (live ? r : 0) * pairs, ga, gb);
-            if (kGain && gain) {
-#pragma unroll
-              for (int i = 0; i < V; ++i) {
-                sa[i] += ga[i];
-                sb[i] += gb[i];
-              }
-            }
+            head_backward<T, kHalf, kGain>(u[k], dst + (row0 + r) * dp, live, a.f, m, lh, gain,
+                                           angles_of(sh, side, (live ? r : 0) * pairs), sum);
           }
         }
       } else {
         row_angles(sh, side, a, row0, nr);
         __syncthreads();
         rows_backward_any<T>(a, sh, side, row0, nr, a.H, a.q, a.q_pitch, a.dq_out, a.dq, a.q_gain, buf[kVec ? 0 : w],
-                             kGain ? acc[0][kGain ? w : 0] : nullptr);
+                             kGain ? acc[0][w] : nullptr);
         rows_backward_any<T>(a, sh, side, row0, nr, a.Hk, a.k, a.k_pitch, a.dk_out, a.dk, a.k_gain, buf[kVec ? 0 : w],
-                             kGain ? acc[1][kGain ? w : 0] : nullptr);
+                             kGain ? acc[1][w] : nullptr);
       }
     }
     if (kVec && kGain) {
       // over the warp's lanes of the same columns, q's and k's heads apart
+      float sx[V], sy[V];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        ptx::f32x2_unpack(sum.X[i], sx[2 * i], sx[2 * i + 1]);
+        ptx::f32x2_unpack(sum.Y[i], sy[2 * i], sy[2 * i + 1]);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float qa = mine && is_q ? sa[i] : 0.f, qb = mine && is_q ? sb[i] : 0.f;
-        float ka = mine && !is_q ? sa[i] : 0.f, kb = mine && !is_q ? sb[i] : 0.f;
+        float qx = mine && is_q ? sx[i] : 0.f, qy = mine && is_q ? sy[i] : 0.f;
+        float kx = mine && !is_q ? sx[i] : 0.f, ky = mine && !is_q ? sy[i] : 0.f;
         for (int o = 16; o >= lh; o >>= 1) {
-          qa += __shfl_xor_sync(0xffffffffu, qa, o);
-          qb += __shfl_xor_sync(0xffffffffu, qb, o);
-          ka += __shfl_xor_sync(0xffffffffu, ka, o);
-          kb += __shfl_xor_sync(0xffffffffu, kb, o);
+          qx += __shfl_xor_sync(0xffffffffu, qx, o);
+          qy += __shfl_xor_sync(0xffffffffu, qy, o);
+          kx += __shfl_xor_sync(0xffffffffu, kx, o);
+          ky += __shfl_xor_sync(0xffffffffu, ky, o);
         }
         if ((threadIdx.x & 31) < lh) {
-          acc[0][kGain ? w : 0][m.off0 + i] += qa;
-          acc[0][kGain ? w : 0][m.off1 + i] += qb;
-          acc[1][kGain ? w : 0][m.off0 + i] += ka;
-          acc[1][kGain ? w : 0][m.off1 + i] += kb;
+          const int cx = Pairs<T, kHalf>::col_x(m, i), cy = Pairs<T, kHalf>::col_y(m, i);
+          acc[0][w][kGain ? cx : 0] += qx;
+          acc[0][w][kGain ? cy : 0] += qy;
+          acc[1][w][kGain ? cx : 0] += kx;
+          acc[1][w][kGain ? cy : 0] += ky;
         }
       }
     }
@@ -525,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, kVec ? 2 : 1) qk_backward_kernel(con
   for (int i = threadIdx.x; i < 2 * a.f.d_h; i += kThreads) {
     const int side = i / a.f.d_h, c = i - side * a.f.d_h;  // q's gain, k's gain
     float s = 0.f;
-    for (int k = 0; k < (kGain ? kThreads / 32 : 0); ++k) s += acc[side][k][c];
+    for (int k = 0; k < kThreads / 32; ++k) s += acc[side][k][kGain ? c : 0];
     a.part[((size_t)blockIdx.x * 2 + side) * a.f.d_h + c] = s;
   }
 }
@@ -535,9 +586,10 @@ __global__ void __launch_bounds__(kThreads, kVec ? 2 : 1) qk_backward_kernel(con
 __global__ void __launch_bounds__(256) qk_gain_sum_kernel(const float* part, int blocks, int d_h, float* dqg, float* dkg) {
   const int c = blockIdx.x * 8 + threadIdx.x / 32, side = blockIdx.y, lane = threadIdx.x & 31;
   float* dst = side ? dkg : dqg;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c >= d_h || !dst) return;
   float s = 0.f;
-  for (int b = lane; b < blocks; b += 32) s += part[((size_t)b * 2 + side) * d_h + c];
+  for (int b = lane; b < blocks; b += 32) s += __ldcg(part + ((size_t)b * 2 + side) * d_h + c);
   s = group_sum(s, 32);
   if (lane == 0) dst[c] = s;
 }
@@ -584,7 +636,7 @@ template <> __device__ __forceinline__ float silu_of<__nv_bfloat16>(float x) { r
 
 constexpr int kGateVecs = 4;  // 16-byte vectors of a thread that are on their way at a time
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kHalf>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs<T> a) {
   __shared__ QkShared sh;
   __shared__ Slot slot[kMaxRowsBlk];
@@ -652,7 +704,9 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
     __syncthreads();
     for (int i = threadIdx.x; i < nr * pairs; i += kThreads) {
       const int r = i / pairs, c = i - r * pairs;
-      sh.cs[side][i] = turn_cos_sin(sh.turns[c], slot[r].pos);
+      const float2 e = turn_cos_sin(sh.turns[c], slot[r].pos);
+      sh.cos[side][i] = e.x;
+      sh.sin[side][i] = e.y;
     }
     __syncthreads();
     const int heads = nr * HT;
@@ -668,9 +722,9 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
         const uint4 z = make_uint4(0, 0, 0, 0);
         const uint4 u0 = live ? *reinterpret_cast<const uint4*>(src + m.off0) : z;
         const uint4 u1 = live ? *reinterpret_cast<const uint4*>(src + m.off1) : z;
-        head_forward<T>(u0, u1, dst, live, a.f, m, lh, nullptr, sh.cs[side] + x.r * pairs);
+        head_forward<T, kHalf>(u0, u1, dst, live, a.f, m, lh, nullptr, angles_of(sh, side, x.r * pairs));
       } else if (live) {
-        head_forward_any<T>(src, dst, a.f, nullptr, sh.cs[side] + x.r * pairs, buf[kVec ? 0 : w]);
+        head_forward_any<T>(src, dst, a.f, nullptr, angles_of(sh, side, x.r * pairs), buf[kVec ? 0 : w]);
       }
     }
   }
@@ -737,20 +791,21 @@ int qk_grid(long long rows, int rb, int per_sm) {
 template <typename T>
 cudaError_t forward_t(const QkCall& c, cudaStream_t s) {
   const QkArgs<T> a = qk_args<T>(c);
-  const int grid = qk_grid(c.rows, a.rb, 8);
+  const int grid = qk_grid(c.rows, a.rb, 4);
   if (vec_heads(c.d_h, c.rotary, sizeof(T), {c.q, c.k, c.q_out, c.k_out}, {c.q_pitch, c.k_pitch}))
-    qk_forward_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
+    c.layout == TG_ROPE_HALF ? qk_forward_kernel<T, true, true><<<grid, kThreads, 0, s>>>(a)
+                             : qk_forward_kernel<T, true, false><<<grid, kThreads, 0, s>>>(a);
   else
-    qk_forward_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
+    qk_forward_kernel<T, false, true><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-constexpr int kBwdPerSm = 4;
+constexpr int kBwdPerSm = 2;  // the blocks that fit: the grid is persistent
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kHalf>
 void backward_vt(const QkArgs<T>& a, int grid, cudaStream_t s) {
-  if (a.want_gain) qk_backward_kernel<T, kVec, true><<<grid, kThreads, 0, s>>>(a);
-  else qk_backward_kernel<T, kVec, false><<<grid, kThreads, 0, s>>>(a);
+  if (a.want_gain) qk_backward_kernel<T, kVec, kHalf, true><<<grid, kThreads, 0, s>>>(a);
+  else qk_backward_kernel<T, kVec, kHalf, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <typename T>
@@ -758,13 +813,22 @@ cudaError_t backward_t(const QkCall& c, cudaStream_t s) {
   const QkArgs<T> a = qk_args<T>(c);
   const int grid = qk_grid(c.rows, a.rb, kBwdPerSm);
   if (vec_heads(c.d_h, c.rotary, sizeof(T), {c.q, c.k, c.dq_out, c.dk_out, c.dq, c.dk}, {c.q_pitch, c.k_pitch}))
-    backward_vt<T, true>(a, grid, s);
+    c.layout == TG_ROPE_HALF ? backward_vt<T, true, true>(a, grid, s) : backward_vt<T, true, false>(a, grid, s);
   else
-    backward_vt<T, false>(a, grid, s);
+    backward_vt<T, false, true>(a, grid, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.want_gain) return e;
-  qk_gain_sum_kernel<<<dim3(ceil_div(c.d_h, 8), 2), 256, 0, s>>>(c.part, grid, c.d_h, c.dq_gain, c.dk_gain);
-  return cudaGetLastError();
+  // launched while the last blocks still run; it waits for their sums itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(c.d_h, 8), 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_gain_sum_kernel, (const float*)c.part, grid, c.d_h, c.dq_gain, c.dk_gain);
 }
 
 template <typename T>
@@ -790,9 +854,10 @@ cudaError_t append_t(const AppendCall& c, cudaStream_t s) {
   const long long blocks = a.qk_blocks + (long long)c.p.N * a.chunks;
   if (blocks > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
   if (vec)
-    cache_append_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    c.layout == TG_ROPE_HALF ? cache_append_kernel<T, true, true><<<(unsigned)blocks, kThreads, 0, s>>>(a)
+                             : cache_append_kernel<T, true, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
   else
-    cache_append_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    cache_append_kernel<T, false, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
