@@ -89,6 +89,7 @@ struct TcArgs {
   int nc_cap;                // key ranges of a tile, at most
   int n_slots;
   int box_rows;              // rows of a G box
+  int pair;                  // two CTAs per 256 rows
   float s;
   const float* tau;
   const float* null_bias;
@@ -142,9 +143,12 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
   clear_counters(a, tile, hl, span);
   const TileRef tr = find_tile<kM>(a.p, tile, hl == 0 && span == 0);
   const int vis = tr.pos0 + tr.n;
-  const int key0 = span * a.span_keys, key1 = min(key0 + a.span_keys, (vis + 63) & ~63);
-  if (tr.n == 0 || vis <= 0 || key0 >= vis) return;
   const PagedSeq sq = paged_seq(a.p, tr.b, false);
+  // the first tile of a pair gets zeros for the keys that only the second one sees
+  const int before = (tr.row0 - sq.r0) / (2 * kM) * (2 * kM);
+  const int end = a.pair ? sq.len - sq.n + min(sq.n, before + 2 * kM) : vis;
+  const int key0 = span * a.span_keys, key1 = min(key0 + a.span_keys, (end + 63) & ~63);
+  if (tr.n == 0 || end <= 0 || key0 >= end) return;
   const int prow = scratch_row(sq.r0, tr.b) + (tr.row0 - sq.r0), r8 = up8(tr.n);
 
   if (t == 0) {
@@ -350,9 +354,20 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_few_kernel(const TcAr
 
 // ============================================================================== gates
 
-constexpr int kStages = 4;
+// One CTA per tile, or (kPair) two CTAs of a cluster on two neighbouring row tiles of a strip:
+// each holds its rows' P and half of the step's G, which halves what G takes from L2 to the
+// SMs (what bounds whole tiles: 48 KB a step and CTA come to about 13 TB/s) and leaves room
+// for 6 stages.
+template <bool kPair> struct Cfg {
+  static constexpr int kStages = kPair ? 6 : 4;
+  static constexpr int kCols = kPair ? kN / 2 : kN;             // G columns in this CTA
+  static constexpr int kChunks = kCols / 64;
+  static constexpr uint32_t kBBytes = kK * kCols * 2;           // 16 or 32 KB of G
+};
+constexpr int kMaxStages = 6;
 constexpr uint32_t kABytes = kM * 128;       // 16 KB of P
-constexpr uint32_t kBBytes = kK * kN * 2;    // 32 KB of G
+constexpr uint32_t kRingBytes = Cfg<false>::kStages * (kABytes + Cfg<false>::kBBytes);
+static_assert(kRingBytes == Cfg<true>::kStages * (kABytes + Cfg<true>::kBBytes), "both forms share one layout");
 constexpr uint32_t kTurnBytes = 4 * 4096;    // epilogue: 32 rows x 32 columns in f32 per warp
 constexpr int kGThreads = 352;
 constexpr int kJobSlots = 4;
@@ -360,12 +375,14 @@ constexpr int kEpi0 = 2, kScrub0 = 6, kSched = 10;
 
 struct Job {
   int b, row0, rows, pos0, hl, strip, it0, it1, nc, c, tile, prow;  // b < 0: no more jobs
-  int poison;
+  // of the pair's two tiles together (else the tile's own): the keys that some row sees, the
+  // first dirty step; and the other CTA's rows
+  int end, dirty, lo, other;  // lo: rows of the first dirty step that all see
 };
 
 struct __align__(8) GBars {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t dirty_full[kStages], clean[kStages];  // of the dirty steps' G, a ring of their own
+  uint64_t full[kMaxStages], empty[kMaxStages];            // (a pair's full: the leader's)
+  uint64_t dirty_full[kMaxStages], clean[kMaxStages];      // of the dirty steps' G, a ring of their own
   uint64_t acc_full[2], acc_empty[2];
   uint64_t job_full[kJobSlots], job_empty[kJobSlots];
   uint64_t drain;
@@ -374,11 +391,15 @@ struct __align__(8) GBars {
   int last;
   Job job[kJobSlots];
   int page[kJobSlots][32];  // pages of a job's first 32 boxes
+  // Whether the scrub warps (of either CTA) took something out of job n's products, at n % 8.
+  // The epilogue clears its entry; job n + 8 is not copied before both epilogues are through
+  // with job n (two accumulators and at most 6 steps lie between).
+  int poison[8];
 };
 // With the weights kernel's shared memory this exceeds an SM's, so a CTA of this kernel that
 // is launched early never sits beside one of that kernel's (which may still have to
 // allocate its tensor memory).
-constexpr size_t kGSmem = 1024 + kStages * (size_t)(kABytes + kBBytes) + kTurnBytes + sizeof(GBars);
+constexpr size_t kGSmem = 1024 + (size_t)kRingBytes + kTurnBytes + sizeof(GBars);
 static_assert(kGSmem <= 232448, "shared memory budget");
 static_assert(kGSmem + kWSmem > 233472, "the two kernels never share an SM");
 
@@ -411,11 +432,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars&
 // are written too.
 __device__ __forceinline__ int steps_of(int vis) { return max(1, (vis + kK - 1) / kK); }
 
-// Steps of one (head, strip) of a sequence, all its tiles.
-__device__ __forceinline__ long long seq_steps(const PagedSeq& s) {
+// Steps of one (head, strip) of a sequence, all its tiles of `rows` (128 or 256) rows.
+__device__ __forceinline__ long long seq_steps(const PagedSeq& s, int rows) {
   if (s.n == 0) return 0;
-  const long long mt = (s.n + kM - 1) / kM, before = max(0, s.len - s.n + kK - 1) / kK;
-  return (mt - 1) * before + mt * (mt - 1) + steps_of(s.len);
+  const long long mt = (s.n + rows - 1) / rows, before = max(0, s.len - s.n + kK - 1) / kK;
+  return (mt - 1) * before + mt * (mt - 1) / 2 * (rows / kK) + steps_of(s.len);
 }
 
 struct Ring {
@@ -446,20 +467,23 @@ __device__ __forceinline__ int box_page(const TcArgs& a, int b, int box, int box
 }
 // Boxes of a sequence up to the end of a job's keys.
 __device__ __forceinline__ int job_boxes(const TcArgs& a, const Job& j) {
-  const int vis = j.pos0 + j.rows;
-  return vis <= 0 ? 0 : (min(j.it1 * kK, vis) + a.box_rows - 1) / a.box_rows;
+  return j.end <= 0 ? 0 : (min(j.it1 * kK, j.end) + a.box_rows - 1) / a.box_rows;
 }
 
-// Warp kSched: takes jobs from the counter, works out what they are and hands them to the
-// other roles, a few ahead of the one that runs.
-__device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
+// Warp kSched: takes jobs, works out what they are and hands them to the other roles, a few
+// ahead of the one that runs.  Single CTAs take them from a counter; pairs in turn, so that
+// both CTAs know their job without asking.
+template <bool kPair>
+__device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, int rank) {
+  constexpr int kRows = kPair ? 2 * kM : kM;  // rows of a job
+  const int workers = kPair ? gridDim.x / 2 : gridDim.x;
   // steps of the whole launch, and from them the steps of a key range
   const int HS = a.heads * a.strips;
   long long total = 0;
-  for (int i = lane; i < a.p.B; i += 32) total += seq_steps(paged_seq(a.p, i, false));
+  for (int i = lane; i < a.p.B; i += 32) total += seq_steps(paged_seq(a.p, i, false), kRows);
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= HS;
-  const long long want = a.jobs_per_sm * (long long)gridDim.x;
+  const long long want = a.jobs_per_sm * (long long)workers;
   const int range = (int)max((long long)a.min_steps, (total + want - 1) / want);
 
   // a window of 32 sequences, one per lane: rows, length, jobs (inclusive prefix)
@@ -470,7 +494,7 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
   Ring jr;
   int nxt = 0;
   bool first = true;
-  long long j = blockIdx.x;  // then from the counter, gridDim.x on
+  long long j = kPair ? blockIdx.x / 2 : blockIdx.x;  // then from the counter, gridDim.x on
   while (true) {
     while (j >= jend && w0 + 32 < a.p.B) {
       w0 += 32;
@@ -478,7 +502,7 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       long long jobs = 0;
       if (w0 + lane < a.p.B) {
         ws = paged_seq(a.p, w0 + lane, false);
-        wmt = (ws.n + kM - 1) / kM;
+        wmt = (ws.n + kRows - 1) / kRows;
         jobs = (long long)wmt * ((steps_of(ws.len) + range - 1) / range) * HS;
       }
       pre = jobs;
@@ -504,18 +528,22 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       const int ti = mt - 1 - idx % mt, hs = idx / mt % HS;
       job.c = idx / mt / HS;
       job.b = w0 + owner;
-      job.row0 = r0 + ti * kM;
-      job.rows = min(kM, n - ti * kM);
-      job.pos0 = len - n + ti * kM;
+      const int before_rows = ti * kRows + (kPair ? rank * kM : 0);  // the sequence's new tokens before
+      job.row0 = r0 + before_rows;
+      job.rows = min(kM, max(0, n - before_rows));
+      job.other = kPair ? min(kM, max(0, n - ti * kRows - (1 - rank) * kM)) : 0;
+      job.pos0 = len - n + before_rows;
+      job.end = len - n + min(n, (ti + 1) * kRows);
+      job.dirty = first_dirty(len - n + ti * kRows);
+      job.lo = len - n + ti * kRows + 1 - job.dirty * kK;
       job.hl = hs / a.strips;
       job.strip = hs - job.hl * a.strips;
-      const int u = steps_of(job.pos0 + job.rows);
+      const int u = steps_of(job.end);
       job.nc = (u + range - 1) / range;
       job.it0 = job.c * range;
       job.it1 = min(u, job.it0 + range);
-      job.tile = r0 / kM + job.b + ti;
-      job.prow = scratch_row(r0, job.b) + ti * kM;
-      job.poison = 0;
+      job.tile = r0 / kM + job.b + before_rows / kM;
+      job.prow = scratch_row(r0, job.b) + before_rows;
       skip = job.c >= job.nc;  // a tile of the sequence that sees fewer keys
     }
     if (!skip) {
@@ -529,6 +557,10 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       jr.next(kJobSlots);
       if (job.b < 0) break;
     }
+    if (kPair) {
+      j += workers;
+      continue;
+    }
     if (first) {
       griddep_wait();  // the counters are the weights kernel's
       first = false;
@@ -541,26 +573,39 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
 }
 
 // Warp 0: copies each step's P and G.
+template <bool kPair>
 __device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, uint8_t* sB, const CUtensorMap* tmG,
-                                        const CUtensorMap* tmG4, int lane) {
+                                        const CUtensorMap* tmG4, const CUtensorMap* tmP, int lane, int rank) {
+  constexpr int kStages = Cfg<kPair>::kStages, kChunks = Cfg<kPair>::kChunks;
+  constexpr uint32_t kBBytes = Cfg<kPair>::kBBytes;
   Ring st, jr, dr;
   uint32_t issued_mask = 0, issued_phase = 0;  // bits 0..: full, 8..: dirty_full
   bool ok = true, waited = false;
   const int br = a.box_rows, spp = kK / br;  // boxes of a step
   const int win = 32 / spp;                  // steps of a window of 32 boxes
-  const int lane_step = lane / spp, lane_dst = (lane - lane_step * spp) * (4 * br * 128);
+  const int lane_step = lane / spp, lane_dst = (lane - lane_step * spp) * (kChunks * br * 128);
   while (ok) {
     if (!(ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a))) break;
     const Job job = b.job[jr.stage];
     int page = b.page[jr.stage][lane], page2 = a.p.n_pages;  // this window's, and the next one's
     if (job.b < 0) break;
-    const int nbc = (job_cols(a, job) + 63) / 64, head = a.h0 + job.hl, x0 = job.strip * kN;
-    const bool whole = x0 + kN <= a.m_h;  // the strip's four 64-column boxes in one copy
+    const int head = a.h0 + job.hl, x0 = job.strip * kN + rank * Cfg<kPair>::kCols;
+    // 64-column chunks of this CTA's columns that hold gates (and of the other CTA's)
+    const int nbc = min(kChunks, max(0, (a.m_h - x0 + 63) / 64));
+    const int nbc2 = kPair ? min(kChunks, max(0, (a.m_h - job.strip * kN - (1 - rank) * Cfg<kPair>::kCols + 63) / 64)) : 0;
+    const bool whole = x0 + Cfg<kPair>::kCols <= a.m_h;  // all chunks in one copy
     const int box1 = job_boxes(a, job), r8 = up8(job.rows);
-    const uint32_t pbytes = job.pos0 + job.rows > 0 ? (uint32_t)r8 * 128 : 0u;
-    const uint32_t box_bytes = (uint32_t)(whole ? 4 : nbc) * br * 128;
+    // (a pair's P comes in boxes of 128 rows, whatever a last tile has)
+    const uint32_t pbytes = job.end <= 0 || job.rows == 0 ? 0u : kPair ? kABytes : (uint32_t)r8 * 128;
+    const uint32_t pbytes2 = !kPair || job.end <= 0 || job.other == 0 ? 0u : kABytes;
+    const uint32_t box_bytes = (uint32_t)nbc * br * 128, box_bytes2 = (uint32_t)nbc2 * br * 128;
     const uint8_t* psrc = p_block(a, job.hl, job.prow, r8, job.it0);
-    const int dirty = first_dirty(job.pos0), nsteps = job.it1 - job.it0;
+    const int nsteps = job.it1 - job.it0;
+    auto load_p = [&](int stage, const uint8_t* src) {
+      if (lane != 0 || pbytes == 0) return;
+      if (kPair) tma_load_2d_pair(sA + stage * kABytes, tmP, cluster_addr(&b.full[stage], 0), 0, (int)((src - a.P) / 128));
+      else bulk_load(sA + stage * kABytes, src, pbytes, &b.full[stage]);
+    };
     for (int w = 0; w < nsteps && ok; w += win) {
       const int box = (job.it0 + w) * spp + lane, prw = box * br % a.p.page_size;
       if (w + win < nsteps) page2 = box_page(a, job.b, box + 32, box1);
@@ -571,22 +616,33 @@ __device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, 
           ok = warp_wait(&b.empty[st.stage], st.phase ^ 1, b, a);
           if (!ok) break;
         }
-        const bool is_dirty = job.it0 + w + i >= dirty;
-        uint64_t* gbar = is_dirty ? &b.dirty_full[dr.stage] : &b.full[st.stage];
+        const bool is_dirty = job.it0 + w + i >= job.dirty;
         const bool issue = there && lane_step == i;
-        const uint32_t gbytes = __popc(__ballot_sync(0xffffffffu, issue)) * box_bytes;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
         if (lane == 0) {
-          mbar_arrive_expect_tx(&b.full[st.stage], pbytes + (is_dirty ? 0u : gbytes));
-          if (is_dirty) mbar_arrive_expect_tx(gbar, gbytes);
-          if (pbytes && waited) bulk_load(sA + st.stage * kABytes, psrc, pbytes, &b.full[st.stage]);
+          // a pair's bytes, both CTAs', are counted by the leader's barrier
+          if (!kPair || rank == 0)
+            mbar_arrive_expect_tx(&b.full[st.stage], pbytes + pbytes2 + (is_dirty ? 0u : boxes * (box_bytes + box_bytes2)));
+          if (is_dirty) mbar_arrive_expect_tx(&b.dirty_full[dr.stage], boxes * box_bytes);
         }
+        if (waited) load_p(st.stage, psrc);
         __syncwarp();
-        if (issue) {
+        if (issue && nbc > 0) {
           uint8_t* dst = sB + st.stage * kBBytes + lane_dst;
-          if (whole) {
-            tma_load_5d(dst, tmG4, gbar, 0, prw, x0 / 64, head, page);
+          if (is_dirty || !kPair) {
+            uint64_t* gbar = is_dirty ? &b.dirty_full[dr.stage] : &b.full[st.stage];
+            if (whole) {
+              tma_load_5d(dst, tmG4, gbar, 0, prw, x0 / 64, head, page);
+            } else {
+              for (int c = 0; c < nbc; ++c) tma_load_4d(dst + c * br * 128, tmG, gbar, x0 + c * 64, head, prw, page);
+            }
           } else {
-            for (int c = 0; c < nbc; ++c) tma_load_4d(dst + c * br * 128, tmG, gbar, x0 + c * 64, head, prw, page);
+            const uint32_t gbar = cluster_addr(&b.full[st.stage], 0);
+            if (whole) {
+              tma_load_5d_pair(dst, tmG4, gbar, 0, prw, x0 / 64, head, page);
+            } else {
+              for (int c = 0; c < nbc; ++c) tma_load_4d_pair(dst + c * br * 128, tmG, gbar, x0 + c * 64, head, prw, page);
+            }
           }
         }
         issued_mask |= 1u << st.stage;
@@ -598,13 +654,11 @@ __device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, 
         }
         st.next(kStages);
         psrc += (size_t)r8 * 128;
-        if (!waited && w + i + 1 == min(nsteps, kStages)) {
+        if (!waited && w + i + 1 == min(nsteps, min(kStages, win))) {
           // the first stages' G is on its way; their P once the weights are there
           griddep_wait();
           waited = true;
-          if (lane == 0 && pbytes)
-            for (int x = 0; x <= w + i; ++x)
-              bulk_load(sA + x * kABytes, p_block(a, job.hl, job.prow, r8, job.it0 + x), pbytes, &b.full[x]);
+          for (int x = 0; x <= w + i; ++x) load_p(x, p_block(a, job.hl, job.prow, r8, job.it0 + x));
         }
       }
       page = page2;
@@ -614,27 +668,30 @@ __device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, 
     jr.next(kJobSlots);
   }
   if (!waited) griddep_wait();
-  // copies still in flight must land before the CTA exits
+  // copies still in flight must land before the CTA exits (a pair's leader waits for both)
   for (int s = 0; s < kStages; ++s) {
-    if (issued_mask >> s & 1) mbar_wait(&b.full[s], issued_phase >> s & 1, a.timeout_ns);
+    if ((!kPair || rank == 0) && (issued_mask >> s & 1)) mbar_wait(&b.full[s], issued_phase >> s & 1, a.timeout_ns);
     if (issued_mask >> (s + 8) & 1) mbar_wait(&b.dirty_full[s], issued_phase >> (s + 8) & 1, a.timeout_ns);
   }
 }
 
-// Warp 1, one thread: issues the products.
+// Warp 1, one thread (a pair's leader's): issues the products.
+template <bool kPair>
 __device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_t* sA, const uint8_t* sB, uint32_t tmem) {
   // Descriptors stay in registers: stages and k-steps differ in the start address alone,
   // whose field (bytes / 16, shared memory < 256 KB) never carries.  G lies as [box of br
   // keys][64-column chunk][key][128 bytes]: 64-column chunks are br * 128 bytes apart, 8-key
   // groups 1024 (or, in boxes of 8 keys, a whole box).
+  constexpr int kStages = Cfg<kPair>::kStages, kChunks = Cfg<kPair>::kChunks;
+  constexpr uint32_t kBBytes = Cfg<kPair>::kBBytes;
   const int br = a.box_rows;
   const uint64_t pd0 = smem_desc(smem_u32(sA), 16, 1024, kSwizzle128B);
-  const uint64_t gd0 = smem_desc(smem_u32(sB), br * 128, br == 8 ? 4096u : 1024u, kSwizzle128B);
+  const uint64_t gd0 = smem_desc(smem_u32(sB), br * 128, br == 8 ? kChunks * 1024u : 1024u, kSwizzle128B);
   uint32_t koff[4];
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
     const int key = kk * 16, box = key / br;
-    koff[kk] = (uint32_t)(box * (4 * br * 128) + (key - box * br) * 128) >> 4;
+    koff[kk] = (uint32_t)(box * (kChunks * br * 128) + (key - box * br) * 128) >> 4;
   }
   Ring st, jr, acc, dr;
   bool ok = true;
@@ -642,21 +699,29 @@ __device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_
     if (!(ok = wait_bar(&b.job_full[jr.stage], jr.phase, b, a))) break;
     const Job job = b.job[jr.stage];
     if (job.b < 0) break;
-    const int vis = job.pos0 + job.rows;
-    const uint32_t idesc = idesc_bf16_f32(kM, (job_cols(a, job) + 15) & ~15, false, true);
+    const uint32_t idesc =
+        kPair ? idesc_bf16_f32(2 * kM, kN, false, true) : idesc_bf16_f32(kM, (job_cols(a, job) + 15) & ~15, false, true);
     const uint32_t d = tmem + acc.stage * kN;
     if (!(ok = wait_bar(&b.acc_empty[acc.stage], acc.phase ^ 1, b, a))) break;
     tc_fence_after_nc();
     uint32_t accum = 0;  // of a step's first k-step
+    auto product = [&](uint64_t pd, uint64_t gd, int kk) {
+      if (kPair) mma_bf16_ss_pair(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
+      else mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (kPair) mma_commit_pair(bar);
+      else mma_commit_nc(bar);
+    };
     int it = job.it0;
-    for (const int e = min(first_dirty(job.pos0), job.it1); it < e; ++it) {
+    for (const int e = min(job.dirty, job.it1); it < e; ++it) {
       if (!(ok = wait_bar(&b.full[st.stage], st.phase, b, a))) break;
       tc_fence_after_nc();
       const uint64_t pd = pd0 + (uint64_t)(st.stage * (kABytes >> 4)), gd = gd0 + (uint64_t)(st.stage * (kBBytes >> 4));
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
+      for (int kk = 0; kk < 4; ++kk) product(pd, gd, kk);
       accum = 1;
-      mma_commit_nc(&b.empty[st.stage]);
+      commit(&b.empty[st.stage]);
       st.next(kStages);
     }
     for (; ok && it < job.it1; ++it) {
@@ -665,80 +730,93 @@ __device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_
       dr.next(kStages);
       tc_fence_after_nc();
       const uint64_t pd = pd0 + (uint64_t)(st.stage * (kABytes >> 4)), gd = gd0 + (uint64_t)(st.stage * (kBBytes >> 4));
-      const int keys = vis - it * kK;
+      const int keys = job.end - it * kK;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (kk * 16 < keys) mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
+        if (kk * 16 < keys) product(pd, gd, kk);
       accum = 1;
-      mma_commit_nc(&b.empty[st.stage]);
+      commit(&b.empty[st.stage]);
       st.next(kStages);
     }
     if (!ok) break;
-    mma_commit(&b.acc_full[acc.stage]);
+    commit(&b.acc_full[acc.stage]);
     mbar_arrive(&b.job_empty[jr.stage]);
     acc.next(2);
     jr.next(kJobSlots);
   }
-  mma_commit(&b.drain);
+  if (kPair) mma_commit_pair(&b.drain);
+  else mma_commit(&b.drain);
   mbar_wait(&b.drain, 0, a.timeout_ns);
 }
 
 // Warps 6-9: dirty steps.
-__device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, int t, int lane) {
+template <bool kPair>
+__device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, int t, int lane, int rank) {
+  constexpr int kStages = Cfg<kPair>::kStages, kChunks = Cfg<kPair>::kChunks;
+  constexpr uint32_t kBBytes = Cfg<kPair>::kBBytes;
   const int br = a.box_rows;
   Ring jr, dr;
   int step = 0;  // steps before the job, modulo the stages
+  int n = 0;     // jobs before
   bool ok = true;
   while (ok) {
     if (!(ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a))) break;
     const Job job = b.job[jr.stage];
     if (job.b < 0) break;
-    for (int it = max(job.it0, first_dirty(job.pos0)); it < job.it1; ++it) {
+    const int nbc = min(kChunks, max(0, (a.m_h - job.strip * kN - rank * Cfg<kPair>::kCols + 63) / 64));
+    for (int it = max(job.it0, job.dirty); it < job.it1; ++it) {
       if (!(ok = warp_wait(&b.dirty_full[dr.stage], dr.phase, b, a))) break;
-      const int keys = min(kK, max(0, job.pos0 + job.rows - it * kK)), rows = (keys + 15) & ~15;
-      const int lo = max(0, job.pos0 + 1 - it * kK);  // rows before are seen by all
+      const int keys = min(kK, max(0, job.end - it * kK)), rows = (keys + 15) & ~15;
+      const int lo = it == job.dirty ? max(0, job.lo) : 0;  // rows before are seen by all
       const uint32_t s0 = smem_u32(sB + ((step + it - job.it0) % kStages) * kBBytes);
       // rows t / 8 + 16 k: their 16-byte pieces are on their way before the first is looked
       // at (this stands between a step's copy and its product)
       bool found = false;
 #pragma unroll
       for (int k2 = 0; k2 < 2; ++k2) {
-        uint4 x[2][4];
+        uint4 x[2][kChunks];
         uint32_t at[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = t / 8 + 16 * (2 * k2 + k), box = r / br;
-          at[k] = s0 + box * (4 * br * 128) + (r - box * br) * 128 + (t & 7) * 16;
+          at[k] = s0 + box * (kChunks * br * 128) + (r - box * br) * 128 + (t & 7) * 16;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            x[k][c] = r >= lo && r < keys ? ld_shared_v4(at[k] + c * br * 128) : make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < kChunks; ++c)
+            x[k][c] = c < nbc && r >= lo && r < keys ? ld_shared_v4(at[k] + c * br * 128) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = t / 8 + 16 * (2 * k2 + k);
           uint32_t any = 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < kChunks; ++c)
             any |= non_finite(x[k][c].x) | non_finite(x[k][c].y) | non_finite(x[k][c].z) | non_finite(x[k][c].w);
           if (r >= keys && r < rows) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) st_shared_v4(at[k] + c * br * 128, make_uint4(0, 0, 0, 0));
-          } else if (any) {  // (chunks past the strip's columns hold anything: unused)
+            for (int c = 0; c < kChunks; ++c) st_shared_v4(at[k] + c * br * 128, make_uint4(0, 0, 0, 0));
+          } else if (any) {
             found = true;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < kChunks; ++c)
               st_shared_v4(at[k] + c * br * 128, make_uint4(drop(x[k][c].x), drop(x[k][c].y), drop(x[k][c].z), drop(x[k][c].w)));
           }
         }
       }
-      if (found) *(volatile int*)&b.job[jr.stage].poison = 1;
+      if (found) {
+        *(volatile int*)&b.poison[n & 7] = 1;
+        if (kPair) st_cluster(cluster_addr(&b.poison[n & 7], 1 - rank), 1);
+      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b.clean[dr.stage]);
+      if (lane == 0) {
+        if (kPair) mbar_arrive_cluster(cluster_addr(&b.clean[dr.stage], 0));
+        else mbar_arrive(&b.clean[dr.stage]);
+      }
       dr.next(kStages);
     }
     if (!ok) break;
     step = (step + job.it1 - job.it0) % kStages;
+    ++n;
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.job_empty[jr.stage]);
     jr.next(kJobSlots);
@@ -746,12 +824,13 @@ __device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, in
 }
 
 // Warps 2-5: accumulators to outputs, or to partial sums.
+template <bool kPair>
 __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t* sTurn, uint32_t tmem, int warp, int lane) {
   const int quarter = warp & 3, r = quarter * 32 + lane;  // TMEM lane, the tile's row
   const bool lead = warp == kEpi0 && lane == 0;
   const size_t width = (size_t)a.H * a.m_pitch;
   Ring jr, acc;
-  while (true) {
+  for (int n = 0;; ++n) {
     bool ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a);
     const Job job = b.job[jr.stage];
     const int cols = ok && job.b >= 0 ? job_cols(a, job) : 0;
@@ -765,7 +844,7 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
     if (!named_bar_and(1, 128, ok)) break;
     if (job.b < 0) break;
     tc_fence_after();
-    const bool poison = *(volatile int*)&b.job[jr.stage].poison != 0;
+    const bool poison = *(volatile int*)&b.poison[n & 7] != 0;
     const int vis = job.pos0 + job.rows, head = a.h0 + job.hl, pos = job.pos0 + r, r8 = up8(job.rows);
     const uint32_t trow = tmem + acc.stage * kN + ((uint32_t)(quarter * 32) << 16);
     const bool warp_rows = quarter * 32 < job.rows;  // else this warp's rows are not there
@@ -777,7 +856,7 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
     const float null_w = a.null_bias ? expf(a.null_bias[head] - head_tau(a.tau, a.s, head, a.p.err, kKernPaged)) : 0.f;
 
     // The keys whose non-finite gates the scrub warps took out of this job's product.
-    const int bad0 = max(job.pos0 + 1, job.it0 * kK), bad1 = min(vis, job.it1 * kK);
+    const int bad0 = max(job.dirty * kK + job.lo, job.it0 * kK), bad1 = min(vis, job.it1 * kK);
     // The accumulator's 32 columns from c0 on of row r, with what was taken out put back
     // where the row sees it.
     auto fetch = [&](int c0, float (&y)[32]) {
@@ -832,7 +911,9 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
       for (int k = 0; k < kSlotRegs; ++k) sl_reg[k] = k0 + k < job.nc ? __ldcg(a.slot + tkey * a.nc_cap + k0 + k) : -1;
     };
 
-    if (job.rows <= kFewRows) {
+    if (job.rows == 0) {
+      // ---- a pair's second CTA without rows
+    } else if (job.rows <= kFewRows) {
       // ---- few rows: the accumulator's rows go to shared memory, then this thread takes
       // columns 2 t and 2 t + 1 of each
       const int t = threadIdx.x - kEpi0 * 32, c = 2 * t;
@@ -1024,10 +1105,15 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
         }
       }
     }
+    if (poison) {  // all four warps have read it
+      named_bar_sync(1, 128);
+      if (lead) b.poison[n & 7] = 0;
+    }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&b.acc_empty[acc.stage]);
+      if (kPair) mbar_arrive_cluster(cluster_addr(&b.acc_empty[acc.stage], 0));
+      else mbar_arrive(&b.acc_empty[acc.stage]);
       mbar_arrive(&b.job_empty[jr.stage]);
     }
     acc.next(2);
@@ -1035,60 +1121,75 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
   }
 }
 
+template <bool kPair>
 __global__ void __launch_bounds__(kGThreads, 1)
-    paged_gates_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG4, const TcArgs a) {
+    paged_gates_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG4,
+                       const __grid_constant__ CUtensorMap tmP, const TcArgs a) {
+  constexpr int kStages = Cfg<kPair>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = base;
   uint8_t* sB = base + kStages * kABytes;
-  uint8_t* sTurn = sB + kStages * kBBytes;
+  uint8_t* sTurn = base + kRingBytes;
   GBars& b = *reinterpret_cast<GBars*>(sTurn + kTurnBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int rank = kPair ? (int)cluster_rank() : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&b.full[s], 1);
       mbar_init(&b.empty[s], 1);
       mbar_init(&b.dirty_full[s], 1);
-      mbar_init(&b.clean[s], 4);
+      mbar_init(&b.clean[s], kPair ? 8 : 4);  // scrub warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.acc_full[i], 1);
-      mbar_init(&b.acc_empty[i], 4);
+      mbar_init(&b.acc_empty[i], kPair ? 8 : 4);  // epilogue warps
     }
     for (int i = 0; i < kJobSlots; ++i) {
       mbar_init(&b.job_full[i], 1);
-      mbar_init(&b.job_empty[i], 10);  // producer, MMA issuer, 4 epilogue warps, 4 scrub warps
+      // producer, 4 epilogue warps, 4 scrub warps and the MMA issuer (a pair's leader's)
+      mbar_init(&b.job_empty[i], rank == 0 ? 10 : 9);
     }
     mbar_init(&b.drain, 1);
     b.abort = 0;
+    for (int i = 0; i < 8; ++i) b.poison[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&b.tmem_base, 512);
-    tmem_relinquish();
+    if (kPair) {
+      tmem_alloc_pair(&b.tmem_base, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&b.tmem_base, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (kPair) cluster_sync();  // the other CTA's barriers too
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = b.tmem_base;
 
   if (warp == 0) {
-    produce(a, b, sA, sB, &tmG, &tmG4, lane);
+    produce<kPair>(a, b, sA, sB, &tmG, &tmG4, &tmP, lane, rank);
   } else if (warp == 1) {
-    if (lane == 0) multiply(a, b, sA, sB, tmem);
+    if (lane == 0 && rank == 0) multiply<kPair>(a, b, sA, sB, tmem);
   } else if (warp < kScrub0) {
-    finish_tiles(a, b, sTurn, tmem, warp, lane);
+    finish_tiles<kPair>(a, b, sTurn, tmem, warp, lane);
   } else if (warp < kSched) {
-    scrub(a, b, sB, threadIdx.x - kScrub0 * 32, lane);
+    scrub<kPair>(a, b, sB, threadIdx.x - kScrub0 * 32, lane, rank);
   } else {
-    schedule(a, b, lane);
+    schedule<kPair>(a, b, lane, rank);
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (kPair) cluster_sync();  // nothing of this CTA is still to be signalled or read by the other
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (kPair) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
   }
 }
 
@@ -1110,6 +1211,7 @@ int box_rows(int page_size) {
 }
 
 struct TcPlan {
+  int pair;
   int rows_tot, key_blocks, span_keys, spans, strips, tiles, r8cap, min_steps, jobs_per_sm, nc_cap, n_slots, heads, grid;
   size_t P, den, part, slot, done, next, total;
 };
@@ -1117,6 +1219,7 @@ struct TcPlan {
 TcPlan tc_plan(const PagedCall& c) {
   TcPlan l;
   const int sms = num_sms();
+  l.pair = c.p.max_new > kM;  // some sequence has two row tiles
   l.rows_tot = up8(c.p.N) + 8 * c.p.B;
   l.key_blocks = ceil_div(c.p.max_len, kK);
   // at most 32 spans of whole 128-key blocks (their sums are added once per strip)
@@ -1131,7 +1234,7 @@ TcPlan tc_plan(const PagedCall& c) {
   l.min_steps = l.r8cap <= kFewRows ? 3 : 8;
   l.jobs_per_sm = l.r8cap <= kFewRows ? kJobsPerSm : 2;
   l.nc_cap = ceil_div(l.key_blocks, l.min_steps);
-  l.grid = sms;
+  l.grid = l.pair ? sms & ~1 : sms;
   // a tile that is cut has at most twice as many ranges as whole ranges fit in it
   l.n_slots = 2 * kJobsPerSm * sms;
   // heads of a pass: as many as keep P within 2 GB
@@ -1179,6 +1282,7 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   a.rows_tot = l.rows_tot; a.key_blocks = l.key_blocks; a.span_keys = l.span_keys; a.spans = l.spans;
   a.strips = l.strips; a.tiles = l.tiles; a.r8cap = l.r8cap; a.min_steps = l.min_steps; a.jobs_per_sm = l.jobs_per_sm; a.nc_cap = l.nc_cap; a.n_slots = l.n_slots;
   a.box_rows = box_rows(c.p.page_size);
+  a.pair = l.pair;
   a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
   a.v_vec = c.v && (reinterpret_cast<uintptr_t>(c.v) & 15u) == 0 && c.v_pitch % 8 == 0;
   a.q = static_cast<const __nv_bfloat16*>(c.q); a.v = static_cast<const __nv_bfloat16*>(c.v);
@@ -1193,15 +1297,18 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   a.next = reinterpret_cast<int*>(base + l.next);
   a.timeout_ns = kTimeoutNs;
 
-  CUtensorMap mG, mG4;
+  CUtensorMap mG, mG4, mP;
   cudaError_t e = make_tmap_4d_heads(&mG, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 64);
-  mG4 = mG;  // used only where a head holds a whole strip
-  if (e == cudaSuccess && c.m_h >= kN)
-    e = make_tmap_5d_chunks(&mG4, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 4);
+  mG4 = mP = mG;  // (a head's whole columns of a CTA; a pair's P)
+  const int cols = l.pair ? Cfg<true>::kCols : Cfg<false>::kCols;
+  if (e == cudaSuccess && c.m_h >= cols)
+    e = make_tmap_5d_chunks(&mG4, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, cols / 64);
+  if (e == cudaSuccess && l.pair) e = make_tmap_2d_plain(&mP, a.P, (uint64_t)l.rows_tot * l.key_blocks * l.heads, 64, 64, kM, 64);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(paged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_gates_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
+    e = cudaFuncSetAttribute(l.pair ? paged_gates_kernel<true> : paged_gates_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
   if (e != cudaSuccess) return e;
   for (a.h0 = 0; a.h0 < c.H; a.h0 += l.heads) {
     a.heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
@@ -1215,12 +1322,16 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
     cfg.blockDim = dim3(kGThreads);
     cfg.dynamicSmemBytes = kGSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_gates_kernel, mG, mG4, a);
+    cfg.numAttrs = l.pair ? 2 : 1;
+    e = l.pair ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<true>, mG, mG4, mP, a)
+               : cudaLaunchKernelEx(&cfg, paged_gates_kernel<false>, mG, mG4, mP, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
