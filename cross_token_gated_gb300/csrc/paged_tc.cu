@@ -371,6 +371,7 @@ static_assert(kRingBytes == Cfg<true>::kStages * (kABytes + Cfg<true>::kBBytes),
 constexpr uint32_t kTurnBytes = 4 * 4096;    // epilogue: 32 rows x 32 columns in f32 per warp
 constexpr int kGThreads = 352;
 constexpr int kJobSlots = 4;
+constexpr int kNearEnd = 8;  // steps of a job that are left when the next one is taken
 constexpr int kEpi0 = 2, kScrub0 = 6, kSched = 10;
 
 struct Job {
@@ -385,6 +386,7 @@ struct __align__(8) GBars {
   uint64_t dirty_full[kMaxStages], clean[kMaxStages];      // of the dirty steps' G, a ring of their own
   uint64_t acc_full[2], acc_empty[2];
   uint64_t job_full[kJobSlots], job_empty[kJobSlots];
+  uint64_t near_end;  // the producer is in a job's last steps: time to take the next one
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -492,8 +494,8 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, in
   PagedSeq ws{0, 0, 0};
   int wmt = 0;
   Ring jr;
-  int nxt = 0;
   bool first = true;
+  uint32_t taken = 0;  // jobs handed out and nearly copied
   long long j = kPair ? blockIdx.x / 2 : blockIdx.x;  // then from the counter, gridDim.x on
   while (true) {
     while (j >= jend && w0 + 32 < a.p.B) {
@@ -561,13 +563,16 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, in
       j += workers;
       continue;
     }
-    if (first) {
-      griddep_wait();  // the counters are the weights kernel's
-      first = false;
-      if (lane == 0) nxt = atomicAdd(a.next, 1);
+    if (first) griddep_wait();  // the counters are the weights kernel's
+    first = false;
+    // no earlier: a CTA that held jobs in advance would leave others without
+    if (!skip) {
+      if (!warp_wait(&b.near_end, taken & 1, b, a)) break;
+      ++taken;
     }
+    int nxt = 0;
+    if (lane == 0) nxt = atomicAdd(a.next, 1);
     j = (long long)gridDim.x + __shfl_sync(0xffffffffu, nxt, 0);
-    if (lane == 0) nxt = atomicAdd(a.next, 1);  // the number after, while this job is handed out
   }
   if (first) griddep_wait();
 }
@@ -612,6 +617,7 @@ __device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, 
       const bool there = box < box1;
       const int wn = min(win, nsteps - w);
       for (int i = 0; i < wn; ++i) {
+        if (!kPair && lane == 0 && w + i == max(0, nsteps - kNearEnd)) mbar_arrive(&b.near_end);
         if (waited && !__all_sync(0xffffffffu, mbar_try_wait(&b.empty[st.stage], st.phase ^ 1))) {
           ok = warp_wait(&b.empty[st.stage], st.phase ^ 1, b, a);
           if (!ok) break;
@@ -1151,6 +1157,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       // producer, 4 epilogue warps, 4 scrub warps and the MMA issuer (a pair's leader's)
       mbar_init(&b.job_empty[i], rank == 0 ? 10 : 9);
     }
+    mbar_init(&b.near_end, 1);
     mbar_init(&b.drain, 1);
     b.abort = 0;
     for (int i = 0; i < 8; ++i) b.poison[i] = 0;
