@@ -13,21 +13,21 @@
 // paged_weights_few_kernel  the same P for up to 8 new tokens of a sequence on the CUDA
 //     cores, a thread per key: a 128-row product would be nearly all padding.
 // paged_gates_kernel    U = P G: tiles of 128 rows x 256 gate columns, 64 keys a step.
-//     warp 0     TMA producer (4 stages of P 16 KB + G 32 KB), 32 pages looked up at a time,
-//                one lane per page issues its copies; the first job's G is asked for while
-//                the weights kernel still runs
+//     warps 0, 3 TMA producers (4 stages of P 16 KB + G 32 KB), a step each in turn; 32 pages
+//                looked up at a time, one lane per page issues its copies; the first job's G
+//                is asked for while the weights kernel still runs
 //     warp 1     MMA issuer (128 x 256 x 16), two accumulators in TMEM.  Tiles of a few rows
 //                run the same product on unused rows: it is shorter than the step's G takes
 //                from memory (D^T = G^T P^T with 16 columns, which does an eighth of the work,
 //                measured slower: 8 products a step of about 100 cycles each)
-//     warps 2-5  epilogue: times 1 / den and v, bf16 out; or f32 partial sums of a key range.
+//     warp 2     scheduler: takes jobs from a counter, works out what they are
+//     warps 4-11 epilogue: times 1 / den and v, bf16 out; or f32 partial sums of a key range.
 //                Rows are turned into columns through shared memory, so that v and out move
 //                in whole 64-byte pieces of a row
-//     warps 6-9  scrub: only in steps with keys that some row of the tile does not see:
+//     warps 12-15 scrub: only in steps with keys that some row of the tile does not see:
 //                slots past the sequence's length become zeros, and non-finite gates of the
 //                chunk's own tokens are taken out of the product (0 * NaN would reach rows
 //                that do not see them); the epilogue adds them back to the rows that do
-//     warp 10    scheduler: takes jobs from a counter, works out what they are
 //
 // A job is a (sequence, key range, head, strip, row tile) with the row tile fastest, so the
 // CTAs that work side by side share their G out of L2.  Key ranges are cut when the tiles
@@ -89,7 +89,6 @@ struct TcArgs {
   int nc_cap;                // key ranges of a tile, at most
   int n_slots;
   int box_rows;              // rows of a G box
-  int pair;                  // two CTAs per 256 rows
   float s;
   const float* tau;
   const float* null_bias;
@@ -100,9 +99,9 @@ struct TcArgs {
   const __nv_bfloat16 *k_pages, *g_pages;
   uint8_t* P;                // [head][row][key block][128 bytes], see p_block()
   float* den;                // [head][row][span]
-  float* part;               // [slot]: [64][r8cap][4], or [row][256] for tiles of few rows
-  int* slot;                 // [head][strip][tile][nc_cap]
-  int* done;                 // [head][strip][tile]: ranges that are done
+  float* part;               // [slot]: [32][r8cap][4], or [row][128] for tiles of few rows
+  int* slot;                 // [head][strip][tile][half][nc_cap]
+  int* done;                 // [head][strip][tile][half]: ranges that are done
   int* next;                 // [0] next job, [1] next partial slot
   uint64_t timeout_ns;
 };
@@ -116,7 +115,7 @@ __device__ __forceinline__ uint8_t* p_block(const TcArgs& a, int hl, int prow, i
 
 // The gates kernel's counters, cleared by all CTAs of a weights kernel together.
 __device__ __forceinline__ void clear_counters(const TcArgs& a, int tile, int hl, int span) {
-  const size_t n = (size_t)a.heads * a.strips * a.tiles;
+  const size_t n = (size_t)a.heads * a.strips * a.tiles * 2;
   const size_t cta = ((size_t)span * gridDim.y + hl) * gridDim.x + tile, ctas = (size_t)gridDim.x * gridDim.y * gridDim.z;
   for (size_t i = cta * blockDim.x + threadIdx.x; i < n; i += ctas * blockDim.x) a.done[i] = 0;
   if (cta == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
@@ -143,12 +142,9 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
   clear_counters(a, tile, hl, span);
   const TileRef tr = find_tile<kM>(a.p, tile, hl == 0 && span == 0);
   const int vis = tr.pos0 + tr.n;
+  const int key0 = span * a.span_keys, key1 = min(key0 + a.span_keys, (vis + 63) & ~63);
+  if (tr.n == 0 || vis <= 0 || key0 >= vis) return;
   const PagedSeq sq = paged_seq(a.p, tr.b, false);
-  // the first tile of a pair gets zeros for the keys that only the second one sees
-  const int before = (tr.row0 - sq.r0) / (2 * kM) * (2 * kM);
-  const int end = a.pair ? sq.len - sq.n + min(sq.n, before + 2 * kM) : vis;
-  const int key0 = span * a.span_keys, key1 = min(key0 + a.span_keys, (end + 63) & ~63);
-  if (tr.n == 0 || end <= 0 || key0 >= end) return;
   const int prow = scratch_row(sq.r0, tr.b) + (tr.row0 - sq.r0), r8 = up8(tr.n);
 
   if (t == 0) {
@@ -354,54 +350,40 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_few_kernel(const TcAr
 
 // ============================================================================== gates
 
-// One CTA per tile, or (kPair) two CTAs of a cluster on two neighbouring row tiles of a strip:
-// each holds its rows' P and half of the step's G, which halves what G takes from L2 to the
-// SMs (what bounds whole tiles: 48 KB a step and CTA come to about 13 TB/s) and leaves room
-// for 6 stages.
-template <bool kPair> struct Cfg {
-  static constexpr int kStages = kPair ? 6 : 4;
-  static constexpr int kCols = kPair ? kN / 2 : kN;             // G columns in this CTA
-  static constexpr int kChunks = kCols / 64;
-  static constexpr uint32_t kBBytes = kK * kCols * 2;           // 16 or 32 KB of G
-};
-constexpr int kMaxStages = 6;
+constexpr int kStages = 4;
 constexpr uint32_t kABytes = kM * 128;       // 16 KB of P
-constexpr uint32_t kRingBytes = Cfg<false>::kStages * (kABytes + Cfg<false>::kBBytes);
-static_assert(kRingBytes == Cfg<true>::kStages * (kABytes + Cfg<true>::kBBytes), "both forms share one layout");
-constexpr uint32_t kTurnBytes = 4 * 4096;    // epilogue: 32 rows x 32 columns in f32 per warp
-constexpr int kGThreads = 352;
+constexpr uint32_t kBBytes = kK * kN * 2;    // 32 KB of G
+constexpr uint32_t kTurnBytes = 8 * 4096;    // epilogue: 32 rows x 32 columns in f32 per warp
+constexpr int kGThreads = 512;
 constexpr int kJobSlots = 4;
-constexpr int kNearEnd = 8;  // steps of a job that are left when the next one is taken
-constexpr int kEpi0 = 2, kScrub0 = 6, kSched = 10;
+constexpr int kNearEnd = 12;  // steps of a job that are left when the next one is taken
+constexpr int kSched = 2, kProducers = 2, kEpi0 = 4, kScrub0 = 12;  // warps (producers: 0 and 3)
 
 struct Job {
   int b, row0, rows, pos0, hl, strip, it0, it1, nc, c, tile, prow;  // b < 0: no more jobs
-  // of the pair's two tiles together (else the tile's own): the keys that some row sees, the
-  // first dirty step; and the other CTA's rows
-  int end, dirty, lo, other;  // lo: rows of the first dirty step that all see
 };
 
 struct __align__(8) GBars {
-  uint64_t full[kMaxStages], empty[kMaxStages];            // (a pair's full: the leader's)
-  uint64_t dirty_full[kMaxStages], clean[kMaxStages];      // of the dirty steps' G, a ring of their own
+  uint64_t full[kStages], empty[kStages];
+  uint64_t dirty_full[kStages], clean[kStages];  // of the dirty steps' G, a ring of their own
   uint64_t acc_full[2], acc_empty[2];
   uint64_t job_full[kJobSlots], job_empty[kJobSlots];
-  uint64_t near_end;  // the producer is in a job's last steps: time to take the next one
+  uint64_t near_end;  // the producers are in a job's last steps: time to take the next one
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int last;
+  int last[2];
   Job job[kJobSlots];
   int page[kJobSlots][32];  // pages of a job's first 32 boxes
-  // Whether the scrub warps (of either CTA) took something out of job n's products, at n % 8.
-  // The epilogue clears its entry; job n + 8 is not copied before both epilogues are through
-  // with job n (two accumulators and at most 6 steps lie between).
-  int poison[8];
+  // Whether the scrub warps took something out of job n's products, at n % 8, for each half of
+  // the epilogue, which clears its entry.  Job n + 8 is not copied before both are through
+  // with job n (two accumulators and at most 4 steps lie between).
+  int poison[2][8];
 };
 // With the weights kernel's shared memory this exceeds an SM's, so a CTA of this kernel that
 // is launched early never sits beside one of that kernel's (which may still have to
 // allocate its tensor memory).
-constexpr size_t kGSmem = 1024 + (size_t)kRingBytes + kTurnBytes + sizeof(GBars);
+constexpr size_t kGSmem = 1024 + kStages * (size_t)(kABytes + kBBytes) + kTurnBytes + sizeof(GBars);
 static_assert(kGSmem <= 232448, "shared memory budget");
 static_assert(kGSmem + kWSmem > 233472, "the two kernels never share an SM");
 
@@ -434,11 +416,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars&
 // are written too.
 __device__ __forceinline__ int steps_of(int vis) { return max(1, (vis + kK - 1) / kK); }
 
-// Steps of one (head, strip) of a sequence, all its tiles of `rows` (128 or 256) rows.
-__device__ __forceinline__ long long seq_steps(const PagedSeq& s, int rows) {
+// Steps of one (head, strip) of a sequence, all its tiles.
+__device__ __forceinline__ long long seq_steps(const PagedSeq& s) {
   if (s.n == 0) return 0;
-  const long long mt = (s.n + rows - 1) / rows, before = max(0, s.len - s.n + kK - 1) / kK;
-  return (mt - 1) * before + mt * (mt - 1) / 2 * (rows / kK) + steps_of(s.len);
+  const long long mt = (s.n + kM - 1) / kM, before = max(0, s.len - s.n + kK - 1) / kK;
+  return (mt - 1) * before + mt * (mt - 1) + steps_of(s.len);
 }
 
 struct Ring {
@@ -469,23 +451,20 @@ __device__ __forceinline__ int box_page(const TcArgs& a, int b, int box, int box
 }
 // Boxes of a sequence up to the end of a job's keys.
 __device__ __forceinline__ int job_boxes(const TcArgs& a, const Job& j) {
-  return j.end <= 0 ? 0 : (min(j.it1 * kK, j.end) + a.box_rows - 1) / a.box_rows;
+  const int vis = j.pos0 + j.rows;
+  return vis <= 0 ? 0 : (min(j.it1 * kK, vis) + a.box_rows - 1) / a.box_rows;
 }
 
-// Warp kSched: takes jobs, works out what they are and hands them to the other roles, a few
-// ahead of the one that runs.  Single CTAs take them from a counter; pairs in turn, so that
-// both CTAs know their job without asking.
-template <bool kPair>
-__device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, int rank) {
-  constexpr int kRows = kPair ? 2 * kM : kM;  // rows of a job
-  const int workers = kPair ? gridDim.x / 2 : gridDim.x;
+// Warp kSched: takes jobs from the counter, works out what they are and hands them to the
+// other roles.
+__device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
   // steps of the whole launch, and from them the steps of a key range
   const int HS = a.heads * a.strips;
   long long total = 0;
-  for (int i = lane; i < a.p.B; i += 32) total += seq_steps(paged_seq(a.p, i, false), kRows);
+  for (int i = lane; i < a.p.B; i += 32) total += seq_steps(paged_seq(a.p, i, false));
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= HS;
-  const long long want = a.jobs_per_sm * (long long)workers;
+  const long long want = a.jobs_per_sm * (long long)gridDim.x;
   const int range = (int)max((long long)a.min_steps, (total + want - 1) / want);
 
   // a window of 32 sequences, one per lane: rows, length, jobs (inclusive prefix)
@@ -495,8 +474,8 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, in
   int wmt = 0;
   Ring jr;
   bool first = true;
-  uint32_t taken = 0;  // jobs handed out and nearly copied
-  long long j = kPair ? blockIdx.x / 2 : blockIdx.x;  // then from the counter, gridDim.x on
+  uint32_t taken = 0;        // jobs handed out and nearly copied
+  long long j = blockIdx.x;  // then from the counter, gridDim.x on
   while (true) {
     while (j >= jend && w0 + 32 < a.p.B) {
       w0 += 32;
@@ -504,7 +483,7 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, in
       long long jobs = 0;
       if (w0 + lane < a.p.B) {
         ws = paged_seq(a.p, w0 + lane, false);
-        wmt = (ws.n + kRows - 1) / kRows;
+        wmt = (ws.n + kM - 1) / kM;
         jobs = (long long)wmt * ((steps_of(ws.len) + range - 1) / range) * HS;
       }
       pre = jobs;
@@ -530,22 +509,17 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, in
       const int ti = mt - 1 - idx % mt, hs = idx / mt % HS;
       job.c = idx / mt / HS;
       job.b = w0 + owner;
-      const int before_rows = ti * kRows + (kPair ? rank * kM : 0);  // the sequence's new tokens before
-      job.row0 = r0 + before_rows;
-      job.rows = min(kM, max(0, n - before_rows));
-      job.other = kPair ? min(kM, max(0, n - ti * kRows - (1 - rank) * kM)) : 0;
-      job.pos0 = len - n + before_rows;
-      job.end = len - n + min(n, (ti + 1) * kRows);
-      job.dirty = first_dirty(len - n + ti * kRows);
-      job.lo = len - n + ti * kRows + 1 - job.dirty * kK;
+      job.row0 = r0 + ti * kM;
+      job.rows = min(kM, n - ti * kM);
+      job.pos0 = len - n + ti * kM;
       job.hl = hs / a.strips;
       job.strip = hs - job.hl * a.strips;
-      const int u = steps_of(job.end);
+      const int u = steps_of(job.pos0 + job.rows);
       job.nc = (u + range - 1) / range;
       job.it0 = job.c * range;
       job.it1 = min(u, job.it0 + range);
-      job.tile = r0 / kM + job.b + before_rows / kM;
-      job.prow = scratch_row(r0, job.b) + before_rows;
+      job.tile = r0 / kM + job.b + ti;
+      job.prow = scratch_row(r0, job.b) + ti * kM;
       skip = job.c >= job.nc;  // a tile of the sequence that sees fewer keys
     }
     if (!skip) {
@@ -558,10 +532,6 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, in
       if (lane == 0) mbar_arrive(&b.job_full[jr.stage]);
       jr.next(kJobSlots);
       if (job.b < 0) break;
-    }
-    if (kPair) {
-      j += workers;
-      continue;
     }
     if (first) griddep_wait();  // the counters are the weights kernel's
     first = false;
@@ -577,80 +547,64 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane, in
   if (first) griddep_wait();
 }
 
-// Warp 0: copies each step's P and G.
-template <bool kPair>
+// Warps 0 and 3: copy each step's P and G, in turn.
 __device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, uint8_t* sB, const CUtensorMap* tmG,
-                                        const CUtensorMap* tmG4, const CUtensorMap* tmP, int lane, int rank) {
-  constexpr int kStages = Cfg<kPair>::kStages, kChunks = Cfg<kPair>::kChunks;
-  constexpr uint32_t kBBytes = Cfg<kPair>::kBBytes;
+                                        const CUtensorMap* tmG4, int part, int lane) {
   Ring st, jr, dr;
   uint32_t issued_mask = 0, issued_phase = 0;  // bits 0..: full, 8..: dirty_full
   bool ok = true, waited = false;
+  int turn = 0;                              // whose step it is
   const int br = a.box_rows, spp = kK / br;  // boxes of a step
   const int win = 32 / spp;                  // steps of a window of 32 boxes
-  const int lane_step = lane / spp, lane_dst = (lane - lane_step * spp) * (kChunks * br * 128);
+  const int lane_step = lane / spp, lane_dst = (lane - lane_step * spp) * (4 * br * 128);
   while (ok) {
     if (!(ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a))) break;
     const Job job = b.job[jr.stage];
     int page = b.page[jr.stage][lane], page2 = a.p.n_pages;  // this window's, and the next one's
     if (job.b < 0) break;
-    const int head = a.h0 + job.hl, x0 = job.strip * kN + rank * Cfg<kPair>::kCols;
-    // 64-column chunks of this CTA's columns that hold gates (and of the other CTA's)
-    const int nbc = min(kChunks, max(0, (a.m_h - x0 + 63) / 64));
-    const int nbc2 = kPair ? min(kChunks, max(0, (a.m_h - job.strip * kN - (1 - rank) * Cfg<kPair>::kCols + 63) / 64)) : 0;
-    const bool whole = x0 + Cfg<kPair>::kCols <= a.m_h;  // all chunks in one copy
+    const int nbc = (job_cols(a, job) + 63) / 64, head = a.h0 + job.hl, x0 = job.strip * kN;
+    const bool whole = x0 + kN <= a.m_h;  // the strip's four 64-column boxes in one copy
     const int box1 = job_boxes(a, job), r8 = up8(job.rows);
-    // (a pair's P comes in boxes of 128 rows, whatever a last tile has)
-    const uint32_t pbytes = job.end <= 0 || job.rows == 0 ? 0u : kPair ? kABytes : (uint32_t)r8 * 128;
-    const uint32_t pbytes2 = !kPair || job.end <= 0 || job.other == 0 ? 0u : kABytes;
-    const uint32_t box_bytes = (uint32_t)nbc * br * 128, box_bytes2 = (uint32_t)nbc2 * br * 128;
+    const uint32_t pbytes = job.pos0 + job.rows > 0 ? (uint32_t)r8 * 128 : 0u;
+    const uint32_t box_bytes = (uint32_t)(whole ? 4 : nbc) * br * 128;
     const uint8_t* psrc = p_block(a, job.hl, job.prow, r8, job.it0);
-    const int nsteps = job.it1 - job.it0;
-    auto load_p = [&](int stage, const uint8_t* src) {
-      if (lane != 0 || pbytes == 0) return;
-      if (kPair) tma_load_2d_pair(sA + stage * kABytes, tmP, cluster_addr(&b.full[stage], 0), 0, (int)((src - a.P) / 128));
-      else bulk_load(sA + stage * kABytes, src, pbytes, &b.full[stage]);
-    };
+    const int dirty = first_dirty(job.pos0), nsteps = job.it1 - job.it0;
+    bool told = false;  // that the job nears its end
     for (int w = 0; w < nsteps && ok; w += win) {
       const int box = (job.it0 + w) * spp + lane, prw = box * br % a.p.page_size;
       if (w + win < nsteps) page2 = box_page(a, job.b, box + 32, box1);
       const bool there = box < box1;
       const int wn = min(win, nsteps - w);
       for (int i = 0; i < wn; ++i) {
-        if (!kPair && lane == 0 && w + i == max(0, nsteps - kNearEnd)) mbar_arrive(&b.near_end);
-        if (waited && !__all_sync(0xffffffffu, mbar_try_wait(&b.empty[st.stage], st.phase ^ 1))) {
-          ok = warp_wait(&b.empty[st.stage], st.phase ^ 1, b, a);
-          if (!ok) break;
-        }
-        const bool is_dirty = job.it0 + w + i >= job.dirty;
-        const bool issue = there && lane_step == i;
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
-        if (lane == 0) {
-          // a pair's bytes, both CTAs', are counted by the leader's barrier
-          if (!kPair || rank == 0)
-            mbar_arrive_expect_tx(&b.full[st.stage], pbytes + pbytes2 + (is_dirty ? 0u : boxes * (box_bytes + box_bytes2)));
-          if (is_dirty) mbar_arrive_expect_tx(&b.dirty_full[dr.stage], boxes * box_bytes);
-        }
-        if (waited) load_p(st.stage, psrc);
-        __syncwarp();
-        if (issue && nbc > 0) {
-          uint8_t* dst = sB + st.stage * kBBytes + lane_dst;
-          if (is_dirty || !kPair) {
-            uint64_t* gbar = is_dirty ? &b.dirty_full[dr.stage] : &b.full[st.stage];
+        const bool is_dirty = job.it0 + w + i >= dirty;
+        if (turn == part) {
+          if (w + i >= nsteps - kNearEnd && !told) {
+            told = true;
+            if (lane == 0) mbar_arrive(&b.near_end);
+          }
+          if (waited && !__all_sync(0xffffffffu, mbar_try_wait(&b.empty[st.stage], st.phase ^ 1))) {
+            ok = warp_wait(&b.empty[st.stage], st.phase ^ 1, b, a);
+            if (!ok) break;
+          }
+          uint64_t* gbar = is_dirty ? &b.dirty_full[dr.stage] : &b.full[st.stage];
+          const bool issue = there && lane_step == i;
+          const uint32_t gbytes = __popc(__ballot_sync(0xffffffffu, issue)) * box_bytes;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&b.full[st.stage], pbytes + (is_dirty ? 0u : gbytes));
+            if (is_dirty) mbar_arrive_expect_tx(gbar, gbytes);
+            if (pbytes && waited) bulk_load(sA + st.stage * kABytes, psrc, pbytes, &b.full[st.stage]);
+          }
+          __syncwarp();
+          if (issue) {
+            uint8_t* dst = sB + st.stage * kBBytes + lane_dst;
             if (whole) {
               tma_load_5d(dst, tmG4, gbar, 0, prw, x0 / 64, head, page);
             } else {
               for (int c = 0; c < nbc; ++c) tma_load_4d(dst + c * br * 128, tmG, gbar, x0 + c * 64, head, prw, page);
             }
-          } else {
-            const uint32_t gbar = cluster_addr(&b.full[st.stage], 0);
-            if (whole) {
-              tma_load_5d_pair(dst, tmG4, gbar, 0, prw, x0 / 64, head, page);
-            } else {
-              for (int c = 0; c < nbc; ++c) tma_load_4d_pair(dst + c * br * 128, tmG, gbar, x0 + c * 64, head, prw, page);
-            }
           }
         }
+        // (each producer keeps count of all steps: which fill of a stage is the last one)
         issued_mask |= 1u << st.stage;
         issued_phase = (issued_phase & ~(1u << st.stage)) | (st.phase << st.stage);
         if (is_dirty) {
@@ -659,45 +613,46 @@ __device__ __forceinline__ void produce(const TcArgs& a, GBars& b, uint8_t* sA, 
           dr.next(kStages);
         }
         st.next(kStages);
+        if (++turn == kProducers) turn = 0;
         psrc += (size_t)r8 * 128;
-        if (!waited && w + i + 1 == min(nsteps, min(kStages, win))) {
+        if (!waited && w + i + 1 == min(nsteps, kStages)) {
           // the first stages' G is on its way; their P once the weights are there
           griddep_wait();
           waited = true;
-          for (int x = 0; x <= w + i; ++x) load_p(x, p_block(a, job.hl, job.prow, r8, job.it0 + x));
+          if (lane == 0 && pbytes)
+            for (int x = part; x <= w + i; x += kProducers)
+              bulk_load(sA + x * kABytes, p_block(a, job.hl, job.prow, r8, job.it0 + x), pbytes, &b.full[x]);
         }
       }
       page = page2;
     }
+    if (!told && lane == 0) mbar_arrive(&b.near_end);  // (none of the last steps was this warp's)
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.job_empty[jr.stage]);
     jr.next(kJobSlots);
   }
   if (!waited) griddep_wait();
-  // copies still in flight must land before the CTA exits (a pair's leader waits for both)
+  // copies still in flight must land before the CTA exits
   for (int s = 0; s < kStages; ++s) {
-    if ((!kPair || rank == 0) && (issued_mask >> s & 1)) mbar_wait(&b.full[s], issued_phase >> s & 1, a.timeout_ns);
+    if (issued_mask >> s & 1) mbar_wait(&b.full[s], issued_phase >> s & 1, a.timeout_ns);
     if (issued_mask >> (s + 8) & 1) mbar_wait(&b.dirty_full[s], issued_phase >> (s + 8) & 1, a.timeout_ns);
   }
 }
 
-// Warp 1, one thread (a pair's leader's): issues the products.
-template <bool kPair>
+// Warp 1, one thread: issues the products.
 __device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_t* sA, const uint8_t* sB, uint32_t tmem) {
   // Descriptors stay in registers: stages and k-steps differ in the start address alone,
   // whose field (bytes / 16, shared memory < 256 KB) never carries.  G lies as [box of br
   // keys][64-column chunk][key][128 bytes]: 64-column chunks are br * 128 bytes apart, 8-key
   // groups 1024 (or, in boxes of 8 keys, a whole box).
-  constexpr int kStages = Cfg<kPair>::kStages, kChunks = Cfg<kPair>::kChunks;
-  constexpr uint32_t kBBytes = Cfg<kPair>::kBBytes;
   const int br = a.box_rows;
   const uint64_t pd0 = smem_desc(smem_u32(sA), 16, 1024, kSwizzle128B);
-  const uint64_t gd0 = smem_desc(smem_u32(sB), br * 128, br == 8 ? kChunks * 1024u : 1024u, kSwizzle128B);
+  const uint64_t gd0 = smem_desc(smem_u32(sB), br * 128, br == 8 ? 4096u : 1024u, kSwizzle128B);
   uint32_t koff[4];
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
     const int key = kk * 16, box = key / br;
-    koff[kk] = (uint32_t)(box * (kChunks * br * 128) + (key - box * br) * 128) >> 4;
+    koff[kk] = (uint32_t)(box * (4 * br * 128) + (key - box * br) * 128) >> 4;
   }
   Ring st, jr, acc, dr;
   bool ok = true;
@@ -705,29 +660,21 @@ __device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_
     if (!(ok = wait_bar(&b.job_full[jr.stage], jr.phase, b, a))) break;
     const Job job = b.job[jr.stage];
     if (job.b < 0) break;
-    const uint32_t idesc =
-        kPair ? idesc_bf16_f32(2 * kM, kN, false, true) : idesc_bf16_f32(kM, (job_cols(a, job) + 15) & ~15, false, true);
+    const int vis = job.pos0 + job.rows;
+    const uint32_t idesc = idesc_bf16_f32(kM, (job_cols(a, job) + 15) & ~15, false, true);
     const uint32_t d = tmem + acc.stage * kN;
     if (!(ok = wait_bar(&b.acc_empty[acc.stage], acc.phase ^ 1, b, a))) break;
     tc_fence_after_nc();
     uint32_t accum = 0;  // of a step's first k-step
-    auto product = [&](uint64_t pd, uint64_t gd, int kk) {
-      if (kPair) mma_bf16_ss_pair(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
-      else mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (kPair) mma_commit_pair(bar);
-      else mma_commit_nc(bar);
-    };
     int it = job.it0;
-    for (const int e = min(job.dirty, job.it1); it < e; ++it) {
+    for (const int e = min(first_dirty(job.pos0), job.it1); it < e; ++it) {
       if (!(ok = wait_bar(&b.full[st.stage], st.phase, b, a))) break;
       tc_fence_after_nc();
       const uint64_t pd = pd0 + (uint64_t)(st.stage * (kABytes >> 4)), gd = gd0 + (uint64_t)(st.stage * (kBBytes >> 4));
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) product(pd, gd, kk);
+      for (int kk = 0; kk < 4; ++kk) mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
       accum = 1;
-      commit(&b.empty[st.stage]);
+      mma_commit_nc(&b.empty[st.stage]);
       st.next(kStages);
     }
     for (; ok && it < job.it1; ++it) {
@@ -736,30 +683,26 @@ __device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_
       dr.next(kStages);
       tc_fence_after_nc();
       const uint64_t pd = pd0 + (uint64_t)(st.stage * (kABytes >> 4)), gd = gd0 + (uint64_t)(st.stage * (kBBytes >> 4));
-      const int keys = job.end - it * kK;
+      const int keys = vis - it * kK;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (kk * 16 < keys) product(pd, gd, kk);
+        if (kk * 16 < keys) mma_bf16_ss_nc(d, pd + kk * 2, gd + koff[kk], idesc, accum | (uint32_t)(kk > 0));
       accum = 1;
-      commit(&b.empty[st.stage]);
+      mma_commit_nc(&b.empty[st.stage]);
       st.next(kStages);
     }
     if (!ok) break;
-    commit(&b.acc_full[acc.stage]);
+    mma_commit(&b.acc_full[acc.stage]);
     mbar_arrive(&b.job_empty[jr.stage]);
     acc.next(2);
     jr.next(kJobSlots);
   }
-  if (kPair) mma_commit_pair(&b.drain);
-  else mma_commit(&b.drain);
+  mma_commit(&b.drain);
   mbar_wait(&b.drain, 0, a.timeout_ns);
 }
 
-// Warps 6-9: dirty steps.
-template <bool kPair>
-__device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, int t, int lane, int rank) {
-  constexpr int kStages = Cfg<kPair>::kStages, kChunks = Cfg<kPair>::kChunks;
-  constexpr uint32_t kBBytes = Cfg<kPair>::kBBytes;
+// Warps 12-15: dirty steps.
+__device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, int t, int lane) {
   const int br = a.box_rows;
   Ring jr, dr;
   int step = 0;  // steps before the job, modulo the stages
@@ -769,25 +712,25 @@ __device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, in
     if (!(ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a))) break;
     const Job job = b.job[jr.stage];
     if (job.b < 0) break;
-    const int nbc = min(kChunks, max(0, (a.m_h - job.strip * kN - rank * Cfg<kPair>::kCols + 63) / 64));
-    for (int it = max(job.it0, job.dirty); it < job.it1; ++it) {
+    const int nbc = (job_cols(a, job) + 63) / 64;
+    for (int it = max(job.it0, first_dirty(job.pos0)); it < job.it1; ++it) {
       if (!(ok = warp_wait(&b.dirty_full[dr.stage], dr.phase, b, a))) break;
-      const int keys = min(kK, max(0, job.end - it * kK)), rows = (keys + 15) & ~15;
-      const int lo = it == job.dirty ? max(0, job.lo) : 0;  // rows before are seen by all
+      const int keys = min(kK, max(0, job.pos0 + job.rows - it * kK)), rows = (keys + 15) & ~15;
+      const int lo = max(0, job.pos0 + 1 - it * kK);  // rows before are seen by all
       const uint32_t s0 = smem_u32(sB + ((step + it - job.it0) % kStages) * kBBytes);
       // rows t / 8 + 16 k: their 16-byte pieces are on their way before the first is looked
       // at (this stands between a step's copy and its product)
       bool found = false;
 #pragma unroll
       for (int k2 = 0; k2 < 2; ++k2) {
-        uint4 x[2][kChunks];
+        uint4 x[2][4];
         uint32_t at[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = t / 8 + 16 * (2 * k2 + k), box = r / br;
-          at[k] = s0 + box * (kChunks * br * 128) + (r - box * br) * 128 + (t & 7) * 16;
+          at[k] = s0 + box * (4 * br * 128) + (r - box * br) * 128 + (t & 7) * 16;
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
+          for (int c = 0; c < 4; ++c)
             x[k][c] = c < nbc && r >= lo && r < keys ? ld_shared_v4(at[k] + c * br * 128) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
@@ -795,29 +738,26 @@ __device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, in
           const int r = t / 8 + 16 * (2 * k2 + k);
           uint32_t any = 0;
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
+          for (int c = 0; c < 4; ++c)
             any |= non_finite(x[k][c].x) | non_finite(x[k][c].y) | non_finite(x[k][c].z) | non_finite(x[k][c].w);
           if (r >= keys && r < rows) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) st_shared_v4(at[k] + c * br * 128, make_uint4(0, 0, 0, 0));
+            for (int c = 0; c < 4; ++c) st_shared_v4(at[k] + c * br * 128, make_uint4(0, 0, 0, 0));
           } else if (any) {
             found = true;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
+            for (int c = 0; c < 4; ++c)
               st_shared_v4(at[k] + c * br * 128, make_uint4(drop(x[k][c].x), drop(x[k][c].y), drop(x[k][c].z), drop(x[k][c].w)));
           }
         }
       }
       if (found) {
-        *(volatile int*)&b.poison[n & 7] = 1;
-        if (kPair) st_cluster(cluster_addr(&b.poison[n & 7], 1 - rank), 1);
+        *(volatile int*)&b.poison[0][n & 7] = 1;
+        *(volatile int*)&b.poison[1][n & 7] = 1;
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if (kPair) mbar_arrive_cluster(cluster_addr(&b.clean[dr.stage], 0));
-        else mbar_arrive(&b.clean[dr.stage]);
-      }
+      if (lane == 0) mbar_arrive(&b.clean[dr.stage]);
       dr.next(kStages);
     }
     if (!ok) break;
@@ -829,40 +769,44 @@ __device__ __forceinline__ void scrub(const TcArgs& a, GBars& b, uint8_t* sB, in
   }
 }
 
-// Warps 2-5: accumulators to outputs, or to partial sums.
-template <bool kPair>
+// Warps 4-11: accumulators to outputs, or to partial sums.  Two halves of four warps take 128
+// columns each and know nothing of each other: a load waits for thousands of cycles behind
+// the copies, and twice the warps have twice the loads on their way.
 __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t* sTurn, uint32_t tmem, int warp, int lane) {
+  const int g = (warp - kEpi0) / 4, bar = 1 + g;
   const int quarter = warp & 3, r = quarter * 32 + lane;  // TMEM lane, the tile's row
-  const bool lead = warp == kEpi0 && lane == 0;
+  const bool lead = quarter == 0 && lane == 0;
+  constexpr int kHalfN = kN / 2;
   const size_t width = (size_t)a.H * a.m_pitch;
   Ring jr, acc;
   for (int n = 0;; ++n) {
     bool ok = warp_wait(&b.job_full[jr.stage], jr.phase, b, a);
     const Job job = b.job[jr.stage];
-    const int cols = ok && job.b >= 0 ? job_cols(a, job) : 0;
+    const bool is_job = ok && job.b >= 0;
+    const int cols = is_job ? min(kHalfN, max(0, job_cols(a, job) - g * kHalfN)) : 0;
     // v's rows of the tile come into L2 while the products run
     if (a.v && cols > 0 && r < job.rows) {
       const char* vp = reinterpret_cast<const char*>(a.v + (size_t)(job.row0 + r) * a.v_pitch +
-                                                     (size_t)(a.h0 + job.hl) * a.m_pitch + job.strip * kN);
+                                                     (size_t)(a.h0 + job.hl) * a.m_pitch + job.strip * kN + g * kHalfN);
       for (int x = 0; x < cols * 2; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + x));
     }
-    if (cols > 0) ok = warp_wait(&b.acc_full[acc.stage], acc.phase, b, a);
-    if (!named_bar_and(1, 128, ok)) break;
+    if (is_job) ok = warp_wait(&b.acc_full[acc.stage], acc.phase, b, a);
+    if (!named_bar_and(bar, 128, ok)) break;
     if (job.b < 0) break;
     tc_fence_after();
-    const bool poison = *(volatile int*)&b.poison[n & 7] != 0;
+    const bool poison = *(volatile int*)&b.poison[g][n & 7] != 0;
     const int vis = job.pos0 + job.rows, head = a.h0 + job.hl, pos = job.pos0 + r, r8 = up8(job.rows);
-    const uint32_t trow = tmem + acc.stage * kN + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t trow = tmem + acc.stage * kN + g * kHalfN + ((uint32_t)(quarter * 32) << 16);
     const bool warp_rows = quarter * 32 < job.rows;  // else this warp's rows are not there
     const bool live = r < job.rows;
-    const size_t tkey = ((size_t)job.hl * a.strips + job.strip) * a.tiles + job.tile;
-    const size_t col0 = (size_t)head * a.m_pitch + job.strip * kN;
+    const size_t tkey = (((size_t)job.hl * a.strips + job.strip) * a.tiles + job.tile) * 2 + g;
+    const size_t col0 = (size_t)head * a.m_pitch + job.strip * kN + g * kHalfN;
     const float* den = a.den + ((size_t)job.hl * a.rows_tot + job.prow) * a.spans;
     const int ns = vis <= 0 ? 0 : (vis + a.span_keys - 1) / a.span_keys;
     const float null_w = a.null_bias ? expf(a.null_bias[head] - head_tau(a.tau, a.s, head, a.p.err, kKernPaged)) : 0.f;
 
     // The keys whose non-finite gates the scrub warps took out of this job's product.
-    const int bad0 = max(job.dirty * kK + job.lo, job.it0 * kK), bad1 = min(vis, job.it1 * kK);
+    const int bad0 = max(job.pos0 + 1, job.it0 * kK), bad1 = min(vis, job.it1 * kK);
     // The accumulator's 32 columns from c0 on of row r, with what was taken out put back
     // where the row sees it.
     auto fetch = [&](int c0, float (&y)[32]) {
@@ -894,20 +838,20 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
       if (lead) {
         const int sl = atomicAdd(a.next + 1, 1);
         a.slot[tkey * a.nc_cap + job.c] = sl;
-        b.last = sl;
+        b.last[g] = sl;
       }
-      named_bar_sync(1, 128);
-      return b.last;
+      named_bar_sync(bar, 128);
+      return b.last[g];
     };
     auto is_last = [&]() -> bool {
       __threadfence();
-      named_bar_sync(1, 128);
+      named_bar_sync(bar, 128);
       if (lead) {
-        b.last = atomicAdd(a.done + tkey, 1) == job.nc - 1;
+        b.last[g] = atomicAdd(a.done + tkey, 1) == job.nc - 1;
         __threadfence();
       }
-      named_bar_sync(1, 128);
-      return b.last != 0;
+      named_bar_sync(bar, 128);
+      return b.last[g] != 0;
     };
     // slots of kSlotRegs ranges, looked up side by side
     constexpr int kSlotRegs = 4;
@@ -917,34 +861,22 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
       for (int k = 0; k < kSlotRegs; ++k) sl_reg[k] = k0 + k < job.nc ? __ldcg(a.slot + tkey * a.nc_cap + k0 + k) : -1;
     };
 
-    if (job.rows == 0) {
-      // ---- a pair's second CTA without rows
-    } else if (job.rows <= kFewRows) {
+    if (job.rows <= kFewRows) {
       // ---- few rows: the accumulator's rows go to shared memory, then this thread takes
-      // columns 2 t and 2 t + 1 of each
-      const int t = threadIdx.x - kEpi0 * 32, c = 2 * t;
-      float* turn = reinterpret_cast<float*>(sTurn);
-      auto at = [](int row, int col) { return row * kN + ((((col >> 2) ^ (row & 7)) << 2) | (col & 3)); };
+      // column t of each
+      const int t = (threadIdx.x - kEpi0 * 32) & 127, c = t;
+      float* turn = reinterpret_cast<float*>(sTurn) + g * (kFewRows * kHalfN);
+      auto at = [](int row, int col) { return row * kHalfN + ((((col >> 2) ^ (row & 7)) << 2) | (col & 3)); };
       // v and the denominators' parts arrive meanwhile
-      float2 vv[kFewRows];
-      float dn[kFewRows];
+      float vv[kFewRows], dn[kFewRows];
       auto ask = [&]() {
 #pragma unroll
         for (int i = 0; i < kFewRows; ++i) {
           dn[i] = 0.f;
-          vv[i] = make_float2(1.f, 1.f);
+          vv[i] = 1.f;
           if (i < job.rows && job.pos0 + i >= 0) {
             for (int k = lane; k < ns; k += 32) dn[i] += __ldcg(den + (size_t)i * a.spans + k);
-            if (a.v && c < cols) {
-              const __nv_bfloat16* vp = a.v + (size_t)(job.row0 + i) * a.v_pitch + col0 + c;
-              if (a.v_vec) {
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(vp);
-                vv[i] = make_float2(bf16lo(x), bf16hi(x));
-              } else {
-                vv[i].x = __bfloat162float(vp[0]);
-                if (c + 1 < cols) vv[i].y = __bfloat162float(vp[1]);
-              }
-            }
+            if (a.v && c < cols) vv[i] = __bfloat162float(a.v[(size_t)(job.row0 + i) * a.v_pitch + col0 + c]);
           }
         }
       };
@@ -961,35 +893,31 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
           }
         }
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(bar, 128);
       bool finish = true;
       if (job.nc > 1) {
         const int sl = take_slot();
-        float* dst = a.part + (size_t)sl * (kN * a.r8cap);
+        float* dst = a.part + (size_t)sl * (kHalfN * a.r8cap);
         if ((unsigned)sl < (unsigned)a.n_slots) {
-          for (int i = 0; i < job.rows; ++i)
-            __stcg(reinterpret_cast<float2*>(dst + i * kN + c), *reinterpret_cast<const float2*>(turn + at(i, c)));
+          for (int i = 0; i < job.rows; ++i) __stcg(dst + i * kHalfN + c, turn[at(i, c)]);
         }
         finish = is_last();
         if (finish) ask();
       }
       if (finish) {
-        float2 y[kFewRows];
+        float y[kFewRows];
 #pragma unroll
-        for (int i = 0; i < kFewRows; ++i)
-          y[i] = job.nc == 1 && i < job.rows ? *reinterpret_cast<const float2*>(turn + at(i, c)) : make_float2(0.f, 0.f);
+        for (int i = 0; i < kFewRows; ++i) y[i] = job.nc == 1 && i < job.rows ? turn[at(i, c)] : 0.f;
         for (int k0 = 0; job.nc > 1 && k0 < job.nc; k0 += kSlotRegs) {
           slots(k0);
 #pragma unroll
           for (int k = 0; k < kSlotRegs; ++k) {
             if ((unsigned)sl_reg[k] >= (unsigned)a.n_slots) continue;
-            const float* src = a.part + (size_t)sl_reg[k] * (kN * a.r8cap) + c;
+            const float* src = a.part + (size_t)sl_reg[k] * (kHalfN * a.r8cap) + c;
 #pragma unroll
             for (int i = 0; i < kFewRows; ++i) {
               if (i >= job.rows) break;
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(src + i * kN));
-              y[i].x += x.x;
-              y[i].y += x.y;
+              y[i] += __ldcg(src + i * kHalfN);
             }
           }
         }
@@ -1000,17 +928,15 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
           for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
           const int ps = job.pos0 + i;
           const float inv = 1.f / (d + (float)(ps + 1) * null_w);
-          // pairs: the last one may run into the pitch's padding
           if (c < cols)
-            *reinterpret_cast<uint32_t*>(a.out + (size_t)(job.row0 + i) * width + col0 + c) =
-                ps >= 0 ? pack_bf16x2(y[i].x * inv * vv[i].x, y[i].y * inv * vv[i].y) : 0u;
+            a.out[(size_t)(job.row0 + i) * width + col0 + c] = __float2bfloat16_rn(ps >= 0 ? y[i] * inv * vv[i] : 0.f);
         }
       }
     } else {
       bool finish = true;
       if (job.nc > 1) {
         const int sl = take_slot();
-        float* dst = a.part + (size_t)sl * (kN * a.r8cap);
+        float* dst = a.part + (size_t)sl * (kHalfN * a.r8cap);
         if (warp_rows && (unsigned)sl < (unsigned)a.n_slots) {
           for (int c0 = 0; c0 < cols; c0 += 32) {
             float y[32];
@@ -1026,31 +952,22 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
         finish = is_last();
       }
       if (finish && warp_rows) {
-        uint8_t* turn = sTurn + quarter * 4096;
+        uint8_t* turn = sTurn + (warp - kEpi0) * 4096;
         const uint32_t t_s = smem_u32(turn);
         // in row order this lane takes 4 columns of rows quarter * 32 + lane / 8 + 4 k
         const int lr = quarter * 32 + lane / 8, lc = (lane & 7) * 4;
-        const bool all_rows = quarter * 32 + 32 <= job.rows && job.pos0 >= 0;
-        uint2 vn[8];  // v of the next 32 columns
-        auto load_v = [&](int c) {
+        // v of 4 columns of such a row; rows and columns that are not there read ones that are
+        // (no branch, so that the eight loads of a pass go out together)
+        auto load_v = [&](int k, int c) -> uint2 {
+          const int rr = min(lr + 4 * k, job.rows - 1), cc = min(c, (cols - 1) & ~3);
+          const __nv_bfloat16* vp = a.v + (size_t)(job.row0 + rr) * a.v_pitch + col0 + cc;
+          if (a.v_vec) return *reinterpret_cast<const uint2*>(vp);
+          uint32_t w[2];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            vn[k] = make_uint2(0x3f803f80u, 0x3f803f80u);  // ones
-            const int rr = lr + 4 * k;
-            if (a.v && c < cols && (all_rows || (rr < job.rows && job.pos0 + rr >= 0))) {
-              const __nv_bfloat16* vp = a.v + (size_t)(job.row0 + rr) * a.v_pitch + col0 + c;
-              if (a.v_vec) {
-                vn[k] = *reinterpret_cast<const uint2*>(vp);
-              } else {
-                float e[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) e[q] = c + q < cols ? __bfloat162float(vp[q]) : 0.f;
-                vn[k] = make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
-              }
-            }
-          }
+          for (int q = 0; q < 2; ++q)
+            w[q] = pack_bf16x2(__bfloat162float(vp[2 * q]), cc + 2 * q + 1 < cols ? __bfloat162float(vp[2 * q + 1]) : 0.f);
+          return make_uint2(w[0], w[1]);
         };
-        load_v(lc);
         float inv = 0.f;
         if (live && pos >= 0) {
           float d = 0.f;
@@ -1064,9 +981,10 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
         for (int c0 = 0; c0 < cols; c0 += 32) {
           const int c = c0 + lc;
           uint2 vr[8];
+          if (a.v) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) vr[k] = vn[k];
-          load_v(c + 32);
+            for (int k = 0; k < 8; ++k) vr[k] = load_v(k, c);
+          }
           float y[32];
           if (job.nc == 1) {
             fetch(c0, y);
@@ -1078,7 +996,7 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
 #pragma unroll
               for (int k = 0; k < kSlotRegs; ++k) {
                 if (!live || (unsigned)sl_reg[k] >= (unsigned)a.n_slots) continue;
-                const float4* src = reinterpret_cast<const float4*>(a.part + (size_t)sl_reg[k] * (kN * a.r8cap));
+                const float4* src = reinterpret_cast<const float4*>(a.part + (size_t)sl_reg[k] * (kHalfN * a.r8cap));
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                   const float4 x = __ldcg(src + (size_t)(c0 / 4 + u) * a.r8cap + r);
@@ -1102,24 +1020,26 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
           for (int k = 0; k < 8; ++k) {
             const int rw = lane / 8 + 4 * k, rr = quarter * 32 + rw;
             const uint4 x = ld_shared_v4(t_s + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
+            float z[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+            if (a.v && job.pos0 + rr >= 0) {
+              z[0] *= bf16lo(vr[k].x); z[1] *= bf16hi(vr[k].x); z[2] *= bf16lo(vr[k].y); z[3] *= bf16hi(vr[k].y);
+            }
             // four columns: the last ones may run into the pitch's padding
             if (rr < job.rows && c < cols)
               *reinterpret_cast<uint2*>(a.out + (size_t)(job.row0 + rr) * width + col0 + c) =
-                  make_uint2(pack_bf16x2(__uint_as_float(x.x) * bf16lo(vr[k].x), __uint_as_float(x.y) * bf16hi(vr[k].x)),
-                             pack_bf16x2(__uint_as_float(x.z) * bf16lo(vr[k].y), __uint_as_float(x.w) * bf16hi(vr[k].y)));
+                  make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
           }
         }
       }
     }
-    if (poison) {  // all four warps have read it
-      named_bar_sync(1, 128);
-      if (lead) b.poison[n & 7] = 0;
+    if (poison) {  // (the same for the half's four warps, which have all read it)
+      named_bar_sync(bar, 128);
+      if (lead) b.poison[g][n & 7] = 0;
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      if (kPair) mbar_arrive_cluster(cluster_addr(&b.acc_empty[acc.stage], 0));
-      else mbar_arrive(&b.acc_empty[acc.stage]);
+      mbar_arrive(&b.acc_empty[acc.stage]);
       mbar_arrive(&b.job_empty[jr.stage]);
     }
     acc.next(2);
@@ -1127,76 +1047,62 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
   }
 }
 
-template <bool kPair>
 __global__ void __launch_bounds__(kGThreads, 1)
-    paged_gates_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG4,
-                       const __grid_constant__ CUtensorMap tmP, const TcArgs a) {
-  constexpr int kStages = Cfg<kPair>::kStages;
+    paged_gates_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG4, const TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = base;
   uint8_t* sB = base + kStages * kABytes;
-  uint8_t* sTurn = base + kRingBytes;
+  uint8_t* sTurn = sB + kStages * kBBytes;
   GBars& b = *reinterpret_cast<GBars*>(sTurn + kTurnBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int rank = kPair ? (int)cluster_rank() : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&b.full[s], 1);
       mbar_init(&b.empty[s], 1);
       mbar_init(&b.dirty_full[s], 1);
-      mbar_init(&b.clean[s], kPair ? 8 : 4);  // scrub warps
+      mbar_init(&b.clean[s], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.acc_full[i], 1);
-      mbar_init(&b.acc_empty[i], kPair ? 8 : 4);  // epilogue warps
+      mbar_init(&b.acc_empty[i], 8);
     }
     for (int i = 0; i < kJobSlots; ++i) {
       mbar_init(&b.job_full[i], 1);
-      // producer, 4 epilogue warps, 4 scrub warps and the MMA issuer (a pair's leader's)
-      mbar_init(&b.job_empty[i], rank == 0 ? 10 : 9);
+      mbar_init(&b.job_empty[i], kProducers + 1 + 8 + 4);  // producers, MMA issuer, epilogue and scrub warps
     }
-    mbar_init(&b.near_end, 1);
+    mbar_init(&b.near_end, kProducers);
     mbar_init(&b.drain, 1);
     b.abort = 0;
-    for (int i = 0; i < 8; ++i) b.poison[i] = 0;
+    for (int i = 0; i < 16; ++i) (&b.poison[0][0])[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    if (kPair) {
-      tmem_alloc_pair(&b.tmem_base, 512);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(&b.tmem_base, 512);
-      tmem_relinquish();
-    }
+    tmem_alloc(&b.tmem_base, 512);
+    tmem_relinquish();
   }
   tc_fence_before();
-  if (kPair) cluster_sync();  // the other CTA's barriers too
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = b.tmem_base;
 
-  if (warp == 0) {
-    produce<kPair>(a, b, sA, sB, &tmG, &tmG4, &tmP, lane, rank);
+  if (warp == 0 || warp == 3) {
+    produce(a, b, sA, sB, &tmG, &tmG4, warp == 0 ? 0 : 1, lane);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) multiply<kPair>(a, b, sA, sB, tmem);
+    if (lane == 0) multiply(a, b, sA, sB, tmem);
+  } else if (warp == kSched) {
+    schedule(a, b, lane);
   } else if (warp < kScrub0) {
-    finish_tiles<kPair>(a, b, sTurn, tmem, warp, lane);
-  } else if (warp < kSched) {
-    scrub<kPair>(a, b, sB, threadIdx.x - kScrub0 * 32, lane, rank);
+    finish_tiles(a, b, sTurn, tmem, warp, lane);
   } else {
-    schedule<kPair>(a, b, lane, rank);
+    scrub(a, b, sB, threadIdx.x - kScrub0 * 32, lane);
   }
-  __syncwarp();
   tc_fence_before();
-  if (kPair) cluster_sync();  // nothing of this CTA is still to be signalled or read by the other
-  else __syncthreads();
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    if (kPair) tmem_dealloc_pair(tmem, 512);
-    else tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -1218,7 +1124,6 @@ int box_rows(int page_size) {
 }
 
 struct TcPlan {
-  int pair;
   int rows_tot, key_blocks, span_keys, spans, strips, tiles, r8cap, min_steps, jobs_per_sm, nc_cap, n_slots, heads, grid;
   size_t P, den, part, slot, done, next, total;
 };
@@ -1226,7 +1131,6 @@ struct TcPlan {
 TcPlan tc_plan(const PagedCall& c) {
   TcPlan l;
   const int sms = num_sms();
-  l.pair = c.p.max_new > kM;  // some sequence has two row tiles
   l.rows_tot = up8(c.p.N) + 8 * c.p.B;
   l.key_blocks = ceil_div(c.p.max_len, kK);
   // at most 32 spans of whole 128-key blocks (their sums are added once per strip)
@@ -1241,18 +1145,18 @@ TcPlan tc_plan(const PagedCall& c) {
   l.min_steps = l.r8cap <= kFewRows ? 3 : 8;
   l.jobs_per_sm = l.r8cap <= kFewRows ? kJobsPerSm : 2;
   l.nc_cap = ceil_div(l.key_blocks, l.min_steps);
-  l.grid = l.pair ? sms & ~1 : sms;
-  // a tile that is cut has at most twice as many ranges as whole ranges fit in it
-  l.n_slots = 2 * kJobsPerSm * sms;
+  l.grid = sms;
+  // a tile that is cut has at most twice as many ranges as whole ranges fit in it; two halves
+  l.n_slots = 2 * 2 * kJobsPerSm * sms;
   // heads of a pass: as many as keep P within 2 GB
   const size_t per_head = (size_t)l.rows_tot * l.key_blocks * 128;
   const size_t fit = (size_t(2) << 30) / per_head;
   l.heads = (int)(fit < 1 ? 1 : fit > (size_t)c.H ? (size_t)c.H : fit);
-  const size_t tk = (size_t)l.heads * l.strips * l.tiles;
+  const size_t tk = (size_t)l.heads * l.strips * l.tiles * 2;
   l.P = 0;
   l.den = l.P + align256(per_head * l.heads);
   l.part = l.den + align256((size_t)l.heads * l.rows_tot * l.spans * 4);
-  l.slot = l.part + align256((size_t)l.n_slots * kN * l.r8cap * 4);
+  l.slot = l.part + align256((size_t)l.n_slots * (kN / 2) * l.r8cap * 4);
   l.done = l.slot + align256(tk * l.nc_cap * 4);
   l.next = l.done + align256(tk * 4);
   l.total = l.next + 256;
@@ -1289,7 +1193,6 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   a.rows_tot = l.rows_tot; a.key_blocks = l.key_blocks; a.span_keys = l.span_keys; a.spans = l.spans;
   a.strips = l.strips; a.tiles = l.tiles; a.r8cap = l.r8cap; a.min_steps = l.min_steps; a.jobs_per_sm = l.jobs_per_sm; a.nc_cap = l.nc_cap; a.n_slots = l.n_slots;
   a.box_rows = box_rows(c.p.page_size);
-  a.pair = l.pair;
   a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
   a.v_vec = c.v && (reinterpret_cast<uintptr_t>(c.v) & 15u) == 0 && c.v_pitch % 8 == 0;
   a.q = static_cast<const __nv_bfloat16*>(c.q); a.v = static_cast<const __nv_bfloat16*>(c.v);
@@ -1304,18 +1207,15 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   a.next = reinterpret_cast<int*>(base + l.next);
   a.timeout_ns = kTimeoutNs;
 
-  CUtensorMap mG, mG4, mP;
+  CUtensorMap mG, mG4;
   cudaError_t e = make_tmap_4d_heads(&mG, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 64);
-  mG4 = mP = mG;  // (a head's whole columns of a CTA; a pair's P)
-  const int cols = l.pair ? Cfg<true>::kCols : Cfg<false>::kCols;
-  if (e == cudaSuccess && c.m_h >= cols)
-    e = make_tmap_5d_chunks(&mG4, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, cols / 64);
-  if (e == cudaSuccess && l.pair) e = make_tmap_2d_plain(&mP, a.P, (uint64_t)l.rows_tot * l.key_blocks * l.heads, 64, 64, kM, 64);
+  mG4 = mG;  // used only where a head holds a whole strip
+  if (e == cudaSuccess && c.m_h >= kN)
+    e = make_tmap_5d_chunks(&mG4, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 4);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(paged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(l.pair ? paged_gates_kernel<true> : paged_gates_kernel<false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
+    e = cudaFuncSetAttribute(paged_gates_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
   if (e != cudaSuccess) return e;
   for (a.h0 = 0; a.h0 < c.H; a.h0 += l.heads) {
     a.heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
@@ -1329,16 +1229,12 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
     cfg.blockDim = dim3(kGThreads);
     cfg.dynamicSmemBytes = kGSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = l.pair ? 2 : 1;
-    e = l.pair ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<true>, mG, mG4, mP, a)
-               : cudaLaunchKernelEx(&cfg, paged_gates_kernel<false>, mG, mG4, mP, a);
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_gates_kernel, mG, mG4, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -13,10 +13,6 @@ namespace tg {
 cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch_elems,
                          uint32_t box_rows, uint32_t box_cols);
 
-// The same without a swizzle: boxes are copied as they lie.
-cudaError_t make_tmap_2d_plain(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch_elems,
-                               uint32_t box_rows, uint32_t box_cols);
-
 // Same over a [batch, rows, cols] tensor (row pitch cols, batch pitch rows*cols),
 // box [1, box_rows, box_cols]; out-of-range rows of one batch read as zero
 // instead of running into the next batch.

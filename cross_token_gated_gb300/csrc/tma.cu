@@ -33,13 +33,12 @@ CUtensorMapSwizzle swizzle_for(uint32_t inner_bytes) {
 }
 
 cudaError_t encode(CUtensorMap* map, const void* base, cuuint32_t rank, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box, bool swizzle = true) {
+                   const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn enc = encoder();
   if (!enc) return cudaErrorNotSupported;
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle ? swizzle_for(box[0] * 2) : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_for(box[0] * 2), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -52,14 +51,6 @@ cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint
   cuuint64_t strides[1] = {pitch_elems * 2};
   cuuint32_t box[2] = {box_cols, box_rows};
   return encode(map, base, 2, dims, strides, box);
-}
-
-cudaError_t make_tmap_2d_plain(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch_elems,
-                               uint32_t box_rows, uint32_t box_cols) {
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {pitch_elems * 2};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  return encode(map, base, 2, dims, strides, box, false);
 }
 
 cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t cols,
