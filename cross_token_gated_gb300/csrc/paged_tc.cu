@@ -790,6 +790,32 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
                                                      (size_t)(a.h0 + job.hl) * a.m_pitch + job.strip * kN + g * kHalfN);
       for (int x = 0; x < cols * 2; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + x));
     }
+    // In row order this lane takes 4 columns of rows quarter * 32 + lane / 8 + 4 k.  v of the
+    // first 64 columns is on its way before the products are done, that of the others while
+    // the first are finished.
+    const int lr = quarter * 32 + lane / 8, lc = (lane & 7) * 4;
+    const bool turned = is_job && job.rows > kFewRows && quarter * 32 < job.rows && cols > 0;
+    uint2 vr[2][8];
+    // v of such a row's columns c .. c + 3; rows and columns that are not there read ones that
+    // are (no branch, so that the loads go out together)
+    auto load_v = [&](int k, int c) -> uint2 {
+      const int rr = min(lr + 4 * k, job.rows - 1), cc = min(c, (cols - 1) & ~3);
+      const __nv_bfloat16* vp = a.v + (size_t)(job.row0 + rr) * a.v_pitch + (size_t)(a.h0 + job.hl) * a.m_pitch +
+                                job.strip * kN + g * kHalfN + cc;
+      if (a.v_vec) return *reinterpret_cast<const uint2*>(vp);
+      uint32_t w[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        w[q] = pack_bf16x2(__bfloat162float(vp[2 * q]), cc + 2 * q + 1 < cols ? __bfloat162float(vp[2 * q + 1]) : 0.f);
+      return make_uint2(w[0], w[1]);
+    };
+    auto load_v64 = [&](int c0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) vr[h][k] = load_v(k, c0 + h * 32 + lc);
+    };
+    if (a.v && turned) load_v64(0);
     if (is_job) ok = warp_wait(&b.acc_full[acc.stage], acc.phase, b, a);
     if (!named_bar_and(bar, 128, ok)) break;
     if (job.b < 0) break;
@@ -954,20 +980,6 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
       if (finish && warp_rows) {
         uint8_t* turn = sTurn + (warp - kEpi0) * 4096;
         const uint32_t t_s = smem_u32(turn);
-        // in row order this lane takes 4 columns of rows quarter * 32 + lane / 8 + 4 k
-        const int lr = quarter * 32 + lane / 8, lc = (lane & 7) * 4;
-        // v of 4 columns of such a row; rows and columns that are not there read ones that are
-        // (no branch, so that the eight loads of a pass go out together)
-        auto load_v = [&](int k, int c) -> uint2 {
-          const int rr = min(lr + 4 * k, job.rows - 1), cc = min(c, (cols - 1) & ~3);
-          const __nv_bfloat16* vp = a.v + (size_t)(job.row0 + rr) * a.v_pitch + col0 + cc;
-          if (a.v_vec) return *reinterpret_cast<const uint2*>(vp);
-          uint32_t w[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            w[q] = pack_bf16x2(__bfloat162float(vp[2 * q]), cc + 2 * q + 1 < cols ? __bfloat162float(vp[2 * q + 1]) : 0.f);
-          return make_uint2(w[0], w[1]);
-        };
         float inv = 0.f;
         if (live && pos >= 0) {
           float d = 0.f;
@@ -978,13 +990,12 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
           }
           inv = 1.f / (d + (float)(pos + 1) * null_w);
         }
-        for (int c0 = 0; c0 < cols; c0 += 32) {
-          const int c = c0 + lc;
-          uint2 vr[8];
-          if (a.v) {
+        for (int c64 = 0; c64 < cols; c64 += 64) {
+          if (a.v && c64 > 0) load_v64(c64);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) vr[k] = load_v(k, c);
-          }
+          for (int h = 0; h < 2; ++h) {
+          const int c0 = c64 + h * 32, c = c0 + lc;
+          if (c0 >= cols) break;
           float y[32];
           if (job.nc == 1) {
             fetch(c0, y);
@@ -1022,12 +1033,13 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
             const uint4 x = ld_shared_v4(t_s + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
             float z[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
             if (a.v && job.pos0 + rr >= 0) {
-              z[0] *= bf16lo(vr[k].x); z[1] *= bf16hi(vr[k].x); z[2] *= bf16lo(vr[k].y); z[3] *= bf16hi(vr[k].y);
+              z[0] *= bf16lo(vr[h][k].x); z[1] *= bf16hi(vr[h][k].x); z[2] *= bf16lo(vr[h][k].y); z[3] *= bf16hi(vr[h][k].y);
             }
             // four columns: the last ones may run into the pitch's padding
             if (rr < job.rows && c < cols)
               *reinterpret_cast<uint2*>(a.out + (size_t)(job.row0 + rr) * width + col0 + c) =
                   make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+          }
           }
         }
       }
@@ -1087,15 +1099,22 @@ __global__ void __launch_bounds__(kGThreads, 1)
   tc_fence_after();
   const uint32_t tmem = b.tmem_base;
 
-  if (warp == 0 || warp == 3) {
-    produce(a, b, sA, sB, &tmG, &tmG4, warp == 0 ? 0 : 1, lane);
-  } else if (warp == 1) {
-    if (lane == 0) multiply(a, b, sA, sB, tmem);
-  } else if (warp == kSched) {
-    schedule(a, b, lane);
+  // the epilogue's two warpgroups take registers that the other two do not need (2 x 128 x 80 +
+  // 2 x 128 x 176 = the 65,536 that the block has)
+  if (warp < kEpi0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 1) {
+      if (lane == 0) multiply(a, b, sA, sB, tmem);
+    } else if (warp == kSched) {
+      schedule(a, b, lane);
+    } else {
+      produce(a, b, sA, sB, &tmG, &tmG4, warp == 0 ? 0 : 1, lane);
+    }
   } else if (warp < kScrub0) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     finish_tiles(a, b, sTurn, tmem, warp, lane);
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     scrub(a, b, sB, threadIdx.x - kScrub0 * 32, lane);
   }
   tc_fence_before();
