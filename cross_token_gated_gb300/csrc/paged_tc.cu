@@ -423,6 +423,9 @@ __device__ __forceinline__ long long seq_steps(const PagedSeq& s) {
   return (mt - 1) * before + mt * (mt - 1) + steps_of(s.len);
 }
 
+// Key ranges of a tile of u steps: as many as of `range` steps come nearest.
+__device__ __forceinline__ int ranges_of(int u, int range) { return max(1, (u + range / 2) / range); }
+
 struct Ring {
   int stage = 0;
   uint32_t phase = 0;
@@ -484,7 +487,7 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       if (w0 + lane < a.p.B) {
         ws = paged_seq(a.p, w0 + lane, false);
         wmt = (ws.n + kM - 1) / kM;
-        jobs = (long long)wmt * ((steps_of(ws.len) + range - 1) / range) * HS;
+        jobs = (long long)wmt * ranges_of(steps_of(ws.len), range) * HS;
       }
       pre = jobs;
       for (int o = 1; o < 32; o <<= 1) {
@@ -515,9 +518,9 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       job.hl = hs / a.strips;
       job.strip = hs - job.hl * a.strips;
       const int u = steps_of(job.pos0 + job.rows);
-      job.nc = (u + range - 1) / range;
-      job.it0 = job.c * range;
-      job.it1 = min(u, job.it0 + range);
+      job.nc = ranges_of(u, range);
+      job.it0 = (int)((long long)u * job.c / job.nc);  // never empty: u >= nc
+      job.it1 = (int)((long long)u * (job.c + 1) / job.nc);
       job.tile = r0 / kM + job.b + ti;
       job.prow = scratch_row(r0, job.b) + ti * kM;
       skip = job.c >= job.nc;  // a tile of the sequence that sees fewer keys
@@ -891,7 +894,8 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
       // ---- few rows: the accumulator's rows go to shared memory, then this thread takes
       // column t of each
       const int t = (threadIdx.x - kEpi0 * 32) & 127, c = t;
-      float* turn = reinterpret_cast<float*>(sTurn) + g * (kFewRows * kHalfN);
+      float* turn = reinterpret_cast<float*>(sTurn + g * (kTurnBytes / 2));  // this half's own part
+      static_assert(kFewRows * kHalfN * 4 <= kTurnBytes / 2, "a half's few rows fit its part");
       auto at = [](int row, int col) { return row * kHalfN + ((((col >> 2) ^ (row & 7)) << 2) | (col & 3)); };
       // v and the denominators' parts arrive meanwhile
       float vv[kFewRows], dn[kFewRows];
@@ -1161,11 +1165,11 @@ TcPlan tc_plan(const PagedCall& c) {
   l.r8cap = c.p.max_new < kM ? up8(c.p.max_new) : kM;
   // joining key ranges is cheap for few rows; for many it moves as much as their products
   // take, so tiles are left whole when they are about two per SM
-  l.min_steps = l.r8cap <= kFewRows ? 3 : 8;
+  l.min_steps = 8;
   l.jobs_per_sm = l.r8cap <= kFewRows ? kJobsPerSm : 2;
   l.nc_cap = ceil_div(l.key_blocks, l.min_steps);
   l.grid = sms;
-  // a tile that is cut has at most twice as many ranges as whole ranges fit in it; two halves
+  // a tile that is cut has at most 4/3 as many ranges as whole ranges fit in it; two halves
   l.n_slots = 2 * 2 * kJobsPerSm * sms;
   // heads of a pass: as many as keep P within 2 GB
   const size_t per_head = (size_t)l.rows_tot * l.key_blocks * 128;

@@ -122,19 +122,20 @@ class Batch:
 
 STEP = [(1, t) for t in (1, 2, 15, 16, 17, 64, 127, 128, 129, 300)]
 FEW = [(3, 3), (8, 8), (5, 200), (1, 1), (2, 65), (7, 130), (0, 40), (8, 513)]
+MID = [(64, 64), (33, 250), (100, 300), (9, 9), (17, 1000), (1, 700), (0, 5), (128, 128)]
 CHUNK = [(130, 130), (1, 77), (0, 0), (64, 64), (33, 250), (9, 9), (129, 400), (17, 1000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("H,d_h,m_h,pitch,page", [(2, 64, 520, 520, 16), (4, 32, 252, 256, 64), (1, 16, 1100, 1104, 8),
                                                   (2, 64, 300, 304, 128)])
-@pytest.mark.parametrize("seqs", [STEP, FEW, CHUNK], ids=["step", "few", "chunk"])
+@pytest.mark.parametrize("seqs", [STEP, FEW, MID, CHUNK], ids=["step", "few", "mid", "chunk"])
 def test_ragged(seqs, H, d_h, m_h, pitch, page, dtype):
     Batch(seqs, H, d_h, m_h, dtype, page, pitch).check()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("seqs", [STEP, FEW, CHUNK], ids=["step", "few", "chunk"])
+@pytest.mark.parametrize("seqs", [STEP, FEW, MID, CHUNK], ids=["step", "few", "mid", "chunk"])
 def test_null_tau_and_no_v(seqs, dtype):
     """The null gate, per-head temperatures up to 20 and 0, gates alone."""
     b = Batch(seqs, 3, 32, 264, dtype, 32, seed=1)
@@ -164,6 +165,22 @@ def test_long_context(dtype):
     """Long caches: spans joined from many parts; many rows against a long prefix."""
     Batch([(1, 5000), (1, 37)], 2, 64, 264, dtype, 64, seed=4).check()
     Batch([(40, 4100), (300, 2000)], 1, 64, 264, dtype, 64, seed=5).check()
+
+
+@pytest.mark.parametrize("length", [449, 700, 769, 3000, 6200, 6209])
+@pytest.mark.parametrize("n", [1, 20])
+def test_key_ranges_cut_every_way(n, length):
+    """Lengths whose steps divide evenly over the key ranges, and not: no range is empty and
+    none is lost."""
+    Batch([(n, length)], 1, 32, 72, "bf16", 32, seed=length).check()
+
+
+def test_many_sequences():
+    """More sequences than a warp's window of 32, some without new tokens, in one launch."""
+    seqs = [((i * 7) % 4, 3 + (i * 37) % 190) for i in range(150)]
+    Batch(seqs, 2, 16, 72, "bf16", 16, seed=40).check()
+    Batch(seqs[:70] + [(90, 95)] + seqs[70:], 2, 16, 72, "bf16", 16, seed=41).check()
+    Batch(seqs, 2, 16, 72, "f32", 16, seed=42).check()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
