@@ -183,6 +183,16 @@ def test_many_sequences():
     Batch(seqs, 2, 16, 72, "f32", 16, seed=42).check()
 
 
+def test_tiles_of_every_size_in_one_launch():
+    """Several jobs per SM, tiles of one row and of 128 in turn, gates over many strips: what
+    one tile leaves in shared memory must not reach the next."""
+    seqs = [(300, 300), (1, 500), (7, 20), (129, 600), (1, 64), (16, 90), (17, 80), (1, 1), (200, 260), (2, 130)]
+    b = Batch(seqs, 2, 32, 3500, "bf16", 32, 3504, seed=50)
+    first = b.check()
+    for _ in range(5):
+        assert torch.equal(b.run().double().cpu().view(b.N, 2, -1)[..., :3500], first)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_without_keys(dtype):
     """Rows at negative positions see nothing: zeros, and the others are not touched."""
