@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kKeysBlk) paged_scores_kernel(const SimtArgs<T
   __shared__ float red[kKeysBlk / 32][R];
   const int tile = blockIdx.x, hl = blockIdx.y, head = a.h0 + hl, t = threadIdx.x;
   const size_t th = (size_t)tile * gridDim.y + hl;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.z == 0 && a.count)
     for (int c = t; c < a.chunks; c += kKeysBlk) a.count[th * a.chunks + c] = 0;
   const TileRef tr = find_tile<R>(a.p, tile, hl == 0 && blockIdx.z == 0);
@@ -147,19 +148,21 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
   __shared__ int last;
   const int tile = blockIdx.x, hl = blockIdx.y / a.chunks, chunk = blockIdx.y - hl * a.chunks, head = a.h0 + hl;
   const int heads = gridDim.y / a.chunks, t = threadIdx.x;
+  // launched while the scores kernel still runs: what follows up to the wait is not its work
   const TileRef tr = find_tile<R>(a.p, tile, false);
-  if (tr.n == 0) return;
   const int vis = max(0, tr.pos0 + tr.n), k0 = blockIdx.z * a.span_keys;
   const int nsp = max(1, (vis + a.span_keys - 1) / a.span_keys);
-  if ((int)blockIdx.z >= nsp) return;
-  const int nk = min(a.span_keys, vis - k0);
+  const bool mine = tr.n > 0 && (int)blockIdx.z < nsp;
+  const int nk = mine ? min(a.span_keys, vis - k0) : 0;
   const size_t th = (size_t)tile * heads + hl;
   for (int i = t; i < nk; i += kVT) {
     const int key = k0 + i, pi = key / a.p.page_size, pg = paged_page(a.p, tr.b, pi);
     tok[i] = pg < 0 ? -1 : pg * a.p.page_size + (key - pi * a.p.page_size);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
   const float* w = a.w + (th * a.key_pitch + k0) * R;
-  for (int i = t; i < nk * R; i += kVT) ws[i] = w[i];
+  for (int i = t; i < nk * R; i += kVT) ws[i] = __ldcg(w + i);
   __syncthreads();
   const int c0 = chunk * kVT * EV + (kVec ? t * EV : t);  // first column of the head
   constexpr int cs = kVec ? 1 : kVT;                      // and the step to the next
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
   // keys that every row of the tile sees, then the last ones, which some rows do not
   const int all = min(nk, max(0, tr.pos0 + 1 - k0));
   if (live) {
-    constexpr int U = kVec ? kUnroll : kUnroll / 2;
+    constexpr int U = kUnroll;
     int i = 0;
     for (; i + U <= all; i += U) {
       float g[U][EV];
@@ -215,9 +218,11 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
     float* mine = base + (size_t)blockIdx.z * (R * kVT * EV) + t;
     if (live) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
+        if (r >= tr.n) break;
 #pragma unroll
         for (int e = 0; e < EV; ++e) __stcg(mine + (r * EV + e) * kVT, acc[r][e]);
+      }
     }
     __threadfence();
     __syncthreads();
@@ -227,15 +232,16 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
     __threadfence();
     if (live) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
+        if (r >= tr.n) break;
 #pragma unroll
         for (int e = 0; e < EV; ++e) acc[r][e] = 0.f;
-      for (int z = 0; z < nsp; ++z) {
-        const float* src = base + (size_t)z * (R * kVT * EV) + t;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
+#pragma unroll 8
+        for (int z = 0; z < nsp; ++z) {
+          const float* src = base + (size_t)z * (R * kVT * EV) + t;
 #pragma unroll
           for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(src + (r * EV + e) * kVT);
+        }
       }
     }
   }
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
   if (t < R) {
     const int pos = tr.pos0 + t, ns = (vis + kKeysBlk - 1) / kKeysBlk;
     float d = 0.f;
-    for (int z = 0; z < ns; ++z) d += a.den[(th * a.spans + z) * R + t];
+    for (int z = 0; z < ns; ++z) d += __ldcg(a.den + (th * a.spans + z) * R + t);
     if (a.null_bias && pos >= 0) {
       const float tau = head_tau(a.tau, a.s, head, a.p.err, kKernPaged);
       d += (float)(pos + 1) * expf(a.null_bias[head] - tau);
@@ -291,7 +297,7 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
   // spans of 512 keys, shorter where they would leave SMs without work
   l.span_keys = kSpanMax;
   while (l.span_keys > 64 &&
-         (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 16LL * sm_count())
+         (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 32LL * sm_count())
     l.span_keys /= 2;
   l.gspans = ceil_div(c.p.max_len, l.span_keys);
   // heads of a pass: as many as keep the scratch near 1 GB
@@ -332,9 +338,19 @@ cudaError_t run(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
     if (gs.z > 65535 || gg.y > 65535 || gg.z > 65535) return cudaErrorInvalidConfiguration;
     if (kvec) paged_scores_kernel<T, R, true><<<gs, kKeysBlk, 0, s>>>(a);
     else paged_scores_kernel<T, R, false><<<gs, kKeysBlk, 0, s>>>(a);
-    if (gvec) paged_gates_kernel<T, R, true><<<gg, kVT, 0, s>>>(a);
-    else paged_gates_kernel<T, R, false><<<gg, kVT, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = gg;
+    cfg.blockDim = dim3(kVT);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true>, a)
+             : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false>, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
