@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
 
 // grid (tiles, heads, spans), 256 threads, one key each per round.
 template <int R, int DH>
-__global__ void __launch_bounds__(kWThreads) paged_weights_few_kernel(const TcArgs a) {
+__global__ void __launch_bounds__(kWThreads, 4) paged_weights_few_kernel(const TcArgs a) {
   __shared__ __align__(16) float qs[R][DH];
   __shared__ float red[kWThreads / 32][R];
   const int t = threadIdx.x, lane = t & 31;
