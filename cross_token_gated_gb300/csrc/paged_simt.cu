@@ -13,6 +13,9 @@
 //       tile, 8 keys of a thread in flight; tiles of one chunk stand next to each other in
 //       the grid and share the gates in L2.  The spans of one output are joined by the block that finishes last,
 //       in the spans' order (no order-dependent sums).
+// 71 new tokens of 4 sequences over 2,297 cached ones, fp32, 2 x 4,747 gates in rows that are not
+// 16-byte aligned: 46 us, bound by the latency of 4-byte loads and of two kernels in a row (the
+// bytes alone would take 14 us); spans of 512 keys for all took 74 us there.
 // Weights past a row's own position are selected away, not multiplied by zero, so gates of
 // later tokens and of unused slots may be NaN.
 #include "tg_common.cuh"

@@ -10,12 +10,17 @@
 // 2^64, and pos * F wraps at whole turns by itself; its high 32 bits are the angle in units
 // of 2^-31 half turns, exact at any position, for sincospi.
 //
-// All of it is bound by HBM bandwidth (each value is read and written once) and, for few
-// rows, by launch latency.  A block takes a few rows at a time: one thread per (row, pair)
-// forms the angles' cos and sin in shared memory once for all heads of the row (a sincospi
-// per element pair and head would cost more issue slots than the copy leaves), then
-// threads walk the rows' heads in memory order, 32 bytes of a head per thread in two
-// 16-byte vectors, the norm's sums by shuffles between the d_h / E lanes of a head.
+// All of it is bound by HBM bandwidth (each value is read and written once), closely followed
+// by issue slots, and for few rows by launch latency.  A block takes a few rows at a time: one
+// thread per (row, pair) forms the angles' cos and sin in shared memory once for all heads of
+// the row (a sincospi per element pair and head would cost more issue slots than the copy
+// leaves).  A thread keeps one place of a row, 32 bytes of one head in two 16-byte vectors,
+// and walks the rows, loaded ahead of the angles; the norm's sums are shuffles between the
+// d_h / E lanes of a head, the arithmetic is packed two f32 at a time.  65,536 rows of 32
+// heads of 32 in bf16 take 49.5 us (5.4 TB/s); gradients of 16,384 rows of 12 heads of 64 with
+// gains 34.5 us, bound by latency at 16 warps an SM (128 registers a thread).  An append of
+// 9,192 tokens of 9,504 gates takes 61.7 us (5.8 TB/s): a block per row, the row's slot looked
+// up once while its gates are on their way.
 #include <math.h>
 
 #include "tg_common.cuh"

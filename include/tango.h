@@ -500,7 +500,12 @@ tg_status tg_rope_freqs(int rotary_dim, double base, double factor, long long or
  * unspecified.
  * The cache is two pools owned by the caller: k_pages [n_pages, page_size, H * d_h]
  * (normed, rotated keys) and g_pages [n_pages, page_size, H * m_pitch].  Slots past a
- * sequence's length may hold anything (NaN included): they are never used.
+ * sequence's length may hold anything (NaN included): they are never used.  The columns
+ * between m_h and m_pitch of a head may be read and are written with unspecified values;
+ * they reach no result.
+ * TG_BF16 runs the aggregation on the tensor cores when d_h is 16, 32 or 64, m_pitch and page_size
+ * are multiples of 8, and q, out and the pools are
+ * 16-byte aligned; anything else, and TG_F32, runs on the CUDA cores.
  */
 typedef struct {
     int B, H, d_h, m, m_pitch, N, max_new, max_len, page_size, n_pages, table_pitch;

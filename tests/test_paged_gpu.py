@@ -258,6 +258,72 @@ def test_slices_and_in_place():
         assert torch.equal(v, want)
 
 
+@pytest.mark.parametrize("n", [1, 12, 70])
+def test_addresses_off_16_bytes(n):
+    """v, q, out or a pool that start anywhere: other kernels, the same values."""
+    b = Batch([(n, 90), (n, 300)], 2, 32, 264, "bf16", 16, seed=14)
+
+    def off(t):
+        x = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        x.copy_(t)
+        return x
+    b.check(v=torch.cat([b.v.new_zeros(b.N, 3), b.v], 1)[:, 3:])
+    for name in ("q", "k_pages", "g_pages"):
+        keep = getattr(b, name)
+        setattr(b, name, off(keep))
+        b.check()
+        setattr(b, name, keep)
+    out = off(torch.zeros(b.N, 528, dtype=torch.bfloat16, device="cuda"))
+    tg.tango_paged_aggregate(b.q, b.v, out, b.k_pages, b.g_pages, b.table, b.cu, b.lens, H=2, max_new=n, max_len=300)
+    assert (out.double() - b.run().double()).abs().max().item() <= 4 * 2.0 ** -8 * out.abs().max().item()
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 1), ("bf16", 20), ("f32", 3)])
+def test_pages_beyond_32_bit_offsets(dtype, n):
+    """Slots whose element offset passes 2^31: appended to and read back."""
+    m_h, pages = 14240, 1250          # 1,250 pages x 64 tokens x 28,480 gates = 2.28e9 values
+    b = Batch([(n, 70), (n, 130)], 2, 64, m_h, dtype, 64, seed=15)
+    dt, first = DT[dtype], pages - b.k_pages.shape[0]
+    k_pages = torch.empty(pages, 64, 128, dtype=dt, device="cuda")
+    g_pages = torch.empty(pages, 64, 2 * m_h, dtype=dt, device="cuda")
+    k_pages[first:], g_pages[first:] = b.k_pages, b.g_pages
+    b.k_pages, b.g_pages, b.table = k_pages, g_pages, b.table + first
+    assert first * 64 * 2 * m_h > 2 ** 31
+    b.check()
+    # the last tokens' gates once more, through the append
+    k = torch.randn(b.N, 128, device="cuda").to(dt)
+    g = torch.randn(b.N, 2 * m_h, device="cuda").to(dt)
+    tg.tango_cache_append(None, k, g, None, k_pages, g_pages, b.table, b.cu, b.lens, None, H=2, norm=tg.TG_NORM_NONE,
+                          silu=False)
+    pos = torch.cat([torch.arange(t - n, t) for n, t in b.seqs]).cuda()
+    seq = torch.arange(2).repeat_interleave(n).cuda()
+    page = b.table[seq, pos // 64].long()
+    assert torch.equal(g_pages[page, pos % 64], g) and torch.equal(k_pages[page, pos % 64], k)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_seeded_draws(seed):
+    """Head and gate widths, page sizes, lengths and options at random."""
+    import random
+    rng = random.Random(seed)
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    H, d_h = rng.choice([(1, 64), (2, 64), (4, 32), (3, 16), (2, 128), (2, 24)])
+    m_h = rng.randrange(1, 900)
+    pitch = rng.choice([m_h, -(-m_h // 8) * 8, -(-m_h // 8) * 8 + 8])
+    page = rng.choice([1, 5, 8, 16, 24, 32, 64, 96, 128, 256])
+    most = rng.choice([1, 1, 8, 40, 300])
+    seqs = []
+    for _ in range(rng.randrange(1, 9)):
+        new = rng.randrange(0, most + 1)
+        seqs.append((new, rng.choice([new, new + rng.randrange(0, 70), new + rng.randrange(0, 900), max(0, new - 2)])))
+    if not any(n for n, _ in seqs):
+        seqs[0] = (1, 5)
+    kw = dict(v=rng.choice([True, False]), s=rng.choice([0.0, 3.5, 10.0, 20.0]))
+    if rng.random() < 0.4:
+        kw["null"] = torch.randn(H, generator=torch.Generator().manual_seed(seed)).cuda()
+    Batch(seqs, H, d_h, m_h, dtype, page, pitch, seed=seed).check(**kw)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_repeats_bit_for_bit(dtype):
     """Joined spans add in a fixed order; a workspace's earlier contents do not matter."""
