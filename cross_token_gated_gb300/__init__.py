@@ -578,7 +578,7 @@ def tango_qk_norm_rope(q, k, q_out, k_out, freqs, *, H, H_k=None, positions=None
     per row, or None (the index along T).  q_gain, k_gain: float32 [d_h] or None."""
     p, (qo, ko), dev = _qk_params(q, k, (("q_out", q_out, q), ("k_out", k_out, k)), freqs, H, H_k, positions, layout,
                                   norm, q_gain, k_gain, eps)
-    st = load().tango_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), qo, ko, _stream_on(stream, dev))
+    st = (_lib or load()).tango_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), qo, ko, _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_qk_norm_rope")
     return q_out, k_out
@@ -666,8 +666,9 @@ def tango_cache_append(q, k, g, q_out, k_pages, g_pages, page_table, cu_new, len
         fp = _dense(freqs, "freqs", torch.float64, dev)
         rotary = 2 * freqs.numel()
     a = tg_append_params(rotary, layout, norm, eps, fp, 1 if silu else 0, q_pitch, k_pitch, g_pitch)
-    st = load().tango_cache_append(ctypes.byref(p), ctypes.byref(a), _ptr(q), k.data_ptr(), g.data_ptr(), qo,
-                                   k_pages.data_ptr(), g_pages.data_ptr(), _stream_on(stream, dev))
+    st = (_lib or load()).tango_cache_append(ctypes.byref(p), ctypes.byref(a), _ptr(q), k.data_ptr(),
+                                             g.data_ptr(), qo, k_pages.data_ptr(), g_pages.data_ptr(),
+                                             _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_cache_append")
     return q_out
@@ -691,10 +692,10 @@ def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens,
             raise ValueError("v must have one row per new token, as wide as the cache's gates")
     p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=max_new, max_len=max_len, m_h=m_h,
                      s=s, tau=tau, null_bias=null_bias, v_pitch=v_pitch)
-    lib = load()
-    wbuf = _scratch(lib.tg_workspace_size(TG_WS_PAGED, ctypes.byref(p)), q.device, ws, stream)
+    lib, ref = _lib or load(), ctypes.byref(p)
+    wbuf = ws if ws is not None else _scratch(lib.tg_workspace_size(TG_WS_PAGED, ref), q.device, None, stream)
     wp, wn = _ws_ptr(wbuf)
-    st = lib.tango_paged_aggregate(ctypes.byref(p), qp, _ptr(v), op, k_pages.data_ptr(), g_pages.data_ptr(), wp, wn,
+    st = lib.tango_paged_aggregate(ref, qp, _ptr(v), op, k_pages.data_ptr(), g_pages.data_ptr(), wp, wn,
                                    _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_paged_aggregate")

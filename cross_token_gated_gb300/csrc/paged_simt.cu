@@ -275,13 +275,6 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct SimtPlan {
@@ -300,7 +293,7 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
   // spans of 512 keys, shorter where they would leave SMs without work
   l.span_keys = kSpanMax;
   while (l.span_keys > 64 &&
-         (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 32LL * sm_count())
+         (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 32LL * serve_sm_count())
     l.span_keys /= 2;
   l.gspans = ceil_div(c.p.max_len, l.span_keys);
   // heads of a pass: as many as keep the scratch near 1 GB

@@ -41,6 +41,8 @@
 // flight: 512 new tokens over 8,192 take 206 us, 1,131 TFLOP/s.  Any other load of the SM waits
 // some 5,000 cycles behind the copies, hence eight epilogue warps and v asked for before the
 // products end (prompts of 2,048 tokens and decode steps in one batch: 832 -> 729 us).
+#include <atomic>
+
 #include "tg_common.cuh"
 #include "tg_paged.cuh"
 #include "tg_ptx.cuh"
@@ -1138,13 +1140,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
 
 // ============================================================================= launch
 
-int num_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Rows of a G box: the largest power of two that divides a page, at most a step.
@@ -1160,7 +1155,7 @@ struct TcPlan {
 
 TcPlan tc_plan(const PagedCall& c) {
   TcPlan l;
-  const int sms = num_sms();
+  const int sms = serve_sm_count();
   l.rows_tot = up8(c.p.N) + 8 * c.p.B;
   l.key_blocks = ceil_div(c.p.max_len, kK);
   // at most 32 spans of whole 128-key blocks (their sums are added once per strip)
@@ -1206,6 +1201,21 @@ void launch_weights_few(const TcArgs& a, int rows, dim3 g, cudaStream_t s) {
   else launch_weights_few_dh<16>(a, rows, g, s);
 }
 
+// Both kernels' dynamic shared memory, allowed once per device.
+cudaError_t allow_shared_memory() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(paged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_gates_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
+  if (e == cudaSuccess && kept) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 }  // namespace
 
 bool paged_tc_takes(tg_dtype dt, const PagedCall& c) {
@@ -1242,10 +1252,7 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   mG4 = mG;  // used only where a head holds a whole strip
   if (e == cudaSuccess && c.m_h >= kN)
     e = make_tmap_5d_chunks(&mG4, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 4);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_gates_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
+  if (e == cudaSuccess) e = allow_shared_memory();
   if (e != cudaSuccess) return e;
   for (a.h0 = 0; a.h0 < c.H; a.h0 += l.heads) {
     a.heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;

@@ -23,6 +23,8 @@
 // up once while its gates are on their way.
 #include <math.h>
 
+#include <atomic>
+
 #include "tg_common.cuh"
 #include "tg_kernels.h"
 #include "tg_paged.cuh"
@@ -737,13 +739,6 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
 
 // --------------------------------------------------------------------------- launch
 
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -763,7 +758,7 @@ bool vec_heads(int d_h, int rotary, int es, std::initializer_list<const void*> p
 // Rows of a block's step: as many as its threads load ahead (`places` threads a row), fewer
 // while that leaves SMs idle.
 int rows_per_block(long long rows, int places, int pairs) {
-  const int want = 2 * sm_count();
+  const int want = 2 * serve_sm_count();
   int rb = kAheadRows * (places < kThreads ? kThreads / places : 1);
   if (rb > kMaxRowsBlk) rb = kMaxRowsBlk;
   if (pairs > 0 && rb > kAngles / pairs) rb = kAngles / pairs;
@@ -789,7 +784,7 @@ QkArgs<T> qk_args(const QkCall& c) {
 }
 
 int qk_grid(long long rows, int rb, int per_sm) {
-  const long long blocks = (rows + rb - 1) / rb, most = (long long)sm_count() * per_sm;
+  const long long blocks = (rows + rb - 1) / rb, most = (long long)serve_sm_count() * per_sm;
   return (int)(blocks < most ? blocks : most);
 }
 
@@ -854,7 +849,7 @@ cudaError_t append_t(const AppendCall& c, cudaStream_t s) {
   // of one as keeps the SMs busy
   constexpr int EV = 16 / sizeof(T);
   const int most = ceil_div((long long)c.H * (vec ? c.m_pitch / EV : c.m_h), kThreads);
-  const int want = ceil_div(8LL * sm_count(), c.p.N);
+  const int want = ceil_div(8LL * serve_sm_count(), c.p.N);
   a.chunks = want < most ? want : most;
   const long long blocks = a.qk_blocks + (long long)c.p.N * a.chunks;
   if (blocks > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
@@ -868,7 +863,19 @@ cudaError_t append_t(const AppendCall& c, cudaStream_t s) {
 
 }  // namespace
 
-size_t qk_backward_part_bytes(int d_h) { return (size_t)sm_count() * kBwdPerSm * 2 * d_h * sizeof(float); }
+int serve_sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const bool kept = dev >= 0 && dev < 64;
+  int n = kept ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  if (kept) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+size_t qk_backward_part_bytes(int d_h) { return (size_t)serve_sm_count() * kBwdPerSm * 2 * d_h * sizeof(float); }
 
 cudaError_t launch_qk_forward(tg_dtype dt, const QkCall& c, cudaStream_t s) {
   return dt == TG_F32 ? forward_t<float>(c, s) : forward_t<__nv_bfloat16>(c, s);

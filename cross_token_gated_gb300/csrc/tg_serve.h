@@ -7,6 +7,9 @@
 
 namespace tg {
 
+// SMs of the current device (looked up once per device).
+int serve_sm_count();
+
 // ---- qk_rope.cu
 struct QkCall {
   long long rows;
