@@ -237,12 +237,15 @@ def _workspace(nbytes: int, device, ws):
 
 
 def _scratch(nbytes: int, device, ws, stream):
-    """_workspace for a call on `stream`: scratch made here stays allocated until that
-    stream has passed the call, also when it is not the current one."""
-    buf = _workspace(nbytes, device, ws)
-    if ws is None and buf is not None and stream is not None:
-        buf.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return buf
+    """_workspace for a call on `stream`.  Scratch made here is allocated on that stream, so
+    that memory is neither taken while another stream's work on it is pending nor given
+    away before the call has run."""
+    if ws is not None or stream is None:
+        return _workspace(nbytes, device, ws)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return _workspace(nbytes, device, None)
 
 
 def _ws_ptr(ws):

@@ -373,6 +373,32 @@ def test_side_stream_and_graph():
         assert torch.equal(out, b.run())
 
 
+def test_scratch_is_taken_from_the_calls_stream(monkeypatch):
+    """A call on a stream that is not the current one allocates its scratch there: a block
+    freed on the current stream may still be written by work that waits on it."""
+    b = Batch([(20, 90), (20, 300)], 2, 32, 264, "bf16", 16, seed=12)
+    want, out = b.run(), torch.zeros(b.N, 2 * 264, dtype=torch.bfloat16, device="cuda")
+    x, dx, gain = torch.randn(40, 64, device="cuda"), torch.empty(40, 64, device="cuda"), torch.ones(32, device="cuda")
+    torch.cuda.synchronize()
+    took, allocate = [], tg._workspace
+    monkeypatch.setattr(tg, "_workspace",
+                        lambda *a: (took.append(torch.cuda.current_stream().cuda_stream), allocate(*a))[1])
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    for stream in (side, side.cuda_stream, 0, None):
+        out.zero_()
+        torch.cuda.synchronize()
+        tg.tango_paged_aggregate(b.q, b.v, out, b.k_pages, b.g_pages, b.table, b.cu, b.lens, H=2, max_new=20,
+                                 max_len=300, m_h=264, stream=stream)
+        tg.tango_qk_norm_rope_backward(x, None, x, None, dx, None, None, H=2, norm=tg.TG_NORM_RMS, q_gain=gain,
+                                       dq_gain=torch.empty_like(gain), stream=stream)
+        where = here.cuda_stream if stream is None else getattr(stream, "cuda_stream", stream)
+        assert took == [where, where]
+        assert torch.cuda.current_stream() == here
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        took.clear()
+
+
 def test_bad_device_values_are_flagged_and_not_followed():
     """Pages outside the pool, lengths and row offsets outside their bounds: the checks in
     the kernels skip or clamp them and set the error word."""
