@@ -10,14 +10,22 @@
 //       weights in f32 to scratch [tile][head][key][R], and the key span's weight sums.
 //   paged_gates_kernel   per (tile, head, 512 or 1024 columns, span of keys): the weighted sum
 //       over the span's gate rows.  Bound by HBM for few rows: each gate is read once per
-//       tile, 8 keys of a thread in flight; tiles of one chunk stand next to each other in
-//       the grid and share the gates in L2.  The spans of one output are joined by the block that finishes last,
-//       in the spans' order (no order-dependent sums).
+//       tile; tiles of one chunk stand next to each other in the grid and share the gates in
+//       L2.  4 keys of a thread are multiplied while the next 4 are on their way, rows in pairs
+//       through f32x2 arithmetic.  The spans of one output are joined by the block that
+//       finishes last, in the spans' order (no order-dependent sums).
 // 71 new tokens of 4 sequences over 2,297 cached ones, fp32, 2 x 4,747 gates in rows that are not
 // 16-byte aligned: 46 us, bound by the latency of 4-byte loads and of two kernels in a row (the
-// bytes alone would take 14 us); spans of 512 keys for all took 74 us there.
-// Weights past a row's own position are selected away, not multiplied by zero, so gates of
+// bytes alone would take 14 us).  Whole chunks are bound by the latency of L2 and of a block's start:
+// 201 rows over 870 keys, 16 x 1,780 gates: 328 us, 27 TFLOP/s (660 us without the second
+// batch of loads and with single f32 arithmetic).  Tiles of 16 rows halve the reads but leave
+// 12 to 16 warps on an SM: 352 to 412 us there.  A ring of asynchronous copies in shared memory
+// instead of registers: 351 us there, 2 to 3 % faster for few aligned rows, 117 -> 156 us for
+// unaligned single rows.
+// Keys past a row's own position are selected away, not multiplied by zero, so gates of
 // later tokens and of unused slots may be NaN.
+#include <type_traits>
+
 #include "tg_common.cuh"
 #include "tg_kernels.h"
 #include "tg_paged.cuh"
@@ -29,7 +37,6 @@ namespace {
 
 constexpr int kKeysBlk = 128;   // keys of a scores block
 constexpr int kVT = 128;        // column vectors of a gates block
-constexpr int kUnroll = 8;
 
 template <typename T>
 struct SimtArgs {
@@ -142,11 +149,15 @@ constexpr int kSpanMax = 512;
 // grid (tiles, chunks * heads, gspans), 128 threads; a thread owns EV columns of R rows: EV
 // neighbours (one 16-byte load) where the gates' rows are 16-byte aligned, else every 128th
 // (so that a warp's loads are neighbours).
+// At least 5 blocks on an SM (3 for bf16, whose threads hold twice the columns): with the 110
+// registers that the compiler would take there are 4, and 201 rows over 870 keys take 466 us
+// instead of 339 (6 blocks, with spills: 354).
 template <typename T, int R, bool kVec>
-__global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
+__global__ void __launch_bounds__(kVT, sizeof(T) == 4 ? 5 : 3) paged_gates_kernel(const SimtArgs<T> a) {
   constexpr int EV = Cols<T>::EV;
-  __shared__ int tok[kSpanMax];
-  __shared__ __align__(16) float ws[kSpanMax * R];
+  constexpr int U = R == 1 ? 8 : 4;  // keys of a batch of loads
+  __shared__ __align__(16) int tok[kSpanMax + 3 * U];
+  __shared__ __align__(16) float ws[(kSpanMax + U) * R];
   __shared__ float dinv[R];
   __shared__ int last;
   const int tile = blockIdx.x, hl = blockIdx.y / a.chunks, chunk = blockIdx.y - hl * a.chunks, head = a.h0 + hl;
@@ -158,61 +169,127 @@ __global__ void __launch_bounds__(kVT) paged_gates_kernel(const SimtArgs<T> a) {
   const bool mine = tr.n > 0 && (int)blockIdx.z < nsp;
   const int nk = mine ? min(a.span_keys, vis - k0) : 0;
   const size_t th = (size_t)tile * heads + hl;
-  for (int i = t; i < nk; i += kVT) {
-    const int key = k0 + i, pi = key / a.p.page_size, pg = paged_page(a.p, tr.b, pi);
-    tok[i] = pg < 0 ? -1 : pg * a.p.page_size + (key - pi * a.p.page_size);
+  // the span's tokens, and some more for the loads that run ahead (any token of the pool does)
+  bool bad = false;
+  for (int i = t; i < nk + 3 * U; i += kVT) {
+    const int key = k0 + i, pi = key / a.p.page_size, pg = i < nk ? paged_page(a.p, tr.b, pi) : 0;
+    bad |= pg < 0;
+    tok[i] = i >= nk ? 0 : pg < 0 ? -1 : pg * a.p.page_size + (key - pi * a.p.page_size);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
   const float* w = a.w + (th * a.key_pitch + k0) * R;
-  for (int i = t; i < nk * R; i += kVT) ws[i] = __ldcg(w + i);
-  __syncthreads();
+  // weights are not negative; -1 stands for a key to be skipped
+  for (int i = t; i < (nk + U) * R; i += kVT) ws[i] = i < nk * R ? __ldcg(w + i) : -1.f;
+  bad = __syncthreads_or(bad);
+  if (bad) {  // pages outside the pool: their gates count as zeros
+    for (int i = t; i < nk; i += kVT)
+      if (tok[i] < 0) {
+        tok[i] = 0;
+        for (int r = 0; r < R; ++r) ws[i * R + r] = -1.f;
+      }
+    __syncthreads();
+  }
   const int c0 = chunk * kVT * EV + (kVec ? t * EV : t);  // first column of the head
   constexpr int cs = kVec ? 1 : kVT;                      // and the step to the next
   const bool live = c0 < a.m_h;
-  float acc[R][EV] = {};
+  constexpr int P = R > 1 ? 2 : 1;  // rows of an accumulator: pairs go through f32x2 arithmetic
+  uint64_t acc2[R / P][EV];
+  float acc[R][EV];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int e = 0; e < EV; ++e) acc[r][e] = 0.f, acc2[r / P][e] = 0;
+  }
   const size_t row_elems = (size_t)a.H * a.m_pitch;
   const T* gcol = a.g_pages + (size_t)head * a.m_pitch + c0;
-  auto load = [&](int i, float (&g)[EV]) {
-    const int tk = tok[i];
-    if (kVec) {
-      Cols<T>::get(tk >= 0 ? ptx::ld_global_v4(gcol + (size_t)tk * row_elems) : make_uint4(0, 0, 0, 0), g);
-    } else {
+  // gates of U keys as loaded: one vector each, or EV single values
+  using Raw = typename std::conditional<kVec, uint4, T[EV]>::type;
+  auto load = [&](int i, Raw (&g)[U]) {
 #pragma unroll
-      for (int e = 0; e < EV; ++e) g[e] = tk >= 0 && c0 + e * cs < a.m_h ? io<T>::ld(gcol + (size_t)tk * row_elems + e * cs) : 0.f;
+    for (int j = 0; j < U; ++j) {
+      const T* src = gcol + (size_t)(unsigned)tok[i + j] * row_elems;
+      if constexpr (kVec) {
+        g[j] = ptx::ld_global_v4(src);
+      } else {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) g[j][e] = e == 0 || c0 + e * cs < a.m_h ? src[e * cs] : T(0.f);
+      }
     }
   };
-  // keys that every row of the tile sees, then the last ones, which some rows do not
-  const int all = min(nk, max(0, tr.pos0 + 1 - k0));
-  if (live) {
-    constexpr int U = kUnroll;
-    int i = 0;
-    for (; i + U <= all; i += U) {
-      float g[U][EV];
+  auto widen = [&](const Raw& g, float (&f)[EV]) {
+    if constexpr (kVec) {
+      Cols<T>::get(g, f);
+    } else {
 #pragma unroll
-      for (int j = 0; j < U; ++j) load(i + j, g[j]);
+      for (int e = 0; e < EV; ++e) f[e] = io<T>::ld(&g[e]);
+    }
+  };
+  // keys up to `all` are seen by every row of the tile, the last ones by some
+  const int all = bad ? 0 : min(nk, max(0, tr.pos0 + 1 - k0));
+  auto add = [&](int i, const Raw (&g)[U]) {
+    if (i + U <= all) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
+        float f[EV];
+        widen(g[j], f);
+        if constexpr (R == 1) {
+          const float wr = ws[i + j];
+#pragma unroll
+          for (int e = 0; e < EV; ++e) acc[0][e] = fmaf(wr, f[e], acc[0][e]);
+        } else {
+          uint64_t ff[EV];
+#pragma unroll
+          for (int e = 0; e < EV; ++e) ff[e] = ptx::f32x2_pack(f[e], f[e]);
+#pragma unroll
+          for (int r = 0; r < R / 2; ++r) {
+            const uint64_t wr = *reinterpret_cast<const uint64_t*>(&ws[(i + j) * R + 2 * r]);
+#pragma unroll
+            for (int e = 0; e < EV; ++e) acc2[r][e] = ptx::fma_f32x2(wr, ff[e], acc2[r][e]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float f[EV];
+        widen(g[j], f);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float wr = ws[(i + j) * R + r];
+          if (!(wr < 0.f) && k0 + i + j <= tr.pos0 + r) {
 #pragma unroll
-          for (int e = 0; e < EV; ++e) acc[r][e] = fmaf(wr, g[j][e], acc[r][e]);
+            for (int e = 0; e < EV; ++e) {
+              if constexpr (R == 1) {
+                acc[0][e] = fmaf(wr, f[e], acc[0][e]);
+              } else {
+                float x[2];
+                ptx::f32x2_unpack(acc2[r / 2][e], x[0], x[1]);
+                x[r % 2] = fmaf(wr, f[e], x[r % 2]);
+                acc2[r / 2][e] = ptx::f32x2_pack(x[0], x[1]);
+              }
+            }
+          }
         }
       }
     }
-    for (; i < nk; ++i) {
-      if (tok[i] < 0) continue;
-      float g[EV];
-      load(i, g);
+  };
+  if (live && nk > 0) {
+    Raw ga[U], gb[U];
+    load(0, ga);
+#pragma unroll 1
+    for (int i = 0; i < nk; i += 2 * U) {
+      load(i + U, gb);
+      add(i, ga);
+      load(i + 2 * U, ga);
+      if (i + U < nk) add(i + U, gb);
+    }
+  }
+  if constexpr (R > 1) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float wr = ws[i * R + r];
-        if (i < all || k0 + i <= tr.pos0 + r) {
+    for (int r = 0; r < R; r += 2) {
 #pragma unroll
-          for (int e = 0; e < EV; ++e) acc[r][e] = fmaf(wr, g[e], acc[r][e]);
-        }
-      }
+      for (int e = 0; e < EV; ++e) ptx::f32x2_unpack(acc2[r / 2][e], acc[r][e], acc[r + 1][e]);
     }
   }
   if (nsp > 1) {
@@ -290,10 +367,13 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
   l.spans = ceil_div(c.p.max_len, kKeysBlk);
   l.key_pitch = l.spans * kKeysBlk;
   l.chunks = ceil_div(c.m_h, kVT * EV);
-  // spans of 512 keys, shorter where they would leave SMs without work
+  // spans of 512 keys, shorter where the grid would hold fewer than 20 blocks per SM (a block
+  // starts with some 4 us of dependent look-ups and its sums are written and read again: over
+  // batches of 1 to 276 new rows, fp32, 147 us on average against 153 with 32; with 16 the
+  // 71-row batch takes 56 us instead of 46)
   l.span_keys = kSpanMax;
   while (l.span_keys > 64 &&
-         (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 32LL * serve_sm_count())
+         (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 20LL * serve_sm_count())
     l.span_keys /= 2;
   l.gspans = ceil_div(c.p.max_len, l.span_keys);
   // heads of a pass: as many as keep the scratch near 1 GB
