@@ -12,8 +12,8 @@
 //       over the span's gate rows.  Bound by HBM for few rows: each gate is read once per
 //       tile; tiles of one chunk stand next to each other in the grid and share the gates in
 //       L2.  4 keys of a thread are multiplied while the next 4 are on their way, rows in pairs
-//       through f32x2 arithmetic.  The spans of one output are joined by the block that
-//       finishes last, in the spans' order (no order-dependent sums).
+//       through f32x2 arithmetic.  The spans of one output are joined, 16 neighbours first, by
+//       the block of them that finishes last, in the spans' order (no order-dependent sums).
 // 71 new tokens of 4 sequences over 2,297 cached ones, fp32, 2 x 4,747 gates in rows that are not
 // 16-byte aligned: 46 us, bound by the latency of 4-byte loads and of two kernels in a row (the
 // bytes alone would take 14 us).  Whole chunks are bound by the latency of L2 and of a block's start:
@@ -46,6 +46,7 @@ struct SimtArgs {
   int spans;                     // score spans: ceil(max_len / kKeysBlk)
   int span_keys, gspans;         // keys of a gates block's span; spans of the longest sequence
   int chunks;                    // column chunks of a head
+  int counts;                    // counters of a chunk's spans: the groups', then each group's
   float s;
   const float* tau;
   const float* null_bias;
@@ -56,7 +57,7 @@ struct SimtArgs {
   float* w;     // [tile][head of the pass][key][R]
   float* den;   // [tile][head of the pass][span][R]
   float* part;  // [tile][head of the pass][chunk][gspan][R][128 EV]
-  int* count;   // [tile][head of the pass][chunk]: spans that are done
+  int* count;   // [tile][head of the pass][chunk][counts]: spans or groups that are done
 };
 
 // grid (tiles, heads, spans), 128 threads.
@@ -67,8 +68,8 @@ __global__ void __launch_bounds__(kKeysBlk) paged_scores_kernel(const SimtArgs<T
   const int tile = blockIdx.x, hl = blockIdx.y, head = a.h0 + hl, t = threadIdx.x;
   const size_t th = (size_t)tile * gridDim.y + hl;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.z == 0 && a.count)
-    for (int c = t; c < a.chunks; c += kKeysBlk) a.count[th * a.chunks + c] = 0;
+  if (blockIdx.z == 0)
+    for (int c = t; c < a.chunks * a.counts; c += kKeysBlk) a.count[th * a.chunks * a.counts + c] = 0;
   const TileRef tr = find_tile<R>(a.p, tile, hl == 0 && blockIdx.z == 0);
   const int vis = tr.pos0 + tr.n;  // keys that the last row sees
   if (tr.n == 0 || (int)blockIdx.z * kKeysBlk >= vis) return;
@@ -145,6 +146,9 @@ template <> struct Cols<__nv_bfloat16> {
 };
 
 constexpr int kSpanMax = 512;
+// Spans whose sums are joined first.  One block that adds 125 spans of 8 rows up alone takes
+// 60 us of the 103 of 20 rows over 8,000 keys (4 x 256 gates); in groups of 16 all take 56.
+constexpr int kJoin = 16;
 
 // grid (tiles, chunks * heads, gspans), 128 threads; a thread owns EV columns of R rows: EV
 // neighbours (one 16-byte load) where the gates' rows are 16-byte aligned, else every 128th
@@ -153,7 +157,7 @@ constexpr int kSpanMax = 512;
 // registers that the compiler would take there are 4, and 201 rows over 870 keys take 466 us
 // instead of 339 (6 blocks, with spills: 354).
 template <typename T, int R, bool kVec>
-__global__ void __launch_bounds__(kVT, sizeof(T) == 4 ? 5 : 3) paged_gates_kernel(const SimtArgs<T> a) {
+__global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) paged_gates_kernel(const SimtArgs<T> a) {
   constexpr int EV = Cols<T>::EV;
   constexpr int U = R == 1 ? 8 : 4;  // keys of a batch of loads
   __shared__ __align__(16) int tok[kSpanMax + 3 * U];
@@ -293,36 +297,65 @@ __global__ void __launch_bounds__(kVT, sizeof(T) == 4 ? 5 : 3) paged_gates_kerne
     }
   }
   if (nsp > 1) {
-    // this span's sums, then, in the block that finishes last, all spans' in order
-    float* base = a.part + ((th * a.chunks + chunk) * a.gspans) * (size_t)(R * kVT * EV);
-    float* mine = base + (size_t)blockIdx.z * (R * kVT * EV) + t;
-    if (live) {
+    // This span's sums go to scratch; the block that finishes last of kJoin neighbouring spans
+    // adds theirs up in order, and the last of those blocks the groups' sums.
+    constexpr size_t kSums = (size_t)R * kVT * EV;
+    float* base = a.part + (th * a.chunks + chunk) * a.gspans * kSums + t;
+    int* count = a.count + (th * a.chunks + chunk) * a.counts;
+    auto put = [&](int z) {
+      if (live) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r >= tr.n) break;
+        for (int r = 0; r < R; ++r) {
+          if (r >= tr.n) break;
 #pragma unroll
-        for (int e = 0; e < EV; ++e) __stcg(mine + (r * EV + e) * kVT, acc[r][e]);
-      }
-    }
-    __threadfence();
-    __syncthreads();
-    if (t == 0) last = atomicAdd(a.count + th * a.chunks + chunk, 1) == nsp - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    if (live) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r >= tr.n) break;
-#pragma unroll
-        for (int e = 0; e < EV; ++e) acc[r][e] = 0.f;
-#pragma unroll 8
-        for (int z = 0; z < nsp; ++z) {
-          const float* src = base + (size_t)z * (R * kVT * EV) + t;
-#pragma unroll
-          for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(src + (r * EV + e) * kVT);
+          for (int e = 0; e < EV; ++e) __stcg(base + z * kSums + (r * EV + e) * kVT, acc[r][e]);
         }
       }
+    };
+    auto last_of = [&](int* c, int n) {
+      __threadfence();
+      __syncthreads();
+      if (t == 0) last = atomicAdd(c, 1) == n - 1;
+      __syncthreads();
+      if (last) __threadfence();
+      return last != 0;
+    };
+    auto add_up = [&](int z, int end, int step) {
+      if (!live) return;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) acc[r][e] = 0.f;
+      }
+      if (tr.n == R) {  // full tiles: 32 to 64 loads of a thread in flight
+#pragma unroll(R >= 4 ? 2 : 8 / R)
+        for (int i = z; i < end; i += step) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(base + i * kSums + (r * EV + e) * kVT);
+          }
+        }
+        return;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= tr.n) break;
+#pragma unroll 8
+        for (int i = z; i < end; i += step) {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(base + i * kSums + (r * EV + e) * kVT);
+        }
+      }
+    };
+    const int z = blockIdx.z, z0 = z / kJoin * kJoin, z1 = min(nsp, z0 + kJoin);
+    put(z);
+    if (!last_of(count + 1 + z / kJoin, z1 - z0)) return;
+    add_up(z0, z1, 1);
+    if (nsp > kJoin) {
+      put(z0);
+      if (!last_of(count, (nsp + kJoin - 1) / kJoin)) return;
+      add_up(0, nsp, kJoin);
     }
   }
   // denominators of the tile's rows: the spans' sums, and the null gate
@@ -355,7 +388,7 @@ __global__ void __launch_bounds__(kVT, sizeof(T) == 4 ? 5 : 3) paged_gates_kerne
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct SimtPlan {
-  int R, tiles, heads, spans, span_keys, gspans, chunks, key_pitch;
+  int R, tiles, heads, spans, span_keys, gspans, chunks, counts, key_pitch;
   size_t w, den, part, count, total;
 };
 
@@ -376,9 +409,10 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
          (long long)l.tiles * c.H * l.chunks * ceil_div(c.p.max_len, l.span_keys) < 20LL * serve_sm_count())
     l.span_keys /= 2;
   l.gspans = ceil_div(c.p.max_len, l.span_keys);
+  l.counts = 1 + ceil_div(l.gspans, kJoin);
   // heads of a pass: as many as keep the scratch near 1 GB
   const size_t per_head = (size_t)l.tiles * ((size_t)l.key_pitch * l.R * 4 + (size_t)l.spans * l.R * 4 +
-                                             (size_t)l.chunks * l.gspans * l.R * kVT * EV * 4 + (size_t)l.chunks * 4);
+                                             (size_t)l.chunks * l.gspans * l.R * kVT * EV * 4 + (size_t)l.chunks * l.counts * 4);
   const size_t fit = (size_t(1) << 30) / (per_head ? per_head : 1);
   l.heads = (int)(fit < 1 ? 1 : fit > (size_t)c.H ? (size_t)c.H : fit);
   const size_t th = (size_t)l.tiles * l.heads;
@@ -386,7 +420,7 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
   l.den = l.w + align256(th * l.key_pitch * l.R * 4);
   l.part = l.den + align256(th * l.spans * l.R * 4);
   l.count = l.part + align256(th * l.chunks * l.gspans * l.R * kVT * EV * 4);
-  l.total = l.count + align256(th * l.chunks * 4);
+  l.total = l.count + align256(th * l.chunks * l.counts * 4);
   return l;
 }
 
@@ -394,7 +428,7 @@ template <typename T, int R>
 cudaError_t run(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
   SimtArgs<T> a;
   a.p = c.p; a.H = c.H; a.d_h = c.d_h; a.m_h = c.m_h; a.m_pitch = c.m_pitch;
-  a.key_pitch = l.key_pitch; a.spans = l.spans; a.span_keys = l.span_keys; a.gspans = l.gspans; a.chunks = l.chunks;
+  a.key_pitch = l.key_pitch; a.spans = l.spans; a.span_keys = l.span_keys; a.gspans = l.gspans; a.chunks = l.chunks; a.counts = l.counts;
   a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
   a.q = static_cast<const T*>(c.q); a.v = static_cast<const T*>(c.v); a.out = static_cast<T*>(c.out);
   a.k_pages = static_cast<const T*>(c.k_pages); a.g_pages = static_cast<const T*>(c.g_pages);

@@ -373,6 +373,17 @@ def test_side_stream_and_graph():
         assert torch.equal(out, b.run())
 
 
+@pytest.mark.parametrize("seqs", [[(1, 3000)], [(2, 2500), (1, 1025)], [(4, 1100), (3, 1024)], [(8, 2100), (5, 1089)]])
+def test_sums_of_many_key_spans_are_joined_in_order(seqs):
+    """More than 16 spans of one output (groups of spans, then the groups), full tiles and
+    tiles with rows to spare, on the CUDA cores in both types; the same bits every time."""
+    for dtype, pitch in (("f32", 260), ("f32", 259), ("bf16", 259)):
+        b = Batch(seqs, 2, 16, 259, dtype, 16, pitch=pitch, seed=21)
+        got = b.check()
+        for _ in range(3):
+            assert torch.equal(b.run().double().cpu().view(b.N, 2, -1)[..., :259], got)
+
+
 def test_scratch_is_taken_from_the_calls_stream(monkeypatch):
     """A call on a stream that is not the current one allocates its scratch there: a block
     freed on the current stream may still be written by work that waits on it."""
