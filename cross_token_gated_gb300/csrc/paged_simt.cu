@@ -8,8 +8,8 @@
 // Rows are taken in tiles of R (1, 2, 4 or 8) new tokens of one sequence.
 //   paged_scores_kernel  one thread per cached key: its R dot products (q in shared memory),
 //       weights in f32 to scratch [tile][head][key][R], and the key span's weight sums.
-//   paged_gates_kernel   per (tile, head, 512 or 1024 columns, span of keys): the weighted sum
-//       over the span's gate rows.  Bound by HBM for few rows: each gate is read once per
+//   paged_gates_kernel   per (tile, head, up to 512 or 1024 columns, span of keys): the weighted
+//       sum over the span's gate rows.  Bound by HBM for few rows: each gate is read once per
 //       tile; tiles of one chunk stand next to each other in the grid and share the gates in
 //       L2.  4 keys of a thread are multiplied while the next 4 are on their way, rows in pairs
 //       through f32x2 arithmetic.  The spans of one output are joined, 16 neighbours first, by
@@ -17,7 +17,7 @@
 // 71 new tokens of 4 sequences over 2,297 cached ones, fp32, 2 x 4,747 gates in rows that are not
 // 16-byte aligned: 46 us, bound by the latency of 4-byte loads and of two kernels in a row (the
 // bytes alone would take 14 us).  Whole chunks are bound by the latency of L2 and of a block's start:
-// 201 rows over 870 keys, 16 x 1,780 gates: 328 us, 27 TFLOP/s (660 us without the second
+// 201 rows over 870 keys, 16 x 1,780 gates: 320 us, 28 TFLOP/s (660 us without the second
 // batch of loads and with single f32 arithmetic).  Tiles of 16 rows halve the reads but leave
 // 12 to 16 warps on an SM: 352 to 412 us there.  A ring of asynchronous copies in shared memory
 // instead of registers: 351 us there, 2 to 3 % faster for few aligned rows, 117 -> 156 us for
@@ -36,7 +36,7 @@ namespace tg {
 namespace {
 
 constexpr int kKeysBlk = 128;   // keys of a scores block
-constexpr int kVT = 128;        // column vectors of a gates block
+constexpr int kVT = 128;        // column vectors of a gates block, half of them for narrow heads
 
 template <typename T>
 struct SimtArgs {
@@ -156,8 +156,8 @@ constexpr int kJoin = 16;
 // At least 5 blocks on an SM (3 for bf16, whose threads hold twice the columns): with the 110
 // registers that the compiler would take there are 4, and 201 rows over 870 keys take 466 us
 // instead of 339 (6 blocks, with spills: 354).
-template <typename T, int R, bool kVec>
-__global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) paged_gates_kernel(const SimtArgs<T> a) {
+template <typename T, int R, bool kVec, int VT>
+__global__ void __launch_bounds__(VT, (sizeof(T) == 4 ? 5 : 3) * (128 / VT)) paged_gates_kernel(const SimtArgs<T> a) {
   constexpr int EV = Cols<T>::EV;
   constexpr int U = R == 1 ? 8 : 4;  // keys of a batch of loads
   __shared__ __align__(16) int tok[kSpanMax + 3 * U];
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) p
   const size_t th = (size_t)tile * heads + hl;
   // the span's tokens, and some more for the loads that run ahead (any token of the pool does)
   bool bad = false;
-  for (int i = t; i < nk + 3 * U; i += kVT) {
+  for (int i = t; i < nk + 3 * U; i += VT) {
     const int key = k0 + i, pi = key / a.p.page_size, pg = i < nk ? paged_page(a.p, tr.b, pi) : 0;
     bad |= pg < 0;
     tok[i] = i >= nk ? 0 : pg < 0 ? -1 : pg * a.p.page_size + (key - pi * a.p.page_size);
@@ -184,18 +184,18 @@ __global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) p
   if (!mine) return;
   const float* w = a.w + (th * a.key_pitch + k0) * R;
   // weights are not negative; -1 stands for a key to be skipped
-  for (int i = t; i < (nk + U) * R; i += kVT) ws[i] = i < nk * R ? __ldcg(w + i) : -1.f;
+  for (int i = t; i < (nk + U) * R; i += VT) ws[i] = i < nk * R ? __ldcg(w + i) : -1.f;
   bad = __syncthreads_or(bad);
   if (bad) {  // pages outside the pool: their gates count as zeros
-    for (int i = t; i < nk; i += kVT)
+    for (int i = t; i < nk; i += VT)
       if (tok[i] < 0) {
         tok[i] = 0;
         for (int r = 0; r < R; ++r) ws[i * R + r] = -1.f;
       }
     __syncthreads();
   }
-  const int c0 = chunk * kVT * EV + (kVec ? t * EV : t);  // first column of the head
-  constexpr int cs = kVec ? 1 : kVT;                      // and the step to the next
+  const int c0 = chunk * VT * EV + (kVec ? t * EV : t);  // first column of the head
+  constexpr int cs = kVec ? 1 : VT;                      // and the step to the next
   const bool live = c0 < a.m_h;
   constexpr int P = R > 1 ? 2 : 1;  // rows of an accumulator: pairs go through f32x2 arithmetic
   uint64_t acc2[R / P][EV];
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) p
   if (nsp > 1) {
     // This span's sums go to scratch; the block that finishes last of kJoin neighbouring spans
     // adds theirs up in order, and the last of those blocks the groups' sums.
-    constexpr size_t kSums = (size_t)R * kVT * EV;
+    constexpr size_t kSums = (size_t)R * VT * EV;
     float* base = a.part + (th * a.chunks + chunk) * a.gspans * kSums + t;
     int* count = a.count + (th * a.chunks + chunk) * a.counts;
     auto put = [&](int z) {
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) p
         for (int r = 0; r < R; ++r) {
           if (r >= tr.n) break;
 #pragma unroll
-          for (int e = 0; e < EV; ++e) __stcg(base + z * kSums + (r * EV + e) * kVT, acc[r][e]);
+          for (int e = 0; e < EV; ++e) __stcg(base + z * kSums + (r * EV + e) * VT, acc[r][e]);
         }
       }
     };
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) p
 #pragma unroll
           for (int r = 0; r < R; ++r) {
 #pragma unroll
-            for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(base + i * kSums + (r * EV + e) * kVT);
+            for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(base + i * kSums + (r * EV + e) * VT);
           }
         }
         return;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) p
 #pragma unroll 8
         for (int i = z; i < end; i += step) {
 #pragma unroll
-          for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(base + i * kSums + (r * EV + e) * kVT);
+          for (int e = 0; e < EV; ++e) acc[r][e] += __ldcg(base + i * kSums + (r * EV + e) * VT);
         }
       }
     };
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kVT, (sizeof(T) == 4 ? 5 : 3) * (128 / kVT)) p
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct SimtPlan {
-  int R, tiles, heads, spans, span_keys, gspans, chunks, counts, key_pitch;
+  int VT, R, tiles, heads, spans, span_keys, gspans, chunks, counts, key_pitch;
   size_t w, den, part, count, total;
 };
 
@@ -399,7 +399,10 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
   l.tiles = c.p.N / l.R + c.p.B;
   l.spans = ceil_div(c.p.max_len, kKeysBlk);
   l.key_pitch = l.spans * kKeysBlk;
-  l.chunks = ceil_div(c.m_h, kVT * EV);
+  // heads of up to 64 vectors: a wider block's other threads would idle (1,500 rows over 3,000
+  // keys, 4 x 256 gates, fp32: 370 -> 294 us)
+  l.VT = c.m_h <= kVT / 2 * EV ? kVT / 2 : kVT;
+  l.chunks = ceil_div(c.m_h, l.VT * EV);
   // spans of 512 keys, shorter where the grid would hold fewer than 20 blocks per SM (a block
   // starts with some 4 us of dependent look-ups and its sums are written and read again: over
   // batches of 1 to 276 new rows, fp32, 147 us on average against 153 with 32; with 16 the
@@ -412,14 +415,14 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
   l.counts = 1 + ceil_div(l.gspans, kJoin);
   // heads of a pass: as many as keep the scratch near 1 GB
   const size_t per_head = (size_t)l.tiles * ((size_t)l.key_pitch * l.R * 4 + (size_t)l.spans * l.R * 4 +
-                                             (size_t)l.chunks * l.gspans * l.R * kVT * EV * 4 + (size_t)l.chunks * l.counts * 4);
+                                             (size_t)l.chunks * l.gspans * l.R * l.VT * EV * 4 + (size_t)l.chunks * l.counts * 4);
   const size_t fit = (size_t(1) << 30) / (per_head ? per_head : 1);
   l.heads = (int)(fit < 1 ? 1 : fit > (size_t)c.H ? (size_t)c.H : fit);
   const size_t th = (size_t)l.tiles * l.heads;
   l.w = 0;
   l.den = l.w + align256(th * l.key_pitch * l.R * 4);
   l.part = l.den + align256(th * l.spans * l.R * 4);
-  l.count = l.part + align256(th * l.chunks * l.gspans * l.R * kVT * EV * 4);
+  l.count = l.part + align256(th * l.chunks * l.gspans * l.R * l.VT * EV * 4);
   l.total = l.count + align256(th * l.chunks * l.counts * 4);
   return l;
 }
@@ -452,15 +455,19 @@ cudaError_t run(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = gg;
-    cfg.blockDim = dim3(kVT);
+    cfg.blockDim = dim3(l.VT);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true>, a)
-             : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false>, a);
+    if (l.VT == kVT)
+      e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true, kVT>, a)
+               : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false, kVT>, a);
+    else
+      e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true, kVT / 2>, a)
+               : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false, kVT / 2>, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
