@@ -414,10 +414,13 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, GBars& 
   return false;
 }
 
-// The same for a whole warp: one lane polls, every lane returns its answer.
+// The same for a whole warp: one lane polls, every lane returns its answer.  What the barrier
+// guards (jobs, pages, copied gates) is read by all lanes: __syncwarp hands the polling lane's
+// view of memory to the others, which the shuffle does not.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars& b, const TcArgs& a) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, b, a);
+  __syncwarp();
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
