@@ -13,6 +13,7 @@ Functions (same names as the C ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -471,6 +472,26 @@ def wango_decode_step(q, k, g, v, out, state, pos, *, H, window, s=10.0, tau=Non
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_HERE = contextlib.nullcontext()
+
+
+def _on_device(dev):
+    """The context that a call on tensors of device dev runs in.  The library launches on the
+    current device and sizes its grids and scratch by it, so another one is made current for the
+    call; host tensors (dev < 0) are refused, as their addresses mean nothing to a kernel."""
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    return _HERE if dev == _current_device() else torch.cuda.device(dev)
+
+
+def _given_ws(ws, dev):
+    """A caller's scratch, checked as far as the library's own size check does not see."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous memory of the call's device")
+    return ws
+
+
 def _stream_on(stream, dev):
     """The stream to launch on: the caller's, or device dev's current one."""
     if stream is None and _raw_stream is not None and dev >= 0:
@@ -581,7 +602,8 @@ def tango_qk_norm_rope(q, k, q_out, k_out, freqs, *, H, H_k=None, positions=None
     per row, or None (the index along T).  q_gain, k_gain: float32 [d_h] or None."""
     p, (qo, ko), dev = _qk_params(q, k, (("q_out", q_out, q), ("k_out", k_out, k)), freqs, H, H_k, positions, layout,
                                   norm, q_gain, k_gain, eps)
-    st = (_lib or load()).tango_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), qo, ko, _stream_on(stream, dev))
+    with _on_device(dev):
+        st = (_lib or load()).tango_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), qo, ko, _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_qk_norm_rope")
     return q_out, k_out
@@ -598,11 +620,13 @@ def tango_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, freqs, *, H, H_k=N
     dqg = _optional(dq_gain, "dq_gain", torch.float32, dev, (p.d_h,))
     dkg = _optional(dk_gain, "dk_gain", torch.float32, dev, (p.d_h,))
     wp, wn, wbuf = None, 0, None
-    if dqg is not None or dkg is not None:
-        wbuf = _scratch(load().tg_workspace_size(TG_WS_QK_BWD, ctypes.byref(p)), q.device, ws, stream)
-        wp, wn = _ws_ptr(wbuf)
-    st = load().tango_qk_norm_rope_backward(ctypes.byref(p), _ptr(q), _ptr(k), dqo, dko, dqp, dkp, dqg, dkg, wp, wn,
-                                            _stream_on(stream, dev))
+    with _on_device(dev):
+        if dqg is not None or dkg is not None:
+            wbuf = _given_ws(ws, dev) if ws is not None else _scratch(
+                load().tg_workspace_size(TG_WS_QK_BWD, ctypes.byref(p)), q.device, None, stream)
+            wp, wn = _ws_ptr(wbuf)
+        st = load().tango_qk_norm_rope_backward(ctypes.byref(p), _ptr(q), _ptr(k), dqo, dko, dqp, dkp, dqg, dkg, wp,
+                                                wn, _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_qk_norm_rope_backward")
     return dq, dk
@@ -669,9 +693,10 @@ def tango_cache_append(q, k, g, q_out, k_pages, g_pages, page_table, cu_new, len
         fp = _dense(freqs, "freqs", torch.float64, dev)
         rotary = 2 * freqs.numel()
     a = tg_append_params(rotary, layout, norm, eps, fp, 1 if silu else 0, q_pitch, k_pitch, g_pitch)
-    st = (_lib or load()).tango_cache_append(ctypes.byref(p), ctypes.byref(a), _ptr(q), k.data_ptr(),
-                                             g.data_ptr(), qo, k_pages.data_ptr(), g_pages.data_ptr(),
-                                             _stream_on(stream, dev))
+    with _on_device(dev):
+        st = (_lib or load()).tango_cache_append(ctypes.byref(p), ctypes.byref(a), _ptr(q), k.data_ptr(),
+                                                 g.data_ptr(), qo, k_pages.data_ptr(), g_pages.data_ptr(),
+                                                 _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_cache_append")
     return q_out
@@ -696,10 +721,12 @@ def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens,
     p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=max_new, max_len=max_len, m_h=m_h,
                      s=s, tau=tau, null_bias=null_bias, v_pitch=v_pitch)
     lib, ref = _lib or load(), ctypes.byref(p)
-    wbuf = ws if ws is not None else _scratch(lib.tg_workspace_size(TG_WS_PAGED, ref), q.device, None, stream)
-    wp, wn = _ws_ptr(wbuf)
-    st = lib.tango_paged_aggregate(ref, qp, _ptr(v), op, k_pages.data_ptr(), g_pages.data_ptr(), wp, wn,
-                                   _stream_on(stream, dev))
+    with _on_device(dev):
+        wbuf = _given_ws(ws, dev) if ws is not None else _scratch(lib.tg_workspace_size(TG_WS_PAGED, ref), q.device,
+                                                                  None, stream)
+        wp, wn = _ws_ptr(wbuf)
+        st = lib.tango_paged_aggregate(ref, qp, _ptr(v), op, k_pages.data_ptr(), g_pages.data_ptr(), wp, wn,
+                                       _stream_on(stream, dev))
     if st != TG_OK:
         raise TgError(st, "tango_paged_aggregate")
     return out

@@ -195,3 +195,71 @@ def test_binding_checks_tensors(lib):
         tg.tango_cache_append(None, q, out, q, kp, gp, **ok, freqs=fr, H=2)
     with pytest.raises(ValueError):
         tg.tango_cache_append(None, q, out[:, :200], None, kp, gp, **ok, freqs=fr, H=2)
+
+
+def _cpu_calls():
+    """Well-formed calls of all four functions on host tensors."""
+    bf, i32 = torch.bfloat16, torch.int32
+    x, dx, gain = torch.ones(4, 128, dtype=bf), torch.ones(4, 128, dtype=bf), torch.ones(64)
+    fr = torch.zeros(32, dtype=torch.float64)
+    kp, gp = tg.cache_pools(4, 16, 2, 64, 104, device="cpu")
+    batch = (torch.zeros(1, 2, dtype=i32), torch.tensor([0, 4], dtype=i32), torch.tensor([4], dtype=i32))
+    g = torch.ones(4, 208, dtype=bf)
+    return [lambda: tg.tango_qk_norm_rope(x, None, dx, None, fr, H=2),
+            lambda: tg.tango_qk_norm_rope_backward(x, None, dx, None, dx, None, fr, H=2, q_gain=gain, dq_gain=gain.clone()),
+            lambda: tg.tango_cache_append(x, x, g, dx, kp, gp, *batch, fr, H=2),
+            lambda: tg.tango_paged_aggregate(x, g, torch.ones(4, 208, dtype=bf), kp, gp, *batch, H=2, max_new=4, max_len=4)]
+
+
+class _NoCalls:
+    """The library with its launching functions replaced: a call that gets there is recorded."""
+
+    def __init__(self):
+        self.raw, self.calls = tg.load(), []
+
+    def __getattr__(self, name):
+        if not name.startswith("tango_"):
+            return getattr(self.raw, name)
+        return lambda *a: self.calls.append(name) or tg.TG_OK
+
+
+def test_host_tensors_are_refused_before_the_library_sees_them(lib, monkeypatch):
+    fake = _NoCalls()
+    monkeypatch.setattr(tg, "_lib", fake)
+    for call in _cpu_calls():
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    assert fake.calls == []
+
+
+def test_calls_run_on_their_tensors_device(lib, monkeypatch):
+    """Where another device is current, the tensors' own is made current for the workspace's
+    size, the stream and the launch, and given back."""
+    seen = []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            seen.append(self.dev)
+
+        def __exit__(self, *a):
+            seen.append("left")
+    monkeypatch.setattr(tg, "_current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    with tg._on_device(1):
+        assert seen == []
+    with tg._on_device(0):
+        assert seen == [0]
+    assert seen == [0, "left"]
+
+
+def test_given_workspaces_are_checked():
+    """Scratch of another device, or with gaps, is refused."""
+    ws = torch.zeros(512, dtype=torch.uint8)
+    assert tg._given_ws(ws, -1) is ws
+    with pytest.raises(ValueError):
+        tg._given_ws(ws, 0)
+    with pytest.raises(ValueError):
+        tg._given_ws(ws[::2], -1)
