@@ -41,7 +41,8 @@ constexpr int kVT = 128;        // column vectors of a gates block, half of them
 template <typename T>
 struct SimtArgs {
   PagedBatch p;
-  int H, d_h, m_h, m_pitch, h0;  // heads [h0, h0 + gridDim heads)
+  int H, d_h, m_h, m_pitch;
+  int h0, tile0;                 // the pass: heads from h0, tiles from tile0 (the grid says how many)
   int key_pitch;                 // keys of a (tile, head) in the weights scratch
   int spans;                     // score spans: ceil(max_len / kKeysBlk)
   int span_keys, gspans;         // keys of a gates block's span; spans of the longest sequence
@@ -54,10 +55,11 @@ struct SimtArgs {
   const T *q, *v;
   T* out;
   const T *k_pages, *g_pages;
-  float* w;     // [tile][head of the pass][key][R]
-  float* den;   // [tile][head of the pass][span][R]
-  float* part;  // [tile][head of the pass][chunk][gspan][R][128 EV]
-  int* count;   // [tile][head of the pass][chunk][counts]: spans or groups that are done
+  // scratch, by the tile and head of the pass
+  float* w;     // [tile][head][key][R]
+  float* den;   // [tile][head][span][R]
+  float* part;  // [tile][head][chunk][gspan][R][VT EV]
+  int* count;   // [tile][head][chunk][counts]: spans or groups that are done
 };
 
 // grid (tiles, heads, spans), 128 threads.
@@ -65,8 +67,8 @@ template <typename T, int R, bool kVec>
 __global__ void __launch_bounds__(kKeysBlk) paged_scores_kernel(const SimtArgs<T> a) {
   __shared__ __align__(16) float qs[R][128];
   __shared__ float red[kKeysBlk / 32][R];
-  const int tile = blockIdx.x, hl = blockIdx.y, head = a.h0 + hl, t = threadIdx.x;
-  const size_t th = (size_t)tile * gridDim.y + hl;
+  const int tile = a.tile0 + blockIdx.x, hl = blockIdx.y, head = a.h0 + hl, t = threadIdx.x;
+  const size_t th = (size_t)blockIdx.x * gridDim.y + hl;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.z == 0)
     for (int c = t; c < a.chunks * a.counts; c += kKeysBlk) a.count[th * a.chunks * a.counts + c] = 0;
@@ -164,7 +166,8 @@ __global__ void __launch_bounds__(VT, (sizeof(T) == 4 ? 5 : 3) * (128 / VT)) pag
   __shared__ __align__(16) float ws[(kSpanMax + U) * R];
   __shared__ float dinv[R];
   __shared__ int last;
-  const int tile = blockIdx.x, hl = blockIdx.y / a.chunks, chunk = blockIdx.y - hl * a.chunks, head = a.h0 + hl;
+  const int tile = a.tile0 + blockIdx.x, hl = blockIdx.y / a.chunks, chunk = blockIdx.y - hl * a.chunks;
+  const int head = a.h0 + hl;
   const int heads = gridDim.y / a.chunks, t = threadIdx.x;
   // launched while the scores kernel still runs: what follows up to the wait is not its work
   const TileRef tr = find_tile<R>(a.p, tile, false);
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(VT, (sizeof(T) == 4 ? 5 : 3) * (128 / VT)) pag
   const int nsp = max(1, (vis + a.span_keys - 1) / a.span_keys);
   const bool mine = tr.n > 0 && (int)blockIdx.z < nsp;
   const int nk = mine ? min(a.span_keys, vis - k0) : 0;
-  const size_t th = (size_t)tile * heads + hl;
+  const size_t th = (size_t)blockIdx.x * heads + hl;
   // the span's tokens, and some more for the loads that run ahead (any token of the pool does)
   bool bad = false;
   for (int i = t; i < nk + 3 * U; i += VT) {
@@ -387,8 +390,11 @@ __global__ void __launch_bounds__(VT, (sizeof(T) == 4 ? 5 : 3) * (128 / VT)) pag
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+constexpr size_t kScratch = size_t(1) << 30;  // of a pass
+
 struct SimtPlan {
-  int VT, R, tiles, heads, spans, span_keys, gspans, chunks, counts, key_pitch;
+  int VT, R, tiles, spans, span_keys, gspans, chunks, counts, key_pitch;
+  int heads, pass_tiles;  // of a pass
   size_t w, den, part, count, total;
 };
 
@@ -413,12 +419,15 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
     l.span_keys /= 2;
   l.gspans = ceil_div(c.p.max_len, l.span_keys);
   l.counts = 1 + ceil_div(l.gspans, kJoin);
-  // heads of a pass: as many as keep the scratch near 1 GB
-  const size_t per_head = (size_t)l.tiles * ((size_t)l.key_pitch * l.R * 4 + (size_t)l.spans * l.R * 4 +
-                                             (size_t)l.chunks * l.gspans * l.R * l.VT * EV * 4 + (size_t)l.chunks * l.counts * 4);
-  const size_t fit = (size_t(1) << 30) / (per_head ? per_head : 1);
-  l.heads = (int)(fit < 1 ? 1 : fit > (size_t)c.H ? (size_t)c.H : fit);
-  const size_t th = (size_t)l.tiles * l.heads;
+  // A pass takes as many heads as fit kScratch, or, where one does not, as many tiles of one
+  // head; never less than one tile of one head (4 R bytes a key for the weights, 4 R / span_keys
+  // bytes a key and gate for the sums: 1.6 % of an fp32 cache's own bytes in spans of 512).
+  const size_t per = (size_t)l.key_pitch * l.R * 4 + (size_t)l.spans * l.R * 4 +
+                     (size_t)l.chunks * l.gspans * l.R * l.VT * EV * 4 + (size_t)l.chunks * l.counts * 4;
+  const size_t fit = kScratch / per;  // (tile, head) pairs
+  l.heads = (int)(fit / l.tiles < 1 ? 1 : fit / l.tiles > (size_t)c.H ? (size_t)c.H : fit / l.tiles);
+  l.pass_tiles = (int)(fit < 1 ? 1 : fit > (size_t)l.tiles ? (size_t)l.tiles : fit);
+  const size_t th = (size_t)l.pass_tiles * l.heads;
   l.w = 0;
   l.den = l.w + align256(th * l.key_pitch * l.R * 4);
   l.part = l.den + align256(th * l.spans * l.R * 4);
@@ -446,29 +455,32 @@ cudaError_t run(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
   // into the next head
   const bool gvec = al(c.g_pages) && c.m_pitch * sizeof(T) % 16 == 0;
   for (a.h0 = 0; a.h0 < c.H; a.h0 += l.heads) {
-    const int heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
-    const dim3 gs(l.tiles, heads, l.spans), gg(l.tiles, heads * l.chunks, l.gspans);
-    if (gs.z > 65535 || gg.y > 65535 || gg.z > 65535) return cudaErrorInvalidConfiguration;
-    if (kvec) paged_scores_kernel<T, R, true><<<gs, kKeysBlk, 0, s>>>(a);
-    else paged_scores_kernel<T, R, false><<<gs, kKeysBlk, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = gg;
-    cfg.blockDim = dim3(l.VT);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (l.VT == kVT)
-      e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true, kVT>, a)
-               : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false, kVT>, a);
-    else
-      e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true, kVT / 2>, a)
-               : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false, kVT / 2>, a);
-    if (e != cudaSuccess) return e;
+    for (a.tile0 = 0; a.tile0 < l.tiles; a.tile0 += l.pass_tiles) {
+      const int heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
+      const int tiles = l.tiles - a.tile0 < l.pass_tiles ? l.tiles - a.tile0 : l.pass_tiles;
+      const dim3 gs(tiles, heads, l.spans), gg(tiles, heads * l.chunks, l.gspans);
+      if (gs.z > 65535 || gg.y > 65535 || gg.z > 65535) return cudaErrorInvalidConfiguration;
+      if (kvec) paged_scores_kernel<T, R, true><<<gs, kKeysBlk, 0, s>>>(a);
+      else paged_scores_kernel<T, R, false><<<gs, kKeysBlk, 0, s>>>(a);
+      cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = gg;
+      cfg.blockDim = dim3(l.VT);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (l.VT == kVT)
+        e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true, kVT>, a)
+                 : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false, kVT>, a);
+      else
+        e = gvec ? cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, true, kVT / 2>, a)
+                 : cudaLaunchKernelEx(&cfg, paged_gates_kernel<T, R, false, kVT / 2>, a);
+      if (e != cudaSuccess) return e;
+    }
   }
   return cudaSuccess;
 }

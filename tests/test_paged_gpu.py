@@ -521,3 +521,36 @@ def test_append_then_aggregate_equals_the_whole_sequence():
         tg.tango_paged_aggregate(qo, v[a:e], out, kp, gp, table, cu, ln, H=H, max_new=e - a, max_len=T)
         assert (out - whole[0, a:e]).abs().max().item() <= 2e-5 * whole.abs().max().item()
         a = e
+
+
+# ------------------------------------------------------------------------------ passes
+
+PASSES = [(130, 300), (1, 700), (40, 41), (0, 9), (64, 600), (60, 60)]  # 295 rows
+
+
+def _loose(b, max_len):
+    """The batch with a page table that a bound of max_len tokens needs, and its scratch with
+    H heads."""
+    b.table = torch.cat([b.table, b.table.new_full((b.B, -(-max_len // b.page)), -1)], 1).contiguous()
+
+    def scratch(H):
+        p = tg.paged_params(b.N, b.k_pages, b.g_pages, b.table, b.cu, b.lens, H=b.H, max_new=b.max_new, max_len=max_len,
+                            m_h=b.m_h)
+        p.m, p.H = p.m // p.H * H, H
+        return tg.tg_workspace_size(tg.TG_WS_PAGED, p)
+    return scratch
+
+
+@pytest.mark.parametrize("dtype,d_h", [("f32", 32), ("bf16", 128)])
+def test_cuda_core_passes_over_heads_and_tiles(dtype, d_h):
+    """Bounds far above the batch make one pass's scratch too small for all heads, then for all
+    tiles of one head; the last pass of either kind is a shorter one."""
+    for max_len, by_tiles in ((1 << 17, False), (900000, True)):
+        b = Batch(PASSES, 7, d_h, 72, dtype, 64, seed=60)
+        scratch = _loose(b, max_len)
+        assert scratch(7) <= (1 << 30) + (1 << 16)
+        # one head at a time; or several, but not all
+        assert (scratch(7) == scratch(1)) == by_tiles and scratch(7) < 6 * scratch(1)
+        null = torch.linspace(-1, 2, 7).cuda()
+        got = b.check(null=null, max_len=max_len)
+        assert torch.equal(b.run(null=null, max_len=max_len).double().cpu().view(b.N, 7, -1), got)

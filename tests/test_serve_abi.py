@@ -263,3 +263,29 @@ def test_given_workspaces_are_checked():
         tg._given_ws(ws, 0)
     with pytest.raises(ValueError):
         tg._given_ws(ws[::2], -1)
+
+
+def _wide(B, N, max_len, dtype, **kw):
+    """A batch at the paper's gate width over pages of 64 tokens."""
+    base = dict(B=B, N=N, max_new=-(-N // B), max_len=max_len, m=28480, page_size=64, n_pages=1 << 14,
+                table_pitch=-(-max_len // 64), dtype=dtype)
+    base.update(kw)
+    return _paged(**base)
+
+
+@pytest.mark.parametrize("B,N,max_len", [(1, 2048, 8192), (1, 8192, 8192), (8, 16384, 8192), (1, 2048, 131072),
+                                         (8, 16384, 65536), (257, 768, 32768), (4096, 4096, 131072)])
+def test_cuda_core_scratch_stays_within_a_pass(lib, B, N, max_len):
+    """Whatever the rows and the length, the weights and partial sums of one pass: 1 GB."""
+    for p in (_wide(B, N, max_len, tg.TG_F32), _wide(B, N, max_len, tg.TG_BF16, d_h=128),
+              _wide(B, N, max_len, tg.TG_F32, m=9494, max_new=N)):
+        assert 0 < tg.tg_workspace_size(tg.TG_WS_PAGED, p) <= (1 << 30) + (1 << 16)
+
+
+def test_cuda_core_scratch_of_one_tile(lib):
+    """Where one tile of 8 rows of one head is more, it is that: 32 bytes a key, and 8 sums of 4
+    bytes for every 512 keys and gate (gates in whole blocks of 512 columns)."""
+    length = 1 << 22
+    p = _wide(1, 64, length, tg.TG_F32)
+    most = 32 * length + 8 * 4 * (length // 512) * (28 * 512) + length
+    assert (1 << 30) < tg.tg_workspace_size(tg.TG_WS_PAGED, p) <= most
