@@ -87,7 +87,8 @@ struct TcArgs {
   PagedBatch p;
   int H, d_h, m_h, m_pitch;
   int h0, heads;             // heads of this pass
-  int rows_tot;              // scratch rows of a head: up8(N) + 8 B
+  int row0, rows;            // tiles of this pass: scratch rows from row0 on, in a span of `rows`
+  int rows_tot;              // scratch rows of a head: those, and one tile's more unless it is all
   int key_blocks;            // ceil(max_len / 64)
   int span_keys, spans;      // of the weights kernel; spans: ceil(max_len / span_keys), up to 4s
   int strips;                // ceil(m_h / 256)
@@ -115,8 +116,9 @@ struct TcArgs {
   uint64_t timeout_ns;
 };
 
-// Scratch row of a sequence's first row: sequences start at multiples of 8.
-__device__ __forceinline__ int scratch_row(int r0, int b) { return up8(r0) + 8 * b; }
+// Scratch row of a sequence's first row: sequences start at multiples of 8.  Less than 0, or
+// from a.rows on, a tile belongs to another pass.
+__device__ __forceinline__ int scratch_row(const TcArgs& a, int r0, int b) { return up8(r0) + 8 * b - a.row0; }
 // P of key block kb of a tile with r8 scratch rows.
 __device__ __forceinline__ uint8_t* p_block(const TcArgs& a, int hl, int prow, int r8, int kb) {
   return a.P + (((size_t)hl * a.rows_tot + prow) * a.key_blocks + (size_t)kb * r8) * 128;
@@ -154,7 +156,8 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
   const int key0 = span * a.span_keys, key1 = min(key0 + a.span_keys, (vis + 63) & ~63);
   if (tr.n == 0 || vis <= 0 || key0 >= vis) return;
   const PagedSeq sq = paged_seq(a.p, tr.b, false);
-  const int prow = scratch_row(sq.r0, tr.b) + (tr.row0 - sq.r0), r8 = up8(tr.n);
+  const int prow = scratch_row(a, sq.r0, tr.b) + (tr.row0 - sq.r0), r8 = up8(tr.n);
+  if (prow < 0 || prow >= a.rows) return;
 
   if (t == 0) {
     mbar_init(bar, 1);
@@ -293,7 +296,8 @@ __global__ void __launch_bounds__(kWThreads, 4) paged_weights_few_kernel(const T
   if (tr.n == 0 || vis <= 0 || key0 >= vis) return;
   const int rows = min(tr.n, R);  // R >= max_new
   const PagedSeq sq = paged_seq(a.p, tr.b, false);
-  const int prow = scratch_row(sq.r0, tr.b), r8 = up8(tr.n);
+  const int prow = scratch_row(a, sq.r0, tr.b), r8 = up8(tr.n);
+  if (prow < 0 || prow >= a.rows) return;
   constexpr int C = DH / 8;
   uint4 u[C];
   auto load = [&](int key) {
@@ -428,11 +432,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars&
 // are written too.
 __device__ __forceinline__ int steps_of(int vis) { return max(1, (vis + kK - 1) / kK); }
 
-// Steps of one (head, strip) of a sequence, all its tiles.
-__device__ __forceinline__ long long seq_steps(const PagedSeq& s) {
-  if (s.n == 0) return 0;
-  const long long mt = (s.n + kM - 1) / kM, before = max(0, s.len - s.n + kK - 1) / kK;
-  return (mt - 1) * before + mt * (mt - 1) + steps_of(s.len);
+// A sequence's row tiles of this pass, [t0, t1).
+struct SeqTiles {
+  int t0, t1;
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const TcArgs& a, const PagedSeq& s, int b) {
+  const int at = scratch_row(a, s.r0, b), mt = (s.n + kM - 1) / kM;
+  SeqTiles t;
+  t.t0 = min(mt, (max(0, -at) + kM - 1) / kM);
+  t.t1 = max(t.t0, min(mt, (max(0, a.rows - at) + kM - 1) / kM));
+  return t;
+}
+// Keys that a sequence's tiles up to t1 see.
+__device__ __forceinline__ int seq_vis(const PagedSeq& s, int t1) { return s.len - s.n + min(s.n, t1 * kM); }
+// Steps of one (head, strip) of a sequence's tiles [t0, t1): whole tiles, each two steps more
+// than the one before, and the last one.
+__device__ __forceinline__ long long seq_steps(const PagedSeq& s, const SeqTiles& t) {
+  if (t.t0 >= t.t1) return 0;
+  const long long before = max(0, s.len - s.n + kK - 1) / kK, x = t.t0, y = t.t1 - 1;
+  return (y - x) * before + y * (y + 1) - x * (x + 1) + steps_of(seq_vis(s, t.t1));
 }
 
 // Key ranges of a tile of u steps: as many as of `range` steps come nearest.
@@ -476,7 +494,10 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
   // steps of the whole launch, and from them the steps of a key range
   const int HS = a.heads * a.strips;
   long long total = 0;
-  for (int i = lane; i < a.p.B; i += 32) total += seq_steps(paged_seq(a.p, i, false));
+  for (int i = lane; i < a.p.B; i += 32) {
+    const PagedSeq s = paged_seq(a.p, i, false);
+    total += seq_steps(s, seq_tiles(a, s, i));
+  }
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= HS;
   const long long want = a.jobs_per_sm * (long long)gridDim.x;
@@ -486,7 +507,7 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
   int w0 = -32;
   long long jbase = 0, jend = 0, pre = 0;
   PagedSeq ws{0, 0, 0};
-  int wmt = 0;
+  SeqTiles wt{0, 0};
   Ring jr;
   bool first = true;
   uint32_t taken = 0;        // jobs handed out and nearly copied
@@ -498,8 +519,8 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       long long jobs = 0;
       if (w0 + lane < a.p.B) {
         ws = paged_seq(a.p, w0 + lane, false);
-        wmt = (ws.n + kM - 1) / kM;
-        jobs = (long long)wmt * ranges_of(steps_of(ws.len), range) * HS;
+        wt = seq_tiles(a, ws, w0 + lane);
+        jobs = (long long)(wt.t1 - wt.t0) * ranges_of(steps_of(seq_vis(ws, wt.t1)), range) * HS;
       }
       pre = jobs;
       for (int o = 1; o < 32; o <<= 1) {
@@ -517,11 +538,12 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       const long long before = __shfl_sync(0xffffffffu, pre, owner > 0 ? owner - 1 : 0);
       const int idx = (int)(rel - (owner > 0 ? before : 0));
       const int r0 = __shfl_sync(0xffffffffu, ws.r0, owner), n = __shfl_sync(0xffffffffu, ws.n, owner);
-      const int len = __shfl_sync(0xffffffffu, ws.len, owner), mt = __shfl_sync(0xffffffffu, wmt, owner);
+      const int len = __shfl_sync(0xffffffffu, ws.len, owner), t1 = __shfl_sync(0xffffffffu, wt.t1, owner);
+      const int mt = t1 - __shfl_sync(0xffffffffu, wt.t0, owner);
       // row tiles of a strip side by side (they share G in L2), then the strips of the same
       // keys (they share DRAM pages), then the key ranges; later row tiles, the longer ones,
       // come first
-      const int ti = mt - 1 - idx % mt, hs = idx / mt % HS;
+      const int ti = t1 - 1 - idx % mt, hs = idx / mt % HS;
       job.c = idx / mt / HS;
       job.b = w0 + owner;
       job.row0 = r0 + ti * kM;
@@ -534,7 +556,7 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       job.it0 = (int)((long long)u * job.c / job.nc);  // never empty: u >= nc
       job.it1 = (int)((long long)u * (job.c + 1) / job.nc);
       job.tile = r0 / kM + job.b + ti;
-      job.prow = scratch_row(r0, job.b) + ti * kM;
+      job.prow = scratch_row(a, r0, job.b) + ti * kM;
       skip = job.c >= job.nc;  // a tile of the sequence that sees fewer keys
     }
     if (!skip) {
@@ -1151,15 +1173,18 @@ int box_rows(int page_size) {
   return r > kK ? kK : r;
 }
 
+constexpr size_t kScratch = size_t(2) << 30;  // P of a pass
+
 struct TcPlan {
-  int rows_tot, key_blocks, span_keys, spans, strips, tiles, r8cap, min_steps, jobs_per_sm, nc_cap, n_slots, heads, grid;
+  int rows_all, rows, rows_tot;  // scratch rows of a head: of all tiles; of a pass's starts; in a pass
+  int key_blocks, span_keys, spans, strips, tiles, r8cap, min_steps, jobs_per_sm, nc_cap, n_slots, heads, grid;
   size_t P, den, part, slot, done, next, total;
 };
 
 TcPlan tc_plan(const PagedCall& c) {
   TcPlan l;
   const int sms = serve_sm_count();
-  l.rows_tot = up8(c.p.N) + 8 * c.p.B;
+  l.rows_all = up8(c.p.N) + 8 * c.p.B;
   l.key_blocks = ceil_div(c.p.max_len, kK);
   // at most 32 spans of whole 128-key blocks (their sums are added once per strip)
   l.span_keys = ceil_div(ceil_div(c.p.max_len, 32), 128) * 128;
@@ -1172,17 +1197,29 @@ TcPlan tc_plan(const PagedCall& c) {
   // take, so tiles are left whole when they are about two per SM
   l.min_steps = 8;
   l.jobs_per_sm = l.r8cap <= kFewRows ? kJobsPerSm : 2;
-  l.nc_cap = ceil_div(l.key_blocks, l.min_steps);
   l.grid = sms;
   // a tile that is cut has at most 4/3 as many ranges as whole ranges fit in it; two halves
   l.n_slots = 2 * 2 * kJobsPerSm * sms;
-  // heads of a pass: as many as keep P within 2 GB
-  const size_t per_head = (size_t)l.rows_tot * l.key_blocks * 128;
-  const size_t fit = (size_t(2) << 30) / per_head;
-  l.heads = (int)(fit < 1 ? 1 : fit > (size_t)c.H ? (size_t)c.H : fit);
+  // A pass takes as many heads as keep P within kScratch, or, where one does not, the tiles of
+  // one head that start within so many rows (whole tiles' worth of starts: a tile's rows may
+  // reach one tile further); never less than 128 starts, 256 rows.
+  const size_t per_row = (size_t)l.key_blocks * 128, fit = kScratch / per_row;
+  l.rows = l.rows_tot = l.rows_all;
+  l.heads = 1;
+  if (fit < (size_t)l.rows_all) {
+    l.rows = fit < 3 * kM ? kM : (int)((fit - kM) / kM * kM);
+    l.rows_tot = l.rows + kM;
+  } else {
+    l.heads = (int)(fit / l.rows_all > (size_t)c.H ? (size_t)c.H : fit / l.rows_all);
+  }
+  // A tile's steps are at most the launch's in one of its heads and strips, so that it has no
+  // more ranges than the launch has jobs for each of these.
+  const int least = (c.H % l.heads ? c.H % l.heads : l.heads) * l.strips;
+  l.nc_cap = ceil_div(l.key_blocks, l.min_steps);
+  if (l.nc_cap > l.jobs_per_sm * l.grid / least + 1) l.nc_cap = l.jobs_per_sm * l.grid / least + 1;
   const size_t tk = (size_t)l.heads * l.strips * l.tiles * 2;
   l.P = 0;
-  l.den = l.P + align256(per_head * l.heads);
+  l.den = l.P + align256((size_t)l.heads * l.rows_tot * per_row);
   l.part = l.den + align256((size_t)l.heads * l.rows_tot * l.spans * 4);
   l.slot = l.part + align256((size_t)l.n_slots * (kN / 2) * l.r8cap * 4);
   l.done = l.slot + align256(tk * l.nc_cap * 4);
@@ -1233,7 +1270,7 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   const TcPlan l = tc_plan(c);
   TcArgs a = {};
   a.p = c.p; a.H = c.H; a.d_h = c.d_h; a.m_h = c.m_h; a.m_pitch = c.m_pitch;
-  a.rows_tot = l.rows_tot; a.key_blocks = l.key_blocks; a.span_keys = l.span_keys; a.spans = l.spans;
+  a.rows = l.rows; a.rows_tot = l.rows_tot; a.key_blocks = l.key_blocks; a.span_keys = l.span_keys; a.spans = l.spans;
   a.strips = l.strips; a.tiles = l.tiles; a.r8cap = l.r8cap; a.min_steps = l.min_steps; a.jobs_per_sm = l.jobs_per_sm; a.nc_cap = l.nc_cap; a.n_slots = l.n_slots;
   a.box_rows = box_rows(c.p.page_size);
   a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
@@ -1258,24 +1295,26 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   if (e == cudaSuccess) e = allow_shared_memory();
   if (e != cudaSuccess) return e;
   for (a.h0 = 0; a.h0 < c.H; a.h0 += l.heads) {
-    a.heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
-    const dim3 gw(l.tiles, a.heads, ceil_div(c.p.max_len, l.span_keys));
-    if (c.p.max_new > 8) paged_weights_kernel<<<gw, kWThreads, kWSmem, s>>>(a);
-    else launch_weights_few(a, c.p.max_new, gw, s);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(l.grid);
-    cfg.blockDim = dim3(kGThreads);
-    cfg.dynamicSmemBytes = kGSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_gates_kernel, mG, mG4, a);
-    if (e != cudaSuccess) return e;
+    for (a.row0 = 0; a.row0 < l.rows_all; a.row0 += l.rows) {
+      a.heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
+      const dim3 gw(l.tiles, a.heads, ceil_div(c.p.max_len, l.span_keys));
+      if (c.p.max_new > 8) paged_weights_kernel<<<gw, kWThreads, kWSmem, s>>>(a);
+      else launch_weights_few(a, c.p.max_new, gw, s);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(l.grid);
+      cfg.blockDim = dim3(kGThreads);
+      cfg.dynamicSmemBytes = kGSmem;
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaLaunchKernelEx(&cfg, paged_gates_kernel, mG, mG4, a);
+      if (e != cudaSuccess) return e;
+    }
   }
   return cudaSuccess;
 }

@@ -554,3 +554,23 @@ def test_cuda_core_passes_over_heads_and_tiles(dtype, d_h):
         null = torch.linspace(-1, 2, 7).cuda()
         got = b.check(null=null, max_len=max_len)
         assert torch.equal(b.run(null=null, max_len=max_len).double().cpu().view(b.N, 7, -1), got)
+
+
+@pytest.mark.parametrize("seqs,max_len,cut", [
+    (PASSES, 1 << 20, "heads"),                                             # 2 heads a pass, 7 in all
+    (PASSES + [(300, 420), (200, 200)], 1 << 21, "rows"),                   # 384 rows a pass
+    (PASSES, 1 << 23, "rows"),                                              # 128, the least
+    ([(1 + i % 8, 20 + 3 * i) for i in range(110)], 1 << 21, "rows"),       # single tokens and a few
+], ids=["heads", "rows", "least", "few"])
+def test_tensor_core_passes_over_heads_and_rows(seqs, max_len, cut):
+    """The same on the tensor cores, whose passes share the weights, denominators, partial sums
+    and counters: by heads, and by tiles of one head where its weights alone pass 2 GB."""
+    b = Batch(seqs, 7, 32, 72, "bf16", 64, seed=61)
+    scratch = _loose(b, max_len)
+    assert scratch(7) <= 5 << 30
+    assert (scratch(7) == scratch(1)) == (cut == "rows") and scratch(7) < 6 * scratch(1)
+    null = torch.linspace(-1, 2, 7).cuda()
+    got = b.check(null=null, max_len=max_len)
+    assert torch.equal(b.run(null=null, max_len=max_len).double().cpu().view(b.N, 7, -1), got)
+    # one pass over all of it: the same weights, summed in other ranges, each rounded once
+    assert (got - b.run(null=null).double().cpu().view(b.N, 7, -1)).abs().max().item() <= 2.0 ** -6 * got.abs().max().item()

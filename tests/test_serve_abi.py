@@ -289,3 +289,12 @@ def test_cuda_core_scratch_of_one_tile(lib):
     p = _wide(1, 64, length, tg.TG_F32)
     most = 32 * length + 8 * 4 * (length // 512) * (28 * 512) + length
     assert (1 << 30) < tg.tg_workspace_size(tg.TG_WS_PAGED, p) <= most
+
+
+@pytest.mark.parametrize("B,N,max_len", [(8, 65536, 131072), (1, 16384, 262144), (4096, 4096, 262144), (1, 2048, 1 << 20)])
+def test_tensor_core_scratch_stays_within_a_pass(lib, B, N, max_len):
+    """The weights of one pass within 2 GB (and what goes with them: denominators, partial sums,
+    counters: 1/4 GB), where the rows of one head alone would take more."""
+    assert 2 * (N + 8 * B) * max_len > 2 << 30
+    p = _wide(B, N, max_len, tg.TG_BF16)
+    assert 0 < tg.tg_workspace_size(tg.TG_WS_PAGED, p) <= (2 << 30) + (1 << 28)
