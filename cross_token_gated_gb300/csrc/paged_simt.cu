@@ -391,6 +391,10 @@ __global__ void __launch_bounds__(VT, (sizeof(T) == 4 ? 5 : 3) * (128 / VT)) pag
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr size_t kScratch = size_t(1) << 30;  // of a pass
+// Where the call would run on the tensor cores but for a pointer that is not 16-byte aligned:
+// no more than the tensor cores' own scratch, or 256 MB, so that aligned calls, whose scratch has
+// to hold either path's, need not bring more.
+constexpr size_t kScratchTwin = size_t(256) << 20;
 
 struct SimtPlan {
   int VT, R, tiles, spans, span_keys, gspans, chunks, counts, key_pitch;
@@ -419,12 +423,17 @@ SimtPlan simt_plan(tg_dtype dt, const PagedCall& c) {
     l.span_keys /= 2;
   l.gspans = ceil_div(c.p.max_len, l.span_keys);
   l.counts = 1 + ceil_div(l.gspans, kJoin);
-  // A pass takes as many heads as fit kScratch, or, where one does not, as many tiles of one
+  // A pass takes as many heads as fit its scratch, or, where one does not, as many tiles of one
   // head; never less than one tile of one head (4 R bytes a key for the weights, 4 R / span_keys
   // bytes a key and gate for the sums: 1.6 % of an fp32 cache's own bytes in spans of 512).
   const size_t per = (size_t)l.key_pitch * l.R * 4 + (size_t)l.spans * l.R * 4 +
                      (size_t)l.chunks * l.gspans * l.R * l.VT * EV * 4 + (size_t)l.chunks * l.counts * 4;
-  const size_t fit = kScratch / per;  // (tile, head) pairs
+  size_t most = kScratch;
+  if (paged_tc_takes(dt, c)) {
+    const size_t tc = paged_tc_ws_bytes(c);
+    most = tc < kScratchTwin ? kScratchTwin : tc < kScratch ? tc : kScratch;
+  }
+  const size_t fit = most / per;  // (tile, head) pairs
   l.heads = (int)(fit / l.tiles < 1 ? 1 : fit / l.tiles > (size_t)c.H ? (size_t)c.H : fit / l.tiles);
   l.pass_tiles = (int)(fit < 1 ? 1 : fit > (size_t)l.tiles ? (size_t)l.tiles : fit);
   const size_t th = (size_t)l.pass_tiles * l.heads;

@@ -574,3 +574,16 @@ def test_tensor_core_passes_over_heads_and_rows(seqs, max_len, cut):
     assert torch.equal(b.run(null=null, max_len=max_len).double().cpu().view(b.N, 7, -1), got)
     # one pass over all of it: the same weights, summed in other ranges, each rounded once
     assert (got - b.run(null=null).double().cpu().view(b.N, 7, -1)).abs().max().item() <= 2.0 ** -6 * got.abs().max().item()
+
+
+def test_passes_of_unaligned_calls():
+    """bf16 rows off 16 bytes take the CUDA cores in the scratch that the tensor cores would
+    need: more passes, the same values."""
+    b = Batch(PASSES, 7, 32, 72, "bf16", 64, seed=62)
+    scratch = _loose(b, 1 << 17)
+    assert scratch(7) < 1 << 30
+    x = torch.empty(b.q.numel() + 1, dtype=b.q.dtype, device="cuda")[1:].view(b.q.shape)
+    b.q = x.copy_(b.q)
+    null = torch.linspace(-1, 2, 7).cuda()
+    got = b.check(null=null, max_len=1 << 17)
+    assert torch.equal(b.run(null=null, max_len=1 << 17).double().cpu().view(b.N, 7, -1), got)

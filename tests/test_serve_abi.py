@@ -298,3 +298,13 @@ def test_tensor_core_scratch_stays_within_a_pass(lib, B, N, max_len):
     assert 2 * (N + 8 * B) * max_len > 2 << 30
     p = _wide(B, N, max_len, tg.TG_BF16)
     assert 0 < tg.tg_workspace_size(tg.TG_WS_PAGED, p) <= (2 << 30) + (1 << 28)
+
+
+@pytest.mark.parametrize("B,N,max_len", [(1, 2048, 8192), (8, 16384, 8192), (1, 2048, 131072), (257, 768, 32768),
+                                         (32, 32, 8192)])
+def test_tensor_core_calls_need_not_bring_the_other_paths_scratch(lib, B, N, max_len):
+    """bf16 calls have to hold either path's scratch (an address off 16 bytes takes the CUDA
+    cores): that path makes do with the tensor cores' own (weights of 2 bytes a row, key and
+    head, and up to 1/4 GB of sums), or 1/4 GB."""
+    weights = 2 * 2 * (N + 8 * B + 8) * max_len
+    assert 0 < tg.tg_workspace_size(tg.TG_WS_PAGED, _wide(B, N, max_len, tg.TG_BF16)) <= weights + (1 << 28)
