@@ -565,7 +565,7 @@ size_t paged_ws_bytes(const tg_paged_params* p) {
   if (p->N == 0) return 0;
   const PagedCall c = paged_call(p, nullptr);
   // pointers that are not 16-byte aligned take the CUDA-core kernels: room for either
-  const size_t simt = paged_simt_ws_bytes(p->dtype, c);
+  const size_t simt = paged_simt_takes(p->dtype, c) ? paged_simt_ws_bytes(p->dtype, c) : 0;
   if (!paged_tc_takes(p->dtype, c)) return simt;
   const size_t tc = paged_tc_ws_bytes(c);
   return tc > simt ? tc : simt;
@@ -878,13 +878,13 @@ tg_status tango_paged_aggregate(const tg_paged_params* p, const void* q, const v
   const void* ptrs[] = {q, v, out, k_pages, g_pages};
   for (const void* x : ptrs)
     if (!aligned_to(x, es)) return TG_ERR_UNSUPPORTED;
+  PagedCall c = paged_call(p, nullptr);
+  const bool tc = paged_tc_takes(p->dtype, c) && aligned16(q) && aligned16(out) && aligned16(k_pages) && aligned16(g_pages);
+  if (!tc && !paged_simt_takes(p->dtype, c)) return TG_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, paged_ws_bytes(p));
   if (st != TG_OK) return st;
-  unsigned* err = nullptr;
-  if (error_word(&err) != cudaSuccess) return TG_ERR_CUDA;
-  PagedCall c = paged_call(p, err);
+  if (error_word(&c.p.err) != cudaSuccess) return TG_ERR_CUDA;
   c.q = q; c.v = v; c.out = out; c.k_pages = k_pages; c.g_pages = g_pages; c.ws = ws;
-  const bool tc = paged_tc_takes(p->dtype, c) && aligned16(q) && aligned16(out) && aligned16(k_pages) && aligned16(g_pages);
   return cuda_status(tc ? launch_paged_tc(c, reinterpret_cast<cudaStream_t>(stream))
                         : launch_paged_simt(p->dtype, c, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -468,7 +468,6 @@ cudaError_t run(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
       const int heads = c.H - a.h0 < l.heads ? c.H - a.h0 : l.heads;
       const int tiles = l.tiles - a.tile0 < l.pass_tiles ? l.tiles - a.tile0 : l.pass_tiles;
       const dim3 gs(tiles, heads, l.spans), gg(tiles, heads * l.chunks, l.gspans);
-      if (gs.z > 65535 || gg.y > 65535 || gg.z > 65535) return cudaErrorInvalidConfiguration;
       if (kvec) paged_scores_kernel<T, R, true><<<gs, kKeysBlk, 0, s>>>(a);
       else paged_scores_kernel<T, R, false><<<gs, kKeysBlk, 0, s>>>(a);
       cudaError_t e = cudaGetLastError();
@@ -505,6 +504,11 @@ cudaError_t run_t(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool paged_simt_takes(tg_dtype dt, const PagedCall& c) {
+  const SimtPlan l = simt_plan(dt, c);  // (spans of gates are no more than spans of scores)
+  return l.spans <= 65535 && (long long)c.H * l.chunks <= 65535;
+}
 
 size_t paged_simt_ws_bytes(tg_dtype dt, const PagedCall& c) { return simt_plan(dt, c).total; }
 

@@ -57,6 +57,8 @@ struct PagedCall {
   const void *k_pages, *g_pages;
   void* ws;
 };
+// Whether the grids fit: max_len up to 65,535 x 128.
+bool paged_simt_takes(tg_dtype dt, const PagedCall& c);
 size_t paged_simt_ws_bytes(tg_dtype dt, const PagedCall& c);
 cudaError_t launch_paged_simt(tg_dtype dt, const PagedCall& c, cudaStream_t s);
 

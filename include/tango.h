@@ -505,7 +505,8 @@ tg_status tg_rope_freqs(int rotary_dim, double base, double factor, long long or
  * they reach no result.
  * TG_BF16 runs the aggregation on the tensor cores when d_h is 16, 32 or 64, m_pitch and page_size
  * are multiples of 8, and q, out and the pools are
- * 16-byte aligned; anything else, and TG_F32, runs on the CUDA cores.
+ * 16-byte aligned; anything else, and TG_F32, runs on the CUDA cores, which take max_len up to
+ * 8,388,480 (65,535 * 128).
  */
 typedef struct {
     int B, H, d_h, m, m_pitch, N, max_new, max_len, page_size, n_pages, table_pitch;

@@ -308,3 +308,19 @@ def test_tensor_core_calls_need_not_bring_the_other_paths_scratch(lib, B, N, max
     head, and up to 1/4 GB of sums), or 1/4 GB."""
     weights = 2 * 2 * (N + 8 * B + 8) * max_len
     assert 0 < tg.tg_workspace_size(tg.TG_WS_PAGED, _wide(B, N, max_len, tg.TG_BF16)) <= weights + (1 << 28)
+
+
+def test_lengths_past_the_cuda_core_grids(lib):
+    """65,535 spans of 128 keys is what those kernels' grids hold: a longer bound is refused
+    with its reason before the workspace is looked at, also where only an address off 16 bytes
+    keeps the call from the tensor cores; aligned bf16 calls take it."""
+    raw, st = tg.load().tango_paged_aggregate, lambda p, q=A: raw(ctypes.byref(p), q, A, A, A, A, None, 0, None)
+    for kw in (dict(dtype=tg.TG_F32), dict(dtype=tg.TG_BF16, d_h=128)):
+        kw.update(B=1, N=1, max_new=1, m=128, page_size=1 << 16, table_pitch=1 << 10)
+        assert st(_paged(max_len=65535 * 128, **kw)) == tg.TG_ERR_WORKSPACE
+        p = _paged(max_len=65535 * 128 + 1, **kw)
+        assert st(p) == tg.TG_ERR_UNSUPPORTED and tg.tg_workspace_size(tg.TG_WS_PAGED, p) == 0
+    kw.update(d_h=64)
+    p = _paged(max_len=65535 * 128 + 1, **kw)
+    assert st(p) == tg.TG_ERR_WORKSPACE and st(p, A + 2) == tg.TG_ERR_UNSUPPORTED
+    assert tg.tg_workspace_size(tg.TG_WS_PAGED, p) > 0
