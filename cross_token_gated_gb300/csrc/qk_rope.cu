@@ -193,9 +193,11 @@ __device__ __forceinline__ float group_sum(float v, int lh) {
   return v;
 }
 
-// r of the norm from the sum of squares (rsqrtf: within 2 units of the last place).
+// r of the norm from the sum of squares (rsqrtf: within 2 units of the last place).  A NaN stays
+// one (a maximum would replace it by the floor, and leave a head with one NaN 1e12 times its
+// other values).
 __device__ __forceinline__ float inv_norm(float ss, int d_h, int norm, float eps) {
-  if (norm == TG_NORM_UNIT) return rsqrtf(fmaxf(ss, 1e-24f));  // 1 / max(|x|, 1e-12)
+  if (norm == TG_NORM_UNIT) return rsqrtf(ss < 1e-24f ? 1e-24f : ss);  // 1 / max(|x|, 1e-12)
   if (norm == TG_NORM_RMS) return rsqrtf(__fdividef(ss, (float)d_h) + eps);
   return 1.f;
 }

@@ -587,3 +587,16 @@ def test_passes_of_unaligned_calls():
     null = torch.linspace(-1, 2, 7).cuda()
     got = b.check(null=null, max_len=1 << 17)
     assert torch.equal(b.run(null=null, max_len=1 << 17).double().cpu().view(b.N, 7, -1), got)
+
+
+@pytest.mark.parametrize("d_h", [32, 20])
+def test_appended_keys_keep_their_nan(d_h):
+    """A key with one NaN is cached as NaN throughout its head, not as finite values without a
+    meaning."""
+    b = Batch([(3, 7)], 2, d_h, 40, "bf16", 8, seed=63, fill=False)
+    k, g = torch.randn(3, 2 * d_h, device="cuda").bfloat16(), torch.randn(3, 80, device="cuda").bfloat16()
+    k[1, d_h + 3] = math.nan
+    b.k_pages.zero_()
+    tg.tango_cache_append(None, k, g, None, b.k_pages, b.g_pages, b.table, b.cu, b.lens, None, H=2)
+    got = b.k_pages[b.table[0, 0].item(), 4:7].view(3, 2, d_h)
+    assert got[1, 1].isnan().all() and torch.isfinite(got[[0, 2]]).all() and torch.isfinite(got[1, 0]).all()

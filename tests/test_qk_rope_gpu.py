@@ -252,3 +252,28 @@ def test_side_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("norm", [tg.TG_NORM_UNIT, tg.TG_NORM_RMS])
+@pytest.mark.parametrize("d_h,rotary,layout", [(64, 64, 0), (64, 32, 1), (50, 38, 0)])
+def test_a_nan_or_infinity_stays_in_its_head_and_is_not_lost(d_h, rotary, layout, norm, dtype):
+    """The norm of a head with a NaN is NaN, and so is every value of it; a head with an infinity
+    gives zeros, and NaN where the infinity and its pair stood.  Other heads and rows are as
+    without them.  Gradients of such heads are NaN."""
+    rows, H = 6, 3
+    q, _, pos, freqs, _, _, g = _case(11, rows, H, 0, d_h, rotary, dtype, False)
+    q[1, d_h + 5], q[3, 2 * d_h + d_h - 1], q[4, 7] = math.nan, math.nan, math.inf
+    out = torch.zeros(rows, H * d_h, dtype=DT[dtype], device="cuda")
+    tg.tango_qk_norm_rope(q, None, out, None, freqs, H=H, positions=pos, layout=layout, norm=norm)
+    want = _forward64(q, d_h, pos, freqs, layout, norm, None)
+    got = out.double().cpu().reshape(want.shape)
+    assert want[1, 1].isnan().all() and want[3, 2].isnan().all() and want[4, 0].isnan().sum() == (2 if rotary > 7 else 1)
+    assert torch.equal(got.isnan(), want.isnan())
+    keep = torch.nan_to_num(want, nan=0.0)
+    _close(torch.nan_to_num(got, nan=0.0), keep, dtype, d_h)
+    dy, dx = torch.randn(rows, H * d_h, generator=g).to(DT[dtype]).cuda(), torch.zeros_like(out)
+    tg.tango_qk_norm_rope_backward(q, None, dy, None, dx, None, freqs, H=H, positions=pos, layout=layout, norm=norm)
+    bad = torch.zeros(rows, H, dtype=torch.bool)
+    bad[1, 1] = bad[3, 2] = bad[4, 0] = True
+    assert torch.equal(dx.cpu().reshape(rows, H, d_h).isnan(), bad[..., None].expand(-1, -1, d_h))
