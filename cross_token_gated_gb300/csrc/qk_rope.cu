@@ -193,12 +193,21 @@ __device__ __forceinline__ float group_sum(float v, int lh) {
   return v;
 }
 
-// r of the norm from the sum of squares (rsqrtf: within 2 units of the last place).  A NaN stays
-// one (a maximum would replace it by the floor, and leave a head with one NaN 1e12 times its
-// other values).
+// Quotient, and 1 / sqrt: each step rounded once in fp32; the fast forms' errors (2 units of
+// the last place) are far below a bf16 rounding.
+template <typename T> __device__ __forceinline__ float quotient(float x, float y);
+template <> __device__ __forceinline__ float quotient<float>(float x, float y) { return x / y; }
+template <> __device__ __forceinline__ float quotient<__nv_bfloat16>(float x, float y) { return __fdividef(x, y); }
+template <typename T> __device__ __forceinline__ float inv_sqrt(float x);
+template <> __device__ __forceinline__ float inv_sqrt<float>(float x) { return 1.f / sqrtf(x); }
+template <> __device__ __forceinline__ float inv_sqrt<__nv_bfloat16>(float x) { return rsqrtf(x); }
+
+// r of the norm from the sum of squares.  A NaN stays one (a maximum would replace it by the
+// floor, and leave a head with one NaN 1e12 times its other values).
+template <typename T>
 __device__ __forceinline__ float inv_norm(float ss, int d_h, int norm, float eps) {
-  if (norm == TG_NORM_UNIT) return rsqrtf(ss < 1e-24f ? 1e-24f : ss);  // 1 / max(|x|, 1e-12)
-  if (norm == TG_NORM_RMS) return rsqrtf(__fdividef(ss, (float)d_h) + eps);
+  if (norm == TG_NORM_UNIT) return inv_sqrt<T>(ss < 1e-24f ? 1e-24f : ss);  // 1 / max(|x|, 1e-12)
+  if (norm == TG_NORM_RMS) return inv_sqrt<T>(quotient<T>(ss, (float)d_h) + eps);
   return 1.f;
 }
 
@@ -215,7 +224,7 @@ __device__ __forceinline__ void head_forward(const uint4& u0, const uint4& u1, T
                                              const LaneMap& m, int lh, const float* gain, const RowAngles& e) {
   Pairs<T, kHalf> z;
   z.load(u0, u1);
-  if (f.norm != TG_NORM_NONE) z.scale(inv_norm(group_sum(z.dot(z), lh), f.d_h, f.norm, f.eps));
+  if (f.norm != TG_NORM_NONE) z.scale(inv_norm<T>(group_sum(z.dot(z), lh), f.d_h, f.norm, f.eps));
   if (gain) z.times(gain, m);
   z.turn(e, m, false);
   uint4 w0, w1;
@@ -238,7 +247,7 @@ __device__ __forceinline__ void head_forward_any(const T* src, T* dst, const Fwd
     buf[c] = x;
     ss += x * x;
   }
-  const float r = f.norm == TG_NORM_NONE ? 1.f : inv_norm(group_sum(ss, 32), f.d_h, f.norm, f.eps);
+  const float r = f.norm == TG_NORM_NONE ? 1.f : inv_norm<T>(group_sum(ss, 32), f.d_h, f.norm, f.eps);
   __syncwarp();
   const int hp = f.rotary / 2;
   for (int c = lane; c < f.d_h; c += 32) {
@@ -397,7 +406,7 @@ __device__ __forceinline__ void head_backward(const uint4 (&u)[4], T* dst, bool 
   bool floor_hit = false;
   if (f.norm != TG_NORM_NONE) {
     const float ss = group_sum(n.dot(n), lh);
-    rn = inv_norm(ss, f.d_h, f.norm, f.eps);
+    rn = inv_norm<T>(ss, f.d_h, f.norm, f.eps);
     floor_hit = f.norm == TG_NORM_UNIT && ss < 1e-24f;
     n.scale(rn);
   }
@@ -413,7 +422,7 @@ __device__ __forceinline__ void head_backward(const uint4 (&u)[4], T* dst, bool 
   }
   if (f.norm != TG_NORM_NONE) {
     float along = group_sum(n.dot(d), lh);
-    if (f.norm == TG_NORM_RMS) along = __fdividef(along, (float)f.d_h);
+    if (f.norm == TG_NORM_RMS) along = quotient<T>(along, (float)f.d_h);
     if (floor_hit) along = 0.f;
     const uint64_t rr = ptx::f32x2_pack(rn, rn), aa = ptx::f32x2_pack(-along * rn, -along * rn);
 #pragma unroll
@@ -451,7 +460,7 @@ __device__ __forceinline__ void rows_backward_any(const QkArgs<T>& a, QkShared& 
     bool floor_hit = false;
     if (a.f.norm != TG_NORM_NONE) {
       ss = group_sum(ss, 32);
-      rn = inv_norm(ss, a.f.d_h, a.f.norm, a.f.eps);
+      rn = inv_norm<T>(ss, a.f.d_h, a.f.norm, a.f.eps);
       floor_hit = a.f.norm == TG_NORM_UNIT && ss < 1e-24f;
     }
     __syncwarp();

@@ -277,3 +277,17 @@ def test_a_nan_or_infinity_stays_in_its_head_and_is_not_lost(d_h, rotary, layout
     bad = torch.zeros(rows, H, dtype=torch.bool)
     bad[1, 1] = bad[3, 2] = bad[4, 0] = True
     assert torch.equal(dx.cpu().reshape(rows, H, d_h).isnan(), bad[..., None].expand(-1, -1, d_h))
+
+
+@pytest.mark.parametrize("d_h", [64, 50])
+def test_fp32_norms_round_each_step_once(d_h):
+    """Heads with one value a: the sum of squares is exact, so that the quotient by d_h, the sum
+    with eps, the root, its inverse and the product are five roundings in a known order (unit:
+    the last two, the root of a square being exact), the same as of these operations in fp32."""
+    a = torch.arange(1, 4097, dtype=torch.float32)
+    x = torch.zeros(len(a), d_h)
+    x[torch.arange(len(a)), torch.arange(len(a)) % d_h] = a
+    out = torch.zeros(len(a), d_h, device="cuda")
+    for norm, want in ((tg.TG_NORM_UNIT, a * (1 / a)), (tg.TG_NORM_RMS, a * (1 / (a * a / d_h + 1e-6).sqrt()))):
+        tg.tango_qk_norm_rope(x.cuda(), None, out, None, None, H=1, norm=norm)
+        assert torch.equal(out.cpu().sum(1), want)
