@@ -3,7 +3,8 @@
 //   out_i = v_i [ sum_{j<=i} w_ij g_j ] / [ sum_{j<=i} w_ij + (i+1) e^{b - tau} ],
 //   w_ij = e^{tau (q_i . k_j - 1)}.
 // The shift by tau cancels; with unit vectors and tau <= 20 every weight lies in
-// [e^-40, 1] and the sums of key ranges simply add, so no running maximum is kept.
+// [e^-40, 1] and the sums of key ranges simply add, so no running maximum is kept.  A row whose
+// weights say that its vectors are not unit ones is flagged (not_unit).
 //
 // Rows are taken in tiles of R (1, 2, 4 or 8) new tokens of one sequence.
 //   paged_scores_kernel  one thread per cached key: its R dot products (q in shared memory),
@@ -129,6 +130,8 @@ __global__ void __launch_bounds__(kKeysBlk) paged_scores_kernel(const SimtArgs<T
     float s = 0.f;
     for (int i = 0; i < kKeysBlk / 32; ++i) s += red[i][t];
     a.den[(th * a.spans + blockIdx.z) * R + t] = s;
+    const int k0 = blockIdx.z * kKeysBlk;
+    if (t < tr.n && not_unit(s, min(k0 + kKeysBlk, tr.pos0 + t + 1) - k0)) record_error(a.p.err, kErrValue | kKernPaged);
   }
 }
 

@@ -269,7 +269,11 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
   __syncthreads();
   if (wg == 1) half_sum[row] = sum;
   __syncthreads();
-  if (wg == 0 && row < tr.n) a.den[((size_t)hl * a.rows_tot + prow + row) * a.spans + span] = sum + half_sum[row];
+  if (wg == 0 && row < tr.n) {
+    sum += half_sum[row];
+    a.den[((size_t)hl * a.rows_tot + prow + row) * a.spans + span] = sum;
+    if (ok && not_unit(sum, min(key0 + a.span_keys, last + 1) - key0)) record_error(a.p.err, kErrValue | kKernPaged);
+  }
   cp_async_wait_all();
   tc_fence_before();
   __syncthreads();
@@ -358,6 +362,7 @@ __global__ void __launch_bounds__(kWThreads, 4) paged_weights_few_kernel(const T
     float s = 0.f;
     for (int i = 0; i < kWThreads / 32; ++i) s += red[i][t];
     a.den[((size_t)hl * a.rows_tot + prow + t) * a.spans + span] = s;
+    if (not_unit(s, min(key0 + a.span_keys, tr.pos0 + t + 1) - key0)) record_error(a.p.err, kErrValue | kKernPaged);
   }
 }
 

@@ -39,6 +39,15 @@ __device__ __forceinline__ int paged_page(const PagedBatch& p, int b, int page_i
   return -1;
 }
 
+// Whether a row's weights e^{tau (q.k - 1)}, of which n keys' sum up to `sum`, lie outside what
+// unit vectors give.  Rounded to bf16 they are at most 1 + 2^-8 long, so that with tau <= 20 a
+// weight lies within e^{20 (2^-7 + 2^-16)} = 1.17 and e^{-20 (2 + 2^-7 + 2^-16)} = 2^-57.9, and its
+// own rounding moves it by 2^-8.  Longer vectors can leave the range of fp32, which a sum without
+// a running maximum does not survive.  (NaN is no reason: it shows in the result.)
+__device__ __forceinline__ bool not_unit(float sum, int n) {
+  return n > 0 && (sum > 1.25f * (float)n || sum < 0x1p-59f * (float)n);
+}
+
 // The last sequence whose first row is <= row, by a 32-way search; a whole warp calls it
 // with one row.  With rising cu_new this is the row's sequence (empty ones are skipped).
 __device__ __forceinline__ int paged_find(const PagedBatch& p, int row) {

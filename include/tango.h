@@ -520,7 +520,12 @@ typedef struct {
 
 /*
  * What tango_cache_append does to the new tokens on their way into the cache.
- *   rotary_dim, layout, norm, eps, freqs   as in tg_qk_params, positions from lens
+ *   rotary_dim, layout, norm, eps, freqs   as in tg_qk_params, positions from lens; the
+ *                aggregation wants norm TG_NORM_UNIT (or TG_NORM_NONE of unit vectors).  A model
+ *                trained with another norm or with gains (tango_qk_norm_rope, then
+ *                tango_aggregate, which makes unit vectors of them) runs tango_qk_norm_rope at
+ *                the tokens' positions first and appends its outputs with TG_NORM_UNIT and
+ *                rotary_dim 0
  *   silu         1: g holds the gate projection W_g x, and SiLU(g) is cached (eq. 2);
  *                0: g is cached as it is
  *   q_pitch, k_pitch, g_pitch   elements between rows of q, k, g (0: dense)
@@ -548,7 +553,9 @@ tg_status tango_cache_append(const tg_paged_params *p, const tg_append_params *a
  * sequence (already appended),
  *   out = v * sum_{j<=i} e^{l_j} g_j / (sum_{j<=i} e^{l_j} + (i+1) e^{b_a}),  l_j = tau_a q . k_j,
  * as tango_aggregate gives for the row of the whole sequence.  q [N, H * d_h] and the cached
- * keys are unit vectors per head.  v [N, H * m_pitch] or NULL (out = gbar); out [N, H *
+ * keys are unit vectors per head (TG_NORM_UNIT, or already so): tango_aggregate normalises, this
+ * call does not.  Where they are not and a row's mean weight e^{l_j - tau_a} leaves [2^-59, 1.25],
+ * outside of what unit vectors in bf16 reach, the row is unspecified and flagged TG_ERR_DEVICE.  v [N, H * m_pitch] or NULL (out = gbar); out [N, H *
  * m_pitch], written (columns past m_h of a head: unspecified); may alias a dense v.
  * ws: device scratch of tg_workspace_size(TG_WS_PAGED, p) bytes, 256-byte aligned.
  */

@@ -600,3 +600,76 @@ def test_appended_keys_keep_their_nan(d_h):
     tg.tango_cache_append(None, k, g, None, b.k_pages, b.g_pages, b.table, b.cu, b.lens, None, H=2)
     got = b.k_pages[b.table[0, 0].item(), 4:7].view(3, 2, d_h)
     assert got[1, 1].isnan().all() and torch.isfinite(got[[0, 2]]).all() and torch.isfinite(got[1, 0]).all()
+
+
+# ------------------------------------------------------------------------- unit vectors
+
+@pytest.mark.parametrize("dtype,d_h", [("bf16", 64), ("f32", 64), ("bf16", 48)])
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_vectors_that_are_not_unit_are_flagged(n, dtype, d_h):
+    """RMS-normed keys and queries have products up to d_h: weights beyond fp32.  The call says so
+    instead of returning what is left of them."""
+    b = Batch([(n, 60), (n, 200)], 2, d_h, 264, dtype, 16, seed=64)
+    k = torch.randn(b.N, 2 * d_h, device="cuda").to(DT[dtype])
+    g, qo = torch.randn(b.N, 528, device="cuda").to(DT[dtype]), torch.empty_like(k)
+    how = dict(page_table=b.table, cu_new=b.cu, lens=b.lens, H=2)
+    for norm, status in ((tg.TG_NORM_UNIT, tg.TG_OK), (tg.TG_NORM_RMS, tg.TG_ERR_DEVICE), (tg.TG_NORM_UNIT, tg.TG_OK)):
+        # (a token's own key is its query here: their product is d_h)
+        tg.tango_cache_append(k, k, g, qo, b.k_pages, b.g_pages, freqs=None, norm=norm, **how)
+        b.q = qo
+        b.run()
+        st, word = tg.tg_check_device_error()
+        assert st == status and (st == tg.TG_OK or ((word >> 8) & 0xff == 6 and word & 2))
+    # the other way: products of -64, whose weights vanish
+    b.k_pages[:] = -qo[0]
+    b.q = (64 * qo[:1]).expand(b.N, -1).contiguous()
+    b.run()
+    assert tg.tg_check_device_error()[0] == tg.TG_ERR_DEVICE
+
+
+def test_extreme_unit_vectors_are_not_flagged():
+    """Keys equal and opposite to the query at tau = 20, and zero vectors, with components rounded
+    away from zero, stay inside the range."""
+    for dtype in ("bf16", "f32"):
+        for n in (1, 6, 40):
+            b = Batch([(n, 130)], 1, 64, 72, dtype, 16, seed=65)
+            # half of the components one step up: 1 + 2^-8 long, as far as bf16 rounding goes
+            x = torch.full((64,), 0.125)
+            x[::2] *= 1 + 2.0 ** -7
+            for sign in (1.0, -1.0, 0.0):
+                b.q = x.to(DT[dtype]).repeat(n, 1).cuda()
+                b.keys[0] = (sign * x).to(DT[dtype]).view(1, 1, 64).repeat(130, 1, 1)
+                for p in range(b.table.shape[1] - 1):
+                    b.k_pages[b.table[0, p].item()] = b.keys[0][0].cuda()
+                b.run(s=20.0)
+                assert tg.tg_check_device_error()[0] == tg.TG_OK
+
+
+def test_training_with_gains_serves_through_the_cache():
+    """RMS norm with gains, rotation, then the aggregation's own unit norm, as training has it:
+    served by tango_qk_norm_rope at the tokens' positions and an append that makes unit vectors
+    (fp32: both sides a few 2^-20)."""
+    T, H, d_h, m_h = 70, 2, 64, 200
+    g = torch.Generator().manual_seed(66)
+    q, k = torch.randn(T, H * d_h, generator=g).cuda(), torch.randn(T, H * d_h, generator=g).cuda()
+    gates, v = torch.randn(T, H * m_h, generator=g).cuda(), torch.randn(T, H * m_h, generator=g).cuda()
+    how = dict(H=H, norm=tg.TG_NORM_RMS, q_gain=(1 + 0.3 * torch.randn(d_h, generator=g)).cuda(),
+               k_gain=(1 + 0.3 * torch.randn(d_h, generator=g)).cuda())
+    fr = tg.tg_rope_freqs(d_h)
+    qr, kr, whole = torch.empty_like(q), torch.empty_like(k), torch.empty(1, T, H * m_h, device="cuda")
+    tg.tango_qk_norm_rope(q, k, qr, kr, fr, **how)
+    tg.tango_aggregate(qr[None], kr[None], gates[None], v[None], whole, H=H)
+    kp, gp = tg.cache_pools(5, 16, H, d_h, m_h, dtype=torch.float32)
+    table = torch.tensor([[3, 0, 4, 1, 2]], dtype=torch.int32, device="cuda")
+    a = 0
+    for e in (33, 34, 50, T):
+        cu, ln = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, e - a], [e]))
+        pos = torch.arange(a, e, dtype=torch.int32, device="cuda")
+        qa, ka, qo = (torch.empty(e - a, H * d_h, device="cuda") for _ in range(3))
+        out = torch.empty(e - a, H * m_h, device="cuda")
+        tg.tango_qk_norm_rope(q[a:e], k[a:e], qa, ka, fr, positions=pos, **how)
+        tg.tango_cache_append(qa, ka, gates[a:e], qo, kp, gp, table, cu, ln, None, H=H, silu=False)
+        tg.tango_paged_aggregate(qo, v[a:e], out, kp, gp, table, cu, ln, H=H, max_new=e - a, max_len=T)
+        assert (out - whole[0, a:e]).abs().max().item() <= 2e-5 * whole.abs().max().item()
+        a = e
+    assert tg.tg_check_device_error()[0] == tg.TG_OK
