@@ -557,7 +557,7 @@ __device__ __forceinline__ void schedule(const TcArgs& a, GBars& b, int lane) {
       job.hl = hs / a.strips;
       job.strip = hs - job.hl * a.strips;
       const int u = steps_of(job.pos0 + job.rows);
-      job.nc = ranges_of(u, range);
+      job.nc = min(ranges_of(u, range), a.nc_cap);
       job.it0 = (int)((long long)u * job.c / job.nc);  // never empty: u >= nc
       job.it1 = (int)((long long)u * (job.c + 1) / job.nc);
       job.tile = r0 / kM + job.b + ti;
@@ -905,6 +905,8 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
     auto take_slot = [&]() -> int {
       if (lead) {
         const int sl = atomicAdd(a.next + 1, 1);
+        // (never by the plan's count; a sum that is not kept must not pass unseen)
+        if ((unsigned)sl >= (unsigned)a.n_slots) record_error(a.p.err, kErrValue | kKernPaged);
         a.slot[tkey * a.nc_cap + job.c] = sl;
         b.last[g] = sl;
       }
@@ -1203,7 +1205,9 @@ TcPlan tc_plan(const PagedCall& c) {
   l.min_steps = 8;
   l.jobs_per_sm = l.r8cap <= kFewRows ? kJobsPerSm : 2;
   l.grid = sms;
-  // a tile that is cut has at most 4/3 as many ranges as whole ranges fit in it; two halves
+  // A tile that is cut has at least 3/2 ranges' worth of steps and at most 4/3 as many ranges as
+  // whole ones fit in it: together at most 4/3 of the jobs wanted.  Two halves each: 8/3 of them,
+  // for 4.
   l.n_slots = 2 * 2 * kJobsPerSm * sms;
   // A pass takes as many heads as keep P within kScratch, or, where one does not, the tiles of
   // one head that start within so many rows (whole tiles' worth of starts: a tile's rows may
