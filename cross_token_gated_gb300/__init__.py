@@ -84,7 +84,7 @@ class tg_qk_params(ctypes.Structure):
 class tg_paged_params(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "d_h", "m", "m_pitch", "N", "max_new", "max_len", "page_size",
                                             "n_pages", "table_pitch")] +                [(n, ctypes.c_void_p) for n in ("cu_new", "lens", "page_table")] +                [("s", ctypes.c_float), ("tau", ctypes.c_void_p), ("null_bias", ctypes.c_void_p),
-                ("v_pitch", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+                ("v_pitch", ctypes.c_longlong), ("dtype", ctypes.c_int), ("flags", ctypes.c_uint)]
 
 
 class tg_append_params(ctypes.Structure):
@@ -644,7 +644,7 @@ def cache_pools(n_pages, page_size, H, d_h, m_h, *, dtype=torch.bfloat16, m_pitc
 
 
 def paged_params(N, k_pages, g_pages, page_table, cu_new, lens, *, H, max_new, max_len, m_h=None, s=10.0, tau=None,
-                 null_bias=None, v_pitch=0) -> tg_paged_params:
+                 null_bias=None, v_pitch=0, flags=0) -> tg_paged_params:
     """tg_paged_params of a batch: page_table int32 [B, pages], cu_new int32 [B + 1], lens
     int32 [B]."""
     n_pages, page_size, dqk = k_pages.shape
@@ -664,7 +664,8 @@ def paged_params(N, k_pages, g_pages, page_table, cu_new, lens, *, H, max_new, m
     lp = _dense(lens, "lens", i32, dev, (B,))
     return tg_paged_params(B, H, dqk // H, H * (pitch if m_h is None else int(m_h)), pitch, N, max_new, max_len,
                            page_size, n_pages, cols, cp, lp, tp, s, _optional(tau, "tau", torch.float32, dev, (H,)),
-                           _optional(null_bias, "null_bias", torch.float32, dev, (H,)), v_pitch, _dtype_code(k_pages))
+                           _optional(null_bias, "null_bias", torch.float32, dev, (H,)), v_pitch, _dtype_code(k_pages),
+                           flags)
 
 
 def tango_cache_append(q, k, g, q_out, k_pages, g_pages, page_table, cu_new, lens, freqs, *, H, m_h=None,
@@ -703,7 +704,7 @@ def tango_cache_append(q, k, g, q_out, k_pages, g_pages, page_table, cu_new, len
 
 
 def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens, *, H, max_new, max_len, s=10.0,
-                          tau=None, null_bias=None, m_h=None, ws=None, stream=None):
+                          tau=None, null_bias=None, m_h=None, flags=0, ws=None, stream=None):
     """TANGO aggregation of the new tokens (already appended) over the paged cache.  q [N,
     H * d_h] unit vectors per head; v [N, H * pitch] or None (out = gbar); out [N, H *
     pitch].  max_new, max_len: host bounds of the sequences' new tokens and lengths."""
@@ -719,7 +720,7 @@ def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens,
         if v_rows != N or v_width != width:
             raise ValueError("v must have one row per new token, as wide as the cache's gates")
     p = paged_params(N, k_pages, g_pages, page_table, cu_new, lens, H=H, max_new=max_new, max_len=max_len, m_h=m_h,
-                     s=s, tau=tau, null_bias=null_bias, v_pitch=v_pitch)
+                     s=s, tau=tau, null_bias=null_bias, v_pitch=v_pitch, flags=flags)
     lib, ref = _lib or load(), ctypes.byref(p)
     with _on_device(dev):
         wbuf = _given_ws(ws, dev) if ws is not None else _scratch(lib.tg_workspace_size(TG_WS_PAGED, ref), q.device,

@@ -534,6 +534,7 @@ tg_status validate_paged(const tg_paged_params* p) {
   if ((long long)p->table_pitch * p->page_size < p->max_len) return TG_ERR_INVALID_ARG;
   if (p->dtype != TG_F32 && p->dtype != TG_BF16) return TG_ERR_INVALID_ARG;
   if (!p->cu_new || !p->lens || !p->page_table) return TG_ERR_INVALID_ARG;
+  if (p->flags & ~TG_FLAG_DEBUG_TIMEOUT) return TG_ERR_INVALID_ARG;
   if (!p->tau && !(p->s >= 0.f && p->s <= 20.f)) return TG_ERR_INVALID_ARG;
   const long long width = (long long)p->H * (p->m_pitch ? p->m_pitch : p->m / p->H);
   if (p->v_pitch != 0 && p->v_pitch < width) return TG_ERR_INVALID_ARG;
@@ -558,6 +559,7 @@ PagedCall paged_call(const tg_paged_params* p, unsigned* err) {
   c.H = p->H; c.d_h = p->d_h; c.m_h = p->m / p->H; c.m_pitch = p->m_pitch ? p->m_pitch : c.m_h;
   c.s = p->s; c.tau = p->tau; c.null_bias = p->null_bias;
   c.v_pitch = p->v_pitch ? p->v_pitch : (long long)c.H * c.m_pitch;
+  c.debug_timeout = (p->flags & TG_FLAG_DEBUG_TIMEOUT) ? 1 : 0;
   return c;
 }
 

@@ -114,6 +114,7 @@ struct TcArgs {
   int* done;                 // [head][strip][tile][half]: ranges that are done
   int* next;                 // [0] next job, [1] next partial slot
   uint64_t timeout_ns;
+  int debug_timeout;         // test hook: both kernels first wait on a barrier nothing signals
 };
 
 // Scratch row of a sequence's first row: sequences start at multiples of 8.  Less than 0, or
@@ -143,8 +144,8 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base, *sK = base + kWQ, *sP = base + 3 * kWQ;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sP + 2 * kM * 128);
-  uint32_t* tm = reinterpret_cast<uint32_t*>(bar + 1);
+  uint64_t *bar = reinterpret_cast<uint64_t*>(sP + 2 * kM * 128), *never = bar + 1;
+  uint32_t* tm = reinterpret_cast<uint32_t*>(bar + 2);
   __shared__ float half_sum[kM];
   const int t = threadIdx.x, warp = t / 32, lane = t & 31;
   const int tile = blockIdx.x, hl = blockIdx.y, span = blockIdx.z, head = a.h0 + hl;
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
 
   if (t == 0) {
     mbar_init(bar, 1);
+    mbar_init(never, 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -221,8 +223,8 @@ __global__ void __launch_bounds__(kWThreads) paged_weights_kernel(const TcArgs a
       mma_commit(bar);
     }
     if (k0 + 128 < key1) load_keys(k0 + 128, buf ^ 1);
-    // one wait per warp; a bounded one, after which every warp leaves together below
-    ok = mbar_wait(bar, n & 1, a.timeout_ns);
+    // a bounded wait, after which every warp leaves together below
+    ok = mbar_wait(a.debug_timeout ? never : bar, n & 1, a.timeout_ns);
     if (!__syncthreads_and(ok)) {
       if (t == 0) record_error(a.p.err, kErrTimeout | kKernPaged);
       break;
@@ -387,7 +389,7 @@ struct __align__(8) GBars {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t job_full[kJobSlots], job_empty[kJobSlots];
   uint64_t near_end;  // the producers are in a job's last steps: time to take the next one
-  uint64_t drain;
+  uint64_t drain, never;
   uint32_t tmem_base;
   int abort;
   int last[2];
@@ -697,7 +699,7 @@ __device__ __forceinline__ void multiply(const TcArgs& a, GBars& b, const uint8_
     koff[kk] = (uint32_t)(box * (4 * br * 128) + (key - box * br) * 128) >> 4;
   }
   Ring st, jr, acc, dr;
-  bool ok = true;
+  bool ok = !a.debug_timeout || wait_bar(&b.never, 0, b, a);  // nothing ever arrives there
   while (ok) {
     if (!(ok = wait_bar(&b.job_full[jr.stage], jr.phase, b, a))) break;
     const Job job = b.job[jr.stage];
@@ -1131,6 +1133,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
     mbar_init(&b.near_end, kProducers);
     mbar_init(&b.drain, 1);
+    mbar_init(&b.never, 1);
     b.abort = 0;
     for (int i = 0; i < 16; ++i) (&b.poison[0][0])[i] = 0;
     fence_mbar_init();
@@ -1294,7 +1297,8 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   a.slot = reinterpret_cast<int*>(base + l.slot);
   a.done = reinterpret_cast<int*>(base + l.done);
   a.next = reinterpret_cast<int*>(base + l.next);
-  a.timeout_ns = kTimeoutNs;
+  a.debug_timeout = c.debug_timeout;
+  a.timeout_ns = c.debug_timeout ? 1000000ull : kTimeoutNs;
 
   CUtensorMap mG, mG4;
   cudaError_t e = make_tmap_4d_heads(&mG, c.g_pages, c.p.n_pages, c.p.page_size, c.H, c.m_h, c.m_pitch, a.box_rows, 64);

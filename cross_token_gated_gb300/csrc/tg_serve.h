@@ -56,6 +56,7 @@ struct PagedCall {
   void* out;
   const void *k_pages, *g_pages;
   void* ws;
+  int debug_timeout;
 };
 // Whether the grids fit: max_len up to 65,535 x 128.
 bool paged_simt_takes(tg_dtype dt, const PagedCall& c);

@@ -72,7 +72,9 @@ typedef enum { TG_F32 = 0, TG_BF16 = 1 } tg_dtype;
                                         the gate-strip kernel; tango_block_forward: the
                                         projection GEMM; tango/wango_aggregate_backward:
                                         the pair-gradient, dq/dk and running-sum scan
-                                        kernels (the outputs are then undefined) */
+                                        kernels; tango_paged_aggregate: the weights and
+                                        gates kernels of the tensor-core path (the outputs
+                                        are then undefined) */
 #define TG_FLAG_FUSED_V 0x200u       /* tango_block_forward, WANGO mode, bf16: v = W_v x is
                                         formed inside the aggregation kernel instead of by
                                         the projection GEMM (v is then never stored); see
@@ -494,6 +496,7 @@ tg_status tg_rope_freqs(int rotary_dim, double base, double factor, long long or
  *   s, tau, null_bias   as in tg_agg_params (aggregation only)
  *   v_pitch      elements between rows of v (0: H * m_pitch)
  *   dtype        of the cache and of every tensor
+ *   flags        0 or TG_FLAG_DEBUG_TIMEOUT (aggregation only)
  * Device values outside their range (cu_new not rising within [0, N], more new tokens
  * than max_new, lens outside [0, max_len], a page outside [0, n_pages)) are clamped or
  * skipped, never followed, and flagged TG_ERR_DEVICE; the sequence's results are then
@@ -516,6 +519,7 @@ typedef struct {
     const float *null_bias;
     long long v_pitch;
     tg_dtype dtype;
+    unsigned flags;
 } tg_paged_params;
 
 /*

@@ -673,3 +673,18 @@ def test_training_with_gains_serves_through_the_cache():
         assert (out - whole[0, a:e]).abs().max().item() <= 2e-5 * whole.abs().max().item()
         a = e
     assert tg.tg_check_device_error()[0] == tg.TG_OK
+
+
+@pytest.mark.parametrize("seqs", [[(1, 70), (1, 1300)], [(40, 300), (200, 260), (1, 5)], [(600, 2000)]],
+                         ids=["few", "chunks", "ranges"])
+def test_bounded_wait_timeout_reports_status(seqs):
+    """TG_FLAG_DEBUG_TIMEOUT makes the tensor-core kernels wait on barriers that nothing signals:
+    the waits run out after 1 ms, every role leaves its loops, copies in flight are waited for,
+    and the error word says so.  The next call is right."""
+    b = Batch(seqs, 2, 32, 520, "bf16", 16, seed=67)
+    b.run(flags=tg.TG_FLAG_DEBUG_TIMEOUT)
+    st, word = tg.tg_check_device_error()
+    assert st == tg.TG_ERR_TIMEOUT and word & 1 and (word >> 8) & 0xff == 6
+    assert tg.tg_check_device_error() == (tg.TG_OK, 0)
+    first = b.check()
+    assert torch.equal(b.run().double().cpu().view(b.N, 2, -1), first)

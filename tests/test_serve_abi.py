@@ -324,3 +324,13 @@ def test_lengths_past_the_cuda_core_grids(lib):
     p = _paged(max_len=65535 * 128 + 1, **kw)
     assert st(p) == tg.TG_ERR_WORKSPACE and st(p, A + 2) == tg.TG_ERR_UNSUPPORTED
     assert tg.tg_workspace_size(tg.TG_WS_PAGED, p) > 0
+
+
+def test_paged_flags(lib):
+    """The test hook is the only flag of these parameters."""
+    raw, P = tg.load(), ctypes.byref
+    for flags, status in ((tg.TG_FLAG_DEBUG_TIMEOUT, tg.TG_ERR_WORKSPACE), (tg.TG_FLAG_QK_NORMALIZED, tg.TG_ERR_INVALID_ARG),
+                          (1 << 31, tg.TG_ERR_INVALID_ARG)):
+        assert raw.tango_paged_aggregate(P(_paged(flags=flags)), A, A, A, A, A, None, 0, None) == status
+    assert raw.tango_cache_append(P(_paged(flags=2)), P(_append()), A, A, A, A, A, A, None) == tg.TG_ERR_INVALID_ARG
+    assert tg.tg_workspace_size(tg.TG_WS_PAGED, _paged(flags=2)) == 0
