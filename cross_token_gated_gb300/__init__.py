@@ -7,7 +7,8 @@ the library cannot be loaded, every call raises.
 
 Functions (same names as the C ABI):
   tango_aggregate, tango_aggregate_noalloc, wango_aggregate, tango_aggregate_save,
-  wango_aggregate_save, tango_aggregate_backward, wango_aggregate_backward, wango_decode_step, tango_block_forward, tango_model_forward,
+  wango_aggregate_save, tango_aggregate_backward, wango_aggregate_backward, wango_decode_step,
+  tango_block_forward, tango_model_forward,
   tango_qk_norm_rope, tango_qk_norm_rope_backward, tg_rope_freqs, tango_cache_append, tango_paged_aggregate,
   tg_workspace_size, tg_status_string, tg_check_device_error, tg_version
 """
@@ -83,7 +84,9 @@ class tg_qk_params(ctypes.Structure):
 
 class tg_paged_params(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "d_h", "m", "m_pitch", "N", "max_new", "max_len", "page_size",
-                                            "n_pages", "table_pitch")] +                [(n, ctypes.c_void_p) for n in ("cu_new", "lens", "page_table")] +                [("s", ctypes.c_float), ("tau", ctypes.c_void_p), ("null_bias", ctypes.c_void_p),
+                                            "n_pages", "table_pitch")] + \
+               [(n, ctypes.c_void_p) for n in ("cu_new", "lens", "page_table")] + \
+               [("s", ctypes.c_float), ("tau", ctypes.c_void_p), ("null_bias", ctypes.c_void_p),
                 ("v_pitch", ctypes.c_longlong), ("dtype", ctypes.c_int), ("flags", ctypes.c_uint)]
 
 

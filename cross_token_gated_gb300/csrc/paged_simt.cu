@@ -452,7 +452,8 @@ template <typename T, int R>
 cudaError_t run(const PagedCall& c, const SimtPlan& l, cudaStream_t s) {
   SimtArgs<T> a;
   a.p = c.p; a.H = c.H; a.d_h = c.d_h; a.m_h = c.m_h; a.m_pitch = c.m_pitch;
-  a.key_pitch = l.key_pitch; a.spans = l.spans; a.span_keys = l.span_keys; a.gspans = l.gspans; a.chunks = l.chunks; a.counts = l.counts;
+  a.key_pitch = l.key_pitch; a.spans = l.spans; a.span_keys = l.span_keys; a.gspans = l.gspans;
+  a.chunks = l.chunks; a.counts = l.counts;
   a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
   a.q = static_cast<const T*>(c.q); a.v = static_cast<const T*>(c.v); a.out = static_cast<T*>(c.out);
   a.k_pages = static_cast<const T*>(c.k_pages); a.g_pages = static_cast<const T*>(c.g_pages);

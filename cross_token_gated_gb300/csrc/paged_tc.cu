@@ -1041,52 +1041,53 @@ __device__ __forceinline__ void finish_tiles(const TcArgs& a, GBars& b, uint8_t*
           if (a.v && c64 > 0) load_v64(c64);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-          const int c0 = c64 + h * 32, c = c0 + lc;
-          if (c0 >= cols) break;
-          float y[32];
-          if (job.nc == 1) {
-            fetch(c0, y);
-          } else {
+            const int c0 = c64 + h * 32, c = c0 + lc;
+            if (c0 >= cols) break;
+            float y[32];
+            if (job.nc == 1) {
+              fetch(c0, y);
+            } else {
 #pragma unroll
-            for (int q = 0; q < 32; ++q) y[q] = 0.f;
-            for (int k0 = 0; k0 < job.nc; k0 += kSlotRegs) {
-              if (c0 == 0 || job.nc > kSlotRegs) slots(k0);
+              for (int q = 0; q < 32; ++q) y[q] = 0.f;
+              for (int k0 = 0; k0 < job.nc; k0 += kSlotRegs) {
+                if (c0 == 0 || job.nc > kSlotRegs) slots(k0);
 #pragma unroll
-              for (int k = 0; k < kSlotRegs; ++k) {
-                if (!live || (unsigned)sl_reg[k] >= (unsigned)a.n_slots) continue;
-                const float4* src = reinterpret_cast<const float4*>(a.part + (size_t)sl_reg[k] * (kHalfN * a.r8cap));
+                for (int k = 0; k < kSlotRegs; ++k) {
+                  if (!live || (unsigned)sl_reg[k] >= (unsigned)a.n_slots) continue;
+                  const float4* src = reinterpret_cast<const float4*>(a.part + (size_t)sl_reg[k] * (kHalfN * a.r8cap));
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                  const float4 x = __ldcg(src + (size_t)(c0 / 4 + u) * a.r8cap + r);
-                  y[4 * u] += x.x; y[4 * u + 1] += x.y; y[4 * u + 2] += x.z; y[4 * u + 3] += x.w;
+                  for (int u = 0; u < 8; ++u) {
+                    const float4 x = __ldcg(src + (size_t)(c0 / 4 + u) * a.r8cap + r);
+                    y[4 * u] += x.x; y[4 * u + 1] += x.y; y[4 * u + 2] += x.z; y[4 * u + 3] += x.w;
+                  }
                 }
               }
             }
-          }
-          // a row without keys gives zeros, whatever its accumulator holds
-          const bool seen = live && pos >= 0;
-          __syncwarp();  // the previous columns have been read
+            // a row without keys gives zeros, whatever its accumulator holds
+            const bool seen = live && pos >= 0;
+            __syncwarp();  // the previous columns have been read
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            uint32_t e[4];
+            for (int u = 0; u < 8; ++u) {
+              uint32_t e[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e[q] = seen ? __float_as_uint(y[4 * u + q] * inv) : 0u;
-            st_shared_v4(t_s + lane * 128 + ((u ^ (lane & 7)) << 4), make_uint4(e[0], e[1], e[2], e[3]));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rw = lane / 8 + 4 * k, rr = quarter * 32 + rw;
-            const uint4 x = ld_shared_v4(t_s + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
-            float z[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
-            if (a.v && job.pos0 + rr >= 0) {
-              z[0] *= bf16lo(vr[h][k].x); z[1] *= bf16hi(vr[h][k].x); z[2] *= bf16lo(vr[h][k].y); z[3] *= bf16hi(vr[h][k].y);
+              for (int q = 0; q < 4; ++q) e[q] = seen ? __float_as_uint(y[4 * u + q] * inv) : 0u;
+              st_shared_v4(t_s + lane * 128 + ((u ^ (lane & 7)) << 4), make_uint4(e[0], e[1], e[2], e[3]));
             }
-            // four columns: the last ones may run into the pitch's padding
-            if (rr < job.rows && c < cols)
-              *reinterpret_cast<uint2*>(a.out + (size_t)(job.row0 + rr) * width + col0 + c) =
-                  make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
-          }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rw = lane / 8 + 4 * k, rr = quarter * 32 + rw;
+              const uint4 x = ld_shared_v4(t_s + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
+              float z[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+              if (a.v && job.pos0 + rr >= 0) {
+                z[0] *= bf16lo(vr[h][k].x); z[1] *= bf16hi(vr[h][k].x);
+                z[2] *= bf16lo(vr[h][k].y); z[3] *= bf16hi(vr[h][k].y);
+              }
+              // four columns: the last ones may run into the pitch's padding
+              if (rr < job.rows && c < cols)
+                *reinterpret_cast<uint2*>(a.out + (size_t)(job.row0 + rr) * width + col0 + c) =
+                    make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+            }
           }
         }
       }
@@ -1283,7 +1284,8 @@ cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s) {
   TcArgs a = {};
   a.p = c.p; a.H = c.H; a.d_h = c.d_h; a.m_h = c.m_h; a.m_pitch = c.m_pitch;
   a.rows = l.rows; a.rows_tot = l.rows_tot; a.key_blocks = l.key_blocks; a.span_keys = l.span_keys; a.spans = l.spans;
-  a.strips = l.strips; a.tiles = l.tiles; a.r8cap = l.r8cap; a.min_steps = l.min_steps; a.jobs_per_sm = l.jobs_per_sm; a.nc_cap = l.nc_cap; a.n_slots = l.n_slots;
+  a.strips = l.strips; a.tiles = l.tiles; a.r8cap = l.r8cap; a.min_steps = l.min_steps;
+  a.jobs_per_sm = l.jobs_per_sm; a.nc_cap = l.nc_cap; a.n_slots = l.n_slots;
   a.box_rows = box_rows(c.p.page_size);
   a.s = c.s; a.tau = c.tau; a.null_bias = c.null_bias; a.v_pitch = c.v_pitch;
   a.v_vec = c.v && (reinterpret_cast<uintptr_t>(c.v) & 15u) == 0 && c.v_pitch % 8 == 0;

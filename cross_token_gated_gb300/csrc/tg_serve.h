@@ -44,7 +44,8 @@ struct AppendCall {
 cudaError_t launch_cache_append(tg_dtype dt, const AppendCall& c, cudaStream_t s);
 
 // ---- aggregation over the cache: the weights of every (row, head) first, into scratch,
-// then the gates they average.  Heads are taken in passes that keep the scratch bounded.
+// then the gates they average.  Heads, and row tiles of one head, are taken in passes that keep
+// the scratch bounded.
 struct PagedCall {
   PagedBatch p;
   int H, d_h, m_h, m_pitch;
@@ -64,8 +65,8 @@ size_t paged_simt_ws_bytes(tg_dtype dt, const PagedCall& c);
 cudaError_t launch_paged_simt(tg_dtype dt, const PagedCall& c, cudaStream_t s);
 
 // The same on the tensor cores (bf16).  Whether the shapes are ones it takes: head widths and
-// pitches that TMA and tcgen05 read, pages of a multiple of 8 tokens.  q, v, out and the pools must also be 16-byte aligned (v: else
-// read element-wise).
+// pitches that TMA and tcgen05 read, pages of a multiple of 8 tokens.  q, out and the pools must
+// also be 16-byte aligned (v need not be, and is read element-wise then).
 bool paged_tc_takes(tg_dtype dt, const PagedCall& c);
 size_t paged_tc_ws_bytes(const PagedCall& c);
 cudaError_t launch_paged_tc(const PagedCall& c, cudaStream_t s);

@@ -506,10 +506,15 @@ tg_status tg_rope_freqs(int rotary_dim, double base, double factor, long long or
  * sequence's length may hold anything (NaN included): they are never used.  The columns
  * between m_h and m_pitch of a head may be read and are written with unspecified values;
  * they reach no result.
- * TG_BF16 runs the aggregation on the tensor cores when d_h is 16, 32 or 64, m_pitch and page_size
- * are multiples of 8, and q, out and the pools are
- * 16-byte aligned; anything else, and TG_F32, runs on the CUDA cores, which take max_len up to
- * 8,388,480 (65,535 * 128).
+ * Rows of no sequence (before cu_new[0], from cu_new[B] on) are left as they are.
+ * TG_BF16 runs the aggregation on the tensor cores when d_h is 16, 32 or 64, m_pitch and
+ * page_size are multiples of 8, and q, out and the pools are 16-byte aligned; anything else, and
+ * TG_F32, runs on the CUDA cores, which take max_len up to 8,388,480 (65,535 * 128).
+ * On the tensor cores the weights e^{l_j - tau_a} are rounded to bf16 before they are summed (as
+ * in tango_aggregate), and the denominators sum the rounded ones; sums, and everything on the
+ * CUDA cores, are fp32.
+ * max_new and max_len size grids, spans and scratch: results do not depend on them, times and
+ * scratch do.  Bounds near the batch's own are the fastest.
  */
 typedef struct {
     int B, H, d_h, m, m_pitch, N, max_new, max_len, page_size, n_pages, table_pitch;
@@ -546,8 +551,9 @@ typedef struct {
  * Appends the new tokens' keys and gates to the cache: k [N, H * d_h] normed and rotated
  * at its token's position, g [N, H * m_pitch] through SiLU if asked, both written to the
  * token's slot.  q [N, H * d_h], if not NULL, is normed and rotated in the same launch into
- * q_out [N, H * d_h] (dense; may be a dense q) for the aggregation that follows.  A token's slot must not be
- * shared with another sequence's new token.
+ * q_out [N, H * d_h] (dense; may be a dense q) for the aggregation that follows; a row of no
+ * sequence leaves an unspecified row there.  A token's slot must not be shared with another
+ * sequence's new token.
  */
 tg_status tango_cache_append(const tg_paged_params *p, const tg_append_params *a, const void *q, const void *k,
                              const void *g, void *q_out, void *k_pages, void *g_pages, tg_stream_t stream);
@@ -561,7 +567,11 @@ tg_status tango_cache_append(const tg_paged_params *p, const tg_append_params *a
  * call does not.  Where they are not and a row's mean weight e^{l_j - tau_a} leaves [2^-59, 1.25],
  * outside of what unit vectors in bf16 reach, the row is unspecified and flagged TG_ERR_DEVICE.  v [N, H * m_pitch] or NULL (out = gbar); out [N, H *
  * m_pitch], written (columns past m_h of a head: unspecified); may alias a dense v.
- * ws: device scratch of tg_workspace_size(TG_WS_PAGED, p) bytes, 256-byte aligned.
+ * ws: device scratch of tg_workspace_size(TG_WS_PAGED, p) bytes, 256-byte aligned.  Large batches
+ * run in passes over it: at most 1 GB on the CUDA cores, or what 8 rows of one head take there if
+ * that is more (32 bytes a key of max_len, and 1/16 byte a key and gate); on the tensor cores at
+ * most 2 GB of weights, or what 256 rows of one head take (512 bytes a key), and, for up to 65,536
+ * sequences, half a GB of sums and counters.
  */
 tg_status tango_paged_aggregate(const tg_paged_params *p, const void *q, const void *v, void *out,
                                 const void *k_pages, const void *g_pages, void *ws, size_t ws_bytes,
