@@ -291,3 +291,24 @@ def test_fp32_norms_round_each_step_once(d_h):
     for norm, want in ((tg.TG_NORM_UNIT, a * (1 / a)), (tg.TG_NORM_RMS, a * (1 / (a * a / d_h + 1e-6).sqrt()))):
         tg.tango_qk_norm_rope(x.cuda(), None, out, None, None, H=1, norm=norm)
         assert torch.equal(out.cpu().sum(1), want)
+
+
+@pytest.mark.parametrize("d_h", [64, 50])
+def test_fp32_cosines_and_sines(d_h):
+    """Pairs (1, 0) turn into the cosine and sine themselves: off by the angle, which fp32 holds to
+    pi 2^-27 from the next quarter turn (and 64 bits of turns a position: 2^-30 at 2^24), and by one
+    unit of sincospi, 2^-24 below 1."""
+    rows = 20000
+    g = torch.Generator().manual_seed(12)
+    pos = torch.randint(-(1 << 24), 1 << 24, (rows,), generator=g, dtype=torch.int32)
+    pos[:64] = torch.arange(64)
+    freqs = tg.tg_rope_freqs(d_h, device="cpu")
+    x = torch.zeros(rows, d_h)
+    x[:, :d_h // 2] = 1
+    out = torch.empty(rows, d_h, device="cuda")
+    tg.tango_qk_norm_rope(x.cuda(), None, out, None, freqs.cuda(), H=1, positions=pos.cuda(), norm=tg.TG_NORM_NONE)
+    # the angle in 64-bit turns, reduced exactly in integers
+    frac = [int(f.item() / (2 * math.pi) % 1.0 * 2.0 ** 64) for f in freqs]
+    ang = torch.tensor([[(f * p) % (1 << 64) / 2.0 ** 64 for f in frac] for p in pos.tolist()], dtype=torch.float64)
+    want = torch.cat([(2 * math.pi * ang).cos(), (2 * math.pi * ang).sin()], 1)
+    assert (out.double().cpu() - want).abs().max().item() <= math.pi * 2.0 ** -27 + 2.0 ** -24 + 2.0 ** -30
