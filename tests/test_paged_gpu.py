@@ -688,3 +688,25 @@ def test_bounded_wait_timeout_reports_status(seqs):
     assert tg.tg_check_device_error() == (tg.TG_OK, 0)
     first = b.check()
     assert torch.equal(b.run().double().cpu().view(b.N, 2, -1), first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_rows_of_no_sequence_are_left_alone(n, dtype):
+    """Rows before cu_new[0] and from cu_new[B] on (a captured graph's spare rows) keep what they
+    hold, whatever q and v hold there; the others are as without them."""
+    b = Batch([(n, 60), (n, 200)], 2, 32, 264, dtype, 16, seed=68)
+    want = b.run()
+
+    def padded(t, fill):
+        spare = torch.full_like(t[:1], fill)
+        return torch.cat([spare.repeat(3, 1), t, spare.repeat(150, 1)])
+    b.q, b.v, b.cu, out = padded(b.q, math.nan), padded(b.v, math.nan), b.cu + 3, padded(torch.zeros_like(want), 7.0)
+    tg.tango_paged_aggregate(b.q, b.v, out, b.k_pages, b.g_pages, b.table, b.cu, b.lens, H=2, max_new=n, max_len=200)
+    assert torch.equal(out[3:3 + b.N], want)
+    assert (out[:3] == 7).all() and (out[3 + b.N:] == 7).all()
+    k, g = padded(b.q[3:3 + b.N], 1.0), padded(b.v[3:3 + b.N], 1.0)
+    kp, gp = torch.full_like(b.k_pages, math.nan), torch.full_like(b.g_pages, math.nan)
+    tg.tango_cache_append(None, k, g, None, kp, gp, b.table, b.cu, b.lens, None, H=2)
+    assert torch.isfinite(kp[..., 0]).sum() == b.N and torch.isfinite(gp[..., 0]).sum() == b.N
+    assert tg.tg_check_device_error()[0] == tg.TG_OK
