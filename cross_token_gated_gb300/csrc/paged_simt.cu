@@ -16,7 +16,7 @@
 //       through f32x2 arithmetic.  The spans of one output are joined, 16 neighbours first, by
 //       the block of them that finishes last, in the spans' order (no order-dependent sums).
 // 71 new tokens of 4 sequences over 2,297 cached ones, fp32, 2 x 4,747 gates in rows that are not
-// 16-byte aligned: 46 us, bound by the latency of 4-byte loads and of two kernels in a row (the
+// 16-byte aligned: 47 us, bound by the latency of 4-byte loads and of two kernels in a row (the
 // bytes alone would take 14 us).  Whole chunks are bound by the latency of L2 and of a block's start:
 // 201 rows over 870 keys, 16 x 1,780 gates: 320 us, 28 TFLOP/s (660 us without the second
 // batch of loads and with single f32 arithmetic).  Tiles of 16 rows halve the reads but leave

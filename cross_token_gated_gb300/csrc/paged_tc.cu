@@ -29,6 +29,9 @@
 //                chunk's own tokens are taken out of the product (0 * NaN would reach rows
 //                that do not see them); the epilogue adds them back to the rows that do
 //
+// The weights of a pass stay within 2 GB: a pass takes some of the heads, or the tiles of one head
+// that start within a range of scratch rows.
+//
 // A job is a (sequence, key range, head, strip, row tile) with the row tile fastest, so the
 // CTAs that work side by side share their G out of L2.  Key ranges are cut when the tiles
 // alone would not fill the SMs; the job that finishes a tile last adds the ranges' partial
@@ -36,11 +39,12 @@
 // the error word.
 //
 // Decode steps are bound by HBM: 8 sequences of one new token over 1,025 to 8,192 cached ones
-// (2 x 14,240 gates) take 360 us, 6.47 TB/s.  Whole tiles are bound by what comes into an SM
-// (48 KB a step at 64 bytes a clock, against 512 cycles of products) and by the 4 steps in
-// flight: 512 new tokens over 8,192 take 206 us, 1,131 TFLOP/s.  Any other load of the SM waits
-// some 5,000 cycles behind the copies, hence eight epilogue warps and v asked for before the
-// products end (prompts of 2,048 tokens and decode steps in one batch: 832 -> 729 us).
+// (2 x 14,240 gates) take 361 to 367 us, 6.36 TB/s.  512 new tokens over 8,192 take 208 us, 1,118
+// TFLOP/s; what bounds whole tiles is not known.  A step brings 48 KB into the SM, 768 cycles at 64
+// bytes a clock against 512 of products, but CTA pairs, which bring 32 KB, gained nothing.  Any
+// other load of the SM waits some 5,000 cycles behind the copies, hence eight epilogue warps and v
+// asked for before the products end (prompts of 2,048 tokens and decode steps in one batch: 832 ->
+// 733 us).
 #include <atomic>
 
 #include "tg_common.cuh"

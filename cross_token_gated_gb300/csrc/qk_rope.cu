@@ -18,7 +18,7 @@
 // and walks the rows, loaded ahead of the angles; the norm's sums are shuffles between the
 // d_h / E lanes of a head, the arithmetic is packed two f32 at a time.  65,536 rows of 32
 // heads of 32 in bf16 take 49.5 us (5.4 TB/s); gradients of 16,384 rows of 12 heads of 64 with
-// gains 34.5 us, bound by latency at 16 warps an SM (128 registers a thread).  An append of
+// gains 35.5 us, bound by latency at 16 warps an SM (124 registers a thread).  An append of
 // 9,192 tokens of 9,504 gates takes 61.7 us (5.8 TB/s): a block per row, the row's slot looked
 // up once while its gates are on their way.
 #include <math.h>
