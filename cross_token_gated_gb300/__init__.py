@@ -10,6 +10,8 @@ Functions (same names as the C ABI):
   wango_aggregate_save, tango_aggregate_backward, wango_aggregate_backward, wango_decode_step,
   tango_block_forward, tango_model_forward,
   tango_qk_norm_rope, tango_qk_norm_rope_backward, tg_rope_freqs, tango_cache_append, tango_paged_aggregate,
+  tango_embed, tango_embed_backward, tango_norm, tango_norm_backward, tango_distill, tango_distill_backward,
+  tango_sample,
   tg_workspace_size, tg_status_string, tg_check_device_error, tg_version
 """
 from __future__ import annotations
@@ -34,9 +36,10 @@ TG_FLAG_BWD_FAR_SCAN = 0x400
 TG_FLAG_BWD_FAR_PAIRS = 0x800
 TG_MODE_TANGO, TG_MODE_WANGO = 0, 1
 TG_WS_TANGO, TG_WS_WANGO, TG_WS_BLOCK, TG_WS_MODEL, TG_WS_DECODE, TG_WS_TANGO_BWD, TG_WS_WANGO_BWD = range(7)
-TG_WS_QK_BWD, TG_WS_PAGED = 16, 17
+TG_WS_QK_BWD, TG_WS_PAGED, TG_WS_EMBED_BWD, TG_WS_NORM_BWD = range(16, 20)
 TG_ROPE_HALF, TG_ROPE_INTERLEAVED = 0, 1
-TG_NORM_NONE, TG_NORM_UNIT, TG_NORM_RMS = range(3)
+TG_NORM_NONE, TG_NORM_UNIT, TG_NORM_RMS, TG_NORM_LAYER = range(4)
+TG_MAX_TEACHER = 1024
 
 HEADER = os.path.join(_build.INCLUDE, "tango.h")
 
@@ -94,6 +97,30 @@ class tg_append_params(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("norm", ctypes.c_int),
                 ("eps", ctypes.c_float), ("freqs", ctypes.c_void_p), ("silu", ctypes.c_int),
                 ("q_pitch", ctypes.c_longlong), ("k_pitch", ctypes.c_longlong), ("g_pitch", ctypes.c_longlong)]
+
+
+class tg_embed_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("d", ctypes.c_int), ("vocab", ctypes.c_int), ("scale", ctypes.c_float),
+                ("pad_id", ctypes.c_int), ("pitch", ctypes.c_longlong), ("dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int)]
+
+
+class tg_norm_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("d", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_float),
+                ("x_pitch", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+class tg_distill_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("vocab", ctypes.c_int), ("k", ctypes.c_int),
+                ("temperature", ctypes.c_float), ("pitch", ctypes.c_longlong), ("grad_pitch", ctypes.c_longlong),
+                ("dtype", ctypes.c_int)]
+
+
+class tg_sample_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("vocab", ctypes.c_int), ("pitch", ctypes.c_longlong), ("dtype", ctypes.c_int),
+                ("temperature", ctypes.c_float), ("top_k", ctypes.c_int), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
 
 
 _lib = None
@@ -155,6 +182,14 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.tango_cache_append.restype = ctypes.c_int
         lib.tango_paged_aggregate.argtypes = [P(tg_paged_params), vp, vp, vp, vp, vp, vp, sz, vp]
         lib.tango_paged_aggregate.restype = ctypes.c_int
+        for name, params, n_ptrs, has_ws in (
+                ("tango_embed", tg_embed_params, 3, False), ("tango_embed_backward", tg_embed_params, 4, True),
+                ("tango_norm", tg_norm_params, 4, False), ("tango_norm_backward", tg_norm_params, 7, True),
+                ("tango_distill", tg_distill_params, 5, False), ("tango_distill_backward", tg_distill_params, 7, False),
+                ("tango_sample", tg_sample_params, 4, False)):
+            f = getattr(lib, name)
+            f.argtypes = [P(params)] + [vp] * n_ptrs + ([vp, sz] if has_ws else []) + [vp]
+            f.restype = ctypes.c_int
         lib.tg_workspace_size.argtypes = [ctypes.c_int, vp]
         lib.tg_workspace_size.restype = sz
         lib.tg_status_string.argtypes = [ctypes.c_int]
@@ -734,3 +769,182 @@ def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens,
     if st != TG_OK:
         raise TgError(st, "tango_paged_aggregate")
     return out
+
+
+# ------------------------------------------------------- the model's ends: lookup and norm
+
+def _embed_params(ids, width, rows, pitch, vocab, dtype, grad_dtype, scale, pad_id, dev):
+    if ids.numel() != rows:
+        raise ValueError("ids must hold one token per row")
+    ip = _dense(ids, "ids", torch.int32, dev)
+    return tg_embed_params(rows, width, vocab, scale, pad_id, pitch, dtype, grad_dtype), ip
+
+
+def _matrix(t, name, dtype, dev, width=None):
+    """Address of a dense [rows, width] tensor."""
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name} must be a matrix" + ("" if width is None else f" of {width} columns"))
+    return _dense(t, name, dtype, dev)
+
+
+def tango_embed(ids, embedding, out, *, scale=1.0, pad_id=-1, stream=None):
+    """out[n] = scale * embedding[ids[n]]: ids int32 [...], embedding [vocab, d], out [..., d] (its
+    rows at one pitch).  Ids equal to pad_id give zero rows."""
+    dt, dev = embedding.dtype, embedding.get_device()
+    ep = _matrix(embedding, "embedding", dt, dev)
+    vocab, d = embedding.shape
+    rows, width, pitch = _rows_pitch(out, "out", dt, dev)
+    if width != d:
+        raise ValueError("out must be as wide as the embedding")
+    code = _dtype_code(embedding)
+    p, ip = _embed_params(ids, d, rows, pitch, vocab, code, code, scale, pad_id, dev)
+    with _on_device(dev):
+        st = (_lib or load()).tango_embed(ctypes.byref(p), ip, ep, out.data_ptr(), _stream_on(stream, dev))
+    if st != TG_OK:
+        raise TgError(st, "tango_embed")
+    return out
+
+
+def tango_embed_backward(ids, dout, dembedding, *, base=None, scale=1.0, pad_id=-1, ws=None, stream=None):
+    """dembedding[v] = base[v] + scale * sum of dout's rows whose id is v: ids int32 [...], dout
+    [..., d] (its rows at one pitch), dembedding and base [vocab, d] float32 or bfloat16.  base may
+    be None (zeros) or dembedding itself (accumulation)."""
+    dt, gt, dev = dout.dtype, dembedding.dtype, dout.get_device()
+    gp = _matrix(dembedding, "dembedding", gt, dev)
+    vocab, d = dembedding.shape
+    bp = _optional(base, "base", gt, dev, dembedding.shape)
+    rows, width, pitch = _rows_pitch(dout, "dout", dt, dev)
+    if width != d:
+        raise ValueError("dout must be as wide as dembedding")
+    p, ip = _embed_params(ids, d, rows, pitch, vocab, _dtype_code(dout), _dtype_code(dembedding), scale, pad_id, dev)
+    lib, ref = _lib or load(), ctypes.byref(p)
+    with _on_device(dev):
+        wbuf = _given_ws(ws, dev) if ws is not None else _scratch(lib.tg_workspace_size(TG_WS_EMBED_BWD, ref),
+                                                                  dout.device, None, stream)
+        wp, wn = _ws_ptr(wbuf)
+        st = lib.tango_embed_backward(ref, ip, dout.data_ptr(), bp, gp, wp, wn, _stream_on(stream, dev))
+    if st != TG_OK:
+        raise TgError(st, "tango_embed_backward")
+    return dembedding
+
+
+def _norm_params(x, norm, eps, outs, vectors):
+    """tg_norm_params, and the addresses of dense tensors like x and of [d] vectors (or None)."""
+    dt, dev = x.dtype, x.get_device()
+    rows, d, pitch = _rows_pitch(x, "x", dt, dev)
+    ptrs = [_optional(t, name, dt, dev, x.shape) for name, t in outs]
+    vecs = [_optional(t, name, vt or dt, dev, (d,)) for name, t, vt in vectors]
+    return tg_norm_params(rows, d, norm, eps, pitch, _dtype_code(x)), ptrs, vecs, dev
+
+
+def tango_norm(x, gamma, beta, y, *, norm=TG_NORM_RMS, eps=1e-6, stream=None):
+    """y = gamma * n + beta with n the RMS (or TG_NORM_LAYER) norm of x's rows: x [..., d], its rows
+    at one pitch; gamma and beta [d] or None; y dense, like x."""
+    p, (yp,), (gp, bp), dev = _norm_params(x, norm, eps, (("y", y),), (("gamma", gamma, None), ("beta", beta, None)))
+    with _on_device(dev):
+        st = (_lib or load()).tango_norm(ctypes.byref(p), x.data_ptr(), gp, bp, yp, _stream_on(stream, dev))
+    if st != TG_OK:
+        raise TgError(st, "tango_norm")
+    return y
+
+
+def tango_norm_backward(x, gamma, dy, dx, *, norm=TG_NORM_RMS, eps=1e-6, dres=None, dgamma=None, dbeta=None, ws=None,
+                        stream=None):
+    """Gradients of tango_norm: dx (dense, like x) from dy, plus dres where given; dgamma and dbeta
+    (float32 [d]) where given."""
+    p, (dyp, rp, dxp), (gp, dgp, dbp), dev = _norm_params(
+        x, norm, eps, (("dy", dy), ("dres", dres), ("dx", dx)),
+        (("gamma", gamma, None), ("dgamma", dgamma, torch.float32), ("dbeta", dbeta, torch.float32)))
+    lib, ref = _lib or load(), ctypes.byref(p)
+    wp, wn, wbuf = None, 0, None
+    with _on_device(dev):
+        if dgp is not None or dbp is not None:
+            wbuf = _given_ws(ws, dev) if ws is not None else _scratch(lib.tg_workspace_size(TG_WS_NORM_BWD, ref),
+                                                                      x.device, None, stream)
+            wp, wn = _ws_ptr(wbuf)
+        st = lib.tango_norm_backward(ref, x.data_ptr(), gp, dyp, rp, dxp, dgp, dbp, wp, wn, _stream_on(stream, dev))
+    if st != TG_OK:
+        raise TgError(st, "tango_norm_backward")
+    return dx
+
+
+# ------------------------------------------------- the model's ends: distillation, sampling
+
+def _distill_params(logits, t_logits, t_ids, loss, temperature, grad, f32s):
+    dt, dev = logits.dtype, logits.get_device()
+    rows, vocab, pitch = _rows_pitch(logits, "logits", dt, dev)
+    k = t_logits.shape[-1]
+    if t_logits.numel() != rows * k or t_ids.shape != t_logits.shape:
+        raise ValueError("t_logits and t_ids must hold k entries per row of logits")
+    tp = _dense(t_logits, "t_logits", torch.float32, dev)
+    ip = _dense(t_ids, "t_ids", torch.int32, dev)
+    grad_pitch = 0
+    if grad is not None:
+        g_rows, g_width, grad_pitch = _rows_pitch(grad, "dlogits", dt, dev)
+        if g_rows != rows or g_width != vocab:
+            raise ValueError("dlogits must have logits' rows and width")
+    ptrs = []
+    for name, t, per_row in f32s:
+        if t is not None and t.numel() != rows * per_row:
+            raise ValueError(f"{name} must hold {per_row} value(s) per row")
+        ptrs.append(_optional(t, name, torch.float32, dev))
+    return tg_distill_params(rows, vocab, k, temperature, pitch, grad_pitch, _dtype_code(logits)), tp, ip, ptrs, dev
+
+
+def tango_distill(logits, t_logits, t_ids, loss, *, temperature=1.0, stats=None, stream=None):
+    """Per row, T^2 times the divergence of softmax(logits / T) over the vocabulary from a teacher's
+    softmax over its top k entries: logits [..., vocab] (rows at one pitch), t_logits float32 and
+    t_ids int32 [..., k] (negative ids: absent), loss float32 [...].  stats: float32 [..., 2] or
+    None, kept for the backward."""
+    p, tp, ip, (lp, sp), dev = _distill_params(logits, t_logits, t_ids, loss, temperature, None,
+                                               (("loss", loss, 1), ("stats", stats, 2)))
+    with _on_device(dev):
+        st = (_lib or load()).tango_distill(ctypes.byref(p), logits.data_ptr(), tp, ip, lp, sp, _stream_on(stream, dev))
+    if st != TG_OK:
+        raise TgError(st, "tango_distill")
+    return loss
+
+
+def tango_distill_backward(logits, t_logits, t_ids, dloss, dlogits, *, temperature=1.0, stats=None, loss=None,
+                           stream=None):
+    """Gradient of sum(dloss * loss) with respect to the logits, into dlogits (which may be logits).
+    stats from tango_distill, or None: formed here, and the loss too where it is given."""
+    p, tp, ip, (dp, sp, lp), dev = _distill_params(logits, t_logits, t_ids, loss, temperature, dlogits,
+                                                   (("dloss", dloss, 1), ("stats", stats, 2), ("loss", loss, 1)))
+    with _on_device(dev):
+        st = (_lib or load()).tango_distill_backward(ctypes.byref(p), logits.data_ptr(), tp, ip, dp, sp,
+                                                     dlogits.data_ptr(), lp, _stream_on(stream, dev))
+    if st != TG_OK:
+        raise TgError(st, "tango_distill_backward")
+    return dlogits
+
+
+def tango_sample(logits, uniform, token, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, logprob=None, stream=None):
+    """Draws one token per row of logits [..., vocab] (rows at one pitch) with the uniform numbers
+    uniform float32 [...] into token int32 [...], and the ln of its probability into logprob float32
+    [...].  Each setting is a number, or a tensor of one per row (float32; top_k int32)."""
+    dt, dev = logits.dtype, logits.get_device()
+    rows, vocab, pitch = _rows_pitch(logits, "logits", dt, dev)
+    f32, i32 = torch.float32, torch.int32
+    ptrs = []
+    for name, t, kind in (("uniform", uniform, f32), ("token", token, i32), ("logprob", logprob, f32)):
+        if t is not None and t.numel() != rows:
+            raise ValueError(f"{name} must hold one value per row")
+        ptrs.append(_optional(t, name, kind, dev))
+    scalars, arrays = [], []
+    for name, x, kind in (("temperature", temperature, f32), ("top_k", top_k, i32), ("top_p", top_p, f32),
+                          ("min_p", min_p, f32)):
+        if isinstance(x, torch.Tensor):
+            if x.numel() != rows:
+                raise ValueError(f"{name} must hold one value per row")
+            scalars.append(0)
+            arrays.append(_dense(x, name, kind, dev))
+        else:
+            scalars.append(x)
+            arrays.append(None)
+    p = tg_sample_params(rows, vocab, pitch, _dtype_code(logits), *scalars, *arrays)
+    with _on_device(dev):
+        st = (_lib or load()).tango_sample(ctypes.byref(p), logits.data_ptr(), *ptrs, _stream_on(stream, dev))
+    if st != TG_OK:
+        raise TgError(st, "tango_sample")
+    return token

@@ -10,6 +10,7 @@
 #include "tango.h"
 #include "tg_kernels.h"
 #include "tg_common.cuh"
+#include "tg_ends.h"
 #include "tg_serve.h"
 #include "tg_tc.h"
 
@@ -524,6 +525,68 @@ QkCall qk_call(const tg_qk_params* p, const void* q, const void* k) {
   return c;
 }
 
+// ---- the model's ends: lookup, norm, distillation, sampling
+bool dtype_ok(tg_dtype dt) { return dt == TG_F32 || dt == TG_BF16; }
+
+tg_status validate_embed(const tg_embed_params* p) {
+  if (!p || p->rows < 0 || p->d < 1 || p->vocab < 1) return TG_ERR_INVALID_ARG;
+  if (!dtype_ok(p->dtype) || !dtype_ok(p->grad_dtype)) return TG_ERR_INVALID_ARG;
+  if (p->pitch != 0 && p->pitch < p->d) return TG_ERR_INVALID_ARG;
+  if (p->rows > (1LL << 30) || p->vocab > (1 << 28) || p->d > (1 << 24)) return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
+EmbedCall embed_call(const tg_embed_params* p) {
+  EmbedCall c = {};
+  c.rows = p->rows; c.d = p->d; c.vocab = p->vocab; c.pad_id = p->pad_id; c.scale = p->scale;
+  c.pitch = p->pitch ? p->pitch : p->d;
+  c.dtype = p->dtype; c.grad_dtype = p->grad_dtype;
+  return c;
+}
+
+tg_status validate_norm(const tg_norm_params* p) {
+  if (!p || p->rows < 0 || p->d < 1) return TG_ERR_INVALID_ARG;
+  if ((p->norm != TG_NORM_RMS && p->norm != TG_NORM_LAYER) || !(p->eps > 0.f)) return TG_ERR_INVALID_ARG;
+  if (!dtype_ok(p->dtype) || (p->x_pitch != 0 && p->x_pitch < p->d)) return TG_ERR_INVALID_ARG;
+  if (p->rows > (1LL << 40) || p->d > (1 << 24)) return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
+NormCall norm_call(const tg_norm_params* p) {
+  NormCall c = {};
+  c.rows = p->rows; c.d = p->d; c.norm = p->norm; c.eps = p->eps; c.dtype = p->dtype;
+  c.x_pitch = p->x_pitch ? p->x_pitch : p->d;
+  return c;
+}
+
+tg_status validate_distill(const tg_distill_params* p) {
+  if (!p || p->rows < 0 || p->vocab < 1 || p->k < 1) return TG_ERR_INVALID_ARG;
+  if (!dtype_ok(p->dtype) || !(p->temperature >= 1e-3f && p->temperature <= 1e3f)) return TG_ERR_INVALID_ARG;
+  if ((p->pitch != 0 && p->pitch < p->vocab) || (p->grad_pitch != 0 && p->grad_pitch < p->vocab))
+    return TG_ERR_INVALID_ARG;
+  if (p->k > TG_MAX_TEACHER || p->rows > (1LL << 40) || p->vocab > (1 << 24)) return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
+DistillCall distill_call(const tg_distill_params* p, const void* logits, const float* t_logits, const int* t_ids) {
+  DistillCall c = {};
+  c.rows = p->rows; c.vocab = p->vocab; c.k = p->k; c.temperature = p->temperature; c.dtype = p->dtype;
+  c.pitch = p->pitch ? p->pitch : p->vocab;
+  c.grad_pitch = p->grad_pitch ? p->grad_pitch : p->vocab;
+  c.logits = logits; c.t_logits = t_logits; c.t_ids = t_ids;
+  return c;
+}
+
+tg_status validate_sample(const tg_sample_params* p) {
+  if (!p || p->rows < 0 || p->vocab < 1) return TG_ERR_INVALID_ARG;
+  if (!dtype_ok(p->dtype) || (p->pitch != 0 && p->pitch < p->vocab)) return TG_ERR_INVALID_ARG;
+  if (!p->temperatures && !(p->temperature >= 0.f)) return TG_ERR_INVALID_ARG;
+  if (!p->top_ps && p->top_p != p->top_p) return TG_ERR_INVALID_ARG;
+  if (!p->min_ps && !(p->min_p <= 1.f)) return TG_ERR_INVALID_ARG;
+  if (p->vocab > (1 << 19)) return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
 tg_status validate_paged(const tg_paged_params* p) {
   if (!p) return TG_ERR_INVALID_ARG;
   if (p->B < 1 || p->H < 1 || p->H > TG_MAX_HEADS || p->d_h < 1 || p->m < 1 || p->m % p->H != 0)
@@ -891,8 +954,139 @@ tg_status tango_paged_aggregate(const tg_paged_params* p, const void* q, const v
                         : launch_paged_simt(p->dtype, c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+tg_status tango_embed(const tg_embed_params* p, const int* ids, const void* embedding, void* out, tg_stream_t stream) {
+  tg_status st = validate_embed(p);
+  if (st != TG_OK) return st;
+  if (p->rows == 0) return TG_OK;  // an empty tensor may have no address
+  if (!ids || !embedding || !out) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  if (!aligned_to(ids, 4) || !aligned_to(embedding, es) || !aligned_to(out, es)) return TG_ERR_UNSUPPORTED;
+  EmbedCall c = embed_call(p);
+  if (error_word(&c.err) != cudaSuccess) return TG_ERR_CUDA;
+  c.ids = ids; c.E = embedding; c.out = out;
+  return cuda_status(launch_embed_lookup(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tango_embed_backward(const tg_embed_params* p, const int* ids, const void* dout, const void* base,
+                               void* dembedding, void* ws, size_t ws_bytes, tg_stream_t stream) {
+  tg_status st = validate_embed(p);
+  if (st != TG_OK) return st;
+  if ((p->rows > 0 && (!ids || !dout)) || !dembedding) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype), gs = elem_size(p->grad_dtype);
+  if (!aligned_to(ids, 4) || !aligned_to(dout, es) || !aligned_to(base, gs) || !aligned_to(dembedding, gs))
+    return TG_ERR_UNSUPPORTED;
+  EmbedCall c = embed_call(p);
+  st = check_ws(ws, ws_bytes, align256(embed_backward_ws_bytes(c)));
+  if (st != TG_OK) return st;
+  if (error_word(&c.err) != cudaSuccess) return TG_ERR_CUDA;
+  c.ids = ids; c.dout = dout; c.base = base; c.dE = dembedding; c.ws = ws;
+  return cuda_status(launch_embed_backward(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tango_norm(const tg_norm_params* p, const void* x, const void* gamma, const void* beta, void* y,
+                     tg_stream_t stream) {
+  tg_status st = validate_norm(p);
+  if (st != TG_OK) return st;
+  if (p->rows == 0) return TG_OK;
+  if (!x || !y) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  const void* ptrs[] = {x, gamma, beta, y};
+  for (const void* q : ptrs)
+    if (!aligned_to(q, es)) return TG_ERR_UNSUPPORTED;
+  NormCall c = norm_call(p);
+  c.x = x; c.gamma = gamma; c.beta = beta; c.y = y;
+  return cuda_status(launch_norm(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tango_norm_backward(const tg_norm_params* p, const void* x, const void* gamma, const void* dy,
+                              const void* dres, void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                              tg_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  tg_status st = validate_norm(p);
+  if (st != TG_OK) return st;
+  if (dgamma && !gamma) return TG_ERR_INVALID_ARG;
+  if (!aligned_to(dgamma, 4) || !aligned_to(dbeta, 4)) return TG_ERR_UNSUPPORTED;
+  if (p->rows == 0) {  // empty sums (and an empty tensor may have no address)
+    cudaError_t e = dgamma ? cudaMemsetAsync(dgamma, 0, p->d * sizeof(float), stream) : cudaSuccess;
+    if (e == cudaSuccess && dbeta) e = cudaMemsetAsync(dbeta, 0, p->d * sizeof(float), stream);
+    return cuda_status(e);
+  }
+  if (!x || !dy || !dx) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  const void* ptrs[] = {x, gamma, dy, dres, dx};
+  for (const void* q : ptrs)
+    if (!aligned_to(q, es)) return TG_ERR_UNSUPPORTED;
+  NormCall c = norm_call(p);
+  if (dgamma || dbeta) {
+    st = check_ws(ws, ws_bytes, align256(norm_backward_ws_bytes(c)));
+    if (st != TG_OK) return st;
+  }
+  c.x = x; c.gamma = gamma; c.dy = dy; c.dres = dres; c.dx = dx; c.dgamma = dgamma; c.dbeta = dbeta; c.ws = ws;
+  return cuda_status(launch_norm_backward(c, stream));
+}
+
+tg_status tango_distill(const tg_distill_params* p, const void* logits, const float* t_logits, const int* t_ids,
+                        float* loss, float* stats, tg_stream_t stream) {
+  tg_status st = validate_distill(p);
+  if (st != TG_OK) return st;
+  if (p->rows == 0) return TG_OK;
+  if (!logits || !t_logits || !t_ids || !loss) return TG_ERR_INVALID_ARG;
+  if (!aligned_to(logits, elem_size(p->dtype)) || !aligned_to(t_logits, 4) || !aligned_to(t_ids, 4) ||
+      !aligned_to(loss, 4) || !aligned_to(stats, 8))
+    return TG_ERR_UNSUPPORTED;
+  DistillCall c = distill_call(p, logits, t_logits, t_ids);
+  if (error_word(&c.err) != cudaSuccess) return TG_ERR_CUDA;
+  c.loss = loss; c.stats_out = stats;
+  return cuda_status(launch_distill(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tango_distill_backward(const tg_distill_params* p, const void* logits, const float* t_logits,
+                                 const int* t_ids, const float* dloss, const float* stats, void* dlogits, float* loss,
+                                 tg_stream_t stream) {
+  tg_status st = validate_distill(p);
+  if (st != TG_OK) return st;
+  if (stats && loss) return TG_ERR_INVALID_ARG;
+  if (p->rows == 0) return TG_OK;
+  if (!logits || !t_logits || !t_ids || !dloss || !dlogits) return TG_ERR_INVALID_ARG;
+  const size_t es = elem_size(p->dtype);
+  if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned_to(t_logits, 4) || !aligned_to(t_ids, 4) ||
+      !aligned_to(dloss, 4) || !aligned_to(loss, 4) || !aligned_to(stats, 8))
+    return TG_ERR_UNSUPPORTED;
+  DistillCall c = distill_call(p, logits, t_logits, t_ids);
+  if (dlogits == logits && c.pitch != c.grad_pitch) return TG_ERR_INVALID_ARG;
+  if (error_word(&c.err) != cudaSuccess) return TG_ERR_CUDA;
+  c.dloss = dloss; c.stats = stats; c.dlogits = dlogits; c.loss = loss;
+  return cuda_status(launch_distill_backward(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tango_sample(const tg_sample_params* p, const void* logits, const float* uniform, int* token,
+                       float* logprob, tg_stream_t stream) {
+  tg_status st = validate_sample(p);
+  if (st != TG_OK) return st;
+  if (p->rows == 0) return TG_OK;
+  if (!logits || !uniform || !token) return TG_ERR_INVALID_ARG;
+  if (!aligned_to(logits, elem_size(p->dtype))) return TG_ERR_UNSUPPORTED;
+  const void* words[] = {uniform, token, logprob, p->temperatures, p->top_ks, p->top_ps, p->min_ps};
+  for (const void* q : words)
+    if (!aligned_to(q, 4)) return TG_ERR_UNSUPPORTED;
+  SampleCall c = {};
+  c.p = *p;
+  if (c.p.pitch == 0) c.p.pitch = p->vocab;
+  if (error_word(&c.err) != cudaSuccess) return TG_ERR_CUDA;
+  c.logits = logits; c.uniform = uniform; c.token = token; c.logprob = logprob;
+  return cuda_status(launch_sample(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t tg_workspace_size(int which, const void* params) {
   if (!params) return 0;
+  if (which == TG_WS_EMBED_BWD) {
+    const tg_embed_params* p = static_cast<const tg_embed_params*>(params);
+    return validate_embed(p) == TG_OK ? align256(embed_backward_ws_bytes(embed_call(p))) : 0;
+  }
+  if (which == TG_WS_NORM_BWD) {
+    const tg_norm_params* p = static_cast<const tg_norm_params*>(params);
+    return validate_norm(p) == TG_OK && p->rows > 0 ? align256(norm_backward_ws_bytes(norm_call(p))) : 0;
+  }
   if (which == TG_WS_QK_BWD) {
     const tg_qk_params* p = static_cast<const tg_qk_params*>(params);
     if (validate_qk(p) != TG_OK || (!p->q_gain && !p->k_gain)) return 0;

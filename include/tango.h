@@ -103,6 +103,8 @@ typedef enum { TG_F32 = 0, TG_BF16 = 1 } tg_dtype;
 
 #define TG_WS_QK_BWD 16 /* params: const tg_qk_params*: tango_qk_norm_rope_backward */
 #define TG_WS_PAGED 17  /* params: const tg_paged_params*: tango_paged_aggregate */
+#define TG_WS_EMBED_BWD 18 /* params: const tg_embed_params*: tango_embed_backward */
+#define TG_WS_NORM_BWD 19  /* params: const tg_norm_params*: tango_norm_backward */
 
 #define TG_MAX_HEADS 64
 
@@ -114,6 +116,11 @@ typedef enum { TG_F32 = 0, TG_BF16 = 1 } tg_dtype;
 #define TG_NORM_NONE 0 /* n = x                          */
 #define TG_NORM_UNIT 1 /* n = x / max(|x|, 1e-12)        */
 #define TG_NORM_RMS 2  /* n = x / sqrt(mean(x^2) + eps)  */
+/* tg_norm_params.norm: TG_NORM_RMS, or */
+#define TG_NORM_LAYER 3 /* n = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) */
+
+/* most teacher entries of a row (tg_distill_params.k) */
+#define TG_MAX_TEACHER 1024
 
 /*
  * Parameters of one aggregation (eq. 5).
@@ -577,6 +584,163 @@ tg_status tango_paged_aggregate(const tg_paged_params *p, const void *q, const v
                                 const void *k_pages, const void *g_pages, void *ws, size_t ws_bytes,
                                 tg_stream_t stream);
 
+/*
+ * Token lookup and its gradient, as tango_model_forward's embedding is trained.
+ *   rows        tokens (0: the lookup launches nothing; the gradient is base or zeros);
+ *               <= 2^30
+ *   d, vocab    width and rows of the embedding
+ *   scale       factor on every looked-up row
+ *   pad_id      an id that stands for no token: its output rows are zeros and it gives no
+ *               gradient (any value; -1 for ids that are padded with -1)
+ *   pitch       elements between rows of out / dout (0: d)
+ *   dtype       of the embedding, out and dout
+ *   grad_dtype  of dembedding and base
+ * ids: device int[rows].  An id that is neither pad_id nor in [0, vocab) gives a zero row,
+ * no gradient and TG_ERR_DEVICE (kernel code 4).
+ */
+typedef struct {
+    long long rows;
+    int d, vocab;
+    float scale;
+    int pad_id;
+    long long pitch;
+    tg_dtype dtype, grad_dtype;
+} tg_embed_params;
+
+/* out[n] = scale * embedding[ids[n]], formed in fp32 and rounded once (scale 1: the row itself).
+ * embedding: device [vocab, d]; out: device [rows, d] at `pitch`, written. */
+tg_status tango_embed(const tg_embed_params *p, const int *ids, const void *embedding, void *out,
+                      tg_stream_t stream);
+
+/*
+ * dembedding[v] = base[v] + scale * sum over the tokens n with ids[n] = v of dout[n].
+ * base: device [vocab, d] or NULL (zeros); may be dembedding itself, so that the gradient of the
+ * tied output matrix is added to.  dembedding: device [vocab, d], dense, every row written.  The
+ * tokens are sorted by id first and summed in fp32 in an order that depends on the sizes only
+ * (no atomics on sums: the same call gives the same bits).  ws: device scratch of
+ * tg_workspace_size(TG_WS_EMBED_BWD, p) bytes, 256-byte aligned.
+ */
+tg_status tango_embed_backward(const tg_embed_params *p, const int *ids, const void *dout, const void *base,
+                               void *dembedding, void *ws, size_t ws_bytes, tg_stream_t stream);
+
+/*
+ * RMS or layer norm of rows of d values, y = gamma * n + beta.
+ *   rows     rows (0 launches nothing but for the gradients' zeros)
+ *   d        width (1..2^24)
+ *   norm     TG_NORM_RMS or TG_NORM_LAYER
+ *   eps      > 0
+ *   x_pitch  elements between rows of x (0: d)
+ *   dtype    of x, gamma, beta, y and their gradients dy, dres, dx; arithmetic is fp32, outputs
+ *            are rounded once
+ */
+typedef struct {
+    long long rows;
+    int d, norm;
+    float eps;
+    long long x_pitch;
+    tg_dtype dtype;
+} tg_norm_params;
+
+/* gamma, beta: device [d], or NULL (1, 0).  y: device [rows, d], dense, written; may be a dense x. */
+tg_status tango_norm(const tg_norm_params *p, const void *x, const void *gamma, const void *beta, void *y,
+                     tg_stream_t stream);
+
+/*
+ * Gradients of tango_norm: with r = 1 / sqrt(mean square + eps) and dn = gamma * dy,
+ *   dx = r (dn - n mean(dn * n) - mean(dn)) + dres     (rms: without mean(dn)),
+ *   dgamma = sum over rows of dy * n,  dbeta = sum over rows of dy.
+ * The row statistics are formed from x again.  dres: device [rows, d] or NULL: the gradient that
+ * reaches x past the norm (a residual stream's).  dx: device [rows, d], written; may be dy, dres or
+ * a dense x.  dgamma, dbeta: device float[d], written (summed in a fixed order), or NULL; dgamma
+ * needs gamma.  ws: device scratch of tg_workspace_size(TG_WS_NORM_BWD, p) bytes, 256-byte aligned
+ * (not used, and may be NULL, without dgamma and dbeta).
+ */
+tg_status tango_norm_backward(const tg_norm_params *p, const void *x, const void *gamma, const void *dy,
+                              const void *dres, void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                              tg_stream_t stream);
+
+/*
+ * Distillation from a teacher's top logits.  Per row, with the student's logits z over the
+ * vocabulary and the teacher's k logits t at the tokens i_1 .. i_k:
+ *   p = softmax(t / T) over the row's entries,  q = softmax(z / T) over the vocabulary,
+ *   loss = T^2 sum_e p_e (ln p_e - ln q_{i_e}).
+ * One entry a row (k = 1) at T = 1 is the cross entropy with that token.
+ *   rows         rows (0 launches nothing)
+ *   vocab, k     1 <= vocab, 1 <= k <= TG_MAX_TEACHER
+ *   temperature  T in [0.001, 1000]
+ *   pitch        elements between rows of logits (0: vocab)
+ *   grad_pitch   elements between rows of dlogits (0: vocab)
+ *   dtype        of logits and dlogits; arithmetic is fp32
+ * t_logits: device float[rows, k].  t_ids: device int[rows, k]: an entry with a negative id, or
+ * with t = -inf, is absent; an id >= vocab is absent too and flagged TG_ERR_DEVICE (kernel code
+ * 7).  A token may stand in several entries.  A row without entries (padding) has loss 0 and
+ * gradient 0.  Student logits of -inf have q = 0 (an entry there gives loss inf; its gradient is
+ * finite); a row with NaN gives NaN.
+ */
+typedef struct {
+    long long rows;
+    int vocab, k;
+    float temperature;
+    long long pitch, grad_pitch;
+    tg_dtype dtype;
+} tg_distill_params;
+
+/* loss: device float[rows], written.  stats: device float[rows, 2] or NULL: every row's largest
+ * logit and sum of e^{(z - largest) / T}, for the backward; written. */
+tg_status tango_distill(const tg_distill_params *p, const void *logits, const float *t_logits, const int *t_ids,
+                        float *loss, float *stats, tg_stream_t stream);
+
+/*
+ * Gradient of sum over rows of dloss * loss:
+ *   dz_j = dloss T (q_j - sum over the entries e with i_e = j of p_e).
+ * dloss: device float[rows].  dlogits: device [rows, vocab] at grad_pitch, written; may be logits
+ * (at the same pitch).  stats: as tango_distill left them for the same arguments, or NULL: they are
+ * formed here from the one reading of the logits, so that with `loss` (device float[rows] or NULL;
+ * NULL with stats) one call gives a training step's loss and gradient.
+ */
+tg_status tango_distill_backward(const tg_distill_params *p, const void *logits, const float *t_logits,
+                                 const int *t_ids, const float *dloss, const float *stats, void *dlogits, float *loss,
+                                 tg_stream_t stream);
+
+/*
+ * Draws one token a row from given uniform numbers.  Per row, with logits x:
+ *   w_i = e^{(x_i - max x) / T}; a token with w_i < 2^-40 (-inf, NaN) is never drawn;
+ *   of these the k largest (top_k); of these the shortest run from the largest down with at least
+ *   the share top_p of their mass; of these the ones with w_i >= min_p (the largest stays always);
+ *   the token is the first one i in ascending order with
+ *   sum over kept j <= i of w_j  >  u * sum over kept j of w_j.
+ * Equal logits are ranked by ascending index.  T = 0 takes the largest logit (lowest index).  +inf
+ * logits share the row evenly.  A row with no token to draw (all -inf or NaN) gives -1.  The sums
+ * are formed in 64-bit fixed point from weights of 40 bits and more, so that the token is that of
+ * the real numbers but where u or top_p lie within about 1e-12 of a border.
+ *   rows, vocab     rows >= 0 (0 launches nothing); 1 <= vocab <= 2^19
+ *   pitch           elements between rows of logits (0: vocab)
+ *   dtype           of logits
+ *   temperature, top_k, top_p, min_p   settings of every row, unless the array of that setting is
+ *                   given: T >= 0; top_k <= 0: off; top_p >= 1: off, <= 0: the largest only;
+ *                   min_p <= 0: off
+ *   temperatures, top_ks, top_ps, min_ps  device [rows], or NULL.  Values outside their range (T < 0,
+ *                   NaN, min_p > 1) are clamped into it (NaN: the setting is off, T = 1) and
+ *                   flagged TG_ERR_DEVICE (kernel code 8)
+ */
+typedef struct {
+    int rows, vocab;
+    long long pitch;
+    tg_dtype dtype;
+    float temperature;
+    int top_k;
+    float top_p, min_p;
+    const float *temperatures;
+    const int *top_ks;
+    const float *top_ps, *min_ps;
+} tg_sample_params;
+
+/* uniform: device float[rows], in [0, 1); other values are clamped into it and flagged TG_ERR_DEVICE (kernel
+ * code 8).  token: device int[rows], written.  logprob: device float[rows] or NULL: ln of the
+ * probability the token was drawn with, w / sum over kept (T = 0: 0; no token: -inf); written. */
+tg_status tango_sample(const tg_sample_params *p, const void *logits, const float *uniform, int *token,
+                       float *logprob, tg_stream_t stream);
+
 /* Workspace bytes needed by the call `which` (TG_WS_*) with `params`; 0 for invalid
  * parameters (validate with the call itself to get the reason). */
 size_t tg_workspace_size(int which, const void *params);
@@ -590,7 +754,7 @@ const char *tg_status_string(tg_status s);
  * TG_ERR_CUDA if the synchronisation itself failed.  If `detail` is not NULL it
  * receives the raw word (bit 0: timeout, bit 1: value out of range; bits 8..15:
  * the kernel that recorded it, 1 = TANGO, 2 = WANGO, 3 = GEMM, 4 = embedding lookup,
- * 5 = the aggregation backward, 6 = the paged cache calls).
+ * 5 = the aggregation backward, 6 = the paged cache calls, 7 = distillation, 8 = sampling).
  */
 tg_status tg_check_device_error(tg_stream_t stream, unsigned *detail);
 
