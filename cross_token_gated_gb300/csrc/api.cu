@@ -532,7 +532,7 @@ tg_status validate_embed(const tg_embed_params* p) {
   if (!p || p->rows < 0 || p->d < 1 || p->vocab < 1) return TG_ERR_INVALID_ARG;
   if (!dtype_ok(p->dtype) || !dtype_ok(p->grad_dtype)) return TG_ERR_INVALID_ARG;
   if (p->pitch != 0 && p->pitch < p->d) return TG_ERR_INVALID_ARG;
-  if (p->rows > (1LL << 30) || p->vocab > (1 << 28) || p->d > (1 << 24)) return TG_ERR_UNSUPPORTED;
+  if (p->rows > (1LL << 30) || p->vocab > (1 << 28) || p->d > (1 << 20)) return TG_ERR_UNSUPPORTED;
   return TG_OK;
 }
 

@@ -588,7 +588,7 @@ tg_status tango_paged_aggregate(const tg_paged_params *p, const void *q, const v
  * Token lookup and its gradient, as tango_model_forward's embedding is trained.
  *   rows        tokens (0: the lookup launches nothing; the gradient is base or zeros);
  *               <= 2^30
- *   d, vocab    width and rows of the embedding
+ *   d, vocab    width (<= 2^20) and rows (<= 2^28) of the embedding
  *   scale       factor on every looked-up row
  *   pad_id      an id that stands for no token: its output rows are zeros and it gives no
  *               gradient (any value; -1 for ids that are padded with -1)
