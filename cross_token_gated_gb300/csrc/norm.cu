@@ -5,10 +5,17 @@
 //   dn = gamma dy,  dx = r (dn - n <dn n> - <dn>) + dres,  dgamma = sum dy n,  dbeta = sum dy
 //
 // Means are over the row, <dn> only with mu.  All of it is bound by HBM bandwidth: each value is
-// read and written once.
+// read and written once.  A row stays in the registers of its group of threads (8 lanes, a warp, or
+// 128 or 512 threads, by the row's length), as the 16-byte vectors that were loaded, and the next
+// row is on its way meanwhile.  The gradient needs two joins a row: sum x, then sum (x - mu)^2,
+// sum dn and sum dn (x - mu) at once (rms: one).  A thread keeps its columns' dgamma and dbeta in
+// registers over all rows of its persistent block.
 #include "tg_common.cuh"
 #include "tg_ends.h"
+#include "tg_ptx.cuh"
 #include "tg_serve.h"
+
+#include <type_traits>
 
 namespace tg {
 namespace {
@@ -106,17 +113,259 @@ __global__ void __launch_bounds__(kThreads) norm_backward_any_kernel(const NormA
   }
 }
 
-// dgamma (blockIdx.y 0) and dbeta (1): a warp per column adds up the blocks' partial sums.
-__global__ void __launch_bounds__(256) norm_weight_sum_kernel(const float* part, int blocks, int d, float* dgamma,
-                                                              float* dbeta) {
-  const int c = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+// ------------------------------------------------------------------- rows in registers
+
+template <typename T> struct Wide;  // 16 bytes of T
+template <> struct Wide<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  static __device__ __forceinline__ float inv_sqrt(float v) { return 1.f / sqrtf(v); }
+};
+template <> struct Wide<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
+    f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
+    f[4] = ptx::bf16lo(u.z); f[5] = ptx::bf16hi(u.z); f[6] = ptx::bf16lo(u.w); f[7] = ptx::bf16hi(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]), ptx::pack_bf16x2(f[4], f[5]),
+                      ptx::pack_bf16x2(f[6], f[7]));
+  }
+  static __device__ __forceinline__ float inv_sqrt(float v) { return rsqrtf(v); }  // 2 units: far below a bf16 rounding
+};
+
+template <int kGroup> constexpr int kBlock = kGroup > 256 ? kGroup : 256;
+
+// Sums over the group of K values at a time; every thread gets them.  Groups of several warps join
+// through shared memory, in two buffers taken in turn (all groups of a block make the same calls).
+template <int kGroup, int K>
+struct GroupSum {
+  float (*buf)[K][kBlock<kGroup> / 32];
+  int side = 0;
+  __device__ __forceinline__ void operator()(float (&v)[K]) {
+    constexpr int W = kGroup / 32;
+#pragma unroll
+    for (int o = (kGroup < 32 ? kGroup : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if constexpr (W > 1) {
+      const int warp = threadIdx.x / 32;
+      if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < K; ++i) buf[side][i][warp] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        v[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) v[i] += buf[side][i][warp / W * W + w];
+      }
+      side ^= 1;
+    }
+  }
+};
+
+// One row of the group's: NV vectors a thread, vector k * kGroup + lane.
+template <int kGroup, int NV>
+__device__ __forceinline__ void load_row(uint4 (&u)[NV], const void* row, int lane, int nvec, bool live) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = k * kGroup + lane;
+    u[k] = live && i < nvec ? reinterpret_cast<const uint4*>(row)[i] : make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <typename T, int kGroup, int NV>
+__global__ void __launch_bounds__(kBlock<kGroup>) norm_kernel(const NormArgs<T> a) {
+  constexpr int E = Wide<T>::E, kRows = kBlock<kGroup> / kGroup;
+  __shared__ float buf[2][1][kBlock<kGroup> / 32];
+  GroupSum<kGroup, 1> sum{buf};
+  const int lane = threadIdx.x % kGroup, nvec = a.d / E;
+  const float inv_d = 1.f / (float)a.d;
+  uint4 g[NV], b[NV], u[NV];
+  load_row<kGroup>(g, a.gamma, lane, nvec, a.gamma != nullptr);
+  load_row<kGroup>(b, a.beta, lane, nvec, a.beta != nullptr);
+  const long long step = (long long)gridDim.x * kRows;
+  long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup, row0 = (long long)blockIdx.x * kRows;
+  load_row<kGroup>(u, a.x + row * a.x_pitch, lane, nvec, row < a.rows);
+  for (; row0 < a.rows; row0 += step, row += step) {
+    uint4 next[NV];
+    load_row<kGroup>(next, a.x + (row + step) * a.x_pitch, lane, nvec, row + step < a.rows);
+    float mu = 0.f;
+    if (a.layer) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float f[E];
+        Wide<T>::unpack(u[k], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[0] += f[e];
+      }
+      sum(s);
+      mu = s[0] * inv_d;
+    }
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (k * kGroup + lane >= nvec) continue;
+      float f[E];
+      Wide<T>::unpack(u[k], f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) ss[0] = fmaf(f[e] - mu, f[e] - mu, ss[0]);
+    }
+    sum(ss);
+    const float r = Wide<T>::inv_sqrt(fmaf(ss[0], inv_d, a.eps));
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = k * kGroup + lane;
+      if (row >= a.rows || i >= nvec) continue;
+      float f[E], gf[E], bf[E];
+      Wide<T>::unpack(u[k], f);
+      Wide<T>::unpack(g[k], gf);
+      Wide<T>::unpack(b[k], bf);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mu) * r, a.gamma ? gf[e] : 1.f, bf[e]);
+      reinterpret_cast<uint4*>(a.y + row * a.d)[i] = Wide<T>::pack(f);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) u[k] = next[k];
+  }
+}
+
+// The block's sums of dgamma or dbeta, of its groups in order, into its row of part.
+template <int kGroup, int NV, int E>
+__device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float* sh, float* dst, int d) {
+  constexpr int kRows = kBlock<kGroup> / kGroup;
+  const int lane = threadIdx.x % kGroup, nvec = d / E;
+  float* mine = kRows > 1 ? sh + (threadIdx.x / kGroup) * d : dst;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = k * kGroup + lane;
+    if (i < nvec)
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<float4*>(mine + i * E + e) = make_float4(acc[k * E + e], acc[k * E + e + 1], acc[k * E + e + 2], acc[k * E + e + 3]);
+  }
+  if constexpr (kRows > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += kBlock<kGroup>) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRows; ++w) s += sh[w * d + c];
+      dst[c] = s;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int kGroup, int NV>
+__global__ void __launch_bounds__(kBlock<kGroup>) norm_backward_kernel(const NormArgs<T> a) {
+  constexpr int E = Wide<T>::E, kRows = kBlock<kGroup> / kGroup;
+  extern __shared__ float columns[];  // [kRows][d], where kRows > 1
+  __shared__ float buf1[2][1][kBlock<kGroup> / 32], buf3[2][3][kBlock<kGroup> / 32];
+  GroupSum<kGroup, 1> sum1{buf1};
+  GroupSum<kGroup, 3> sum3{buf3};
+  const int lane = threadIdx.x % kGroup, nvec = a.d / E;
+  const float inv_d = 1.f / (float)a.d;
+  uint4 g[NV], x[NV], y[NV];
+  float dg[NV * E] = {}, db[NV * E] = {};
+  load_row<kGroup>(g, a.gamma, lane, nvec, a.gamma != nullptr);
+  const long long step = (long long)gridDim.x * kRows;
+  long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup, row0 = (long long)blockIdx.x * kRows;
+  load_row<kGroup>(x, a.x + row * a.x_pitch, lane, nvec, row < a.rows);
+  load_row<kGroup>(y, a.dy + row * a.d, lane, nvec, row < a.rows);
+  for (; row0 < a.rows; row0 += step, row += step) {
+    uint4 res[NV], next_x[NV], next_y[NV];
+    const bool live = row < a.rows, more = row + step < a.rows;
+    load_row<kGroup>(res, a.dres + row * a.d, lane, nvec, live && a.dres);
+    load_row<kGroup>(next_x, a.x + (row + step) * a.x_pitch, lane, nvec, more);
+    load_row<kGroup>(next_y, a.dy + (row + step) * a.d, lane, nvec, more);
+    float mu = 0.f;
+    if (a.layer) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float f[E];
+        Wide<T>::unpack(x[k], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[0] += f[e];
+      }
+      sum1(s);
+      mu = s[0] * inv_d;
+    }
+    float s[3] = {0.f, 0.f, 0.f};  // (x - mu)^2, dn (x - mu), dn
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (k * kGroup + lane >= nvec) continue;
+      float f[E], h[E], gf[E];
+      Wide<T>::unpack(x[k], f);
+      Wide<T>::unpack(y[k], h);
+      Wide<T>::unpack(g[k], gf);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float c = f[e] - mu, dn = a.gamma ? h[e] * gf[e] : h[e];
+        s[0] = fmaf(c, c, s[0]);
+        s[1] = fmaf(dn, c, s[1]);
+        s[2] += dn;
+      }
+    }
+    sum3(s);
+    const float r = Wide<T>::inv_sqrt(fmaf(s[0], inv_d, a.eps));
+    const float m1 = s[1] * inv_d * r, m0 = a.layer ? s[2] * inv_d : 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = k * kGroup + lane;
+      if (!live || i >= nvec) continue;
+      float f[E], h[E], gf[E], rf[E];
+      Wide<T>::unpack(x[k], f);
+      Wide<T>::unpack(y[k], h);
+      Wide<T>::unpack(g[k], gf);
+      Wide<T>::unpack(res[k], rf);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float n = (f[e] - mu) * r, dn = a.gamma ? h[e] * gf[e] : h[e];
+        dg[k * E + e] = fmaf(h[e], n, dg[k * E + e]);
+        db[k * E + e] += h[e];
+        f[e] = fmaf(r, dn - fmaf(n, m1, m0), rf[e]);
+      }
+      reinterpret_cast<uint4*>(a.dx + row * a.d)[i] = Wide<T>::pack(f);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      x[k] = next_x[k];
+      y[k] = next_y[k];
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.want_gamma) block_columns<kGroup, NV, E>(dg, columns, a.part + (size_t)blockIdx.x * a.d, a.d);
+  if (a.want_beta) block_columns<kGroup, NV, E>(db, columns, a.part + ((size_t)gridDim.x + blockIdx.x) * a.d, a.d);
+}
+
+// dgamma (blockIdx.y 0) and dbeta (1): 32 columns a block, each by 32 threads that take every 32nd
+// of the blocks' partial sums.  Launched while the last blocks still run.
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* part, int blocks, int d, float* dgamma,
+                                                               float* dbeta) {
+  __shared__ float sh[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   float* dst = blockIdx.y ? dbeta : dgamma;
-  if (c >= d || !dst) return;
-  const float* p = part + (size_t)blockIdx.y * blocks * d + c;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!dst) return;
   float s = 0.f;
-  for (int b = lane; b < blocks; b += 32) s += p[(size_t)b * d];
+  if (c < d) {
+    const float* p = part + (size_t)blockIdx.y * blocks * d + c;
+#pragma unroll 4
+    for (int b = warp; b < blocks; b += 32) s += __ldcg(p + (size_t)b * d);
+  }
+  sh[warp][lane] = s;
+  __syncthreads();
+  s = sh[lane][warp];
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) dst[c] = s;
+  if (lane == 0 && blockIdx.x * 32 + warp < d) dst[blockIdx.x * 32 + warp] = s;
 }
 
 template <typename T>
@@ -136,21 +385,77 @@ int grid_of(long long rows, int per_sm) {
   return (int)(rows < most ? rows : most);
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Whether rows are taken 16 bytes at a time and fit the registers of at most 512 threads.
+template <typename T>
+bool in_registers(const NormArgs<T>& a) {
+  constexpr int E = Wide<T>::E;
+  const void* ptrs[] = {a.x, a.gamma, a.beta, a.dy, a.dres, a.y, a.dx};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return false;
+  return a.d % E == 0 && a.x_pitch % E == 0 && a.d / E <= 2048;
+}
+
+// Calls f with the group and the vectors of a thread for a row of nvec: 8 lanes up to 16 vectors, a
+// warp up to 128, 128 threads up to 512, else 512 (a thread holds at most 4).
+template <typename F>
+auto by_length(int nvec, F f) {
+  using std::integral_constant;
+#define TG_CASE(G, N) f(integral_constant<int, G>(), integral_constant<int, N>())
+  if (nvec <= 8) return TG_CASE(8, 1);
+  if (nvec <= 16) return TG_CASE(8, 2);
+  if (nvec <= 32) return TG_CASE(32, 1);
+  if (nvec <= 64) return TG_CASE(32, 2);
+  if (nvec <= 96) return TG_CASE(32, 3);
+  if (nvec <= 128) return TG_CASE(32, 4);
+  if (nvec <= 256) return TG_CASE(128, 2);
+  if (nvec <= 512) return TG_CASE(128, 4);
+  if (nvec <= 1024) return TG_CASE(512, 2);
+  return TG_CASE(512, 4);
+#undef TG_CASE
+}
+
 template <typename T>
 cudaError_t norm_t(const NormCall& c, cudaStream_t s) {
-  norm_any_kernel<T><<<grid_of(c.rows, 8), kThreads, 0, s>>>(norm_args<T>(c));
+  const NormArgs<T> a = norm_args<T>(c);
+  if (in_registers(a))
+    return by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
+      constexpr int G = decltype(group)::value, B = kBlock<G>;
+      norm_kernel<T, G, decltype(nv)::value><<<grid_of((c.rows + B / G - 1) / (B / G), 1024 / B), B, 0, s>>>(a);
+      return cudaGetLastError();
+    });
+  norm_any_kernel<T><<<grid_of(c.rows, 8), kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t norm_backward_t(const NormCall& c, cudaStream_t s) {
   const NormArgs<T> a = norm_args<T>(c);
-  const int grid = grid_of(c.rows, kBwdPerSm);
-  norm_backward_any_kernel<T><<<grid, kThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  int grid = grid_of(c.rows, kBwdPerSm);
+  cudaError_t e;
+  if (in_registers(a)) {
+    e = by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
+      constexpr int G = decltype(group)::value, B = kBlock<G>, R = B / G;
+      grid = grid_of((c.rows + R - 1) / R, G > 256 ? 1 : 2);
+      norm_backward_kernel<T, G, decltype(nv)::value><<<grid, B, R > 1 ? R * c.d * sizeof(float) : 0, s>>>(a);
+      return cudaGetLastError();
+    });
+  } else {
+    norm_backward_any_kernel<T><<<grid, kThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess || !(c.dgamma || c.dbeta)) return e;
-  norm_weight_sum_kernel<<<dim3(ceil_div(c.d, 8), 2), 256, 0, s>>>(a.part, grid, c.d, c.dgamma, c.dbeta);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(c.d, 32), 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_weight_sum_kernel, (const float*)a.part, grid, c.d, c.dgamma, c.dbeta);
 }
 
 }  // namespace
