@@ -35,12 +35,6 @@ struct DistillArgs {
   unsigned* err;
 };
 
-struct Teacher {
-  int id[TG_MAX_TEACHER];    // -1: absent
-  float p[TG_MAX_TEACHER];   // the logit first, then e^{(t - max) / T}, then the probability
-  float z[TG_MAX_TEACHER];   // the student's logit there
-};
-
 __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -102,24 +96,32 @@ __device__ __forceinline__ RowSpan row_span(const T* row, int vocab) {
 template <typename T>
 __device__ __forceinline__ int edge_col(const RowSpan& r, int i) { return i < r.lead ? i : i + r.nvec * Wide<T>::E; }
 
-// Largest value so far and sum of e^{(z - largest) / T}; -inf and 0 at the start.
+// Largest value and sum of e^{(z - largest) / T} of a part of a row; -inf and 0 without elements.
 struct Running {
   float m, s;
 };
-__device__ __forceinline__ Running join(Running a, Running b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return Running{m, a.s + b.s};  // 0, or NaN
-  return Running{m, a.s * ptx::ex2_approx((a.m - m) * c) + b.s * ptx::ex2_approx((b.m - m) * c)};
-}
 
-// The row's, from its warps'; the largest value as 0 where there is none above -inf.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The row's, from its warps' by a whole warp; the largest value as 0 where there is none above -inf.
 template <int W>
 __device__ __forceinline__ Running row_total(const Running (&part)[W], float c) {
-  Running st = part[0];
+  static_assert(W <= 32 && (W & (W - 1)) == 0, "warps of a row");
+  Running st = part[threadIdx.x & (W - 1)];
+  float m = st.m;
 #pragma unroll
-  for (int w = 1; w < W; ++w) st = join(st, part[w], c);
-  if (st.m == -INFINITY) st.m = 0.f;
-  return st;
+  for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (m == -INFINITY) m = 0.f;
+  st.s = st.m == -INFINITY ? st.s : st.s * ptx::ex2_approx((st.m - m) * c);
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+  return Running{m, st.s};
 }
 template <typename T>
 __device__ __forceinline__ Running kept_stats(const DistillArgs<T>& a, long long row) {
@@ -128,112 +130,217 @@ __device__ __forceinline__ Running kept_stats(const DistillArgs<T>& a, long long
 }
 __device__ __forceinline__ float inverse(float s) { return s == 0.f ? 0.f : 1.f / s; }
 
-// The gradient at the entries' tokens, where the teacher's share comes off: each token by its first
-// entry, with the shares of all entries that name it.
+// A row's entries (dynamic shared memory, k of each; four rows in turn).
+struct Entries {
+  int* id;      // -1: absent, or another entry stands for the token
+  float* p;     // probability
+  float* z;     // the student's logit
+  float* share; // sum of p over the entries of this token
+};
+constexpr int kSeenWords = 1024;  // one bit per token, modulo 32,768
+
+// The gradient at the entries' tokens, where the teacher's share comes off.
 template <typename T>
-__device__ __forceinline__ void fix_entries(const DistillArgs<T>& a, const Teacher& t, long long row, Running st, int tid, int threads) {
-  T* dz = a.dz + row * a.grad_pitch;
-  const float f = a.dloss[row] * a.temp, inv = inverse(st.s);
-  for (int e = tid; e < a.k; e += threads) {
-    const int id = t.id[e];
-    if (id < 0) continue;
-    float p = 0.f;
-    bool first = true;
-    for (int i = 0; i < a.k; ++i)
-      if (t.id[i] == id) {
-        first &= i >= e;
-        p += t.p[i];
-      }
-    if (first) io<T>::st(dz + id, f * (exp2f((t.z[e] - st.m) * a.c) * inv - p));
+__device__ __forceinline__ void fix_entries(const DistillArgs<T>& a, const Entries& t, T* dz, float f, Running st, int tid,
+                                            int threads) {
+  const float inv = inverse(st.s);
+  for (int e = tid; e < a.k; e += threads)
+    if (t.id[e] >= 0) io<T>::st(dz + t.id[e], f * (exp2f((t.z[e] - st.m) * a.c) * inv - t.share[e]));
+}
+
+// The teacher's warp takes a row's entries in three steps, a row apart each, so that no step waits
+// for its loads: ids and logits on their way to shared memory; the student's logits there; the
+// probabilities.
+template <typename T>
+__device__ __forceinline__ void fetch_entries(const DistillArgs<T>& a, long long row, const Entries& t, int lane) {
+  for (int e = lane; e < a.k; e += 32) {
+    cp_async4(t.id + e, a.ids + row * a.k + e);
+    cp_async4(t.p + e, a.t + row * a.k + e);
   }
 }
 
-// kRow threads hold the row, NV vectors each at a time; the last warp looks after the teacher.
+constexpr int kGather = 4;  // student's logits of a lane that are under way at a time
+
+// Ids to -1 where an entry is absent; whether any is left.  The first logits are left in z.
+template <typename T>
+__device__ __forceinline__ bool begin_gather(const DistillArgs<T>& a, long long row, const Entries& t, int lane, T (&z)[kGather]) {
+  bool some = false;
+  const T* src = a.z + row * a.pitch;
+#pragma unroll
+  for (int j = 0; j < kGather; ++j) z[j] = T(0.f);
+  for (int e0 = 0; e0 < a.k; e0 += 32 * kGather) {
+#pragma unroll
+    for (int j = 0; j < kGather; ++j) {
+      const int e = e0 + 32 * j + lane;
+      if (e >= a.k) continue;
+      int id = t.id[e];
+      if (id >= a.vocab) record_error(a.err, kErrValue | kKernDistill);
+      if (id < 0 || id >= a.vocab || t.p[e] == -INFINITY) t.id[e] = id = -1;
+      some |= id >= 0;
+      if (e0 == 0) {
+        if (id >= 0) z[j] = src[id];
+      } else {
+        t.z[e] = id >= 0 ? io<T>::ld(src + id) : 0.f;
+      }
+    }
+  }
+  return __any_sync(0xffffffffu, some);
+}
+template <typename T>
+__device__ __forceinline__ void end_gather(const DistillArgs<T>& a, const Entries& t, int lane, const T (&z)[kGather]) {
+#pragma unroll
+  for (int j = 0; j < kGather; ++j)
+    if (32 * j + lane < a.k) t.z[32 * j + lane] = (float)z[j];
+}
+
+// The probabilities; `seen` holds zeros before and after.
+template <typename T>
+__device__ __forceinline__ void finish_entries(const DistillArgs<T>& a, const Entries& t, unsigned* seen, int lane, bool shares) {
+  float mx = -INFINITY;
+  bool nan = false;
+  for (int e = lane; e < a.k; e += 32) {
+    const float v = t.p[e];
+    if (t.id[e] < 0) continue;
+    mx = fmaxf(mx, v);
+    nan |= v != v;
+  }
+  if (__any_sync(0xffffffffu, nan)) mx = NAN;
+  else mx = warp_max(mx);
+  float s = 0.f;
+  for (int e = lane; e < a.k; e += 32) {
+    const float w = t.id[e] >= 0 ? exp2f((t.p[e] - mx) * a.c) : 0.f;
+    t.p[e] = w;
+    s += w;
+  }
+  const float inv = 1.f / warp_sum(s);
+  for (int e = lane; e < a.k; e += 32) t.share[e] = t.p[e] *= inv;
+  if (!shares) return;
+  // entries that may name a token a second time (or one that differs by a multiple of 32,768) take
+  // the token's entries together under the first of them
+  bool again = false;
+  for (int e0 = 0; e0 < a.k; e0 += 32) {
+    const int id = e0 + lane < a.k ? t.id[e0 + lane] : -1;
+    const unsigned bit = 1u << (id & 31);
+    again |= id >= 0 && (atomicOr(seen + (id >> 5 & (kSeenWords - 1)), bit) & bit);
+  }
+  __syncwarp();
+  for (int e = lane; e < a.k; e += 32)
+    if (t.id[e] >= 0) seen[t.id[e] >> 5 & (kSeenWords - 1)] = 0;
+  __syncwarp();
+  if (!__any_sync(0xffffffffu, again)) return;
+  for (int e = 0; e < a.k; ++e) {
+    const int token = t.id[e];
+    if (token < 0) continue;
+    float sum = t.share[e];
+    bool more = false;
+    for (int i0 = e + 1; i0 < a.k; i0 += 32) {
+      const bool same = i0 + lane < a.k && t.id[i0 + lane] == token;
+      unsigned who = __ballot_sync(0xffffffffu, same);
+      more |= who != 0;
+      for (unsigned w = who; w; w &= w - 1) sum += t.share[i0 + __ffs(w) - 1];
+      if (same) t.id[i0 + lane] = -1;
+    }
+    __syncwarp();
+    if (more && lane == 0) t.share[e] = sum;
+    __syncwarp();
+  }
+}
+
+// kRow threads hold the row, NV vectors each at a time; the next ones are on their way to shared
+// memory meanwhile, each to a slot of the thread that will read it.  The last warp looks after the
+// teacher.
 template <typename T, int kRow, int NV, Mode kMode>
 __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_kernel(const DistillArgs<T> a) {
   constexpr int E = Wide<T>::E, W = kRow / 32;
-  __shared__ Teacher te[2];
-  __shared__ int any[2];
+  extern __shared__ __align__(16) uint4 ahead[];  // [NV][kRow], then the entries of four rows
+  __shared__ int any[4];                          // whether a row has entries: of this row and the next ones
+  __shared__ unsigned seen[kSeenWords];
   __shared__ Running part[2][W];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-  const bool teacher = warp == W;
-
-  // the entries of a row and their probabilities, by the last warp
-  auto prepare = [&](long long row, int side) {
-    Teacher& t = te[side];
-    const T* z = a.z + row * a.pitch;
-    float mx = -INFINITY;
-    bool some = false, nan = false;
-    for (int e = lane; e < a.k; e += 32) {
-      int id = a.ids[row * a.k + e];
-      const float v = a.t[row * a.k + e];
-      if (id >= a.vocab) record_error(a.err, kErrValue | kKernDistill);
-      if (id < 0 || id >= a.vocab || v == -INFINITY) id = -1;
-      t.id[e] = id;
-      t.p[e] = v;
-      t.z[e] = id >= 0 ? io<T>::ld(z + id) : 0.f;
-      some |= id >= 0;
-      if (id >= 0) mx = fmaxf(mx, v);
-      nan |= id >= 0 && v != v;
-    }
-    some = __any_sync(0xffffffffu, some);
-    if (__any_sync(0xffffffffu, nan)) mx = NAN;
-    else mx = warp_max(mx);
-    float s = 0.f;
-    for (int e = lane; e < a.k; e += 32) {
-      const float w = t.id[e] >= 0 ? exp2f((t.p[e] - mx) * a.c) : 0.f;
-      t.p[e] = w;
-      s += w;
-    }
-    const float inv = 1.f / warp_sum(s);
-    for (int e = lane; e < a.k; e += 32) t.p[e] *= inv;
-    if (lane == 0) any[side] = some;
+  float* const words = reinterpret_cast<float*>(ahead + NV * kRow);
+  auto entries = [&](int n) {
+    float* w = words + (n & 3) * 4 * a.k;
+    return Entries{reinterpret_cast<int*>(w), w + a.k, w + 2 * a.k, w + 3 * a.k};
   };
-  // T^2 sum p (ln p - ln q), by the last warp
-  auto loss_of = [&](long long row, int side, Running st, bool some) {
-    const Teacher& t = te[side];
-    const float lse = logf(st.s);
-    float s = 0.f;
-    if (some)
-      for (int e = lane; e < a.k; e += 32) {
-        const float p = t.p[e], z = t.z[e];
-        if (t.id[e] >= 0 && p != 0.f) s += p * (logf(p) - (z == -INFINITY ? z : (z - st.m) / a.temp - lse));
-      }
-    s = warp_sum(s);
-    if (lane == 0) a.loss[row] = a.temp * a.temp * s;
-  };
-
   // all threads meet here; the last warp and the others come from different places
   auto meet = [] { ptx::named_bar_sync(1, kRow + 32); };
+  const long long step = gridDim.x;
+  int n = 0;  // rows so far
 
-  int side = 0;
-  if (teacher) {
-    if (blockIdx.x < a.rows) prepare(blockIdx.x, 0);
+  if (warp == W) {
+    T z[kGather];
+    auto arrived = [] {
+      cp_async_wait();
+      __syncwarp();
+    };
+    for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
+    const long long row0 = blockIdx.x;
+    fetch_entries(a, row0, entries(0), lane);
+    if (row0 + step < a.rows) fetch_entries(a, row0 + step, entries(1), lane);
+    arrived();
+    bool some = begin_gather(a, row0, entries(0), lane, z);
+    end_gather(a, entries(0), lane, z);
+    finish_entries(a, entries(0), seen, lane, kMode != kLoss);
+    bool next = row0 + step < a.rows && begin_gather(a, row0 + step, entries(1), lane, z);
+    if (next) end_gather(a, entries(1), lane, z);
+    if (row0 + 2 * step < a.rows) fetch_entries(a, row0 + 2 * step, entries(2), lane);
+    if (lane == 0) any[0] = some, any[1] = next;
     meet();
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, side ^= 1) {
-      const bool some = any[side], more = row + gridDim.x < a.rows;
+    for (long long row = row0; row < a.rows; row += step, ++n) {
+      arrived();
+      const bool after = row + 2 * step < a.rows && begin_gather(a, row + 2 * step, entries(n + 2), lane, z);
+      if (lane == 0) any[(n + 2) & 3] = after;
+      if (next) finish_entries(a, entries(n + 1), seen, lane, kMode != kLoss);
+      if (after) end_gather(a, entries(n + 2), lane, z);
       Running st{0.f, 0.f};
-      if (kMode == kLoss && more) prepare(row + gridDim.x, side ^ 1);  // (no other warp reads entries)
       if (kMode == kGradAndLoss || (kMode == kLoss && some)) {
-        meet();  // (also in padding: the row before is through with the other buffer)
-        if (some) st = row_total(part[side], a.c);
+        meet();  // (also in padding: the row before is through with its entries)
+        if (some) st = row_total(part[n & 1], a.c);
       }
+      if (row + 3 * step < a.rows) fetch_entries(a, row + 3 * step, entries(n + 3), lane);
       if (lane == 0 && kMode == kLoss && a.stats_out) *reinterpret_cast<float2*>(a.stats_out + 2 * row) = make_float2(st.m, st.s);
-      if (kMode != kGradFromStats && a.loss) loss_of(row, side, st, some);
-      if (kMode != kLoss && more) prepare(row + gridDim.x, side ^ 1);
+      if (kMode != kGradFromStats && a.loss) {
+        const Entries t = entries(n);
+        const float lse = logf(st.s);
+        float s = 0.f;
+        if (some)
+          for (int e = lane; e < a.k; e += 32) {
+            const float p = t.p[e], zt = t.z[e];
+            if (p != 0.f) s += p * (logf(p) - (zt == -INFINITY ? zt : (zt - st.m) / a.temp - lse));
+          }
+        s = warp_sum(s);
+        if (lane == 0) a.loss[row] = a.temp * a.temp * s;
+      }
       if (kMode != kLoss || !some) meet();
-      if (kMode != kLoss && some) fix_entries(a, te[side], row, kMode == kGradFromStats ? kept_stats(a, row) : st, tid, kRow + 32);
       if (kMode == kGradFromStats && some) meet();
+      some = next;
+      next = after;
     }
     return;
   }
 
   const uint64_t cc = ptx::f32x2_pack(a.c, a.c);
+  uint4* const slot = ahead + tid;
+  auto fetch = [&](const T* z, int batch) {
+    const RowSpan r = row_span(z, a.vocab);
+    const uint4* v = reinterpret_cast<const uint4*>(z + r.lead);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (batch * NV + k) * kRow + tid;
+      constexpr unsigned none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+      // -inf elements where there is no vector: they add nothing
+      if (i < r.nvec) cp_async16(slot + k * kRow, v + i);
+      else slot[k * kRow] = make_uint4(none, none, none, none);
+    }
+  };
   meet();
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, side ^= 1) {
+  if (any[0]) fetch(a.z + blockIdx.x * a.pitch, 0);
+  for (long long row = blockIdx.x; row < a.rows; row += step, ++n) {
     const T* z = a.z + row * a.pitch;
     T* dz = a.dz + row * a.grad_pitch;
-    if (!any[side]) {  // padding
+    const bool next = any[(n + 1) & 3];
+    if (!any[n & 3]) {  // padding
+      if (next) fetch(z + step * a.pitch, 0);
       if (kMode == kGradAndLoss) meet();
       if (kMode != kLoss) {
         const RowSpan r = row_span(dz, a.vocab);
@@ -245,24 +352,24 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
       continue;
     }
     const RowSpan r = row_span(z, a.vocab);
-    uint4 u[NV];
     const float edge = tid < r.edge ? io<T>::ld(z + edge_col<T>(r, tid)) : -INFINITY;
-    auto load = [&](int i0) {
+    // batches in order, then back (the last one is still in registers) for the gradient
+    const int batches = max(1, (r.nvec + NV * kRow - 1) / (NV * kRow));
+    const int tiles = kMode == kGradAndLoss ? 2 * batches - 1 : batches;
+    uint4 u[NV];
+    auto take = [&](int tile) {  // this batch into registers, and the next one on its way
+      cp_async_wait();
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int i = i0 + k * kRow + tid;
-        // -inf elements where there is no vector: they add nothing
-        constexpr unsigned none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-        u[k] = i < r.nvec ? reinterpret_cast<const uint4*>(z + r.lead)[i] : make_uint4(none, none, none, none);
-      }
+      for (int k = 0; k < NV; ++k) u[k] = slot[k * kRow];
+      if (tile + 1 < tiles) fetch(z, tile + 1 < batches ? tile + 1 : 2 * batches - 2 - (tile + 1));
+      else if (next) fetch(z + step * a.pitch, 0);
     };
-    const int batches = (r.nvec + NV * kRow - 1) / (NV * kRow);
     Running st{edge, edge == -INFINITY ? 0.f : edge - edge + 1.f};  // (NaN stays NaN)
     if constexpr (kMode == kGradFromStats) {
       st = kept_stats(a, row);
     } else {
       for (int b = 0; b < batches; ++b) {
-        load(b * NV * kRow);
+        take(b);
         float m = Wide<T>::largest(u[0]);
 #pragma unroll
         for (int k = 1; k < NV; ++k) m = fmaxf(m, Wide<T>::largest(u[k]));
@@ -291,21 +398,21 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
       // over the warp: its largest value, then its threads' sums
       const float m = warp_max(st.m);
       st.s = warp_sum(st.m == -INFINITY ? st.s : st.s * ptx::ex2_approx((st.m - m) * a.c));
-      if (lane == 0) part[side][warp] = Running{m, st.s};
+      if (lane == 0) part[n & 1][warp] = Running{m, st.s};
       meet();
       if (kMode == kLoss) continue;
-      st = row_total(part[side], a.c);
+      st = row_total(part[n & 1], a.c);
     }
     if constexpr (kMode != kLoss) {
-      const float g = a.dloss[row] * a.temp * inverse(st.s);
+      const float f = a.dloss[row] * a.temp, g = f * inverse(st.s);
       uint4* o = reinterpret_cast<uint4*>(dz + r.lead);
       const uint64_t neg = ptx::f32x2_pack(-st.m, -st.m), gg = ptx::f32x2_pack(g, g);
-      // the batch that is still in registers first
-      for (int b = batches - 1; b >= 0; --b) {
-        if (kMode == kGradFromStats || b < batches - 1) load(b * NV * kRow);
+      for (int tile = kMode == kGradAndLoss ? batches - 1 : 0; tile < tiles; ++tile) {
+        if (kMode == kGradFromStats || tile >= batches) take(tile);
+        const int b = tile < batches ? tile : 2 * batches - 2 - tile;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int i = b * NV * kRow + k * kRow + tid;
+          const int i = (b * NV + k) * kRow + tid;
           uint64_t p[E / 2];
           float q[E];
           Wide<T>::pairs(u[k], p);
@@ -320,13 +427,19 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
       }
       if (tid < r.edge) io<T>::st(dz + edge_col<T>(r, tid), ptx::ex2_approx((edge - st.m) * a.c) * g);
       meet();
-      fix_entries(a, te[side], row, st, tid, kRow + 32);
+      fix_entries(a, entries(n), dz, f, st, tid, kRow);
       if (kMode == kGradFromStats) meet();  // before the entries' buffer is written again
     }
   }
 }
 
 // ------------------------------------------------------------------- element by element
+
+struct Teacher {
+  int id[TG_MAX_TEACHER];    // -1: absent
+  float p[TG_MAX_TEACHER];   // the logit first, then e^{(t - max) / T}, then the probability
+  float z[TG_MAX_TEACHER];   // the student's logit there
+};
 
 // Over the block, for every thread; the barrier at the end frees buf again.
 __device__ __forceinline__ float block_sum(float v, float* buf) {
@@ -429,7 +542,19 @@ __global__ void __launch_bounds__(kThreads) distill_backward_kernel(const Distil
     const float g = a.dloss[row] * a.temp * inverse(st.y);
     for (int j = threadIdx.x; j < a.vocab; j += kThreads) io<T>::st(dz + j, exp2f((io<T>::ld(z + j) - st.x) * a.c) * g);
     __syncthreads();
-    fix_entries(a, te, row, Running{st.x, st.y}, threadIdx.x, kThreads);
+    const float f = a.dloss[row] * a.temp, inv = inverse(st.y);
+    for (int e = threadIdx.x; e < a.k; e += kThreads) {
+      const int id = te.id[e];
+      if (id < 0) continue;
+      float p = 0.f;
+      bool first = true;  // each token by its first entry
+      for (int i = 0; i < a.k; ++i)
+        if (te.id[i] == id) {
+          first &= i >= e;
+          p += te.p[i];
+        }
+      if (first) io<T>::st(dz + id, f * (exp2f((te.z[e] - st.x) * a.c) * inv - p));
+    }
     __syncthreads();
   }
 }
@@ -458,14 +583,21 @@ bool same_alignment(const DistillArgs<T>& a) {
                    (a.pitch - a.grad_pitch) % E == 0);
 }
 
+template <typename T, int kRow, Mode kMode>
+cudaError_t rows_of(const DistillArgs<T>& a, int per_sm, cudaStream_t s) {
+  const auto kernel = distill_row_kernel<T, kRow, 8, kMode>;
+  const int smem = 8 * kRow * 16 + 4 * 4 * a.k * 4;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             8 * kRow * 16 + 4 * 4 * TG_MAX_TEACHER * 4);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid_of(a.rows, per_sm), kRow + 32, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 // Blocks of 512 threads and a warp, two per SM, or of 128 for rows of up to 1,024 vectors.
 template <typename T, Mode kMode>
 cudaError_t rows_t(const DistillArgs<T>& a, cudaStream_t s) {
-  if (a.vocab <= 1024 * Wide<T>::E)
-    distill_row_kernel<T, 128, 8, kMode><<<grid_of(a.rows, 6), 160, 0, s>>>(a);
-  else
-    distill_row_kernel<T, 512, 8, kMode><<<grid_of(a.rows, 2), 544, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.vocab <= 1024 * Wide<T>::E ? rows_of<T, 128, kMode>(a, 6, s) : rows_of<T, 512, kMode>(a, 2, s);
 }
 
 template <typename T>

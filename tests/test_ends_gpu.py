@@ -327,6 +327,29 @@ def test_distill(lib, rows, V, K, dt, T):
     no_error()
 
 
+@pytest.mark.parametrize("rows,V,K", [(4001, 203, 12), (1500, 9000, 40), (1001, 40009, 5)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_distill_many_rows(lib, rows, V, K, dt):
+    """Several rows for every block, with padding in runs and alone, repeated and absent entries."""
+    gen = generator(rows)
+    z, t, ids = distill_inputs(gen, rows, V, K, dt)
+    some = torch.randint(0, K, (rows, 3), generator=gen, device="cuda")
+    ids.scatter_(1, some, ids.gather(1, some.flip(1)))                   # repeated tokens
+    ids[torch.rand(rows, K, generator=gen, device="cuda") < 0.1] = -1
+    ids[torch.rand(rows, generator=gen, device="cuda") < 0.3] = -1       # padding
+    ids[rows // 3: rows // 3 + 900] = -1
+    dloss, loss, stats = normal(gen, rows), torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+    tg.tango_distill(z, t, ids, loss, temperature=1.5, stats=stats)
+    check_distill(z, t, ids, 1.5, None, loss, None)
+    dz, one = torch.full_like(z, math.nan), torch.full_like(z, math.nan)
+    tg.tango_distill_backward(z, t, ids, dloss, dz, temperature=1.5, stats=stats)
+    check_distill(z, t, ids, 1.5, dloss, None, dz)
+    both = torch.empty_like(loss)
+    tg.tango_distill_backward(z, t, ids, dloss, one, temperature=1.5, loss=both)
+    check_distill(z, t, ids, 1.5, dloss, both, one)
+    no_error()
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_distill_pitches(lib, dt):
     """Rows of a padded vocabulary, aligned or not: what lies between them is neither read nor written."""
