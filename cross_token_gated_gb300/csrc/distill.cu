@@ -107,6 +107,9 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The row's, from its warps' by a whole warp; the largest value as 0 where there is none above -inf.
@@ -130,7 +133,9 @@ __device__ __forceinline__ Running kept_stats(const DistillArgs<T>& a, long long
 }
 __device__ __forceinline__ float inverse(float s) { return s == 0.f ? 0.f : 1.f / s; }
 
-// A row's entries (dynamic shared memory, k of each; four rows in turn).
+constexpr int kSlots = 8;  // rows whose entries are held
+
+// A row's entries (dynamic shared memory, k of each).
 struct Entries {
   int* id;      // -1: absent, or another entry stands for the token
   float* p;     // probability
@@ -250,16 +255,16 @@ __device__ __forceinline__ void finish_entries(const DistillArgs<T>& a, const En
 // memory meanwhile, each to a slot of the thread that will read it.  The last warp looks after the
 // teacher.
 template <typename T, int kRow, int NV, Mode kMode>
-__global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_kernel(const DistillArgs<T> a) {
+__global__ void __launch_bounds__(kRow + 32, kRow == 512 ? 2 : kRow == 256 ? 4 : 6) distill_row_kernel(const DistillArgs<T> a) {
   constexpr int E = Wide<T>::E, W = kRow / 32;
-  extern __shared__ __align__(16) uint4 ahead[];  // [NV][kRow], then the entries of four rows
-  __shared__ int any[4];                          // whether a row has entries: of this row and the next ones
+  extern __shared__ __align__(16) uint4 ahead[];  // [NV][kRow], then the entries of kSlots rows
+  __shared__ int any[kSlots];                     // whether a row has entries: of this row and the next ones
   __shared__ unsigned seen[kSeenWords];
   __shared__ Running part[2][W];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   float* const words = reinterpret_cast<float*>(ahead + NV * kRow);
   auto entries = [&](int n) {
-    float* w = words + (n & 3) * 4 * a.k;
+    float* w = words + (n & (kSlots - 1)) * 4 * a.k;
     return Entries{reinterpret_cast<int*>(w), w + a.k, w + 2 * a.k, w + 3 * a.k};
   };
   // all threads meet here; the last warp and the others come from different places
@@ -268,42 +273,46 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
   int n = 0;  // rows so far
 
   if (warp == W) {
-    T z[kGather];
-    auto arrived = [] {
-      cp_async_wait();
-      __syncwarp();
-    };
-    for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
+    // of row n: the loss; of n + 1: the probabilities; of n + 2: logits arrive; of n + 3: they are
+    // asked for; of n + 5: ids and the teacher's logits are asked for
     const long long row0 = blockIdx.x;
-    fetch_entries(a, row0, entries(0), lane);
-    if (row0 + step < a.rows) fetch_entries(a, row0 + step, entries(1), lane);
-    arrived();
-    bool some = begin_gather(a, row0, entries(0), lane, z);
-    end_gather(a, entries(0), lane, z);
-    finish_entries(a, entries(0), seen, lane, kMode != kLoss);
-    bool next = row0 + step < a.rows && begin_gather(a, row0 + step, entries(1), lane, z);
-    if (next) end_gather(a, entries(1), lane, z);
-    if (row0 + 2 * step < a.rows) fetch_entries(a, row0 + 2 * step, entries(2), lane);
-    if (lane == 0) any[0] = some, any[1] = next;
+    const int rows = (int)((a.rows - row0 + step - 1) / step);  // of this block
+    T z[kGather];
+    bool live[4];  // of rows n .. n + 3, as any
+    for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
+    for (int i = 0; i < 5 && i < rows; ++i) fetch_entries(a, row0 + i * step, entries(i), lane);
+    cp_async_wait();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      live[i] = i < rows && begin_gather(a, row0 + i * step, entries(i), lane, z);
+      if (live[i]) end_gather(a, entries(i), lane, z);
+      if (lane == 0) any[i] = live[i];
+    }
+    if (live[0]) finish_entries(a, entries(0), seen, lane, kMode != kLoss);
+    live[3] = false;
     meet();
-    for (long long row = row0; row < a.rows; row += step, ++n) {
-      arrived();
-      const bool after = row + 2 * step < a.rows && begin_gather(a, row + 2 * step, entries(n + 2), lane, z);
-      if (lane == 0) any[(n + 2) & 3] = after;
-      if (next) finish_entries(a, entries(n + 1), seen, lane, kMode != kLoss);
-      if (after) end_gather(a, entries(n + 2), lane, z);
+    for (; n < rows; ++n) {
+      const long long row = row0 + n * step;
+      cp_async_wait_but<1>();
+      __syncwarp();
+      if (n > 0 && live[2]) end_gather(a, entries(n + 2), lane, z);
+      live[3] = n + 3 < rows && begin_gather(a, row + 3 * step, entries(n + 3), lane, z);
+      if (lane == 0) any[(n + 3) & (kSlots - 1)] = live[3];
+      if (n + 5 < rows) fetch_entries(a, row + 5 * step, entries(n + 5), lane);
+      cp_async_commit();
+      if (live[1]) finish_entries(a, entries(n + 1), seen, lane, kMode != kLoss);
       Running st{0.f, 0.f};
-      if (kMode == kGradAndLoss || (kMode == kLoss && some)) {
-        meet();  // (also in padding: the row before is through with its entries)
-        if (some) st = row_total(part[n & 1], a.c);
+      if (kMode == kGradAndLoss || (kMode == kLoss && live[0])) {
+        meet();  // (also in padding: one step for all)
+        if (live[0]) st = row_total(part[n & 1], a.c);
       }
-      if (row + 3 * step < a.rows) fetch_entries(a, row + 3 * step, entries(n + 3), lane);
       if (lane == 0 && kMode == kLoss && a.stats_out) *reinterpret_cast<float2*>(a.stats_out + 2 * row) = make_float2(st.m, st.s);
       if (kMode != kGradFromStats && a.loss) {
         const Entries t = entries(n);
         const float lse = logf(st.s);
         float s = 0.f;
-        if (some)
+        if (live[0])
           for (int e = lane; e < a.k; e += 32) {
             const float p = t.p[e], zt = t.z[e];
             if (p != 0.f) s += p * (logf(p) - (zt == -INFINITY ? zt : (zt - st.m) / a.temp - lse));
@@ -311,10 +320,10 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
         s = warp_sum(s);
         if (lane == 0) a.loss[row] = a.temp * a.temp * s;
       }
-      if (kMode != kLoss || !some) meet();
-      if (kMode == kGradFromStats && some) meet();
-      some = next;
-      next = after;
+      if (kMode != kLoss || !live[0]) meet();
+      live[0] = live[1];
+      live[1] = live[2];
+      live[2] = live[3];
     }
     return;
   }
@@ -324,6 +333,12 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
   auto fetch = [&](const T* z, int batch) {
     const RowSpan r = row_span(z, a.vocab);
     const uint4* v = reinterpret_cast<const uint4*>(z + r.lead);
+    if ((batch + 1) * NV * kRow <= r.nvec) {
+      v += batch * NV * kRow + tid;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) cp_async16(slot + k * kRow, v + k * kRow);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = (batch * NV + k) * kRow + tid;
@@ -338,8 +353,8 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
   for (long long row = blockIdx.x; row < a.rows; row += step, ++n) {
     const T* z = a.z + row * a.pitch;
     T* dz = a.dz + row * a.grad_pitch;
-    const bool next = any[(n + 1) & 3];
-    if (!any[n & 3]) {  // padding
+    const bool next = any[(n + 1) & (kSlots - 1)];
+    if (!any[n & (kSlots - 1)]) {  // padding
       if (next) fetch(z + step * a.pitch, 0);
       if (kMode == kGradAndLoss) meet();
       if (kMode != kLoss) {
@@ -428,7 +443,6 @@ __global__ void __launch_bounds__(kRow + 32, 1088 / (kRow + 32)) distill_row_ker
       if (tid < r.edge) io<T>::st(dz + edge_col<T>(r, tid), ptx::ex2_approx((edge - st.m) * a.c) * g);
       meet();
       fix_entries(a, entries(n), dz, f, st, tid, kRow);
-      if (kMode == kGradFromStats) meet();  // before the entries' buffer is written again
     }
   }
 }
@@ -586,9 +600,9 @@ bool same_alignment(const DistillArgs<T>& a) {
 template <typename T, int kRow, Mode kMode>
 cudaError_t rows_of(const DistillArgs<T>& a, int per_sm, cudaStream_t s) {
   const auto kernel = distill_row_kernel<T, kRow, 8, kMode>;
-  const int smem = 8 * kRow * 16 + 4 * 4 * a.k * 4;
+  const int smem = 8 * kRow * 16 + kSlots * 4 * a.k * 4;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             8 * kRow * 16 + 4 * 4 * TG_MAX_TEACHER * 4);
+                                             8 * kRow * 16 + kSlots * 4 * TG_MAX_TEACHER * 4);
   if (e != cudaSuccess) return e;
   kernel<<<grid_of(a.rows, per_sm), kRow + 32, smem, s>>>(a);
   return cudaGetLastError();
@@ -597,7 +611,8 @@ cudaError_t rows_of(const DistillArgs<T>& a, int per_sm, cudaStream_t s) {
 // Blocks of 512 threads and a warp, two per SM, or of 128 for rows of up to 1,024 vectors.
 template <typename T, Mode kMode>
 cudaError_t rows_t(const DistillArgs<T>& a, cudaStream_t s) {
-  return a.vocab <= 1024 * Wide<T>::E ? rows_of<T, 128, kMode>(a, 6, s) : rows_of<T, 512, kMode>(a, 2, s);
+  if (a.vocab <= 1024 * Wide<T>::E) return rows_of<T, 128, kMode>(a, 6, s);
+  return kMode == kLoss ? rows_of<T, 256, kMode>(a, 4, s) : rows_of<T, 512, kMode>(a, 2, s);
 }
 
 template <typename T>
