@@ -13,6 +13,7 @@
 #include "tg_common.cuh"
 #include "tg_ends.h"
 #include "tg_exp2_table.cuh"
+#include "tg_ptx.cuh"
 #include "tg_serve.h"
 
 namespace tg {
@@ -95,13 +96,20 @@ __device__ __forceinline__ float value_of(unsigned key) {
 
 // --------------------------------------------------------------------------- reductions
 
+constexpr int kBins = 2 * kThreads, kList = 1024, kSpans = kThreads;
+
 struct Shared {
   Exp2Entry tab[256];
-  uint64_t mass[kThreads];
-  int ties[kThreads];
+  uint64_t mass[kSpans];     // kept mass of the row's spans
+  unsigned bins[kBins];
+  unsigned key[kList];       // the logits of the bins that hold a border
+  unsigned idx[kList];
+  uint64_t w[kList];
+  int listed;
   uint64_t buf[kWarps];
-  unsigned ubuf[kWarps];
-  int seg, tie_before;
+  unsigned ubuf[2][kWarps];
+  float fbuf[kWarps];
+  int first, last;
   uint64_t rest;
 };
 
@@ -109,6 +117,7 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
+// Over the block, for every thread; the barrier at the end frees the buffer again.
 __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
   v = warp_sum64(v);
   if ((threadIdx.x & 31) == 0) sh.buf[threadIdx.x / 32] = v;
@@ -117,35 +126,145 @@ __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
   __syncthreads();
   return v;
 }
-__device__ __forceinline__ unsigned block_max(unsigned v, Shared& sh) {
-  v = __reduce_max_sync(kFull, v);
-  if ((threadIdx.x & 31) == 0) sh.ubuf[threadIdx.x / 32] = v;
+__device__ __forceinline__ uint64_t block_min64(uint64_t v, Shared& sh) {
+  auto least = [](uint64_t x) {
+    for (int o = 16; o > 0; o >>= 1) x = min(x, (uint64_t)__shfl_xor_sync(kFull, x, o));
+    return x;
+  };
+  v = least(v);
+  if ((threadIdx.x & 31) == 0) sh.buf[threadIdx.x / 32] = v;
   __syncthreads();
-  v = __reduce_max_sync(kFull, sh.ubuf[threadIdx.x & 31]);
+  v = least(sh.buf[threadIdx.x & 31]);
   __syncthreads();
   return v;
 }
-// Sum over the threads before this one.
-__device__ __forceinline__ uint64_t block_before(uint64_t v, Shared& sh, uint64_t* total) {
+__device__ __forceinline__ unsigned block_max(unsigned v, Shared& sh) {
+  v = __reduce_max_sync(kFull, v);
+  if ((threadIdx.x & 31) == 0) sh.ubuf[0][threadIdx.x / 32] = v;
+  __syncthreads();
+  v = __reduce_max_sync(kFull, sh.ubuf[0][threadIdx.x & 31]);
+  __syncthreads();
+  return v;
+}
+// Sum over the threads before this one, and over all.
+template <typename N>
+__device__ __forceinline__ N block_before(N v, N* buf, N* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  uint64_t incl = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t up = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) sh.buf[warp] = incl;
+  auto scan = [lane](N x) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const N up = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += up;
+    }
+    return x;
+  };
+  const N incl = scan(v);
+  if (lane == 31) buf[warp] = incl;
   __syncthreads();
-  uint64_t before = 0, all = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sh.buf[w];
-    all += sh.buf[w];
-  }
+  const N warps = scan(buf[lane]);
+  const N before = __shfl_sync(kFull, warps, (warp + 31) & 31);
+  *total = __shfl_sync(kFull, warps, 31);
   __syncthreads();
-  *total = all;
-  return before + incl - v;
+  return (warp ? before : N(0)) + incl - v;
 }
 
-// ------------------------------------------------------------------------------- kernel
+// --------------------------------------------------------------------------------- row
+
+// What is kept of the row's order: larger keys, and of the equal ones those up to an index.
+struct Cut {
+  unsigned key, last;
+  __device__ __forceinline__ bool keeps(unsigned k, unsigned i) const { return k > key || (k == key && i <= last); }
+};
+
+template <typename T> struct Wide;
+template <> struct Wide<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+};
+template <> struct Wide<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
+    f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
+    f[4] = ptx::bf16lo(u.z); f[5] = ptx::bf16hi(u.z); f[6] = ptx::bf16lo(u.w); f[7] = ptx::bf16hi(u.w);
+  }
+};
+
+// The row as 16-byte vectors, with the elements before the first and after the last one by
+// themselves; it is read again in every pass, from L1 or L2.  32 vectors that a warp reads at once
+// are a span; `wide` doublings of that keep their number within kSpans.
+template <typename T>
+struct Row {
+  static constexpr int E = Wide<T>::E;
+  const T* x;
+  int V, lead, nvec, edge, wide;
+  __device__ __forceinline__ Row(const T* row, int vocab) : x(row), V(vocab) {
+    lead = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
+    nvec = (vocab - lead) / E;
+    edge = vocab - nvec * E;
+    wide = 0;
+    while ((nvec >> 5 >> wide) >= kSpans) ++wide;
+  }
+  static __device__ __forceinline__ float clean(float v) { return v == v ? v + 0.f : -INFINITY; }  // NaN as -inf, -0 as 0
+  __device__ __forceinline__ float at(int i) const { return clean(io<T>::ld(x + i)); }
+  __device__ __forceinline__ int span_of(int i) const { return i < lead ? 0 : min(nvec > 0 ? (nvec - 1) >> 5 >> wide : 0, (i - lead) / E >> 5 >> wide); }
+  // elements of a span
+  __device__ __forceinline__ int2 span(int s) const {
+    const int per = (32 << wide) * E, n = nvec > 0 ? ((nvec - 1) >> 5 >> wide) + 1 : 1;
+    return make_int2(s == 0 ? 0 : lead + s * per, s == n - 1 ? V : lead + (s + 1) * per);
+  }
+  // f(value, index) for the thread's elements
+  template <int U, typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int tid = threadIdx.x;
+    if (tid < edge) {  // (fewer than 16)
+      const int i = tid < lead ? tid : tid + nvec * E;
+      f(at(i), i);
+    }
+    const uint4* v = reinterpret_cast<const uint4*>(x + lead);
+#pragma unroll 1
+    for (int b = tid; b < nvec; b += U * kThreads) {
+      uint4 u[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (b + k * kThreads < nvec) u[k] = __ldg(v + b + k * kThreads);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (b + k * kThreads >= nvec) break;
+        float e[E];
+        Wide<T>::unpack(u[k], e);
+#pragma unroll
+        for (int j = 0; j < E; ++j) f(clean(e[j]), lead + (b + k * kThreads) * E + j);
+      }
+    }
+  }
+  // Adds f(value, index) up in mass[span], which holds zeros.
+  template <typename F>
+  __device__ __forceinline__ void sum_spans(uint64_t* mass, F f) const {
+    using u64 = unsigned long long;
+    const int tid = threadIdx.x;
+    if (tid < edge) {
+      const int i = tid < lead ? tid : tid + nvec * E;
+      const uint64_t w = f(at(i), i);
+      if (w) atomicAdd((u64*)mass + span_of(i), (u64)w);
+    }
+    const uint4* v = reinterpret_cast<const uint4*>(x + lead);
+#pragma unroll 1
+    for (int b = tid & ~31; b < nvec; b += kThreads) {
+      const int i = b + (tid & 31);
+      uint64_t w = 0;
+      if (i < nvec) {
+        float e[E];
+        Wide<T>::unpack(__ldg(v + i), e);
+#pragma unroll
+        for (int j = 0; j < E; ++j) w += f(clean(e[j]), lead + i * E + j);
+      }
+      if (!__any_sync(kFull, w != 0)) continue;
+      w = warp_sum64(w);
+      if ((tid & 31) == 0) atomicAdd((u64*)mass + (b >> 5 >> wide), (u64)w);
+    }
+  }
+};
 
 struct Settings {
   float temp, top_p, min_p, u;
@@ -168,134 +287,277 @@ __device__ Settings settings_of(const SampleCall& c, int row) {
 // u in [0, 1) as a fraction of 2^64.
 __device__ __forceinline__ uint64_t fraction(float u) { return (uint64_t)(u * 18446744073709551616.f); }
 
-// One block per row.
+// Bins of a row: equal steps of the logits from the largest one down to 2^-40 of its weight, or to
+// the lowest logit.
+struct Bins {
+  float mx, per_unit, log2_step;
+  __device__ __forceinline__ Bins(float mx_, float low, float temp, Scale sc) : mx(mx_) {
+    // 27.8 > 40 ln 2; logits that differ by less than 1e-30 may share a bin
+    const float reach = fmaxf(fminf(27.8f * temp, __fsub_rn(mx, low)), 1e-30f);
+    per_unit = __fdiv_rn(kBins - 0.01f, reach);
+    log2_step = sc.hi / per_unit;
+  }
+  // the bin of a logit and the place in it; >= kBins, or NaN, outside
+  __device__ __forceinline__ float place(float x) const { return x == mx ? 0.f : __fmul_rn(__fsub_rn(mx, x), per_unit); }
+};
+
+// Exact borders by bisection, for rows whose listed bins hold too many logits.  A cut from a key and the
+// number of logits equal to it that are kept (at least one).
+template <typename T>
+__device__ __noinline__ Cut cut_from(const Row<T>& row, unsigned key, uint64_t equal, Shared& sh) {
+  sh.mass[threadIdx.x] = 0;
+  __syncthreads();
+  row.sum_spans(sh.mass, [&](float x, int) { return (uint64_t)(key_of(x) == key); });
+  __syncthreads();
+  uint64_t total;
+  const uint64_t mine = sh.mass[threadIdx.x], before = block_before(mine, sh.buf, &total);
+  if (equal >= total) return Cut{key, kFull};
+  if (before < equal && equal <= before + mine) {  // walk through the span
+    const int2 at = row.span(threadIdx.x);
+    uint64_t n = before;
+    for (int i = at.x; i < at.y; ++i) {
+      n += key_of(row.at(i)) == key;
+      if (n == equal) {
+        sh.last = i;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  const unsigned last = sh.last;
+  __syncthreads();
+  return Cut{key, last};
+}
+template <typename T>
+__device__ __noinline__ Cut bisect_count(const Row<T>& row, unsigned lo, unsigned hi, uint64_t k, Shared& sh) {
+  auto count = [&](unsigned key) {  // logits of at least this key
+    uint64_t n = 0;
+    row.template each<1>([&](float x, int) { n += key_of(x) >= key; });
+    return block_sum64(n, sh);
+  };
+  while (lo < hi) {  // the largest key that at least k logits reach
+    const unsigned mid = lo + (hi - lo + 1) / 2;
+    if (count(mid) >= k) lo = mid;
+    else hi = mid - 1;
+  }
+  return cut_from(row, lo, k - (lo < kFull ? count(lo + 1) : 0), sh);
+}
+template <typename T>
+__device__ __noinline__ Cut bisect_mass(const Row<T>& row, unsigned lo, unsigned hi, Cut within, uint64_t need, float mx,
+                                        Scale sc, Shared& sh) {
+  auto above = [&](unsigned key) {  // mass of the larger keys
+    uint64_t g = 0;
+    row.template each<1>([&](float x, int i) {
+      const unsigned k = key_of(x);
+      if (k > key && within.keeps(k, i)) g += weight(x, mx, sc, sh.tab);
+    });
+    return block_sum64(g, sh);
+  };
+  while (lo < hi) {  // the smallest key above which there is less than what is needed
+    const unsigned mid = lo + (hi - lo) / 2;
+    if (above(mid) < need) hi = mid;
+    else lo = mid + 1;
+  }
+  const uint64_t w = weight(value_of(lo), mx, sc, sh.tab);
+  if (w == 0) return Cut{lo, kFull};  // all of the mass is needed
+  const Cut cut = cut_from(row, lo, (need - above(lo) + w - 1) / w, sh);
+  return lo == within.key && within.last < cut.last ? within : cut;
+}
+
+// One block per row.  A border (of the k-th logit, or of the share of the mass) is found with a
+// histogram of counts, or of masses good to about 1e-5; only the logits of the bins that may hold it
+// are listed and compared one by one, in exact sums.  Should there be too many of them, the
+// border is bisected.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c) {
+  using u64 = unsigned long long;
   __shared__ Shared sh;
-  const int row = blockIdx.x, V = c.p.vocab, tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-  const T* x = static_cast<const T*>(c.logits) + (long long)row * c.p.pitch;
-  // NaN as -inf, -0 as 0
-  auto at = [&](int i) {
-    const float v = io<T>::ld(x + i);
-    return v == v ? v + 0.f : -INFINITY;
-  };
-  const Settings s = settings_of(c, row);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  const long long r = blockIdx.x;
+  const Row<T> row(static_cast<const T*>(c.logits) + r * c.p.pitch, c.p.vocab);
+  const Settings s = settings_of(c, (int)r);
+  unsigned top = 0, low = kFull;
+  row.template each<4>([&](float x, int) {
+    const unsigned k = key_of(x);
+    top = max(top, k);
+    low = min(low, k);
+  });
   load_exp2(sh.tab);
-  unsigned top = 0;
-  for (int i = tid; i < V; i += kThreads) top = max(top, key_of(at(i)));
-  top = block_max(top, sh);
+  sh.mass[tid] = 0;
+  top = __reduce_max_sync(kFull, top);
+  low = __reduce_min_sync(kFull, low);
+  if (lane == 0) sh.ubuf[0][warp] = top, sh.ubuf[1][warp] = low;
+  __syncthreads();
+  top = __reduce_max_sync(kFull, sh.ubuf[0][lane]);
+  low = __reduce_min_sync(kFull, sh.ubuf[1][lane]);
+  __syncthreads();
   const float mx = value_of(top);
   if (mx == -INFINITY || s.temp == 0.f) {
     unsigned first = 0;
-    for (int i = tid; i < V; i += kThreads)
-      if (at(i) == mx) first = max(first, kFull - (unsigned)i);
+    row.template each<2>([&](float x, int i) {
+      if (x == mx) first = max(first, kFull - (unsigned)i);
+    });
     first = kFull - block_max(first, sh);
     if (tid == 0) {
-      c.token[row] = mx == -INFINITY ? -1 : (int)first;
-      if (c.logprob) c.logprob[row] = mx == -INFINITY ? mx : 0.f;
+      c.token[r] = mx == -INFINITY ? -1 : (int)first;
+      if (c.logprob) c.logprob[r] = mx == -INFINITY ? mx : 0.f;
     }
     return;
   }
   const Scale sc = scale_of(s.temp);
-
-  // the cut: logits with a larger key are kept, and the first `ties` of those that equal it
-  unsigned cut = 0;
-  uint64_t ties = ~0ull;
-  if (s.top_k > 0 && s.top_k < V) {  // the largest key that at least top_k logits reach
-    unsigned lo = 0, hi = top;
-    while (lo < hi) {
-      const unsigned mid = lo + (hi - lo + 1) / 2;
-      unsigned n = 0;
-      for (int i = tid; i < V; i += kThreads) n += key_of(at(i)) >= mid;
-      if (block_sum64(n, sh) >= (uint64_t)s.top_k) lo = mid;
-      else hi = mid - 1;
-    }
-    cut = lo;
-    unsigned n = 0;
-    for (int i = tid; i < V; i += kThreads) n += key_of(at(i)) > cut;
-    ties = s.top_k - block_sum64(n, sh);
-  }
-  auto above = [&](unsigned key) {  // mass of the logits above a key
-    uint64_t g = 0;
-    for (int i = tid; i < V; i += kThreads) {
-      const float v = at(i);
-      if (key_of(v) > key) g += weight(v, mx, sc, sh.tab);
-    }
-    return block_sum64(g, sh);
-  };
-  if (s.top_p < 1.f) {  // the smallest key above which there is less than the share
-    const uint64_t w_cut = cut ? weight(value_of(cut), mx, sc, sh.tab) : 0;
-    const uint64_t mass = above(cut) + (w_cut ? ties * w_cut : 0);
-    const uint64_t f = fraction(s.top_p > 0.f ? s.top_p : 0.f), hi_part = __umul64hi(f, mass);
-    uint64_t need = hi_part + (f * mass != 0);
-    need = need ? need : 1;
-    unsigned lo = cut, hi = top;
-    while (lo < hi) {
-      const unsigned mid = lo + (hi - lo) / 2;
-      if (above(mid) < need) hi = mid;
-      else lo = mid + 1;
-    }
-    const uint64_t w = lo ? weight(value_of(lo), mx, sc, sh.tab) : 0, g = above(lo);
-    if (w) {
-      const uint64_t n = (need - g + w - 1) / w;
-      ties = lo > cut || n < ties ? n : ties;
-    }
-    cut = lo;
-  }
+  const Bins bins(mx, value_of(low), s.temp, sc);
   const uint64_t least = s.min_p > 0.f ? (uint64_t)ceilf(s.min_p * 17592186044416.f) : 0;  // 2^44
-  const uint64_t w_cut = cut ? weight(value_of(cut), mx, sc, sh.tab) : 0;
-  const bool cut_lives = w_cut && w_cut >= least;
+  auto clear_bins = [&] {
+    sh.bins[tid] = sh.bins[tid + kThreads] = 0;
+    if (tid == 0) sh.listed = 0;
+    __syncthreads();
+  };
+  auto list = [&](unsigned key, int i, uint64_t w) {
+    const int n = atomicAdd(&sh.listed, 1);
+    if (n < kList) {
+      sh.key[n] = key;
+      sh.idx[n] = i;
+      sh.w[n] = w;
+    }
+  };
+  // entries come in the row's order by key, falling, then by index; as one number that falls
+  auto order_of = [&](int j) { return (uint64_t)sh.key[j] << 32 | (kFull - sh.idx[j]); };
+  auto cut_at = [&](uint64_t order) { return Cut{(unsigned)(order >> 32), kFull - (unsigned)order}; };
 
-  // mass and ties of up to kThreads equal spans of the row, then of the span that holds the token
-  int span = 256;
-  while ((V + span - 1) / span > kThreads) span *= 2;
-  const int spans = (V + span - 1) / span;
-  for (int g = warp; g < kThreads; g += kWarps) {
-    uint64_t m = 0;
-    unsigned n = 0;
-    const int i1 = g < spans ? min(V, (g + 1) * span) : 0;
-    for (int i = g * span + lane; i < i1; i += 32) {
-      const float v = at(i);
-      const unsigned key = key_of(v);
-      if (key > cut) {
-        const uint64_t w = weight(v, mx, sc, sh.tab);
-        if (w >= least) m += w;
+  Cut cut{0, kFull};
+  if (s.top_k > 0 && s.top_k < row.V) {
+    const unsigned k = s.top_k;
+    clear_bins();
+    row.template each<2>([&](float x, int) {
+      const float y = bins.place(x);
+      if (y < (float)kBins) atomicAdd(sh.bins + (int)y, 1u);
+    });
+    __syncthreads();
+    const unsigned c0 = sh.bins[2 * tid], c1 = sh.bins[2 * tid + 1];
+    unsigned total;
+    const unsigned before = block_before(c0 + c1, sh.ubuf[0], &total);
+    if (total > k) {  // (else the k-th has less than 2^-40)
+      if (before < k && k <= before + c0) sh.first = 2 * tid, sh.last = before;
+      else if (before + c0 < k && k <= before + c0 + c1) sh.first = 2 * tid + 1, sh.last = before + c0;
+      __syncthreads();
+      const int bin = sh.first;
+      const unsigned above = sh.last;
+      if (sh.bins[bin] <= kList) {
+        row.template each<2>([&](float x, int i) {
+          const float y = bins.place(x);
+          if (y < (float)kBins && (int)y == bin) list(key_of(x), i, 0);
+        });
+        __syncthreads();
+        const int n = sh.listed;
+        uint64_t last = ~0ull;
+        if (tid < n) {
+          const uint64_t mine = order_of(tid);
+          unsigned rank = above;
+          for (int j = 0; j < n; ++j) rank += order_of(j) > mine;
+          if (rank < k) last = mine;
+        }
+        cut = cut_at(block_min64(last, sh));
+      } else {
+        cut = bisect_count(row, low, top, k, sh);
+        __syncthreads();
+        sh.mass[tid] = 0;
+        __syncthreads();
       }
-      n += key == cut;
     }
-    m = warp_sum64(m);
-    n = __reduce_add_sync(kFull, n);
-    if (lane == 0) {
-      sh.mass[g] = m;
-      sh.ties[g] = n;
+  }
+
+  if (s.top_p < 1.f) {
+    clear_bins();
+    constexpr float unit = 262144.f;  // 2^18: a bin's masses in units of 2^-18 of its largest weight
+    row.template each<2>([&](float x, int i) {
+      const float y = bins.place(x);
+      if (y < (float)kBins && cut.keeps(key_of(x), i)) {
+        const int b = (int)y;
+        atomicAdd(sh.bins + b, (unsigned)(ptx::ex2_approx(((float)b - y) * bins.log2_step) * unit));
+      }
+    });
+    __syncthreads();
+    const float m0 = (float)sh.bins[2 * tid] * ptx::ex2_approx((float)(-2 * tid) * bins.log2_step);
+    const float m1 = (float)sh.bins[2 * tid + 1] * ptx::ex2_approx((float)(-2 * tid - 1) * bins.log2_step);
+    float all;
+    const float before = block_before(m0 + m1, sh.fbuf, &all);
+    const float share = s.top_p > 0.f ? s.top_p : 0.f, from = share * all * (1.f - 3e-5f), to = share * all * (1.f + 3e-5f);
+    const unsigned b0 = 2 * tid, none = kBins - 1;
+    const unsigned f = __reduce_min_sync(kFull, before + m0 >= from ? b0 : before + m0 + m1 >= from ? b0 + 1 : none);
+    const unsigned t = __reduce_min_sync(kFull, before + m0 >= to ? b0 : before + m0 + m1 >= to ? b0 + 1 : none);
+    if (lane == 0) sh.ubuf[0][warp] = f, sh.ubuf[1][warp] = t;
+    __syncthreads();
+    const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane]), last = __reduce_min_sync(kFull, sh.ubuf[1][lane]);
+    // exact sums of everything and of the bins before; the bins between are listed
+    uint64_t mass = 0, sure = 0;
+    row.sum_spans(sh.mass, [&](float x, int i) -> uint64_t {
+      const float y = bins.place(x);
+      const unsigned key = key_of(x);
+      if (!(y < (float)kBins) || !cut.keeps(key, i)) return 0;
+      const uint64_t w = weight(x, mx, sc, sh.tab);
+      mass += w;
+      if ((int)y >= first) {
+        if ((int)y <= last && w) list(key, i, w);
+        return 0;
+      }
+      sure += w;
+      return w >= least ? w : 0;
+    });
+    mass = block_sum64(mass, sh);
+    sure = block_sum64(sure, sh);
+    const uint64_t p = fraction(share);
+    uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
+    if (need == 0) need = 1;
+    const int n = sh.listed;
+    const uint64_t listed = block_sum64(tid < n && n <= kList ? sh.w[tid] : 0, sh);
+    if (n <= kList && sure < need && sure + listed >= need) {
+      uint64_t order = ~0ull;
+      if (tid < n) {
+        const uint64_t mine = order_of(tid);
+        uint64_t g = sure;
+        for (int j = 0; j < n; ++j) g += order_of(j) > mine ? sh.w[j] : 0;
+        if (g < need) {
+          order = mine;
+          if (sh.w[tid] >= least) atomicAdd((u64*)sh.mass + row.span_of(sh.idx[tid]), (u64)sh.w[tid]);
+        }
+      }
+      cut = cut_at(block_min64(order, sh));
+    } else {
+      cut = bisect_mass(row, max(low, cut.key), top, cut, need, mx, sc, sh);
+      __syncthreads();
+      sh.mass[tid] = 0;
+      __syncthreads();
+      row.sum_spans(sh.mass, [&](float x, int i) {
+        const uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
+        return w >= least ? w : 0;
+      });
     }
+  } else {
+    row.sum_spans(sh.mass, [&](float x, int i) {
+      const uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
+      return w >= least ? w : 0;
+    });
   }
   __syncthreads();
+
+  // the span that holds the token, then the token
   uint64_t total;
-  const uint64_t tie_before = block_before(sh.ties[tid], sh, &total);
-  const uint64_t tie_left = tie_before < ties ? ties - tie_before : 0;
-  const uint64_t n = tie_left < (uint64_t)sh.ties[tid] ? tie_left : sh.ties[tid];
-  const uint64_t mine = sh.mass[tid] + (cut_lives ? n * w_cut : 0);
-  const uint64_t before = block_before(mine, sh, &total);
+  const uint64_t mine = sh.mass[tid], before = block_before(mine, sh.buf, &total);
   const uint64_t target = __umul64hi(fraction(s.u), total);  // the token is the first to pass it
   if (before <= target && target < before + mine) {
-    sh.seg = tid;
+    sh.first = tid;
     sh.rest = target - before;
-    sh.tie_before = (int)(tie_before < ties ? tie_before : ties);
   }
   __syncthreads();
   if (warp != 0) return;
   uint64_t rest = sh.rest;
-  uint64_t tb = sh.tie_before;
-  const int i1 = min(V, (sh.seg + 1) * span);
-  for (int i0 = sh.seg * span; i0 < i1; i0 += 32) {
-    const float v = i0 + lane < i1 ? at(i0 + lane) : -INFINITY;
-    const unsigned key = key_of(v);
-    const bool tie = key == cut && i0 + lane < i1;
-    const unsigned tie_mask = __ballot_sync(kFull, tie);
-    uint64_t w = key > cut || (tie && tb + __popc(tie_mask & ((1u << lane) - 1)) < ties) ? weight(v, mx, sc, sh.tab) : 0;
+  const int2 span = row.span(sh.first);
+  for (int i0 = span.x; i0 < span.y; i0 += 32) {
+    const int i = i0 + lane;
+    const float x = i < span.y ? row.at(i) : -INFINITY;
+    uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
     if (w < least) w = 0;
-    tb += __popc(tie_mask);
+    if (!__any_sync(kFull, w != 0)) continue;
     uint64_t incl = w;
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t up = __shfl_up_sync(kFull, incl, o);
@@ -304,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     const unsigned hit = __ballot_sync(kFull, incl > rest);
     if (hit) {
       if (lane == __ffs(hit) - 1) {
-        c.token[row] = i0 + lane;
-        if (c.logprob) c.logprob[row] = w == total ? 0.f : logf((float)w / (float)total);
+        c.token[r] = i;
+        if (c.logprob) c.logprob[r] = w == total ? 0.f : logf((float)w / (float)total);
       }
       return;
     }
