@@ -5,8 +5,8 @@
 //   dn = gamma dy,  dx = r (dn - n <dn n> - <dn>) + dres,  dgamma = sum dy n,  dbeta = sum dy
 //
 // Means are over the row, <dn> only with mu.  All of it is bound by HBM bandwidth: each value is
-// read and written once.  A row stays in the registers of its group of threads (8 lanes, a warp, or
-// 128 or 512 threads, by the row's length), as the 16-byte vectors that were loaded, and the next
+// read and written once.  A row stays in the registers of its group of threads (8 lanes to 512
+// threads, by the row's length), as the 16-byte vectors that were loaded, and the next
 // row is on its way meanwhile.  The gradient needs two joins a row: sum x, then sum (x - mu)^2,
 // sum dn and sum dn (x - mu) at once (rms: one).  A thread keeps its columns' dgamma and dbeta in
 // registers over all rows of its persistent block.
@@ -139,13 +139,18 @@ template <> struct Wide<__nv_bfloat16> {
   static __device__ __forceinline__ float inv_sqrt(float v) { return rsqrtf(v); }  // 2 units: far below a bf16 rounding
 };
 
-template <int kGroup> constexpr int kBlock = kGroup > 256 ? kGroup : 256;
+// Threads of a block: as many warps an SM as the registers of NV vectors a thread leave.
+template <int kGroup, int NV> constexpr int kBlock = kGroup >= 256 ? kGroup : NV <= 2 ? 384 : 256;
+
+// Blocks of the persistent grids per SM.
+template <int kGroup, int NV> constexpr int kForwardPerSm = kGroup > 256 ? 2 : kGroup < 256 && NV <= 2 ? 3 : 4;
+template <int kGroup, int NV> constexpr int kBackwardPerSm = kGroup > 256 ? 1 : kGroup == 256 && NV <= 2 ? 3 : 2;
 
 // Sums over the group of K values at a time; every thread gets them.  Groups of several warps join
 // through shared memory, in two buffers taken in turn (all groups of a block make the same calls).
-template <int kGroup, int K>
+template <int kGroup, int K, int kWarpsOfBlock>
 struct GroupSum {
-  float (*buf)[K][kBlock<kGroup> / 32];
+  float (*buf)[K][kWarpsOfBlock];
   int side = 0;
   __device__ __forceinline__ void operator()(float (&v)[K]) {
     constexpr int W = kGroup / 32;
@@ -180,19 +185,33 @@ __device__ __forceinline__ void load_row(uint4 (&u)[NV], const void* row, int la
   }
 }
 
+// gamma and beta (or ones and zeros) as vectors in shared memory: kept in registers they would cost
+// more warps an SM than their reading costs time.
+template <typename T>
+__device__ __forceinline__ void stage_vector(uint4* dst, const T* src, float otherwise, int nvec) {
+  float f[Wide<T>::E];
+#pragma unroll
+  for (int e = 0; e < Wide<T>::E; ++e) f[e] = otherwise;
+  const uint4 none = Wide<T>::pack(f);
+  for (int i = threadIdx.x; i < nvec; i += blockDim.x) dst[i] = src ? reinterpret_cast<const uint4*>(src)[i] : none;
+}
+
 template <typename T, int kGroup, int NV>
-__global__ void __launch_bounds__(kBlock<kGroup>) norm_kernel(const NormArgs<T> a) {
-  constexpr int E = Wide<T>::E, kRows = kBlock<kGroup> / kGroup;
-  __shared__ float buf[2][1][kBlock<kGroup> / 32];
-  GroupSum<kGroup, 1> sum{buf};
+__global__ void __launch_bounds__(kBlock<kGroup, NV>, kForwardPerSm<kGroup, NV>) norm_kernel(const NormArgs<T> a) {
+  constexpr int E = Wide<T>::E, B = kBlock<kGroup, NV>, kRows = B / kGroup;
+  extern __shared__ __align__(16) uint4 weights[];  // [2][nvec]: gamma, beta
+  __shared__ float buf[2][1][B / 32];
+  GroupSum<kGroup, 1, B / 32> sum{buf};
   const int lane = threadIdx.x % kGroup, nvec = a.d / E;
   const float inv_d = 1.f / (float)a.d;
-  uint4 g[NV], b[NV], u[NV];
-  load_row<kGroup>(g, a.gamma, lane, nvec, a.gamma != nullptr);
-  load_row<kGroup>(b, a.beta, lane, nvec, a.beta != nullptr);
+  stage_vector(weights, a.gamma, 1.f, nvec);
+  stage_vector(weights + nvec, a.beta, 0.f, nvec);
+  const uint32_t g = ptx::smem_u32(weights);
+  uint4 u[NV];
   const long long step = (long long)gridDim.x * kRows;
   long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup, row0 = (long long)blockIdx.x * kRows;
   load_row<kGroup>(u, a.x + row * a.x_pitch, lane, nvec, row < a.rows);
+  __syncthreads();
   for (; row0 < a.rows; row0 += step, row += step) {
     uint4 next[NV];
     load_row<kGroup>(next, a.x + (row + step) * a.x_pitch, lane, nvec, row + step < a.rows);
@@ -226,10 +245,10 @@ __global__ void __launch_bounds__(kBlock<kGroup>) norm_kernel(const NormArgs<T> 
       if (row >= a.rows || i >= nvec) continue;
       float f[E], gf[E], bf[E];
       Wide<T>::unpack(u[k], f);
-      Wide<T>::unpack(g[k], gf);
-      Wide<T>::unpack(b[k], bf);
+      Wide<T>::unpack(ptx::ld_shared_v4(g + i * 16), gf);
+      Wide<T>::unpack(ptx::ld_shared_v4(g + (nvec + i) * 16), bf);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mu) * r, a.gamma ? gf[e] : 1.f, bf[e]);
+      for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mu) * r, gf[e], bf[e]);
       reinterpret_cast<uint4*>(a.y + row * a.d)[i] = Wide<T>::pack(f);
     }
 #pragma unroll
@@ -240,7 +259,7 @@ __global__ void __launch_bounds__(kBlock<kGroup>) norm_kernel(const NormArgs<T> 
 // The block's sums of dgamma or dbeta, of its groups in order, into its row of part.
 template <int kGroup, int NV, int E>
 __device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float* sh, float* dst, int d) {
-  constexpr int kRows = kBlock<kGroup> / kGroup;
+  constexpr int B = kBlock<kGroup, NV>, kRows = B / kGroup;
   const int lane = threadIdx.x % kGroup, nvec = d / E;
   float* mine = kRows > 1 ? sh + (threadIdx.x / kGroup) * d : dst;
 #pragma unroll
@@ -253,7 +272,7 @@ __device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float*
   }
   if constexpr (kRows > 1) {
     __syncthreads();
-    for (int c = threadIdx.x; c < d; c += kBlock<kGroup>) {
+    for (int c = threadIdx.x; c < d; c += B) {
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < kRows; ++w) s += sh[w * d + c];
@@ -263,22 +282,25 @@ __device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float*
   }
 }
 
-template <typename T, int kGroup, int NV>
-__global__ void __launch_bounds__(kBlock<kGroup>) norm_backward_kernel(const NormArgs<T> a) {
-  constexpr int E = Wide<T>::E, kRows = kBlock<kGroup> / kGroup;
-  extern __shared__ float columns[];  // [kRows][d], where kRows > 1
-  __shared__ float buf1[2][1][kBlock<kGroup> / 32], buf3[2][3][kBlock<kGroup> / 32];
-  GroupSum<kGroup, 1> sum1{buf1};
-  GroupSum<kGroup, 3> sum3{buf3};
+template <typename T, int kGroup, int NV, bool kBeta>
+__global__ void __launch_bounds__(kBlock<kGroup, NV>, kBackwardPerSm<kGroup, NV>) norm_backward_kernel(const NormArgs<T> a) {
+  constexpr int E = Wide<T>::E, B = kBlock<kGroup, NV>, kRows = B / kGroup;
+  extern __shared__ __align__(16) uint4 weights[];  // gamma [nvec], then float [kRows][d], where kRows > 1
+  __shared__ float buf1[2][1][B / 32], buf3[2][3][B / 32];
+  GroupSum<kGroup, 1, B / 32> sum1{buf1};
+  GroupSum<kGroup, 3, B / 32> sum3{buf3};
   const int lane = threadIdx.x % kGroup, nvec = a.d / E;
   const float inv_d = 1.f / (float)a.d;
-  uint4 g[NV], x[NV], y[NV];
-  float dg[NV * E] = {}, db[NV * E] = {};
-  load_row<kGroup>(g, a.gamma, lane, nvec, a.gamma != nullptr);
+  stage_vector(weights, a.gamma, 1.f, nvec);
+  const uint32_t g = ptx::smem_u32(weights);
+  float* columns = reinterpret_cast<float*>(weights + nvec);
+  uint4 x[NV], y[NV];
+  float dg[NV * E] = {}, db[kBeta ? NV * E : 1] = {};
   const long long step = (long long)gridDim.x * kRows;
   long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup, row0 = (long long)blockIdx.x * kRows;
   load_row<kGroup>(x, a.x + row * a.x_pitch, lane, nvec, row < a.rows);
   load_row<kGroup>(y, a.dy + row * a.d, lane, nvec, row < a.rows);
+  __syncthreads();
   for (; row0 < a.rows; row0 += step, row += step) {
     uint4 res[NV], next_x[NV], next_y[NV];
     const bool live = row < a.rows, more = row + step < a.rows;
@@ -305,10 +327,10 @@ __global__ void __launch_bounds__(kBlock<kGroup>) norm_backward_kernel(const Nor
       float f[E], h[E], gf[E];
       Wide<T>::unpack(x[k], f);
       Wide<T>::unpack(y[k], h);
-      Wide<T>::unpack(g[k], gf);
+      Wide<T>::unpack(ptx::ld_shared_v4(g + (k * kGroup + lane) * 16), gf);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float c = f[e] - mu, dn = a.gamma ? h[e] * gf[e] : h[e];
+        const float c = f[e] - mu, dn = h[e] * gf[e];
         s[0] = fmaf(c, c, s[0]);
         s[1] = fmaf(dn, c, s[1]);
         s[2] += dn;
@@ -324,13 +346,13 @@ __global__ void __launch_bounds__(kBlock<kGroup>) norm_backward_kernel(const Nor
       float f[E], h[E], gf[E], rf[E];
       Wide<T>::unpack(x[k], f);
       Wide<T>::unpack(y[k], h);
-      Wide<T>::unpack(g[k], gf);
+      Wide<T>::unpack(ptx::ld_shared_v4(g + i * 16), gf);
       Wide<T>::unpack(res[k], rf);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float n = (f[e] - mu) * r, dn = a.gamma ? h[e] * gf[e] : h[e];
+        const float n = (f[e] - mu) * r, dn = h[e] * gf[e];
         dg[k * E + e] = fmaf(h[e], n, dg[k * E + e]);
-        db[k * E + e] += h[e];
+        if constexpr (kBeta) db[k * E + e] += h[e];
         f[e] = fmaf(r, dn - fmaf(n, m1, m0), rf[e]);
       }
       reinterpret_cast<uint4*>(a.dx + row * a.d)[i] = Wide<T>::pack(f);
@@ -343,7 +365,7 @@ __global__ void __launch_bounds__(kBlock<kGroup>) norm_backward_kernel(const Nor
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.want_gamma) block_columns<kGroup, NV, E>(dg, columns, a.part + (size_t)blockIdx.x * a.d, a.d);
-  if (a.want_beta) block_columns<kGroup, NV, E>(db, columns, a.part + ((size_t)gridDim.x + blockIdx.x) * a.d, a.d);
+  if constexpr (kBeta) block_columns<kGroup, NV, E>(db, columns, a.part + ((size_t)gridDim.x + blockIdx.x) * a.d, a.d);
 }
 
 // dgamma (blockIdx.y 0) and dbeta (1): 32 columns a block, each by 32 threads that take every 32nd
@@ -397,8 +419,8 @@ bool in_registers(const NormArgs<T>& a) {
   return a.d % E == 0 && a.x_pitch % E == 0 && a.d / E <= 2048;
 }
 
-// Calls f with the group and the vectors of a thread for a row of nvec: 8 lanes up to 16 vectors, a
-// warp up to 128, 128 threads up to 512, else 512 (a thread holds at most 4).
+// Calls f with the group and the vectors of a thread for a row of nvec: as few threads as hold it in
+// 2 or 3 vectors each, so that rows enough are under way (5,003 fp32 rows of 768: 64 threads with 3).
 template <typename F>
 auto by_length(int nvec, F f) {
   using std::integral_constant;
@@ -408,10 +430,14 @@ auto by_length(int nvec, F f) {
   if (nvec <= 32) return TG_CASE(32, 1);
   if (nvec <= 64) return TG_CASE(32, 2);
   if (nvec <= 96) return TG_CASE(32, 3);
-  if (nvec <= 128) return TG_CASE(32, 4);
+  if (nvec <= 128) return TG_CASE(64, 2);
+  if (nvec <= 192) return TG_CASE(64, 3);
   if (nvec <= 256) return TG_CASE(128, 2);
-  if (nvec <= 512) return TG_CASE(128, 4);
+  if (nvec <= 384) return TG_CASE(128, 3);
+  if (nvec <= 512) return TG_CASE(256, 2);
+  if (nvec <= 768) return TG_CASE(256, 3);
   if (nvec <= 1024) return TG_CASE(512, 2);
+  if (nvec <= 1536) return TG_CASE(512, 3);
   return TG_CASE(512, 4);
 #undef TG_CASE
 }
@@ -421,8 +447,13 @@ cudaError_t norm_t(const NormCall& c, cudaStream_t s) {
   const NormArgs<T> a = norm_args<T>(c);
   if (in_registers(a))
     return by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
-      constexpr int G = decltype(group)::value, B = kBlock<G>;
-      norm_kernel<T, G, decltype(nv)::value><<<grid_of((c.rows + B / G - 1) / (B / G), 1024 / B), B, 0, s>>>(a);
+      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G, N>, R = B / G;
+      const int smem = 2 * c.d * (int)sizeof(T), per_sm = kForwardPerSm<G, N>;
+      if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(norm_kernel<T, G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+      }
+      norm_kernel<T, G, N><<<grid_of((c.rows + R - 1) / R, per_sm), B, smem, s>>>(a);
       return cudaGetLastError();
     });
   norm_any_kernel<T><<<grid_of(c.rows, 8), kThreads, 0, s>>>(a);
@@ -436,9 +467,15 @@ cudaError_t norm_backward_t(const NormCall& c, cudaStream_t s) {
   cudaError_t e;
   if (in_registers(a)) {
     e = by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
-      constexpr int G = decltype(group)::value, B = kBlock<G>, R = B / G;
-      grid = grid_of((c.rows + R - 1) / R, G > 256 ? 1 : 2);
-      norm_backward_kernel<T, G, decltype(nv)::value><<<grid, B, R > 1 ? R * c.d * sizeof(float) : 0, s>>>(a);
+      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G, N>, R = B / G;
+      const auto kernel = c.dbeta ? norm_backward_kernel<T, G, N, true> : norm_backward_kernel<T, G, N, false>;
+      const int smem = c.d * (int)sizeof(T) + (R > 1 ? R * c.d * 4 : 0);
+      if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (err != cudaSuccess) return err;
+      }
+      grid = grid_of((c.rows + R - 1) / R, kBackwardPerSm<G, N>);
+      kernel<<<grid, B, smem, s>>>(a);
       return cudaGetLastError();
     });
   } else {
