@@ -139,12 +139,12 @@ template <> struct Wide<__nv_bfloat16> {
   static __device__ __forceinline__ float inv_sqrt(float v) { return rsqrtf(v); }  // 2 units: far below a bf16 rounding
 };
 
-// Threads of a block: as many warps an SM as the registers of NV vectors a thread leave.
-template <int kGroup, int NV> constexpr int kBlock = kGroup >= 256 ? kGroup : NV <= 2 ? 384 : 256;
+template <int kGroup> constexpr int kBlock = kGroup > 256 ? kGroup : 256;
 
 // Blocks of the persistent grids per SM.
-template <int kGroup, int NV> constexpr int kForwardPerSm = kGroup > 256 ? 2 : kGroup < 256 && NV <= 2 ? 3 : 4;
-template <int kGroup, int NV> constexpr int kBackwardPerSm = kGroup > 256 ? 1 : kGroup == 256 && NV <= 2 ? 3 : 2;
+template <int kGroup> constexpr int kForwardPerSm = kGroup > 256 ? 2 : 4;
+// (gradients of 16,384 x 512 from L2: 2 blocks of 256 threads 14.6 us, 3 of them, or 2 of 384, 18.6 us)
+template <int kGroup> constexpr int kBackwardPerSm = kGroup > 256 ? 1 : 2;
 
 // Sums over the group of K values at a time; every thread gets them.  Groups of several warps join
 // through shared memory, in two buffers taken in turn (all groups of a block make the same calls).
@@ -197,8 +197,8 @@ __device__ __forceinline__ void stage_vector(uint4* dst, const T* src, float oth
 }
 
 template <typename T, int kGroup, int NV>
-__global__ void __launch_bounds__(kBlock<kGroup, NV>, kForwardPerSm<kGroup, NV>) norm_kernel(const NormArgs<T> a) {
-  constexpr int E = Wide<T>::E, B = kBlock<kGroup, NV>, kRows = B / kGroup;
+__global__ void __launch_bounds__(kBlock<kGroup>, kForwardPerSm<kGroup>) norm_kernel(const NormArgs<T> a) {
+  constexpr int E = Wide<T>::E, B = kBlock<kGroup>, kRows = B / kGroup;
   extern __shared__ __align__(16) uint4 weights[];  // [2][nvec]: gamma, beta
   __shared__ float buf[2][1][B / 32];
   GroupSum<kGroup, 1, B / 32> sum{buf};
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kBlock<kGroup, NV>, kForwardPerSm<kGroup, NV>)
 // The block's sums of dgamma or dbeta, of its groups in order, into its row of part.
 template <int kGroup, int NV, int E>
 __device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float* sh, float* dst, int d) {
-  constexpr int B = kBlock<kGroup, NV>, kRows = B / kGroup;
+  constexpr int B = kBlock<kGroup>, kRows = B / kGroup;
   const int lane = threadIdx.x % kGroup, nvec = d / E;
   float* mine = kRows > 1 ? sh + (threadIdx.x / kGroup) * d : dst;
 #pragma unroll
@@ -283,8 +283,8 @@ __device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float*
 }
 
 template <typename T, int kGroup, int NV, bool kBeta>
-__global__ void __launch_bounds__(kBlock<kGroup, NV>, kBackwardPerSm<kGroup, NV>) norm_backward_kernel(const NormArgs<T> a) {
-  constexpr int E = Wide<T>::E, B = kBlock<kGroup, NV>, kRows = B / kGroup;
+__global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_backward_kernel(const NormArgs<T> a) {
+  constexpr int E = Wide<T>::E, B = kBlock<kGroup>, kRows = B / kGroup;
   extern __shared__ __align__(16) uint4 weights[];  // gamma [nvec], then float [kRows][d], where kRows > 1
   __shared__ float buf1[2][1][B / 32], buf3[2][3][B / 32];
   GroupSum<kGroup, 1, B / 32> sum1{buf1};
@@ -447,8 +447,8 @@ cudaError_t norm_t(const NormCall& c, cudaStream_t s) {
   const NormArgs<T> a = norm_args<T>(c);
   if (in_registers(a))
     return by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
-      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G, N>, R = B / G;
-      const int smem = 2 * c.d * (int)sizeof(T), per_sm = kForwardPerSm<G, N>;
+      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G>, R = B / G;
+      const int smem = 2 * c.d * (int)sizeof(T), per_sm = kForwardPerSm<G>;
       if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(norm_kernel<T, G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -467,14 +467,14 @@ cudaError_t norm_backward_t(const NormCall& c, cudaStream_t s) {
   cudaError_t e;
   if (in_registers(a)) {
     e = by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
-      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G, N>, R = B / G;
+      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G>, R = B / G;
       const auto kernel = c.dbeta ? norm_backward_kernel<T, G, N, true> : norm_backward_kernel<T, G, N, false>;
       const int smem = c.d * (int)sizeof(T) + (R > 1 ? R * c.d * 4 : 0);
       if (smem > 48 * 1024) {
         const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
       }
-      grid = grid_of((c.rows + R - 1) / R, kBackwardPerSm<G, N>);
+      grid = grid_of((c.rows + R - 1) / R, kBackwardPerSm<G>);
       kernel<<<grid, B, smem, s>>>(a);
       return cudaGetLastError();
     });
