@@ -48,27 +48,23 @@ __device__ __forceinline__ Scale scale_of(float temp) {
   return Scale{hi, (fmaf(-hi, temp, lh) + ll) / temp};
 }
 
-// e^{(x - max) / T} in units of 2^-44, 0 where it is less than 2^-40.  y = (x - max) log2(e) / T
-// is carried as a sum of two floats; 2^y = 2^k 2^(i/256) (1 + t + t^2/2 + ...), |t| < 2^-9.5, whose
-// terms up to t^4 reach 2^-44.  Sums and products are rounded one by one (none may be fused).
+// e^{(x - max) / T} in units of 2^-44, 0 where it is less than 2^-40 (and for NaN); max is finite.
+// y = (x - max) log2(e) / T is carried as a sum of two floats; 2^y = 2^k 2^(i/256) (1 + t + t^2/2 + ...),
+// |t| < 2^-9.5, whose terms up to t^4 reach 2^-44.  Sums and products are rounded one by one (none
+// may be fused).
 __device__ __forceinline__ uint64_t weight(float x, float mx, Scale c, const Exp2Entry* tab) {
-  if (x == mx) return 1ull << kUnit;
   const float d = __fsub_rn(x, mx), back = __fsub_rn(d, x);
   const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(mx, back));
-  float yh = __fmul_rn(d, c.hi);
-  if (!(yh > -41.f)) return 0;  // -inf and NaN too
-  float yl = __fadd_rn(__fmaf_rn(d, c.hi, -yh), __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi)));
-  const float y = __fadd_rn(yh, yl);
-  yl = __fsub_rn(yl, __fsub_rn(y, yh));
-  yh = y;
-  if (yh < -40.f || (yh == -40.f && yl < 0.f)) return 0;
+  const float yh = __fmul_rn(d, c.hi);
+  const float yl = __fadd_rn(__fmaf_rn(d, c.hi, -yh), __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi)));
+  if (!(__fadd_rn(yh, yl) >= -40.f)) return 0;
   const float m = __fmaf_rn(yh, 256.f, 12582912.f);  // 1.5 2^23: the sum's low bits are the nearest integer
   const int n = __float_as_int(m) - 0x4b400000;
   const float r0 = __fmaf_rn(__fsub_rn(m, 12582912.f), -0.00390625f, yh), r = __fadd_rn(r0, yl);
-  yl = __fsub_rn(yl, __fsub_rn(r, r0));
+  const float rl = __fsub_rn(yl, __fsub_rn(r, r0));
   constexpr float l2h = 0.693147182464599609375f, l2l = -1.9046542121259336e-09f;  // ln 2
   const float th = __fmul_rn(r, l2h);
-  const float tl = __fadd_rn(__fmaf_rn(r, l2h, -th), __fmaf_rn(r, l2l, __fmul_rn(yl, l2h)));
+  const float tl = __fadd_rn(__fmaf_rn(r, l2h, -th), __fmaf_rn(r, l2l, __fmul_rn(rl, l2h)));
   const float q = __fmul_rn(__fmul_rn(th, th), __fmaf_rn(th, __fmaf_rn(th, 1.f / 24, 1.f / 6), 0.5f));
   const Exp2Entry e = tab[n & 255];
   const float p = __fmul_rn(e.hi, th);
@@ -80,14 +76,14 @@ __device__ __forceinline__ uint64_t weight(float x, float mx, Scale c, const Exp
   const int i1 = __float_as_int(s1) - __float_as_int(c1);
   const float rest = __fadd_rn(__fsub_rn(p, __fsub_rn(s1, c1)), low);
   const int i2 = __float_as_int(__fadd_rn(rest, c2)) - __float_as_int(c2);
-  const uint64_t w = e.t + (int64_t)i1 * 65536 + (int64_t)i2 * 32;
+  const uint64_t w = e.t + (int64_t)i1 * 65536 + (int64_t)(i2 * 32);
   const int s = 46 - kUnit - (n >> 8);  // 2..42
   return (w + (1ull << (s - 1))) >> s;
 }
 
 // Order of the logits as unsigned integers.
 __device__ __forceinline__ unsigned key_of(float x) {
-  const unsigned b = __float_as_uint(x);
+  const unsigned b = __float_as_uint(__fadd_rn(x, 0.f));  // (-0 as 0)
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(unsigned key) {
@@ -175,11 +171,18 @@ struct Cut {
   __device__ __forceinline__ bool keeps(unsigned k, unsigned i) const { return k > key || (k == key && i <= last); }
 };
 
-template <typename T> struct Wide;
+template <typename T> struct Wide;  // 16 bytes of T
 template <> struct Wide<float> {
   static constexpr int E = 4;
   static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
     f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  // largest and lowest of all so far, NaN left out
+  static __device__ __forceinline__ void range(const uint4& u, float& top, float& low) {
+    float f[4];
+    unpack(u, f);
+    top = fmaxf(fmaxf(top, fmaxf(f[0], f[1])), fmaxf(f[2], f[3]));
+    low = fminf(fminf(low, fminf(f[0], f[1])), fminf(f[2], f[3]));
   }
 };
 template <> struct Wide<__nv_bfloat16> {
@@ -187,6 +190,13 @@ template <> struct Wide<__nv_bfloat16> {
   static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
     f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
     f[4] = ptx::bf16lo(u.z); f[5] = ptx::bf16hi(u.z); f[6] = ptx::bf16lo(u.w); f[7] = ptx::bf16hi(u.w);
+  }
+  static __device__ __forceinline__ __nv_bfloat162 two(unsigned x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
+  static __device__ __forceinline__ void range(const uint4& u, float& top, float& low) {
+    const __nv_bfloat162 a = two(u.x), b = two(u.y), c = two(u.z), d = two(u.w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(a, b), __hmax2(c, d)), n = __hmin2(__hmin2(a, b), __hmin2(c, d));
+    top = fmaxf(top, fmaxf(__low2float(m), __high2float(m)));
+    low = fminf(low, fminf(__low2float(n), __high2float(n)));
   }
 };
 
@@ -205,13 +215,25 @@ struct Row {
     wide = 0;
     while ((nvec >> 5 >> wide) >= kSpans) ++wide;
   }
-  static __device__ __forceinline__ float clean(float v) { return v == v ? v + 0.f : -INFINITY; }  // NaN as -inf, -0 as 0
-  __device__ __forceinline__ float at(int i) const { return clean(io<T>::ld(x + i)); }
+  __device__ __forceinline__ float at(int i) const { return io<T>::ld(x + i); }
   __device__ __forceinline__ int span_of(int i) const { return i < lead ? 0 : min(nvec > 0 ? (nvec - 1) >> 5 >> wide : 0, (i - lead) / E >> 5 >> wide); }
   // elements of a span
   __device__ __forceinline__ int2 span(int s) const {
     const int per = (32 << wide) * E, n = nvec > 0 ? ((nvec - 1) >> 5 >> wide) + 1 : 1;
     return make_int2(s == 0 ? 0 : lead + s * per, s == n - 1 ? V : lead + (s + 1) * per);
+  }
+  // largest and lowest logit of the thread's, NaN left out
+  __device__ __forceinline__ float2 range() const {
+    float top = -INFINITY, low = INFINITY;
+    if ((int)threadIdx.x < edge) {
+      const float v = at((int)threadIdx.x < lead ? threadIdx.x : threadIdx.x + nvec * E);
+      top = fmaxf(top, v);
+      low = fminf(low, v);
+    }
+    const uint4* v = reinterpret_cast<const uint4*>(x + lead);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nvec; i += kThreads) Wide<T>::range(__ldg(v + i), top, low);
+    return make_float2(top, low);
   }
   // f(value, index) for the thread's elements
   template <int U, typename F>
@@ -234,7 +256,7 @@ struct Row {
         float e[E];
         Wide<T>::unpack(u[k], e);
 #pragma unroll
-        for (int j = 0; j < E; ++j) f(clean(e[j]), lead + (b + k * kThreads) * E + j);
+        for (int j = 0; j < E; ++j) f(e[j], lead + (b + k * kThreads) * E + j);
       }
     }
   }
@@ -257,7 +279,7 @@ struct Row {
         float e[E];
         Wide<T>::unpack(__ldg(v + i), e);
 #pragma unroll
-        for (int j = 0; j < E; ++j) w += f(clean(e[j]), lead + i * E + j);
+        for (int j = 0; j < E; ++j) w += f(e[j], lead + i * E + j);
       }
       if (!__any_sync(kFull, w != 0)) continue;
       w = warp_sum64(w);
@@ -294,45 +316,52 @@ struct Bins {
   __device__ __forceinline__ Bins(float mx_, float low, float temp, Scale sc) : mx(mx_) {
     // 27.8 > 40 ln 2; logits that differ by less than 1e-30 may share a bin
     const float reach = fmaxf(fminf(27.8f * temp, __fsub_rn(mx, low)), 1e-30f);
-    per_unit = __fdiv_rn(kBins - 0.01f, reach);
+    per_unit = __fdiv_rn(kBins - 1, reach);
     log2_step = sc.hi / per_unit;
   }
-  // the bin of a logit and the place in it; >= kBins, or NaN, outside
-  __device__ __forceinline__ float place(float x) const { return x == mx ? 0.f : __fmul_rn(__fsub_rn(mx, x), per_unit); }
+  // distance from the largest in bins; outside where it is not below kBins - 0.5 (NaN too)
+  __device__ __forceinline__ float place(float x) const { return __fmul_rn(__fsub_rn(mx, x), per_unit); }
+  static __device__ __forceinline__ bool inside(float y) { return y < kBins - 0.5f; }
+  // the nearest bin as 1.5 2^23 + bin: its low bits are the number
+  static __device__ __forceinline__ float bin(float y) { return __fadd_rn(y, 12582912.f); }
+  static __device__ __forceinline__ int number(float b) { return __float_as_int(b) - 0x4b400000; }
 };
 
-// Exact borders by bisection, for rows whose listed bins hold too many logits.  A cut from a key and the
-// number of logits equal to it that are kept (at least one).
+// The index of the m-th logit (from 1) that equals a key, or of the last one where
+// there are fewer.  Overwrites sh.mass.
 template <typename T>
-__device__ __noinline__ Cut cut_from(const Row<T>& row, unsigned key, uint64_t equal, Shared& sh) {
+__device__ __noinline__ unsigned nth_equal(const Row<T>& row, unsigned key, uint64_t m, Shared& sh) {
   sh.mass[threadIdx.x] = 0;
   __syncthreads();
   row.sum_spans(sh.mass, [&](float x, int) { return (uint64_t)(key_of(x) == key); });
   __syncthreads();
   uint64_t total;
   const uint64_t mine = sh.mass[threadIdx.x], before = block_before(mine, sh.buf, &total);
-  if (equal >= total) return Cut{key, kFull};
-  if (before < equal && equal <= before + mine) {  // walk through the span
+  if (m > total) m = total;
+  if (before < m && m <= before + mine) {  // walk through the span
     const int2 at = row.span(threadIdx.x);
     uint64_t n = before;
-    for (int i = at.x; i < at.y; ++i) {
+    for (int i = at.x; i < at.y && n < m; ++i) {
       n += key_of(row.at(i)) == key;
-      if (n == equal) {
-        sh.last = i;
-        break;
-      }
+      sh.last = i;
     }
   }
   __syncthreads();
   const unsigned last = sh.last;
   __syncthreads();
-  return Cut{key, last};
+  return last;
+}
+
+// Exact borders by bisection, for rows whose listed bins hold too many logits.
+template <typename T>
+__device__ Cut cut_from(const Row<T>& row, unsigned key, uint64_t equal, Shared& sh) {
+  return Cut{key, nth_equal(row, key, equal, sh)};
 }
 template <typename T>
 __device__ __noinline__ Cut bisect_count(const Row<T>& row, unsigned lo, unsigned hi, uint64_t k, Shared& sh) {
   auto count = [&](unsigned key) {  // logits of at least this key
     uint64_t n = 0;
-    row.template each<1>([&](float x, int) { n += key_of(x) >= key; });
+    row.template each<1>([&](float x, int) { n += x == x && key_of(x) >= key; });
     return block_sum64(n, sh);
   };
   while (lo < hi) {  // the largest key that at least k logits reach
@@ -376,16 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   const long long r = blockIdx.x;
   const Row<T> row(static_cast<const T*>(c.logits) + r * c.p.pitch, c.p.vocab);
   const Settings s = settings_of(c, (int)r);
-  unsigned top = 0, low = kFull;
-  row.template each<4>([&](float x, int) {
-    const unsigned k = key_of(x);
-    top = max(top, k);
-    low = min(low, k);
-  });
+  const float2 own = row.range();
   load_exp2(sh.tab);
   sh.mass[tid] = 0;
-  top = __reduce_max_sync(kFull, top);
-  low = __reduce_min_sync(kFull, low);
+  unsigned top = __reduce_max_sync(kFull, key_of(own.x)), low = __reduce_min_sync(kFull, key_of(own.y));
   if (lane == 0) sh.ubuf[0][warp] = top, sh.ubuf[1][warp] = low;
   __syncthreads();
   top = __reduce_max_sync(kFull, sh.ubuf[0][lane]);
@@ -401,6 +424,23 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     if (tid == 0) {
       c.token[r] = mx == -INFINITY ? -1 : (int)first;
       if (c.logprob) c.logprob[r] = mx == -INFINITY ? mx : 0.f;
+    }
+    return;
+  }
+  if (mx == INFINITY) {  // all weights are 1, of these logits alone
+    uint64_t n = 0;
+    row.template each<1>([&](float x, int) { n += x == mx; });
+    n = block_sum64(n, sh);
+    if (s.top_k > 0 && (uint64_t)s.top_k < n) n = s.top_k;
+    if (s.top_p < 1.f) {
+      const uint64_t f = fraction(s.top_p > 0.f ? s.top_p : 0.f);
+      n = __umul64hi(f, n) + (f * n != 0);
+      if (n == 0) n = 1;
+    }
+    const unsigned at = nth_equal(row, top, __umul64hi(fraction(s.u), n) + 1, sh);
+    if (tid == 0) {
+      c.token[r] = (int)at;
+      if (c.logprob) c.logprob[r] = -logf((float)n);
     }
     return;
   }
@@ -425,12 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   auto cut_at = [&](uint64_t order) { return Cut{(unsigned)(order >> 32), kFull - (unsigned)order}; };
 
   Cut cut{0, kFull};
+  bool some_cut = false;
   if (s.top_k > 0 && s.top_k < row.V) {
     const unsigned k = s.top_k;
     clear_bins();
     row.template each<2>([&](float x, int) {
       const float y = bins.place(x);
-      if (y < (float)kBins) atomicAdd(sh.bins + (int)y, 1u);
+      if (bins.inside(y)) atomicAdd(sh.bins + bins.number(bins.bin(y)), 1u);
     });
     __syncthreads();
     const unsigned c0 = sh.bins[2 * tid], c1 = sh.bins[2 * tid + 1];
@@ -441,11 +482,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
       else if (before + c0 < k && k <= before + c0 + c1) sh.first = 2 * tid + 1, sh.last = before + c0;
       __syncthreads();
       const int bin = sh.first;
+      some_cut = true;
       const unsigned above = sh.last;
       if (sh.bins[bin] <= kList) {
+        const float wanted = 12582912.f + bin;
         row.template each<2>([&](float x, int i) {
-          const float y = bins.place(x);
-          if (y < (float)kBins && (int)y == bin) list(key_of(x), i, 0);
+          if (bins.bin(bins.place(x)) == wanted) list(key_of(x), i, 0);
         });
         __syncthreads();
         const int n = sh.listed;
@@ -468,13 +510,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
 
   if (s.top_p < 1.f) {
     clear_bins();
-    constexpr float unit = 262144.f;  // 2^18: a bin's masses in units of 2^-18 of its largest weight
+    // a bin's masses in units of 2^-18 of the weight at its middle
     row.template each<2>([&](float x, int i) {
       const float y = bins.place(x);
-      if (y < (float)kBins && cut.keeps(key_of(x), i)) {
-        const int b = (int)y;
-        atomicAdd(sh.bins + b, (unsigned)(ptx::ex2_approx(((float)b - y) * bins.log2_step) * unit));
-      }
+      if (!bins.inside(y) || (some_cut && !cut.keeps(key_of(x), i))) return;
+      const float b = bins.bin(y), q = ptx::ex2_approx(fmaf(__fsub_rn(b, 12582912.f) - y, bins.log2_step, 18.f));
+      atomicAdd(sh.bins + bins.number(b), (unsigned)(__float_as_int(q + 8388608.f) - 0x4b000000));
     });
     __syncthreads();
     const float m0 = (float)sh.bins[2 * tid] * ptx::ex2_approx((float)(-2 * tid) * bins.log2_step);
@@ -490,18 +531,18 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane]), last = __reduce_min_sync(kFull, sh.ubuf[1][lane]);
     // exact sums of everything and of the bins before; the bins between are listed
     uint64_t mass = 0, sure = 0;
+    const float first_bin = 12582912.f + first, last_bin = 12582912.f + last;
     row.sum_spans(sh.mass, [&](float x, int i) -> uint64_t {
-      const float y = bins.place(x);
-      const unsigned key = key_of(x);
-      if (!(y < (float)kBins) || !cut.keeps(key, i)) return 0;
+      const float b = bins.bin(bins.place(x));
+      if (some_cut && !cut.keeps(key_of(x), i)) return 0;
       const uint64_t w = weight(x, mx, sc, sh.tab);
       mass += w;
-      if ((int)y >= first) {
-        if ((int)y <= last && w) list(key, i, w);
-        return 0;
+      if (b < first_bin) {
+        sure += w;
+        return w >= least ? w : 0;
       }
-      sure += w;
-      return w >= least ? w : 0;
+      if (b <= last_bin && w) list(key_of(x), i, w);
+      return 0;
     });
     mass = block_sum64(mass, sh);
     sure = block_sum64(sure, sh);
@@ -534,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     }
   } else {
     row.sum_spans(sh.mass, [&](float x, int i) {
-      const uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
+      const uint64_t w = !some_cut || cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
       return w >= least ? w : 0;
     });
   }
