@@ -5,7 +5,7 @@
 //   the mass, of these w >= min_p;  token: first i with sum_{kept j <= i} w_j > u sum_{kept} w_j
 //
 // A token is a whole number, so the sums have to decide as those of the real numbers: weights are
-// formed to about 2^-42 of the largest and summed as integers (units of 2^-44).  What is kept is a
+// formed to a relative 2^-33 and summed as integers (units of 2^-44).  What is kept is a
 // run of the order (logit descending, index ascending): all logits above a cut, and the first
 // few that equal it.
 #include <math.h>
@@ -25,18 +25,21 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // ------------------------------------------------------------------- weights in fixed point
 
-struct Exp2Entry {
-  uint64_t t;    // 2^(i/256) 2^46
-  float hi, lo;  // the same as a sum of two floats
+// 2^(i/256), i < 256: in units of 2^-46, and as a float in units of 2^-38.
+struct Exp2Table {
+  uint64_t t[256];
+  float f[256];
 };
-__device__ __forceinline__ void load_exp2(Exp2Entry* tab) {
-  for (int i = threadIdx.x; i < 256; i += kThreads) {
-    const uint64_t t = kExp2Table[i];
-    // 47 bits: the upper 24 and the lower 23 are exact floats
-    const float hi = (float)(t >> 23) * 1.1920928955078125e-7f;                            // 2^-23
-    tab[i] = Exp2Entry{t, hi, (float)(t & 0x7fffff) * 1.4210854715202004e-14f};            // 2^-46
+// A thread's share of the table, asked for early and stored later.
+struct Exp2Share {
+  uint64_t t;
+  __device__ __forceinline__ Exp2Share() : t(kExp2Table[threadIdx.x & 255]) {}
+  __device__ __forceinline__ void store(Exp2Table& tab) const {
+    if (threadIdx.x >= 256) return;
+    tab.t[threadIdx.x] = t;
+    tab.f[threadIdx.x] = (float)t * 0.00390625f;  // 2^-8
   }
-}
+};
 
 // log2(e) / T as a sum of two floats.
 struct Scale {
@@ -49,36 +52,24 @@ __device__ __forceinline__ Scale scale_of(float temp) {
 }
 
 // e^{(x - max) / T} in units of 2^-44, 0 where it is less than 2^-40 (and for NaN); max is finite.
-// y = (x - max) log2(e) / T is carried as a sum of two floats; 2^y = 2^k 2^(i/256) (1 + t + t^2/2 + ...),
-// |t| < 2^-9.5, whose terms up to t^4 reach 2^-44.  Sums and products are rounded one by one (none
-// may be fused).
-__device__ __forceinline__ uint64_t weight(float x, float mx, Scale c, const Exp2Entry* tab) {
+// y = (x - max) log2(e) / T is carried as a sum of two floats, 2^y = 2^k 2^(i/256) 2^r with |r| < 1/500.
+// 2^r - 1 is below 2^-8.5, so that its roundings in fp32 leave a relative error of 2^-33; the sum
+// with the table's 47 bits and the shift by k are integers.  Sums and products are rounded one by
+// one (none may be fused).
+__device__ __forceinline__ uint64_t weight(float x, float mx, Scale c, const Exp2Table& tab) {
   const float d = __fsub_rn(x, mx), back = __fsub_rn(d, x);
   const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(mx, back));
   const float yh = __fmul_rn(d, c.hi);
   const float yl = __fadd_rn(__fmaf_rn(d, c.hi, -yh), __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi)));
-  if (!(__fadd_rn(yh, yl) >= -40.f)) return 0;
   const float m = __fmaf_rn(yh, 256.f, 12582912.f);  // 1.5 2^23: the sum's low bits are the nearest integer
   const int n = __float_as_int(m) - 0x4b400000;
-  const float r0 = __fmaf_rn(__fsub_rn(m, 12582912.f), -0.00390625f, yh), r = __fadd_rn(r0, yl);
-  const float rl = __fsub_rn(yl, __fsub_rn(r, r0));
-  constexpr float l2h = 0.693147182464599609375f, l2l = -1.9046542121259336e-09f;  // ln 2
-  const float th = __fmul_rn(r, l2h);
-  const float tl = __fadd_rn(__fmaf_rn(r, l2h, -th), __fmaf_rn(r, l2l, __fmul_rn(rl, l2h)));
-  const float q = __fmul_rn(__fmul_rn(th, th), __fmaf_rn(th, __fmaf_rn(th, 1.f / 24, 1.f / 6), 0.5f));
-  const Exp2Entry e = tab[n & 255];
-  const float p = __fmul_rn(e.hi, th);
-  const float pe = __fmaf_rn(e.hi, th, -p);
-  const float low = __fadd_rn(pe, __fmaf_rn(e.lo, th, __fmul_rn(e.hi, __fadd_rn(tl, q))));
-  // the two parts as integers, by sums whose last bit is 2^-30 and 2^-41
-  constexpr float c1 = 0.01171875f, c2 = 5.7220458984375e-06f;  // 1.5 2^-7, 1.5 2^-18
-  const float s1 = __fadd_rn(p, c1);
-  const int i1 = __float_as_int(s1) - __float_as_int(c1);
-  const float rest = __fadd_rn(__fsub_rn(p, __fsub_rn(s1, c1)), low);
-  const int i2 = __float_as_int(__fadd_rn(rest, c2)) - __float_as_int(c2);
-  const uint64_t w = e.t + (int64_t)i1 * 65536 + (int64_t)(i2 * 32);
-  const int s = 46 - kUnit - (n >> 8);  // 2..42
-  return (w + (1ull << (s - 1))) >> s;
+  const float r = __fadd_rn(__fmaf_rn(__fsub_rn(m, 12582912.f), -0.00390625f, yh), yl);
+  // ln 2, ln^2 2 / 2, ln^3 2 / 6
+  const float e = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, 0.055504109f, 0.24022651f), 0.69314718f));
+  const int part = __float2int_rn(__fmul_rn(e, tab.f[n & 255]));
+  const uint64_t w = tab.t[n & 255] + (int64_t)part * 256;
+  const int s = 46 - kUnit - 1 - (n >> 8);  // one less than the shift: 1 .. 41
+  return __fadd_rn(yh, yl) >= -40.f ? ((w >> s) + 1) >> 1 : 0;
 }
 
 // Order of the logits as unsigned integers.
@@ -95,14 +86,14 @@ __device__ __forceinline__ float value_of(unsigned key) {
 constexpr int kBins = 2 * kThreads, kList = 1024, kSpans = kThreads;
 
 struct Shared {
-  Exp2Entry tab[256];
+  Exp2Table tab;
   uint64_t mass[kSpans];     // kept mass of the row's spans
   unsigned bins[kBins];
   unsigned key[kList];       // the logits of the bins that hold a border
   unsigned idx[kList];
   uint64_t w[kList];
   int listed;
-  uint64_t buf[kWarps];
+  uint64_t buf[kWarps], buf2[kWarps], buf3[kWarps];
   unsigned ubuf[2][kWarps];
   float fbuf[kWarps];
   int first, last;
@@ -121,6 +112,19 @@ __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
   v = warp_sum64(sh.buf[threadIdx.x & 31]);
   __syncthreads();
   return v;
+}
+// Three at once.
+__device__ __forceinline__ void block_sum64(uint64_t& a, uint64_t& b, uint64_t& c, Shared& sh) {
+  a = warp_sum64(a);
+  b = warp_sum64(b);
+  c = warp_sum64(c);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  if (lane == 0) sh.buf[warp] = a, sh.buf2[warp] = b, sh.buf3[warp] = c;
+  __syncthreads();
+  a = warp_sum64(lane < kWarps ? sh.buf[lane] : 0);
+  b = warp_sum64(lane < kWarps ? sh.buf2[lane] : 0);
+  c = warp_sum64(lane < kWarps ? sh.buf3[lane] : 0);
+  __syncthreads();
 }
 __device__ __forceinline__ uint64_t block_min64(uint64_t v, Shared& sh) {
   auto least = [](uint64_t x) {
@@ -293,10 +297,12 @@ struct Settings {
   int top_k;
 };
 
-__device__ Settings settings_of(const SampleCall& c, int row) {
+__device__ __forceinline__ Settings settings_of(const SampleCall& c, int row) {
   const tg_sample_params& p = c.p;
-  Settings s{p.temperatures ? p.temperatures[row] : p.temperature, p.top_ps ? p.top_ps[row] : p.top_p,
-             p.min_ps ? p.min_ps[row] : p.min_p, c.uniform[row], p.top_ks ? p.top_ks[row] : p.top_k};
+  return Settings{p.temperatures ? p.temperatures[row] : p.temperature, p.top_ps ? p.top_ps[row] : p.top_p,
+                  p.min_ps ? p.min_ps[row] : p.min_p, c.uniform[row], p.top_ks ? p.top_ks[row] : p.top_k};
+}
+__device__ __forceinline__ Settings checked(Settings s, const SampleCall& c) {
   bool bad = false;
   if (!(s.temp >= 0.f)) { bad = true; s.temp = s.temp < 0.f ? 0.f : 1.f; }
   if (s.top_p != s.top_p) { bad = true; s.top_p = 1.f; }
@@ -404,9 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const long long r = blockIdx.x;
   const Row<T> row(static_cast<const T*>(c.logits) + r * c.p.pitch, c.p.vocab);
-  const Settings s = settings_of(c, (int)r);
+  const Exp2Share share_of_table;
+  const Settings given = settings_of(c, (int)r);
   const float2 own = row.range();
-  load_exp2(sh.tab);
+  const Settings s = checked(given, c);
+  share_of_table.store(sh.tab);
   sh.mass[tid] = 0;
   unsigned top = __reduce_max_sync(kFull, key_of(own.x)), low = __reduce_min_sync(kFull, key_of(own.y));
   if (lane == 0) sh.ubuf[0][warp] = top, sh.ubuf[1][warp] = low;
@@ -544,13 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
       if (b <= last_bin && w) list(key_of(x), i, w);
       return 0;
     });
-    mass = block_sum64(mass, sh);
-    sure = block_sum64(sure, sh);
+    __syncthreads();
+    const int n = sh.listed;
+    uint64_t listed = tid < n && n <= kList ? sh.w[tid] : 0;
+    block_sum64(mass, sure, listed, sh);
     const uint64_t p = fraction(share);
     uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
     if (need == 0) need = 1;
-    const int n = sh.listed;
-    const uint64_t listed = block_sum64(tid < n && n <= kList ? sh.w[tid] : 0, sh);
     if (n <= kList && sure < need && sure + listed >= need) {
       uint64_t order = ~0ull;
       if (tid < n) {
@@ -591,28 +599,32 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   }
   __syncthreads();
   if (warp != 0) return;
-  uint64_t rest = sh.rest;
+  const uint64_t rest = sh.rest;
   const int2 span = row.span(sh.first);
-  for (int i0 = span.x; i0 < span.y; i0 += 32) {
-    const int i = i0 + lane;
-    const float x = i < span.y ? row.at(i) : -INFINITY;
-    uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
-    if (w < least) w = 0;
-    if (!__any_sync(kFull, w != 0)) continue;
-    uint64_t incl = w;
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t up = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += up;
-    }
-    const unsigned hit = __ballot_sync(kFull, incl > rest);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) {
-        c.token[r] = i;
-        if (c.logprob) c.logprob[r] = w == total ? 0.f : logf((float)w / (float)total);
-      }
-      return;
-    }
-    rest -= __shfl_sync(kFull, incl, 31);
+  const int per = (span.y - span.x + 31) / 32, from = span.x + lane * per, to = min(span.y, from + per);
+  auto kept_weight = [&](int i) {
+    const float x = row.at(i);
+    const uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
+    return w < least ? 0 : w;
+  };
+  uint64_t own_mass = 0;
+#pragma unroll 4
+  for (int i = from; i < to; ++i) own_mass += kept_weight(i);
+  uint64_t incl = own_mass;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += up;
+  }
+  const unsigned hit = __ballot_sync(kFull, incl > rest);
+  if (lane != __ffs(hit) - 1) return;
+  uint64_t sum = incl - own_mass;
+  for (int i = from; i < to; ++i) {
+    const uint64_t w = kept_weight(i);
+    sum += w;
+    if (sum <= rest) continue;
+    c.token[r] = i;
+    if (c.logprob) c.logprob[r] = w == total ? 0.f : logf((float)w / (float)total);
+    return;
   }
 }
 

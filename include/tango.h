@@ -711,8 +711,8 @@ tg_status tango_distill_backward(const tg_distill_params *p, const void *logits,
  *   sum over kept j <= i of w_j  >  u * sum over kept j of w_j.
  * Equal logits are ranked by ascending index.  T = 0 takes the largest logit (lowest index).  +inf
  * logits share the row evenly.  A row with no token to draw (all -inf or NaN) gives -1.  The sums
- * are formed in 64-bit fixed point from weights of 40 bits and more, so that the token is that of
- * the real numbers but where u or top_p lie within about 1e-12 of a border.
+ * are formed in 64-bit fixed point from weights good to about 2^-33, so that the token is that of
+ * the real numbers but where u or top_p lie within about 1e-10 of a border.
  *   rows, vocab     rows >= 0 (0 launches nothing); 1 <= vocab <= 2^19
  *   pitch           elements between rows of logits (0: vocab)
  *   dtype           of logits
