@@ -68,8 +68,9 @@ __device__ __forceinline__ uint64_t weight(float x, float mx, Scale c, const Exp
   const float e = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, 0.055504109f, 0.24022651f), 0.69314718f));
   const int part = __float2int_rn(__fmul_rn(e, tab.f[n & 255]));
   const uint64_t w = tab.t[n & 255] + (int64_t)part * 256;
-  const int s = 46 - kUnit - 1 - (n >> 8);  // one less than the shift: 1 .. 41
-  return __fadd_rn(yh, yl) >= -40.f ? ((w >> s) + 1) >> 1 : 0;
+  // one less than the shift, 1 .. 41, or what shifts all out
+  const int s = __fadd_rn(yh, yl) >= -40.f ? 46 - kUnit - 1 - (n >> 8) : 63;
+  return ((w >> s) + 1) >> 1;
 }
 
 // Order of the logits as unsigned integers.
@@ -84,13 +85,14 @@ __device__ __forceinline__ float value_of(unsigned key) {
 // --------------------------------------------------------------------------- reductions
 
 constexpr int kBins = 2 * kThreads, kList = 1024, kSpans = kThreads;
+constexpr int kShort = 256;  // a list that is gone through twice per entry
 
 struct Shared {
   Exp2Table tab;
   uint64_t mass[kSpans];     // kept mass of the row's spans
   unsigned bins[kBins];
-  unsigned key[kList];       // the logits of the bins that hold a border
-  unsigned idx[kList];
+  uint64_t order[kList];     // the logits of the bins that hold a border: a number that falls along
+                             // the row's order, (key, ~index)
   uint64_t w[kList];
   int listed;
   uint64_t buf[kWarps], buf2[kWarps], buf3[kWarps];
@@ -100,9 +102,14 @@ struct Shared {
   uint64_t rest;
 };
 
+// By 32-bit reductions of 22 bits at a time.
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
+  const unsigned lo = __reduce_add_sync(kFull, (unsigned)v & 0x3fffffu), mid = __reduce_add_sync(kFull, (unsigned)(v >> 22) & 0x3fffffu);
+  return lo + ((uint64_t)mid << 22) + ((uint64_t)__reduce_add_sync(kFull, (unsigned)(v >> 44)) << 44);
+}
+__device__ __forceinline__ uint64_t warp_min64(uint64_t v) {
+  const unsigned hi = __reduce_min_sync(kFull, (unsigned)(v >> 32));
+  return (uint64_t)hi << 32 | __reduce_min_sync(kFull, (unsigned)(v >> 32) == hi ? (unsigned)v : kFull);
 }
 // Over the block, for every thread; the barrier at the end frees the buffer again.
 __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
@@ -127,14 +134,10 @@ __device__ __forceinline__ void block_sum64(uint64_t& a, uint64_t& b, uint64_t& 
   __syncthreads();
 }
 __device__ __forceinline__ uint64_t block_min64(uint64_t v, Shared& sh) {
-  auto least = [](uint64_t x) {
-    for (int o = 16; o > 0; o >>= 1) x = min(x, (uint64_t)__shfl_xor_sync(kFull, x, o));
-    return x;
-  };
-  v = least(v);
+  v = warp_min64(v);
   if ((threadIdx.x & 31) == 0) sh.buf[threadIdx.x / 32] = v;
   __syncthreads();
-  v = least(sh.buf[threadIdx.x & 31]);
+  v = warp_min64(sh.buf[threadIdx.x & 31]);
   __syncthreads();
   return v;
 }
@@ -264,14 +267,16 @@ struct Row {
       }
     }
   }
-  // Adds f(value, index) up in mass[span], which holds zeros.
+  // Adds f(value, index) up in mass[span], which holds zeros; returns the thread's own sum.
   template <typename F>
-  __device__ __forceinline__ void sum_spans(uint64_t* mass, F f) const {
+  __device__ __forceinline__ uint64_t sum_spans(uint64_t* mass, F f) const {
     using u64 = unsigned long long;
     const int tid = threadIdx.x;
+    uint64_t all = 0;
     if (tid < edge) {
       const int i = tid < lead ? tid : tid + nvec * E;
       const uint64_t w = f(at(i), i);
+      all += w;
       if (w) atomicAdd((u64*)mass + span_of(i), (u64)w);
     }
     const uint4* v = reinterpret_cast<const uint4*>(x + lead);
@@ -286,9 +291,11 @@ struct Row {
         for (int j = 0; j < E; ++j) w += f(e[j], lead + i * E + j);
       }
       if (!__any_sync(kFull, w != 0)) continue;
+      all += w;
       w = warp_sum64(w);
       if ((tid & 31) == 0) atomicAdd((u64*)mass + (b >> 5 >> wide), (u64)w);
     }
+    return all;
   }
 };
 
@@ -399,6 +406,40 @@ __device__ __noinline__ Cut bisect_mass(const Row<T>& row, unsigned lo, unsigned
   return lo == within.key && within.last < cut.last ? within : cut;
 }
 
+// The token of a row from its list, which holds all of the top_k logits.
+__device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings& s, long long r, uint64_t least, Shared& sh) {
+  const int tid = threadIdx.x, n = sh.listed;
+  uint64_t mine = 0, w = 0, before = 0;
+  unsigned rank = 0;
+  if (tid < n) {
+    mine = sh.order[tid];
+    w = sh.w[tid];
+    for (int j = 0; j < n; ++j)
+      if (sh.order[j] > mine) {
+        ++rank;
+        before += sh.w[j];
+      }
+  }
+  bool kept = tid < n && rank < (unsigned)s.top_k && w > 0;
+  if (s.top_p < 1.f) {
+    const uint64_t mass = block_sum64(kept ? w : 0, sh), p = fraction(s.top_p > 0.f ? s.top_p : 0.f);
+    const uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
+    kept = kept && (before < need || before == 0);
+  }
+  w = kept && w >= least ? w : 0;
+  if (tid < n) sh.mass[tid] = w;
+  const uint64_t total = block_sum64(w, sh), target = __umul64hi(fraction(s.u), total);
+  if (w == 0) return;
+  const unsigned index = kFull - (unsigned)mine;
+  uint64_t sum = 0;
+  for (int j = 0; j < n; ++j)
+    if (kFull - (unsigned)sh.order[j] < index) sum += sh.mass[j];
+  if (sum <= target && target < sum + w) {
+    c.token[r] = (int)index;
+    if (c.logprob) c.logprob[r] = w == total ? 0.f : logf((float)w / (float)total);
+  }
+}
+
 // One block per row.  A border (of the k-th logit, or of the share of the mass) is found with a
 // histogram of counts, or of masses good to about 1e-5; only the logits of the bins that may hold it
 // are listed and compared one by one, in exact sums.  Should there be too many of them, the
@@ -455,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   const Scale sc = scale_of(s.temp);
   const Bins bins(mx, value_of(low), s.temp, sc);
   const uint64_t least = s.min_p > 0.f ? (uint64_t)ceilf(s.min_p * 17592186044416.f) : 0;  // 2^44
+  const bool some_least = least > 0;
   auto clear_bins = [&] {
     sh.bins[tid] = sh.bins[tid + kThreads] = 0;
     if (tid == 0) sh.listed = 0;
@@ -463,13 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   auto list = [&](unsigned key, int i, uint64_t w) {
     const int n = atomicAdd(&sh.listed, 1);
     if (n < kList) {
-      sh.key[n] = key;
-      sh.idx[n] = i;
+      sh.order[n] = (uint64_t)key << 32 | (kFull - (unsigned)i);
       sh.w[n] = w;
     }
   };
-  // entries come in the row's order by key, falling, then by index; as one number that falls
-  auto order_of = [&](int j) { return (uint64_t)sh.key[j] << 32 | (kFull - sh.idx[j]); };
+  // the row's order, by key, falling, then by index, as one number that falls
   auto cut_at = [&](uint64_t order) { return Cut{(unsigned)(order >> 32), kFull - (unsigned)order}; };
 
   Cut cut{0, kFull};
@@ -492,8 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
       const int bin = sh.first;
       some_cut = true;
       const unsigned above = sh.last;
+      const float wanted = 12582912.f + bin;
+      if (above + sh.bins[bin] <= kShort) {  // all that may be kept fits a short list
+        row.template each<2>([&](float x, int i) {
+          if (bins.bin(bins.place(x)) <= wanted) list(key_of(x), i, weight(x, mx, sc, sh.tab));
+        });
+        __syncthreads();
+        draw_listed(c, s, r, least, sh);
+        return;
+      }
       if (sh.bins[bin] <= kList) {
-        const float wanted = 12582912.f + bin;
         row.template each<2>([&](float x, int i) {
           if (bins.bin(bins.place(x)) == wanted) list(key_of(x), i, 0);
         });
@@ -501,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
         const int n = sh.listed;
         uint64_t last = ~0ull;
         if (tid < n) {
-          const uint64_t mine = order_of(tid);
+          const uint64_t mine = sh.order[tid];
           unsigned rank = above;
-          for (int j = 0; j < n; ++j) rank += order_of(j) > mine;
+          for (int j = 0; j < n; ++j) rank += sh.order[j] > mine;
           if (rank < k) last = mine;
         }
         cut = cut_at(block_min64(last, sh));
@@ -538,36 +586,39 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     __syncthreads();
     const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane]), last = __reduce_min_sync(kFull, sh.ubuf[1][lane]);
     // exact sums of everything and of the bins before; the bins between are listed
-    uint64_t mass = 0, sure = 0;
+    uint64_t rest = 0, small = 0;  // mass from the first listed bin on, and of what min_p drops before it
     const float first_bin = 12582912.f + first, last_bin = 12582912.f + last;
-    row.sum_spans(sh.mass, [&](float x, int i) -> uint64_t {
+    uint64_t sure = row.sum_spans(sh.mass, [&](float x, int i) -> uint64_t {
       const float b = bins.bin(bins.place(x));
       if (some_cut && !cut.keeps(key_of(x), i)) return 0;
       const uint64_t w = weight(x, mx, sc, sh.tab);
-      mass += w;
       if (b < first_bin) {
-        sure += w;
-        return w >= least ? w : 0;
+        if (!some_least || w >= least) return w;
+        small += w;
+        return 0;
       }
+      rest += w;
       if (b <= last_bin && w) list(key_of(x), i, w);
       return 0;
     });
+    sure += small;
     __syncthreads();
     const int n = sh.listed;
     uint64_t listed = tid < n && n <= kList ? sh.w[tid] : 0;
-    block_sum64(mass, sure, listed, sh);
+    block_sum64(rest, sure, listed, sh);
+    const uint64_t mass = sure + rest;
     const uint64_t p = fraction(share);
     uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
     if (need == 0) need = 1;
     if (n <= kList && sure < need && sure + listed >= need) {
       uint64_t order = ~0ull;
       if (tid < n) {
-        const uint64_t mine = order_of(tid);
+        const uint64_t mine = sh.order[tid];
         uint64_t g = sure;
-        for (int j = 0; j < n; ++j) g += order_of(j) > mine ? sh.w[j] : 0;
+        for (int j = 0; j < n; ++j) g += sh.order[j] > mine ? sh.w[j] : 0;
         if (g < need) {
           order = mine;
-          if (sh.w[tid] >= least) atomicAdd((u64*)sh.mass + row.span_of(sh.idx[tid]), (u64)sh.w[tid]);
+          if (sh.w[tid] >= least) atomicAdd((u64*)sh.mass + row.span_of(kFull - (unsigned)mine), (u64)sh.w[tid]);
         }
       }
       cut = cut_at(block_min64(order, sh));
@@ -578,13 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
       __syncthreads();
       row.sum_spans(sh.mass, [&](float x, int i) {
         const uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
-        return w >= least ? w : 0;
+        return some_least && w < least ? 0 : w;
       });
     }
   } else {
     row.sum_spans(sh.mass, [&](float x, int i) {
       const uint64_t w = !some_cut || cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
-      return w >= least ? w : 0;
+      return some_least && w < least ? 0 : w;
     });
   }
   __syncthreads();
