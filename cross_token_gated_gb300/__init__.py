@@ -828,19 +828,15 @@ def tango_embed_backward(ids, dout, dembedding, *, base=None, scale=1.0, pad_id=
     return dembedding
 
 
-def _norm_params(x, norm, eps, outs, vectors):
-    """tg_norm_params, and the addresses of dense tensors like x and of [d] vectors (or None)."""
-    dt, dev = x.dtype, x.get_device()
-    rows, d, pitch = _rows_pitch(x, "x", dt, dev)
-    ptrs = [_optional(t, name, dt, dev, x.shape) for name, t in outs]
-    vecs = [_optional(t, name, vt or dt, dev, (d,)) for name, t, vt in vectors]
-    return tg_norm_params(rows, d, norm, eps, pitch, _dtype_code(x)), ptrs, vecs, dev
-
-
 def tango_norm(x, gamma, beta, y, *, norm=TG_NORM_RMS, eps=1e-6, stream=None):
     """y = gamma * n + beta with n the RMS (or TG_NORM_LAYER) norm of x's rows: x [..., d], its rows
     at one pitch; gamma and beta [d] or None; y dense, like x."""
-    p, (yp,), (gp, bp), dev = _norm_params(x, norm, eps, (("y", y),), (("gamma", gamma, None), ("beta", beta, None)))
+    dt, dev = x.dtype, x.get_device()
+    rows, d, pitch = _rows_pitch(x, "x", dt, dev)
+    yp = _dense(y, "y", dt, dev, x.shape)
+    gp = None if gamma is None else _dense(gamma, "gamma", dt, dev, (d,))
+    bp = None if beta is None else _dense(beta, "beta", dt, dev, (d,))
+    p = tg_norm_params(rows, d, norm, eps, pitch, _dtype_code(x))
     with _on_device(dev):
         st = (_lib or load()).tango_norm(ctypes.byref(p), x.data_ptr(), gp, bp, yp, _stream_on(stream, dev))
     if st != TG_OK:
@@ -852,9 +848,15 @@ def tango_norm_backward(x, gamma, dy, dx, *, norm=TG_NORM_RMS, eps=1e-6, dres=No
                         stream=None):
     """Gradients of tango_norm: dx (dense, like x) from dy, plus dres where given; dgamma and dbeta
     (float32 [d]) where given."""
-    p, (dyp, rp, dxp), (gp, dgp, dbp), dev = _norm_params(
-        x, norm, eps, (("dy", dy), ("dres", dres), ("dx", dx)),
-        (("gamma", gamma, None), ("dgamma", dgamma, torch.float32), ("dbeta", dbeta, torch.float32)))
+    dt, dev = x.dtype, x.get_device()
+    rows, d, pitch = _rows_pitch(x, "x", dt, dev)
+    shape, f32 = x.shape, torch.float32
+    dyp, dxp = _dense(dy, "dy", dt, dev, shape), _dense(dx, "dx", dt, dev, shape)
+    rp = None if dres is None else _dense(dres, "dres", dt, dev, shape)
+    gp = None if gamma is None else _dense(gamma, "gamma", dt, dev, (d,))
+    dgp = None if dgamma is None else _dense(dgamma, "dgamma", f32, dev, (d,))
+    dbp = None if dbeta is None else _dense(dbeta, "dbeta", f32, dev, (d,))
+    p = tg_norm_params(rows, d, norm, eps, pitch, _dtype_code(x))
     lib, ref = _lib or load(), ctypes.byref(p)
     wp, wn, wbuf = None, 0, None
     with _on_device(dev):

@@ -538,7 +538,7 @@ tg_status validate_embed(const tg_embed_params* p) {
 
 EmbedCall embed_call(const tg_embed_params* p) {
   EmbedCall c = {};
-  c.rows = p->rows; c.d = p->d; c.vocab = p->vocab; c.pad_id = p->pad_id; c.scale = p->scale;
+  c.rows = p->rows; c.d = p->d; c.vocab = p->vocab; c.pad_id = p->pad_id; c.padded = true; c.scale = p->scale;
   c.pitch = p->pitch ? p->pitch : p->d;
   c.dtype = p->dtype; c.grad_dtype = p->grad_dtype;
   return c;
@@ -795,7 +795,11 @@ tg_status tango_model_forward(const tg_model_params* p, const tg_model_weights* 
   if (error_word(&err) != cudaSuccess) return TG_ERR_CUDA;
 
   // h^(0): token embeddings (the tied matrix)
-  if (launch_embed(ap.dtype, ids, w->embedding, h, BT, d, p->vocab, err, stream) != cudaSuccess) return TG_ERR_CUDA;
+  EmbedCall ec = {};
+  ec.rows = BT; ec.pitch = d; ec.d = d; ec.vocab = p->vocab; ec.padded = false; ec.scale = 1.f;
+  ec.dtype = ec.grad_dtype = ap.dtype;
+  ec.ids = ids; ec.E = w->embedding; ec.out = h; ec.err = err;
+  if (launch_embed_lookup(ec, stream) != cudaSuccess) return TG_ERR_CUDA;
   // eq. 11: h^(r+1) = Block(h^(r)), in place
   // (a set's padded gate weights stay in the block workspace while the next application
   // uses the same set)

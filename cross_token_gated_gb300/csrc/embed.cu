@@ -51,15 +51,15 @@ __device__ __forceinline__ uint4 scaled(uint4 u, float s, __nv_bfloat16) {
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) embed_lookup_kernel(const int* ids, const T* E, T* out, long long rows, int d,
                                                            int vocab, long long pitch, float scale, int pad,
-                                                           unsigned* err) {
+                                                           bool padded, unsigned* err) {
   constexpr int N = kVec ? 16 / (int)sizeof(T) : 1;
   const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
   const int id = ids[r];
-  const bool known = id >= 0 && id < vocab;
-  if (!known && id != pad && lane == 0) record_error(err, kErrValue | kKernModel);
-  const bool live = known && id != pad;
+  const bool known = id >= 0 && id < vocab, none = padded && id == pad;
+  if (!known && !none && lane == 0) record_error(err, kErrValue | kKernModel);
+  const bool live = known && !none;
   const T* src = E + (long long)(live ? id : 0) * d;
   T* dst = out + r * pitch;
 #pragma unroll 4
@@ -567,7 +567,7 @@ cudaError_t lookup(const EmbedCall& c, cudaStream_t s) {
   const unsigned blocks = (unsigned)((c.rows + 7) / 8);
   const auto kernel = c.d % N == 0 && c.pitch % N == 0 && aligned16(c.E) && aligned16(c.out) ? embed_lookup_kernel<T, true>
                                                                                          : embed_lookup_kernel<T, false>;
-  kernel<<<blocks, 256, 0, s>>>(c.ids, E, out, c.rows, c.d, c.vocab, c.pitch, c.scale, c.pad_id, c.err);
+  kernel<<<blocks, 256, 0, s>>>(c.ids, E, out, c.rows, c.d, c.vocab, c.pitch, c.scale, c.pad_id, c.padded, c.err);
   return cudaGetLastError();
 }
 

@@ -413,21 +413,6 @@ cudaError_t launch_rmsnorm(tg_dtype dt, const void* h, const void* gamma, void* 
 
 // ------------------------------------------------------------- model helpers
 
-// Token-embedding lookup (sec. 2.3): h[r, :] = E[ids[r], :], one warp per row.  An id
-// outside [0, vocab) is flagged in the error word and its row is written as zeros.
-template <typename T>
-__global__ void embed_kernel(const int* ids, const T* E, T* h, long long rows, int d, int vocab, unsigned* err) {
-  const long long r = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
-  if (r >= rows) return;
-  const int id = ids[r];
-  const bool ok = id >= 0 && id < vocab;
-  if (!ok && lane == 0) record_error(err, kErrValue | kKernModel);
-  const T* src = E + (long long)(ok ? id : 0) * d;
-  T* dst = h + r * d;
-  for (int c = lane; c < d; c += 32) dst[c] = ok ? src[c] : T(0.f);
-}
-
 // Copy of a gate-indexed weight with each head's block of m_h entries moved to a
 // pitch of m_hp (>= m_h) entries, zeros after it.  axis 0: src [H*m_h, C] -> dst
 // [H*m_hp, C] (W_g, W_v); axis 1: src [R, H*m_h] -> dst [R, H*m_hp] (W_o).  R, C are
@@ -488,19 +473,6 @@ __global__ void __launch_bounds__(256) pad_gate_kernel(const T* src, T* dst, int
     }
     store8(dst + (size_t)r * C + c, v, n, vec);
   }
-}
-
-cudaError_t launch_embed(tg_dtype dt, const int* ids, const void* E, void* h, long long rows, int d, int vocab,
-                         unsigned* err, cudaStream_t s) {
-  const int warps = 8;
-  const unsigned blocks = (unsigned)((rows + warps - 1) / warps);
-  if (dt == TG_F32)
-    embed_kernel<float><<<blocks, warps * 32, 0, s>>>(ids, static_cast<const float*>(E), static_cast<float*>(h),
-                                                      rows, d, vocab, err);
-  else
-    embed_kernel<__nv_bfloat16><<<blocks, warps * 32, 0, s>>>(ids, static_cast<const __nv_bfloat16*>(E),
-                                                              static_cast<__nv_bfloat16*>(h), rows, d, vocab, err);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_pad_gate(tg_dtype dt, const void* src, void* dst, long long R, long long C, int axis, int H,

@@ -14,6 +14,7 @@ constexpr unsigned kKernSample = 8u << 8;
 struct EmbedCall {
   long long rows, pitch;
   int d, vocab, pad_id;
+  bool padded;       // whether pad_id stands for no token
   float scale;
   tg_dtype dtype, grad_dtype;
   const int* ids;

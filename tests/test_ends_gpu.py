@@ -614,6 +614,29 @@ def test_training_ends_together(lib):
     assert (dgamma.double() - g64.grad).abs().max() <= 500 * U * g64.grad.abs().max()
 
 
+def test_example_distills_and_samples(lib):
+    """The example's gradients at the model's two ends against differentiation in 64 bits (bf16
+    logits, their gradient, x and dx: four roundings of 2^-8, compared in the 2-norm), and its
+    sampled tokens."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import generate_tango as ex
+    r = ex.distill_step()
+    E = r["model"]["embedding"].double().requires_grad_()
+    gamma = r["model"]["gamma"].double().requires_grad_()
+    h = E[r["ids"].long()]
+    x = h / (h.square().mean(-1, keepdim=True) + 1e-6).sqrt() * gamma
+    loss = distill_ref(x @ E.t(), r["t_logits"], r["t_ids"], 2.0)[0]
+    loss.mean().backward()
+    assert ((r["loss"].double() - loss).norm() / loss.norm()).item() <= 4 * 2.0 ** -8
+    for got, want in ((r["dE"], E.grad), (r["dgamma"], gamma.grad)):
+        assert ((got.double() - want).norm() / want.norm()).item() <= 4 * 2.0 ** -8
+    seqs, _ = ex.generate([[1, 2, 3], [7]], 5, temperature=0.9, top_k=20, top_p=0.95)
+    again, _ = ex.generate([[1, 2, 3], [7]], 5, temperature=0.9, top_k=20, top_p=0.95)
+    assert seqs == again and [len(s) for s in seqs] == [8, 6] and all(0 <= t < ex.VOCAB for s in seqs for t in s)
+
+
 def _step(b):
     tg.tango_embed(b["ids"], b["E"], b["h"], scale=2.0)
     tg.tango_norm(b["h"], b["gamma"], b["beta"], b["x"], norm=tg.TG_NORM_LAYER)
