@@ -98,8 +98,10 @@ struct Shared {
   uint64_t buf[kWarps], buf2[kWarps], buf3[kWarps];
   unsigned ubuf[2][kWarps];
   float fbuf[kWarps];
-  int first, last;
+  int first, last, found;
   uint64_t rest;
+  uint64_t given[2][3];      // what the cluster's blocks tell each other, in turn
+  uint64_t answer;           // the first block's, to all
 };
 
 // By 32-bit reductions of 22 bits at a time.
@@ -170,6 +172,64 @@ __device__ __forceinline__ N block_before(N v, N* buf, N* total) {
   return (warp ? before : N(0)) + incl - v;
 }
 
+// C blocks that share a row (a cluster; block number `rank`).  The results of these calls are the
+// same in all threads of all blocks.
+template <int C>
+struct Group {
+  Shared& sh;
+  unsigned rank;
+  int turn = 0;
+  __device__ __forceinline__ explicit Group(Shared& s) : sh(s), rank(0) {
+    if constexpr (C > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  }
+  __device__ __forceinline__ void sync() const {
+    if constexpr (C > 1)
+      asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    else __syncthreads();
+  }
+  // before a block ends: no other block reads its memory any more
+  __device__ __forceinline__ void leave() const {
+    if constexpr (C > 1) sync();
+  }
+  // the same variable of block q
+  template <typename N>
+  __device__ __forceinline__ N* of(N* p, unsigned q) const {
+    if constexpr (C == 1) return p;
+    uint64_t a;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"((uint64_t)p), "r"(q));
+    return reinterpret_cast<N*>(a);
+  }
+  // lane q of each warp gets what thread 0 of block q gives (others zero)
+  __device__ __forceinline__ void exchange(uint64_t& a, uint64_t& b, uint64_t& c) {
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) sh.given[turn][0] = a, sh.given[turn][1] = b, sh.given[turn][2] = c;
+    sync();
+    const uint64_t* p = of(sh.given[turn], lane < C ? lane : 0);
+    a = lane < C ? p[0] : 0;
+    b = lane < C ? p[1] : 0;
+    c = lane < C ? p[2] : 0;
+    turn ^= 1;
+  }
+  __device__ __forceinline__ uint64_t sum(uint64_t v) {
+    v = block_sum64(v, sh);
+    if constexpr (C > 1) {
+      uint64_t none = 0, more = 0;
+      exchange(v, none, more);
+      v = warp_sum64(v);
+    }
+    return v;
+  }
+  __device__ __forceinline__ unsigned largest(unsigned v) {
+    v = block_max(v, sh);
+    if constexpr (C > 1) {
+      uint64_t x = v, none = 0, more = 0;
+      exchange(x, none, more);
+      v = __reduce_max_sync(kFull, (unsigned)x);
+    }
+    return v;
+  }
+};
+
 // --------------------------------------------------------------------------------- row
 
 // What is kept of the row's order: larger keys, and of the equal ones those up to an index.
@@ -207,37 +267,54 @@ template <> struct Wide<__nv_bfloat16> {
   }
 };
 
-// The row as 16-byte vectors, with the elements before the first and after the last one by
-// themselves; it is read again in every pass, from L1 or L2.  32 vectors that a warp reads at once
-// are a span; `wide` doublings of that keep their number within kSpans.
-template <typename T>
+// A block's part of the row as 16-byte vectors, with the elements before the first and after the
+// last one of the row by themselves; it is read again in every pass, from L1 or L2.  32 vectors
+// that a warp reads at once are a span; `wide` doublings of that keep their number within kSpans.
+template <typename T, int C>
 struct Row {
   static constexpr int E = Wide<T>::E;
   const T* x;
-  int V, lead, nvec, edge, wide;
-  __device__ __forceinline__ Row(const T* row, int vocab) : x(row), V(vocab) {
+  int V, lead, all, per;   // of the row: elements before the vectors, vectors, vectors of a block
+  int rank, v0, nvec;      // of this block: first vector, vectors
+  int head, edge, wide;    // single elements before the vectors, single elements in all
+  __device__ __forceinline__ Row(const T* row, int vocab, int block) : x(row), V(vocab), rank(block) {
     lead = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
-    nvec = (vocab - lead) / E;
-    edge = vocab - nvec * E;
+    all = (vocab - lead) / E;
+    per = C == 1 ? all : ((all + 31) / 32 + C - 1) / C * 32;
+    v0 = min(rank * per, all);
+    nvec = min(per, all - v0);
+    head = rank == 0 ? lead : 0;
+    edge = head + (rank == C - 1 ? vocab - lead - all * E : 0);
     wide = 0;
-    while ((nvec >> 5 >> wide) >= kSpans) ++wide;
+    while ((per >> 5 >> wide) >= kSpans) ++wide;
   }
   __device__ __forceinline__ float at(int i) const { return io<T>::ld(x + i); }
-  __device__ __forceinline__ int span_of(int i) const { return i < lead ? 0 : min(nvec > 0 ? (nvec - 1) >> 5 >> wide : 0, (i - lead) / E >> 5 >> wide); }
-  // elements of a span
+  __device__ __forceinline__ int edge_index(int t) const { return t < head ? t : lead + all * E + t - head; }
+  __device__ __forceinline__ int index(int v) const { return lead + (v0 + v) * E; }
+  // the block and span of an element
+  __device__ __forceinline__ int owner(int i) const {
+    return C == 1 || i < lead ? 0 : (i - lead) / E >= all ? C - 1 : (i - lead) / E / per;
+  }
+  __device__ __forceinline__ int span_of(int i) const {
+    if (i < lead) return 0;
+    const int q = owner(i), first = min(q * per, all), n = min(per, all - first);
+    return n > 0 ? min(n - 1, (i - lead) / E - first) >> 5 >> wide : 0;
+  }
+  // elements of a span of this block
   __device__ __forceinline__ int2 span(int s) const {
-    const int per = (32 << wide) * E, n = nvec > 0 ? ((nvec - 1) >> 5 >> wide) + 1 : 1;
-    return make_int2(s == 0 ? 0 : lead + s * per, s == n - 1 ? V : lead + (s + 1) * per);
+    const int step = (32 << wide) * E, n = nvec > 0 ? ((nvec - 1) >> 5 >> wide) + 1 : 1;
+    return make_int2(s == 0 && rank == 0 ? 0 : index(0) + s * step,
+                     s < n - 1 ? index(0) + (s + 1) * step : rank == C - 1 ? V : index(nvec));
   }
   // largest and lowest logit of the thread's, NaN left out
   __device__ __forceinline__ float2 range() const {
     float top = -INFINITY, low = INFINITY;
     if ((int)threadIdx.x < edge) {
-      const float v = at((int)threadIdx.x < lead ? threadIdx.x : threadIdx.x + nvec * E);
+      const float v = at(edge_index(threadIdx.x));
       top = fmaxf(top, v);
       low = fminf(low, v);
     }
-    const uint4* v = reinterpret_cast<const uint4*>(x + lead);
+    const uint4* v = reinterpret_cast<const uint4*>(x + lead) + v0;
 #pragma unroll 4
     for (int i = threadIdx.x; i < nvec; i += kThreads) Wide<T>::range(__ldg(v + i), top, low);
     return make_float2(top, low);
@@ -247,10 +324,10 @@ struct Row {
   __device__ __forceinline__ void each(F f) const {
     const int tid = threadIdx.x;
     if (tid < edge) {  // (fewer than 16)
-      const int i = tid < lead ? tid : tid + nvec * E;
+      const int i = edge_index(tid);
       f(at(i), i);
     }
-    const uint4* v = reinterpret_cast<const uint4*>(x + lead);
+    const uint4* v = reinterpret_cast<const uint4*>(x + lead) + v0;
 #pragma unroll 1
     for (int b = tid; b < nvec; b += U * kThreads) {
       uint4 u[U];
@@ -263,7 +340,7 @@ struct Row {
         float e[E];
         Wide<T>::unpack(u[k], e);
 #pragma unroll
-        for (int j = 0; j < E; ++j) f(e[j], lead + (b + k * kThreads) * E + j);
+        for (int j = 0; j < E; ++j) f(e[j], index(b + k * kThreads) + j);
       }
     }
   }
@@ -274,12 +351,12 @@ struct Row {
     const int tid = threadIdx.x;
     uint64_t all = 0;
     if (tid < edge) {
-      const int i = tid < lead ? tid : tid + nvec * E;
+      const int i = edge_index(tid);
       const uint64_t w = f(at(i), i);
       all += w;
       if (w) atomicAdd((u64*)mass + span_of(i), (u64)w);
     }
-    const uint4* v = reinterpret_cast<const uint4*>(x + lead);
+    const uint4* v = reinterpret_cast<const uint4*>(x + lead) + v0;
 #pragma unroll 1
     for (int b = tid & ~31; b < nvec; b += kThreads) {
       const int i = b + (tid & 31);
@@ -288,7 +365,7 @@ struct Row {
         float e[E];
         Wide<T>::unpack(__ldg(v + i), e);
 #pragma unroll
-        for (int j = 0; j < E; ++j) w += f(e[j], lead + i * E + j);
+        for (int j = 0; j < E; ++j) w += f(e[j], index(i) + j);
       }
       if (!__any_sync(kFull, w != 0)) continue;
       all += w;
@@ -340,69 +417,72 @@ struct Bins {
   static __device__ __forceinline__ int number(float b) { return __float_as_int(b) - 0x4b400000; }
 };
 
-// The index of the m-th logit (from 1) that equals a key, or of the last one where
-// there are fewer.  Overwrites sh.mass.
-template <typename T>
-__device__ __noinline__ unsigned nth_equal(const Row<T>& row, unsigned key, uint64_t m, Shared& sh) {
+// The index of the m-th logit (from 1) that equals a key, or of the last one where there are
+// fewer.  Overwrites sh.mass.
+template <typename T, int C>
+__device__ __noinline__ unsigned nth_equal(const Row<T, C>& row, unsigned key, uint64_t m, Group<C>& g) {
+  Shared& sh = g.sh;
   sh.mass[threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.found = 0;
   __syncthreads();
   row.sum_spans(sh.mass, [&](float x, int) { return (uint64_t)(key_of(x) == key); });
   __syncthreads();
   uint64_t total;
-  const uint64_t mine = sh.mass[threadIdx.x], before = block_before(mine, sh.buf, &total);
+  const uint64_t mine = sh.mass[threadIdx.x];
+  uint64_t before = block_before(mine, sh.buf, &total);
+  if constexpr (C > 1) {
+    uint64_t each = total, none = 0, more = 0;
+    g.exchange(each, none, more);
+    before += warp_sum64((threadIdx.x & 31) < g.rank ? each : 0);
+    total = warp_sum64(each);
+  }
   if (m > total) m = total;
   if (before < m && m <= before + mine) {  // walk through the span
     const int2 at = row.span(threadIdx.x);
     uint64_t n = before;
     for (int i = at.x; i < at.y && n < m; ++i) {
       n += key_of(row.at(i)) == key;
-      sh.last = i;
+      sh.found = i;
     }
   }
   __syncthreads();
-  const unsigned last = sh.last;
-  __syncthreads();
-  return last;
+  return g.largest(sh.found);
 }
 
 // Exact borders by bisection, for rows whose listed bins hold too many logits.
-template <typename T>
-__device__ Cut cut_from(const Row<T>& row, unsigned key, uint64_t equal, Shared& sh) {
-  return Cut{key, nth_equal(row, key, equal, sh)};
-}
-template <typename T>
-__device__ __noinline__ Cut bisect_count(const Row<T>& row, unsigned lo, unsigned hi, uint64_t k, Shared& sh) {
+template <typename T, int C>
+__device__ __noinline__ Cut bisect_count(const Row<T, C>& row, unsigned lo, unsigned hi, uint64_t k, Group<C>& g) {
   auto count = [&](unsigned key) {  // logits of at least this key
     uint64_t n = 0;
     row.template each<1>([&](float x, int) { n += x == x && key_of(x) >= key; });
-    return block_sum64(n, sh);
+    return g.sum(n);
   };
   while (lo < hi) {  // the largest key that at least k logits reach
     const unsigned mid = lo + (hi - lo + 1) / 2;
     if (count(mid) >= k) lo = mid;
     else hi = mid - 1;
   }
-  return cut_from(row, lo, k - (lo < kFull ? count(lo + 1) : 0), sh);
+  return Cut{lo, nth_equal(row, lo, k - (lo < kFull ? count(lo + 1) : 0), g)};
 }
-template <typename T>
-__device__ __noinline__ Cut bisect_mass(const Row<T>& row, unsigned lo, unsigned hi, Cut within, uint64_t need, float mx,
-                                        Scale sc, Shared& sh) {
+template <typename T, int C>
+__device__ __noinline__ Cut bisect_mass(const Row<T, C>& row, unsigned lo, unsigned hi, Cut within, uint64_t need, float mx,
+                                        Scale sc, Group<C>& g) {
   auto above = [&](unsigned key) {  // mass of the larger keys
-    uint64_t g = 0;
+    uint64_t n = 0;
     row.template each<1>([&](float x, int i) {
       const unsigned k = key_of(x);
-      if (k > key && within.keeps(k, i)) g += weight(x, mx, sc, sh.tab);
+      if (k > key && within.keeps(k, i)) n += weight(x, mx, sc, g.sh.tab);
     });
-    return block_sum64(g, sh);
+    return g.sum(n);
   };
   while (lo < hi) {  // the smallest key above which there is less than what is needed
     const unsigned mid = lo + (hi - lo) / 2;
     if (above(mid) < need) hi = mid;
     else lo = mid + 1;
   }
-  const uint64_t w = weight(value_of(lo), mx, sc, sh.tab);
+  const uint64_t w = weight(value_of(lo), mx, sc, g.sh.tab);
   if (w == 0) return Cut{lo, kFull};  // all of the mass is needed
-  const Cut cut = cut_from(row, lo, (need - above(lo) + w - 1) / w, sh);
+  const Cut cut{lo, nth_equal(row, lo, (need - above(lo) + w - 1) / w, g)};
   return lo == within.key && within.last < cut.last ? within : cut;
 }
 
@@ -440,17 +520,19 @@ __device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings&
   }
 }
 
-// One block per row.  A border (of the k-th logit, or of the share of the mass) is found with a
+// C blocks per row.  A border (of the k-th logit, or of the share of the mass) is found with a
 // histogram of counts, or of masses good to about 1e-5; only the logits of the bins that may hold it
 // are listed and compared one by one, in exact sums.  Should there be too many of them, the
 // border is bisected.
-template <typename T>
+template <typename T, int C>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c) {
   using u64 = unsigned long long;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-  const long long r = blockIdx.x;
-  const Row<T> row(static_cast<const T*>(c.logits) + r * c.p.pitch, c.p.vocab);
+  const long long r = blockIdx.x / C;
+  Group<C> g(sh);
+  Shared* const home = g.of(&sh, 0);  // the first block's, which keeps the list
+  const Row<T, C> row(static_cast<const T*>(c.logits) + r * c.p.pitch, c.p.vocab, g.rank);
   const Exp2Share share_of_table;
   const Settings given = settings_of(c, (int)r);
   const float2 own = row.range();
@@ -463,34 +545,42 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   top = __reduce_max_sync(kFull, sh.ubuf[0][lane]);
   low = __reduce_min_sync(kFull, sh.ubuf[1][lane]);
   __syncthreads();
+  if constexpr (C > 1) {
+    uint64_t each = top, each_low = low, none = 0;
+    g.exchange(each, each_low, none);
+    top = __reduce_max_sync(kFull, lane < C ? (unsigned)each : 0);
+    low = __reduce_min_sync(kFull, lane < C ? (unsigned)each_low : kFull);
+  }
   const float mx = value_of(top);
   if (mx == -INFINITY || s.temp == 0.f) {
     unsigned first = 0;
     row.template each<2>([&](float x, int i) {
       if (x == mx) first = max(first, kFull - (unsigned)i);
     });
-    first = kFull - block_max(first, sh);
-    if (tid == 0) {
+    first = kFull - g.largest(first);
+    if (tid == 0 && g.rank == 0) {
       c.token[r] = mx == -INFINITY ? -1 : (int)first;
       if (c.logprob) c.logprob[r] = mx == -INFINITY ? mx : 0.f;
     }
+    g.leave();
     return;
   }
   if (mx == INFINITY) {  // all weights are 1, of these logits alone
     uint64_t n = 0;
     row.template each<1>([&](float x, int) { n += x == mx; });
-    n = block_sum64(n, sh);
+    n = g.sum(n);
     if (s.top_k > 0 && (uint64_t)s.top_k < n) n = s.top_k;
     if (s.top_p < 1.f) {
       const uint64_t f = fraction(s.top_p > 0.f ? s.top_p : 0.f);
       n = __umul64hi(f, n) + (f * n != 0);
       if (n == 0) n = 1;
     }
-    const unsigned at = nth_equal(row, top, __umul64hi(fraction(s.u), n) + 1, sh);
-    if (tid == 0) {
+    const unsigned at = nth_equal(row, top, __umul64hi(fraction(s.u), n) + 1, g);
+    if (tid == 0 && g.rank == 0) {
       c.token[r] = (int)at;
       if (c.logprob) c.logprob[r] = -logf((float)n);
     }
+    g.leave();
     return;
   }
   const Scale sc = scale_of(s.temp);
@@ -503,10 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     __syncthreads();
   };
   auto list = [&](unsigned key, int i, uint64_t w) {
-    const int n = atomicAdd(&sh.listed, 1);
+    const int n = atomicAdd(&home->listed, 1);
     if (n < kList) {
-      sh.order[n] = (uint64_t)key << 32 | (kFull - (unsigned)i);
-      sh.w[n] = w;
+      home->order[n] = (uint64_t)key << 32 | (kFull - (unsigned)i);
+      home->w[n] = w;
     }
   };
   // the row's order, by key, falling, then by index, as one number that falls
@@ -521,47 +611,57 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
       const float y = bins.place(x);
       if (bins.inside(y)) atomicAdd(sh.bins + bins.number(bins.bin(y)), 1u);
     });
-    __syncthreads();
-    const unsigned c0 = sh.bins[2 * tid], c1 = sh.bins[2 * tid + 1];
+    g.sync();
+    unsigned c0 = 0, c1 = 0;
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      const uint2 n = *reinterpret_cast<const uint2*>(g.of(sh.bins + 2 * tid, q));
+      c0 += n.x;
+      c1 += n.y;
+    }
     unsigned total;
     const unsigned before = block_before(c0 + c1, sh.ubuf[0], &total);
     if (total > k) {  // (else the k-th has less than 2^-40)
-      if (before < k && k <= before + c0) sh.first = 2 * tid, sh.last = before;
-      else if (before + c0 < k && k <= before + c0 + c1) sh.first = 2 * tid + 1, sh.last = before + c0;
+      if (before < k && k <= before + c0) sh.first = 2 * tid, sh.last = before, sh.found = c0;
+      else if (before + c0 < k && k <= before + c0 + c1) sh.first = 2 * tid + 1, sh.last = before + c0, sh.found = c1;
       __syncthreads();
       const int bin = sh.first;
       some_cut = true;
-      const unsigned above = sh.last;
+      const unsigned above = sh.last, in_bin = sh.found;
       const float wanted = 12582912.f + bin;
-      if (above + sh.bins[bin] <= kShort) {  // all that may be kept fits a short list
+      if (above + in_bin <= kShort) {  // all that may be kept fits a short list
         row.template each<2>([&](float x, int i) {
           if (bins.bin(bins.place(x)) <= wanted) list(key_of(x), i, weight(x, mx, sc, sh.tab));
         });
-        __syncthreads();
-        draw_listed(c, s, r, least, sh);
+        g.sync();
+        if (g.rank == 0) draw_listed(c, s, r, least, sh);
         return;
       }
-      if (sh.bins[bin] <= kList) {
+      if (in_bin <= kList) {
         row.template each<2>([&](float x, int i) {
           if (bins.bin(bins.place(x)) == wanted) list(key_of(x), i, 0);
         });
-        __syncthreads();
-        const int n = sh.listed;
-        uint64_t last = ~0ull;
-        if (tid < n) {
-          const uint64_t mine = sh.order[tid];
-          unsigned rank = above;
-          for (int j = 0; j < n; ++j) rank += sh.order[j] > mine;
-          if (rank < k) last = mine;
+        g.sync();
+        if (g.rank == 0) {
+          const int n = sh.listed;
+          uint64_t last = ~0ull;
+          if (tid < n) {
+            const uint64_t mine = sh.order[tid];
+            unsigned rank = above;
+            for (int j = 0; j < n; ++j) rank += sh.order[j] > mine;
+            if (rank < k) last = mine;
+          }
+          last = block_min64(last, sh);
+          if (tid == 0) sh.answer = last;
         }
-        cut = cut_at(block_min64(last, sh));
+        g.sync();
+        cut = cut_at(home->answer);
       } else {
-        cut = bisect_count(row, low, top, k, sh);
-        __syncthreads();
+        cut = bisect_count(row, low, top, k, g);
         sh.mass[tid] = 0;
-        __syncthreads();
       }
     }
+    g.sync();  // all are through with the bins and the list
   }
 
   if (s.top_p < 1.f) {
@@ -573,9 +673,16 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
       const float b = bins.bin(y), q = ptx::ex2_approx(fmaf(__fsub_rn(b, 12582912.f) - y, bins.log2_step, 18.f));
       atomicAdd(sh.bins + bins.number(b), (unsigned)(__float_as_int(q + 8388608.f) - 0x4b000000));
     });
-    __syncthreads();
-    const float m0 = (float)sh.bins[2 * tid] * ptx::ex2_approx((float)(-2 * tid) * bins.log2_step);
-    const float m1 = (float)sh.bins[2 * tid + 1] * ptx::ex2_approx((float)(-2 * tid - 1) * bins.log2_step);
+    g.sync();
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      const uint2 n = *reinterpret_cast<const uint2*>(g.of(sh.bins + 2 * tid, q));
+      m0 += (float)n.x;
+      m1 += (float)n.y;
+    }
+    m0 *= ptx::ex2_approx((float)(-2 * tid) * bins.log2_step);
+    m1 *= ptx::ex2_approx((float)(-2 * tid - 1) * bins.log2_step);
     float all;
     const float before = block_before(m0 + m1, sh.fbuf, &all);
     const float share = s.top_p > 0.f ? s.top_p : 0.f, from = share * all * (1.f - 3e-5f), to = share * all * (1.f + 3e-5f);
@@ -602,29 +709,43 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
       return 0;
     });
     sure += small;
+    uint64_t unused = 0;
     __syncthreads();
-    const int n = sh.listed;
-    uint64_t listed = tid < n && n <= kList ? sh.w[tid] : 0;
-    block_sum64(rest, sure, listed, sh);
+    block_sum64(rest, sure, unused, sh);
+    if constexpr (C > 1) {
+      g.exchange(rest, sure, unused);
+      rest = warp_sum64(rest);
+      sure = warp_sum64(sure);
+    }
     const uint64_t mass = sure + rest;
     const uint64_t p = fraction(share);
     uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
     if (need == 0) need = 1;
-    if (n <= kList && sure < need && sure + listed >= need) {
+    if (g.rank == 0) {  // the list; its kept entries join their spans
+      const int n = sh.listed;
+      const uint64_t listed = block_sum64(tid < n && n <= kList ? sh.w[tid] : 0, sh);
       uint64_t order = ~0ull;
-      if (tid < n) {
-        const uint64_t mine = sh.order[tid];
-        uint64_t g = sure;
-        for (int j = 0; j < n; ++j) g += sh.order[j] > mine ? sh.w[j] : 0;
-        if (g < need) {
-          order = mine;
-          if (sh.w[tid] >= least) atomicAdd((u64*)sh.mass + row.span_of(kFull - (unsigned)mine), (u64)sh.w[tid]);
+      if (n <= kList && sure < need && sure + listed >= need) {
+        if (tid < n) {
+          const uint64_t mine = sh.order[tid];
+          uint64_t before = sure;
+          for (int j = 0; j < n; ++j) before += sh.order[j] > mine ? sh.w[j] : 0;
+          if (before < need) {
+            const int i = kFull - (unsigned)mine;
+            order = mine;
+            if (sh.w[tid] >= least) atomicAdd((u64*)g.of(sh.mass, row.owner(i)) + row.span_of(i), (u64)sh.w[tid]);
+          }
         }
+        order = block_min64(order, sh);
       }
-      cut = cut_at(block_min64(order, sh));
+      if (tid == 0) sh.answer = order;
+    }
+    g.sync();
+    const uint64_t order = home->answer;
+    if (order != ~0ull) {
+      cut = cut_at(order);
     } else {
-      cut = bisect_mass(row, max(low, cut.key), top, cut, need, mx, sc, sh);
-      __syncthreads();
+      cut = bisect_mass(row, max(low, cut.key), top, cut, need, mx, sc, g);
       sh.mass[tid] = 0;
       __syncthreads();
       row.sum_spans(sh.mass, [&](float x, int i) {
@@ -642,14 +763,24 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
 
   // the span that holds the token, then the token
   uint64_t total;
-  const uint64_t mine = sh.mass[tid], before = block_before(mine, sh.buf, &total);
+  const uint64_t mine = sh.mass[tid];
+  uint64_t before = block_before(mine, sh.buf, &total);
+  if (tid == 0) sh.first = -1;
+  if constexpr (C > 1) {
+    uint64_t each = total, none = 0, more = 0;
+    g.exchange(each, none, more);
+    before += warp_sum64(lane < (int)g.rank ? each : 0);
+    total = warp_sum64(each);
+  }
+  __syncthreads();
   const uint64_t target = __umul64hi(fraction(s.u), total);  // the token is the first to pass it
   if (before <= target && target < before + mine) {
     sh.first = tid;
     sh.rest = target - before;
   }
   __syncthreads();
-  if (warp != 0) return;
+  g.leave();
+  if (warp != 0 || sh.first < 0) return;
   const uint64_t rest = sh.rest;
   const int2 span = row.span(sh.first);
   const int per = (span.y - span.x + 31) / 32, from = span.x + lane * per, to = min(span.y, from + per);
@@ -679,12 +810,36 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   }
 }
 
+template <typename T, int C>
+cudaError_t sample_in(const SampleCall& c, cudaStream_t s) {
+  if (c.p.rows > (int)((1u << 31) - 1) / C) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c.p.rows * C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, C>, c);
+}
+
+// Blocks of a row: as many as leave every SM a block, while each still has a vector a thread.
+template <typename T>
+cudaError_t sample_t(const SampleCall& c, cudaStream_t s) {
+  const int sms = serve_sm_count(), vectors = c.p.vocab / Wide<T>::E;
+  int blocks = 1;
+  while (blocks < 8 && c.p.rows <= sms / (2 * blocks) && vectors >= 2 * blocks * (kThreads / 2)) blocks *= 2;
+  return blocks == 8 ? sample_in<T, 8>(c, s) : blocks == 4 ? sample_in<T, 4>(c, s)
+       : blocks == 2 ? sample_in<T, 2>(c, s) : sample_in<T, 1>(c, s);
+}
+
 }  // namespace
 
 cudaError_t launch_sample(const SampleCall& c, cudaStream_t s) {
-  if (c.p.dtype == TG_F32) sample_kernel<float><<<c.p.rows, kThreads, 0, s>>>(c);
-  else sample_kernel<__nv_bfloat16><<<c.p.rows, kThreads, 0, s>>>(c);
-  return cudaGetLastError();
+  return c.p.dtype == TG_F32 ? sample_t<float>(c, s) : sample_t<__nv_bfloat16>(c, s);
 }
 
 }  // namespace tg
