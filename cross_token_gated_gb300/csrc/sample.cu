@@ -19,7 +19,7 @@
 namespace tg {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kUnit = 44;                      // a weight of 1 is 2^44
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -84,7 +84,7 @@ __device__ __forceinline__ float value_of(unsigned key) {
 
 // --------------------------------------------------------------------------- reductions
 
-constexpr int kBins = 2 * kThreads, kList = 1024, kSpans = kThreads;
+constexpr int kBins = 2 * kThreads, kList = kThreads, kSpans = kThreads;
 constexpr int kShort = 256;  // a list that is gone through twice per entry
 
 struct Shared {
@@ -109,16 +109,13 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   const unsigned lo = __reduce_add_sync(kFull, (unsigned)v & 0x3fffffu), mid = __reduce_add_sync(kFull, (unsigned)(v >> 22) & 0x3fffffu);
   return lo + ((uint64_t)mid << 22) + ((uint64_t)__reduce_add_sync(kFull, (unsigned)(v >> 44)) << 44);
 }
-__device__ __forceinline__ uint64_t warp_min64(uint64_t v) {
-  const unsigned hi = __reduce_min_sync(kFull, (unsigned)(v >> 32));
-  return (uint64_t)hi << 32 | __reduce_min_sync(kFull, (unsigned)(v >> 32) == hi ? (unsigned)v : kFull);
-}
 // Over the block, for every thread; the barrier at the end frees the buffer again.
 __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
   v = warp_sum64(v);
   if ((threadIdx.x & 31) == 0) sh.buf[threadIdx.x / 32] = v;
   __syncthreads();
-  v = warp_sum64(sh.buf[threadIdx.x & 31]);
+  const int lane = threadIdx.x & 31;
+  v = warp_sum64(lane < kWarps ? sh.buf[lane] : 0);
   __syncthreads();
   return v;
 }
@@ -135,19 +132,11 @@ __device__ __forceinline__ void block_sum64(uint64_t& a, uint64_t& b, uint64_t& 
   c = warp_sum64(lane < kWarps ? sh.buf3[lane] : 0);
   __syncthreads();
 }
-__device__ __forceinline__ uint64_t block_min64(uint64_t v, Shared& sh) {
-  v = warp_min64(v);
-  if ((threadIdx.x & 31) == 0) sh.buf[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = warp_min64(sh.buf[threadIdx.x & 31]);
-  __syncthreads();
-  return v;
-}
 __device__ __forceinline__ unsigned block_max(unsigned v, Shared& sh) {
   v = __reduce_max_sync(kFull, v);
   if ((threadIdx.x & 31) == 0) sh.ubuf[0][threadIdx.x / 32] = v;
   __syncthreads();
-  v = __reduce_max_sync(kFull, sh.ubuf[0][threadIdx.x & 31]);
+  v = __reduce_max_sync(kFull, sh.ubuf[0][threadIdx.x & (kWarps - 1)]);
   __syncthreads();
   return v;
 }
@@ -165,9 +154,9 @@ __device__ __forceinline__ N block_before(N v, N* buf, N* total) {
   const N incl = scan(v);
   if (lane == 31) buf[warp] = incl;
   __syncthreads();
-  const N warps = scan(buf[lane]);
+  const N warps = scan(buf[lane & (kWarps - 1)]);  // (lanes past the warps are not looked at)
   const N before = __shfl_sync(kFull, warps, (warp + 31) & 31);
-  *total = __shfl_sync(kFull, warps, 31);
+  *total = __shfl_sync(kFull, warps, kWarps - 1);
   __syncthreads();
   return (warp ? before : N(0)) + incl - v;
 }
@@ -525,7 +514,7 @@ __device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings&
 // are listed and compared one by one, in exact sums.  Should there be too many of them, the
 // border is bisected.
 template <typename T, int C>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c) {
   using u64 = unsigned long long;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -542,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   unsigned top = __reduce_max_sync(kFull, key_of(own.x)), low = __reduce_min_sync(kFull, key_of(own.y));
   if (lane == 0) sh.ubuf[0][warp] = top, sh.ubuf[1][warp] = low;
   __syncthreads();
-  top = __reduce_max_sync(kFull, sh.ubuf[0][lane]);
-  low = __reduce_min_sync(kFull, sh.ubuf[1][lane]);
+  top = __reduce_max_sync(kFull, sh.ubuf[0][lane & (kWarps - 1)]);
+  low = __reduce_min_sync(kFull, sh.ubuf[1][lane & (kWarps - 1)]);
   __syncthreads();
   if constexpr (C > 1) {
     uint64_t each = top, each_low = low, none = 0;
@@ -589,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   const bool some_least = least > 0;
   auto clear_bins = [&] {
     sh.bins[tid] = sh.bins[tid + kThreads] = 0;
-    if (tid == 0) sh.listed = 0;
+    if (tid == 0) sh.listed = 0, sh.answer = ~0ull;
     __syncthreads();
   };
   auto list = [&](unsigned key, int i, uint64_t w) {
@@ -642,17 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
           if (bins.bin(bins.place(x)) == wanted) list(key_of(x), i, 0);
         });
         g.sync();
-        if (g.rank == 0) {
+        if (g.rank == 0 && tid < sh.listed) {
           const int n = sh.listed;
-          uint64_t last = ~0ull;
-          if (tid < n) {
-            const uint64_t mine = sh.order[tid];
-            unsigned rank = above;
-            for (int j = 0; j < n; ++j) rank += sh.order[j] > mine;
-            if (rank < k) last = mine;
-          }
-          last = block_min64(last, sh);
-          if (tid == 0) sh.answer = last;
+          const uint64_t mine = sh.order[tid];
+          unsigned rank = above + 1;
+          for (int j = 0; j < n; ++j) rank += sh.order[j] > mine;
+          if (rank == k) sh.answer = mine;
         }
         g.sync();
         cut = cut_at(home->answer);
@@ -691,7 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     const unsigned t = __reduce_min_sync(kFull, before + m0 >= to ? b0 : before + m0 + m1 >= to ? b0 + 1 : none);
     if (lane == 0) sh.ubuf[0][warp] = f, sh.ubuf[1][warp] = t;
     __syncthreads();
-    const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane]), last = __reduce_min_sync(kFull, sh.ubuf[1][lane]);
+    const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane & (kWarps - 1)]);
+    const int last = __reduce_min_sync(kFull, sh.ubuf[1][lane & (kWarps - 1)]);
     // exact sums of everything and of the bins before; the bins between are listed
     uint64_t rest = 0, small = 0;  // mass from the first listed bin on, and of what min_p drops before it
     const float first_bin = 12582912.f + first, last_bin = 12582912.f + last;
@@ -721,24 +706,17 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
     const uint64_t p = fraction(share);
     uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
     if (need == 0) need = 1;
-    if (g.rank == 0) {  // the list; its kept entries join their spans
+    if (g.rank == 0 && sh.listed <= kList && tid < sh.listed && sure < need) {
+      // the list: its kept entries join their spans, the last of them is the cut
       const int n = sh.listed;
-      const uint64_t listed = block_sum64(tid < n && n <= kList ? sh.w[tid] : 0, sh);
-      uint64_t order = ~0ull;
-      if (n <= kList && sure < need && sure + listed >= need) {
-        if (tid < n) {
-          const uint64_t mine = sh.order[tid];
-          uint64_t before = sure;
-          for (int j = 0; j < n; ++j) before += sh.order[j] > mine ? sh.w[j] : 0;
-          if (before < need) {
-            const int i = kFull - (unsigned)mine;
-            order = mine;
-            if (sh.w[tid] >= least) atomicAdd((u64*)g.of(sh.mass, row.owner(i)) + row.span_of(i), (u64)sh.w[tid]);
-          }
-        }
-        order = block_min64(order, sh);
+      const uint64_t mine = sh.order[tid], w = sh.w[tid];
+      uint64_t before = sure;
+      for (int j = 0; j < n; ++j) before += sh.order[j] > mine ? sh.w[j] : 0;
+      if (before < need) {
+        const int i = kFull - (unsigned)mine;
+        if (w >= least) atomicAdd((u64*)g.of(sh.mass, row.owner(i)) + row.span_of(i), (u64)w);
+        if (before + w >= need) sh.answer = mine;
       }
-      if (tid == 0) sh.answer = order;
     }
     g.sync();
     const uint64_t order = home->answer;
@@ -784,14 +762,18 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   const uint64_t rest = sh.rest;
   const int2 span = row.span(sh.first);
   const int per = (span.y - span.x + 31) / 32, from = span.x + lane * per, to = min(span.y, from + per);
-  auto kept_weight = [&](int i) {
+  auto kept_weight = [&](int i) -> uint64_t {
+    if (i >= to) return 0;
     const float x = row.at(i);
     const uint64_t w = cut.keeps(key_of(x), i) ? weight(x, mx, sc, sh.tab) : 0;
     return w < least ? 0 : w;
   };
-  uint64_t own_mass = 0;
-#pragma unroll 4
-  for (int i = from; i < to; ++i) own_mass += kept_weight(i);
+  // (a span of 32 vectors and edges: at most 9 of a lane)
+  constexpr int kHeld = Wide<T>::E + 1;
+  uint64_t held[kHeld], own_mass = 0;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) own_mass += held[k] = kept_weight(from + k);
+  for (int i = from + kHeld; i < to; ++i) own_mass += kept_weight(i);
   uint64_t incl = own_mass;
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t up = __shfl_up_sync(kFull, incl, o);
@@ -799,15 +781,20 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleCall c)
   }
   const unsigned hit = __ballot_sync(kFull, incl > rest);
   if (lane != __ffs(hit) - 1) return;
-  uint64_t sum = incl - own_mass;
-  for (int i = from; i < to; ++i) {
+  uint64_t sum = incl - own_mass, drawn = 0;
+  int token = -1;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    sum += held[k];
+    if (token < 0 && sum > rest) token = from + k, drawn = held[k];
+  }
+  for (int i = from + kHeld; token < 0 && i < to; ++i) {
     const uint64_t w = kept_weight(i);
     sum += w;
-    if (sum <= rest) continue;
-    c.token[r] = i;
-    if (c.logprob) c.logprob[r] = w == total ? 0.f : logf((float)w / (float)total);
-    return;
+    if (sum > rest) token = i, drawn = w;
   }
+  c.token[r] = token;
+  if (c.logprob) c.logprob[r] = drawn == total ? 0.f : logf((float)drawn / (float)total);
 }
 
 template <typename T, int C>
@@ -826,12 +813,12 @@ cudaError_t sample_in(const SampleCall& c, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, sample_kernel<T, C>, c);
 }
 
-// Blocks of a row: as many as leave every SM a block, while each still has a vector a thread.
+// Blocks of a row: as many as the SMs hold two of at once, while each still has a vector a thread.
 template <typename T>
 cudaError_t sample_t(const SampleCall& c, cudaStream_t s) {
   const int sms = serve_sm_count(), vectors = c.p.vocab / Wide<T>::E;
   int blocks = 1;
-  while (blocks < 8 && c.p.rows <= sms / (2 * blocks) && vectors >= 2 * blocks * (kThreads / 2)) blocks *= 2;
+  while (blocks < 8 && c.p.rows <= sms / blocks && vectors >= 2 * blocks * kThreads) blocks *= 2;
   return blocks == 8 ? sample_in<T, 8>(c, s) : blocks == 4 ? sample_in<T, 4>(c, s)
        : blocks == 2 ? sample_in<T, 2>(c, s) : sample_in<T, 1>(c, s);
 }
