@@ -19,7 +19,11 @@
 namespace tg {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+// Threads of one of the C blocks that share a row.  A row by itself wants all the warps an SM takes at
+// 64 registers (256 rows of 32,768: 36 us, with 512 threads 43 us); shares of rows are passed
+// more quickly through the barriers of half as many (one row by 8 blocks: 16.6 us, 20.7 us).
+template <int C> constexpr int kThreads = C == 1 ? 1024 : 512;
+template <int C> constexpr int kWarps = kThreads<C> / 32;
 constexpr int kUnit = 44;                      // a weight of 1 is 2^44
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -84,20 +88,23 @@ __device__ __forceinline__ float value_of(unsigned key) {
 
 // --------------------------------------------------------------------------- reductions
 
-constexpr int kBins = 2 * kThreads, kList = kThreads, kSpans = kThreads;
+template <int C> constexpr int kBins = 2 * kThreads<C>;
+template <int C> constexpr int kList = kThreads<C>;
+template <int C> constexpr int kSpans = kThreads<C>;
 constexpr int kShort = 256;  // a list that is gone through twice per entry
 
+template <int C>
 struct Shared {
   Exp2Table tab;
-  uint64_t mass[kSpans];     // kept mass of the row's spans
-  unsigned bins[kBins];
-  uint64_t order[kList];     // the logits of the bins that hold a border: a number that falls along
+  uint64_t mass[kSpans<C>];     // kept mass of the row's spans
+  unsigned bins[kBins<C>];
+  uint64_t order[kList<C>];     // the logits of the bins that hold a border: a number that falls along
                              // the row's order, (key, ~index)
-  uint64_t w[kList];
+  uint64_t w[kList<C>];
   int listed;
-  uint64_t buf[kWarps], buf2[kWarps], buf3[kWarps];
-  unsigned ubuf[2][kWarps];
-  float fbuf[kWarps];
+  uint64_t buf[kWarps<C>], buf2[kWarps<C>], buf3[kWarps<C>];
+  unsigned ubuf[2][kWarps<C>];
+  float fbuf[kWarps<C>];
   int first, last, found;
   uint64_t rest;
   uint64_t given[2][3];      // what the cluster's blocks tell each other, in turn
@@ -110,38 +117,41 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   return lo + ((uint64_t)mid << 22) + ((uint64_t)__reduce_add_sync(kFull, (unsigned)(v >> 44)) << 44);
 }
 // Over the block, for every thread; the barrier at the end frees the buffer again.
-__device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
+template <int C>
+__device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared<C>& sh) {
   v = warp_sum64(v);
   if ((threadIdx.x & 31) == 0) sh.buf[threadIdx.x / 32] = v;
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  v = warp_sum64(lane < kWarps ? sh.buf[lane] : 0);
+  v = warp_sum64(lane < kWarps<C> ? sh.buf[lane] : 0);
   __syncthreads();
   return v;
 }
 // Three at once.
-__device__ __forceinline__ void block_sum64(uint64_t& a, uint64_t& b, uint64_t& c, Shared& sh) {
+template <int C>
+__device__ __forceinline__ void block_sum64(uint64_t& a, uint64_t& b, uint64_t& c, Shared<C>& sh) {
   a = warp_sum64(a);
   b = warp_sum64(b);
   c = warp_sum64(c);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   if (lane == 0) sh.buf[warp] = a, sh.buf2[warp] = b, sh.buf3[warp] = c;
   __syncthreads();
-  a = warp_sum64(lane < kWarps ? sh.buf[lane] : 0);
-  b = warp_sum64(lane < kWarps ? sh.buf2[lane] : 0);
-  c = warp_sum64(lane < kWarps ? sh.buf3[lane] : 0);
+  a = warp_sum64(lane < kWarps<C> ? sh.buf[lane] : 0);
+  b = warp_sum64(lane < kWarps<C> ? sh.buf2[lane] : 0);
+  c = warp_sum64(lane < kWarps<C> ? sh.buf3[lane] : 0);
   __syncthreads();
 }
-__device__ __forceinline__ unsigned block_max(unsigned v, Shared& sh) {
+template <int C>
+__device__ __forceinline__ unsigned block_max(unsigned v, Shared<C>& sh) {
   v = __reduce_max_sync(kFull, v);
   if ((threadIdx.x & 31) == 0) sh.ubuf[0][threadIdx.x / 32] = v;
   __syncthreads();
-  v = __reduce_max_sync(kFull, sh.ubuf[0][threadIdx.x & (kWarps - 1)]);
+  v = __reduce_max_sync(kFull, sh.ubuf[0][threadIdx.x & (kWarps<C> - 1)]);
   __syncthreads();
   return v;
 }
 // Sum over the threads before this one, and over all.
-template <typename N>
+template <int C, typename N>
 __device__ __forceinline__ N block_before(N v, N* buf, N* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   auto scan = [lane](N x) {
@@ -154,9 +164,9 @@ __device__ __forceinline__ N block_before(N v, N* buf, N* total) {
   const N incl = scan(v);
   if (lane == 31) buf[warp] = incl;
   __syncthreads();
-  const N warps = scan(buf[lane & (kWarps - 1)]);  // (lanes past the warps are not looked at)
+  const N warps = scan(buf[lane & (kWarps<C> - 1)]);  // (lanes past the warps are not looked at)
   const N before = __shfl_sync(kFull, warps, (warp + 31) & 31);
-  *total = __shfl_sync(kFull, warps, kWarps - 1);
+  *total = __shfl_sync(kFull, warps, kWarps<C> - 1);
   __syncthreads();
   return (warp ? before : N(0)) + incl - v;
 }
@@ -165,10 +175,10 @@ __device__ __forceinline__ N block_before(N v, N* buf, N* total) {
 // same in all threads of all blocks.
 template <int C>
 struct Group {
-  Shared& sh;
+  Shared<C>& sh;
   unsigned rank;
   int turn = 0;
-  __device__ __forceinline__ explicit Group(Shared& s) : sh(s), rank(0) {
+  __device__ __forceinline__ explicit Group(Shared<C>& s) : sh(s), rank(0) {
     if constexpr (C > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   }
   __device__ __forceinline__ void sync() const {
@@ -258,7 +268,7 @@ template <> struct Wide<__nv_bfloat16> {
 
 // A block's part of the row as 16-byte vectors, with the elements before the first and after the
 // last one of the row by themselves; it is read again in every pass, from L1 or L2.  32 vectors
-// that a warp reads at once are a span; `wide` doublings of that keep their number within kSpans.
+// that a warp reads at once are a span; `wide` doublings of that keep their number within kSpans<C>.
 template <typename T, int C>
 struct Row {
   static constexpr int E = Wide<T>::E;
@@ -275,7 +285,7 @@ struct Row {
     head = rank == 0 ? lead : 0;
     edge = head + (rank == C - 1 ? vocab - lead - all * E : 0);
     wide = 0;
-    while ((per >> 5 >> wide) >= kSpans) ++wide;
+    while ((per >> 5 >> wide) >= kSpans<C>) ++wide;
   }
   __device__ __forceinline__ float at(int i) const { return io<T>::ld(x + i); }
   __device__ __forceinline__ int edge_index(int t) const { return t < head ? t : lead + all * E + t - head; }
@@ -305,7 +315,7 @@ struct Row {
     }
     const uint4* v = reinterpret_cast<const uint4*>(x + lead) + v0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < nvec; i += kThreads) Wide<T>::range(__ldg(v + i), top, low);
+    for (int i = threadIdx.x; i < nvec; i += kThreads<C>) Wide<T>::range(__ldg(v + i), top, low);
     return make_float2(top, low);
   }
   // f(value, index) for the thread's elements
@@ -318,18 +328,18 @@ struct Row {
     }
     const uint4* v = reinterpret_cast<const uint4*>(x + lead) + v0;
 #pragma unroll 1
-    for (int b = tid; b < nvec; b += U * kThreads) {
+    for (int b = tid; b < nvec; b += U * kThreads<C>) {
       uint4 u[U];
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (b + k * kThreads < nvec) u[k] = __ldg(v + b + k * kThreads);
+        if (b + k * kThreads<C> < nvec) u[k] = __ldg(v + b + k * kThreads<C>);
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        if (b + k * kThreads >= nvec) break;
+        if (b + k * kThreads<C> >= nvec) break;
         float e[E];
         Wide<T>::unpack(u[k], e);
 #pragma unroll
-        for (int j = 0; j < E; ++j) f(e[j], index(b + k * kThreads) + j);
+        for (int j = 0; j < E; ++j) f(e[j], index(b + k * kThreads<C>) + j);
       }
     }
   }
@@ -347,7 +357,7 @@ struct Row {
     }
     const uint4* v = reinterpret_cast<const uint4*>(x + lead) + v0;
 #pragma unroll 1
-    for (int b = tid & ~31; b < nvec; b += kThreads) {
+    for (int b = tid & ~31; b < nvec; b += kThreads<C>) {
       const int i = b + (tid & 31);
       uint64_t w = 0;
       if (i < nvec) {
@@ -390,17 +400,18 @@ __device__ __forceinline__ uint64_t fraction(float u) { return (uint64_t)(u * 18
 
 // Bins of a row: equal steps of the logits from the largest one down to 2^-40 of its weight, or to
 // the lowest logit.
+template <int C>
 struct Bins {
   float mx, per_unit, log2_step;
   __device__ __forceinline__ Bins(float mx_, float low, float temp, Scale sc) : mx(mx_) {
     // 27.8 > 40 ln 2; logits that differ by less than 1e-30 may share a bin
     const float reach = fmaxf(fminf(27.8f * temp, __fsub_rn(mx, low)), 1e-30f);
-    per_unit = __fdiv_rn(kBins - 1, reach);
+    per_unit = __fdiv_rn(kBins<C> - 1, reach);
     log2_step = sc.hi / per_unit;
   }
-  // distance from the largest in bins; outside where it is not below kBins - 0.5 (NaN too)
+  // distance from the largest in bins; outside where it is not below kBins<C> - 0.5 (NaN too)
   __device__ __forceinline__ float place(float x) const { return __fmul_rn(__fsub_rn(mx, x), per_unit); }
-  static __device__ __forceinline__ bool inside(float y) { return y < kBins - 0.5f; }
+  static __device__ __forceinline__ bool inside(float y) { return y < kBins<C> - 0.5f; }
   // the nearest bin as 1.5 2^23 + bin: its low bits are the number
   static __device__ __forceinline__ float bin(float y) { return __fadd_rn(y, 12582912.f); }
   static __device__ __forceinline__ int number(float b) { return __float_as_int(b) - 0x4b400000; }
@@ -410,7 +421,7 @@ struct Bins {
 // fewer.  Overwrites sh.mass.
 template <typename T, int C>
 __device__ __noinline__ unsigned nth_equal(const Row<T, C>& row, unsigned key, uint64_t m, Group<C>& g) {
-  Shared& sh = g.sh;
+  Shared<C>& sh = g.sh;
   sh.mass[threadIdx.x] = 0;
   if (threadIdx.x == 0) sh.found = 0;
   __syncthreads();
@@ -418,7 +429,7 @@ __device__ __noinline__ unsigned nth_equal(const Row<T, C>& row, unsigned key, u
   __syncthreads();
   uint64_t total;
   const uint64_t mine = sh.mass[threadIdx.x];
-  uint64_t before = block_before(mine, sh.buf, &total);
+  uint64_t before = block_before<C>(mine, sh.buf, &total);
   if constexpr (C > 1) {
     uint64_t each = total, none = 0, more = 0;
     g.exchange(each, none, more);
@@ -476,7 +487,8 @@ __device__ __noinline__ Cut bisect_mass(const Row<T, C>& row, unsigned lo, unsig
 }
 
 // The token of a row from its list, which holds all of the top_k logits.
-__device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings& s, long long r, uint64_t least, Shared& sh) {
+template <int C>
+__device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings& s, long long r, uint64_t least, Shared<C>& sh) {
   const int tid = threadIdx.x, n = sh.listed;
   uint64_t mine = 0, w = 0, before = 0;
   unsigned rank = 0;
@@ -514,13 +526,13 @@ __device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings&
 // are listed and compared one by one, in exact sums.  Should there be too many of them, the
 // border is bisected.
 template <typename T, int C>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c) {
+__global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel(const SampleCall c) {
   using u64 = unsigned long long;
-  __shared__ Shared sh;
+  __shared__ Shared<C> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const long long r = blockIdx.x / C;
   Group<C> g(sh);
-  Shared* const home = g.of(&sh, 0);  // the first block's, which keeps the list
+  Shared<C>* const home = g.of(&sh, 0);  // the first block's, which keeps the list
   const Row<T, C> row(static_cast<const T*>(c.logits) + r * c.p.pitch, c.p.vocab, g.rank);
   const Exp2Share share_of_table;
   const Settings given = settings_of(c, (int)r);
@@ -531,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
   unsigned top = __reduce_max_sync(kFull, key_of(own.x)), low = __reduce_min_sync(kFull, key_of(own.y));
   if (lane == 0) sh.ubuf[0][warp] = top, sh.ubuf[1][warp] = low;
   __syncthreads();
-  top = __reduce_max_sync(kFull, sh.ubuf[0][lane & (kWarps - 1)]);
-  low = __reduce_min_sync(kFull, sh.ubuf[1][lane & (kWarps - 1)]);
+  top = __reduce_max_sync(kFull, sh.ubuf[0][lane & (kWarps<C> - 1)]);
+  low = __reduce_min_sync(kFull, sh.ubuf[1][lane & (kWarps<C> - 1)]);
   __syncthreads();
   if constexpr (C > 1) {
     uint64_t each = top, each_low = low, none = 0;
@@ -573,17 +585,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
     return;
   }
   const Scale sc = scale_of(s.temp);
-  const Bins bins(mx, value_of(low), s.temp, sc);
+  const Bins<C> bins(mx, value_of(low), s.temp, sc);
   const uint64_t least = s.min_p > 0.f ? (uint64_t)ceilf(s.min_p * 17592186044416.f) : 0;  // 2^44
   const bool some_least = least > 0;
   auto clear_bins = [&] {
-    sh.bins[tid] = sh.bins[tid + kThreads] = 0;
+    sh.bins[tid] = sh.bins[tid + kThreads<C>] = 0;
     if (tid == 0) sh.listed = 0, sh.answer = ~0ull;
     __syncthreads();
   };
   auto list = [&](unsigned key, int i, uint64_t w) {
     const int n = atomicAdd(&home->listed, 1);
-    if (n < kList) {
+    if (n < kList<C>) {
       home->order[n] = (uint64_t)key << 32 | (kFull - (unsigned)i);
       home->w[n] = w;
     }
@@ -609,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
       c1 += n.y;
     }
     unsigned total;
-    const unsigned before = block_before(c0 + c1, sh.ubuf[0], &total);
+    const unsigned before = block_before<C>(c0 + c1, sh.ubuf[0], &total);
     if (total > k) {  // (else the k-th has less than 2^-40)
       if (before < k && k <= before + c0) sh.first = 2 * tid, sh.last = before, sh.found = c0;
       else if (before + c0 < k && k <= before + c0 + c1) sh.first = 2 * tid + 1, sh.last = before + c0, sh.found = c1;
@@ -626,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         if (g.rank == 0) draw_listed(c, s, r, least, sh);
         return;
       }
-      if (in_bin <= kList) {
+      if (in_bin <= kList<C>) {
         row.template each<2>([&](float x, int i) {
           if (bins.bin(bins.place(x)) == wanted) list(key_of(x), i, 0);
         });
@@ -668,15 +680,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
     m0 *= ptx::ex2_approx((float)(-2 * tid) * bins.log2_step);
     m1 *= ptx::ex2_approx((float)(-2 * tid - 1) * bins.log2_step);
     float all;
-    const float before = block_before(m0 + m1, sh.fbuf, &all);
+    const float before = block_before<C>(m0 + m1, sh.fbuf, &all);
     const float share = s.top_p > 0.f ? s.top_p : 0.f, from = share * all * (1.f - 3e-5f), to = share * all * (1.f + 3e-5f);
-    const unsigned b0 = 2 * tid, none = kBins - 1;
+    const unsigned b0 = 2 * tid, none = kBins<C> - 1;
     const unsigned f = __reduce_min_sync(kFull, before + m0 >= from ? b0 : before + m0 + m1 >= from ? b0 + 1 : none);
     const unsigned t = __reduce_min_sync(kFull, before + m0 >= to ? b0 : before + m0 + m1 >= to ? b0 + 1 : none);
     if (lane == 0) sh.ubuf[0][warp] = f, sh.ubuf[1][warp] = t;
     __syncthreads();
-    const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane & (kWarps - 1)]);
-    const int last = __reduce_min_sync(kFull, sh.ubuf[1][lane & (kWarps - 1)]);
+    const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane & (kWarps<C> - 1)]);
+    const int last = __reduce_min_sync(kFull, sh.ubuf[1][lane & (kWarps<C> - 1)]);
     // exact sums of everything and of the bins before; the bins between are listed
     uint64_t rest = 0, small = 0;  // mass from the first listed bin on, and of what min_p drops before it
     const float first_bin = 12582912.f + first, last_bin = 12582912.f + last;
@@ -706,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
     const uint64_t p = fraction(share);
     uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
     if (need == 0) need = 1;
-    if (g.rank == 0 && sh.listed <= kList && tid < sh.listed && sure < need) {
+    if (g.rank == 0 && sh.listed <= kList<C> && tid < sh.listed && sure < need) {
       // the list: its kept entries join their spans, the last of them is the cut
       const int n = sh.listed;
       const uint64_t mine = sh.order[tid], w = sh.w[tid];
@@ -742,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
   // the span that holds the token, then the token
   uint64_t total;
   const uint64_t mine = sh.mass[tid];
-  uint64_t before = block_before(mine, sh.buf, &total);
+  uint64_t before = block_before<C>(mine, sh.buf, &total);
   if (tid == 0) sh.first = -1;
   if constexpr (C > 1) {
     uint64_t each = total, none = 0, more = 0;
@@ -802,7 +814,7 @@ cudaError_t sample_in(const SampleCall& c, cudaStream_t s) {
   if (c.p.rows > (int)((1u << 31) - 1) / C) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)c.p.rows * C);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<C>);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -818,7 +830,7 @@ template <typename T>
 cudaError_t sample_t(const SampleCall& c, cudaStream_t s) {
   const int sms = serve_sm_count(), vectors = c.p.vocab / Wide<T>::E;
   int blocks = 1;
-  while (blocks < 8 && c.p.rows <= sms / blocks && vectors >= 2 * blocks * kThreads) blocks *= 2;
+  while (blocks < 8 && c.p.rows <= sms / blocks && vectors >= 2 * blocks * kThreads<8>) blocks *= 2;
   return blocks == 8 ? sample_in<T, 8>(c, s) : blocks == 4 ? sample_in<T, 4>(c, s)
        : blocks == 2 ? sample_in<T, 2>(c, s) : sample_in<T, 1>(c, s);
 }
