@@ -612,7 +612,7 @@ cudaError_t rows_of(const DistillArgs<T>& a, int per_sm, cudaStream_t s) {
 template <typename T, Mode kMode>
 cudaError_t rows_t(const DistillArgs<T>& a, cudaStream_t s) {
   if (a.vocab <= 1024 * Wide<T>::E) return rows_of<T, 128, kMode>(a, 6, s);
-  return kMode == kLoss ? rows_of<T, 256, kMode>(a, 4, s) : rows_of<T, 512, kMode>(a, 2, s);
+  return kMode != kGradAndLoss ? rows_of<T, 256, kMode>(a, 4, s) : rows_of<T, 512, kMode>(a, 2, s);
 }
 
 template <typename T>
