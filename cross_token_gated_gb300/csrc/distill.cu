@@ -142,6 +142,10 @@ struct Entries {
   float* z;     // the student's logit
   float* share; // sum of p over the entries of this token
 };
+// What the loss needs of a row's entries: sums of p ln p and p (z - z0) / T, and z0, the largest z.
+struct Target {
+  float plogp, pz, z0;
+};
 constexpr int kSeenWords = 1024;  // one bit per token, modulo 32,768
 
 // The gradient at the entries' tokens, where the teacher's share comes off.
@@ -164,29 +168,31 @@ __device__ __forceinline__ void fetch_entries(const DistillArgs<T>& a, long long
   }
 }
 
-constexpr int kGather = 4;  // student's logits of a lane that are under way at a time
+constexpr int kGather = 8;  // student's logits of a lane that are under way at a time
 
 // Ids to -1 where an entry is absent; whether any is left.  The first logits are left in z.
 template <typename T>
 __device__ __forceinline__ bool begin_gather(const DistillArgs<T>& a, long long row, const Entries& t, int lane, T (&z)[kGather]) {
   bool some = false;
   const T* src = a.z + row * a.pitch;
-#pragma unroll
-  for (int j = 0; j < kGather; ++j) z[j] = T(0.f);
   for (int e0 = 0; e0 < a.k; e0 += 32 * kGather) {
+    T x[kGather];  // (all of them asked for before the first is stored)
 #pragma unroll
     for (int j = 0; j < kGather; ++j) {
       const int e = e0 + 32 * j + lane;
-      if (e >= a.k) continue;
-      int id = t.id[e];
-      if (id >= a.vocab) record_error(a.err, kErrValue | kKernDistill);
-      if (id < 0 || id >= a.vocab || t.p[e] == -INFINITY) t.id[e] = id = -1;
-      some |= id >= 0;
-      if (e0 == 0) {
-        if (id >= 0) z[j] = src[id];
-      } else {
-        t.z[e] = id >= 0 ? io<T>::ld(src + id) : 0.f;
+      int id = -1;
+      if (e < a.k) {
+        id = t.id[e];
+        if (id >= a.vocab) record_error(a.err, kErrValue | kKernDistill);
+        if (id < 0 || id >= a.vocab || t.p[e] == -INFINITY) t.id[e] = id = -1;
+        some |= id >= 0;
       }
+      x[j] = id >= 0 ? src[id] : T(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < kGather; ++j) {
+      if (e0 == 0) z[j] = x[j];
+      else if (e0 + 32 * j + lane < a.k) t.z[e0 + 32 * j + lane] = (float)x[j];
     }
   }
   return __any_sync(0xffffffffu, some);
@@ -198,65 +204,100 @@ __device__ __forceinline__ void end_gather(const DistillArgs<T>& a, const Entrie
     if (32 * j + lane < a.k) t.z[32 * j + lane] = (float)z[j];
 }
 
+// Largest of a warp's floats (none NaN), by one reduction of integers in the same order.
+__device__ __forceinline__ float warp_largest(float v) {
+  const unsigned b = __float_as_uint(v), m = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
+  return __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
+}
+
 // The probabilities; `seen` holds zeros before and after.
 template <typename T>
-__device__ __forceinline__ void finish_entries(const DistillArgs<T>& a, const Entries& t, unsigned* seen, int lane, bool shares) {
+__device__ __forceinline__ Target finish_entries(const DistillArgs<T>& a, const Entries& t, unsigned* seen, int lane, bool shares) {
   float mx = -INFINITY;
+  Target g{0.f, 0.f, -INFINITY};
   bool nan = false;
+#pragma unroll 4
   for (int e = lane; e < a.k; e += 32) {
-    const float v = t.p[e];
-    if (t.id[e] < 0) continue;
-    mx = fmaxf(mx, v);
-    nan |= v != v;
+    const float v = t.p[e], z = t.z[e];
+    const bool live = t.id[e] >= 0;
+    mx = fmaxf(mx, live ? v : -INFINITY);
+    g.z0 = fmaxf(g.z0, live ? z : -INFINITY);
+    nan |= live && v != v;
   }
+  mx = warp_largest(mx);
+  g.z0 = warp_largest(g.z0);
   if (__any_sync(0xffffffffu, nan)) mx = NAN;
-  else mx = warp_max(mx);
+  if (g.z0 == -INFINITY) g.z0 = 0.f;
   float s = 0.f;
+#pragma unroll 4
   for (int e = lane; e < a.k; e += 32) {
-    const float w = t.id[e] >= 0 ? exp2f((t.p[e] - mx) * a.c) : 0.f;
+    const float y = t.id[e] >= 0 ? (t.p[e] - mx) * a.c : -INFINITY, w = exp2f(y);
     t.p[e] = w;
     s += w;
+    if (w != 0.f) {  // (also NaN)
+      g.plogp = fmaf(w, y, g.plogp);
+      g.pz = fmaf(w, t.z[e] - g.z0, g.pz);
+    }
   }
-  const float inv = 1.f / warp_sum(s);
-  for (int e = lane; e < a.k; e += 32) t.share[e] = t.p[e] *= inv;
-  if (!shares) return;
-  // entries that may name a token a second time (or one that differs by a multiple of 32,768) take
-  // the token's entries together under the first of them
-  bool again = false;
-  for (int e0 = 0; e0 < a.k; e0 += 32) {
-    const int id = e0 + lane < a.k ? t.id[e0 + lane] : -1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    g.plogp += __shfl_xor_sync(0xffffffffu, g.plogp, o);
+    g.pz += __shfl_xor_sync(0xffffffffu, g.pz, o);
+  }
+  const float inv = 1.f / s;
+  g.plogp = fmaf(g.plogp * inv, 0.69314718f, -logf(s));
+  g.pz = g.pz * inv / a.temp;
+#pragma unroll 4
+  for (int e = lane; e < a.k; e += 32) t.share[e] = t.p[e] * inv;
+  if (!shares) return g;
+  // Entries that may name a token a second time (or one that differs by a multiple of 32,768), by
+  // lane and number; the token's entries are taken together under the first of them.
+  unsigned late = 0;
+#pragma unroll 4
+  for (int e = lane; e < a.k; e += 32) {
+    const int id = t.id[e];
     const unsigned bit = 1u << (id & 31);
-    again |= id >= 0 && (atomicOr(seen + (id >> 5 & (kSeenWords - 1)), bit) & bit);
+    if (id >= 0 && (atomicOr(seen + (id >> 5 & (kSeenWords - 1)), bit) & bit)) late |= 1u << (e >> 5);
   }
   __syncwarp();
+#pragma unroll 4
   for (int e = lane; e < a.k; e += 32)
     if (t.id[e] >= 0) seen[t.id[e] >> 5 & (kSeenWords - 1)] = 0;
   __syncwarp();
-  if (!__any_sync(0xffffffffu, again)) return;
-  for (int e = 0; e < a.k; ++e) {
-    const int token = t.id[e];
-    if (token < 0) continue;
-    float sum = t.share[e];
-    bool more = false;
-    for (int i0 = e + 1; i0 < a.k; i0 += 32) {
-      const bool same = i0 + lane < a.k && t.id[i0 + lane] == token;
-      unsigned who = __ballot_sync(0xffffffffu, same);
-      more |= who != 0;
-      for (unsigned w = who; w; w &= w - 1) sum += t.share[i0 + __ffs(w) - 1];
-      if (same) t.id[i0 + lane] = -1;
+  if (!__any_sync(0xffffffffu, late != 0)) return g;
+  for (int c = 0; 32 * c < a.k; ++c) {
+    for (unsigned todo = __ballot_sync(0xffffffffu, late >> c & 1); todo; todo &= todo - 1) {
+      const int token = t.id[32 * c + __ffs(todo) - 1];
+      if (token < 0) continue;  // already taken together
+      int first = -1;
+      float sum = 0.f;
+      for (int i0 = 0; i0 < a.k; i0 += 32) {
+        const bool same = i0 + lane < a.k && t.id[i0 + lane] == token;
+        const unsigned who = __ballot_sync(0xffffffffu, same);
+        if (first < 0 && who) first = i0 + __ffs(who) - 1;
+        for (unsigned w = who; w; w &= w - 1) sum += t.share[i0 + __ffs(w) - 1];
+        if (same && i0 + lane != first) t.id[i0 + lane] = -1;
+      }
+      __syncwarp();
+      if (lane == 0) t.share[first] = sum;
+      __syncwarp();
     }
-    __syncwarp();
-    if (more && lane == 0) t.share[e] = sum;
-    __syncwarp();
   }
+  return g;
 }
 
+// Warps that look after the teacher: one, or, where the row's own time is short beside theirs, one
+// that gathers the entries and one that forms probabilities and loss.
+template <Mode kMode, int kRow> constexpr int kTeachers = kMode == kGradAndLoss && kRow == 512 ? 2 : 1;
+
 // kRow threads hold the row, NV vectors each at a time; the next ones are on their way to shared
-// memory meanwhile, each to a slot of the thread that will read it.  The last warp looks after the
+// memory meanwhile, each to a slot of the thread that will read it.  The last warps look after the
 // teacher.
 template <typename T, int kRow, int NV, Mode kMode>
-__global__ void __launch_bounds__(kRow + 32, kRow == 512 ? 2 : kRow == 256 ? 4 : 6) distill_row_kernel(const DistillArgs<T> a) {
-  constexpr int E = Wide<T>::E, W = kRow / 32;
+__global__ void __launch_bounds__(kRow + 32 * kTeachers<kMode, kRow>, kRow == 512 ? 2 : kRow == 256 ? 4 : kRow == 128 ? 6 : 16)
+    distill_row_kernel(const DistillArgs<T> a) {
+  constexpr int E = Wide<T>::E, W = kRow / 32, kAll = kRow + 32 * kTeachers<kMode, kRow>;
   extern __shared__ __align__(16) uint4 ahead[];  // [NV][kRow], then the entries of kSlots rows
   __shared__ int any[kSlots];                     // whether a row has entries: of this row and the next ones
   __shared__ unsigned seen[kSeenWords];
@@ -267,63 +308,70 @@ __global__ void __launch_bounds__(kRow + 32, kRow == 512 ? 2 : kRow == 256 ? 4 :
     float* w = words + (n & (kSlots - 1)) * 4 * a.k;
     return Entries{reinterpret_cast<int*>(w), w + a.k, w + 2 * a.k, w + 3 * a.k};
   };
-  // all threads meet here; the last warp and the others come from different places
-  auto meet = [] { ptx::named_bar_sync(1, kRow + 32); };
+  auto has_entries = [&](int n) { return any[n & (kSlots - 1)] != 0; };
+  // all threads meet here; the last warps and the others come from different places
+  auto meet = [] { ptx::named_bar_sync(1, kAll); };
   const long long step = gridDim.x;
   int n = 0;  // rows so far
 
-  if (warp == W) {
+  if (warp >= W) {
     // of row n: the loss; of n + 1: the probabilities; of n + 2: logits arrive; of n + 3: they are
     // asked for; of n + 5: ids and the teacher's logits are asked for
+    const bool finishes = warp == W, gathers = warp == W + kTeachers<kMode, kRow> - 1;
     const long long row0 = blockIdx.x;
     const int rows = (int)((a.rows - row0 + step - 1) / step);  // of this block
     T z[kGather];
-    bool live[4];  // of rows n .. n + 3, as any
-    for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
-    for (int i = 0; i < 5 && i < rows; ++i) fetch_entries(a, row0 + i * step, entries(i), lane);
-    cp_async_wait();
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      live[i] = i < rows && begin_gather(a, row0 + i * step, entries(i), lane, z);
-      if (live[i]) end_gather(a, entries(i), lane, z);
-      if (lane == 0) any[i] = live[i];
+    bool arriving = false;  // row n + 2 has logits under way
+    Target now{0.f, 0.f, 0.f}, ahead_of{0.f, 0.f, 0.f};  // of rows n and n + 1
+    if (gathers) {
+      for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
+      for (int i = 0; i < 5 && i < rows; ++i) fetch_entries(a, row0 + i * step, entries(i), lane);
+      cp_async_wait();
+      __syncwarp();
+#pragma unroll 1
+      for (int i = 0; i < 3; ++i) {
+        const bool live = i < rows && begin_gather(a, row0 + i * step, entries(i), lane, z);
+        if (live) end_gather(a, entries(i), lane, z);
+        if (lane == 0) any[i] = live;
+      }
     }
-    if (live[0]) finish_entries(a, entries(0), seen, lane, kMode != kLoss);
-    live[3] = false;
+    if (kTeachers<kMode, kRow> > 1) ptx::named_bar_sync(2, 64);
+    else __syncwarp();
+    if (finishes && has_entries(0)) now = finish_entries(a, entries(0), seen, lane, kMode != kLoss);
     meet();
     for (; n < rows; ++n) {
       const long long row = row0 + n * step;
-      cp_async_wait_but<1>();
-      __syncwarp();
-      if (n > 0 && live[2]) end_gather(a, entries(n + 2), lane, z);
-      live[3] = n + 3 < rows && begin_gather(a, row + 3 * step, entries(n + 3), lane, z);
-      if (lane == 0) any[(n + 3) & (kSlots - 1)] = live[3];
-      if (n + 5 < rows) fetch_entries(a, row + 5 * step, entries(n + 5), lane);
-      cp_async_commit();
-      if (live[1]) finish_entries(a, entries(n + 1), seen, lane, kMode != kLoss);
+      const bool live = has_entries(n);
+      auto look_ahead = [&] {
+        if (gathers) {
+          cp_async_wait_but<1>();
+          __syncwarp();
+          if (arriving) end_gather(a, entries(n + 2), lane, z);
+          arriving = n + 3 < rows && begin_gather(a, row + 3 * step, entries(n + 3), lane, z);
+          if (lane == 0) any[(n + 3) & (kSlots - 1)] = arriving;
+          if (n + 5 < rows) fetch_entries(a, row + 5 * step, entries(n + 5), lane);
+          cp_async_commit();
+        }
+        if (finishes && n + 1 < rows && has_entries(n + 1))
+          ahead_of = finish_entries(a, entries(n + 1), seen, lane, kMode != kLoss);
+      };
+      if (kMode == kGradAndLoss) look_ahead();
       Running st{0.f, 0.f};
-      if (kMode == kGradAndLoss || (kMode == kLoss && live[0])) {
+      if (kMode == kGradAndLoss || (kMode == kLoss && live)) {
         meet();  // (also in padding: one step for all)
-        if (live[0]) st = row_total(part[n & 1], a.c);
+        if (live) st = row_total(part[n & 1], a.c);
       }
-      if (lane == 0 && kMode == kLoss && a.stats_out) *reinterpret_cast<float2*>(a.stats_out + 2 * row) = make_float2(st.m, st.s);
-      if (kMode != kGradFromStats && a.loss) {
-        const Entries t = entries(n);
-        const float lse = logf(st.s);
-        float s = 0.f;
-        if (live[0])
-          for (int e = lane; e < a.k; e += 32) {
-            const float p = t.p[e], zt = t.z[e];
-            if (p != 0.f) s += p * (logf(p) - (zt == -INFINITY ? zt : (zt - st.m) / a.temp - lse));
-          }
-        s = warp_sum(s);
-        if (lane == 0) a.loss[row] = a.temp * a.temp * s;
+      if (finishes && lane == 0 && kMode == kLoss && a.stats_out)
+        *reinterpret_cast<float2*>(a.stats_out + 2 * row) = make_float2(st.m, st.s);
+      // sum p (ln p - ln q), ln q_e = (z_e - z0) / T + (z0 - m) / T - ln sum; inf where an entry has z = -inf
+      if (finishes && kMode != kGradFromStats && a.loss && lane == 0) {
+        float loss = now.plogp - now.pz - (now.z0 - st.m) / a.temp + logf(st.s);
+        if (now.pz == -INFINITY) loss = INFINITY + 0.f * st.s;  // (NaN if the row has one)
+        a.loss[row] = live ? a.temp * a.temp * loss : 0.f;
       }
-      if (kMode != kLoss || !live[0]) meet();
-      live[0] = live[1];
-      live[1] = live[2];
-      live[2] = live[3];
+      if (kMode != kGradAndLoss) look_ahead();
+      if (kMode != kLoss || !live) meet();
+      now = ahead_of;
     }
     return;
   }
@@ -349,12 +397,12 @@ __global__ void __launch_bounds__(kRow + 32, kRow == 512 ? 2 : kRow == 256 ? 4 :
     }
   };
   meet();
-  if (any[0]) fetch(a.z + blockIdx.x * a.pitch, 0);
+  if (has_entries(0)) fetch(a.z + blockIdx.x * a.pitch, 0);
   for (long long row = blockIdx.x; row < a.rows; row += step, ++n) {
     const T* z = a.z + row * a.pitch;
     T* dz = a.dz + row * a.grad_pitch;
-    const bool next = any[(n + 1) & (kSlots - 1)];
-    if (!any[n & (kSlots - 1)]) {  // padding
+    const bool next = row + step < a.rows && has_entries(n + 1);
+    if (!has_entries(n)) {  // padding
       if (next) fetch(z + step * a.pitch, 0);
       if (kMode == kGradAndLoss) meet();
       if (kMode != kLoss) {
@@ -604,13 +652,16 @@ cudaError_t rows_of(const DistillArgs<T>& a, int per_sm, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              8 * kRow * 16 + kSlots * 4 * TG_MAX_TEACHER * 4);
   if (e != cudaSuccess) return e;
-  kernel<<<grid_of(a.rows, per_sm), kRow + 32, smem, s>>>(a);
+  kernel<<<grid_of(a.rows, per_sm), kRow + 32 * kTeachers<kMode, kRow>, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-// Blocks of 512 threads and a warp, two per SM, or of 128 for rows of up to 1,024 vectors.
+// Threads of a row: 512 where it stays in registers for its gradient (4,096 vectors), else 256 with
+// twice the blocks; 128 or 32 for short ones (up to 1,024 or 256 vectors), whose time is the
+// latency of a row's steps.
 template <typename T, Mode kMode>
 cudaError_t rows_t(const DistillArgs<T>& a, cudaStream_t s) {
+  if (a.vocab <= 256 * Wide<T>::E) return rows_of<T, 32, kMode>(a, 16, s);
   if (a.vocab <= 1024 * Wide<T>::E) return rows_of<T, 128, kMode>(a, 6, s);
   return kMode != kGradAndLoss ? rows_of<T, 256, kMode>(a, 4, s) : rows_of<T, 512, kMode>(a, 2, s);
 }
