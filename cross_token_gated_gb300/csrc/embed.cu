@@ -84,25 +84,30 @@ constexpr int kAhead = 16;          // ids of a lane that are loaded at a time
 struct SortArgs {
   const int* ids;
   int N, vocab, pad;
-  int R;        // ids of a block
+  int R;        // ids of a block: b, b + gridDim.x, b + 2 gridDim.x, ...
+  unsigned magic;  // 2^shift / gridDim.x, rounded up
+  int shift;
   int* order;   // [N] tokens by id, then by position
   int* sorted;  // [N] their ids
   int* start;   // [vocab] first entry of each id in order
   int* count;   // [vocab]
+  int* total;   // tokens in order
   int* arrived; // the sums' counters, to be zeroed
   long long n_arrived;
   unsigned* err;
 };
 
-// Block b sorts the ids of [b R, (b + 1) R): every block reads all ids, so that it also knows how
-// many lie below its own, and no block waits for another (the ids are a small part of dout, and
-// stay in L2).  Warp w counts, and then places, the w-th share of the positions; a counter per
-// (warp, id) keeps the order of positions.
+// Block b sorts the ids that leave the remainder b (frequent tokens often have neighbouring ids,
+// which would fall to few blocks otherwise); the order is by remainder, then by id.  Every block
+// reads all ids, so that it also knows how many come before its own, and no block waits for another
+// (the ids are a small part of dout, and stay in L2).  Warp w counts, and then places, the w-th
+// share of the positions; a counter per (warp, id) keeps the order of positions.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs a) {
   extern __shared__ int cnt[];  // [kSortWarps][R]
   __shared__ int below_w[kSortWarps], scan_w[kSortWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int v0 = blockIdx.x * a.R, nr = min(a.R, a.vocab - v0);
+  const int mod = gridDim.x, nr = (a.vocab - (int)blockIdx.x + mod - 1) / mod;
+  auto quotient = [&](int id) { return (int)((uint64_t)(unsigned)id * a.magic >> a.shift); };
   const int share = ((a.N + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const int n0 = (int)min((long long)warp * share, (long long)a.N), n1 = (int)min((long long)n0 + share, (long long)a.N);
   int* mine = cnt + warp * a.R;
@@ -125,11 +130,12 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
       if (n + 32 * j >= n1) break;
       const bool live = id[j] != a.pad && id[j] >= 0 && id[j] < a.vocab;
       bad |= !live && id[j] != a.pad;
-      below += live && id[j] < v0;
-      const bool in = live && id[j] >= v0 && id[j] < v0 + nr;
+      const int at = quotient(id[j]), rest = id[j] - at * mod;
+      below += live && rest < (int)blockIdx.x;
+      const bool in = live && rest == (int)blockIdx.x;
       if (__ballot_sync(0xffffffffu, in) == 0) continue;
-      const unsigned same = __match_any_sync(0xffffffffu, in ? id[j] - v0 : -1);
-      if (in && (same & ((1u << lane) - 1)) == 0) mine[id[j] - v0] += __popc(same);
+      const unsigned same = __match_any_sync(0xffffffffu, in ? at : -1);
+      if (in && (same & ((1u << lane) - 1)) == 0) mine[at] += __popc(same);
       __syncwarp();
     }
   }
@@ -168,8 +174,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     const int next = __shfl_sync(0xffffffffu, at + sum, lane | (kShare - 1));
     if (r < nr) {
       if (part == 0) {
-        a.start[v0 + r] = first;
-        a.count[v0 + r] = next - first;
+        a.start[r * mod + blockIdx.x] = first;
+        a.count[r * mod + blockIdx.x] = next - first;
       }
 #pragma unroll
       for (int w = 0; w < kEach; ++w) {
@@ -179,22 +185,24 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     }
     __syncthreads();
   }
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *a.total = run;
   for (int n = n0; n < n1; n += 32 * kAhead) {
     if (share > 32 * kAhead) load(n);  // (else they are still there)
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (n + 32 * j >= n1) break;
-      const bool in = id[j] != a.pad && id[j] >= v0 && id[j] < v0 + nr;
+      const int q = quotient(id[j]);
+      const bool in = id[j] != a.pad && id[j] >= 0 && id[j] < a.vocab && id[j] - q * mod == (int)blockIdx.x;
       if (__ballot_sync(0xffffffffu, in) == 0) continue;
-      const unsigned same = __match_any_sync(0xffffffffu, in ? id[j] - v0 : -1);
+      const unsigned same = __match_any_sync(0xffffffffu, in ? q : -1);
       const unsigned earlier = same & ((1u << lane) - 1);
-      const int at = in ? mine[id[j] - v0] : 0;
+      const int at = in ? mine[q] : 0;
       if (in) {
         a.order[at + __popc(earlier)] = n + 32 * j + lane;
         a.sorted[at + __popc(earlier)] = id[j];
       }
       __syncwarp();
-      if (in && earlier == 0) mine[id[j] - v0] = at + __popc(same);
+      if (in && earlier == 0) mine[q] = at + __popc(same);
       __syncwarp();
     }
   }
@@ -223,7 +231,7 @@ template <> struct Wide<__nv_bfloat16> {
 
 template <typename T, typename G>
 struct SumArgs {
-  const int *order, *sorted, *start, *count;
+  const int *order, *sorted, *start, *count, *total;
   const T* dout;
   const G* base;
   G* dE;
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(256, kVec && !kBase ? 3 : 2) embed_sum_kernel(
   const bool mine = lane < a.chunk && p0 + lane < a.N;
   const int token = mine ? a.order[p0 + lane] : 0, sorted = mine ? a.sorted[p0 + lane] : -1;
   const int left = p0 > 0 && p0 < a.N ? a.sorted[p0 - 1] : -1, right = p0 + a.chunk < a.N ? a.sorted[p0 + a.chunk] : -1;
-  const int M = a.start[a.vocab - 1] + a.count[a.vocab - 1];  // (padding is not in order)
+  const int M = *a.total;  // (padding is not in order)
   if (q * 8 * a.chunk >= M) return;
   // (of the entries from M on, only their memory is there)
   const int n = min(a.chunk, M - p0), id = lane < n ? sorted : -1, before = n > 0 ? left : -1;
@@ -515,7 +523,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // How the sums are taken, from the sizes alone (the workspace's size depends on it).
 struct EmbedPlan {
   int chunk, blocks, tile, tiles, part_pitch;
-  size_t order, sorted, start, count, arrived, part, total;  // offsets in the workspace
+  size_t order, sorted, start, count, tokens, arrived, part, total;  // offsets in the workspace
 };
 EmbedPlan embed_plan(const EmbedCall& c, bool vec) {
   EmbedPlan w;
@@ -531,7 +539,8 @@ EmbedPlan embed_plan(const EmbedCall& c, bool vec) {
   w.sorted = tokens;
   w.start = 2 * tokens;
   w.count = w.start + ids;
-  w.arrived = w.count + ids;
+  w.tokens = w.count + ids;
+  w.arrived = w.tokens + 256;
   w.part = w.arrived + up256((size_t)w.tiles * 3 * w.blocks * 4);
   w.total = w.part + up256((size_t)w.blocks * 2 * w.part_pitch * 4);
   return w;
@@ -546,7 +555,7 @@ bool vector_rows(const EmbedCall& c) {
 template <typename T, typename G>
 cudaError_t sums(const EmbedCall& c, const SortArgs& t, const EmbedPlan& w, bool vec, cudaStream_t s) {
   SumArgs<T, G> a;
-  a.order = t.order; a.sorted = t.sorted; a.start = t.start; a.count = t.count; a.arrived = t.arrived;
+  a.order = t.order; a.sorted = t.sorted; a.start = t.start; a.count = t.count; a.total = t.total; a.arrived = t.arrived;
   a.dout = static_cast<const T*>(c.dout); a.base = static_cast<const G*>(c.base); a.dE = static_cast<G*>(c.dE);
   a.part = reinterpret_cast<float*>(static_cast<char*>(c.ws) + w.part);
   a.N = (int)c.rows; a.d = c.d; a.vocab = c.vocab; a.part_pitch = w.part_pitch; a.pitch = c.pitch; a.scale = c.scale;
@@ -594,6 +603,7 @@ cudaError_t launch_embed_backward(const EmbedCall& c, cudaStream_t s) {
   a.sorted = reinterpret_cast<int*>(ws + w.sorted);
   a.start = reinterpret_cast<int*>(ws + w.start);
   a.count = reinterpret_cast<int*>(ws + w.count);
+  a.total = reinterpret_cast<int*>(ws + w.tokens);
   a.arrived = reinterpret_cast<int*>(ws + w.arrived);
   a.n_arrived = (long long)w.tiles * 3 * w.blocks;
   a.err = c.err;
@@ -601,7 +611,11 @@ cudaError_t launch_embed_backward(const EmbedCall& c, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSortWarps * kMaxSortRows * 4);
   if (e != cudaSuccess) return e;
-  embed_sort_kernel<<<ceil_div(c.vocab, a.R), kSortThreads, smem, s>>>(a);
+  const unsigned blocks = ceil_div(c.vocab, a.R);
+  a.shift = 31;
+  while ((1u << (a.shift - 31)) < blocks) ++a.shift;  // quotients of ids below 2^31 are exact
+  a.magic = (unsigned)(((1ull << a.shift) + blocks - 1) / blocks);
+  embed_sort_kernel<<<blocks, kSortThreads, smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   using bf16 = __nv_bfloat16;
