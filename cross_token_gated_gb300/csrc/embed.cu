@@ -80,11 +80,14 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const int* ids, const
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kMaxSortRows = 1536;  // ids of a block: kSortWarps counters each in shared memory
 constexpr int kAhead = 16;          // ids of a lane that are loaded at a time
+constexpr int kOffsetBits = 21;     // of a queue entry: the position; the id's number takes 11
+constexpr int kSortSmem = 224 * 1024;
 
 struct SortArgs {
   const int* ids;
   int N, vocab, pad;
   int R;        // ids of a block: b, b + gridDim.x, b + 2 gridDim.x, ...
+  int queue;    // entries of a warp's queue
   unsigned magic;  // 2^shift / gridDim.x, rounded up
   int shift;
   int* order;   // [N] tokens by id, then by position
@@ -101,9 +104,11 @@ struct SortArgs {
 // which would fall to few blocks otherwise); the order is by remainder, then by id.  Every block
 // reads all ids, so that it also knows how many come before its own, and no block waits for another
 // (the ids are a small part of dout, and stay in L2).  Warp w counts, and then places, the w-th
-// share of the positions; a counter per (warp, id) keeps the order of positions.
+// share of the positions; a counter per (warp, id) keeps the order of positions.  What a warp finds
+// in the first pass it queues in shared memory for the second (which goes through the ids again
+// where a very frequent token fills the queue).
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs a) {
-  extern __shared__ int cnt[];  // [kSortWarps][R]
+  extern __shared__ int cnt[];  // [kSortWarps][R], then the queues [kSortWarps][queue]
   __shared__ int below_w[kSortWarps], scan_w[kSortWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int mod = gridDim.x, nr = (a.vocab - (int)blockIdx.x + mod - 1) / mod;
@@ -111,6 +116,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
   const int share = ((a.N + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const int n0 = (int)min((long long)warp * share, (long long)a.N), n1 = (int)min((long long)n0 + share, (long long)a.N);
   int* mine = cnt + warp * a.R;
+  unsigned* queue = reinterpret_cast<unsigned*>(cnt + kSortWarps * a.R) + warp * a.queue;
+  int queued = 0;
   let_next_start();
   for (int i = threadIdx.x; i < kSortWarps * a.R; i += kSortThreads) cnt[i] = 0;
   for (long long i = (long long)blockIdx.x * kSortThreads + threadIdx.x; i < a.n_arrived; i += (long long)gridDim.x * kSortThreads)
@@ -128,14 +135,18 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (n + 32 * j >= n1) break;
-      const bool live = id[j] != a.pad && id[j] >= 0 && id[j] < a.vocab;
-      bad |= !live && id[j] != a.pad;
+      const bool known = (unsigned)id[j] < (unsigned)a.vocab, live = known && id[j] != a.pad;
+      bad |= !known && id[j] != a.pad;
       const int at = quotient(id[j]), rest = id[j] - at * mod;
       below += live && rest < (int)blockIdx.x;
       const bool in = live && rest == (int)blockIdx.x;
-      if (__ballot_sync(0xffffffffu, in) == 0) continue;
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      if (who == 0) continue;
       const unsigned same = __match_any_sync(0xffffffffu, in ? at : -1);
       if (in && (same & ((1u << lane) - 1)) == 0) mine[at] += __popc(same);
+      const int k = queued + __popc(who & ((1u << lane) - 1));
+      if (in && k < a.queue) queue[k] = (unsigned)at << kOffsetBits | (unsigned)(n - n0 + 32 * j + lane);
+      queued += __popc(who);
       __syncwarp();
     }
   }
@@ -186,24 +197,33 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     __syncthreads();
   }
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *a.total = run;
+  auto place = [&](bool in, int q, int position) {
+    const unsigned same = __match_any_sync(0xffffffffu, in ? q : -1);
+    const unsigned earlier = same & ((1u << lane) - 1);
+    const int at = in ? mine[q] : 0;
+    if (in) {
+      a.order[at + __popc(earlier)] = position;
+      a.sorted[at + __popc(earlier)] = q * mod + blockIdx.x;
+    }
+    __syncwarp();
+    if (in && earlier == 0) mine[q] = at + __popc(same);
+    __syncwarp();
+  };
+  if (queued <= a.queue && share <= 1 << kOffsetBits) {
+    for (int k = 0; k < queued; k += 32) {
+      const unsigned e = k + lane < queued ? queue[k + lane] : 0;
+      place(k + lane < queued, e >> kOffsetBits, n0 + (int)(e & ((1u << kOffsetBits) - 1)));
+    }
+    return;
+  }
   for (int n = n0; n < n1; n += 32 * kAhead) {
-    if (share > 32 * kAhead) load(n);  // (else they are still there)
+    load(n);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (n + 32 * j >= n1) break;
       const int q = quotient(id[j]);
-      const bool in = id[j] != a.pad && id[j] >= 0 && id[j] < a.vocab && id[j] - q * mod == (int)blockIdx.x;
-      if (__ballot_sync(0xffffffffu, in) == 0) continue;
-      const unsigned same = __match_any_sync(0xffffffffu, in ? q : -1);
-      const unsigned earlier = same & ((1u << lane) - 1);
-      const int at = in ? mine[q] : 0;
-      if (in) {
-        a.order[at + __popc(earlier)] = n + 32 * j + lane;
-        a.sorted[at + __popc(earlier)] = id[j];
-      }
-      __syncwarp();
-      if (in && earlier == 0) mine[q] = at + __popc(same);
-      __syncwarp();
+      const bool in = (unsigned)id[j] < (unsigned)a.vocab && id[j] != a.pad && id[j] - q * mod == (int)blockIdx.x;
+      if (__any_sync(0xffffffffu, in)) place(in, q, n + 32 * j + lane);
     }
   }
 }
@@ -607,9 +627,14 @@ cudaError_t launch_embed_backward(const EmbedCall& c, cudaStream_t s) {
   a.arrived = reinterpret_cast<int*>(ws + w.arrived);
   a.n_arrived = (long long)w.tiles * 3 * w.blocks;
   a.err = c.err;
-  const size_t smem = (size_t)kSortWarps * a.R * 4;
+  const int counters = kSortWarps * a.R * 4, left = (kSortSmem - counters) / (kSortWarps * 4);
+  // a token that a quarter of the positions name still fits (more shared memory than that delays the
+  // kernel behind: 16,384 tokens 25 us with 512 entries, 26 with 2,048; 262,144 tokens 201 and 154 us)
+  a.queue = a.N / kSortWarps / 4 > 512 ? a.N / kSortWarps / 4 : 512;
+  if (a.queue > left) a.queue = left;
+  const int smem = counters + kSortWarps * a.queue * 4;
   cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSortWarps * kMaxSortRows * 4);
+                                       kSortSmem);
   if (e != cudaSuccess) return e;
   const unsigned blocks = ceil_div(c.vocab, a.R);
   a.shift = 31;
