@@ -115,8 +115,11 @@ __global__ void __launch_bounds__(kThreads) norm_backward_any_kernel(const NormA
 
 // ------------------------------------------------------------------- rows in registers
 
-template <typename T> struct Wide;  // 16 bytes of T
+// A thread's share of a row comes in vectors: 16 bytes, or single values where rows are not aligned.
+template <typename T> struct Wide;
 template <> struct Wide<float> {
+  using Value = float;
+  using Raw = uint4;
   static constexpr int E = 4;
   static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
     f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
@@ -124,9 +127,11 @@ template <> struct Wide<float> {
   static __device__ __forceinline__ uint4 pack(const float* f) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
-  static __device__ __forceinline__ float inv_sqrt(float v) { return 1.f / sqrtf(v); }
+  static __device__ __forceinline__ uint4 shared(uint32_t a) { return ptx::ld_shared_v4(a); }
 };
 template <> struct Wide<__nv_bfloat16> {
+  using Value = __nv_bfloat16;
+  using Raw = uint4;
   static constexpr int E = 8;
   static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
     f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
@@ -136,8 +141,35 @@ template <> struct Wide<__nv_bfloat16> {
     return make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]), ptx::pack_bf16x2(f[4], f[5]),
                       ptx::pack_bf16x2(f[6], f[7]));
   }
-  static __device__ __forceinline__ float inv_sqrt(float v) { return rsqrtf(v); }  // 2 units: far below a bf16 rounding
+  static __device__ __forceinline__ uint4 shared(uint32_t a) { return ptx::ld_shared_v4(a); }
 };
+template <typename T> struct Single;
+template <> struct Single<float> {
+  using Value = float;
+  using Raw = uint32_t;
+  static constexpr int E = 1;
+  static __device__ __forceinline__ void unpack(uint32_t u, float* f) { f[0] = __uint_as_float(u); }
+  static __device__ __forceinline__ uint32_t pack(const float* f) { return __float_as_uint(f[0]); }
+  static __device__ __forceinline__ uint32_t shared(uint32_t a) {
+    uint32_t u;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(a));
+    return u;
+  }
+};
+template <> struct Single<__nv_bfloat16> {
+  using Value = __nv_bfloat16;
+  using Raw = uint16_t;
+  static constexpr int E = 1;
+  static __device__ __forceinline__ void unpack(uint16_t u, float* f) { f[0] = __uint_as_float((uint32_t)u << 16); }
+  static __device__ __forceinline__ uint16_t pack(const float* f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f[0])); }
+  static __device__ __forceinline__ uint16_t shared(uint32_t a) {
+    uint16_t u;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(a));
+    return u;
+  }
+};
+__device__ __forceinline__ float inv_sqrt(float v, float) { return 1.f / sqrtf(v); }
+__device__ __forceinline__ float inv_sqrt(float v, __nv_bfloat16) { return rsqrtf(v); }  // 2 units: far below a bf16 rounding
 
 template <int kGroup> constexpr int kBlock = kGroup > 256 ? kGroup : 256;
 
@@ -176,44 +208,46 @@ struct GroupSum {
 };
 
 // One row of the group's: NV vectors a thread, vector k * kGroup + lane.
-template <int kGroup, int NV>
-__device__ __forceinline__ void load_row(uint4 (&u)[NV], const void* row, int lane, int nvec, bool live) {
+template <int kGroup, int NV, typename Raw>
+__device__ __forceinline__ void load_row(Raw (&u)[NV], const void* row, int lane, int nvec, bool live) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = k * kGroup + lane;
-    u[k] = live && i < nvec ? reinterpret_cast<const uint4*>(row)[i] : make_uint4(0, 0, 0, 0);
+    u[k] = live && i < nvec ? reinterpret_cast<const Raw*>(row)[i] : Raw();
   }
 }
 
 // gamma and beta (or ones and zeros) as vectors in shared memory: kept in registers they would cost
 // more warps an SM than their reading costs time.
-template <typename T>
-__device__ __forceinline__ void stage_vector(uint4* dst, const T* src, float otherwise, int nvec) {
-  float f[Wide<T>::E];
+template <typename V>
+__device__ __forceinline__ void stage_vector(typename V::Raw* dst, const typename V::Value* src, float otherwise, int nvec) {
+  float f[V::E];
 #pragma unroll
-  for (int e = 0; e < Wide<T>::E; ++e) f[e] = otherwise;
-  const uint4 none = Wide<T>::pack(f);
-  for (int i = threadIdx.x; i < nvec; i += blockDim.x) dst[i] = src ? reinterpret_cast<const uint4*>(src)[i] : none;
+  for (int e = 0; e < V::E; ++e) f[e] = otherwise;
+  const typename V::Raw none = V::pack(f);
+  for (int i = threadIdx.x; i < nvec; i += blockDim.x) dst[i] = src ? reinterpret_cast<const typename V::Raw*>(src)[i] : none;
 }
 
-template <typename T, int kGroup, int NV>
-__global__ void __launch_bounds__(kBlock<kGroup>, kForwardPerSm<kGroup>) norm_kernel(const NormArgs<T> a) {
-  constexpr int E = Wide<T>::E, B = kBlock<kGroup>, kRows = B / kGroup;
+template <typename V, int kGroup, int NV>
+__global__ void __launch_bounds__(kBlock<kGroup>, kForwardPerSm<kGroup>) norm_kernel(const NormArgs<typename V::Value> a) {
+  using Raw = typename V::Raw;
+  constexpr int E = V::E, B = kBlock<kGroup>, kRows = B / kGroup;
   extern __shared__ __align__(16) uint4 weights[];  // [2][nvec]: gamma, beta
   __shared__ float buf[2][1][B / 32];
   GroupSum<kGroup, 1, B / 32> sum{buf};
   const int lane = threadIdx.x % kGroup, nvec = a.d / E;
   const float inv_d = 1.f / (float)a.d;
-  stage_vector(weights, a.gamma, 1.f, nvec);
-  stage_vector(weights + nvec, a.beta, 0.f, nvec);
+  Raw* const staged = reinterpret_cast<Raw*>(weights);
+  stage_vector<V>(staged, a.gamma, 1.f, nvec);
+  stage_vector<V>(staged + nvec, a.beta, 0.f, nvec);
   const uint32_t g = ptx::smem_u32(weights);
-  uint4 u[NV];
+  Raw u[NV];
   const long long step = (long long)gridDim.x * kRows;
   long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup, row0 = (long long)blockIdx.x * kRows;
   load_row<kGroup>(u, a.x + row * a.x_pitch, lane, nvec, row < a.rows);
   __syncthreads();
   for (; row0 < a.rows; row0 += step, row += step) {
-    uint4 next[NV];
+    Raw next[NV];
     load_row<kGroup>(next, a.x + (row + step) * a.x_pitch, lane, nvec, row + step < a.rows);
     float mu = 0.f;
     if (a.layer) {
@@ -221,7 +255,7 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kForwardPerSm<kGroup>) norm_ke
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         float f[E];
-        Wide<T>::unpack(u[k], f);
+        V::unpack(u[k], f);
 #pragma unroll
         for (int e = 0; e < E; ++e) s[0] += f[e];
       }
@@ -233,23 +267,23 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kForwardPerSm<kGroup>) norm_ke
     for (int k = 0; k < NV; ++k) {
       if (k * kGroup + lane >= nvec) continue;
       float f[E];
-      Wide<T>::unpack(u[k], f);
+      V::unpack(u[k], f);
 #pragma unroll
       for (int e = 0; e < E; ++e) ss[0] = fmaf(f[e] - mu, f[e] - mu, ss[0]);
     }
     sum(ss);
-    const float r = Wide<T>::inv_sqrt(fmaf(ss[0], inv_d, a.eps));
+    const float r = inv_sqrt(fmaf(ss[0], inv_d, a.eps), typename V::Value());
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = k * kGroup + lane;
       if (row >= a.rows || i >= nvec) continue;
       float f[E], gf[E], bf[E];
-      Wide<T>::unpack(u[k], f);
-      Wide<T>::unpack(ptx::ld_shared_v4(g + i * 16), gf);
-      Wide<T>::unpack(ptx::ld_shared_v4(g + (nvec + i) * 16), bf);
+      V::unpack(u[k], f);
+      V::unpack(V::shared(g + i * (int)sizeof(Raw)), gf);
+      V::unpack(V::shared(g + (nvec + i) * (int)sizeof(Raw)), bf);
 #pragma unroll
       for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mu) * r, gf[e], bf[e]);
-      reinterpret_cast<uint4*>(a.y + row * a.d)[i] = Wide<T>::pack(f);
+      reinterpret_cast<Raw*>(a.y + row * a.d)[i] = V::pack(f);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) u[k] = next[k];
@@ -265,10 +299,14 @@ __device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float*
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = k * kGroup + lane;
-    if (i < nvec)
+    if (i >= nvec) continue;
+    if constexpr (E == 1) {
+      mine[i] = acc[k];
+    } else {
 #pragma unroll
       for (int e = 0; e < E; e += 4)
         *reinterpret_cast<float4*>(mine + i * E + e) = make_float4(acc[k * E + e], acc[k * E + e + 1], acc[k * E + e + 2], acc[k * E + e + 3]);
+    }
   }
   if constexpr (kRows > 1) {
     __syncthreads();
@@ -282,19 +320,20 @@ __device__ __forceinline__ void block_columns(const float (&acc)[NV * E], float*
   }
 }
 
-template <typename T, int kGroup, int NV, bool kBeta>
-__global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_backward_kernel(const NormArgs<T> a) {
-  constexpr int E = Wide<T>::E, B = kBlock<kGroup>, kRows = B / kGroup;
+template <typename V, int kGroup, int NV, bool kBeta>
+__global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_backward_kernel(const NormArgs<typename V::Value> a) {
+  using Raw = typename V::Raw;
+  constexpr int E = V::E, B = kBlock<kGroup>, kRows = B / kGroup;
   extern __shared__ __align__(16) uint4 weights[];  // gamma [nvec], then float [kRows][d], where kRows > 1
   __shared__ float buf1[2][1][B / 32], buf3[2][3][B / 32];
   GroupSum<kGroup, 1, B / 32> sum1{buf1};
   GroupSum<kGroup, 3, B / 32> sum3{buf3};
   const int lane = threadIdx.x % kGroup, nvec = a.d / E;
   const float inv_d = 1.f / (float)a.d;
-  stage_vector(weights, a.gamma, 1.f, nvec);
+  stage_vector<V>(reinterpret_cast<Raw*>(weights), a.gamma, 1.f, nvec);
   const uint32_t g = ptx::smem_u32(weights);
-  float* columns = reinterpret_cast<float*>(weights + nvec);
-  uint4 x[NV], y[NV];
+  float* columns = reinterpret_cast<float*>(weights + (nvec * (int)sizeof(Raw) + 15) / 16);
+  Raw x[NV], y[NV];
   float dg[NV * E] = {}, db[kBeta ? NV * E : 1] = {};
   const long long step = (long long)gridDim.x * kRows;
   long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup, row0 = (long long)blockIdx.x * kRows;
@@ -302,7 +341,7 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_b
   load_row<kGroup>(y, a.dy + row * a.d, lane, nvec, row < a.rows);
   __syncthreads();
   for (; row0 < a.rows; row0 += step, row += step) {
-    uint4 res[NV], next_x[NV], next_y[NV];
+    Raw res[NV], next_x[NV], next_y[NV];
     const bool live = row < a.rows, more = row + step < a.rows;
     load_row<kGroup>(res, a.dres + row * a.d, lane, nvec, live && a.dres);
     load_row<kGroup>(next_x, a.x + (row + step) * a.x_pitch, lane, nvec, more);
@@ -313,7 +352,7 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_b
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         float f[E];
-        Wide<T>::unpack(x[k], f);
+        V::unpack(x[k], f);
 #pragma unroll
         for (int e = 0; e < E; ++e) s[0] += f[e];
       }
@@ -325,9 +364,9 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_b
     for (int k = 0; k < NV; ++k) {
       if (k * kGroup + lane >= nvec) continue;
       float f[E], h[E], gf[E];
-      Wide<T>::unpack(x[k], f);
-      Wide<T>::unpack(y[k], h);
-      Wide<T>::unpack(ptx::ld_shared_v4(g + (k * kGroup + lane) * 16), gf);
+      V::unpack(x[k], f);
+      V::unpack(y[k], h);
+      V::unpack(V::shared(g + (k * kGroup + lane) * (int)sizeof(Raw)), gf);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float c = f[e] - mu, dn = h[e] * gf[e];
@@ -337,17 +376,17 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_b
       }
     }
     sum3(s);
-    const float r = Wide<T>::inv_sqrt(fmaf(s[0], inv_d, a.eps));
+    const float r = inv_sqrt(fmaf(s[0], inv_d, a.eps), typename V::Value());
     const float m1 = s[1] * inv_d * r, m0 = a.layer ? s[2] * inv_d : 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = k * kGroup + lane;
       if (!live || i >= nvec) continue;
       float f[E], h[E], gf[E], rf[E];
-      Wide<T>::unpack(x[k], f);
-      Wide<T>::unpack(y[k], h);
-      Wide<T>::unpack(ptx::ld_shared_v4(g + i * 16), gf);
-      Wide<T>::unpack(res[k], rf);
+      V::unpack(x[k], f);
+      V::unpack(y[k], h);
+      V::unpack(V::shared(g + i * (int)sizeof(Raw)), gf);
+      V::unpack(res[k], rf);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float n = (f[e] - mu) * r, dn = h[e] * gf[e];
@@ -355,7 +394,7 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_b
         if constexpr (kBeta) db[k * E + e] += h[e];
         f[e] = fmaf(r, dn - fmaf(n, m1, m0), rf[e]);
       }
-      reinterpret_cast<uint4*>(a.dx + row * a.d)[i] = Wide<T>::pack(f);
+      reinterpret_cast<Raw*>(a.dx + row * a.d)[i] = V::pack(f);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -442,19 +481,59 @@ auto by_length(int nvec, F f) {
 #undef TG_CASE
 }
 
+// The same for rows of n single values, 4 or 8 of a thread (16 of the longest).
+constexpr int kMostSingles = 8192;
+template <typename F>
+auto by_count(int n, F f) {
+  using std::integral_constant;
+#define TG_CASE(G, N) f(integral_constant<int, G>(), integral_constant<int, N>())
+  if (n <= 32) return TG_CASE(8, 4);
+  if (n <= 128) return TG_CASE(32, 4);
+  if (n <= 256) return TG_CASE(32, 8);
+  if (n <= 512) return TG_CASE(64, 8);
+  if (n <= 1024) return TG_CASE(128, 8);
+  if (n <= 2048) return TG_CASE(256, 8);
+  if (n <= 4096) return TG_CASE(512, 8);
+  return TG_CASE(512, 16);
+#undef TG_CASE
+}
+
+template <typename V, int G, int N>
+cudaError_t forward_in(const NormArgs<typename V::Value>& a, cudaStream_t s) {
+  constexpr int B = kBlock<G>, R = B / G;
+  const int smem = 2 * a.d * (int)sizeof(typename V::Value);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_kernel<V, G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  norm_kernel<V, G, N><<<grid_of((a.rows + R - 1) / R, kForwardPerSm<G>), B, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename V, int G, int N>
+cudaError_t backward_in(const NormArgs<typename V::Value>& a, int* grid, cudaStream_t s) {
+  constexpr int B = kBlock<G>, R = B / G;
+  const auto kernel = a.want_beta ? norm_backward_kernel<V, G, N, true> : norm_backward_kernel<V, G, N, false>;
+  const int smem = (a.d * (int)sizeof(typename V::Value) + 15) / 16 * 16 + (R > 1 ? R * a.d * 4 : 0);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  *grid = grid_of((a.rows + R - 1) / R, kBackwardPerSm<G>);
+  kernel<<<*grid, B, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t norm_t(const NormCall& c, cudaStream_t s) {
   const NormArgs<T> a = norm_args<T>(c);
   if (in_registers(a))
-    return by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
-      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G>, R = B / G;
-      const int smem = 2 * c.d * (int)sizeof(T), per_sm = kForwardPerSm<G>;
-      if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(norm_kernel<T, G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-      }
-      norm_kernel<T, G, N><<<grid_of((c.rows + R - 1) / R, per_sm), B, smem, s>>>(a);
-      return cudaGetLastError();
+    return by_length(c.d / Wide<T>::E, [&](auto group, auto n) {
+      return forward_in<Wide<T>, decltype(group)::value, decltype(n)::value>(a, s);
+    });
+  if (c.d <= kMostSingles)
+    return by_count(c.d, [&](auto group, auto n) {
+      return forward_in<Single<T>, decltype(group)::value, decltype(n)::value>(a, s);
     });
   norm_any_kernel<T><<<grid_of(c.rows, 8), kThreads, 0, s>>>(a);
   return cudaGetLastError();
@@ -466,17 +545,12 @@ cudaError_t norm_backward_t(const NormCall& c, cudaStream_t s) {
   int grid = grid_of(c.rows, kBwdPerSm);
   cudaError_t e;
   if (in_registers(a)) {
-    e = by_length(c.d / Wide<T>::E, [&](auto group, auto nv) {
-      constexpr int G = decltype(group)::value, N = decltype(nv)::value, B = kBlock<G>, R = B / G;
-      const auto kernel = c.dbeta ? norm_backward_kernel<T, G, N, true> : norm_backward_kernel<T, G, N, false>;
-      const int smem = c.d * (int)sizeof(T) + (R > 1 ? R * c.d * 4 : 0);
-      if (smem > 48 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (err != cudaSuccess) return err;
-      }
-      grid = grid_of((c.rows + R - 1) / R, kBackwardPerSm<G>);
-      kernel<<<grid, B, smem, s>>>(a);
-      return cudaGetLastError();
+    e = by_length(c.d / Wide<T>::E, [&](auto group, auto n) {
+      return backward_in<Wide<T>, decltype(group)::value, decltype(n)::value>(a, &grid, s);
+    });
+  } else if (c.d <= kMostSingles) {
+    e = by_count(c.d, [&](auto group, auto n) {
+      return backward_in<Single<T>, decltype(group)::value, decltype(n)::value>(a, &grid, s);
     });
   } else {
     norm_backward_any_kernel<T><<<grid, kThreads, 0, s>>>(a);
