@@ -88,7 +88,7 @@ __device__ __forceinline__ float value_of(unsigned key) {
 
 // --------------------------------------------------------------------------- reductions
 
-template <int C> constexpr int kBins = 2 * kThreads<C>;
+constexpr int kMostBins = 4096;
 template <int C> constexpr int kList = kThreads<C>;
 template <int C> constexpr int kSpans = kThreads<C>;
 constexpr int kShort = 256;  // a list that is gone through twice per entry
@@ -97,7 +97,7 @@ template <int C>
 struct Shared {
   Exp2Table tab;
   uint64_t mass[kSpans<C>];     // kept mass of the row's spans
-  unsigned bins[kBins<C>];
+  unsigned bins[kMostBins];
   uint64_t order[kList<C>];     // the logits of the bins that hold a border: a number that falls along
                              // the row's order, (key, ~index)
   uint64_t w[kList<C>];
@@ -399,22 +399,29 @@ __device__ __forceinline__ Settings checked(Settings s, const SampleCall& c) {
 __device__ __forceinline__ uint64_t fraction(float u) { return (uint64_t)(u * 18446744073709551616.f); }
 
 // Bins of a row: equal steps of the logits from the largest one down to 2^-40 of its weight, or to
-// the lowest logit.
+// the lowest logit.  2 of each thread, or 8 for the largest vocabularies, whose bins would hold more
+// than the list.
 template <int C>
 struct Bins {
+  int each, count;
   float mx, per_unit, log2_step;
-  __device__ __forceinline__ Bins(float mx_, float low, float temp, Scale sc) : mx(mx_) {
+  __device__ __forceinline__ Bins(float mx_, float low, float temp, Scale sc, int vocab) : mx(mx_) {
+    each = vocab > 1 << 17 && C > 1 ? kMostBins / kThreads<C> : 2;
+    count = each * kThreads<C>;
     // 27.8 > 40 ln 2; logits that differ by less than 1e-30 may share a bin
     const float reach = fmaxf(fminf(27.8f * temp, __fsub_rn(mx, low)), 1e-30f);
-    per_unit = __fdiv_rn(kBins<C> - 1, reach);
+    per_unit = __fdiv_rn((float)(count - 1), reach);
     log2_step = sc.hi / per_unit;
   }
-  // distance from the largest in bins; outside where it is not below kBins<C> - 0.5 (NaN too)
+  // distance from the largest in bins; outside where it is not below count - 0.5 (NaN too)
   __device__ __forceinline__ float place(float x) const { return __fmul_rn(__fsub_rn(mx, x), per_unit); }
-  static __device__ __forceinline__ bool inside(float y) { return y < kBins<C> - 0.5f; }
+  __device__ __forceinline__ bool inside(float y) const { return y < (float)count - 0.5f; }
   // the nearest bin as 1.5 2^23 + bin: its low bits are the number
   static __device__ __forceinline__ float bin(float y) { return __fadd_rn(y, 12582912.f); }
   static __device__ __forceinline__ int number(float b) { return __float_as_int(b) - 0x4b400000; }
+  // the keys that bins first .. last and their neighbours may hold, but for roundings
+  __device__ __forceinline__ unsigned lowest_key(int last) const { return key_of(mx - (float)(last + 1) / per_unit); }
+  __device__ __forceinline__ unsigned highest_key(int first) const { return key_of(mx - (float)(first - 1) / per_unit); }
 };
 
 // The index of the m-th logit (from 1) that equals a key, or of the last one where there are
@@ -449,41 +456,67 @@ __device__ __noinline__ unsigned nth_equal(const Row<T, C>& row, unsigned key, u
   return g.largest(sh.found);
 }
 
-// Exact borders by bisection, for rows whose listed bins hold too many logits.
+// Exact borders by bisection between two keys, for rows whose listed bins hold too many logits (few
+// distinct ones, as a rule).  bf16 logits need the keys' upper half only.  The border is first
+// looked for in [lo, hi], and in all of [low, top] if it is not there.
+template <typename T> constexpr int kKeyShift = sizeof(T) == 2 ? 16 : 0;
+template <typename T>
+__device__ __forceinline__ unsigned short_key(float x) { return key_of(x) >> kKeyShift<T>; }
+template <typename T>
+__device__ __forceinline__ unsigned whole_key(unsigned k) {
+  return kKeyShift<T> == 0 ? k : k << 16 | (k & 0x8000u ? 0u : 0xffffu);
+}
+struct Between {
+  unsigned lo, hi, low, top;
+  template <typename T>
+  __device__ __forceinline__ Between shortened() const {
+    const Between b{max(lo, low) >> kKeyShift<T>, min(hi, top) >> kKeyShift<T>, low >> kKeyShift<T>, top >> kKeyShift<T>};
+    return b.lo <= b.hi ? b : Between{b.low, b.top, b.low, b.top};
+  }
+};
+
 template <typename T, int C>
-__device__ __noinline__ Cut bisect_count(const Row<T, C>& row, unsigned lo, unsigned hi, uint64_t k, Group<C>& g) {
+__device__ __noinline__ Cut bisect_count(const Row<T, C>& row, Between keys, uint64_t k, Group<C>& g) {
   auto count = [&](unsigned key) {  // logits of at least this key
     uint64_t n = 0;
-    row.template each<1>([&](float x, int) { n += x == x && key_of(x) >= key; });
+    row.template each<1>([&](float x, int) { n += x == x && short_key<T>(x) >= key; });
     return g.sum(n);
   };
-  while (lo < hi) {  // the largest key that at least k logits reach
-    const unsigned mid = lo + (hi - lo + 1) / 2;
-    if (count(mid) >= k) lo = mid;
-    else hi = mid - 1;
+  Between b = keys.shortened<T>();
+  if (b.lo > b.low && count(b.lo) < k) b.lo = b.low;
+  if (b.hi < b.top && count(b.hi + 1) >= k) b.hi = b.top;
+  while (b.lo < b.hi) {  // the largest key that at least k logits reach
+    const unsigned mid = b.lo + (b.hi - b.lo + 1) / 2;
+    if (count(mid) >= k) b.lo = mid;
+    else b.hi = mid - 1;
   }
-  return Cut{lo, nth_equal(row, lo, k - (lo < kFull ? count(lo + 1) : 0), g)};
+  const uint64_t above = b.lo < b.top ? count(b.lo + 1) : 0;
+  const unsigned key = whole_key<T>(b.lo);
+  return Cut{key, nth_equal(row, key, k - above, g)};
 }
 template <typename T, int C>
-__device__ __noinline__ Cut bisect_mass(const Row<T, C>& row, unsigned lo, unsigned hi, Cut within, uint64_t need, float mx,
-                                        Scale sc, Group<C>& g) {
+__device__ __noinline__ Cut bisect_mass(const Row<T, C>& row, Between keys, Cut within, uint64_t need, float mx, Scale sc,
+                                        Group<C>& g) {
   auto above = [&](unsigned key) {  // mass of the larger keys
     uint64_t n = 0;
     row.template each<1>([&](float x, int i) {
-      const unsigned k = key_of(x);
-      if (k > key && within.keeps(k, i)) n += weight(x, mx, sc, g.sh.tab);
+      if (short_key<T>(x) > key && within.keeps(key_of(x), i)) n += weight(x, mx, sc, g.sh.tab);
     });
     return g.sum(n);
   };
-  while (lo < hi) {  // the smallest key above which there is less than what is needed
-    const unsigned mid = lo + (hi - lo) / 2;
-    if (above(mid) < need) hi = mid;
-    else lo = mid + 1;
+  Between b = keys.shortened<T>();
+  if (b.hi < b.top && above(b.hi) >= need) b.hi = b.top;
+  if (b.lo > b.low && above(b.lo - 1) < need) b.lo = b.low;
+  while (b.lo < b.hi) {  // the smallest key above which there is less than what is needed
+    const unsigned mid = b.lo + (b.hi - b.lo) / 2;
+    if (above(mid) < need) b.hi = mid;
+    else b.lo = mid + 1;
   }
-  const uint64_t w = weight(value_of(lo), mx, sc, g.sh.tab);
-  if (w == 0) return Cut{lo, kFull};  // all of the mass is needed
-  const Cut cut{lo, nth_equal(row, lo, (need - above(lo) + w - 1) / w, g)};
-  return lo == within.key && within.last < cut.last ? within : cut;
+  const unsigned key = whole_key<T>(b.lo);
+  const uint64_t w = weight(value_of(key), mx, sc, g.sh.tab);
+  if (w == 0) return Cut{key, kFull};  // all of the mass is needed
+  const Cut cut{key, nth_equal(row, key, (need - above(b.lo) + w - 1) / w, g)};
+  return key == within.key && within.last < cut.last ? within : cut;
 }
 
 // The token of a row from its list, which holds all of the top_k logits.
@@ -585,11 +618,11 @@ __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel
     return;
   }
   const Scale sc = scale_of(s.temp);
-  const Bins<C> bins(mx, value_of(low), s.temp, sc);
+  const Bins<C> bins(mx, value_of(low), s.temp, sc, c.p.vocab);
   const uint64_t least = s.min_p > 0.f ? (uint64_t)ceilf(s.min_p * 17592186044416.f) : 0;  // 2^44
   const bool some_least = least > 0;
   auto clear_bins = [&] {
-    sh.bins[tid] = sh.bins[tid + kThreads<C>] = 0;
+    for (int i = tid; i < bins.count; i += kThreads<C>) sh.bins[i] = 0;
     if (tid == 0) sh.listed = 0, sh.answer = ~0ull;
     __syncthreads();
   };
@@ -613,18 +646,25 @@ __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel
       if (bins.inside(y)) atomicAdd(sh.bins + bins.number(bins.bin(y)), 1u);
     });
     g.sync();
-    unsigned c0 = 0, c1 = 0;
+    // the thread's bins of all blocks, those before them, and the one that holds the k-th
+    unsigned own = 0, total;
+    for (int j = 0; j < bins.each; j += 2)
 #pragma unroll
-    for (int q = 0; q < C; ++q) {
-      const uint2 n = *reinterpret_cast<const uint2*>(g.of(sh.bins + 2 * tid, q));
-      c0 += n.x;
-      c1 += n.y;
-    }
-    unsigned total;
-    const unsigned before = block_before<C>(c0 + c1, sh.ubuf[0], &total);
+      for (int q = 0; q < C; ++q) {
+        const uint2 n = *reinterpret_cast<const uint2*>(g.of(sh.bins, q) + tid * bins.each + j);
+        own += n.x + n.y;
+      }
+    unsigned before = block_before<C>(own, sh.ubuf[0], &total);
     if (total > k) {  // (else the k-th has less than 2^-40)
-      if (before < k && k <= before + c0) sh.first = 2 * tid, sh.last = before, sh.found = c0;
-      else if (before + c0 < k && k <= before + c0 + c1) sh.first = 2 * tid + 1, sh.last = before + c0, sh.found = c1;
+      if (before < k && k <= before + own) {
+        for (int j = 0; j < bins.each; ++j) {
+          unsigned n = 0;
+#pragma unroll
+          for (int q = 0; q < C; ++q) n += g.of(sh.bins, q)[tid * bins.each + j];
+          if (before < k && k <= before + n) sh.first = tid * bins.each + j, sh.last = before, sh.found = n;
+          before += n;
+        }
+      }
       __syncthreads();
       const int bin = sh.first;
       some_cut = true;
@@ -653,7 +693,7 @@ __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel
         g.sync();
         cut = cut_at(home->answer);
       } else {
-        cut = bisect_count(row, low, top, k, g);
+        cut = bisect_count(row, Between{bins.lowest_key(bin), bins.highest_key(bin), low, top}, k, g);
         sh.mass[tid] = 0;
       }
     }
@@ -670,21 +710,35 @@ __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel
       atomicAdd(sh.bins + bins.number(b), (unsigned)(__float_as_int(q + 8388608.f) - 0x4b000000));
     });
     g.sync();
-    float m0 = 0.f, m1 = 0.f;
+    // the first bins that reach the share less and more the error
+    float m[kMostBins / kThreads<8>], own = 0.f, all;
 #pragma unroll
-    for (int q = 0; q < C; ++q) {
-      const uint2 n = *reinterpret_cast<const uint2*>(g.of(sh.bins + 2 * tid, q));
-      m0 += (float)n.x;
-      m1 += (float)n.y;
+    for (int j = 0; j < kMostBins / kThreads<8>; j += 2) {
+      m[j] = m[j + 1] = 0.f;
+      if (j >= bins.each) continue;
+      const int b = tid * bins.each + j;
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        const uint2 n = *reinterpret_cast<const uint2*>(g.of(sh.bins, q) + b);
+        m[j] += (float)n.x;
+        m[j + 1] += (float)n.y;
+      }
+      own += m[j] *= ptx::ex2_approx((float)-b * bins.log2_step);
+      own += m[j + 1] *= ptx::ex2_approx((float)(-b - 1) * bins.log2_step);
     }
-    m0 *= ptx::ex2_approx((float)(-2 * tid) * bins.log2_step);
-    m1 *= ptx::ex2_approx((float)(-2 * tid - 1) * bins.log2_step);
-    float all;
-    const float before = block_before<C>(m0 + m1, sh.fbuf, &all);
+    float reached = block_before<C>(own, sh.fbuf, &all);
     const float share = s.top_p > 0.f ? s.top_p : 0.f, from = share * all * (1.f - 3e-5f), to = share * all * (1.f + 3e-5f);
-    const unsigned b0 = 2 * tid, none = kBins<C> - 1;
-    const unsigned f = __reduce_min_sync(kFull, before + m0 >= from ? b0 : before + m0 + m1 >= from ? b0 + 1 : none);
-    const unsigned t = __reduce_min_sync(kFull, before + m0 >= to ? b0 : before + m0 + m1 >= to ? b0 + 1 : none);
+    unsigned f = bins.count - 1, t = f;
+#pragma unroll
+    for (int j = 0; j < kMostBins / kThreads<8>; ++j) {
+      if (j >= bins.each) continue;
+      reached += m[j];
+      const unsigned b = tid * bins.each + j;
+      if (reached >= from) f = min(f, b);
+      if (reached >= to) t = min(t, b);
+    }
+    f = __reduce_min_sync(kFull, f);
+    t = __reduce_min_sync(kFull, t);
     if (lane == 0) sh.ubuf[0][warp] = f, sh.ubuf[1][warp] = t;
     __syncthreads();
     const int first = __reduce_min_sync(kFull, sh.ubuf[0][lane & (kWarps<C> - 1)]);
@@ -735,7 +789,8 @@ __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel
     if (order != ~0ull) {
       cut = cut_at(order);
     } else {
-      cut = bisect_mass(row, max(low, cut.key), top, cut, need, mx, sc, g);
+      const Between keys{bins.lowest_key(last), bins.highest_key(first), max(low, cut.key), top};
+      cut = bisect_mass(row, keys, cut, need, mx, sc, g);
       sh.mass[tid] = 0;
       __syncthreads();
       row.sum_spans(sh.mass, [&](float x, int i) {

@@ -520,6 +520,23 @@ def test_sample_ties(lib, dt):
             check_sample(x, u, T, k, p, m)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_sample_many_close_logits(lib, dt):
+    """More logits between two bins' borders than the kernel lists: few distinct values, the largest
+    vocabulary, values that differ in their last bits only."""
+    gen = generator(18)
+    u = torch.rand(3, generator=gen, device="cuda")
+    near = (1000 + torch.rand(3, 40000, generator=gen, device="cuda") * 1e-2).to(dt)
+    few = (torch.randint(-6, 7, (3, 50000), generator=gen, device="cuda") / 4).to(dt)
+    wide = normal(gen, 3, 1 << 19, dt=dt, scale=1.5)
+    two = normal(gen, 3, 20000, dt=dt)
+    two[:, 1:] = two[:, :-1].clamp(-0.25, 0.25).sign()
+    for x in (near, few, wide, two, -near):
+        for T, k, p, m in ((1.0, 0, 0.9, 0.0), (0.7, 15000, 1.0, 0.0), (1.3, 19000, 0.6, 0.0), (1e-3, 0, 0.5, 0.0), (30.0, 9999, 0.999, 0.1)):
+            check_sample(x, u, T, k, p, m)
+    no_error()
+
+
 def test_sample_extremes_of_u(lib):
     x = normal(generator(14), 6, 3001, scale=4.0)
     u = torch.tensor([0.0, 2.0 ** -24, 2.0 ** -30, 0.99999994, 0.5, 1e-38], device="cuda")
