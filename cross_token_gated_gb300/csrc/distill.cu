@@ -15,6 +15,7 @@
 #include "tg_ends.h"
 #include "tg_ptx.cuh"
 #include "tg_serve.h"
+#include "tg_vec.cuh"
 
 namespace tg {
 namespace {
@@ -47,9 +48,8 @@ __device__ __forceinline__ float warp_max(float v) {
 
 enum Mode { kLoss, kGradFromStats, kGradAndLoss };
 
-template <typename T> struct Wide;  // 16 bytes of T
-template <> struct Wide<float> {
-  static constexpr int E = 4;
+template <typename T> struct Wide;
+template <> struct Wide<float> : Vec16<float> {
   static __device__ __forceinline__ float largest(const uint4& u) {
     return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
   }
@@ -57,12 +57,8 @@ template <> struct Wide<float> {
     p[0] = ptx::f32x2_pack(__uint_as_float(u.x), __uint_as_float(u.y));
     p[1] = ptx::f32x2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
 };
-template <> struct Wide<__nv_bfloat16> {
-  static constexpr int E = 8;
+template <> struct Wide<__nv_bfloat16> : Vec16<__nv_bfloat16> {
   static __device__ __forceinline__ __nv_bfloat162 two(unsigned x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
   static __device__ __forceinline__ float largest(const uint4& u) {
     const __nv_bfloat162 m = __hmax2(__hmax2(two(u.x), two(u.y)), __hmax2(two(u.z), two(u.w)));
@@ -70,10 +66,6 @@ template <> struct Wide<__nv_bfloat16> {
   }
   static __device__ __forceinline__ void pairs(const uint4& u, uint64_t* p) {
     p[0] = ptx::bf16x2_widen(u.x); p[1] = ptx::bf16x2_widen(u.y); p[2] = ptx::bf16x2_widen(u.z); p[3] = ptx::bf16x2_widen(u.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    return make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]), ptx::pack_bf16x2(f[4], f[5]),
-                      ptx::pack_bf16x2(f[6], f[7]));
   }
 };
 
@@ -86,8 +78,7 @@ template <typename T>
 __device__ __forceinline__ RowSpan row_span(const T* row, int vocab) {
   constexpr int E = Wide<T>::E;
   RowSpan r;
-  r.lead = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);
-  if (r.lead > vocab) r.lead = vocab;
+  r.lead = row_lead(row, vocab);
   r.nvec = (vocab - r.lead) / E;
   r.edge = vocab - r.nvec * E;
   return r;

@@ -12,39 +12,21 @@
 #include "tg_ends.h"
 #include "tg_ptx.cuh"
 #include "tg_serve.h"
+#include "tg_vec.cuh"
 
 namespace tg {
 namespace {
 
-// A kernel's launch that may start while the one before it still runs; it waits itself.
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------------------- lookup
 
-// E values of 16 bytes times s, each rounded once.
-__device__ __forceinline__ uint4 scaled(uint4 u, float s, float) {
-  return make_uint4(__float_as_uint(__uint_as_float(u.x) * s), __float_as_uint(__uint_as_float(u.y) * s),
-                    __float_as_uint(__uint_as_float(u.z) * s), __float_as_uint(__uint_as_float(u.w) * s));
-}
-__device__ __forceinline__ uint4 scaled(uint4 u, float s, __nv_bfloat16) {
-  return make_uint4(ptx::pack_bf16x2(ptx::bf16lo(u.x) * s, ptx::bf16hi(u.x) * s),
-                    ptx::pack_bf16x2(ptx::bf16lo(u.y) * s, ptx::bf16hi(u.y) * s),
-                    ptx::pack_bf16x2(ptx::bf16lo(u.z) * s, ptx::bf16hi(u.z) * s),
-                    ptx::pack_bf16x2(ptx::bf16lo(u.w) * s, ptx::bf16hi(u.w) * s));
+// A vector's values times s, each rounded once.
+template <typename T>
+__device__ __forceinline__ uint4 scaled(const uint4& u, float s) {
+  float f[Vec16<T>::E];
+  Vec16<T>::unpack(u, f);
+#pragma unroll
+  for (int e = 0; e < Vec16<T>::E; ++e) f[e] *= s;
+  return Vec16<T>::pack(f);
 }
 
 // One warp per row, 16 bytes a lane (kVec) or single values.  A scale of 1 copies the bits.
@@ -66,7 +48,7 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const int* ids, const
   for (int c = lane * N; c < d; c += 32 * N) {
     if constexpr (kVec) {
       const uint4 u = live ? *reinterpret_cast<const uint4*>(src + c) : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(dst + c) = scale == 1.f ? u : scaled(u, scale, T());
+      *reinterpret_cast<uint4*>(dst + c) = scale == 1.f ? u : scaled<T>(u, scale);
     } else {
       if (!live) dst[c] = T(0.f);
       else if (scale == 1.f) dst[c] = src[c];
@@ -234,21 +216,6 @@ constexpr int kRows = 8;      // rows of dout that a warp has under way
 constexpr int kFill = 4;      // ids of a warp that writes rows without tokens
 constexpr int kGroup = 32;    // parts of an id's sum that are joined first
 
-template <typename T> struct Wide;  // 16 bytes of T
-template <> struct Wide<float> {
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void add(const uint4& u, float* f) {
-    f[0] += __uint_as_float(u.x); f[1] += __uint_as_float(u.y); f[2] += __uint_as_float(u.z); f[3] += __uint_as_float(u.w);
-  }
-};
-template <> struct Wide<__nv_bfloat16> {
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void add(const uint4& u, float* f) {
-    f[0] += ptx::bf16lo(u.x); f[1] += ptx::bf16hi(u.x); f[2] += ptx::bf16lo(u.y); f[3] += ptx::bf16hi(u.y);
-    f[4] += ptx::bf16lo(u.z); f[5] += ptx::bf16hi(u.z); f[6] += ptx::bf16lo(u.w); f[7] += ptx::bf16hi(u.w);
-  }
-};
-
 template <typename T, typename G>
 struct SumArgs {
   const int *order, *sorted, *start, *count, *total;
@@ -327,7 +294,7 @@ __device__ __forceinline__ void finish_vec(__nv_bfloat16* dst, const float* f, f
 // A warp's columns of a tile: lane l holds a vector (kVec), or 4 single columns.
 template <typename T, bool kVec>
 struct Columns {
-  static constexpr int E = kVec ? Wide<T>::E : 1, NV = kVec ? 1 : 4, N = NV * E, kTile = 32 * N;
+  static constexpr int E = kVec ? Vec16<T>::E : 1, NV = kVec ? 1 : 4, N = NV * E, kTile = 32 * N;
   float f[N];
   int c0;  // first column of the tile
   __device__ __forceinline__ int col(int k) const { return c0 + (k * 32 + (int)(threadIdx.x & 31)) * E; }
@@ -490,8 +457,14 @@ __global__ void __launch_bounds__(256, kVec && !kBase ? 3 : 2) embed_sum_kernel(
       if (i0 + i >= n) break;
 #pragma unroll
       for (int k = 0; k < Cols::NV; ++k) {
-        if constexpr (kVec) Wide<T>::add(u[i][k], acc.f + k * Cols::E);
-        else acc.f[k] += f[i][k];
+        if constexpr (kVec) {
+          float x[Cols::E];
+          Vec16<T>::unpack(u[i][k], x);
+#pragma unroll
+          for (int e = 0; e < Cols::E; ++e) acc.f[k * Cols::E + e] += x[e];
+        } else {
+          acc.f[k] += f[i][k];
+        }
       }
       const int v = __shfl_sync(0xffffffffu, id, i0 + i);
       const bool last = i0 + i == n - 1;
@@ -538,7 +511,6 @@ int sort_rows(int vocab) {
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // How the sums are taken, from the sizes alone (the workspace's size depends on it).
 struct EmbedPlan {
@@ -569,7 +541,7 @@ EmbedPlan embed_plan(const EmbedCall& c, bool vec) {
 // Whether rows of dout, base and dE are read and written 16 bytes at a time.
 bool vector_rows(const EmbedCall& c) {
   const int E = c.dtype == TG_F32 ? 4 : 8;
-  return c.d % E == 0 && c.pitch % E == 0 && aligned16(c.dout) && aligned16(c.base) && aligned16(c.dE);
+  return c.d % E == 0 && c.pitch % E == 0 && aligned_16(c.dout) && aligned_16(c.base) && aligned_16(c.dE);
 }
 
 template <typename T, typename G>
@@ -594,7 +566,7 @@ cudaError_t lookup(const EmbedCall& c, cudaStream_t s) {
   T* out = static_cast<T*>(c.out);
   constexpr int N = 16 / sizeof(T);
   const unsigned blocks = (unsigned)((c.rows + 7) / 8);
-  const auto kernel = c.d % N == 0 && c.pitch % N == 0 && aligned16(c.E) && aligned16(c.out) ? embed_lookup_kernel<T, true>
+  const auto kernel = c.d % N == 0 && c.pitch % N == 0 && aligned_16(c.E) && aligned_16(c.out) ? embed_lookup_kernel<T, true>
                                                                                          : embed_lookup_kernel<T, false>;
   kernel<<<blocks, 256, 0, s>>>(c.ids, E, out, c.rows, c.d, c.vocab, c.pitch, c.scale, c.pad_id, c.padded, c.err);
   return cudaGetLastError();

@@ -14,6 +14,7 @@
 #include "tg_ends.h"
 #include "tg_ptx.cuh"
 #include "tg_serve.h"
+#include "tg_vec.cuh"
 
 #include <type_traits>
 
@@ -116,31 +117,10 @@ __global__ void __launch_bounds__(kThreads) norm_backward_any_kernel(const NormA
 // ------------------------------------------------------------------- rows in registers
 
 // A thread's share of a row comes in vectors: 16 bytes, or single values where rows are not aligned.
-template <typename T> struct Wide;
-template <> struct Wide<float> {
-  using Value = float;
+template <typename T>
+struct Wide : Vec16<T> {
+  using Value = T;
   using Raw = uint4;
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
-    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
-  static __device__ __forceinline__ uint4 shared(uint32_t a) { return ptx::ld_shared_v4(a); }
-};
-template <> struct Wide<__nv_bfloat16> {
-  using Value = __nv_bfloat16;
-  using Raw = uint4;
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
-    f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
-    f[4] = ptx::bf16lo(u.z); f[5] = ptx::bf16hi(u.z); f[6] = ptx::bf16lo(u.w); f[7] = ptx::bf16hi(u.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    return make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]), ptx::pack_bf16x2(f[4], f[5]),
-                      ptx::pack_bf16x2(f[6], f[7]));
-  }
   static __device__ __forceinline__ uint4 shared(uint32_t a) { return ptx::ld_shared_v4(a); }
 };
 template <typename T> struct Single;
@@ -402,7 +382,7 @@ __global__ void __launch_bounds__(kBlock<kGroup>, kBackwardPerSm<kGroup>) norm_b
       y[k] = next_y[k];
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   if (a.want_gamma) block_columns<kGroup, NV, E>(dg, columns, a.part + (size_t)blockIdx.x * a.d, a.d);
   if constexpr (kBeta) block_columns<kGroup, NV, E>(db, columns, a.part + ((size_t)gridDim.x + blockIdx.x) * a.d, a.d);
 }
@@ -414,7 +394,7 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* part
   __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   float* dst = blockIdx.y ? dbeta : dgamma;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   if (!dst) return;
   float s = 0.f;
   if (c < d) {
@@ -446,15 +426,13 @@ int grid_of(long long rows, int per_sm) {
   return (int)(rows < most ? rows : most);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // Whether rows are taken 16 bytes at a time and fit the registers of at most 512 threads.
 template <typename T>
 bool in_registers(const NormArgs<T>& a) {
   constexpr int E = Wide<T>::E;
   const void* ptrs[] = {a.x, a.gamma, a.beta, a.dy, a.dres, a.y, a.dx};
   for (const void* p : ptrs)
-    if (!aligned16(p)) return false;
+    if (!aligned_16(p)) return false;
   return a.d % E == 0 && a.x_pitch % E == 0 && a.d / E <= 2048;
 }
 
@@ -557,16 +535,7 @@ cudaError_t norm_backward_t(const NormCall& c, cudaStream_t s) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || !(c.dgamma || c.dbeta)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ceil_div(c.d, 32), 2);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_weight_sum_kernel, (const float*)a.part, grid, c.d, c.dgamma, c.dbeta);
+  return launch_early(norm_weight_sum_kernel, dim3(ceil_div(c.d, 32), 2), 1024, s, (const float*)a.part, grid, c.d, c.dgamma, c.dbeta);
 }
 
 }  // namespace

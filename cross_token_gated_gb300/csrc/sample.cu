@@ -15,6 +15,7 @@
 #include "tg_exp2_table.cuh"
 #include "tg_ptx.cuh"
 #include "tg_serve.h"
+#include "tg_vec.cuh"
 
 namespace tg {
 namespace {
@@ -237,12 +238,8 @@ struct Cut {
   __device__ __forceinline__ bool keeps(unsigned k, unsigned i) const { return k > key || (k == key && i <= last); }
 };
 
-template <typename T> struct Wide;  // 16 bytes of T
-template <> struct Wide<float> {
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
-    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-  }
+template <typename T> struct Wide;
+template <> struct Wide<float> : Vec16<float> {
   // largest and lowest of all so far, NaN left out
   static __device__ __forceinline__ void range(const uint4& u, float& top, float& low) {
     float f[4];
@@ -251,12 +248,7 @@ template <> struct Wide<float> {
     low = fminf(fminf(low, fminf(f[0], f[1])), fminf(f[2], f[3]));
   }
 };
-template <> struct Wide<__nv_bfloat16> {
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
-    f[0] = ptx::bf16lo(u.x); f[1] = ptx::bf16hi(u.x); f[2] = ptx::bf16lo(u.y); f[3] = ptx::bf16hi(u.y);
-    f[4] = ptx::bf16lo(u.z); f[5] = ptx::bf16hi(u.z); f[6] = ptx::bf16lo(u.w); f[7] = ptx::bf16hi(u.w);
-  }
+template <> struct Wide<__nv_bfloat16> : Vec16<__nv_bfloat16> {
   static __device__ __forceinline__ __nv_bfloat162 two(unsigned x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
   static __device__ __forceinline__ void range(const uint4& u, float& top, float& low) {
     const __nv_bfloat162 a = two(u.x), b = two(u.y), c = two(u.z), d = two(u.w);
@@ -277,7 +269,7 @@ struct Row {
   int rank, v0, nvec;      // of this block: first vector, vectors
   int head, edge, wide;    // single elements before the vectors, single elements in all
   __device__ __forceinline__ Row(const T* row, int vocab, int block) : x(row), V(vocab), rank(block) {
-    lead = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
+    lead = row_lead(row, vocab);
     all = (vocab - lead) / E;
     per = C == 1 ? all : ((all + 31) / 32 + C - 1) / C * 32;
     v0 = min(rank * per, all);
