@@ -7,8 +7,12 @@
 // Bound by HBM: the logits are read once and the gradient written once.  A block takes a row at a
 // time and keeps it in registers, as the 16-byte vectors that were loaded, from its largest value
 // and sum (formed at once, per thread, and joined over one barrier) to its gradient; rows that are
-// longer are taken in batches and read again, mostly from L2.  One warp more than the row needs
-// prepares the next row's teacher entries and forms the loss meanwhile.
+// longer are taken in batches and read again, mostly from L2.  The next vectors are on their way to
+// shared memory meanwhile.  One or two warps more than the row needs prepare the next rows' teacher
+// entries, in steps a row apart so that none waits for its loads, and form the loss.
+//
+// Loss of 8,192 rows of 32,768 bf16 logits: 90 us (6.0 TB/s of a measured copy's 6.8); without the
+// fetch ahead and the steps 154 us.  Gradient of 16,384 rows: 338 us (6.4 TB/s), 547 us without.
 #include <math.h>
 
 #include "tg_common.cuh"

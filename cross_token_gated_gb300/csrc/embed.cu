@@ -8,6 +8,10 @@
 // dout in fp32 in equal chunks, so that a frequent token loads no warp more than a rare one; sums
 // that cross chunks are joined in order by the warp that comes last.  The rows of ids without tokens
 // are written by the same launch.
+//
+// 16,384 tokens of 512 bf16 values into 32,768 fp32 rows: 25 us (floor 12.4), most of it the sums,
+// whose first loads wait for order, row and neighbour in a row.  5,003 fp32 tokens of 768 onto a
+// base: 51 us (floor 32), most of it the copy of the base.
 #include "tg_common.cuh"
 #include "tg_ends.h"
 #include "tg_ptx.cuh"

@@ -653,7 +653,8 @@ tg_status tango_norm(const tg_norm_params *p, const void *x, const void *gamma, 
  * reaches x past the norm (a residual stream's).  dx: device [rows, d], written; may be dy, dres or
  * a dense x.  dgamma, dbeta: device float[d], written (summed in a fixed order), or NULL; dgamma
  * needs gamma.  ws: device scratch of tg_workspace_size(TG_WS_NORM_BWD, p) bytes, 256-byte aligned
- * (not used, and may be NULL, without dgamma and dbeta).
+ * (not used, and may be NULL, without dgamma and dbeta).  The size follows the current device's
+ * number of SMs: ask for it with the device current that the call runs on.
  */
 tg_status tango_norm_backward(const tg_norm_params *p, const void *x, const void *gamma, const void *dy,
                               const void *dres, void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
@@ -675,7 +676,8 @@ tg_status tango_norm_backward(const tg_norm_params *p, const void *x, const void
  * with t = -inf, is absent; an id >= vocab is absent too and flagged TG_ERR_DEVICE (kernel code
  * 7).  A token may stand in several entries.  A row without entries (padding) has loss 0 and
  * gradient 0.  Student logits of -inf have q = 0 (an entry there gives loss inf; its gradient is
- * finite); a row with NaN gives NaN.
+ * finite); a row with NaN gives NaN, as does a student's +inf; a teacher's +inf gives loss NaN and
+ * NaN in its entries' columns.
  */
 typedef struct {
     long long rows;

@@ -402,6 +402,26 @@ def test_distill_masked_and_extreme_logits(lib, dt):
         assert l[6] == 0 and l[7] == 0 and (g[6:] == 0).all()
 
 
+@pytest.mark.parametrize("V", [777, 40000])
+@pytest.mark.parametrize("dt", [F32, BF], ids=["fp32", "bf16"])
+def test_distill_infinite_logits(lib, dt, V):
+    # +inf: softmax has inf - inf.  A student's reaches the whole row, a teacher's its entries' columns.
+    gen = generator(9)
+    z, t, ids = distill_inputs(gen, 3, V, 5, dt)
+    ids[:] = torch.tensor([0, 5, 9, V // 2, V - 1], device="cuda", dtype=I32)
+    want_z, want_t = z[2:].clone(), t[2:].clone()
+    z[0, 3], t[1, 2] = math.inf, math.inf
+    loss, dz = torch.empty(3, device="cuda"), torch.empty_like(z)
+    tg.tango_distill_backward(z, t, ids, torch.ones(3, device="cuda"), dz, loss=loss)
+    assert loss[:2].isnan().all() and dz[0].isnan().all()
+    entries = torch.zeros(V, dtype=torch.bool, device="cuda")
+    entries[ids[1].long()] = True
+    assert dz[1, entries].isnan().all() and torch.isfinite(dz[1, ~entries]).all()
+    # The finite row is held to the bounds on sums, not to its bits alone: row 2 of 777 bf16 values starts
+    # 3,108 = 194 * 16 + 4 bytes in, so its vectors, and with them the order of its sums, are others.
+    check_distill(want_z, want_t, ids[2:], 1.0, torch.ones(1, device="cuda"), loss[2:], dz[2:])
+
+
 def test_distill_is_cross_entropy_with_one_entry(lib):
     gen = generator(8)
     z = normal(gen, 50, 999, scale=3.0)
