@@ -517,6 +517,93 @@ __device__ __noinline__ Cut bisect_mass(const Row<T, C>& row, Between keys, Cut 
   return key == within.key && within.last < cut.last ? within : cut;
 }
 
+// The list's kept entries join their spans, the last of them is the cut; `sure` is the mass before
+// the list.  No cut (all ones) where the list is too long or does not hold the border.  All blocks
+// have to be through with the list.
+template <typename T, int C>
+__device__ __forceinline__ uint64_t join_list(const Row<T, C>& row, uint64_t sure, uint64_t need, uint64_t least, Group<C>& g) {
+  Shared<C>& sh = g.sh;
+  const int n = sh.listed;
+  if (g.rank == 0 && n <= kList<C> && (int)threadIdx.x < n && sure < need) {
+    const uint64_t mine = sh.order[threadIdx.x], w = sh.w[threadIdx.x];
+    uint64_t before = sure;
+    for (int j = 0; j < n; ++j) before += sh.order[j] > mine ? sh.w[j] : 0;
+    if (before < need) {
+      const int i = kFull - (unsigned)mine;
+      if (w >= least) atomicAdd((unsigned long long*)g.of(sh.mass, row.owner(i)) + row.span_of(i), (unsigned long long)w);
+      if (before + w >= need) sh.answer = mine;
+    }
+  }
+  g.sync();
+  return g.of(&sh, 0)->answer;
+}
+
+// The border of the mass where bins first .. last hold too many logits for the list, which is so
+// from a top_p of some 0.9995 on: their exact masses in kSteps finer steps of equal width, and a list
+// of the one step that holds the border.  Two passes in place of a bisection's many.
+template <typename T, int C>
+__device__ __noinline__ uint64_t finer_border(const Row<T, C>& row, const Bins<C>& bins, int first, int last, Cut within,
+                                              uint64_t sure, uint64_t need, uint64_t least, float mx, Scale sc, Group<C>& g) {
+  using u64 = unsigned long long;
+  constexpr int kSteps = kMostBins / 2, kEach = kSteps / kThreads<C>;
+  Shared<C>& sh = g.sh;
+  Shared<C>* const home = g.of(&sh, 0);
+  const int tid = threadIdx.x;
+  u64* const steps = reinterpret_cast<u64*>(sh.bins);
+  g.sync();  // all have read that there is no answer yet
+  for (int j = 0; j < kEach; ++j) steps[tid + j * kThreads<C>] = 0;
+  sh.mass[tid] = 0;
+  if (tid == 0) sh.listed = 0, sh.answer = ~0ull, sh.first = -1;
+  g.sync();
+  const float first_bin = 12582912.f + first, last_bin = 12582912.f + last;
+  const float start = (float)first - 0.5f, per_bin = __fdiv_rn((float)kSteps, (float)(last - first + 1));
+  // falls with x, as each of its roundings keeps the order
+  auto step = [&](float y) { return max(0, min(kSteps - 1, (int)__fmul_rn(__fsub_rn(y, start), per_bin))); };
+  row.template each<1>([&](float x, int i) {
+    const float y = bins.place(x), b = bins.bin(y);
+    if (!(b >= first_bin && b <= last_bin) || !within.keeps(key_of(x), i)) return;
+    const uint64_t w = weight(x, mx, sc, sh.tab);
+    if (w) atomicAdd(steps + step(y), (u64)w);
+  });
+  g.sync();
+  uint64_t m[kEach], own = 0, total;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    m[j] = 0;
+#pragma unroll
+    for (int q = 0; q < C; ++q) m[j] += g.of(steps, q)[tid * kEach + j];
+    own += m[j];
+  }
+  uint64_t before = sure + block_before<C>(own, sh.buf, &total);
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    if (before < need && need <= before + m[j]) sh.first = tid * kEach + j, sh.rest = before;
+    before += m[j];
+  }
+  __syncthreads();
+  const int at = sh.first;
+  if (at >= 0) {  // (the same in all blocks)
+    sure = sh.rest;
+    row.sum_spans(sh.mass, [&](float x, int i) -> uint64_t {
+      const float y = bins.place(x), b = bins.bin(y);
+      if (!(b <= last_bin) || !within.keeps(key_of(x), i)) return 0;
+      const int n = b < first_bin ? -1 : step(y);
+      if (n > at) return 0;
+      const uint64_t w = weight(x, mx, sc, sh.tab);
+      if (n < at) return w >= least ? w : 0;
+      if (w == 0) return 0;
+      const int e = atomicAdd(&home->listed, 1);
+      if (e < kList<C>) {
+        home->order[e] = (uint64_t)key_of(x) << 32 | (kFull - (unsigned)i);
+        home->w[e] = w;
+      }
+      return 0;
+    });
+  }
+  g.sync();
+  return at >= 0 ? join_list(row, sure, need, least, g) : ~0ull;
+}
+
 // The token of a row from its list, which holds all of the top_k logits.
 template <int C>
 __device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings& s, long long r, uint64_t least, Shared<C>& sh) {
@@ -554,8 +641,9 @@ __device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings&
 
 // C blocks per row.  A border (of the k-th logit, or of the share of the mass) is found with a
 // histogram of counts, or of masses good to about 1e-5; only the logits of the bins that may hold it
-// are listed and compared one by one, in exact sums.  Should there be too many of them, the
-// border is bisected.
+// are listed and compared one by one, in exact sums.  Should there be too many of them, a border of
+// the mass is looked for in finer steps; what is too many then (many equal logits), and a border of
+// the counts, is bisected.
 template <typename T, int C>
 __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel(const SampleCall c) {
   using u64 = unsigned long long;
@@ -770,20 +858,8 @@ __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel
     const uint64_t p = fraction(share);
     uint64_t need = __umul64hi(p, mass) + (p * mass != 0);
     if (need == 0) need = 1;
-    if (g.rank == 0 && sh.listed <= kList<C> && tid < sh.listed && sure < need) {
-      // the list: its kept entries join their spans, the last of them is the cut
-      const int n = sh.listed;
-      const uint64_t mine = sh.order[tid], w = sh.w[tid];
-      uint64_t before = sure;
-      for (int j = 0; j < n; ++j) before += sh.order[j] > mine ? sh.w[j] : 0;
-      if (before < need) {
-        const int i = kFull - (unsigned)mine;
-        if (w >= least) atomicAdd((u64*)g.of(sh.mass, row.owner(i)) + row.span_of(i), (u64)w);
-        if (before + w >= need) sh.answer = mine;
-      }
-    }
-    g.sync();
-    const uint64_t order = home->answer;
+    uint64_t order = join_list(row, sure, need, least, g);
+    if (order == ~0ull) order = finer_border(row, bins, first, last, cut, sure, need, least, mx, sc, g);
     if (order != ~0ull) {
       cut = cut_at(order);
     } else {

@@ -557,6 +557,24 @@ def test_sample_many_close_logits(lib, dt):
     no_error()
 
 
+@pytest.mark.parametrize("rows,V", [(1, 32768), (5, 32771), (30, 131072), (60, 32768), (170, 32771), (2, 400001)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_sample_shares_near_one(lib, rows, V, dt):
+    """The border of the mass deep in the tail, where the bins about it hold thousands of logits, with
+    the lowest drawn tokens among them."""
+    gen = generator(19 + rows)
+    x = normal(gen, rows, V, dt=dt, scale=2.0)
+    u = torch.rand(rows, generator=gen, device="cuda")
+    u[::3] = 1 - u[::3] * 1e-4
+    u.clamp_(max=0.99999994)
+    near = torch.tensor([0.9993, 0.9997, 0.9999, 0.99999, 0.999999, 0.99999994], device="cuda")
+    p = near[torch.randint(0, 6, (rows,), generator=gen, device="cuda")]
+    for T, k, m in ((1.0, 0, 0.0), (0.8, 0, 1e-3), (2.5, V - V // 8, 0.0), (1.0, V // 2, 1e-4)):
+        check_sample(x, u, T, k, p, m)
+    check_sample(x, u, 0.8, 0, 0.9999, 0.0)
+    no_error()
+
+
 def test_sample_extremes_of_u(lib):
     x = normal(generator(14), 6, 3001, scale=4.0)
     u = torch.tensor([0.0, 2.0 ** -24, 2.0 ** -30, 0.99999994, 0.5, 1e-38], device="cuda")
