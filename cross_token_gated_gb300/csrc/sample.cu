@@ -13,7 +13,7 @@
 // histogram and one with exact weights (about 76 instructions a logit, from the issue rate and the
 // cycles of 61 fp32 rows).  One row of 32,768 bf16 logits
 // with top-p takes 16.6 us on 8 blocks; 256 rows with settings of their own 36 us, with top-k 50 and top-p
-// 26 us, greedily 12 us.
+// 26 us, greedily 12 us.  A border deep in the tail (top-p 0.9999) takes one row 50 us, 256 rows 103 us.
 #include <math.h>
 
 #include "tg_common.cuh"
@@ -540,7 +540,8 @@ __device__ __forceinline__ uint64_t join_list(const Row<T, C>& row, uint64_t sur
 
 // The border of the mass where bins first .. last hold too many logits for the list, which is so
 // from a top_p of some 0.9995 on: their exact masses in kSteps finer steps of equal width, and a list
-// of the one step that holds the border.  Two passes in place of a bisection's many.
+// of the one step that holds the border.  Two passes in place of a bisection's many (256 rows of 32,768
+// with top_p 0.9999: 103 us, 281 us bisected).
 template <typename T, int C>
 __device__ __noinline__ uint64_t finer_border(const Row<T, C>& row, const Bins<C>& bins, int first, int last, Cut within,
                                               uint64_t sure, uint64_t need, uint64_t least, float mx, Scale sc, Group<C>& g) {

@@ -16,6 +16,12 @@
  *                          respect to q, k, g and v), for training (sec. 3); the
  *                          tango_aggregate_save / wango_aggregate_save forwards keep what
  *                          they need
+ *   - tango_qk_norm_rope (and _backward), tango_cache_append, tango_paged_aggregate
+ *                          norm and rotation of q and k, and serving from a paged cache
+ *   - tango_embed, tango_norm, tango_distill (each with _backward), tango_sample
+ *                          the model's two ends (sec. 2.3) for training and generation: token
+ *                          lookup, RMS or layer norm, the loss against a teacher's top
+ *                          logits, and drawing tokens
  *
  * Conventions shared by every call:
  *   - Every pointer argument named as "device" is a CUDA device pointer owned by the
