@@ -1,6 +1,7 @@
 // C ABI of the gate-aggregation library: argument validation, workspace layout,
 // dispatch to the kernels, and the per-device error word.  See include/tango.h.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -580,7 +581,7 @@ DistillCall distill_call(const tg_distill_params* p, const void* logits, const f
 tg_status validate_sample(const tg_sample_params* p) {
   if (!p || p->rows < 0 || p->vocab < 1) return TG_ERR_INVALID_ARG;
   if (!dtype_ok(p->dtype) || (p->pitch != 0 && p->pitch < p->vocab)) return TG_ERR_INVALID_ARG;
-  if (!p->temperatures && !(p->temperature >= 0.f)) return TG_ERR_INVALID_ARG;
+  if (!p->temperatures && !(p->temperature >= 0.f && p->temperature <= FLT_MAX)) return TG_ERR_INVALID_ARG;
   if (!p->top_ps && p->top_p != p->top_p) return TG_ERR_INVALID_ARG;
   if (!p->min_ps && !(p->min_p <= 1.f)) return TG_ERR_INVALID_ARG;
   if (p->vocab > (1 << 19)) return TG_ERR_UNSUPPORTED;

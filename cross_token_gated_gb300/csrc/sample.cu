@@ -14,6 +14,7 @@
 // cycles of 61 fp32 rows).  One row of 32,768 bf16 logits
 // with top-p takes 16.6 us on 8 blocks; 256 rows with settings of their own 36 us, with top-k 50 and top-p
 // 26 us, greedily 12 us.  A border deep in the tail (top-p 0.9999) takes one row 50 us, 256 rows 103 us.
+#include <float.h>
 #include <math.h>
 
 #include "tg_common.cuh"
@@ -52,7 +53,7 @@ struct Exp2Share {
   }
 };
 
-// log2(e) / T as a sum of two floats.
+// log2(e) / T as a sum of two floats; both are finite for T from FLT_MIN to FLT_MAX.
 struct Scale {
   float hi, lo;
 };
@@ -386,6 +387,9 @@ __device__ __forceinline__ Settings settings_of(const SampleCall& c, int row) {
 __device__ __forceinline__ Settings checked(Settings s, const SampleCall& c) {
   bool bad = false;
   if (!(s.temp >= 0.f)) { bad = true; s.temp = s.temp < 0.f ? 0.f : 1.f; }
+  if (s.temp > FLT_MAX) { bad = true; s.temp = FLT_MAX; }
+  // log2(e) / T overflows from a T of 4e-39 down; the weights differ for logits less than 3.3e-37 apart only
+  if (s.temp > 0.f) s.temp = fmaxf(s.temp, FLT_MIN);
   if (s.top_p != s.top_p) { bad = true; s.top_p = 1.f; }
   if (!(s.min_p <= 1.f)) { bad = true; s.min_p = s.min_p > 1.f ? 1.f : 0.f; }
   if (!(s.u >= 0.f && s.u < 1.f)) { bad = true; s.u = s.u >= 1.f ? 0.99999994f : 0.f; }
@@ -406,8 +410,9 @@ struct Bins {
   __device__ __forceinline__ Bins(float mx_, float low, float temp, Scale sc, int vocab) : mx(mx_) {
     each = vocab > 1 << 17 && C > 1 ? kMostBins / kThreads<C> : 2;
     count = each * kThreads<C>;
-    // 27.8 > 40 ln 2; logits that differ by less than 1e-30 may share a bin
-    const float reach = fmaxf(fminf(27.8f * temp, __fsub_rn(mx, low)), 1e-30f);
+    // 27.8 > 40 ln 2; logits that differ by less than 1e-30 may share a bin; both may overflow (masked
+    // logits at a T above 1.2e37)
+    const float reach = fmaxf(fminf(fminf(27.8f * temp, __fsub_rn(mx, low)), FLT_MAX), 1e-30f);
     per_unit = __fdiv_rn((float)(count - 1), reach);
     log2_step = sc.hi / per_unit;
   }

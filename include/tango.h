@@ -720,16 +720,17 @@ tg_status tango_distill_backward(const tg_distill_params *p, const void *logits,
  * Equal logits are ranked by ascending index.  T = 0 takes the largest logit (lowest index).  +inf
  * logits share the row evenly.  A row with no token to draw (all -inf or NaN) gives -1.  The sums
  * are formed in 64-bit fixed point from weights good to about 2^-33, so that the token is that of
- * the real numbers but where u or top_p lie within about 1e-10 of a border.
+ * the real numbers but where u or top_p lie within about 1e-10 of a border.  (From T = 2^112 on the
+ * weights are good to |x - max x| 2^-150; a logit more than 3.4e38 below the largest weighs nothing.)
  *   rows, vocab     rows >= 0 (0 launches nothing); 1 <= vocab <= 2^19
  *   pitch           elements between rows of logits (0: vocab)
  *   dtype           of logits
  *   temperature, top_k, top_p, min_p   settings of every row, unless the array of that setting is
- *                   given: T >= 0; top_k <= 0: off; top_p >= 1: off, <= 0: the largest only;
- *                   min_p <= 0: off
+ *                   given: T >= 0 and finite (0 < T < 2^-126 counts as 2^-126); top_k <= 0: off;
+ *                   top_p >= 1: off, <= 0: the largest only; min_p <= 0: off
  *   temperatures, top_ks, top_ps, min_ps  device [rows], or NULL.  Values outside their range (T < 0,
- *                   NaN, min_p > 1) are clamped into it (NaN: the setting is off, T = 1) and
- *                   flagged TG_ERR_DEVICE (kernel code 8)
+ *                   T = inf, NaN, min_p > 1) are clamped into it (NaN: the setting is off, T = 1)
+ *                   and flagged TG_ERR_DEVICE (kernel code 8)
  */
 typedef struct {
     int rows, vocab;

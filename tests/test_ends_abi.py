@@ -126,6 +126,15 @@ def test_sample_refusals(lib, kw, status):
     assert tg.load().tango_sample(ctypes.byref(_sample(**kw)), A, A, A, None, None) == status
 
 
+def test_sample_refuses_an_infinite_temperature(lib):
+    f = tg.load().tango_sample
+    assert f(ctypes.byref(_sample(temperature=math.inf)), A, A, A, None, None) == BAD
+    assert f(ctypes.byref(_sample(temperature=1e39)), A, A, A, None, None) == BAD  # inf as a float
+    assert f(ctypes.byref(_sample(temperature=math.inf, rows=0)), A, A, A, None, None) == BAD
+    # the settings of the rows count, and are looked at on the device
+    assert f(ctypes.byref(_sample(temperature=math.inf, temperatures=A, rows=0)), A, A, A, None, None) == tg.TG_OK
+
+
 def test_sample_pointer_refusals(lib):
     f, ref = tg.load().tango_sample, ctypes.byref(_sample())
     assert f(None, A, A, A, None, None) == BAD

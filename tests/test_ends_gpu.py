@@ -622,6 +622,39 @@ def test_sample_bad_settings_are_flagged(lib):
     same(dict(u=torch.tensor([0.99999994, 0.99999994, 0.2], device="cuda")), u=torch.tensor([1.0, math.inf, 0.2], device="cuda"))
 
 
+@pytest.mark.parametrize("rows,V", [(3, 37), (200, 500), (2, 32771), (1, 131072)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_sample_extreme_temperatures(lib, dt, rows, V):
+    """Temperatures at the ends of their range, down to denormal ones, with equal largest logits and
+    masked ones: only the largest are left, or all weigh the same."""
+    gen = generator(21 + rows)
+    x = normal(gen, rows, V, dt=dt, scale=3.0)
+    x[:, ::7] = -math.inf
+    x[:, 5], x[:, V // 2 + 1] = 40.0, 40.0
+    x[:, 7 * (V // 14)] = 40.0
+    u = torch.rand(rows, generator=gen, device="cuda")
+    for T in (1e-45, 1e-39, 1.1e-38, 1e-37, 1e30, 3.3e38):
+        for k, p, m in ((0, 1.0, 0.0), (5, 1.0, 0.0), (300, 1.0, 0.0), (0, 0.6, 0.0), (V // 2, 0.7, 0.5)):
+            check_sample(x, u, T, k, p, m)
+            check_sample(x, u, torch.full((rows,), T, device="cuda"), k, p, m)
+    no_error()
+
+
+def test_sample_infinite_temperature_is_flagged(lib):
+    """In a row of its own settings it counts as the largest finite one."""
+    gen = generator(22)
+    x, u = normal(gen, 4, 300), torch.rand(4, generator=gen, device="cuda")
+    T = torch.tensor([0.5, math.inf, 1.0, math.inf], device="cuda")
+    most = torch.where(T == math.inf, torch.finfo(F32).max, T)
+    for how in (dict(), dict(top_k=20), dict(top_p=0.8), dict(top_k=290, top_p=0.5, min_p=0.1)):
+        token, want = torch.full((4,), -7, dtype=I32, device="cuda"), torch.full((4,), -8, dtype=I32, device="cuda")
+        tg.tango_sample(x, u, token, temperature=T, **how)
+        flagged(8)
+        tg.tango_sample(x, u, want, temperature=most, **how)
+        no_error()
+        assert torch.equal(token, want)
+
+
 def test_sample_slices(lib):
     """Rows of a padded vocabulary, aligned or not."""
     gen = generator(17)
