@@ -480,11 +480,15 @@ auto by_count(int n, F f) {
 #undef TG_CASE
 }
 
+// Dynamic shared memory that a kernel may have without asking: 48 KB with its static variables, which are
+// less than 1 KB here.
+constexpr int kDefaultSmem = 47 * 1024;
+
 template <typename V, int G, int N>
 cudaError_t forward_in(const NormArgs<typename V::Value>& a, cudaStream_t s) {
   constexpr int B = kBlock<G>, R = B / G;
   const int smem = 2 * a.d * (int)sizeof(typename V::Value);
-  if (smem > 48 * 1024) {
+  if (smem > kDefaultSmem) {
     const cudaError_t e = cudaFuncSetAttribute(norm_kernel<V, G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
@@ -497,7 +501,7 @@ cudaError_t backward_in(const NormArgs<typename V::Value>& a, int* grid, cudaStr
   constexpr int B = kBlock<G>, R = B / G;
   const auto kernel = a.want_beta ? norm_backward_kernel<V, G, N, true> : norm_backward_kernel<V, G, N, false>;
   const int smem = (a.d * (int)sizeof(typename V::Value) + 15) / 16 * 16 + (R > 1 ? R * a.d * 4 : 0);
-  if (smem > 48 * 1024) {
+  if (smem > kDefaultSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }

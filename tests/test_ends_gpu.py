@@ -239,6 +239,21 @@ def test_norm_backward_by_differences(lib):
         assert abs((dg.double() * v[0]).sum() - d) <= 1e-4 * (dg.double() * v[0]).abs().sum()
 
 
+@pytest.mark.parametrize("dt,d", [(F32, 6128), (F32, 6132), (F32, 6144), (F32, 6148), (BF, 12256), (BF, 12264), (BF, 12288),
+                                  (BF, 12296), (F32, 8192), (F32, 8191), (F32, 6143), (F32, 6147), (BF, 16384), (BF, 8191)])
+def test_norm_widths_about_48_kb_of_weights(lib, dt, d):
+    """Gain and bias in shared memory, up to and past what a kernel may have without asking."""
+    gen = generator(d)
+    x, gamma, beta = normal(gen, 3, d, dt=dt), normal(gen, d, dt=dt), normal(gen, d, dt=dt)
+    y = torch.empty_like(x)
+    for layer in (False, True):
+        tg.tango_norm(x, gamma, beta, y, norm=tg.TG_NORM_LAYER if layer else tg.TG_NORM_RMS, eps=1e-5)
+        want, n, r = norm_ref(x, gamma, beta, layer, 1e-5)
+        size = r * x.double().abs().mean(-1, keepdim=True) + n.abs()
+        bound = (d / 32 + 24) * U * size * gamma.double().abs() + 2 * U * (want.abs() + beta.double().abs())
+        within(y, want, bound + half_step(dt) * want.abs() * (1 + 2 ** -6))
+
+
 def test_norm_special_rows(lib):
     """Zero rows stay finite, a NaN stays in its row, rows of one value, an empty batch."""
     x = torch.zeros(4, 64, dtype=BF, device="cuda")
