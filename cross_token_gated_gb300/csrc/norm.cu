@@ -488,8 +488,10 @@ template <typename V, int G, int N>
 cudaError_t forward_in(const NormArgs<typename V::Value>& a, cudaStream_t s) {
   constexpr int B = kBlock<G>, R = B / G;
   const int smem = 2 * a.d * (int)sizeof(typename V::Value);
-  if (smem > kDefaultSmem) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_kernel<V, G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the longest rows', whatever these are: another thread's lower one might come before the launch
+  constexpr int kMost = 2 * G * N * (int)sizeof(typename V::Raw);
+  if constexpr (kMost > kDefaultSmem) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_kernel<V, G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   norm_kernel<V, G, N><<<grid_of((a.rows + R - 1) / R, kForwardPerSm<G>), B, smem, s>>>(a);
@@ -501,10 +503,7 @@ cudaError_t backward_in(const NormArgs<typename V::Value>& a, int* grid, cudaStr
   constexpr int B = kBlock<G>, R = B / G;
   const auto kernel = a.want_beta ? norm_backward_kernel<V, G, N, true> : norm_backward_kernel<V, G, N, false>;
   const int smem = (a.d * (int)sizeof(typename V::Value) + 15) / 16 * 16 + (R > 1 ? R * a.d * 4 : 0);
-  if (smem > kDefaultSmem) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  static_assert(G * N * (int)sizeof(typename V::Raw) + (R > 1 ? R * G * N * V::E * 4 : 0) <= kDefaultSmem);
   *grid = grid_of((a.rows + R - 1) / R, kBackwardPerSm<G>);
   kernel<<<*grid, B, smem, s>>>(a);
   return cudaGetLastError();

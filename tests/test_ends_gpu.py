@@ -848,3 +848,40 @@ def test_offsets_past_32_bits(lib):
     within(dE[1], x[-3:].double().sum(0), 8 * U * x[-3:].double().abs().sum(0))
     tg.tango_embed(ids, torch.arange(2 * d, device="cuda").view(2, d).to(BF), y)
     assert (y[-1] == torch.arange(d, 2 * d, device="cuda").to(BF)).all() and (y[0] == torch.arange(d, device="cuda").to(BF)).all()
+
+
+def at_once(calls, times):
+    """Makes each of `calls` (returning a status) from a thread of its own, all at the same time; the
+    statuses that came back."""
+    import threading
+    start, seen = threading.Barrier(len(calls)), [set() for _ in calls]
+
+    def work(i):
+        start.wait()
+        for _ in range(times):
+            seen[i].add(calls[i]())
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return set().union(*seen)
+
+
+def test_norms_of_other_widths_at_once(lib):
+    """Host threads that norm rows of different widths, which ask for different amounts of shared memory
+    of one kernel, do not disturb one another."""
+    import ctypes
+    raw, keep, calls = tg.load(), [], []
+    for d in (8192, 6148, 7168, 8191, 6147):
+        x, y = normal(generator(d), 2, d), torch.empty(2, d, device="cuda")
+        p, s = tg.tg_norm_params(2, d, tg.TG_NORM_RMS, 1e-6, 0, tg.TG_F32), torch.cuda.Stream()
+        keep.append((x, y, s))
+        args = (ctypes.byref(p), x.data_ptr(), None, None, y.data_ptr(), s.cuda_stream)
+        calls.append(lambda args=args: raw.tango_norm(*args))
+    torch.cuda.synchronize()
+    assert at_once(calls, 4000) == {tg.TG_OK}
+    for x, y, _ in keep:
+        want, n, _ = norm_ref(x, None, None, False, 1e-6)
+        within(y, want, (x.shape[1] / 32 + 30) * U * 2 * n.abs())
