@@ -356,22 +356,31 @@ __global__ void __launch_bounds__(kThreads) wango_simt_kernel(AggArgs p) {
   }
 }
 
+// Shared memory of the two kernels for heads of d_h values.
+constexpr size_t tango_smem(int d_h) {
+  return sizeof(float) * (size_t)(kRows * d_h + kSrc * d_h + kSrc * kCols + kRows * 33);
+}
+constexpr size_t wango_smem(int d_h) {
+  return sizeof(float) * (size_t)(d_h * kCols + d_h + 2 * kRows * d_h + 2 * kSrc * d_h + kSrc * kCols + kRows * 33);
+}
+constexpr int kMaxHead = 128;  // of d_h; the kernels' limits are this width's, whatever a call's is: another
+                               // thread's lower one might come before the launch
+
 template <typename T>
 cudaError_t launch_agg(const AggArgs& p, cudaStream_t s, bool wango) {
   const int d_h = p.dqk / p.H, m_hp = p.m / p.H, m_h = p.m_h ? p.m_h : m_hp;
   const int ntile = (m_h + kCols - 1) / kCols;
   if (!wango) {
-    const size_t smem = sizeof(float) * (size_t)(kRows * d_h + kSrc * d_h + kSrc * kCols + kRows * 33);
+    const size_t smem = tango_smem(d_h);
     auto kern = tango_simt_kernel<T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tango_smem(kMaxHead));
     if (e != cudaSuccess) return e;
     dim3 grid(p.H * ntile, (p.T + kRows - 1) / kRows, p.B);
     kern<<<grid, kThreads, smem, s>>>(p);
   } else {
-    const size_t smem = sizeof(float) * (size_t)(d_h * kCols + d_h + 2 * kRows * d_h + 2 * kSrc * d_h +
-                                                 kSrc * kCols + kRows * 33);
+    const size_t smem = wango_smem(d_h);
     auto kern = wango_simt_kernel<T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)wango_smem(kMaxHead));
     if (e != cudaSuccess) return e;
     dim3 grid(p.H * ntile, 1, p.B);
     kern<<<grid, kThreads, smem, s>>>(p);

@@ -738,3 +738,44 @@ def test_wango_matches_its_rounding_points(case, null):
     # measured: 0.1-1.7 % of the outputs differ (the fp32 state and accumulation orders
     # flip a bf16 rounding now and then), normwise at most 1.2e-3
     assert stats["differ"] <= 5e-2 and stats["norm"] <= 2.0 ** -8, stats
+
+
+def test_fp32_head_widths_at_once(lib):
+    """Host threads that aggregate over heads of different widths, which ask for different amounts of
+    shared memory of one kernel, do not disturb one another."""
+    import ctypes
+    import threading
+    raw, keep, calls = tg.load(), [], []
+    B, T, m = 1, 40, 64
+    for name, which in (("tango_aggregate", tg.TG_WS_TANGO), ("wango_aggregate", tg.TG_WS_WANGO)):
+        for d in (128, 16, 64):
+            gen = torch.Generator().manual_seed(d)
+            q, k, g, v = (torch.randn(B, T, n, generator=gen).cuda() for n in (d, d, m, m))
+            p = tg.agg_params(B, T, 1, d, m, dtype=tg.TG_F32, window=8)
+            need, s = tg.tg_workspace_size(which, p), torch.cuda.Stream()
+            ws, out = torch.empty(need + 256, dtype=torch.uint8, device="cuda"), torch.empty_like(v)
+            at = (ws.data_ptr() + 255) & ~255
+            args = (ctypes.byref(p), *(t.data_ptr() for t in (q, k, g, v, out)), at, need, s.cuda_stream)
+            keep.append((name, p, q, k, g, v, out, ws, s))
+            calls.append(lambda f=getattr(raw, name), args=args: f(*args))
+    torch.cuda.synchronize()
+    want = []
+    for call, case in zip(calls, keep):
+        assert call() == tg.TG_OK
+        torch.cuda.synchronize()
+        want.append(case[6].clone())
+    start, seen = threading.Barrier(len(calls)), [set() for _ in calls]
+
+    def work(i):
+        start.wait()
+        for _ in range(1500):
+            seen[i].add(calls[i]())
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert set().union(*seen) == {tg.TG_OK}
+    for w, case in zip(want, keep):
+        assert torch.equal(case[6], w)
