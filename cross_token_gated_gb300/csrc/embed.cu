@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const int* ids, const
   for (int c = lane * N; c < d; c += 32 * N) {
     if constexpr (kVec) {
       const uint4 u = live ? *reinterpret_cast<const uint4*>(src + c) : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(dst + c) = scale == 1.f ? u : scaled<T>(u, scale);
+      *reinterpret_cast<uint4*>(dst + c) = scale == 1.f || !live ? u : scaled<T>(u, scale);
     } else {
       if (!live) dst[c] = T(0.f);
       else if (scale == 1.f) dst[c] = src[c];

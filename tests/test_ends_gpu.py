@@ -82,6 +82,20 @@ def test_embed_pad_and_bad_ids(lib):
         flagged(4)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("d", [64, 7])
+@pytest.mark.parametrize("scale", [math.inf, math.nan, -2.0])
+def test_embed_padding_is_zero_at_any_scale(lib, dt, d, scale):
+    """Rows without a token are zeros (+0) whatever the factor."""
+    E = normal(generator(31), 10, d, dt=dt)
+    ids = torch.tensor([-1, 4, -1], dtype=I32, device="cuda")
+    out = torch.full((3, d), 5.0, dtype=dt, device="cuda")
+    tg.tango_embed(ids, E, out, scale=scale)
+    assert (out[::2].view(torch.int16 if dt is BF else I32) == 0).all()
+    assert torch.equal(out[1].isnan(), (E[4].float() * scale).isnan())
+    no_error()
+
+
 def embed_ids(kind, rows, vocab, gen):
     if kind == "same":
         return torch.full((rows,), vocab // 2, dtype=I32, device="cuda")
