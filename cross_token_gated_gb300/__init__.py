@@ -555,6 +555,13 @@ def _dense(t, name, dtype, dev, shape=None):
     return t.data_ptr()
 
 
+_MOST_INT = 2 ** 31 - 1  # of the parameters' int fields, which ctypes would cut to their low bits
+
+
+def _too_large(name):
+    raise ValueError(f"{name}'s sizes and numbers must be below 2^31")
+
+
 def _rows_pitch(t, name, dtype, dev):
     """(rows, width, pitch in elements) of a [..., width] tensor whose rows lie at one pitch
     (a dense tensor, or a column slice of one)."""
@@ -563,6 +570,8 @@ def _rows_pitch(t, name, dtype, dev):
     shape, stride = t.shape, t.stride()
     if len(shape) < 2 or (stride[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be [..., width] with unit stride along its last dimension")
+    if shape[-1] > _MOST_INT:
+        _too_large(name)
     if len(shape) == 2:
         rows, width = shape
         pitch = stride[0] if rows > 1 else width
@@ -776,6 +785,8 @@ def tango_paged_aggregate(q, v, out, k_pages, g_pages, page_table, cu_new, lens,
 def _embed_params(ids, width, rows, pitch, vocab, dtype, grad_dtype, scale, pad_id, dev):
     if ids.numel() != rows:
         raise ValueError("ids must hold one token per row")
+    if not -_MOST_INT - 1 <= pad_id <= _MOST_INT:
+        raise ValueError("pad_id must be an int32 as ids are")
     ip = _dense(ids, "ids", torch.int32, dev)
     return tg_embed_params(rows, width, vocab, scale, pad_id, pitch, dtype, grad_dtype), ip
 
@@ -784,6 +795,8 @@ def _matrix(t, name, dtype, dev, width=None):
     """Address of a dense [rows, width] tensor."""
     if t.dim() != 2 or (width is not None and t.shape[1] != width):
         raise ValueError(f"{name} must be a matrix" + ("" if width is None else f" of {width} columns"))
+    if t.shape[0] > _MOST_INT:  # (its width is looked at with its rows')
+        _too_large(name)
     return _dense(t, name, dtype, dev)
 
 
@@ -876,6 +889,8 @@ def _distill_params(logits, t_logits, t_ids, loss, temperature, grad, f32s):
     dt, dev = logits.dtype, logits.get_device()
     rows, vocab, pitch = _rows_pitch(logits, "logits", dt, dev)
     k = t_logits.shape[-1]
+    if k > _MOST_INT:
+        _too_large("t_logits")
     if t_logits.numel() != rows * k or t_ids.shape != t_logits.shape:
         raise ValueError("t_logits and t_ids must hold k entries per row of logits")
     tp = _dense(t_logits, "t_logits", torch.float32, dev)
@@ -927,6 +942,10 @@ def tango_sample(logits, uniform, token, *, temperature=1.0, top_k=0, top_p=1.0,
     [...].  Each setting is a number, or a tensor of one per row (float32; top_k int32)."""
     dt, dev = logits.dtype, logits.get_device()
     rows, vocab, pitch = _rows_pitch(logits, "logits", dt, dev)
+    if rows > _MOST_INT:
+        _too_large("logits")
+    if not isinstance(top_k, torch.Tensor):
+        top_k = min(max(top_k, 0), _MOST_INT)  # (0 and less, and the vocabulary and more: off)
     f32, i32 = torch.float32, torch.int32
     ptrs = []
     for name, t, kind in (("uniform", uniform, f32), ("token", token, i32), ("logprob", logprob, f32)):

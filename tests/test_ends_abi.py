@@ -198,3 +198,39 @@ def test_binding_refuses_wrong_tensors(lib):
         tg.tango_sample(z, row, tok, temperature=row[:2])
     with pytest.raises(ValueError):
         tg.tango_sample(z, row, tok)                                      # a host tensor
+
+
+def _shape(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype, device="meta")  # has a size, but no memory
+
+
+def test_binding_refuses_numbers_past_32_bits(lib):
+    """The library's int fields would take their low bits: a row of 2^32 + 8 values would be normed as one
+    of 8, a padding id of 2^32 + 3 would drop token 3."""
+    i32, f32, wide, far = torch.int32, torch.float32, 2 ** 32 + 8, "2\\^31"
+    x = _shape(1, wide)
+    with pytest.raises(ValueError, match=far):
+        tg.tango_norm(x, None, None, x)
+    with pytest.raises(ValueError, match=far):
+        tg.tango_norm_backward(x, None, x, x)
+    with pytest.raises(ValueError, match=far):
+        tg.tango_embed(_shape(1, dtype=i32), _shape(wide, 8), _shape(1, 8))
+    with pytest.raises(ValueError, match=far):
+        tg.tango_embed_backward(_shape(1, dtype=i32), _shape(1, 8), _shape(wide, 8))
+    for pad_id in (2 ** 32 + 3, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="pad_id"):
+            tg.tango_embed(_t(4, dtype=i32), _t(10, 8), _t(4, 8), pad_id=pad_id)
+        with pytest.raises(ValueError, match="pad_id"):
+            tg.tango_embed_backward(_t(4, dtype=i32), _t(4, 8), _t(10, 8, dtype=f32), pad_id=pad_id)
+    for pad_id in (2 ** 31 - 1, -2 ** 31):
+        with pytest.raises(ValueError, match="cpu|host|device"):
+            tg.tango_embed(_t(4, dtype=i32), _t(10, 8), _t(4, 8), pad_id=pad_id)
+    row = _shape(1, dtype=f32)
+    with pytest.raises(ValueError, match=far):
+        tg.tango_distill(x, _shape(1, 3, dtype=f32), _shape(1, 3, dtype=i32), row)
+    with pytest.raises(ValueError, match=far):
+        tg.tango_distill(_shape(1, 30), _shape(1, wide, dtype=f32), _shape(1, wide, dtype=i32), row)
+    with pytest.raises(ValueError, match=far):
+        tg.tango_sample(x, row, _shape(1, dtype=i32))
+    with pytest.raises(ValueError, match=far):
+        tg.tango_sample(_shape(wide, 2), _shape(wide, dtype=f32), _shape(wide, dtype=i32))

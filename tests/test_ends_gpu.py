@@ -684,6 +684,14 @@ def test_sample_infinite_temperature_is_flagged(lib):
         assert torch.equal(token, want)
 
 
+def test_sample_top_k_past_32_bits_is_off(lib):
+    x, u = normal(generator(23), 50, 200), torch.rand(50, generator=generator(24), device="cuda")
+    token, want = torch.empty(50, dtype=I32, device="cuda"), torch.empty(50, dtype=I32, device="cuda")
+    tg.tango_sample(x, u, want)
+    for k in (2 ** 32 + 1, 2 ** 31, 2 ** 63, -2 ** 32 + 1, -2 ** 40, 200, -1):
+        assert torch.equal(tg.tango_sample(x, u, token, top_k=k), want), k
+
+
 def test_sample_slices(lib):
     """Rows of a padded vocabulary, aligned or not."""
     gen = generator(17)
