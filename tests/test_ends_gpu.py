@@ -233,6 +233,32 @@ def test_norm_backward(lib, rows, d, dt, layer, affine, res):
         assert torch.equal(over, dx)
 
 
+@pytest.mark.parametrize("rows,d", [(700, 4096), (400, 16384), (900, 8191), (1500, 16392), (1300, 40000)])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("layer", [False, True])
+def test_norm_several_wide_rows_of_a_block(lib, rows, d, dt, layer):
+    """More rows than blocks where many threads share a row: the next row is on its way, buffers are
+    taken in turn and the weights' gradients are summed over a block's rows."""
+    gen = generator(rows + d)
+    x = normal(gen, rows, d, dt=dt, scale=1.5) + 0.5
+    gamma, dy = (1 + normal(gen, d, scale=0.3)).to(dt), normal(gen, rows, d, dt=dt)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    dg, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    how = dict(norm=tg.TG_NORM_LAYER if layer else tg.TG_NORM_RMS, eps=1e-5)
+    tg.tango_norm(x, gamma, None, y, **how)
+    tg.tango_norm_backward(x, gamma, dy, dx, dgamma=dg, dbeta=db, **how)
+    want, n, r = norm_ref(x, gamma, None, layer, 1e-5)
+    k = d / 32 + 24  # terms of a thread and of the joins, and single roundings
+    size = r * x.double().abs().mean(-1, keepdim=True) + n.abs()  # n is off by k U of this at most
+    within(y, want, k * U * size * gamma.double().abs() + 2 * U * want.abs() + half_step(dt) * want.abs() * (1 + 2 ** -6))
+    dn = dy.double() * gamma.double()
+    want = r * (dn - n * (dn * n).mean(-1, keepdim=True) - (dn.mean(-1, keepdim=True) if layer else 0.0))
+    terms = 2 * dn.abs() + 4 * size * (dn.abs() * size).mean(-1, keepdim=True) + 2 * dn.abs().mean(-1, keepdim=True)
+    within(dx, want, k * U * r * terms + 2 * U * want.abs() + half_step(dt) * want.abs() * (1 + 2 ** -6))
+    within(dg, (dy.double() * n).sum(0), (rows + 2 * k) * U * (dy.double().abs() * size).sum(0))
+    within(db, dy.double().sum(0), rows * U * dy.double().abs().sum(0))
+
+
 def test_norm_backward_by_differences(lib):
     """fp32 gradients of a scalar against its differences along one direction."""
     gen = generator(9)
