@@ -612,6 +612,22 @@ def test_sample_many_close_logits(lib, dt):
     no_error()
 
 
+@pytest.mark.parametrize("rows,V", [(160, 40000), (2, 1 << 19)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_sample_many_logits_of_a_bin(lib, rows, V, dt):
+    """More than 2^14 equal logits of one block, the largest ones or in the middle: the histogram of
+    masses overflows there."""
+    gen = generator(25 + rows)
+    x = normal(gen, rows, V, dt=dt) - 2
+    same = torch.rand(rows, V, generator=gen, device="cuda") < torch.linspace(0.3, 0.9, rows, device="cuda")[:, None]
+    x[same] = 1.5
+    x[::2, 7] = 4.0
+    u = torch.rand(rows, generator=gen, device="cuda")
+    for T, k, p, m in ((1.0, 0, 0.3, 0.0), (1.0, 0, 0.95, 0.0), (0.8, V // 3, 0.6, 0.0), (2.0, V - 100, 0.999, 0.02)):
+        check_sample(x, u, T, k, p, m)
+    no_error()
+
+
 @pytest.mark.parametrize("rows,V", [(1, 32768), (5, 32771), (30, 131072), (60, 32768), (170, 32771), (2, 400001)])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_sample_shares_near_one(lib, rows, V, dt):
