@@ -6,8 +6,10 @@
 // Both are bound by HBM bandwidth: rows are read and written once.  The gradient sorts the tokens
 // by id (a stable counting sort, so that the order of every sum is fixed) and sums the sorted rows of
 // dout in fp32 in equal chunks, so that a frequent token loads no warp more than a rare one; sums
-// that cross chunks are joined in order by the warp that comes last.  The rows of ids without tokens
-// are written by the same launch.
+// that cross chunks are joined in order by the warp that comes last.  Where a token's chunks begin
+// follows from the other ids, from the number of SMs (the sort's order) and from the alignment (the
+// chunks' size), and so do the last bits of its sum.  The rows of ids without tokens are written by the
+// same launch.
 //
 // 16,384 tokens of 512 bf16 values into 32,768 fp32 rows: 25 us (floor 12.4), most of it the sums,
 // whose first loads wait for order, row and neighbour in a row.  5,003 fp32 tokens of 768 onto a

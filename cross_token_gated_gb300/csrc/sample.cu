@@ -649,7 +649,9 @@ __device__ __forceinline__ void draw_listed(const SampleCall& c, const Settings&
 // histogram of counts, or of masses good to about 1e-5; only the logits of the bins that may hold it
 // are listed and compared one by one, in exact sums.  Should there be too many of them, a border of
 // the mass is looked for in finer steps; what is too many then (many equal logits), and a border of
-// the counts, is bisected.
+// the counts, is bisected.  The histogram of masses is a hint only: more than 16,383 logits of a block
+// in one bin overflow it.  Where its bins do not hold the border then, the exact sums show it, and the
+// border is bisected over the whole row.
 template <typename T, int C>
 __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel(const SampleCall c) {
   using u64 = unsigned long long;
@@ -794,7 +796,7 @@ __global__ void __launch_bounds__(kThreads<C>, 1024 / kThreads<C>) sample_kernel
 
   if (s.top_p < 1.f) {
     clear_bins();
-    // a bin's masses in units of 2^-18 of the weight at its middle
+    // a bin's masses in units of 2^-18 of the weight at its middle, modulo 2^32
     row.template each<2>([&](float x, int i) {
       const float y = bins.place(x);
       if (!bins.inside(y) || (some_cut && !cut.keeps(key_of(x), i))) return;

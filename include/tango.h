@@ -622,8 +622,9 @@ tg_status tango_embed(const tg_embed_params *p, const int *ids, const void *embe
  * dembedding[v] = base[v] + scale * sum over the tokens n with ids[n] = v of dout[n].
  * base: device [vocab, d] or NULL (zeros); may be dembedding itself, so that the gradient of the
  * tied output matrix is added to.  dembedding: device [vocab, d], dense, every row written.  The
- * tokens are sorted by id first and summed in fp32 in an order that depends on the sizes only
- * (no atomics on sums: the same call gives the same bits).  ws: device scratch of
+ * tokens are sorted by id first and summed in fp32 in an order that the sizes, the ids, whether dout,
+ * base and dembedding are 16-byte aligned, and the device's number of SMs fix (no atomics on sums:
+ * the same call on the same memory gives the same bits).  ws: device scratch of
  * tg_workspace_size(TG_WS_EMBED_BWD, p) bytes, 256-byte aligned.
  */
 tg_status tango_embed_backward(const tg_embed_params *p, const int *ids, const void *dout, const void *base,
@@ -677,7 +678,8 @@ tg_status tango_norm_backward(const tg_norm_params *p, const void *x, const void
  *   temperature  T in [0.001, 1000]
  *   pitch        elements between rows of logits (0: vocab)
  *   grad_pitch   elements between rows of dlogits (0: vocab)
- *   dtype        of logits and dlogits; arithmetic is fp32
+ *   dtype        of logits and dlogits; arithmetic is fp32 (the loss is good to some 2^-22 of
+ *                T^2 ln vocab, which counts at a high T where p and q are nearly alike)
  * t_logits: device float[rows, k].  t_ids: device int[rows, k]: an entry with a negative id, or
  * with t = -inf, is absent; an id >= vocab is absent too and flagged TG_ERR_DEVICE (kernel code
  * 7).  A token may stand in several entries.  A row without entries (padding) has loss 0 and
