@@ -678,8 +678,9 @@ tg_status tango_norm_backward(const tg_norm_params *p, const void *x, const void
  *   temperature  T in [0.001, 1000]
  *   pitch        elements between rows of logits (0: vocab)
  *   grad_pitch   elements between rows of dlogits (0: vocab)
- *   dtype        of logits and dlogits; arithmetic is fp32 (the loss is good to some 2^-22 of
- *                T^2 ln vocab, which counts at a high T where p and q are nearly alike)
+ *   dtype        of logits and dlogits; arithmetic is fp32.  From T = 1 on the loss is good to
+ *                2^-22 T^2 ln vocab: where the entries are the whole vocabulary, so that the loss
+ *                does not grow with T, T = 30 leaves it three digits and T = 1000 none
  * t_logits: device float[rows, k].  t_ids: device int[rows, k]: an entry with a negative id, or
  * with t = -inf, is absent; an id >= vocab is absent too and flagged TG_ERR_DEVICE (kernel code
  * 7).  A token may stand in several entries.  A row without entries (padding) has loss 0 and
